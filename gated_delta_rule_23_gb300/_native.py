@@ -17,10 +17,11 @@ CSRC = os.path.join(_PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(_PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libkda.so")
-UNITS = ["kda_api", "kda_prep", "kda_recur", "kda_recurrent", "kda_decode", "kda_host", "kda_noalloc", "kda_scan"]
+UNITS = ["kda_api", "kda_prep", "kda_recur", "kda_recurrent", "kda_decode", "kda_host", "kda_noalloc", "kda_scan",
+         "kda_step", "kda_append", "kda_attn", "kda_beam", "kda_reorder"]
 SOURCES = [os.path.join(CSRC, u + ".cu") for u in UNITS]
 HEADERS = [os.path.join(INCLUDE, "kda.h"), os.path.join(CSRC, "kda_device.cuh"), os.path.join(CSRC, "kda_internal.h"),
-           os.path.join(CSRC, "kda_plan.h")]
+           os.path.join(CSRC, "kda_plan.h"), os.path.join(CSRC, "kda_step.cuh"), os.path.join(CSRC, "kda_attn.cuh")]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 _lock = threading.Lock()
@@ -112,6 +113,26 @@ def load() -> ctypes.CDLL:
         lib.kda_set_wait_limit.restype = None
         lib.kda_fwd_smem_bytes.argtypes = []
         lib.kda_fwd_smem_bytes.restype = ctypes.c_size_t
+        Z = ctypes.c_size_t
+        cache = [P, I, I64, I, I, I, I64, I, I]      # cu_seqlens, N, T, Hq, Hkv, D, pages, page, max_pages
+        lib.kda_kv_append.argtypes = [P, I64, P, I64, P, P, P, P, P, P, I, I64, I, P, I64, P] + cache + [P]
+        lib.kda_kv_append.restype = I
+        attn = [P, I64, P, P, P, P, P, P, F, I, I] + cache
+        lib.kda_window_attn.argtypes = attn + [P]
+        lib.kda_window_attn.restype = I
+        lib.kda_window_attn_ws.argtypes = attn + [P, Z, P]
+        lib.kda_window_attn_ws.restype = I
+        lib.kda_window_attn_workspace_size.argtypes = [I, I, I, I, I64, I, I, I, I, I]
+        lib.kda_window_attn_workspace_size.restype = Z
+        beam = [P, I, I64, P, P, I, P, P, P, I, I, I, I]
+        lib.kda_beam_select.argtypes = beam + [P]
+        lib.kda_beam_select.restype = I
+        lib.kda_beam_select_ws.argtypes = beam + [P, Z, P]
+        lib.kda_beam_select_ws.restype = I
+        lib.kda_beam_select_workspace_size.argtypes = [I, I, I, I]
+        lib.kda_beam_select_workspace_size.restype = Z
+        lib.kda_state_reorder.argtypes = [P, P, P, I, P, I, I, P]
+        lib.kda_state_reorder.restype = I
         _lib = lib
     return _lib
 

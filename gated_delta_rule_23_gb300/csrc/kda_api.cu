@@ -811,7 +811,10 @@ extern "C" kda_status_t kda_device_status(kda_stream_t stream)
         if (cudaMemcpyToSymbol(g_kda_plan_error, &zero, sizeof zero) != cudaSuccess)
             return KDA_ERR_CUDA;
     }
-    const unsigned int bits = flag | flag2 | flag3 | flag4 | flag5;
+    unsigned int flag6 = 0;
+    if (step_read_and_clear_error(&flag6) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    const unsigned int bits = flag | flag2 | flag3 | flag4 | flag5 | flag6;
     if (bits & DEVERR_TIMEOUT)
         return KDA_ERR_TIMEOUT;
     if (bits & DEVERR_CU_SEQLENS)

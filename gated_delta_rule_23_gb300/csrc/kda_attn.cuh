@@ -1,0 +1,76 @@
+// Windowed attention over the paged cache: the problem description, and the row form of the definition.
+#pragma once
+
+#include "kda_step.cuh"
+
+namespace kda {
+
+struct AttnArgs {
+    const __nv_bfloat16 *q;
+    int64_t q_stride;
+    __nv_bfloat16 *out;
+    float *lse;                  // or nullptr
+    float scale_log2;            // scale * log2(e): the softmax is taken in base 2
+    int window, sinks;
+    int hq, group;               // group = query heads of one key head
+    PagedCache cache;
+    Tokens tok;
+    unsigned int *err;
+};
+
+constexpr float LN2 = 0.6931471805599453f;
+
+// One query row (token t of the batch, head h) at position pos, by a whole warp, straight from the definition:
+// every visible key in order, with the running maximum m and sum l of the softmax in base 2.  Keys that the row
+// does not see are never read.
+template <int DIM>
+__device__ void attn_row(const AttnArgs &p, int n, int64_t t, int h, int64_t pos, bool &bad)
+{
+    constexpr int PER = DIM / 32;
+    const int lane = threadIdx.x & 31;
+    const __nv_bfloat16 *q = p.q + t * p.q_stride + (int64_t)h * DIM + lane * PER;
+    const int64_t head = ((int64_t)(h / p.group) << p.cache.page_shift) * DIM;
+    float qf[PER], o[PER];
+#pragma unroll
+    for (int e = 0; e < PER; e++) {
+        qf[e] = __bfloat162float(q[e]) * p.scale_log2;
+        o[e] = 0.0f;
+    }
+    float m = -INFINITY, l = 0.0f;
+    const int64_t left = pos - p.window + 1;
+    for (int64_t j = 0; j <= pos; j++) {
+        if (j >= p.sinks && j < left) {
+            j = left;
+        }
+        const int64_t row = cache_row(p.cache, n, j);
+        if (row < 0) {
+            bad = true;
+            continue;
+        }
+        const __nv_bfloat16 *k = p.cache.k + row + head + lane * PER, *v = p.cache.v + row + head + lane * PER;
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < PER; e++)
+            s = fmaf(qf[e], __bfloat162float(k[e]), s);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1)
+            s += __shfl_xor_sync(0xffffffffu, s, x);
+        const float mn = fmaxf(m, s);
+        const float mu = mn == -INFINITY ? 0.0f : mn;
+        const float a = exp2f(m - mu), w = exp2f(s - mu);
+        l = l * a + w;
+#pragma unroll
+        for (int e = 0; e < PER; e++)
+            o[e] = fmaf(o[e], a, w * __bfloat162float(v[e]));
+        m = mn;
+    }
+    const float r = l == 0.0f ? 0.0f : 1.0f / l;
+    __nv_bfloat16 *out = p.out + (t * p.hq + h) * DIM + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; e++)
+        out[e] = __float2bfloat16_rn(l == 0.0f ? 0.0f : o[e] * r);
+    if (p.lse && lane == 0)
+        p.lse[t * p.hq + h] = l == 0.0f ? -INFINITY : LN2 * (m + log2f(l));
+}
+
+}  // namespace kda

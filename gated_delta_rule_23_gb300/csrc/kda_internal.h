@@ -70,4 +70,12 @@ cudaError_t read_and_clear_device_error(unsigned int *flag);
 cudaError_t prep_read_and_clear_error(unsigned int *flag);
 cudaError_t recurrent_read_and_clear_error(unsigned int *flag);
 
+// ---- decoder-step operators (append, windowed attention, beam selection, reorder)
+// Device address of the word these kernels report in on the current device (looked up once per device).
+cudaError_t step_error_word(unsigned int **word);
+cudaError_t step_read_and_clear_error(unsigned int *flag);
+// SM count of the current device (looked up once per device); 0 when it cannot be read.
+int device_sms();
+inline bool is_aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
 }  // namespace kda

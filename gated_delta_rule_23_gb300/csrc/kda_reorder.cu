@@ -1,0 +1,113 @@
+// kda_state_reorder: rows of states (or anything) follow their beams.
+//
+// No arithmetic: the floor is each parent row read once and each row written once.  A thread owns one 16-byte
+// column of a group's rows: it reads that column of every row that is some row's parent, then writes.  All of a
+// column's reads come before its writes in the same thread, which is what makes the in-place form safe.
+#include "kda_step.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int REORDER_THREADS = 256;
+constexpr int REORDER_TENSORS = 64;   // tensors of one launch (their pointers travel as kernel arguments)
+
+struct ReorderArgs {
+    const uint4 *src[REORDER_TENSORS];
+    uint4 *dst[REORDER_TENSORS];
+    int64_t vecs[REORDER_TENSORS];    // 16-byte vectors of a row
+    const int32_t *parents;
+    int beams;
+    unsigned int *err;
+};
+
+template <int MAXW> __global__ void __launch_bounds__(REORDER_THREADS) kda_reorder_kernel(const ReorderArgs p)
+{
+    const uint4 *src = p.src[blockIdx.z];
+    uint4 *dst = p.dst[blockIdx.z];
+    const int64_t vecs = p.vecs[blockIdx.z];
+    const int64_t n0 = (int64_t)blockIdx.y * p.beams;
+    bool bad = false;
+    for (int64_t x = (int64_t)blockIdx.x * REORDER_THREADS + threadIdx.x; x < vecs;
+         x += (int64_t)gridDim.x * REORDER_THREADS) {
+        uint4 r[MAXW];
+#pragma unroll
+        for (int w = 0; w < MAXW; w++) {
+            if (w < p.beams) {
+                int64_t from = p.parents[n0 + w];
+                if (from < n0 || from >= n0 + p.beams) {
+                    bad = true;
+                    from = n0 + w;
+                }
+                r[w] = src[from * vecs + x];
+            }
+        }
+#pragma unroll
+        for (int w = 0; w < MAXW; w++)
+            if (w < p.beams)
+                dst[(n0 + w) * vecs + x] = r[w];
+    }
+    report(p.err, bad, DEVERR_CU_SEQLENS);
+}
+
+cudaError_t launch_reorder(const ReorderArgs &p, int64_t most, int groups, int tensors, cudaStream_t st)
+{
+    int64_t gx = (most + REORDER_THREADS - 1) / REORDER_THREADS;
+    if (gx > 4096)
+        gx = 4096;
+    const dim3 grid((unsigned)gx, (unsigned)groups, (unsigned)tensors);
+    if (p.beams <= 4)
+        kda_reorder_kernel<4><<<grid, REORDER_THREADS, 0, st>>>(p);
+    else if (p.beams <= 8)
+        kda_reorder_kernel<8><<<grid, REORDER_THREADS, 0, st>>>(p);
+    else
+        kda_reorder_kernel<32><<<grid, REORDER_THREADS, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" kda_status_t kda_state_reorder(const void *const *src, void *const *dst, const int64_t *row_bytes,
+                                          int tensors, const int32_t *parents, int N, int beams, kda_stream_t stream)
+{
+    if (tensors < 0 || N < 1 || beams < 1 || beams > 32 || N % beams || !parents || !is_aligned(parents, 4))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (tensors > 0 && (!src || !dst || !row_bytes))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (N / beams > 65535)
+        return KDA_ERR_UNSUPPORTED;
+    for (int i = 0; i < tensors; i++) {
+        if (row_bytes[i] < 0 || row_bytes[i] % 16 || row_bytes[i] > ((int64_t)1 << 46))
+            return KDA_ERR_INVALID_ARGUMENT;
+        if (row_bytes[i] > 0 && (!src[i] || !dst[i] || !is_aligned(src[i], 16) || !is_aligned(dst[i], 16)))
+            return KDA_ERR_INVALID_ARGUMENT;
+        // in place, or apart
+        const uintptr_t a = reinterpret_cast<uintptr_t>(src[i]), b = reinterpret_cast<uintptr_t>(dst[i]);
+        const uintptr_t bytes = (uintptr_t)row_bytes[i] * (uintptr_t)N;
+        if (a != b && a < b + bytes && b < a + bytes)
+            return KDA_ERR_INVALID_ARGUMENT;
+    }
+    ReorderArgs p{};
+    p.parents = parents, p.beams = beams;
+    if (step_error_word(&p.err) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    for (int i = 0; i < tensors;) {
+        int used = 0;
+        int64_t most = 0;
+        for (; i < tensors && used < REORDER_TENSORS; i++) {
+            if (row_bytes[i] == 0)
+                continue;
+            p.src[used] = static_cast<const uint4 *>(src[i]);
+            p.dst[used] = static_cast<uint4 *>(dst[i]);
+            p.vecs[used] = row_bytes[i] / 16;
+            most = most > p.vecs[used] ? most : p.vecs[used];
+            used++;
+        }
+        if (used && launch_reorder(p, most, N / beams, used, st) != cudaSuccess)
+            return KDA_ERR_CUDA;
+    }
+    return KDA_OK;
+}

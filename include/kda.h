@@ -364,6 +364,119 @@ void kda_set_wait_limit(uint32_t polls);
 /* Largest dynamic shared memory one CTA of the forward kernels uses (for diagnostics). */
 size_t kda_fwd_smem_bytes(void);
 
+/* ------------------------------------------------------------------------------------------------
+ * The rest of a decoder step.  Hybrid decoders keep a KDA state in most layers and a softmax attention
+ * over a bounded cache in the others; these entry points are what such a step needs around kda_fwd and
+ * kda_fwd_recurrent: keys and values go into a paged cache with their position rotation
+ * (kda_kv_append), attention with a sliding window and sinks reads it (kda_window_attn), beam search
+ * selects over beams and vocabulary (kda_beam_select), and the states follow their beams
+ * (kda_state_reorder).  All are asynchronous on `stream`, allocate nothing the caller has to free,
+ * check their host-visible arguments before any launch, and can be captured into a CUDA graph (with
+ * a caller-owned workspace) once a call has run on the device outside a capture.
+ *
+ * The paged cache: k_cache and v_cache are bf16 [pages, Hkv, page, D], contiguous and 16-byte aligned;
+ * page is a power of two from 16 to 4096; D is 64 or 128.  block_table is int32 [N, max_pages]:
+ * position p of sequence n lies in row p % page of page block_table[n][p / page].  Entries of pages
+ * that hold no position a call touches may have any value (pages that left the window can be reused).
+ * kv_lens is int32 [N]: the tokens of each sequence in the cache INCLUDING the call's new ones.  With
+ * Q_n new tokens, token i has position kv_lens[n] - Q_n + i; a token whose position is negative has
+ * none: it is not stored and sees nothing.
+ *
+ * Token tensors are [B, T, heads, D] as for kda_fwd (B = N without cu_seqlens, B = 1 with it); the inputs'
+ * tokens may lie any number of elements apart (q_stride and so on, a multiple of 8 and at least heads x D:
+ * the rows of one projection's output); the heads of a token are contiguous.  Outputs are contiguous.
+ *
+ * Device-resident arrays (block_table, kv_lens, cu_seqlens, parents) are not checked before the launch.
+ * The kernels never access memory outside the buffers because of them: entries out of range are skipped
+ * or clamped and reported by kda_device_status as KDA_ERR_INVALID_ARGUMENT; the outputs of that call are
+ * not valid.
+ */
+
+/*
+ * kda_kv_append -- rotates and stores the call's new keys and values, and rotates its queries.
+ *
+ *   k, v           bf16 [B, T, Hkv, D], tokens k_stride / v_stride elements apart.
+ *   cos, sin       fp32 [positions, rotary / 2], row p for position p; both NULL: no rotation.
+ *   rotary         leading elements of a head that are rotated (a multiple of 16, at most D; ignored
+ *                  without cos); the others pass through.
+ *   interleaved    0: element i pairs with i + rotary / 2; 1: element 2 i pairs with 2 i + 1.  Pair i is
+ *                  (x, y) -> (x cos_i - y sin_i, y cos_i + x sin_i), in fp32, rounded once to bf16.
+ *   q, q_out       bf16 [B, T, Hq, D] (q's tokens q_stride apart; q_out contiguous), or both NULL with
+ *                  Hq = 0.  q_out may equal q where q is contiguous.  Tokens without a position are copied.
+ *
+ * Positions from `positions` on have no row: reported as above.
+ */
+kda_status_t kda_kv_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride, void *k_cache,
+                           void *v_cache, const int32_t *block_table, const int32_t *kv_lens, const float *cos,
+                           const float *sin, int rotary, int64_t positions, int interleaved, const void *q,
+                           int64_t q_stride, void *q_out, const int64_t *cu_seqlens, int N, int64_t T, int Hq,
+                           int Hkv, int D, int64_t pages, int page, int max_pages, kda_stream_t stream);
+
+/*
+ * kda_window_attn -- softmax attention over the paged cache with a sliding window and sinks.  A query at
+ * position p sees key j when j <= p and (j > p - window or j < sinks):
+ *   out = sum_j softmax_j(scale q.k_j) v_j,   lse = log sum_j exp(scale q.k_j)   over the visible j;
+ * a query that sees no key gets out = 0 and lse = -inf.  What lies in keys and values that a query does
+ * not see (stale rows, infinities, NaN) does not reach its output.
+ *
+ *   q              bf16 [B, T, Hq, D], tokens q_stride elements apart; Hq a multiple of Hkv: query head h
+ *                  reads key head h / (Hq / Hkv).
+ *   out            bf16 [B, T, Hq, D];   lse  fp32 [B, T, Hq] or NULL.
+ *   scale          finite, >= 0.
+ *   window         >= 1 (INT32_MAX: every earlier key);   sinks  >= 0.
+ *
+ * Scores, softmax statistics and the output's sums are fp32; the probabilities are rounded to bf16 for the
+ * tensor cores.  kda_window_attn takes its workspace (partial results where few queries face many keys)
+ * from the library's pool, kda_window_attn_ws from the caller: at least
+ * kda_window_attn_workspace_size(...) bytes on the current device, 256-byte aligned (NULL when 0).
+ */
+kda_status_t kda_window_attn(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+                             const int32_t *block_table, const int32_t *kv_lens, void *out, float *lse, float scale,
+                             int window, int sinks, const int64_t *cu_seqlens, int N, int64_t T, int Hq, int Hkv,
+                             int D, int64_t pages, int page, int max_pages, kda_stream_t stream);
+kda_status_t kda_window_attn_ws(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+                                const int32_t *block_table, const int32_t *kv_lens, void *out, float *lse,
+                                float scale, int window, int sinks, const int64_t *cu_seqlens, int N, int64_t T,
+                                int Hq, int Hkv, int D, int64_t pages, int page, int max_pages, void *workspace,
+                                size_t workspace_bytes, kda_stream_t stream);
+/* Workspace bytes of a call of these sizes (varlen: whether cu_seqlens is given); 0 for invalid sizes. */
+size_t kda_window_attn_workspace_size(int window, int sinks, int varlen, int N, int64_t T, int Hq, int Hkv, int D,
+                                      int page, int max_pages);
+
+/*
+ * kda_beam_select -- beam search's selection.  Row (b, w) of logits gives candidate (w, t) the score
+ *   c + l[t],  c = (beam_scores[b][w] - m) - log(sum_t exp(l[t] - m)),  m = max_t l[t]   (fp32)
+ * and a finished beam the one candidate (w, eos) with score beam_scores[b][w].  Every other candidate, every
+ * NaN logit, and every candidate of a row without a finite maximum or of a beam with score -inf or NaN scores
+ * -inf.  The K best of the batch entry's W x V candidates are written in order of score, ties in order of
+ * (w, t), -inf ones included.
+ *
+ *   logits         bf16 or fp32 [B, W, V] as dtype says, rows row_stride elements apart (>= V).
+ *   beam_scores    fp32 [B, W].   finished  uint8 [B, W] or NULL.   eos  token of finished beams, in [0, V).
+ *   scores         fp32 [B, K];   tokens  int32 [B, K];   parents  int32 [B, K]: b W + w, a row of the batch.
+ *   W <= 32, K <= 64, K <= W V, V <= 2^24, B W < 2^31.
+ * kda_beam_select_ws takes a caller-owned workspace of kda_beam_select_workspace_size bytes, 256-byte aligned.
+ */
+kda_status_t kda_beam_select(const void *logits, kda_dtype_t dtype, int64_t row_stride, const float *beam_scores,
+                             const uint8_t *finished, int eos, float *scores, int32_t *tokens, int32_t *parents,
+                             int B, int W, int V, int K, kda_stream_t stream);
+kda_status_t kda_beam_select_ws(const void *logits, kda_dtype_t dtype, int64_t row_stride, const float *beam_scores,
+                                const uint8_t *finished, int eos, float *scores, int32_t *tokens, int32_t *parents,
+                                int B, int W, int V, int K, void *workspace, size_t workspace_bytes,
+                                kda_stream_t stream);
+/* Workspace bytes of a selection of these sizes; 0 for invalid sizes. */
+size_t kda_beam_select_workspace_size(int B, int W, int V, int K);
+
+/*
+ * kda_state_reorder -- rows follow their beams: dst[i][n] = src[i][parents[n]] for every row n < N of every
+ * tensor i < tensors (states [N, H, 128, 128], cache rows, anything of row_bytes[i] contiguous bytes a row).
+ * Rows come in groups of `beams` (N a multiple of it, beams <= 32) and parents[n] lies in the group of n.
+ * src[i] == dst[i] reorders in place; otherwise the two do not overlap.  src, dst and row_bytes are HOST
+ * arrays read before the call returns; the tensors are 16-byte aligned and row_bytes a multiple of 16.
+ */
+kda_status_t kda_state_reorder(const void *const *src, void *const *dst, const int64_t *row_bytes, int tensors,
+                               const int32_t *parents, int N, int beams, kda_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
