@@ -788,6 +788,8 @@ extern "C" const char *kda_status_string(kda_status_t s)
     return "unknown status";
 }
 
+uint32_t kda::wait_limit() { return g_wait_polls.load(std::memory_order_relaxed); }
+
 extern "C" void kda_set_wait_limit(uint32_t polls) { g_wait_polls.store(polls, std::memory_order_relaxed); }
 
 extern "C" size_t kda_fwd_smem_bytes(void)

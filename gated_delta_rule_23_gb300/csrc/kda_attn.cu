@@ -1,36 +1,60 @@
 // kda_window_attn: argument checks and dispatch.
 #include "kda_attn.cuh"
 
+#include <cfloat>
+
 namespace kda {
 namespace {
 
 constexpr int ROW_THREADS = 256;
 
-// One warp per query row.
-template <int DIM> __global__ void __launch_bounds__(ROW_THREADS) kda_attn_row_kernel(const AttnArgs p, int64_t rows)
+// Joins the partial results of a split call: one warp per query row,
+//   out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s,  M = max m_s,
+// the splits always in order.  A row that does not come out finite is taken again from the definition (see
+// kda_attn_tiles.cu).
+template <int DIM> __global__ void __launch_bounds__(ROW_THREADS) kda_attn_join_kernel(const AttnArgs p, const AttnPlan plan)
 {
+    constexpr int PER = DIM / 32;
     const int64_t r = (int64_t)blockIdx.x * (ROW_THREADS / 32) + threadIdx.x / 32;
-    if (r >= rows)
+    if (r >= plan.rows)
         return;
-    const int64_t t = r / p.hq;
-    const int h = (int)(r % p.hq);
-    bool bad = false;
-    int n;
-    int64_t i, len_q;
-    if (p.tok.cu) {
-        int64_t bos;
-        n = seq_of_token(p.tok.cu, p.tok.N, t);
-        bad |= seq_range(p.tok.cu, n, p.tok.N, p.tok.T, bos, len_q);
-        i = t - bos;
-        if (i < 0 || i >= len_q)
-            i = -(int64_t)INT32_MAX - 1;
-    } else {
-        n = (int)(t / p.tok.T);
-        i = t - (int64_t)n * p.tok.T;
-        len_q = p.tok.T;
+    const int lane = threadIdx.x & 31;
+    float m = -INFINITY, l = 0.0f, o[PER];
+#pragma unroll
+    for (int e = 0; e < PER; e++)
+        o[e] = 0.0f;
+    for (int s = 0; s < plan.splits; s++)
+        m = fmaxf(m, plan.part_ml[s * plan.rows + r].x);
+    const float mu = m == -INFINITY ? 0.0f : m;
+    for (int s = 0; s < plan.splits; s++) {
+        const float2 ml = plan.part_ml[s * plan.rows + r];
+        if (ml.x == -INFINITY && ml.y == 0.0f)
+            continue;                     // a split without a visible key
+        const float w = exp2f(ml.x - mu);
+        const float *src = plan.part_o + (s * plan.rows + r) * DIM + lane * PER;
+        l += w * ml.y;
+#pragma unroll
+        for (int e = 0; e < PER; e++)
+            o[e] = fmaf(w, src[e], o[e]);
     }
-    attn_row<DIM>(p, n, t, h, cache_len(p.cache, n, bad) - len_q + i, bad);
-    report(p.err, bad, DEVERR_CU_SEQLENS);
+    bool finite = l <= FLT_MAX;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    __nv_bfloat16 *out = p.out + r * DIM + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; e++) {
+        finite &= fabsf(o[e]) <= FLT_MAX;
+        out[e] = __float2bfloat16_rn(l == 0.0f ? 0.0f : o[e] * inv);
+    }
+    if (p.lse && lane == 0)
+        p.lse[r] = l == 0.0f ? -INFINITY : LN2 * (m + log2f(l));
+    if (__any_sync(0xffffffffu, !finite)) {
+        const int64_t t = r / p.hq;
+        bool bad = false;
+        int64_t i, len;
+        const int n = token_place(p.tok, t, i, len, bad);
+        if (i >= 0 && i < len)
+            attn_row<DIM>(p, n, t, (int)(r % p.hq), cache_len(p.cache, n, bad) - len + i, bad);
+    }
 }
 
 kda_status_t check_attn(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
@@ -76,18 +100,54 @@ AttnArgs make_attn(const void *q, int64_t q_stride, const void *k_cache, const v
     return p;
 }
 
-cudaError_t launch_attn(const AttnArgs &p, int64_t tokens, cudaStream_t st)
+// Keys a tile of query rows can need at most.
+int64_t most_keys(int window, int sinks, int64_t T, int page, int max_pages)
 {
-    const int64_t rows = tokens * p.hq;
-    const unsigned grid = (unsigned)((rows + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32));
-    if (p.cache.dim == 128)
-        kda_attn_row_kernel<128><<<grid, ROW_THREADS, 0, st>>>(p, rows);
-    else
-        kda_attn_row_kernel<64><<<grid, ROW_THREADS, 0, st>>>(p, rows);
-    return cudaGetLastError();
+    const int64_t cap = (int64_t)max_pages * page, need = (int64_t)window + sinks + T;
+    return need < cap ? need : cap;
+}
+
+// The cut of a call (sizes only, so that the workspace is known beforehand).  The keys are split while that still
+// adds tiles for idle SMs, two key tiles to a split at least.
+AttnPlan make_plan(int window, int sinks, bool varlen, int N, int64_t T, int Hq, int Hkv, int page, int max_pages)
+{
+    AttnPlan plan{};
+    const int group = Hq / Hkv;
+    const int64_t tokens = varlen ? T : (int64_t)N * T;
+    plan.rows = tokens * Hq;
+    plan.tiles = varlen ? (T * group + (int64_t)(ATTN_ROWS - 1) * N) / ATTN_ROWS
+                        : (int64_t)N * ((T * group + ATTN_ROWS - 1) / ATTN_ROWS);
+    if (plan.tiles > T * group && varlen)
+        plan.tiles = T * group;           // a tile holds a row at least
+    const int sms = device_sms();
+    const int64_t ctas = plan.tiles * Hkv;
+    const int64_t key_tiles = (most_keys(window, sinks, T < ATTN_ROWS ? T : ATTN_ROWS, page, max_pages) + 127) / 128 + 1;
+    int64_t s = ctas > 0 ? sms / ctas : 1;
+    s = s < key_tiles / 2 ? s : key_tiles / 2;
+    plan.splits = s < 1 ? 1 : (s > 64 ? 64 : (int)s);
+    plan.wait_polls = wait_limit();
+    return plan;
+}
+
+size_t plan_bytes(const AttnPlan &plan, int dim)
+{
+    if (plan.splits == 1)
+        return 0;
+    return (size_t)plan.splits * plan.rows * (dim * sizeof(float) + sizeof(float2));
 }
 
 }  // namespace
+
+cudaError_t launch_attn_join(const AttnArgs &p, const AttnPlan &plan, cudaStream_t st)
+{
+    const unsigned grid = (unsigned)((plan.rows + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32));
+    if (p.cache.dim == 128)
+        kda_attn_join_kernel<128><<<grid, ROW_THREADS, 0, st>>>(p, plan);
+    else
+        kda_attn_join_kernel<64><<<grid, ROW_THREADS, 0, st>>>(p, plan);
+    return cudaGetLastError();
+}
+
 }  // namespace kda
 
 using namespace kda;
@@ -95,7 +155,10 @@ using namespace kda;
 extern "C" size_t kda_window_attn_workspace_size(int window, int sinks, int varlen, int N, int64_t T, int Hq, int Hkv,
                                                  int D, int page, int max_pages)
 {
-    return 0;
+    if (window < 1 || sinks < 0 || N < 1 || T < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv || (D != 64 && D != 128) || page < 16 ||
+        max_pages < 1 || T > INT32_MAX || (varlen ? T : (int64_t)N * T) * Hq > INT32_MAX)
+        return 0;
+    return plan_bytes(make_plan(window, sinks, varlen != 0, N, T, Hq, Hkv, page, max_pages), D);
 }
 
 extern "C" kda_status_t kda_window_attn_ws(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
@@ -119,7 +182,14 @@ extern "C" kda_status_t kda_window_attn_ws(const void *q, int64_t q_stride, cons
                            cu_seqlens, N, T, Hq, Hkv, D, pages, page, max_pages);
     if (step_error_word(&p.err) != cudaSuccess)
         return KDA_ERR_CUDA;
-    return launch_attn(p, tokens, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    AttnPlan plan = make_plan(window, sinks, cu_seqlens != nullptr, N, T, Hq, Hkv, page, max_pages);
+    plan.part_o = static_cast<float *>(workspace);
+    plan.part_ml = reinterpret_cast<float2 *>(plan.part_o + (size_t)plan.splits * plan.rows * D);
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_attn_tiles(p, plan, st);
+    if (e == cudaSuccess && plan.splits > 1)
+        e = launch_attn_join(p, plan, st);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 extern "C" kda_status_t kda_window_attn(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,

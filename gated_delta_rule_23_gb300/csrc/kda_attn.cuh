@@ -18,7 +18,41 @@ struct AttnArgs {
     unsigned int *err;
 };
 
+// How a call is cut: every (sequence, key head) has group x Q_n query rows, row r being token r / group and head
+// r % group of the group (so that heads sharing keys share a tile); rows come in tiles, and the keys a tile needs are
+// split `splits` ways, the partial results joined by a second kernel when there is more than one.
+constexpr int ATTN_ROWS = 256;   // query rows of a tile
+
+struct AttnPlan {
+    int splits;
+    int64_t tiles;          // row tiles of all sequences (ragged: an upper bound)
+    float *part_o;          // [splits][tokens * hq][dim] fp32, unnormalised (workspace)
+    float2 *part_ml;        // [splits][tokens * hq]: running maximum (base 2) and sum
+    int64_t rows;           // tokens * hq
+    uint32_t wait_polls;
+};
+
+cudaError_t launch_attn_tiles(const AttnArgs &p, const AttnPlan &plan, cudaStream_t stream);
+cudaError_t launch_attn_join(const AttnArgs &p, const AttnPlan &plan, cudaStream_t stream);
+
 constexpr float LN2 = 0.6931471805599453f;
+
+// Sequence, index within it and length of token t's sequence, by a whole warp; an index outside [0, len) for a token
+// that a malformed cu_seqlens gives to nobody.
+__device__ __forceinline__ int token_place(const Tokens &tok, int64_t t, int64_t &i, int64_t &len, bool &bad)
+{
+    if (!tok.cu) {
+        len = tok.T;
+        const int n = (int)(t / tok.T);
+        i = t - (int64_t)n * tok.T;
+        return n;
+    }
+    const int n = seq_of_token(tok.cu, tok.N, t);
+    int64_t bos;
+    bad |= seq_range(tok.cu, n, tok.N, tok.T, bos, len);
+    i = t - bos;
+    return n;
+}
 
 // One query row (token t of the batch, head h) at position pos, by a whole warp, straight from the definition:
 // every visible key in order, with the running maximum m and sum l of the softmax in base 2.  Keys that the row

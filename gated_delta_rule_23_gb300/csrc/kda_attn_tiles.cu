@@ -1,0 +1,617 @@
+// Windowed attention over the paged cache on the tensor cores: 256 query rows a CTA, keys in tiles of 128.
+//
+// Rows.  A CTA owns rows [256 x, 256 x + 256) of one (sequence, key head), in two halves of 128 (row = token * group
+// + head of the group, so heads that share keys share the tile).  Keys.  The tile's rows need the sinks and the
+// positions from the first row's window on: two ranges of positions, cut into granules of at most 32 positions that
+// lie in one page each, and strung together to a list of "virtual" keys; 4 to 8 granules make a key tile, so a few
+// sinks cost a granule and not a tile.  Granules past the end are loaded from outside the cache (zeros).
+//
+// Per key tile and half:  S = Q K^T (tcgen05, fp32 in tensor memory);  P = 2^(scale S - m) with one thread a row, no
+// shuffles;  O += P V with P (bf16) read from tensor memory where S was.  The halves take turns: while one half's
+// threads are at their exponentials, the tensor cores work for the other.  The running maximum m is moved (and O and l
+// rescaled) only when a row's maximum has grown by more than 2^8: any m gives the same quotient, and 2^8 is far from
+// overflow in the fp32 sums.
+//
+// Warps 0..3 and 4..7: the halves' softmax and epilogue; warp 8: bulk tensor copies (K and V tiles in a ring); warp 9:
+// tensor-core issue.
+//
+// A key that a row does not see gets P = 0.  0 x v is NaN for an infinite or NaN v, and the matrix product has no way
+// to skip it: rows past the sequence's end are cleared in shared memory, and an output row that does not come out
+// finite is taken again from the definition, key by key, by attn_row.
+#include "kda_attn.cuh"
+
+#include <cuda.h>
+
+#include <atomic>
+#include <cfloat>
+
+namespace kda {
+namespace {
+
+constexpr int KEYS = 128;                    // keys of a tile
+constexpr int THREADS = 320;
+constexpr int HALF = 128;                    // rows of a half
+constexpr int TMEM_COLS = 512;
+constexpr int TM_S = 0, TM_O = 256;          // columns: S of both halves (128 each), O of both halves
+constexpr float RESCALE_AT = 8.0f;           // base-2 growth of the maximum that moves it
+constexpr unsigned FULL = 0xffffffffu;
+
+template <int DIM> struct Shape {
+    static constexpr int TILE = KEYS * DIM * 2;              // bytes of a K or V tile, and of a half's Q
+    static constexpr int SLOTS = DIM == 128 ? 5 : 10;        // ring: K0 V0 K1 V1 ...
+    static constexpr int BAR = 2 * TILE + SLOTS * TILE;      // mbarriers behind Q and the ring
+    static constexpr int SMEM = 1024 + BAR + 256;            // 1024: alignment of the swizzle atoms
+};
+
+struct Tile {             // what every warp of the CTA knows about its work
+    int n, kvh, split;
+    int64_t len_q, bos;   // tokens of the sequence, first token of it in the batch
+    int64_t len;          // its tokens in the cache
+    int64_t row0;         // first row of the tile
+    int rows;             // rows of the tile, 1..256
+    int granule;          // positions of a granule
+    int64_t sink_span;    // virtual keys of the sinks (a multiple of the granule)
+    int64_t start;        // position of virtual key sink_span
+    int64_t virt;         // virtual keys in all
+    int t0, t1;           // key tiles of this split
+    int lo[2], hi[2];     // of them, the ones a half needs
+};
+
+__device__ __forceinline__ int64_t virt_pos(const Tile &w, int64_t v) { return v < w.sink_span ? v : v - w.sink_span + w.start; }
+
+// Position of row r (of the sequence).
+__device__ __forceinline__ int64_t row_pos(const AttnArgs &p, const Tile &w, int64_t r) { return w.len - w.len_q + r / p.group; }
+
+// Finds the CTA's tile; false when there is none.  By a whole warp.
+__device__ bool find_tile(const AttnArgs &p, const AttnPlan &plan, Tile &w, bool &bad)
+{
+    const int lane = threadIdx.x & 31;
+    // heaviest first where the work grows along a sequence: the last tiles of all key heads
+    int64_t x = blockIdx.x;
+    w.kvh = (int)(x % p.cache.hkv);
+    x /= p.cache.hkv;
+    w.split = blockIdx.y;
+    int64_t tile;
+    if (p.tok.cu) {
+        int64_t before = 0;
+        bool found = false;
+        for (int base = 0; base < p.tok.N && !found; base += 32) {
+            const int n = base + lane;
+            int64_t bos = 0, len = 0, cnt = 0;
+            if (n < p.tok.N) {
+                bad |= seq_range(p.tok.cu, n, p.tok.N, p.tok.T, bos, len);
+                cnt = (len * p.group + ATTN_ROWS - 1) / ATTN_ROWS;
+            }
+            int64_t sum = cnt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(FULL, sum, o);
+                if (lane >= o)
+                    sum += y;
+            }
+            const unsigned m = __ballot_sync(FULL, before + sum > x);
+            if (m) {
+                const int src = __ffs(m) - 1;
+                w.n = base + src;
+                w.bos = __shfl_sync(FULL, bos, src);
+                w.len_q = __shfl_sync(FULL, len, src);
+                tile = x - (before + __shfl_sync(FULL, sum - cnt, src));
+                found = true;
+            }
+            before += __shfl_sync(FULL, sum, 31);
+        }
+        if (!found)
+            return false;
+    } else {
+        const int64_t per = (p.tok.T * p.group + ATTN_ROWS - 1) / ATTN_ROWS;
+        w.n = (int)(x % p.tok.N);
+        tile = per - 1 - x / p.tok.N;
+        w.len_q = p.tok.T;
+        w.bos = w.n * p.tok.T;
+    }
+    w.row0 = tile * ATTN_ROWS;
+    const int64_t left = w.len_q * p.group - w.row0;
+    w.rows = (int)(left < ATTN_ROWS ? left : ATTN_ROWS);
+    w.len = cache_len(p.cache, w.n, bad);
+    const int page = 1 << p.cache.page_shift;
+    w.granule = page < 32 ? page : 32;
+    const int64_t g = w.granule;
+    const int64_t p0 = row_pos(p, w, w.row0), p1 = row_pos(p, w, w.row0 + w.rows - 1);
+    if (p1 < 0) {                                   // nothing before the first token
+        w.sink_span = w.start = w.virt = 0;
+    } else {
+        int64_t lo = p0 - p.window + 1;
+        lo = lo < 0 ? 0 : lo / g * g;
+        int64_t sink = ((int64_t)p.sinks + g - 1) / g * g;
+        if (lo <= sink)
+            sink = lo = 0;                          // one range
+        w.sink_span = sink;
+        w.start = lo;
+        w.virt = sink + (p1 + 1 - lo);
+    }
+    const int64_t tiles = (w.virt + KEYS - 1) / KEYS;
+    w.t0 = (int)(tiles * w.split / plan.splits);
+    w.t1 = (int)(tiles * (w.split + 1) / plan.splits);
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const int first = h * HALF, last = min(w.rows, first + HALF) - 1;
+        w.lo[h] = w.hi[h] = w.t0;
+        if (first > last)
+            continue;
+        const int64_t a = row_pos(p, w, w.row0 + first) - p.window + 1, b = row_pos(p, w, w.row0 + last);
+        if (b < 0)
+            continue;
+        // the half's window, in tiles; tiles with sinks count for every half
+        int64_t lo = a <= w.start ? w.sink_span : a - w.start + w.sink_span;
+        lo = w.sink_span > 0 || p.sinks > 0 ? 0 : lo / KEYS;
+        const int64_t hi = (b - w.start + w.sink_span) / KEYS + 1;
+        w.lo[h] = (int)(lo < w.t0 ? w.t0 : (lo > w.t1 ? w.t1 : lo));
+        w.hi[h] = (int)(hi < w.t0 ? w.t0 : (hi > w.t1 ? w.t1 : hi));
+        if (w.hi[h] < w.lo[h])
+            w.hi[h] = w.lo[h];
+    }
+    return true;
+}
+
+// ---------------------------------------------------------------- tensor cores and copies
+// 128-byte swizzled shared-memory matrix descriptor.  K-major: sbo between groups of 8 rows, lbo unused; MN-major: sbo
+// between groups of 8 along K, lbo between blocks of 64 along MN.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo)
+{
+    return umma_desc(saddr, lbo, sbo) | ((uint64_t)2 << 61);
+}
+// fp32 accumulator, bf16 A and B, A K-major, B K-major or (mn) MN-major
+__device__ __forceinline__ constexpr uint32_t idesc_bf16(int M, int N, bool mn)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int acc)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t mbar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(mbar) : "memory");
+}
+#define R8(a, i) "=f"(a[i]), "=f"(a[i + 1]), "=f"(a[i + 2]), "=f"(a[i + 3]), "=f"(a[i + 4]), "=f"(a[i + 5]), "=f"(a[i + 6]), "=f"(a[i + 7])
+// 64 columns of the warp's 32 lanes, one row a thread
+__device__ __forceinline__ void tmem_ld64(uint32_t addr, float *s)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,"
+                 "%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : R8(s, 0), R8(s, 8), R8(s, 16), R8(s, 24), R8(s, 32), R8(s, 40), R8(s, 48), R8(s, 56)
+                 : "r"(addr) : "memory");
+}
+#undef R8
+
+// bits a..b (inclusive, any integers) of a 128-bit mask, word w
+__device__ __forceinline__ uint32_t range_word(int64_t a, int64_t b, int w)
+{
+    const int64_t lo = a - 32 * w, hi = b - 32 * w;
+    if (hi < 0 || lo > 31 || hi < lo)
+        return 0;
+    const uint32_t x = hi >= 31 ? FULL : (2u << (int)hi) - 1u;
+    return lo <= 0 ? x : x & (FULL << (int)lo);
+}
+
+template <int DIM>
+__global__ void __launch_bounds__(THREADS, 1)
+kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap)
+{
+    using S = Shape<DIM>;
+    constexpr int CB = DIM / 64;                 // 64-column blocks of a row
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    unsigned char *const smem = smem_raw + (base - smem_u32(smem_raw));
+    const uint32_t sm_q = base, sm_ring = base + 2 * S::TILE, bar = base + S::BAR;
+    const uint32_t b_full = bar, b_empty = bar + 8 * S::SLOTS, b_q = bar + 16 * S::SLOTS, b_s = b_q + 8, b_p = b_s + 16,
+                   b_o = b_p + 16, b_drain = b_o + 16;
+    __shared__ uint32_t tmem_slot;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+
+    Tile w;
+    bool bad = false;
+    if (!find_tile(p, plan, w, bad))
+        return;                                  // uniform over the CTA
+    if (tid == 0) {
+        for (int i = 0; i < S::SLOTS; i++) {
+            mbar_init(b_full + 8 * i, 1);
+            mbar_init(b_empty + 8 * i, 1);
+        }
+        mbar_init(b_q, 8);
+        for (int h = 0; h < 2; h++) {
+            mbar_init(b_s + 8 * h, 1);
+            mbar_init(b_p + 8 * h, HALF);
+            mbar_init(b_o + 8 * h, 1);
+        }
+        mbar_init(b_drain, 1);
+        mbar_fence_init();
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                     "r"(TMEM_COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int tiles = w.t1 - w.t0;
+    bool timeout = false;
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ Q, softmax, epilogue
+        const int h = warp / 4;
+        const int r = tid;                                       // row of the tile
+        const bool mine = r < w.rows;
+        const int64_t R = w.row0 + r;
+        const int64_t tok = w.bos + (mine ? R / p.group : 0);
+        const int head = w.kvh * p.group + (int)(mine ? R % p.group : 0);
+        const int64_t pos = mine ? row_pos(p, w, R) : -1;
+        // Q: a warp loads its own 32 rows, lanes along a row; rows past the end are zeros
+        for (int i = lane; i < 32 * (DIM / 8); i += 32) {
+            const int row = i / (DIM / 8) + 32 * warp, c = i % (DIM / 8);
+            const bool in = row < w.rows;
+            const int64_t RR = w.row0 + (in ? row : 0);
+            const __nv_bfloat16 *src = p.q + (w.bos + RR / p.group) * p.q_stride +
+                                       (int64_t)(w.kvh * p.group + RR % p.group) * DIM + c * 8;
+            const int rh = row & (HALF - 1);
+            cp_async16(sm_q + h * S::TILE + (c / 8) * (HALF * 128) + rh * 128 + (((c & 7) ^ (rh & 7)) << 4), src, in);
+        }
+        cp_async_commit();
+        cp_async_wait_all();
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(b_q);
+
+        const uint32_t tm_lane = (uint32_t)(warp & 3) << 21;     // the warp's 32 lanes
+        const uint32_t tm_s = tmem + TM_S + h * 128 + tm_lane, tm_o = tmem + TM_O + h * 128 + tm_lane;
+        float m = -INFINITY, l = 0.0f;
+        int n_s = 0;
+        for (int t = w.lo[h]; t < w.hi[h]; t++, n_s++) {
+            const int64_t v0 = (int64_t)t * KEYS;
+            // what the row sees of the tile, as 128 bits
+            uint32_t mask[4];
+            {
+                const int64_t a = pos - p.window + 1;
+                // columns of the window range, then those of the sink range
+                const int64_t wa = (a > w.start ? a : w.start) - w.start + w.sink_span - v0, wb = pos - w.start + w.sink_span - v0;
+                const int64_t sb = (w.sink_span > 0 ? min((int64_t)p.sinks, pos + 1) : 0) - 1 - v0;
+                const int64_t ka = (w.sink_span > 0 ? (int64_t)0 : min((int64_t)p.sinks, pos + 1)) - 1 - v0;
+#pragma unroll
+                for (int x = 0; x < 4; x++) {
+                    mask[x] = range_word(wa, wb, x);
+                    if (p.sinks > 0)
+                        mask[x] |= range_word(-v0, sb > ka ? sb : ka, x);
+                }
+            }
+            const bool all = __all_sync(FULL, (mask[0] & mask[1] & mask[2] & mask[3]) == FULL);
+            // the sequence's end inside the tile: what lies behind it in its page is cleared from V (K's scores are masked)
+            const int64_t end_v = w.len - w.start + w.sink_span - v0;
+            if (end_v > 0 && end_v < KEYS && end_v % w.granule) {
+                const int it = 2 * (t - w.t0) + 1, slot = it % S::SLOTS;
+                if (!mbar_wait(b_full + 8 * slot, (it / S::SLOTS) & 1, plan.wait_polls)) {
+                    timeout = true;
+                    break;
+                }
+                const int first = (int)end_v, last = (int)((end_v + w.granule - 1) / w.granule * w.granule);
+                uint4 *v = reinterpret_cast<uint4 *>(smem + 2 * S::TILE + slot * S::TILE);
+                for (int i = tid & (HALF - 1); i < (last - first) * 8 * CB; i += HALF)
+                    v[(i / ((last - first) * 8)) * (KEYS * 8) + first * 8 + i % ((last - first) * 8)] = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+            }
+            if (!mbar_wait(b_s + 8 * h, n_s & 1, plan.wait_polls)) {
+                timeout = true;
+                break;
+            }
+            tc_fence_after();
+            float s[128];
+            tmem_ld64(tm_s, s);
+            tmem_ld64(tm_s + 64, s + 64);
+            if (!all) {
+#pragma unroll
+                for (int c = 0; c < 128; c++)
+                    s[c] = (mask[c / 32] >> (c % 32)) & 1 ? s[c] : -INFINITY;
+            }
+            float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+#pragma unroll
+            for (int c = 4; c < 128; c += 4) {
+                mx0 = fmaxf(mx0, s[c]);
+                mx1 = fmaxf(mx1, s[c + 1]);
+                mx2 = fmaxf(mx2, s[c + 2]);
+                mx3 = fmaxf(mx3, s[c + 3]);
+            }
+            const float top = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * p.scale_log2;
+            // 0 x inf (scale 0) is NaN and leaves m alone
+            const bool move = top > m + RESCALE_AT;
+            if (n_s == 0) {
+                if (top > m)
+                    m = top;
+            } else if (__any_sync(FULL, move)) {
+                const float a = move ? ex2_approx(m - top) : 1.0f;
+                if (move)
+                    m = top;
+                l *= a;
+#pragma unroll
+                for (int c = 0; c < DIM; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(tm_o + c, o);
+#pragma unroll
+                    for (int e = 0; e < 32; e++)
+                        o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                    tmem_st32(tm_o + c, o);
+                }
+            }
+            const float mu = m == -INFINITY ? 0.0f : m;
+            const f2 sc = f2_pack(p.scale_log2, p.scale_log2), mm = f2_pack(-mu, -mu);
+            float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+            for (int c = 0; c < 128; c += 64) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int e = 0; e < 32; e++) {
+                    const f2 x = f2_fma(f2_pack(s[c + 2 * e], s[c + 2 * e + 1]), sc, mm);
+                    const float a = ex2_approx(f2_lo(x)), b = ex2_approx(f2_hi(x));
+                    l0 += a;
+                    l1 += b;
+                    const __nv_bfloat162 y = __floats2bfloat162_rn(a, b);
+                    pk[e] = *reinterpret_cast<const uint32_t *>(&y);
+                }
+                tmem_st32(tm_s + c / 2, pk);
+            }
+            l += l0 + l1;
+            tc_fence_before();
+            mbar_arrive(b_p + 8 * h);
+        }
+        // epilogue: the row's thread scales and stores it
+        if (n_s > 0 && !timeout) {
+            if (!mbar_wait(b_o + 8 * h, 0, plan.wait_polls))
+                timeout = true;
+            tc_fence_after();
+        }
+        if (!__any_sync(FULL, timeout)) {
+            bool finite = l <= FLT_MAX;
+            const int64_t at = tok * p.hq + head;
+            const bool split = plan.splits > 1;
+            const float inv = split ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+#pragma unroll
+            for (int c = 0; c < DIM; c += 32) {
+                uint32_t o[32];
+                if (n_s > 0)
+                    tmem_ld32(tm_o + c, o);
+#pragma unroll
+                for (int e = 0; e < 32; e++) {
+                    const float x = n_s > 0 ? __uint_as_float(o[e]) : 0.0f;
+                    finite &= fabsf(x) <= FLT_MAX;
+                    o[e] = __float_as_uint(split || l != 0.0f ? x * inv : 0.0f);
+                }
+                if (!mine)
+                    continue;
+                if (split) {
+                    float4 *dst = reinterpret_cast<float4 *>(plan.part_o + (w.split * plan.rows + at) * DIM + c);
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                             __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+                } else {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * DIM + c);
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * j]),
+                                                                            __uint_as_float(o[8 * e + 2 * j + 1]));
+                            y[j] = *reinterpret_cast<const uint32_t *>(&b2);
+                        }
+                        dst[e] = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                }
+            }
+            if (mine && split)
+                plan.part_ml[w.split * plan.rows + at] = make_float2(m, l);
+            else if (mine && p.lse)
+                p.lse[at] = l == 0.0f ? -INFINITY : LN2 * (m + log2f(l));
+            __syncwarp();                     // the rows' first stores come before the ones below
+            unsigned again = __ballot_sync(FULL, mine && !finite && !split);
+            while (again) {
+                const int src = __ffs(again) - 1;
+                again &= again - 1;
+                attn_row<DIM>(p, w.n, __shfl_sync(FULL, tok, src), __shfl_sync(FULL, head, src), __shfl_sync(FULL, pos, src), bad);
+            }
+        }
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ copies
+        const int ng = KEYS / w.granule;
+        const int64_t last = virt_pos(w, w.virt > 0 ? w.virt - 1 : 0);
+        int issued = 0;
+        for (int t = 0; t < tiles && !timeout; t++) {
+            int y = INT32_MAX - 4096;                            // outside the cache: zeros
+            if (lane < ng) {
+                const int64_t v = (int64_t)(w.t0 + t) * KEYS + lane * w.granule;
+                const int64_t j = virt_pos(w, v);
+                if (v < w.virt && j <= last && j < w.len) {
+                    const int32_t id = p.cache.table[(int64_t)w.n * p.cache.max_pages + (j >> p.cache.page_shift)];
+                    if (id >= 0 && id < p.cache.pages)
+                        y = (int)((((int64_t)id * p.cache.hkv + w.kvh) << p.cache.page_shift) + (j & ((1 << p.cache.page_shift) - 1)));
+                    else
+                        bad = true;
+                }
+            }
+#pragma unroll
+            for (int kv = 0; kv < 2; kv++) {
+                const int it = 2 * t + kv, slot = it % S::SLOTS;
+                if (it >= S::SLOTS && !mbar_wait(b_empty + 8 * slot, ((it / S::SLOTS) - 1) & 1, plan.wait_polls))
+                    timeout = true;
+                if (__any_sync(FULL, timeout)) {
+                    timeout = true;
+                    break;
+                }
+                if (lane == 0)
+                    mbar_expect_tx(b_full + 8 * slot, S::TILE);
+                __syncwarp();
+                if (lane < ng) {
+#pragma unroll
+                    for (int cb = 0; cb < CB; cb++)
+                        tma_load_2d(sm_ring + slot * S::TILE + cb * (KEYS * 128) + lane * w.granule * 128, kv ? &vmap : &kmap,
+                                    cb * 64, y, b_full + 8 * slot);
+                }
+                issued = it + 1;
+            }
+        }
+        // no copy is in flight when the CTA leaves, also where the work was given up
+        for (int it = issued > S::SLOTS ? issued - S::SLOTS : 0; it < issued; it++)
+            mbar_wait(b_full + 8 * (it % S::SLOTS), (it / S::SLOTS) & 1);
+    } else if (lane == 0) {
+        // ------------------------------------------------------------ tensor-core issue
+        const uint32_t id_s = idesc_bf16(HALF, KEYS, false), id_o = idesc_bf16(HALF, DIM, true);
+        int n_p[2] = {0, 0};
+        auto wait = [&](uint32_t b, int parity) {
+            if (!timeout && !mbar_wait(b, parity, plan.wait_polls))
+                timeout = true;
+        };
+        // S of half h and tile t (relative to t0)
+        auto issue_s = [&](int h, int t) {
+            const int g = w.t0 + t;
+            if (timeout || g < w.lo[h] || g >= w.hi[h])
+                return;
+            const int slot = (2 * t) % S::SLOTS;
+            tc_fence_after();
+            const uint32_t a = sm_q + h * S::TILE, b = sm_ring + slot * S::TILE;
+#pragma unroll
+            for (int k = 0; k < DIM / 16; k++) {
+                const uint32_t off = (k / 4) * (KEYS * 128) + (k % 4) * 32;
+                mma_f16_ss(tmem + TM_S + h * 128, desc_sw128(a + off, 16, 1024), desc_sw128(b + off, 16, 1024), id_s, k > 0);
+            }
+            umma_commit(b_s + 8 * h);
+        };
+        wait(b_q, 0);
+        for (int t = 0; t < tiles && !timeout; t++) {
+            if (t == 0) {
+                wait(b_full, 0);
+                issue_s(0, 0);
+                issue_s(1, 0);
+                if (!timeout)
+                    umma_commit(b_empty + 8 * 0);
+            }
+            const int it = 2 * t + 1, slot = it % S::SLOTS;
+            wait(b_full + 8 * slot, (it / S::SLOTS) & 1);
+            for (int h = 0; h < 2 && !timeout; h++) {
+                const int g = w.t0 + t;
+                if (g >= w.lo[h] && g < w.hi[h]) {
+                    wait(b_p + 8 * h, n_p[h] & 1);
+                    if (timeout)
+                        break;
+                    tc_fence_after();
+                    const uint32_t b = sm_ring + slot * S::TILE;
+#pragma unroll
+                    for (int k = 0; k < KEYS / 16; k++)
+                        mma_f16_ts(tmem + TM_O + h * 128, tmem + TM_S + h * 128 + k * 8,
+                                   desc_sw128(b + k * 2048, KEYS * 128, 1024), id_o, n_p[h] > 0 || k > 0);
+                    n_p[h]++;
+                    if (g + 1 == w.hi[h])
+                        umma_commit(b_o + 8 * h);
+                }
+                if (t + 1 < tiles) {
+                    if (h == 0)
+                        wait(b_full + 8 * ((2 * t + 2) % S::SLOTS), ((2 * t + 2) / S::SLOTS) & 1);
+                    issue_s(h, t + 1);
+                }
+            }
+            if (!timeout) {
+                umma_commit(b_empty + 8 * slot);
+                if (t + 1 < tiles)
+                    umma_commit(b_empty + 8 * ((2 * t + 2) % S::SLOTS));
+            }
+        }
+        // everything issued has to be through before tensor memory is freed
+        umma_commit(b_drain);
+        mbar_wait(b_drain, 0);
+    }
+    report(p.err, bad, DEVERR_CU_SEQLENS);
+    report(p.err, timeout, DEVERR_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS));
+    }
+}
+
+// ---------------------------------------------------------------- host
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+cudaError_t encode_fn(EncodeTiled *fn)
+{
+    static std::atomic<void *> cached;
+    void *f = cached.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+        if (e != cudaSuccess)
+            return e;
+        if (found != cudaDriverEntryPointSuccess || !f)
+            return cudaErrorNotSupported;
+        cached.store(f, std::memory_order_release);
+    }
+    *fn = reinterpret_cast<EncodeTiled>(f);
+    return cudaSuccess;
+}
+
+// The cache as a matrix of rows [pages * hkv * page][dim]; a box is 64 columns of one granule's rows.
+cudaError_t make_map(CUtensorMap *map, const void *ptr, const PagedCache &c)
+{
+    EncodeTiled fn;
+    const cudaError_t e = encode_fn(&fn);
+    if (e != cudaSuccess)
+        return e;
+    const int page = 1 << c.page_shift;
+    const cuuint64_t dims[2] = {(cuuint64_t)c.dim, (cuuint64_t)c.pages * c.hkv * page};
+    const cuuint64_t strides[1] = {(cuuint64_t)c.dim * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)(page < 32 ? page : 32)}, step[2] = {1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, step,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int DIM> cudaError_t launch_tiles(const AttnArgs &p, const AttnPlan &plan, cudaStream_t st)
+{
+    static std::atomic<uint64_t> ready;      // devices whose kernel attribute is set
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && !(ready.load() >> dev & 1)) {
+        e = cudaFuncSetAttribute(kda_attn_tiles_kernel<DIM>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<DIM>::SMEM);
+        if (e == cudaSuccess)
+            ready.fetch_or(1ull << dev);
+    }
+    CUtensorMap kmap, vmap;
+    if (e == cudaSuccess)
+        e = make_map(&kmap, p.cache.k, p.cache);
+    if (e == cudaSuccess)
+        e = make_map(&vmap, p.cache.v, p.cache);
+    if (e != cudaSuccess)
+        return e;
+    const dim3 grid((unsigned)(plan.tiles * p.cache.hkv), (unsigned)plan.splits);
+    kda_attn_tiles_kernel<DIM><<<grid, THREADS, Shape<DIM>::SMEM, st>>>(p, plan, kmap, vmap);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tiles(const AttnArgs &p, const AttnPlan &plan, cudaStream_t st)
+{
+    return p.cache.dim == 128 ? launch_tiles<128>(p, plan, st) : launch_tiles<64>(p, plan, st);
+}
+
+}  // namespace kda

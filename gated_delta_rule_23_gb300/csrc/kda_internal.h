@@ -74,6 +74,8 @@ cudaError_t recurrent_read_and_clear_error(unsigned int *flag);
 // Device address of the word these kernels report in on the current device (looked up once per device).
 cudaError_t step_error_word(unsigned int **word);
 cudaError_t step_read_and_clear_error(unsigned int *flag);
+// Polls a wait of the tensor-core kernels may take (kda_set_wait_limit).
+uint32_t wait_limit();
 // SM count of the current device (looked up once per device); 0 when it cannot be read.
 int device_sms();
 inline bool is_aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
