@@ -420,6 +420,18 @@ def test_beam_strided_logits(kda):
         assert all(torch.equal(p, q) for p, q in zip(a, b))
 
 
+@pytest.mark.parametrize("v", [101, 4097, 33003])
+def test_beam_equal_beams_of_odd_rows_tie(kda, v):
+    """Equal beams whose rows are aligned differently have equal scores: their candidates tie by beam."""
+    gen = _gen(v)
+    for dtype in (torch.float32, torch.bfloat16):
+        x = torch.randn((1, 1, v), generator=gen, device="cuda").to(dtype).expand(2, 8, v).contiguous()
+        best, tokens, parents = _select(kda, x, torch.full((2, 8), -3.0, device="cuda"), 8)
+        top = int(x[0, 0].float().argmax())
+        assert tokens.tolist() == [[top] * 8] * 2 and parents.tolist() == [list(range(8)), list(range(8, 16))]
+        assert bool((best == best[0, 0]).all())
+
+
 def test_beam_workspace_and_stream(kda):
     gen = _gen(12)
     x = torch.randn((2, 4, 50001), generator=gen, device="cuda")
