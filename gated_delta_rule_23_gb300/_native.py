@@ -22,6 +22,8 @@ UNITS = ["kda_api", "kda_prep", "kda_recur", "kda_recurrent", "kda_decode", "kda
 SOURCES = [os.path.join(CSRC, u + ".cu") for u in UNITS]
 HEADERS = [os.path.join(INCLUDE, "kda.h"), os.path.join(CSRC, "kda_device.cuh"), os.path.join(CSRC, "kda_internal.h"),
            os.path.join(CSRC, "kda_plan.h"), os.path.join(CSRC, "kda_step.cuh"), os.path.join(CSRC, "kda_attn.cuh")]
+BINDING_SOURCE = os.path.join(CSRC, "kda_binding.cpp")
+BINDING_PATH = os.path.join(BUILD_DIR, "kda_binding.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 _lock = threading.Lock()
@@ -34,14 +36,29 @@ def nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
-    return any(os.path.getmtime(s) > t for s in SOURCES + HEADERS)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
+    return any(os.path.getmtime(s) > t for s in SOURCES + HEADERS + [BINDING_SOURCE])
+
+
+def _binding_command(out: str) -> List[str]:
+    """The host compiler's command for csrc/kda_binding.cpp, a Python module over torch's C++ tensors."""
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            "-I" + INCLUDE, "-I" + os.path.join(t, "include"),
+            "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"),
+            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"), "-o", out, BINDING_SOURCE,
+            "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/*.cu (sm_103a, -O3, -lineinfo), one process per unit, and link _build/libkda.so."""
+    """Compile csrc/*.cu (sm_103a, -O3, -lineinfo), one process per unit, and link _build/libkda.so; compile the
+    decoder-step operators' Python module (csrc/kda_binding.cpp) beside it."""
     with _lock:
         if not force and not _stale():
             return LIB_PATH
@@ -55,16 +72,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
             obj = os.path.join(BUILD_DIR, u + tag + ".o")
             objs.append(obj)
             procs.append(subprocess.Popen(common + ["-c", "-o", obj, src]))
+        binding = BINDING_PATH + tag
+        procs.append(subprocess.Popen(_binding_command(binding)))
         codes = [pr.wait() for pr in procs]
         try:
-            for src, rc in zip(SOURCES, codes):
+            for src, rc in zip(SOURCES + [BINDING_SOURCE], codes):
                 if rc != 0:
-                    raise subprocess.CalledProcessError(rc, f"nvcc {src}")
+                    raise subprocess.CalledProcessError(rc, f"compiling {src}")
             tmp = LIB_PATH + tag
             subprocess.run([nvcc(), *ARCH_FLAGS, "-shared", "-o", tmp, *objs], check=True)
             os.replace(tmp, LIB_PATH)
+            os.replace(binding, BINDING_PATH)
         finally:
-            for o in objs:
+            for o in objs + [binding]:
                 if os.path.exists(o):
                     os.remove(o)
         return LIB_PATH
@@ -135,6 +155,25 @@ def load() -> ctypes.CDLL:
         lib.kda_state_reorder.restype = I
         _lib = lib
     return _lib
+
+
+_binding = None
+
+
+def binding():
+    """The module kda_binding (csrc/kda_binding.cpp), bound to libkda.so."""
+    global _binding
+    if _binding is None:
+        import importlib.util
+        lib = load()
+        spec = importlib.util.spec_from_file_location("kda_binding", BINDING_PATH)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+                   for f in ("kda_kv_append", "kda_window_attn", "kda_window_attn_ws", "kda_beam_select",
+                             "kda_beam_select_ws", "kda_state_reorder")))
+        _binding = mod
+    return _binding
 
 
 def declared_functions() -> List[str]:

@@ -4,6 +4,10 @@ A decode or prefill step of a hybrid decoder around ``kda_fwd`` / ``kda_fwd_recu
 rotated keys and values in a paged cache, ``kda_window_attn`` attends to it through a sliding window with sinks,
 ``kda_beam_select`` picks the next beams from the logits, ``kda_state_reorder`` moves the states after them.  The
 caller passes CUDA tensors and pre-allocated outputs; every step of the computation runs in libkda.so.
+
+Every function first offers its arguments to the compiled binding (csrc/kda_binding.cpp), which makes the call when they
+are exactly what it expects and otherwise declines; the code here then checks them one by one, and makes the call (an
+empty batch, another device than the current one) or says what is wrong.
 """
 from __future__ import annotations
 
@@ -90,6 +94,11 @@ def _workspace(workspace: torch.Tensor, dev: torch.device) -> int:
     return workspace.numel()
 
 
+def _raise(rc: int) -> None:
+    if rc != KDA_OK:
+        raise KDAError(rc)
+
+
 def kda_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                   block_table: torch.Tensor, kv_lens: torch.Tensor, cos: Optional[torch.Tensor] = None,
                   sin: Optional[torch.Tensor] = None, interleaved: bool = False, q: Optional[torch.Tensor] = None,
@@ -102,6 +111,10 @@ def kda_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cac
     in the cache including these; cos, sin: fp32 [positions, rotary / 2] (None: no rotation); cu_seqlens: int64
     [N + 1] with B = 1.  ``q_out`` may be ``q``.  Runs asynchronously on ``stream`` (default: the current stream).
     """
+    rc = _native.binding().kv_append(k, v, k_cache, v_cache, block_table, kv_lens, cos, sin, interleaved, q, q_out,
+                                     cu_seqlens, None if stream is None else stream.cuda_stream)
+    if rc is not None:
+        return _raise(rc)
     dev = _device(k, "kda_kv_append")
     if k.dim() != 4:
         raise ValueError("k must be [B, T, Hkv, D]")
@@ -149,6 +162,10 @@ def kda_window_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     ``workspace``: optional uint8 tensor of ``window_attn_workspace_size`` bytes; without it the library's pool
     provides one where the call needs it.
     """
+    rc = _native.binding().window_attn(q, k_cache, v_cache, block_table, kv_lens, out, window, sinks, scale, lse,
+                                       cu_seqlens, None if stream is None else stream.cuda_stream, workspace)
+    if rc is not None:
+        return _raise(rc)
     dev = _device(q, "kda_window_attn")
     if q.dim() != 4:
         raise ValueError("q must be [B, T, Hq, D]")
@@ -190,6 +207,10 @@ def kda_beam_select(logits: torch.Tensor, beam_scores: torch.Tensor, scores: tor
     [B, W], beams whose one continuation is ``eos`` at their own score.  Writes scores fp32, tokens int32 and parents
     int32 [B, K], best first, ties to the lower (beam, token); parents are rows b * W + w of the batch.
     """
+    rc = _native.binding().beam_select(logits, beam_scores, scores, tokens, parents, finished, eos,
+                                       None if stream is None else stream.cuda_stream, workspace)
+    if rc is not None:
+        return _raise(rc)
     dev = _device(logits, "kda_beam_select")
     if logits.dim() != 3:
         raise ValueError("logits must be [B, W, V]")
@@ -233,6 +254,9 @@ def kda_state_reorder(src: Tensors, parents: torch.Tensor, beams: int, dst: Opti
     """
     src = [src] if isinstance(src, torch.Tensor) else list(src)
     dst = src if dst is None else ([dst] if isinstance(dst, torch.Tensor) else list(dst))
+    rc = _native.binding().state_reorder(src, dst, parents, beams, None if stream is None else stream.cuda_stream)
+    if rc is not None:
+        return _raise(rc)
     if len(src) != len(dst):
         raise ValueError(f"dst: expected {len(src)} tensors, got {len(dst)}")
     dev = _device(parents, "kda_state_reorder")

@@ -492,6 +492,37 @@ def test_reorder_malformed_parents_are_reported(kda):
     kda.device_status()
 
 
+# ---------------------------------------------------------------------------------------------- the two ways in
+def test_calls_the_compiled_binding_declines(kda, monkeypatch):
+    """The checked way through ctypes makes the same calls as the compiled binding."""
+    from gated_delta_rule_23_gb300 import _native
+
+    class Declines:
+        def __getattr__(self, name):
+            return lambda *a: None
+
+    def everything():
+        gen = _gen(30)
+        k_cache, v_cache, table = step_ref.make_cache([90, 40], 2, 64, 16, gen, "cuda")
+        lens = torch.tensor([90, 40], dtype=torch.int32, device="cuda")
+        x = torch.randn((2, 3, 8, 64), generator=gen, device="cuda").to(torch.bfloat16)
+        angle = torch.rand((100, 16), generator=gen, device="cuda")
+        q_out, out = torch.empty_like(x), torch.empty_like(x)
+        kda.kda_kv_append(x[:, :, :2], x[:, :, 2:4], k_cache, v_cache, table, lens, angle.cos(), angle.sin(), True, x, q_out)
+        lse = torch.empty((2, 3, 8), device="cuda")
+        kda.kda_window_attn(q_out, k_cache, v_cache, table, lens, out, 2 ** 40, sinks=1, lse=lse)
+        logits = torch.randn((2, 2, 77), generator=gen, device="cuda")
+        best, tokens, parents = _select(kda, logits, torch.zeros((2, 2), device="cuda"), 2,
+                                        torch.tensor([[True, False]] * 2, device="cuda"), 5)
+        kda.kda_state_reorder(x.flatten(0, 1)[:4], parents.view(-1), 2)
+        torch.cuda.synchronize()
+        return [k_cache, v_cache, q_out, out, lse, best, tokens, parents, x]
+    a = everything()
+    monkeypatch.setattr(_native, "_binding", Declines())
+    b = everything()
+    assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+
+
 # ---------------------------------------------------------------------------------------------- graphs
 def test_step_operators_in_a_graph(kda):
     """A captured step replays with the bits of direct calls on the data then in the buffers."""
