@@ -130,6 +130,43 @@ __device__ uint64_t group_bound(Pick &sh, uint64_t best, int n)
     return sh.bound;
 }
 
+// The same on values alone: the n-th best (ties counted) of the groups' best values; below every value when there are
+// fewer groups with one.
+__device__ float group_bound_value(Pick &sh, float best, int n)
+{
+    const int size = n <= 32 ? 4 : 2, groups = THREADS / size;
+    float *g = reinterpret_cast<float *>(sh.group);
+    best = fmaxf(best, __shfl_xor_sync(FULL, best, 1));
+    const float y = __shfl_xor_sync(FULL, best, 2);
+    if (size == 4)
+        best = fmaxf(best, y);
+    if (threadIdx.x % size == 0)
+        g[threadIdx.x / size] = best;
+    uint32_t *lowest = reinterpret_cast<uint32_t *>(&sh.bound);
+    if (threadIdx.x == 0) {
+        *lowest = FULL;
+        sh.count = 0;
+    }
+    __syncthreads();
+    if (threadIdx.x < groups) {
+        const float x = g[threadIdx.x];
+        int above = 0;
+        const float4 *q = reinterpret_cast<const float4 *>(g);
+#pragma unroll 8
+        for (int i = 0; i < groups / 4; i++) {
+            const float4 v = q[i];
+            above += (v.x > x) + (v.y > x) + (v.z > x) + (v.w > x);
+        }
+        // the smallest of the values that fewer than n are above
+        const uint32_t u = (uint32_t)(key_of(x, 0) >> 32);
+        const uint32_t low = __reduce_min_sync(__activemask(), above < n ? u : FULL);
+        if (threadIdx.x % 32 == 0)
+            atomicMin(lowest, low);
+    }
+    __syncthreads();
+    return key_value((uint64_t)*lowest << 32);
+}
+
 // Ranks the gathered keys (count of them, all distinct) and hands the best n to put(rank, key).
 template <typename F> __device__ void rank_gathered(const Pick &sh, int count, int n, F put)
 {
@@ -214,7 +251,7 @@ template <typename T> __device__ __forceinline__ uint4 load_shifted(const T *l, 
 
 // One CTA per (chunk, row): PER logits a thread in registers, 16-byte vectors strided over the CTA.  Which thread takes
 // which token, and so the order of the sums, does not depend on the row's alignment: equal rows get equal scores.
-template <typename T, int PER> __global__ void __launch_bounds__(THREADS) kda_beam_chunks_kernel(const BeamArgs p)
+template <typename T, int PER> __global__ void __launch_bounds__(THREADS, PER > 16 ? 4 : 6) kda_beam_chunks_kernel(const BeamArgs p)
 {
     constexpr int N = Vec<T>::N;
     __shared__ __align__(16) Pick sh;
@@ -228,66 +265,112 @@ template <typename T, int PER> __global__ void __launch_bounds__(THREADS) kda_be
     const T *l = static_cast<const T *>(p.logits) + row * p.row_stride;
     const int off = (int)(reinterpret_cast<uintptr_t>(l) & 15);
     const int first = chunk * (THREADS * PER);       // token of the chunk's first element
+    const bool whole = first + THREADS * PER <= p.V;
     float v[PER];
 #pragma unroll
     for (int i = 0; i < PER / N; i++)
         unpack(load_shifted(l, first + (i * THREADS + tid) * N, off, p.V), v + i * N, l);
-    float best = -INFINITY;
-    int at = -1;                             // token of the thread's best
+    auto token = [&](int i) { return first + ((i / N) * THREADS + tid) * N + i % N; };
+    if (!whole) {
 #pragma unroll
-    for (int i = 0; i < PER; i++) {
-        const int t = first + ((i / N) * THREADS + tid) * N + i % N;
-        v[i] = t < p.V ? no_nan(v[i]) : -INFINITY;
-        // the first token that exists, then every larger one: the lowest token of the largest value
-        if (t < p.V && (at < 0 || v[i] > best)) {
-            best = v[i];
-            at = t;
-        }
+        for (int i = 0; i < PER; i++)
+            v[i] = token(i) < p.V ? v[i] : -INFINITY;
     }
-    // maximum and sum of the chunk, warp by warp
+    // maximum and sum of the chunk, warp by warp (fmaxf passes over NaN)
+    float best = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PER; i++)
+        best = fmaxf(best, v[i]);
     float m = best;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
     const float mu = fabsf(m) <= FLT_MAX ? m : 0.0f;
-    float sum = 0.0f;
+    // exp(v - mu) = 2^(v L - c) 2^(c - mu L), c = mu L rounded: the second factor is one for the whole warp
+    const float c = mu * LOG2E;
+    const f2 scale = f2_pack(LOG2E, LOG2E), shift = f2_pack(-c, -c);
+    float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-    for (int i = 0; i < PER; i++)
-        sum += ex2_approx((v[i] - mu) * LOG2E);
+    for (int i = 0; i < PER; i += 2) {
+        const f2 x = f2_fma(f2_pack(v[i], v[i + 1]), scale, shift);
+        s0 += ex2_approx(f2_lo(x));
+        s1 += ex2_approx(f2_hi(x));
+    }
+    float sum = s0 + s1;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         sum += __shfl_xor_sync(FULL, sum, o);
+    sum *= ex2_approx(-fmaf(mu, LOG2E, -c));
+    if (sum != sum || fabsf(mu) > 1e30f) {   // NaN logits (they count as -inf), or a product past fp32's range
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            v[i] = no_nan(v[i]);
+            sum += ex2_approx((v[i] - mu) * LOG2E);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            sum += __shfl_xor_sync(FULL, sum, o);
+    }
     if (lane == 0)
         part[warp] = make_float2(m, sum);
 
-    const uint64_t key = at >= 0 ? key_of(best, at) : 0;
-    const uint64_t bound = group_bound(sh, key, n);
-    if (key >= bound) {
+    // In a whole chunk the bound is taken on values alone; a chunk with an end, one whose n-th value is not finite, and
+    // one with more ties than can be gathered go by keys.
+    bool done = false;
+    if (whole) {
+        const float bound = group_bound_value(sh, best, n);
+        if (fabsf(bound) <= FLT_MAX) {
+            if (best >= bound) {
 #pragma unroll
-        for (int i = 0; i < PER; i++) {
-            const int t = first + ((i / N) * THREADS + tid) * N + i % N;
-            if (t >= p.V)
-                continue;
-            const uint64_t x = key_of(v[i], t);
-            if (x >= bound) {
-                const int to = atomicAdd(&sh.count, 1);
-                if (to < CAP)
-                    sh.cand[to] = x;
+                for (int i = 0; i < PER; i++)
+                    if (v[i] >= bound) {
+                        const int to = atomicAdd(&sh.count, 1);
+                        if (to < CAP)
+                            sh.cand[to] = key_of(v[i], token(i));
+                    }
             }
+            __syncthreads();
+            done = sh.count <= CAP;
+            __syncthreads();
         }
     }
-    __syncthreads();
+    if (!done) {
+        uint64_t key = 0;
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            v[i] = no_nan(v[i]);
+            const uint64_t x = token(i) < p.V ? key_of(v[i], token(i)) : 0;
+            key = x > key ? x : key;
+        }
+        const uint64_t bound = group_bound(sh, key, n);
+        if (key >= bound) {
+#pragma unroll
+            for (int i = 0; i < PER; i++) {
+                const uint64_t x = token(i) < p.V ? key_of(v[i], token(i)) : 0;
+                if (x >= bound) {
+                    const int to = atomicAdd(&sh.count, 1);
+                    if (to < CAP)
+                        sh.cand[to] = x;
+                }
+            }
+        }
+        __syncthreads();
+    }
     const int64_t slot = blockIdx.x;
     uint64_t *list = p.lists + slot * n;
-    if (tid == 0) {
-        float M = part[0].x;
-        for (int i = 1; i < THREADS / 32; i++)
-            M = fmaxf(M, part[i].x);
-        float s = 0.0f;
-        for (int i = 0; i < THREADS / 32; i++)
-            if (fabsf(part[i].x) <= FLT_MAX)
-                s += part[i].y * expf(part[i].x - M);
-        p.stats[slot] = make_float2(M, s);
+    if (warp == 0) {
+        const float2 x = lane < THREADS / 32 ? part[lane] : make_float2(-INFINITY, 0.0f);
+        float M = x.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+        float s = fabsf(x.x) <= FLT_MAX ? x.y * expf(x.x - M) : 0.0f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            s += __shfl_xor_sync(FULL, s, o);
+        if (lane == 0)
+            p.stats[slot] = make_float2(M, s);
     }
     const int count = sh.count;
     if (count <= CAP) {
@@ -301,8 +384,7 @@ template <typename T, int PER> __global__ void __launch_bounds__(THREADS) kda_be
             uint64_t b = 0;
 #pragma unroll
             for (int i = 0; i < PER; i++) {
-                const int t = first + ((i / N) * THREADS + tid) * N + i % N;
-                const uint64_t x = t < p.V ? key_of(v[i], t) : 0;
+                const uint64_t x = token(i) < p.V ? key_of(v[i], token(i)) : 0;
                 if (x < last && x > b)
                     b = x;
             }
