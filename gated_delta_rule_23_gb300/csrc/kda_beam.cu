@@ -20,7 +20,8 @@
 namespace kda {
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 256;              // of the chunk kernel
+constexpr int PICK_THREADS = 512;
 constexpr int CAP = 2048;                 // keys gathered for ranking
 constexpr unsigned FULL = 0xffffffffu;
 
@@ -33,7 +34,7 @@ struct BeamArgs {
     float *scores;
     int32_t *tokens, *parents;
     int B, W, V, K;
-    int chunks;              // of a row
+    int chunks, span;        // chunks of a row, pieces of a chunk
     float2 *stats;           // [B W][chunks]: maximum, sum of exp(l - maximum)   (workspace)
     uint64_t *lists;         // [B W][chunks][K + 1]: best logits' keys, 0 past the last
 };
@@ -71,7 +72,7 @@ __device__ __forceinline__ float neighbour(float x, bool up, bool bf16)
     return __uint_as_float(u);
 }
 
-__device__ uint64_t block_max(uint64_t x, uint64_t *sh)
+template <int NT> __device__ uint64_t block_max(uint64_t x, uint64_t *sh)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -84,29 +85,30 @@ __device__ uint64_t block_max(uint64_t x, uint64_t *sh)
     __syncthreads();
     x = sh[0];
 #pragma unroll
-    for (int i = 1; i < THREADS / 32; i++)
+    for (int i = 1; i < NT / 32; i++)
         x = x > sh[i] ? x : sh[i];
     return x;
 }
 
 struct Pick {
-    uint64_t group[THREADS / 2];   // best key of each group of threads
+    uint64_t group[128];           // best key of each group of threads
     uint64_t cand[CAP];
-    uint64_t red[THREADS / 32];
+    uint64_t red[32];
     uint64_t bound;
     int count;
 };
 
-// The n-th best of the groups' best keys (1 when fewer than n groups have one: every key is let through).  Groups of
-// 4 threads while n <= 32, of 2 up to 65, so that there are twice as many groups as wanted keys and few get through.
-__device__ uint64_t group_bound(Pick &sh, uint64_t best, int n)
+// Groups: twice as many as wanted keys at least, so that few more than the wanted ones get past the bound.
+__device__ __forceinline__ int groups_for(int n) { return n <= 32 ? 64 : 128; }
+
+// The n-th best of the groups' best keys; 1 (every key gets through) when fewer than n groups have one.
+template <int NT> __device__ uint64_t group_bound(Pick &sh, uint64_t best, int n)
 {
-    const int size = n <= 32 ? 4 : 2, groups = THREADS / size;
-    uint64_t y = __shfl_xor_sync(FULL, best, 1);
-    best = best > y ? best : y;
-    y = __shfl_xor_sync(FULL, best, 2);
-    if (size == 4)
+    const int groups = groups_for(n), size = NT / groups, lane = threadIdx.x % 32;
+    for (int o = 1; o < size; o <<= 1) {
+        const uint64_t y = __shfl_xor_sync(FULL, best, o);
         best = best > y ? best : y;
+    }
     if (threadIdx.x % size == 0)
         sh.group[threadIdx.x / size] = best;
     if (threadIdx.x == 0) {
@@ -114,32 +116,25 @@ __device__ uint64_t group_bound(Pick &sh, uint64_t best, int n)
         sh.count = 0;
     }
     __syncthreads();
-    if (threadIdx.x < groups) {
-        const uint64_t x = sh.group[threadIdx.x];
+    for (int i = threadIdx.x / 32; i < groups; i += NT / 32) {     // a warp ranks a group
+        const uint64_t x = sh.group[i];
         int rank = 0;
-        const ulonglong2 *g = reinterpret_cast<const ulonglong2 *>(sh.group);
-#pragma unroll 8
-        for (int i = 0; i < groups / 2; i++) {
-            const ulonglong2 v = g[i];
-            rank += (v.x > x) + (v.y > x);
-        }
-        if (x != 0 && rank == n - 1)
+        for (int j = 0; j < groups; j += 32)
+            rank += __popc(__ballot_sync(FULL, sh.group[j + lane] > x));
+        if (lane == 0 && x != 0 && rank == n - 1)
             sh.bound = x;
     }
     __syncthreads();
     return sh.bound;
 }
 
-// The same on values alone: the n-th best (ties counted) of the groups' best values; below every value when there are
-// fewer groups with one.
-__device__ float group_bound_value(Pick &sh, float best, int n)
+// The same on values alone: the n-th best (ties counted) of the groups' best values, -inf when fewer have one.
+template <int NT> __device__ float group_bound_value(Pick &sh, float best, int n)
 {
-    const int size = n <= 32 ? 4 : 2, groups = THREADS / size;
+    const int groups = groups_for(n), size = NT / groups, lane = threadIdx.x % 32;
     float *g = reinterpret_cast<float *>(sh.group);
-    best = fmaxf(best, __shfl_xor_sync(FULL, best, 1));
-    const float y = __shfl_xor_sync(FULL, best, 2);
-    if (size == 4)
-        best = fmaxf(best, y);
+    for (int o = 1; o < size; o <<= 1)
+        best = fmaxf(best, __shfl_xor_sync(FULL, best, o));
     if (threadIdx.x % size == 0)
         g[threadIdx.x / size] = best;
     uint32_t *lowest = reinterpret_cast<uint32_t *>(&sh.bound);
@@ -148,36 +143,41 @@ __device__ float group_bound_value(Pick &sh, float best, int n)
         sh.count = 0;
     }
     __syncthreads();
-    if (threadIdx.x < groups) {
-        const float x = g[threadIdx.x];
+    uint32_t low = FULL;
+    for (int i = threadIdx.x / 32; i < groups; i += NT / 32) {
+        const float x = g[i];
         int above = 0;
-        const float4 *q = reinterpret_cast<const float4 *>(g);
-#pragma unroll 8
-        for (int i = 0; i < groups / 4; i++) {
-            const float4 v = q[i];
-            above += (v.x > x) + (v.y > x) + (v.z > x) + (v.w > x);
-        }
+        for (int j = 0; j < groups; j += 32)
+            above += __popc(__ballot_sync(FULL, g[j + lane] > x));
         // the smallest of the values that fewer than n are above
-        const uint32_t u = (uint32_t)(key_of(x, 0) >> 32);
-        const uint32_t low = __reduce_min_sync(__activemask(), above < n ? u : FULL);
-        if (threadIdx.x % 32 == 0)
-            atomicMin(lowest, low);
+        if (above < n)
+            low = min(low, (uint32_t)(key_of(x, 0) >> 32));
     }
+    if (lane == 0)
+        atomicMin(lowest, low);
     __syncthreads();
     return key_value((uint64_t)*lowest << 32);
 }
 
-// Ranks the gathered keys (count of them, all distinct) and hands the best n to put(rank, key).
-template <typename F> __device__ void rank_gathered(const Pick &sh, int count, int n, F put)
+// Ranks the gathered keys (count of them, all distinct) and hands the best n to put(rank, key), by one thread each.
+template <int NT, typename F> __device__ void rank_gathered(const Pick &sh, int count, int n, F put)
 {
-    for (int i = threadIdx.x; i < count; i += THREADS) {
+    const int lane = threadIdx.x % 32;
+    for (int i = threadIdx.x / 32; i < count; i += NT / 32) {      // a warp ranks a key
         const uint64_t x = sh.cand[i];
         int rank = 0;
-        for (int j = 0; j < count; j++)
+        for (int j = lane; j < count; j += 32)
             rank += sh.cand[j] > x;
-        if (rank < n)
+        rank = __reduce_add_sync(FULL, rank);
+        if (lane == 0 && rank < n)
             put(rank, x);
     }
+}
+__device__ __forceinline__ void gather(Pick &sh, uint64_t key)
+{
+    const int to = atomicAdd(&sh.count, 1);
+    if (to < CAP)
+        sh.cand[to] = key;
 }
 
 template <typename T> struct Vec {
@@ -218,21 +218,17 @@ __device__ __forceinline__ uint4 load_aligned(const __nv_bfloat16 *l, int t, int
             u[e / 2] |= (uint32_t)reinterpret_cast<const unsigned short *>(l)[t + e] << (16 * (e % 2));
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
-// The row's 16 bytes from element t on, in a row that lies `off` bytes past a 16-byte boundary: two aligned vectors, the
-// second one the next lane's first, shifted together.  By a whole warp, lane i at t + i * (16 / size).
-template <typename T> __device__ __forceinline__ uint4 load_shifted(const T *l, int t, int off, int V)
+// 16 bytes that lie `off` bytes (not 0) past a 16-byte boundary: a holds the aligned 16 bytes they begin in, of lane i of
+// a warp at 16 i; the next lane's a is the second half, and lane 31 reads it (element t of the row l on).
+template <typename T> __device__ __forceinline__ uint4 shifted(const uint4 &a, const T *l, int t, int off, int V)
 {
-    const int back = off / (int)sizeof(T);
-    const uint4 a = load_aligned(l, t - back, V);
-    if (off == 0)
-        return a;
     uint4 b;
     b.x = __shfl_down_sync(FULL, a.x, 1);
     b.y = __shfl_down_sync(FULL, a.y, 1);
     b.z = __shfl_down_sync(FULL, a.z, 1);
     b.w = __shfl_down_sync(FULL, a.w, 1);
     if ((threadIdx.x & 31) == 31)
-        b = load_aligned(l, t - back + 16 / (int)sizeof(T), V);
+        b = load_aligned(l, t, V);
     uint32_t x[5];
     const int words = off / 4;
     if (words == 0)
@@ -249,13 +245,56 @@ template <typename T> __device__ __forceinline__ uint4 load_shifted(const T *l, 
     return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// One CTA per (chunk, row): PER logits a thread in registers, 16-byte vectors strided over the CTA.  Which thread takes
-// which token, and so the order of the sums, does not depend on the row's alignment: equal rows get equal scores.
-template <typename T, int PER> __global__ void __launch_bounds__(THREADS, PER > 16 ? 4 : 6) kda_beam_chunks_kernel(const BeamArgs p)
+// The n best keys of tokens [t0, t1) of a row, whatever they are, straight from memory: the bound on keys, and where more
+// than can be gathered lie above it (large values crowded into few threads) one key at a time.
+template <typename T>
+__device__ __noinline__ void list_by_keys(Pick &sh, const T *l, int t0, int t1, int n, uint64_t *list)
 {
-    constexpr int N = Vec<T>::N;
+    uint64_t best = 0;
+    for (int t = t0 + threadIdx.x; t < t1; t += THREADS) {
+        const uint64_t x = key_of(no_nan(load_logit(l + t)), t);
+        best = x > best ? x : best;
+    }
+    const uint64_t bound = group_bound<THREADS>(sh, best, n);
+    if (best >= bound)
+        for (int t = t0 + threadIdx.x; t < t1; t += THREADS) {
+            const uint64_t x = key_of(no_nan(load_logit(l + t)), t);
+            if (x >= bound)
+                gather(sh, x);
+        }
+    __syncthreads();
+    const int count = sh.count;
+    if (count <= CAP) {
+        rank_gathered<THREADS>(sh, count, n, [&](int r, uint64_t k) { list[r] = k; });
+        for (int r = count + threadIdx.x; r < n; r += THREADS)
+            list[r] = 0;
+        return;
+    }
+    uint64_t last = ~0ull;
+    for (int r = 0; r < n; r++) {
+        uint64_t b = 0;
+        for (int t = t0 + threadIdx.x; t < t1; t += THREADS) {
+            const uint64_t x = key_of(no_nan(load_logit(l + t)), t);
+            if (x < last && x > b)
+                b = x;
+        }
+        last = block_max<THREADS>(b, sh.red);
+        if (threadIdx.x == 0)
+            list[r] = last;
+    }
+}
+
+// One CTA per (chunk, row); a chunk is p.span pieces of PER x THREADS logits, the next piece's loads in flight while one
+// is worked on.  The first piece gives the bound: later ones only compare with it (a piece as good as the first adds
+// about K + 1 keys), so there is no barrier between pieces.  Which thread takes which token, and so the order of the
+// sums, does not depend on the row's alignment: equal rows get equal scores.
+constexpr int MAX_SPAN = 4;
+
+template <typename T, int PER> __global__ void __launch_bounds__(THREADS, PER > 16 ? 2 : 6) kda_beam_chunks_kernel(const BeamArgs p)
+{
+    constexpr int N = Vec<T>::N, NV = PER / N, PIECE = THREADS * PER;
     __shared__ __align__(16) Pick sh;
-    __shared__ float2 part[THREADS / 32];
+    __shared__ float2 part[MAX_SPAN * THREADS / 32];
     asm volatile("griddepcontrol.launch_dependents;");
     const int64_t row = blockIdx.x / p.chunks;
     const int chunk = (int)(blockIdx.x % p.chunks);
@@ -263,104 +302,104 @@ template <typename T, int PER> __global__ void __launch_bounds__(THREADS, PER > 
     if (p.finished && p.finished[row])
         return;                              // its one candidate needs no logits
     const T *l = static_cast<const T *>(p.logits) + row * p.row_stride;
-    const int off = (int)(reinterpret_cast<uintptr_t>(l) & 15);
-    const int first = chunk * (THREADS * PER);       // token of the chunk's first element
-    const bool whole = first + THREADS * PER <= p.V;
-    float v[PER];
+    const int off = (int)(reinterpret_cast<uintptr_t>(l) & 15), back = off / (int)sizeof(T);
+    const int t0 = chunk * (PIECE * p.span), t1 = min(p.V, t0 + PIECE * p.span);
+    uint4 next[NV];
+    auto load = [&](int first) {             // all loads before anything waits for one
+        if (first >= back && first + PIECE <= p.V) {
 #pragma unroll
-    for (int i = 0; i < PER / N; i++)
-        unpack(load_shifted(l, first + (i * THREADS + tid) * N, off, p.V), v + i * N, l);
-    auto token = [&](int i) { return first + ((i / N) * THREADS + tid) * N + i % N; };
-    if (!whole) {
+            for (int i = 0; i < NV; i++)
+                next[i] = __ldcs(reinterpret_cast<const uint4 *>(l + (first + (i * THREADS + tid) * N - back)));
+        } else {
 #pragma unroll
-        for (int i = 0; i < PER; i++)
-            v[i] = token(i) < p.V ? v[i] : -INFINITY;
-    }
-    // maximum and sum of the chunk, warp by warp (fmaxf passes over NaN)
-    float best = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < PER; i++)
-        best = fmaxf(best, v[i]);
-    float m = best;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-    const float mu = fabsf(m) <= FLT_MAX ? m : 0.0f;
-    // exp(v - mu) = 2^(v L - c) 2^(c - mu L), c = mu L rounded: the second factor is one for the whole warp
-    const float c = mu * LOG2E;
-    const f2 scale = f2_pack(LOG2E, LOG2E), shift = f2_pack(-c, -c);
-    float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < PER; i += 2) {
-        const f2 x = f2_fma(f2_pack(v[i], v[i + 1]), scale, shift);
-        s0 += ex2_approx(f2_lo(x));
-        s1 += ex2_approx(f2_hi(x));
-    }
-    float sum = s0 + s1;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        sum += __shfl_xor_sync(FULL, sum, o);
-    sum *= ex2_approx(-fmaf(mu, LOG2E, -c));
-    if (sum != sum || fabsf(mu) > 1e30f) {   // NaN logits (they count as -inf), or a product past fp32's range
-        sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < PER; i++) {
-            v[i] = no_nan(v[i]);
-            sum += ex2_approx((v[i] - mu) * LOG2E);
+            for (int i = 0; i < NV; i++)
+                next[i] = load_aligned(l, first + (i * THREADS + tid) * N - back, p.V);
         }
+    };
+    load(t0);
+    float bound = -INFINITY;
+    bool by_keys = false;
+    int pieces = 0;
+    for (int first = t0; first < t1; first += PIECE, pieces++) {
+        float v[PER];
+        if (off) {
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                next[i] = shifted(next[i], l, first + (i * THREADS + tid) * N - back + N, off, p.V);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            unpack(next[i], v + i * N, l);
+        if (first + PIECE < t1)
+            load(first + PIECE);
+        auto token = [&](int i) { return first + ((i / N) * THREADS + tid) * N + i % N; };
+        if (first + PIECE > p.V) {
+#pragma unroll
+            for (int i = 0; i < PER; i++)
+                v[i] = token(i) < p.V ? v[i] : -INFINITY;
+        }
+        // maximum and sum of the piece, warp by warp (fmaxf passes over NaN)
+        float best = -INFINITY, top[NV];     // of the thread, and of each of its vectors
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            top[i] = v[i * N];
+#pragma unroll
+            for (int e = 1; e < N; e++)
+                top[i] = fmaxf(top[i], v[i * N + e]);
+            best = fmaxf(best, top[i]);
+        }
+        float m = best;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+        const float mu = fabsf(m) <= FLT_MAX ? m : 0.0f;
+        // exp(v - mu) = 2^(v L - c) 2^(c - mu L), c = mu L rounded: the second factor is one for the whole warp
+        const float c = mu * LOG2E;
+        const f2 scale = f2_pack(LOG2E, LOG2E), shift = f2_pack(-c, -c);
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; i += 2) {
+            const f2 x = f2_fma(f2_pack(v[i], v[i + 1]), scale, shift);
+            s0 += ex2_approx(f2_lo(x));
+            s1 += ex2_approx(f2_hi(x));
+        }
+        float sum = s0 + s1;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             sum += __shfl_xor_sync(FULL, sum, o);
-    }
-    if (lane == 0)
-        part[warp] = make_float2(m, sum);
-
-    // In a whole chunk the bound is taken on values alone; a chunk with an end, one whose n-th value is not finite, and
-    // one with more ties than can be gathered go by keys.
-    bool done = false;
-    if (whole) {
-        const float bound = group_bound_value(sh, best, n);
-        if (fabsf(bound) <= FLT_MAX) {
-            if (best >= bound) {
+        sum *= ex2_approx(-fmaf(mu, LOG2E, -c));
+        if (sum != sum || fabsf(mu) > 1e30f) {   // NaN logits (they count as -inf), or a product past fp32's range
+            sum = 0.0f;
 #pragma unroll
-                for (int i = 0; i < PER; i++)
-                    if (v[i] >= bound) {
-                        const int to = atomicAdd(&sh.count, 1);
-                        if (to < CAP)
-                            sh.cand[to] = key_of(v[i], token(i));
-                    }
-            }
-            __syncthreads();
-            done = sh.count <= CAP;
-            __syncthreads();
+            for (int i = 0; i < PER; i++)
+                sum += ex2_approx((no_nan(v[i]) - mu) * LOG2E);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                sum += __shfl_xor_sync(FULL, sum, o);
         }
-    }
-    if (!done) {
-        uint64_t key = 0;
-#pragma unroll
-        for (int i = 0; i < PER; i++) {
-            v[i] = no_nan(v[i]);
-            const uint64_t x = token(i) < p.V ? key_of(v[i], token(i)) : 0;
-            key = x > key ? x : key;
+        if (lane == 0)
+            part[pieces * (THREADS / 32) + warp] = make_float2(m, sum);
+        if (first == t0) {
+            bound = group_bound_value<THREADS>(sh, best, n);
+            by_keys = !(fabsf(bound) <= FLT_MAX);      // too few finite values for a bound
         }
-        const uint64_t bound = group_bound(sh, key, n);
-        if (key >= bound) {
+        if (!by_keys && best >= bound) {
 #pragma unroll
-            for (int i = 0; i < PER; i++) {
-                const uint64_t x = token(i) < p.V ? key_of(v[i], token(i)) : 0;
-                if (x >= bound) {
-                    const int to = atomicAdd(&sh.count, 1);
-                    if (to < CAP)
-                        sh.cand[to] = x;
-                }
+            for (int i = 0; i < NV; i++) {
+                if (!(top[i] >= bound))
+                    continue;
+#pragma unroll
+                for (int e = 0; e < N; e++)
+                    if (v[i * N + e] >= bound)
+                        gather(sh, key_of(v[i * N + e], token(i * N + e)));
             }
         }
-        __syncthreads();
     }
+    __syncthreads();
     const int64_t slot = blockIdx.x;
     uint64_t *list = p.lists + slot * n;
     if (warp == 0) {
-        const float2 x = lane < THREADS / 32 ? part[lane] : make_float2(-INFINITY, 0.0f);
+        const float2 x = lane < pieces * (THREADS / 32) ? part[lane] : make_float2(-INFINITY, 0.0f);
         float M = x.x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -373,33 +412,20 @@ template <typename T, int PER> __global__ void __launch_bounds__(THREADS, PER > 
             p.stats[slot] = make_float2(M, s);
     }
     const int count = sh.count;
-    if (count <= CAP) {
-        rank_gathered(sh, count, n, [&](int r, uint64_t k) { list[r] = k; });
-        for (int r = count + tid; r < n; r += THREADS)
-            list[r] = 0;
+    if (by_keys || count > CAP) {            // uniform: many ties, or hardly anything finite
+        __syncthreads();
+        list_by_keys(sh, l, t0, t1, n, list);
     } else {
-        // more than can be gathered (large values crowded into few threads): one at a time
-        uint64_t last = ~0ull;
-        for (int r = 0; r < n; r++) {
-            uint64_t b = 0;
-#pragma unroll
-            for (int i = 0; i < PER; i++) {
-                const uint64_t x = token(i) < p.V ? key_of(v[i], token(i)) : 0;
-                if (x < last && x > b)
-                    b = x;
-            }
-            last = block_max(b, sh.red);
-            if (tid == 0)
-                list[r] = last;
-        }
+        rank_gathered<THREADS>(sh, count, n, [&](int r, uint64_t k) { list[r] = k; });
     }
 }
+static_assert(MAX_SPAN * THREADS / 32 <= 32, "a warp joins the parts");
 
 // Score of a candidate whose beam has offset c (-inf: nothing of the beam counts) and logit l.
 __device__ __forceinline__ float score_of(float c, float l) { return c == -INFINITY ? c : no_nan(c + l); }
 
 // The K best of all W x V candidates, one pass for each: what the short lists are a shortcut of.
-template <typename T> __device__ void pick_all(const BeamArgs &p, int b, const float *c, uint64_t *red)
+template <typename T> __device__ __noinline__ void pick_all(const BeamArgs &p, int b, const float *c, uint64_t *red)
 {
     uint64_t last = ~0ull;
     for (int k = 0; k < p.K; k++) {
@@ -408,7 +434,7 @@ template <typename T> __device__ void pick_all(const BeamArgs &p, int b, const f
             const int64_t row = (int64_t)b * p.W + w;
             const T *l = static_cast<const T *>(p.logits) + row * p.row_stride;
             const bool done = p.finished && p.finished[row];
-            for (int t = threadIdx.x; t < p.V; t += THREADS) {
+            for (int t = threadIdx.x; t < p.V; t += PICK_THREADS) {
                 const float s = done ? (t == p.eos ? no_nan(p.beam_scores[row]) : -INFINITY)
                                      : score_of(c[w], no_nan(load_logit(l + t)));
                 const uint64_t x = key_of(s, (uint32_t)w * p.V + t);
@@ -416,7 +442,7 @@ template <typename T> __device__ void pick_all(const BeamArgs &p, int b, const f
                     best = x;
             }
         }
-        last = block_max(best, red);
+        last = block_max<PICK_THREADS>(best, red);
         if (threadIdx.x == 0) {
             p.scores[(int64_t)b * p.K + k] = key_value(last);
             p.tokens[(int64_t)b * p.K + k] = key_index(last) % p.V;
@@ -426,69 +452,88 @@ template <typename T> __device__ void pick_all(const BeamArgs &p, int b, const f
 }
 
 // One CTA per batch entry.
-template <typename T> __global__ void __launch_bounds__(THREADS) kda_beam_pick_kernel(const BeamArgs p)
+template <typename T> __global__ void __launch_bounds__(PICK_THREADS) kda_beam_pick_kernel(const BeamArgs p)
 {
+    constexpr int HELD = 4;                // candidates a thread keeps in registers
     __shared__ __align__(16) Pick sh;
-    __shared__ float c[32];
-    __shared__ bool plain[32];             // the beam's candidates come from the lists
+    __shared__ float c[32], own[32];       // the beams' offsets, and the scores of finished ones
+    __shared__ int kind[32];               // 0: candidates from the lists; 1: nothing counts; 2: finished
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid % 32, n = p.K + 1;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int w = tid / 32; w < p.W; w += THREADS / 32) {
+    for (int w = tid / 32; w < p.W; w += PICK_THREADS / 32) {
         const int64_t row = (int64_t)b * p.W + w;
         const bool done = p.finished && p.finished[row];
+        const float score = p.beam_scores[row];
         float m = -INFINITY, s = 0.0f;
         if (!done) {
             const float2 *st = p.stats + row * p.chunks;
-            for (int i = lane; i < p.chunks; i += 32)
+            float2 x = lane < p.chunks ? st[lane] : make_float2(-INFINITY, 0.0f);
+            m = x.x;
+            for (int i = lane + 32; i < p.chunks; i += 32)
                 m = fmaxf(m, st[i].x);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-            if (fabsf(m) <= FLT_MAX)
-                for (int i = lane; i < p.chunks; i += 32)
-                    s += st[i].y * expf(st[i].x - m);
+            if (fabsf(m) <= FLT_MAX) {
+                s = x.y * expf(x.x - m);
+                for (int i = lane + 32; i < p.chunks; i += 32) {
+                    x = st[i];
+                    s += x.y * expf(x.x - m);
+                }
+            }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 s += __shfl_xor_sync(FULL, s, o);
         }
         if (lane == 0) {
-            c[w] = fabsf(m) <= FLT_MAX ? no_nan((p.beam_scores[row] - m) - logf(s)) : -INFINITY;
-            plain[w] = !done && c[w] != -INFINITY;
+            const float off = fabsf(m) <= FLT_MAX ? no_nan((score - m) - logf(s)) : -INFINITY;
+            c[w] = off;
+            own[w] = no_nan(score);
+            kind[w] = done ? 2 : (off == -INFINITY ? 1 : 0);
         }
     }
     __syncthreads();
     // candidate i of beam w: a list entry, or for a beam whose candidates are all but one -inf its first tokens and eos
-    const int64_t per = (int64_t)p.chunks * n, total = per * p.W;
-    auto candidate = [&](int64_t x) -> uint64_t {
-        const int w = (int)(x / per);
-        const int64_t i = x % per, row = (int64_t)b * p.W + w;
-        if (plain[w]) {
-            const uint64_t k = p.lists[row * per + i];
-            return k ? key_of(score_of(c[w], key_value(k)), (uint32_t)w * p.V + key_index(k)) : 0;
+    const uint32_t per = (uint32_t)p.chunks * n, total = per * p.W;
+    const uint64_t *lists = p.lists + (int64_t)b * total;
+    auto candidate = [&](uint32_t x) -> uint64_t {
+        const uint32_t w = x / per, i = x - w * per;
+        if (kind[w] == 0) {
+            const uint64_t k = lists[x];
+            return k ? key_of(score_of(c[w], key_value(k)), w * p.V + key_index(k)) : 0;
         }
-        const bool done = p.finished && p.finished[row];
-        int64_t t = i;
-        if (i > p.K || (i == p.K && !(done && p.eos >= p.K)) || (i < p.K && i >= p.V))
+        const bool done = kind[w] == 2;
+        uint32_t t = i;
+        if (i > (uint32_t)p.K || (i == (uint32_t)p.K && !(done && p.eos >= p.K)) ||
+            (i < (uint32_t)p.K && i >= (uint32_t)p.V))
             return 0;
-        if (i == p.K)
-            t = p.eos;
-        return key_of(done && t == p.eos ? no_nan(p.beam_scores[row]) : -INFINITY, (uint32_t)w * p.V + (uint32_t)t);
+        if (i == (uint32_t)p.K)
+            t = (uint32_t)p.eos;
+        return key_of(done && t == (uint32_t)p.eos ? own[w] : -INFINITY, w * p.V + t);
     };
-    uint64_t best = 0;
-    for (int64_t x = tid; x < total; x += THREADS) {
+    uint64_t best = 0, held[HELD];
+#pragma unroll
+    for (int i = 0; i < HELD; i++) {
+        const uint32_t x = i * PICK_THREADS + tid;
+        held[i] = x < total ? candidate(x) : 0;
+        best = held[i] > best ? held[i] : best;
+    }
+    for (uint32_t x = HELD * PICK_THREADS + tid; x < total; x += PICK_THREADS) {
         const uint64_t k = candidate(x);
         best = k > best ? k : best;
     }
-    const uint64_t bound = group_bound(sh, best, p.K);
-    if (best >= bound)
-        for (int64_t x = tid; x < total; x += THREADS) {
+    const uint64_t bound = group_bound<PICK_THREADS>(sh, best, p.K);
+    if (best >= bound) {
+#pragma unroll
+        for (int i = 0; i < HELD; i++)
+            if (held[i] >= bound)
+                gather(sh, held[i]);
+        for (uint32_t x = HELD * PICK_THREADS + tid; x < total; x += PICK_THREADS) {
             const uint64_t k = candidate(x);
-            if (k >= bound && k) {
-                const int to = atomicAdd(&sh.count, 1);
-                if (to < CAP)
-                    sh.cand[to] = k;
-            }
+            if (k >= bound)
+                gather(sh, k);
         }
+    }
     __syncthreads();
     const int count = sh.count;
     bool again = count > CAP;
@@ -497,7 +542,7 @@ template <typename T> __global__ void __launch_bounds__(THREADS) kda_beam_pick_k
         if (tid == 0)
             sh.bound = 0;
         __syncthreads();
-        rank_gathered(sh, count, p.K, [&](int r, uint64_t k) {
+        rank_gathered<PICK_THREADS>(sh, count, p.K, [&](int r, uint64_t k) {
             if (r == p.K - 1)
                 sh.bound = k;
             p.scores[(int64_t)b * p.K + r] = key_value(k);
@@ -506,11 +551,11 @@ template <typename T> __global__ void __launch_bounds__(THREADS) kda_beam_pick_k
         });
         __syncthreads();
         const float last = key_value(sh.bound);
-        for (int x = tid; x < p.W * p.chunks; x += THREADS) {
-            const int w = x / p.chunks;
-            if (!plain[w])
+        for (uint32_t x = tid; x < (uint32_t)p.W * p.chunks; x += PICK_THREADS) {
+            const uint32_t w = x / p.chunks;
+            if (kind[w] != 0)
                 continue;
-            const uint64_t k = p.lists[((int64_t)b * p.W * p.chunks + x) * n + n - 1];
+            const uint64_t k = lists[x * n + n - 1];
             if (!k)
                 continue;
             const float l = key_value(k);
@@ -526,17 +571,24 @@ template <typename T> __global__ void __launch_bounds__(THREADS) kda_beam_pick_k
 
 }  // namespace
 
-// Logits a thread holds.  Many make fewer lists to pick from; few put a small call's logits on more SMs.  See the
-// comment at launch_beam for what was measured.
-constexpr int PER_LARGE = 32, PER_SMALL = 8;
-
-static int beam_per(int B, int W, int V)
+// Logits a thread holds of a piece, and pieces of a chunk.
+struct BeamCut {
+    int per, span;
+};
+static BeamCut beam_cut(int B, int W, int V)
 {
-    return (int64_t)B * W * ((V + THREADS * PER_LARGE - 1) / (THREADS * PER_LARGE)) >= 152 ? PER_LARGE : PER_SMALL;
+    const int64_t rows = (int64_t)B * W;
+    auto ctas = [&](int chunk) { return rows * ((V + chunk - 1) / chunk); };
+    if (ctas(THREADS * 32 * MAX_SPAN) >= 304)
+        return {32, MAX_SPAN};
+    if (ctas(THREADS * 32) >= 152)
+        return {32, 1};
+    return {8, 1};
 }
 static int beam_chunks(int B, int W, int V)
 {
-    const int chunk = THREADS * beam_per(B, W, V);
+    const BeamCut c = beam_cut(B, W, V);
+    const int chunk = THREADS * c.per * c.span;
     return (V + chunk - 1) / chunk;
 }
 
@@ -545,16 +597,16 @@ namespace {
 template <typename T> cudaError_t launch_beam(const BeamArgs &p, cudaStream_t st)
 {
     const unsigned grid = (unsigned)(p.chunks * p.B * p.W);
-    if (beam_per(p.B, p.W, p.V) == PER_LARGE)
-        kda_beam_chunks_kernel<T, PER_LARGE><<<grid, THREADS, 0, st>>>(p);
+    if (beam_cut(p.B, p.W, p.V).per == 32)
+        kda_beam_chunks_kernel<T, 32><<<grid, THREADS, 0, st>>>(p);
     else
-        kda_beam_chunks_kernel<T, PER_SMALL><<<grid, THREADS, 0, st>>>(p);
+        kda_beam_chunks_kernel<T, 8><<<grid, THREADS, 0, st>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)p.B);
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(PICK_THREADS);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -613,6 +665,7 @@ extern "C" kda_status_t kda_beam_select_ws(const void *logits, kda_dtype_t dtype
         return KDA_ERR_INVALID_ARGUMENT;
     BeamArgs p{logits, row_stride, beam_scores, finished, eos, scores, tokens, parents, B, W, V, K};
     p.chunks = beam_chunks(B, W, V);
+    p.span = beam_cut(B, W, V).span;
     p.stats = static_cast<float2 *>(workspace);
     p.lists = reinterpret_cast<uint64_t *>(p.stats + (size_t)B * W * p.chunks);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
