@@ -6,13 +6,12 @@
 // batch entry, turns those few into scores and picks (kda_beam_pick_kernel).  Each logit is read once: the floor.
 //
 // What the short lists may hide: logits so close that their fp32 scores are equal tie by index and not by logit.  That
-// matters only where a chunk's last kept logit reaches the K-th score and a neighbouring logit value has the same score
-// too; the pick then goes over all candidates of the entry again (pick_all).
+// matters only where the value a chunk's list was cut off at reaches the K-th score and a neighbouring logit value has
+// the same score too; the pick then goes over all candidates of the entry again (pick_all).
 //
 // The best of many.  Candidates are 64-bit keys, order-preserving bits of the value above the complement of the index,
-// so all are distinct and a tie goes to the lower index.  The n-th best of the thread groups' best keys is a lower
-// bound on the n-th best key, and at most n groups have keys from it up: those are gathered in shared memory and each
-// ranked by counting the larger ones.
+// so all are distinct and a tie goes to the lower index.  The n-th best of the thread groups' best is a lower bound on
+// the n-th best, and at most n groups have candidates from it up: those are gathered, few more than n.
 #include "kda_step.cuh"
 
 #include <cfloat>
@@ -22,7 +21,10 @@ namespace {
 
 constexpr int THREADS = 256;              // of the chunk kernel
 constexpr int PICK_THREADS = 512;
-constexpr int CAP = 2048;                 // keys gathered for ranking
+constexpr int CAP = 2048;                 // keys gathered in shared memory
+constexpr int SELECTED = 1024;            // of them from the bound up: K groups of 2048 / 64 or 2048 / 128 keys at most
+constexpr int MOST_CHUNK = 32768;         // tokens of a chunk at most
+constexpr int BY_KEYS = 1 << 30;          // in a list's count: the list is the K + 1 best and ends at a logit
 constexpr unsigned FULL = 0xffffffffu;
 
 struct BeamArgs {
@@ -34,9 +36,11 @@ struct BeamArgs {
     float *scores;
     int32_t *tokens, *parents;
     int B, W, V, K;
-    int chunks, span;        // chunks of a row, pieces of a chunk
-    float2 *stats;           // [B W][chunks]: maximum, sum of exp(l - maximum)   (workspace)
-    uint64_t *lists;         // [B W][chunks][K + 1]: best logits' keys, 0 past the last
+    int chunks, chunk;       // chunks of a row, tokens of a chunk
+    int room;                // keys of a list
+    float4 *stats;           // [B W][chunks]: maximum, sum of exp(l - maximum), the value the list was cut off at (NaN:
+                             // nowhere), keys in the list (bits)   (workspace)
+    uint64_t *lists;         // [B W][chunks][room]: keys of all logits from the cut up, K + 1 at least where there are
 };
 
 __device__ __forceinline__ float load_logit(const float *p) { return *p; }
@@ -91,10 +95,11 @@ template <int NT> __device__ uint64_t block_max(uint64_t x, uint64_t *sh)
 }
 
 struct Pick {
-    uint64_t group[128];           // best key of each group of threads
+    uint64_t group[128];           // best of each group of threads
     uint64_t cand[CAP];
     uint64_t red[32];
     uint64_t bound;
+    float value;
     int count;
 };
 
@@ -111,10 +116,8 @@ template <int NT> __device__ uint64_t group_bound(Pick &sh, uint64_t best, int n
     }
     if (threadIdx.x % size == 0)
         sh.group[threadIdx.x / size] = best;
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0)
         sh.bound = 1;
-        sh.count = 0;
-    }
     __syncthreads();
     for (int i = threadIdx.x / 32; i < groups; i += NT / 32) {     // a warp ranks a group
         const uint64_t x = sh.group[i];
@@ -128,46 +131,49 @@ template <int NT> __device__ uint64_t group_bound(Pick &sh, uint64_t best, int n
     return sh.bound;
 }
 
-// The same on values alone: the n-th best (ties counted) of the groups' best values, -inf when fewer have one.
+// The same on values alone, rounded down to 24 bits: a value that the n best groups' best values reach; NaN when fewer
+// groups than n have one above -inf.  One warp finds it bit by bit.
 template <int NT> __device__ float group_bound_value(Pick &sh, float best, int n)
 {
     const int groups = groups_for(n), size = NT / groups, lane = threadIdx.x % 32;
-    float *g = reinterpret_cast<float *>(sh.group);
+    uint32_t *g = reinterpret_cast<uint32_t *>(sh.group);
     for (int o = 1; o < size; o <<= 1)
         best = fmaxf(best, __shfl_xor_sync(FULL, best, o));
     if (threadIdx.x % size == 0)
-        g[threadIdx.x / size] = best;
-    uint32_t *lowest = reinterpret_cast<uint32_t *>(&sh.bound);
-    if (threadIdx.x == 0) {
-        *lowest = FULL;
+        g[threadIdx.x / size] = (uint32_t)(key_of(best, 0) >> 32);
+    if (threadIdx.x == 0)
         sh.count = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        uint32_t u[4], at = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            u[i] = i * 32 < groups ? g[i * 32 + lane] : 0;
+#pragma unroll
+        for (int bit = 31; bit >= 8; bit--) {
+            const uint32_t to = at | (1u << bit);
+            int have = __popc(__ballot_sync(FULL, u[0] >= to)) + __popc(__ballot_sync(FULL, u[1] >= to));
+            if (groups > 64)
+                have += __popc(__ballot_sync(FULL, u[2] >= to)) + __popc(__ballot_sync(FULL, u[3] >= to));
+            if (have >= n)
+                at = to;
+        }
+        if (lane == 0)
+            sh.value = key_value((uint64_t)at << 32);
     }
     __syncthreads();
-    uint32_t low = FULL;
-    for (int i = threadIdx.x / 32; i < groups; i += NT / 32) {
-        const float x = g[i];
-        int above = 0;
-        for (int j = 0; j < groups; j += 32)
-            above += __popc(__ballot_sync(FULL, g[j + lane] > x));
-        // the smallest of the values that fewer than n are above
-        if (above < n)
-            low = min(low, (uint32_t)(key_of(x, 0) >> 32));
-    }
-    if (lane == 0)
-        atomicMin(lowest, low);
-    __syncthreads();
-    return key_value((uint64_t)*lowest << 32);
+    return sh.value;
 }
 
 // Ranks the gathered keys (count of them, all distinct) and hands the best n to put(rank, key), by one thread each.
-template <int NT, typename F> __device__ void rank_gathered(const Pick &sh, int count, int n, F put)
+template <int NT, typename F> __device__ void rank_gathered(const uint64_t *cand, int count, int n, F put)
 {
     const int lane = threadIdx.x % 32;
     for (int i = threadIdx.x / 32; i < count; i += NT / 32) {      // a warp ranks a key
-        const uint64_t x = sh.cand[i];
+        const uint64_t x = cand[i];
         int rank = 0;
         for (int j = lane; j < count; j += 32)
-            rank += sh.cand[j] > x;
+            rank += cand[j] > x;
         rank = __reduce_add_sync(FULL, rank);
         if (lane == 0 && rank < n)
             put(rank, x);
@@ -181,7 +187,7 @@ __device__ __forceinline__ void gather(Pick &sh, uint64_t key)
 }
 
 template <typename T> struct Vec {
-    static constexpr int N = 16 / sizeof(T);
+    static constexpr int N = 16 / sizeof(T);        // logits of a 16-byte vector
 };
 __device__ __forceinline__ void unpack(const uint4 &x, float *v, const float *)
 {
@@ -194,63 +200,88 @@ __device__ __forceinline__ void unpack(const uint4 &x, float *v, const __nv_bflo
     for (int i = 0; i < 4; i++)
         v[2 * i] = bf16_lo(u[i]), v[2 * i + 1] = bf16_hi(u[i]);
 }
+// What a thread keeps of the logits it has seen: their maximum, and the sum of exp(v - ref) as 2^(v L - c), c = ref L
+// rounded; the factor 2^(c - ref L) is put in at the end.  ref follows the maximum only in large steps: any of the
+// logits near it serves.
+struct Seen {
+    float best = -INFINITY, ref = -INFINITY, c = 0.0f, sum = 0.0f;
+    template <int N> __device__ __forceinline__ void add(const float (&v)[N])
+    {
+        float m = v[0];                                 // fmaxf passes over NaN
+#pragma unroll
+        for (int e = 1; e < N; e++)
+            m = fmaxf(m, v[e]);
+        best = fmaxf(best, m);
+        if (m > ref + 40.0f && m <= FLT_MAX) {
+            const float to = m * LOG2E;
+            sum = ref == -INFINITY ? 0.0f : sum * ex2_approx(c - to);
+            ref = m;
+            c = to;
+        }
+#pragma unroll
+        for (int e = 0; e < N; e++)
+            sum += ex2_approx(fmaf(v[e], LOG2E, -c));
+    }
+};
 
-// The aligned 16 bytes that hold the row's elements from t on (t may be negative): one load where the row covers them,
-// else element by element, zeros outside.
-__device__ __forceinline__ uint4 load_aligned(const float *l, int t, int V)
+// Thread i's logits of the tokens [t0, t1): N from t0 + (s THREADS + i) N on for s = 0, 1, ...  DEPTH loads of 16 bytes
+// are in flight.  DEPTH > 0: a multiple of DEPTH whole steps of a row on a 16-byte boundary; else the same logits in the
+// same order one by one, so that the result does not depend on a row's alignment.
+template <typename T, int DEPTH> __device__ __forceinline__ void stream_logits(const T *l, int t0, int t1, Seen &seen)
 {
-    if (t >= 0 && t + 4 <= V)
-        return __ldcs(reinterpret_cast<const uint4 *>(l + t));
-    uint32_t u[4];
+    constexpr int N = Vec<T>::N, STEP = THREADS * N;
+    const int steps = (t1 - t0 + STEP - 1) / STEP;
+    if constexpr (DEPTH > 0) {
+        const uint4 *at = reinterpret_cast<const uint4 *>(l + t0) + threadIdx.x;
+        uint4 raw[DEPTH];
 #pragma unroll
-    for (int e = 0; e < 4; e++)
-        u[e] = t + e >= 0 && t + e < V ? __float_as_uint(l[t + e]) : 0;
-    return make_uint4(u[0], u[1], u[2], u[3]);
-}
-__device__ __forceinline__ uint4 load_aligned(const __nv_bfloat16 *l, int t, int V)
-{
-    if (t >= 0 && t + 8 <= V)
-        return __ldcs(reinterpret_cast<const uint4 *>(l + t));
-    uint32_t u[4] = {0, 0, 0, 0};
+        for (int d = 0; d < DEPTH; d++)
+            raw[d] = __ldg(at + d * THREADS);
+        for (int s = DEPTH; s < steps; s += DEPTH) {
+            at += DEPTH * THREADS;
 #pragma unroll
-    for (int e = 0; e < 8; e++)
-        if (t + e >= 0 && t + e < V)
-            u[e / 2] |= (uint32_t)reinterpret_cast<const unsigned short *>(l)[t + e] << (16 * (e % 2));
-    return make_uint4(u[0], u[1], u[2], u[3]);
-}
-// 16 bytes that lie `off` bytes (not 0) past a 16-byte boundary: a holds the aligned 16 bytes they begin in, of lane i of
-// a warp at 16 i; the next lane's a is the second half, and lane 31 reads it (element t of the row l on).
-template <typename T> __device__ __forceinline__ uint4 shifted(const uint4 &a, const T *l, int t, int off, int V)
-{
-    uint4 b;
-    b.x = __shfl_down_sync(FULL, a.x, 1);
-    b.y = __shfl_down_sync(FULL, a.y, 1);
-    b.z = __shfl_down_sync(FULL, a.z, 1);
-    b.w = __shfl_down_sync(FULL, a.w, 1);
-    if ((threadIdx.x & 31) == 31)
-        b = load_aligned(l, t, V);
-    uint32_t x[5];
-    const int words = off / 4;
-    if (words == 0)
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x;
-    else if (words == 1)
-        x[0] = a.y, x[1] = a.z, x[2] = a.w, x[3] = b.x, x[4] = b.y;
-    else if (words == 2)
-        x[0] = a.z, x[1] = a.w, x[2] = b.x, x[3] = b.y, x[4] = b.z;
-    else
-        x[0] = a.w, x[1] = b.x, x[2] = b.y, x[3] = b.z, x[4] = b.w;
-    if (off & 2)
-        return make_uint4(__funnelshift_r(x[0], x[1], 16), __funnelshift_r(x[1], x[2], 16),
-                          __funnelshift_r(x[2], x[3], 16), __funnelshift_r(x[3], x[4], 16));
-    return make_uint4(x[0], x[1], x[2], x[3]);
+            for (int d = 0; d < DEPTH; d++) {
+                float v[N];
+                unpack(raw[d], v, l);
+                seen.add(v);
+                raw[d] = __ldg(at + d * THREADS);
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < DEPTH; d++) {
+            float v[N];
+            unpack(raw[d], v, l);
+            seen.add(v);
+        }
+    } else {
+        constexpr int FLIGHT = 16 / N;
+        float raw[FLIGHT][N];
+        int t = t0 + threadIdx.x * N;
+        for (int s = 0; s < steps; s += FLIGHT) {
+#pragma unroll
+            for (int d = 0; d < FLIGHT; d++)
+#pragma unroll
+                for (int e = 0; e < N; e++) {
+                    raw[d][e] = -INFINITY;
+                    if (t + d * STEP + e < t1)
+                        raw[d][e] = load_logit(l + t + d * STEP + e);
+                }
+#pragma unroll
+            for (int d = 0; d < FLIGHT; d++)
+                seen.add(raw[d]);
+            t += FLIGHT * STEP;
+        }
+    }
 }
 
 // The n best keys of tokens [t0, t1) of a row, whatever they are, straight from memory: the bound on keys, and where more
-// than can be gathered lie above it (large values crowded into few threads) one key at a time.
+// than can be gathered lie above it (large values crowded into few threads) one key at a time.  Zeros past the last.
 template <typename T>
 __device__ __noinline__ void list_by_keys(Pick &sh, const T *l, int t0, int t1, int n, uint64_t *list)
 {
     uint64_t best = 0;
+    if (threadIdx.x == 0)
+        sh.count = 0;
     for (int t = t0 + threadIdx.x; t < t1; t += THREADS) {
         const uint64_t x = key_of(no_nan(load_logit(l + t)), t);
         best = x > best ? x : best;
@@ -265,7 +296,7 @@ __device__ __noinline__ void list_by_keys(Pick &sh, const T *l, int t0, int t1, 
     __syncthreads();
     const int count = sh.count;
     if (count <= CAP) {
-        rank_gathered<THREADS>(sh, count, n, [&](int r, uint64_t k) { list[r] = k; });
+        rank_gathered<THREADS>(sh.cand, count, n, [&](int r, uint64_t k) { list[r] = k; });
         for (int r = count + threadIdx.x; r < n; r += THREADS)
             list[r] = 0;
         return;
@@ -284,17 +315,14 @@ __device__ __noinline__ void list_by_keys(Pick &sh, const T *l, int t0, int t1, 
     }
 }
 
-// One CTA per (chunk, row); a chunk is p.span pieces of PER x THREADS logits, the next piece's loads in flight while one
-// is worked on.  The first piece gives the bound: later ones only compare with it (a piece as good as the first adds
-// about K + 1 keys), so there is no barrier between pieces.  Which thread takes which token, and so the order of the
-// sums, does not depend on the row's alignment: equal rows get equal scores.
-constexpr int MAX_SPAN = 4;
-
-template <typename T, int PER> __global__ void __launch_bounds__(THREADS, PER > 16 ? 2 : 6) kda_beam_chunks_kernel(const BeamArgs p)
+// One CTA per (chunk, row).  The threads stream through the chunk's logits, with no barrier, and keep their maxima and
+// sums.  The maxima then give a bound that about K + 1 logits reach: only the threads (a few) whose maximum does are
+// looked at again, eight lanes reading one thread's logits out of L2.
+template <typename T> __global__ void __launch_bounds__(THREADS, 4) kda_beam_chunks_kernel(const BeamArgs p)
 {
-    constexpr int N = Vec<T>::N, NV = PER / N, PIECE = THREADS * PER;
+    constexpr int N = Vec<T>::N, STEP = THREADS * N;
     __shared__ __align__(16) Pick sh;
-    __shared__ float2 part[MAX_SPAN * THREADS / 32];
+    __shared__ float2 part[THREADS / 32];
     asm volatile("griddepcontrol.launch_dependents;");
     const int64_t row = blockIdx.x / p.chunks;
     const int chunk = (int)(blockIdx.x % p.chunks);
@@ -302,104 +330,87 @@ template <typename T, int PER> __global__ void __launch_bounds__(THREADS, PER > 
     if (p.finished && p.finished[row])
         return;                              // its one candidate needs no logits
     const T *l = static_cast<const T *>(p.logits) + row * p.row_stride;
-    const int off = (int)(reinterpret_cast<uintptr_t>(l) & 15), back = off / (int)sizeof(T);
-    const int t0 = chunk * (PIECE * p.span), t1 = min(p.V, t0 + PIECE * p.span);
-    uint4 next[NV];
-    auto load = [&](int first) {             // all loads before anything waits for one
-        if (first >= back && first + PIECE <= p.V) {
+    const int t0 = chunk * p.chunk, t1 = min(p.V, t0 + p.chunk);
+    Seen seen;
+    const bool even = (reinterpret_cast<uintptr_t>(l) & 15) == 0 && (t1 - t0) % STEP == 0;
+    const int steps = (t1 - t0) / STEP;
+    if (even && steps % 8 == 0)
+        stream_logits<T, 8>(l, t0, t1, seen);
+    else if (even && steps % 2 == 0)
+        stream_logits<T, 2>(l, t0, t1, seen);
+    else if (even)
+        stream_logits<T, 1>(l, t0, t1, seen);
+    else
+        stream_logits<T, 0>(l, t0, t1, seen);
+    const float best = seen.best;
+    float m = best;
 #pragma unroll
-            for (int i = 0; i < NV; i++)
-                next[i] = __ldcs(reinterpret_cast<const uint4 *>(l + (first + (i * THREADS + tid) * N - back)));
-        } else {
+    for (int o = 16; o > 0; o >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+    const float mu = fabsf(m) <= FLT_MAX ? m : 0.0f;
+    float sum = seen.ref == -INFINITY ? seen.sum
+                                      : seen.sum * (ex2_approx(-fmaf(seen.ref, LOG2E, -seen.c)) * ex2_approx((seen.ref - mu) * LOG2E));
 #pragma unroll
-            for (int i = 0; i < NV; i++)
-                next[i] = load_aligned(l, first + (i * THREADS + tid) * N - back, p.V);
-        }
-    };
-    load(t0);
-    float bound = -INFINITY;
-    bool by_keys = false;
-    int pieces = 0;
-    for (int first = t0; first < t1; first += PIECE, pieces++) {
-        float v[PER];
-        if (off) {
-#pragma unroll
-            for (int i = 0; i < NV; i++)
-                next[i] = shifted(next[i], l, first + (i * THREADS + tid) * N - back + N, off, p.V);
-        }
-#pragma unroll
-        for (int i = 0; i < NV; i++)
-            unpack(next[i], v + i * N, l);
-        if (first + PIECE < t1)
-            load(first + PIECE);
-        auto token = [&](int i) { return first + ((i / N) * THREADS + tid) * N + i % N; };
-        if (first + PIECE > p.V) {
-#pragma unroll
-            for (int i = 0; i < PER; i++)
-                v[i] = token(i) < p.V ? v[i] : -INFINITY;
-        }
-        // maximum and sum of the piece, warp by warp (fmaxf passes over NaN)
-        float best = -INFINITY, top[NV];     // of the thread, and of each of its vectors
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            top[i] = v[i * N];
-#pragma unroll
-            for (int e = 1; e < N; e++)
-                top[i] = fmaxf(top[i], v[i * N + e]);
-            best = fmaxf(best, top[i]);
-        }
-        float m = best;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-        const float mu = fabsf(m) <= FLT_MAX ? m : 0.0f;
-        // exp(v - mu) = 2^(v L - c) 2^(c - mu L), c = mu L rounded: the second factor is one for the whole warp
-        const float c = mu * LOG2E;
-        const f2 scale = f2_pack(LOG2E, LOG2E), shift = f2_pack(-c, -c);
-        float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-        for (int i = 0; i < PER; i += 2) {
-            const f2 x = f2_fma(f2_pack(v[i], v[i + 1]), scale, shift);
-            s0 += ex2_approx(f2_lo(x));
-            s1 += ex2_approx(f2_hi(x));
-        }
-        float sum = s0 + s1;
+    for (int o = 16; o > 0; o >>= 1)
+        sum += __shfl_xor_sync(FULL, sum, o);
+    if (!(sum <= FLT_MAX) || fabsf(mu) > 1e30f) {  // NaN logits (they count as -inf), or a product past fp32's range
+        sum = 0.0f;
+        for (int t = t0 + tid * N; t < t1; t += STEP)
+            for (int e = 0; e < N && t + e < t1; e++)
+                sum += ex2_approx((no_nan(load_logit(l + t + e)) - mu) * LOG2E);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             sum += __shfl_xor_sync(FULL, sum, o);
-        sum *= ex2_approx(-fmaf(mu, LOG2E, -c));
-        if (sum != sum || fabsf(mu) > 1e30f) {   // NaN logits (they count as -inf), or a product past fp32's range
-            sum = 0.0f;
+    }
+    if (lane == 0)
+        part[warp] = make_float2(m, sum);
+    const float bound = group_bound_value<THREADS>(sh, best, n);
+    uint64_t *list = p.lists + (int64_t)blockIdx.x * p.room;
+    const bool by_keys = !(fabsf(bound) <= FLT_MAX);       // too few finite values for a bound
+    if (!by_keys) {
+        constexpr int TURNS = MOST_CHUNK / STEP / 8;       // of eight lanes over a thread's vectors
+        for (unsigned owners = __ballot_sync(FULL, best >= bound); owners;) {
+            int of = -1;
 #pragma unroll
-            for (int i = 0; i < PER; i++)
-                sum += ex2_approx((no_nan(v[i]) - mu) * LOG2E);
+            for (int k = 0; k < 4; k++)
+                if (owners) {
+                    if (lane / 8 == k)
+                        of = tid - lane + __ffs(owners) - 1;
+                    owners &= owners - 1;
+                }
+            float x[TURNS][N];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                sum += __shfl_xor_sync(FULL, sum, o);
-        }
-        if (lane == 0)
-            part[pieces * (THREADS / 32) + warp] = make_float2(m, sum);
-        if (first == t0) {
-            bound = group_bound_value<THREADS>(sh, best, n);
-            by_keys = !(fabsf(bound) <= FLT_MAX);      // too few finite values for a bound
-        }
-        if (!by_keys && best >= bound) {
+            for (int j = 0; j < TURNS; j++)
 #pragma unroll
-            for (int i = 0; i < NV; i++) {
-                if (!(top[i] >= bound))
-                    continue;
+                for (int e = 0; e < N; e++) {
+                    const int t = t0 + ((lane % 8 + 8 * j) * THREADS + of) * N + e;
+                    x[j][e] = -INFINITY;
+                    if (of >= 0 && t < t1)
+                        x[j][e] = load_logit(l + t);
+                }
+#pragma unroll
+            for (int j = 0; j < TURNS; j++)
 #pragma unroll
                 for (int e = 0; e < N; e++)
-                    if (v[i * N + e] >= bound)
-                        gather(sh, key_of(v[i * N + e], token(i * N + e)));
-            }
+                    if (x[j][e] >= bound) {
+                        const int to = atomicAdd(&sh.count, 1);
+                        if (to < p.room)
+                            list[to] = key_of(x[j][e], t0 + ((lane % 8 + 8 * j) * THREADS + of) * N + e);
+                    }
         }
     }
     __syncthreads();
-    const int64_t slot = blockIdx.x;
-    uint64_t *list = p.lists + slot * n;
+    int count = sh.count;
+    float cut = bound;
+    if (by_keys || count > p.room) {         // uniform: many ties, or hardly anything finite
+        __syncthreads();
+        list_by_keys(sh, l, t0, t1, n, list);
+        __syncthreads();
+        count = min(n, t1 - t0) | BY_KEYS;
+        cut = t1 - t0 > n ? key_value(list[n - 1]) : __int_as_float(0x7fffffff);
+    }
     if (warp == 0) {
-        const float2 x = lane < pieces * (THREADS / 32) ? part[lane] : make_float2(-INFINITY, 0.0f);
+        const float2 x = lane < THREADS / 32 ? part[lane] : make_float2(-INFINITY, 0.0f);
         float M = x.x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -409,17 +420,9 @@ template <typename T, int PER> __global__ void __launch_bounds__(THREADS, PER > 
         for (int o = 16; o > 0; o >>= 1)
             s += __shfl_xor_sync(FULL, s, o);
         if (lane == 0)
-            p.stats[slot] = make_float2(M, s);
-    }
-    const int count = sh.count;
-    if (by_keys || count > CAP) {            // uniform: many ties, or hardly anything finite
-        __syncthreads();
-        list_by_keys(sh, l, t0, t1, n, list);
-    } else {
-        rank_gathered<THREADS>(sh, count, n, [&](int r, uint64_t k) { list[r] = k; });
+            p.stats[blockIdx.x] = make_float4(M, s, cut, __int_as_float(count));
     }
 }
-static_assert(MAX_SPAN * THREADS / 32 <= 32, "a warp joins the parts");
 
 // Score of a candidate whose beam has offset c (-inf: nothing of the beam counts) and logit l.
 __device__ __forceinline__ float score_of(float c, float l) { return c == -INFINITY ? c : no_nan(c + l); }
@@ -454,20 +457,23 @@ template <typename T> __device__ __noinline__ void pick_all(const BeamArgs &p, i
 // One CTA per batch entry.
 template <typename T> __global__ void __launch_bounds__(PICK_THREADS) kda_beam_pick_kernel(const BeamArgs p)
 {
-    constexpr int HELD = 4;                // candidates a thread keeps in registers
     __shared__ __align__(16) Pick sh;
+    __shared__ uint64_t sel[SELECTED];     // candidates from the bound up
     __shared__ float c[32], own[32];       // the beams' offsets, and the scores of finished ones
     __shared__ int kind[32];               // 0: candidates from the lists; 1: nothing counts; 2: finished
-    const int b = blockIdx.x, tid = threadIdx.x, lane = tid % 32, n = p.K + 1;
+    __shared__ int selected;
+    const int b = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int w = tid / 32; w < p.W; w += PICK_THREADS / 32) {
+    if (tid == 0)
+        sh.count = selected = 0;
+    for (int w = warp; w < p.W; w += PICK_THREADS / 32) {
         const int64_t row = (int64_t)b * p.W + w;
         const bool done = p.finished && p.finished[row];
         const float score = p.beam_scores[row];
         float m = -INFINITY, s = 0.0f;
         if (!done) {
-            const float2 *st = p.stats + row * p.chunks;
-            float2 x = lane < p.chunks ? st[lane] : make_float2(-INFINITY, 0.0f);
+            const float4 *st = p.stats + row * p.chunks;
+            float4 x = lane < p.chunks ? st[lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
             m = x.x;
             for (int i = lane + 32; i < p.chunks; i += 32)
                 m = fmaxf(m, st[i].x);
@@ -493,56 +499,66 @@ template <typename T> __global__ void __launch_bounds__(PICK_THREADS) kda_beam_p
         }
     }
     __syncthreads();
-    // candidate i of beam w: a list entry, or for a beam whose candidates are all but one -inf its first tokens and eos
-    const uint32_t per = (uint32_t)p.chunks * n, total = per * p.W;
-    const uint64_t *lists = p.lists + (int64_t)b * total;
-    auto candidate = [&](uint32_t x) -> uint64_t {
-        const uint32_t w = x / per, i = x - w * per;
-        if (kind[w] == 0) {
-            const uint64_t k = lists[x];
-            return k ? key_of(score_of(c[w], key_value(k)), w * p.V + key_index(k)) : 0;
+    // hands every candidate to f, a warp at a list (or at a beam whose candidates are all -inf but for a finished one's
+    // eos: its first tokens, and eos); key 0: none
+    const float4 *stats = p.stats + (int64_t)b * p.W * p.chunks;
+    const uint64_t *lists = p.lists + (int64_t)b * p.W * p.chunks * p.room;
+    auto each = [&](auto f) {
+        for (int i = warp; i < p.W * p.chunks; i += PICK_THREADS / 32) {
+            const int w = i / p.chunks;
+            if (kind[w] == 0) {
+                const int have = __float_as_int(stats[i].w) & ~BY_KEYS;
+                for (int j = lane; j < (p.room + 31) / 32 * 32; j += 32) {
+                    const uint64_t k = j < p.room ? lists[(int64_t)i * p.room + j] : 0;
+                    f(j < have ? key_of(score_of(c[w], key_value(k)), (uint32_t)w * p.V + key_index(k)) : 0);
+                }
+            } else if (i % p.chunks == 0) {
+                for (int j = lane; j < (p.K + 32) / 32 * 32; j += 32) {
+                    const bool eos = kind[w] == 2 && (j < p.K ? j == p.eos : j == p.K && p.eos >= p.K);
+                    const int t = eos ? p.eos : j;
+                    f(eos || (j < p.K && j < p.V) ? key_of(eos ? own[w] : -INFINITY, (uint32_t)w * p.V + t) : 0);
+                }
+            }
         }
-        const bool done = kind[w] == 2;
-        uint32_t t = i;
-        if (i > (uint32_t)p.K || (i == (uint32_t)p.K && !(done && p.eos >= p.K)) ||
-            (i < (uint32_t)p.K && i >= (uint32_t)p.V))
-            return 0;
-        if (i == (uint32_t)p.K)
-            t = (uint32_t)p.eos;
-        return key_of(done && t == (uint32_t)p.eos ? own[w] : -INFINITY, w * p.V + t);
     };
-    uint64_t best = 0, held[HELD];
-#pragma unroll
-    for (int i = 0; i < HELD; i++) {
-        const uint32_t x = i * PICK_THREADS + tid;
-        held[i] = x < total ? candidate(x) : 0;
-        best = held[i] > best ? held[i] : best;
-    }
-    for (uint32_t x = HELD * PICK_THREADS + tid; x < total; x += PICK_THREADS) {
-        const uint64_t k = candidate(x);
+    uint64_t best = 0;
+    each([&](uint64_t k) {                 // gathered while there is room
         best = k > best ? k : best;
+        const unsigned m = __ballot_sync(FULL, k != 0);
+        int at = 0;
+        if (lane == 0)
+            at = atomicAdd(&sh.count, __popc(m));
+        at = __shfl_sync(FULL, at, 0) + __popc(m & ((1u << lane) - 1));
+        if (k != 0 && at < CAP)
+            sh.cand[at] = k;
+    });
+    __syncthreads();
+    const int total = sh.count;
+    if (total <= CAP) {
+        best = 0;
+        for (int x = tid; x < total; x += PICK_THREADS)
+            best = sh.cand[x] > best ? sh.cand[x] : best;
     }
     const uint64_t bound = group_bound<PICK_THREADS>(sh, best, p.K);
-    if (best >= bound) {
-#pragma unroll
-        for (int i = 0; i < HELD; i++)
-            if (held[i] >= bound)
-                gather(sh, held[i]);
-        for (uint32_t x = HELD * PICK_THREADS + tid; x < total; x += PICK_THREADS) {
-            const uint64_t k = candidate(x);
-            if (k >= bound)
-                gather(sh, k);
+    auto select = [&](uint64_t k) {
+        if (k >= bound) {
+            const int to = atomicAdd(&selected, 1);
+            if (to < SELECTED)
+                sel[to] = k;
         }
+    };
+    if (total <= CAP) {
+        for (int x = tid; x < total; x += PICK_THREADS)
+            select(sh.cand[x]);
+    } else {
+        each(select);
     }
     __syncthreads();
-    const int count = sh.count;
-    bool again = count > CAP;
+    const int count = selected;
+    bool again = count > SELECTED;
     if (!again) {
         // the K-th score, and whether a list may have cut off a logit that has it too
-        if (tid == 0)
-            sh.bound = 0;
-        __syncthreads();
-        rank_gathered<PICK_THREADS>(sh, count, p.K, [&](int r, uint64_t k) {
+        rank_gathered<PICK_THREADS>(sel, count, p.K, [&](int r, uint64_t k) {
             if (r == p.K - 1)
                 sh.bound = k;
             p.scores[(int64_t)b * p.K + r] = key_value(k);
@@ -551,17 +567,16 @@ template <typename T> __global__ void __launch_bounds__(PICK_THREADS) kda_beam_p
         });
         __syncthreads();
         const float last = key_value(sh.bound);
-        for (uint32_t x = tid; x < (uint32_t)p.W * p.chunks; x += PICK_THREADS) {
-            const uint32_t w = x / p.chunks;
+        for (int x = tid; x < p.W * p.chunks; x += PICK_THREADS) {
+            const int w = x / p.chunks;
             if (kind[w] != 0)
                 continue;
-            const uint64_t k = lists[x * n + n - 1];
-            if (!k)
-                continue;
-            const float l = key_value(k);
-            if (score_of(c[w], l) == last && (score_of(c[w], neighbour(l, true, sizeof(T) == 2)) == last ||
-                                              (l != -INFINITY &&
-                                               score_of(c[w], neighbour(l, false, sizeof(T) == 2)) == last)))
+            // a list by values has every logit from l up; one by keys may have left out equals of its last, l, too
+            const float l = stats[x].z;
+            const bool by_keys = __float_as_int(stats[x].w) & BY_KEYS, step16 = by_keys && sizeof(T) == 2;
+            if (l == l && score_of(c[w], l) == last &&
+                ((by_keys && score_of(c[w], neighbour(l, true, step16)) == last) ||
+                 (l != -INFINITY && score_of(c[w], neighbour(l, false, step16)) == last)))
                 again = true;
         }
     }
@@ -571,36 +586,27 @@ template <typename T> __global__ void __launch_bounds__(PICK_THREADS) kda_beam_p
 
 }  // namespace
 
-// Logits a thread holds of a piece, and pieces of a chunk.
-struct BeamCut {
-    int per, span;
-};
-static BeamCut beam_cut(int B, int W, int V)
+// Tokens of a chunk: long ones leave fewer lists to pick from, short ones put a small call's logits on more SMs.
+static int beam_chunk(int B, int W, int V)
 {
     const int64_t rows = (int64_t)B * W;
     auto ctas = [&](int chunk) { return rows * ((V + chunk - 1) / chunk); };
-    if (ctas(THREADS * 32 * MAX_SPAN) >= 304)
-        return {32, MAX_SPAN};
-    if (ctas(THREADS * 32) >= 152)
-        return {32, 1};
-    return {8, 1};
+    return ctas(MOST_CHUNK) >= 304 ? MOST_CHUNK : (ctas(8192) >= 152 ? 8192 : 2048);
 }
 static int beam_chunks(int B, int W, int V)
 {
-    const BeamCut c = beam_cut(B, W, V);
-    const int chunk = THREADS * c.per * c.span;
+    const int chunk = beam_chunk(B, W, V);
     return (V + chunk - 1) / chunk;
 }
+// Keys of a list: more than K + 1 reach a bound that is rounded down and may be tied.
+static int beam_room(int K) { return (2 * K + 32) / 32 * 32; }
 
 namespace {
 
 template <typename T> cudaError_t launch_beam(const BeamArgs &p, cudaStream_t st)
 {
     const unsigned grid = (unsigned)(p.chunks * p.B * p.W);
-    if (beam_cut(p.B, p.W, p.V).per == 32)
-        kda_beam_chunks_kernel<T, 32><<<grid, THREADS, 0, st>>>(p);
-    else
-        kda_beam_chunks_kernel<T, 8><<<grid, THREADS, 0, st>>>(p);
+    kda_beam_chunks_kernel<T><<<grid, THREADS, 0, st>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
@@ -649,7 +655,7 @@ extern "C" size_t kda_beam_select_workspace_size(int B, int W, int V, int K)
     if (B < 1 || W < 1 || W > 32 || V < 1 || V > (1 << 24) || K < 1 || K > 64 || (int64_t)K > (int64_t)W * V ||
         (int64_t)B * W > INT32_MAX)
         return 0;
-    return (size_t)B * W * beam_chunks(B, W, V) * (sizeof(float2) + (K + 1) * sizeof(uint64_t));
+    return (size_t)B * W * beam_chunks(B, W, V) * (sizeof(float4) + beam_room(K) * sizeof(uint64_t));
 }
 
 extern "C" kda_status_t kda_beam_select_ws(const void *logits, kda_dtype_t dtype, int64_t row_stride,
@@ -665,8 +671,9 @@ extern "C" kda_status_t kda_beam_select_ws(const void *logits, kda_dtype_t dtype
         return KDA_ERR_INVALID_ARGUMENT;
     BeamArgs p{logits, row_stride, beam_scores, finished, eos, scores, tokens, parents, B, W, V, K};
     p.chunks = beam_chunks(B, W, V);
-    p.span = beam_cut(B, W, V).span;
-    p.stats = static_cast<float2 *>(workspace);
+    p.chunk = beam_chunk(B, W, V);
+    p.room = beam_room(K);
+    p.stats = static_cast<float4 *>(workspace);
     p.lists = reinterpret_cast<uint64_t *>(p.stats + (size_t)B * W * p.chunks);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = dtype == KDA_DTYPE_BF16 ? launch_beam<__nv_bfloat16>(p, st) : launch_beam<float>(p, st);
