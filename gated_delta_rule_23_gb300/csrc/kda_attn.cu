@@ -93,7 +93,9 @@ AttnArgs make_attn(const void *q, int64_t q_stride, const void *k_cache, const v
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.lse = lse;
     p.scale_log2 = scale * LOG2E;
-    p.window = window, p.sinks = sinks;
+    // no position is beyond what the table addresses, so neither need a bound be
+    const int cap = max_pages * page;
+    p.window = window < cap ? window : cap, p.sinks = sinks < cap ? sinks : cap;
     p.hq = Hq, p.group = Hq / Hkv;
     p.cache = make_cache(k_cache, v_cache, block_table, kv_lens, Hkv, D, pages, page, max_pages);
     p.tok = Tokens{cu_seqlens, T, N};
@@ -115,16 +117,18 @@ AttnPlan make_plan(int window, int sinks, bool varlen, int N, int64_t T, int Hq,
     const int group = Hq / Hkv;
     const int64_t tokens = varlen ? T : (int64_t)N * T;
     plan.rows = tokens * Hq;
-    plan.tiles = varlen ? (T * group + (int64_t)(ATTN_ROWS - 1) * N) / ATTN_ROWS
-                        : (int64_t)N * ((T * group + ATTN_ROWS - 1) / ATTN_ROWS);
-    if (plan.tiles > T * group && varlen)
-        plan.tiles = T * group;           // a tile holds a row at least
+    plan.granule = page < 32 ? page : 32;
+    int64_t tiles = varlen ? (T * group + (int64_t)(ATTN_ROWS - 1) * N) / ATTN_ROWS
+                           : (int64_t)N * ((T * group + ATTN_ROWS - 1) / ATTN_ROWS);
+    if (varlen && tiles > T * group)
+        tiles = T * group;                // a tile holds a row at least
     const int sms = device_sms();
-    const int64_t ctas = plan.tiles * Hkv;
+    const int64_t ctas = tiles * Hkv;
     const int64_t key_tiles = (most_keys(window, sinks, T < ATTN_ROWS ? T : ATTN_ROWS, page, max_pages) + 127) / 128 + 1;
     int64_t s = ctas > 0 ? sms / ctas : 1;
     s = s < key_tiles / 2 ? s : key_tiles / 2;
     plan.splits = s < 1 ? 1 : (s > 64 ? 64 : (int)s);
+    plan.items = (int)(ctas * plan.splits);
     plan.wait_polls = wait_limit();
     return plan;
 }

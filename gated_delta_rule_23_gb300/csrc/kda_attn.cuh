@@ -25,7 +25,8 @@ constexpr int ATTN_ROWS = 256;   // query rows of a tile
 
 struct AttnPlan {
     int splits;
-    int64_t tiles;          // row tiles of all sequences (ragged: an upper bound)
+    int items;              // (row tile, key head, split) items (ragged: an upper bound)
+    int granule;            // positions of a cache page that are copied together
     float *part_o;          // [splits][tokens * hq][dim] fp32, unnormalised (workspace)
     float2 *part_ml;        // [splits][tokens * hq]: running maximum (base 2) and sum
     int64_t rows;           // tokens * hq

@@ -13,7 +13,8 @@
 // overflow in the fp32 sums.
 //
 // Warps 0..3 and 4..7: the halves' softmax and epilogue; warp 8: bulk tensor copies (K and V tiles in a ring); warp 9:
-// tensor-core issue.
+// tensor-core issue.  One CTA an SM walks the (row tile, key head, split) items: the copies run ahead into the next
+// item, its Q is loaded and its first S formed while the last item's rows are scaled and stored.
 //
 // A key that a row does not see gets P = 0.  0 x v is NaN for an infinite or NaN v, and the matrix product has no way
 // to skip it: rows past the sequence's end are cleared in shared memory, and an output row that does not come out
@@ -29,7 +30,11 @@ namespace kda {
 namespace {
 
 constexpr int KEYS = 128;                    // keys of a tile
-constexpr int THREADS = 320;
+constexpr int THREADS = 384;                 // three warpgroups (two warps of the last have no role)
+// Registers a thread: 168 at launch (65,536 / 384); the softmax warpgroups, which hold a row of S, take what the third gives
+// back: 2 x 128 x 208 + 128 x 88 = 384 x 168.
+constexpr int REGS_SOFTMAX = 208, REGS_REST = 88;
+static_assert(2 * 128 * REGS_SOFTMAX + 128 * REGS_REST <= THREADS * 168, "register split");
 constexpr int HALF = 128;                    // rows of a half
 constexpr int TMEM_COLS = 512;
 constexpr int TM_S = 0, TM_O = 256;          // columns: S of both halves (128 each), O of both halves
@@ -43,49 +48,47 @@ template <int DIM> struct Shape {
     static constexpr int SMEM = 1024 + BAR + 256;            // 1024: alignment of the swizzle atoms
 };
 
-struct Tile {             // what every warp of the CTA knows about its work
+struct Tile {             // one item; positions, rows and tokens fit 32 bits (checked on the host)
     int n, kvh, split;
-    int64_t len_q, bos;   // tokens of the sequence, first token of it in the batch
-    int64_t len;          // its tokens in the cache
-    int64_t row0;         // first row of the tile
-    int rows;             // rows of the tile, 1..256
-    int granule;          // positions of a granule
-    int64_t sink_span;    // virtual keys of the sinks (a multiple of the granule)
-    int64_t start;        // position of virtual key sink_span
-    int64_t virt;         // virtual keys in all
+    int len_q, bos;       // tokens of the sequence, first token of it in the batch
+    int len;              // its tokens in the cache
+    int row0, rows;       // first row of the tile, rows of it (1..256)
+    int sink_span;        // virtual keys of the sinks (a multiple of the granule)
+    int start;            // position of virtual key sink_span
+    int virt;             // virtual keys in all
     int t0, t1;           // key tiles of this split
     int lo[2], hi[2];     // of them, the ones a half needs
 };
 
-__device__ __forceinline__ int64_t virt_pos(const Tile &w, int64_t v) { return v < w.sink_span ? v : v - w.sink_span + w.start; }
+__device__ __forceinline__ int virt_pos(const Tile &w, int v) { return v < w.sink_span ? v : v - w.sink_span + w.start; }
 
 // Position of row r (of the sequence).
-__device__ __forceinline__ int64_t row_pos(const AttnArgs &p, const Tile &w, int64_t r) { return w.len - w.len_q + r / p.group; }
+__device__ __forceinline__ int row_pos(const AttnArgs &p, const Tile &w, int r) { return w.len - w.len_q + r / p.group; }
 
-// Finds the CTA's tile; false when there is none.  By a whole warp.
-__device__ bool find_tile(const AttnArgs &p, const AttnPlan &plan, Tile &w, bool &bad)
+// Fills in item x; false when there is none (ragged batches have fewer tiles than the bound the grid is made for).  By a
+// whole warp.
+__device__ __forceinline__ bool find_tile(const AttnArgs &p, const AttnPlan &plan, int x, Tile &w, bool &bad)
 {
     const int lane = threadIdx.x & 31;
     // heaviest first where the work grows along a sequence: the last tiles of all key heads
-    int64_t x = blockIdx.x;
-    w.kvh = (int)(x % p.cache.hkv);
+    w.kvh = x % p.cache.hkv;
     x /= p.cache.hkv;
-    w.split = blockIdx.y;
-    int64_t tile;
+    w.split = x % plan.splits;
+    x /= plan.splits;
+    int tile = 0;
     if (p.tok.cu) {
-        int64_t before = 0;
+        int before = 0;
         bool found = false;
         for (int base = 0; base < p.tok.N && !found; base += 32) {
             const int n = base + lane;
-            int64_t bos = 0, len = 0, cnt = 0;
-            if (n < p.tok.N) {
+            int64_t bos = 0, len = 0;
+            if (n < p.tok.N)
                 bad |= seq_range(p.tok.cu, n, p.tok.N, p.tok.T, bos, len);
-                cnt = (len * p.group + ATTN_ROWS - 1) / ATTN_ROWS;
-            }
-            int64_t sum = cnt;
+            const int cnt = (int)((len * p.group + ATTN_ROWS - 1) / ATTN_ROWS);
+            int sum = cnt;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(FULL, sum, o);
+                const int y = __shfl_up_sync(FULL, sum, o);
                 if (lane >= o)
                     sum += y;
             }
@@ -93,8 +96,8 @@ __device__ bool find_tile(const AttnArgs &p, const AttnPlan &plan, Tile &w, bool
             if (m) {
                 const int src = __ffs(m) - 1;
                 w.n = base + src;
-                w.bos = __shfl_sync(FULL, bos, src);
-                w.len_q = __shfl_sync(FULL, len, src);
+                w.bos = __shfl_sync(FULL, (int)bos, src);
+                w.len_q = __shfl_sync(FULL, (int)len, src);
                 tile = x - (before + __shfl_sync(FULL, sum - cnt, src));
                 found = true;
             }
@@ -103,52 +106,43 @@ __device__ bool find_tile(const AttnArgs &p, const AttnPlan &plan, Tile &w, bool
         if (!found)
             return false;
     } else {
-        const int64_t per = (p.tok.T * p.group + ATTN_ROWS - 1) / ATTN_ROWS;
-        w.n = (int)(x % p.tok.N);
+        const int per = (int)((p.tok.T * p.group + ATTN_ROWS - 1) / ATTN_ROWS);
+        w.n = x % p.tok.N;
         tile = per - 1 - x / p.tok.N;
-        w.len_q = p.tok.T;
-        w.bos = w.n * p.tok.T;
+        w.len_q = (int)p.tok.T;
+        w.bos = (int)(w.n * p.tok.T);
     }
     w.row0 = tile * ATTN_ROWS;
-    const int64_t left = w.len_q * p.group - w.row0;
-    w.rows = (int)(left < ATTN_ROWS ? left : ATTN_ROWS);
-    w.len = cache_len(p.cache, w.n, bad);
-    const int page = 1 << p.cache.page_shift;
-    w.granule = page < 32 ? page : 32;
-    const int64_t g = w.granule;
-    const int64_t p0 = row_pos(p, w, w.row0), p1 = row_pos(p, w, w.row0 + w.rows - 1);
-    if (p1 < 0) {                                   // nothing before the first token
-        w.sink_span = w.start = w.virt = 0;
-    } else {
-        int64_t lo = p0 - p.window + 1;
-        lo = lo < 0 ? 0 : lo / g * g;
-        int64_t sink = ((int64_t)p.sinks + g - 1) / g * g;
+    w.rows = min(w.len_q * p.group - w.row0, ATTN_ROWS);
+    w.len = (int)cache_len(p.cache, w.n, bad);
+    const int g = plan.granule;
+    const int p0 = row_pos(p, w, w.row0), p1 = row_pos(p, w, w.row0 + w.rows - 1);
+    w.sink_span = w.start = w.virt = 0;
+    if (p1 >= 0) {                                  // else all rows are before the first token
+        int lo = max(p0 - p.window + 1, 0) & -g, sink = (p.sinks + g - 1) & -g;
         if (lo <= sink)
             sink = lo = 0;                          // one range
         w.sink_span = sink;
         w.start = lo;
         w.virt = sink + (p1 + 1 - lo);
     }
-    const int64_t tiles = (w.virt + KEYS - 1) / KEYS;
-    w.t0 = (int)(tiles * w.split / plan.splits);
-    w.t1 = (int)(tiles * (w.split + 1) / plan.splits);
+    const int tiles = (w.virt + KEYS - 1) / KEYS;
+    w.t0 = (int)((int64_t)tiles * w.split / plan.splits);
+    w.t1 = (int)((int64_t)tiles * (w.split + 1) / plan.splits);
 #pragma unroll
     for (int h = 0; h < 2; h++) {
         const int first = h * HALF, last = min(w.rows, first + HALF) - 1;
         w.lo[h] = w.hi[h] = w.t0;
         if (first > last)
             continue;
-        const int64_t a = row_pos(p, w, w.row0 + first) - p.window + 1, b = row_pos(p, w, w.row0 + last);
+        const int a = row_pos(p, w, w.row0 + first) - p.window + 1, b = row_pos(p, w, w.row0 + last);
         if (b < 0)
             continue;
-        // the half's window, in tiles; tiles with sinks count for every half
-        int64_t lo = a <= w.start ? w.sink_span : a - w.start + w.sink_span;
-        lo = w.sink_span > 0 || p.sinks > 0 ? 0 : lo / KEYS;
-        const int64_t hi = (b - w.start + w.sink_span) / KEYS + 1;
-        w.lo[h] = (int)(lo < w.t0 ? w.t0 : (lo > w.t1 ? w.t1 : lo));
-        w.hi[h] = (int)(hi < w.t0 ? w.t0 : (hi > w.t1 ? w.t1 : hi));
-        if (w.hi[h] < w.lo[h])
-            w.hi[h] = w.lo[h];
+        // the half's window, in tiles; with sinks a half needs the tiles from the first on
+        const int lo = p.sinks > 0 || a <= w.start ? 0 : (a - w.start) / KEYS;
+        const int hi = (b - w.start + w.sink_span) / KEYS + 1;
+        w.lo[h] = min(max(lo, w.t0), w.t1);
+        w.hi[h] = max(min(max(hi, w.t0), w.t1), w.lo[h]);
     }
     return true;
 }
@@ -190,14 +184,47 @@ __device__ __forceinline__ void tmem_ld64(uint32_t addr, float *s)
 }
 #undef R8
 
-// bits a..b (inclusive, any integers) of a 128-bit mask, word w
-__device__ __forceinline__ uint32_t range_word(int64_t a, int64_t b, int w)
+// tcgen05.st of 32 columns without the wait for its completion
+__device__ __forceinline__ void tmem_put32(uint32_t addr, const uint32_t (&u)[32])
 {
-    const int64_t lo = a - 32 * w, hi = b - 32 * w;
-    if (hi < 0 || lo > 31 || hi < lo)
-        return 0;
-    const uint32_t x = hi >= 31 ? FULL : (2u << (int)hi) - 1u;
-    return lo <= 0 ? x : x & (FULL << (int)lo);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+                 ::"r"(addr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
+                   "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]),
+                   "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]),
+                   "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
+                 : "memory");
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b)
+{
+    f2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// bits a..b (inclusive, any integers) of a 128-bit mask, word w; PTX shifts of 32 and more give 0
+__device__ __forceinline__ uint32_t range_word(int a, int b, int w)
+{
+    uint32_t x, y;
+    asm("shl.b32 %0, %1, %2;" : "=r"(x) : "r"(FULL), "r"(max(a - 32 * w, 0)));
+    asm("shr.u32 %0, %1, %2;" : "=r"(y) : "r"(FULL), "r"(max(31 - (b - 32 * w), 0)));
+    return x & y;
+}
+
+// Q rows of item w's half into shared memory (not waited for): a warp loads its own 32 rows, lanes along a row; rows past
+// the end are zeros.
+template <int DIM> __device__ __forceinline__ void load_q(const AttnArgs &p, const Tile &w, uint32_t sm_q, int warp, int lane)
+{
+    constexpr int C = DIM / 8;                   // 16-byte vectors of a row
+    const int c = lane % C;
+    for (int i = lane / C; i < 32; i += 32 / C) {
+        const int row = i + 32 * warp, rh = row & (HALF - 1);
+        const bool in = row < w.rows;
+        const int R = w.row0 + (in ? row : 0);
+        const __nv_bfloat16 *src = p.q + (int64_t)(w.bos + R / p.group) * p.q_stride + (w.kvh * p.group + R % p.group) * DIM + c * 8;
+        cp_async16(sm_q + (warp / 4) * Shape<DIM>::TILE + (c / 8) * (HALF * 128) + rh * 128 + (((c & 7) ^ (rh & 7)) << 4), src, in);
+    }
+    cp_async_commit();
 }
 
 template <int DIM>
@@ -211,22 +238,18 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char *const smem = smem_raw + (base - smem_u32(smem_raw));
     const uint32_t sm_q = base, sm_ring = base + 2 * S::TILE, bar = base + S::BAR;
-    const uint32_t b_full = bar, b_empty = bar + 8 * S::SLOTS, b_q = bar + 16 * S::SLOTS, b_s = b_q + 8, b_p = b_s + 16,
+    const uint32_t b_full = bar, b_empty = bar + 8 * S::SLOTS, b_q = bar + 16 * S::SLOTS, b_s = b_q + 16, b_p = b_s + 16,
                    b_o = b_p + 16, b_drain = b_o + 16;
     __shared__ uint32_t tmem_slot;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
-
-    Tile w;
-    bool bad = false;
-    if (!find_tile(p, plan, w, bad))
-        return;                                  // uniform over the CTA
+    const int items = plan.items, g = plan.granule;
     if (tid == 0) {
         for (int i = 0; i < S::SLOTS; i++) {
             mbar_init(b_full + 8 * i, 1);
             mbar_init(b_empty + 8 * i, 1);
         }
-        mbar_init(b_q, 8);
         for (int h = 0; h < 2; h++) {
+            mbar_init(b_q + 8 * h, 4);
             mbar_init(b_s + 8 * h, 1);
             mbar_init(b_p + 8 * h, HALF);
             mbar_init(b_o + 8 * h, 1);
@@ -243,160 +266,173 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    const int tiles = w.t1 - w.t0;
-    bool timeout = false;
+    bool timeout = false, bad = false;
 
     if (warp < 8) {
         // ------------------------------------------------------------ Q, softmax, epilogue
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
         const int h = warp / 4;
-        const int r = tid;                                       // row of the tile
-        const bool mine = r < w.rows;
-        const int64_t R = w.row0 + r;
-        const int64_t tok = w.bos + (mine ? R / p.group : 0);
-        const int head = w.kvh * p.group + (int)(mine ? R % p.group : 0);
-        const int64_t pos = mine ? row_pos(p, w, R) : -1;
-        // Q: a warp loads its own 32 rows, lanes along a row; rows past the end are zeros
-        for (int i = lane; i < 32 * (DIM / 8); i += 32) {
-            const int row = i / (DIM / 8) + 32 * warp, c = i % (DIM / 8);
-            const bool in = row < w.rows;
-            const int64_t RR = w.row0 + (in ? row : 0);
-            const __nv_bfloat16 *src = p.q + (w.bos + RR / p.group) * p.q_stride +
-                                       (int64_t)(w.kvh * p.group + RR % p.group) * DIM + c * 8;
-            const int rh = row & (HALF - 1);
-            cp_async16(sm_q + h * S::TILE + (c / 8) * (HALF * 128) + rh * 128 + (((c & 7) ^ (rh & 7)) << 4), src, in);
-        }
-        cp_async_commit();
-        cp_async_wait_all();
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(b_q);
-
         const uint32_t tm_lane = (uint32_t)(warp & 3) << 21;     // the warp's 32 lanes
         const uint32_t tm_s = tmem + TM_S + h * 128 + tm_lane, tm_o = tmem + TM_O + h * 128 + tm_lane;
-        float m = -INFINITY, l = 0.0f;
-        int n_s = 0;
-        for (int t = w.lo[h]; t < w.hi[h]; t++, n_s++) {
-            const int64_t v0 = (int64_t)t * KEYS;
-            // what the row sees of the tile, as 128 bits
-            uint32_t mask[4];
-            {
-                const int64_t a = pos - p.window + 1;
-                // columns of the window range, then those of the sink range
-                const int64_t wa = (a > w.start ? a : w.start) - w.start + w.sink_span - v0, wb = pos - w.start + w.sink_span - v0;
-                const int64_t sb = (w.sink_span > 0 ? min((int64_t)p.sinks, pos + 1) : 0) - 1 - v0;
-                const int64_t ka = (w.sink_span > 0 ? (int64_t)0 : min((int64_t)p.sinks, pos + 1)) - 1 - v0;
-#pragma unroll
-                for (int x = 0; x < 4; x++) {
-                    mask[x] = range_word(wa, wb, x);
-                    if (p.sinks > 0)
-                        mask[x] |= range_word(-v0, sb > ka ? sb : ka, x);
+        int ring = 0;                                            // key tiles of the items before
+        uint32_t s_phase = 0, o_phase = 0;
+        Tile w{};
+        int x = blockIdx.x;
+        bool have = x < items && find_tile(p, plan, x, w, bad);
+        auto q_ready = [&]() {                                   // the warp's Q rows are in shared memory
+            cp_async_wait_all();
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(b_q + 8 * h);
+        };
+        if (have && w.hi[h] > w.lo[h]) {
+            load_q<DIM>(p, w, sm_q, warp, lane);
+            q_ready();
+        }
+        while (have) {
+            const bool mine = tid < w.rows;
+            const int R = w.row0 + tid;
+            const int tok = w.bos + (mine ? R / p.group : 0), head = w.kvh * p.group + (mine ? R % p.group : 0);
+            const int pos = mine ? row_pos(p, w, R) : -1, split = w.split, n = w.n;
+            float m = -INFINITY, l = 0.0f;
+            bool any = false;
+            for (int t = w.lo[h]; t < w.hi[h]; t++) {
+                const int v0 = t * KEYS;
+                // the sequence's end inside the tile: what lies behind it in its page is cleared from V (K's scores are
+                // masked)
+                const int end_v = w.len - w.start + w.sink_span - v0;
+                if (end_v > 0 && end_v < KEYS && (end_v & (g - 1))) {
+                    const int it = 2 * (ring + t - w.t0) + 1, slot = it % S::SLOTS;
+                    if (!mbar_wait(b_full + 8 * slot, (it / S::SLOTS) & 1, plan.wait_polls)) {
+                        timeout = true;
+                        break;
+                    }
+                    const int count = (g - (end_v & (g - 1))) * 8;       // 16-byte vectors of a column block
+                    uint4 *v = reinterpret_cast<uint4 *>(smem + 2 * S::TILE + slot * S::TILE) + end_v * 8;
+                    for (int i = tid & (HALF - 1); i < count * CB; i += HALF)
+                        v[(i / count) * (KEYS * 8) + i % count] = make_uint4(0, 0, 0, 0);
+                    fence_async_smem();
                 }
-            }
-            const bool all = __all_sync(FULL, (mask[0] & mask[1] & mask[2] & mask[3]) == FULL);
-            // the sequence's end inside the tile: what lies behind it in its page is cleared from V (K's scores are masked)
-            const int64_t end_v = w.len - w.start + w.sink_span - v0;
-            if (end_v > 0 && end_v < KEYS && end_v % w.granule) {
-                const int it = 2 * (t - w.t0) + 1, slot = it % S::SLOTS;
-                if (!mbar_wait(b_full + 8 * slot, (it / S::SLOTS) & 1, plan.wait_polls)) {
+                if (!mbar_wait(b_s + 8 * h, s_phase, plan.wait_polls)) {
                     timeout = true;
                     break;
                 }
-                const int first = (int)end_v, last = (int)((end_v + w.granule - 1) / w.granule * w.granule);
-                uint4 *v = reinterpret_cast<uint4 *>(smem + 2 * S::TILE + slot * S::TILE);
-                for (int i = tid & (HALF - 1); i < (last - first) * 8 * CB; i += HALF)
-                    v[(i / ((last - first) * 8)) * (KEYS * 8) + first * 8 + i % ((last - first) * 8)] = make_uint4(0, 0, 0, 0);
-                fence_async_smem();
+                s_phase ^= 1;
+                tc_fence_after();
+                float s[128];
+                tmem_ld64(tm_s, s);
+                tmem_ld64(tm_s + 64, s + 64);
+                // columns of the tile that the row sees: the window's, and the sinks'
+                const int wa = max(pos - p.window + 1, w.start) - w.start + w.sink_span - v0;
+                const int wb = pos - w.start + w.sink_span - v0;
+                if (!__all_sync(FULL, wa <= 0 && wb >= KEYS - 1)) {
+                    const int sb = min(p.sinks, pos + 1) - 1 - v0;
+#pragma unroll
+                    for (int x4 = 0; x4 < 4; x4++) {
+                        const uint32_t mask = range_word(wa, wb, x4) | range_word(-v0, sb, x4);
+#pragma unroll
+                        for (int c = 0; c < 32; c++)
+                            s[32 * x4 + c] = (mask >> c) & 1 ? s[32 * x4 + c] : -INFINITY;
+                    }
+                }
+                float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int c = 4; c < 128; c += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        mx[e] = fmaxf(mx[e], c + 4 + e < 128 ? fmaxf(s[c + e], s[c + 4 + e]) : s[c + e]);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+                // 0 x inf (scale 0) is NaN and leaves m alone
+                const bool move = top > m + RESCALE_AT;
+                if (!any) {
+                    if (top > m)
+                        m = top;
+                } else if (__any_sync(FULL, move)) {
+                    const float a = move ? ex2_approx(m - top) : 1.0f;
+                    if (move)
+                        m = top;
+                    l *= a;
+#pragma unroll
+                    for (int c = 0; c < DIM; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tm_o + c, o);
+#pragma unroll
+                        for (int e = 0; e < 32; e++)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                        tmem_put32(tm_o + c, o);
+                    }
+                }
+                any = true;
+                const float mu = m == -INFINITY ? 0.0f : m;
+                const f2 sc = f2_pack(p.scale_log2, p.scale_log2), mm = f2_pack(-mu, -mu);
+                f2 l0 = 0, l1 = 0;
+#pragma unroll
+                for (int c = 0; c < 128; c += 64) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int e = 0; e < 32; e++) {
+                        const f2 y = f2_fma(f2_pack(s[c + 2 * e], s[c + 2 * e + 1]), sc, mm);
+                        const float a = ex2_approx(f2_lo(y)), b = ex2_approx(f2_hi(y));
+                        if (e & 1)
+                            l1 = f2_add(l1, f2_pack(a, b));
+                        else
+                            l0 = f2_add(l0, f2_pack(a, b));
+                        const __nv_bfloat162 z = __floats2bfloat162_rn(a, b);
+                        pk[e] = *reinterpret_cast<const uint32_t *>(&z);
+                    }
+                    tmem_put32(tm_s + c / 2, pk);
+                }
+                l0 = f2_add(l0, l1);
+                l += f2_lo(l0) + f2_hi(l0);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                mbar_arrive(b_p + 8 * h);
             }
-            if (!mbar_wait(b_s + 8 * h, n_s & 1, plan.wait_polls)) {
+            if (__any_sync(FULL, timeout)) {
                 timeout = true;
                 break;
             }
-            tc_fence_after();
-            float s[128];
-            tmem_ld64(tm_s, s);
-            tmem_ld64(tm_s + 64, s + 64);
-            if (!all) {
-#pragma unroll
-                for (int c = 0; c < 128; c++)
-                    s[c] = (mask[c / 32] >> (c % 32)) & 1 ? s[c] : -INFINITY;
+            // The next item's Q: the half's last S is formed, so its Q rows are free.
+            const bool stored = any;
+            ring += w.t1 - w.t0;
+            x += gridDim.x;
+            have = x < items && find_tile(p, plan, x, w, bad);
+            const bool more = have && w.hi[h] > w.lo[h];
+            if (more)
+                load_q<DIM>(p, w, sm_q, warp, lane);
+            if (stored) {
+                if (!mbar_wait(b_o + 8 * h, o_phase, plan.wait_polls))
+                    timeout = true;
+                o_phase ^= 1;
+                tc_fence_after();
             }
-            float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
-#pragma unroll
-            for (int c = 4; c < 128; c += 4) {
-                mx0 = fmaxf(mx0, s[c]);
-                mx1 = fmaxf(mx1, s[c + 1]);
-                mx2 = fmaxf(mx2, s[c + 2]);
-                mx3 = fmaxf(mx3, s[c + 3]);
-            }
-            const float top = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * p.scale_log2;
-            // 0 x inf (scale 0) is NaN and leaves m alone
-            const bool move = top > m + RESCALE_AT;
-            if (n_s == 0) {
-                if (top > m)
-                    m = top;
-            } else if (__any_sync(FULL, move)) {
-                const float a = move ? ex2_approx(m - top) : 1.0f;
-                if (move)
-                    m = top;
-                l *= a;
-#pragma unroll
-                for (int c = 0; c < DIM; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(tm_o + c, o);
-#pragma unroll
-                    for (int e = 0; e < 32; e++)
-                        o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-                    tmem_st32(tm_o + c, o);
-                }
-            }
-            const float mu = m == -INFINITY ? 0.0f : m;
-            const f2 sc = f2_pack(p.scale_log2, p.scale_log2), mm = f2_pack(-mu, -mu);
-            float l0 = 0.0f, l1 = 0.0f;
-#pragma unroll
-            for (int c = 0; c < 128; c += 64) {
-                uint32_t pk[32];
-#pragma unroll
-                for (int e = 0; e < 32; e++) {
-                    const f2 x = f2_fma(f2_pack(s[c + 2 * e], s[c + 2 * e + 1]), sc, mm);
-                    const float a = ex2_approx(f2_lo(x)), b = ex2_approx(f2_hi(x));
-                    l0 += a;
-                    l1 += b;
-                    const __nv_bfloat162 y = __floats2bfloat162_rn(a, b);
-                    pk[e] = *reinterpret_cast<const uint32_t *>(&y);
-                }
-                tmem_st32(tm_s + c / 2, pk);
-            }
-            l += l0 + l1;
-            tc_fence_before();
-            mbar_arrive(b_p + 8 * h);
-        }
-        // epilogue: the row's thread scales and stores it
-        if (n_s > 0 && !timeout) {
-            if (!mbar_wait(b_o + 8 * h, 0, plan.wait_polls))
+            if (more)
+                q_ready();
+            if (__any_sync(FULL, timeout)) {
                 timeout = true;
-            tc_fence_after();
-        }
-        if (!__any_sync(FULL, timeout)) {
+                break;
+            }
+            // epilogue: the row's thread scales and stores it
             bool finite = l <= FLT_MAX;
-            const int64_t at = tok * p.hq + head;
-            const bool split = plan.splits > 1;
-            const float inv = split ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+            const int64_t at = (int64_t)tok * p.hq + head;
+            const bool part = plan.splits > 1;
+            const float inv = part ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
 #pragma unroll
             for (int c = 0; c < DIM; c += 32) {
                 uint32_t o[32];
-                if (n_s > 0)
+                if (stored)
                     tmem_ld32(tm_o + c, o);
 #pragma unroll
                 for (int e = 0; e < 32; e++) {
-                    const float x = n_s > 0 ? __uint_as_float(o[e]) : 0.0f;
-                    finite &= fabsf(x) <= FLT_MAX;
-                    o[e] = __float_as_uint(split || l != 0.0f ? x * inv : 0.0f);
+                    const float y = stored ? __uint_as_float(o[e]) : 0.0f;
+                    finite &= fabsf(y) <= FLT_MAX;
+                    o[e] = __float_as_uint(part || l != 0.0f ? y * inv : 0.0f);
                 }
                 if (!mine)
                     continue;
-                if (split) {
-                    float4 *dst = reinterpret_cast<float4 *>(plan.part_o + (w.split * plan.rows + at) * DIM + c);
+                if (part) {
+                    float4 *dst = reinterpret_cast<float4 *>(plan.part_o + (split * plan.rows + at) * DIM + c);
 #pragma unroll
                     for (int e = 0; e < 8; e++)
                         dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
@@ -416,76 +452,90 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                     }
                 }
             }
-            if (mine && split)
-                plan.part_ml[w.split * plan.rows + at] = make_float2(m, l);
+            tc_fence_before();                // O is read before the next item's first P lets it be overwritten
+            if (mine && part)
+                plan.part_ml[split * plan.rows + at] = make_float2(m, l);
             else if (mine && p.lse)
                 p.lse[at] = l == 0.0f ? -INFINITY : LN2 * (m + log2f(l));
-            __syncwarp();                     // the rows' first stores come before the ones below
-            unsigned again = __ballot_sync(FULL, mine && !finite && !split);
-            while (again) {
-                const int src = __ffs(again) - 1;
-                again &= again - 1;
-                attn_row<DIM>(p, w.n, __shfl_sync(FULL, tok, src), __shfl_sync(FULL, head, src), __shfl_sync(FULL, pos, src), bad);
+            unsigned again = __ballot_sync(FULL, mine && !finite && !part);
+            if (again) {
+                __syncwarp();                 // the rows' first stores come before the ones below
+                for (; again; again &= again - 1) {
+                    const int src = __ffs(again) - 1;
+                    attn_row<DIM>(p, n, __shfl_sync(FULL, tok, src), __shfl_sync(FULL, head, src), __shfl_sync(FULL, pos, src), bad);
+                }
             }
         }
-    } else if (warp == 8) {
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
+    }
+    if (warp == 8) {
         // ------------------------------------------------------------ copies
-        const int ng = KEYS / w.granule;
-        const int64_t last = virt_pos(w, w.virt > 0 ? w.virt - 1 : 0);
+        const int ng = KEYS / g;
         int issued = 0;
-        for (int t = 0; t < tiles && !timeout; t++) {
-            int y = INT32_MAX - 4096;                            // outside the cache: zeros
-            if (lane < ng) {
-                const int64_t v = (int64_t)(w.t0 + t) * KEYS + lane * w.granule;
-                const int64_t j = virt_pos(w, v);
-                if (v < w.virt && j <= last && j < w.len) {
-                    const int32_t id = p.cache.table[(int64_t)w.n * p.cache.max_pages + (j >> p.cache.page_shift)];
-                    if (id >= 0 && id < p.cache.pages)
-                        y = (int)((((int64_t)id * p.cache.hkv + w.kvh) << p.cache.page_shift) + (j & ((1 << p.cache.page_shift) - 1)));
-                    else
-                        bad = true;
-                }
-            }
-#pragma unroll
-            for (int kv = 0; kv < 2; kv++) {
-                const int it = 2 * t + kv, slot = it % S::SLOTS;
-                if (it >= S::SLOTS && !mbar_wait(b_empty + 8 * slot, ((it / S::SLOTS) - 1) & 1, plan.wait_polls))
-                    timeout = true;
-                if (__any_sync(FULL, timeout)) {
-                    timeout = true;
-                    break;
-                }
-                if (lane == 0)
-                    mbar_expect_tx(b_full + 8 * slot, S::TILE);
-                __syncwarp();
+        Tile w;
+        for (int x = blockIdx.x; x < items && !timeout && find_tile(p, plan, x, w, bad); x += gridDim.x) {
+            for (int t = w.t0; t < w.t1 && !timeout; t++) {
+                int y = INT32_MAX - 4096;                        // outside the cache: zeros
                 if (lane < ng) {
-#pragma unroll
-                    for (int cb = 0; cb < CB; cb++)
-                        tma_load_2d(sm_ring + slot * S::TILE + cb * (KEYS * 128) + lane * w.granule * 128, kv ? &vmap : &kmap,
-                                    cb * 64, y, b_full + 8 * slot);
+                    const int v = t * KEYS + lane * g, j = virt_pos(w, v);
+                    if (v < w.virt && j < w.len) {
+                        const int32_t id = p.cache.table[(int64_t)w.n * p.cache.max_pages + (j >> p.cache.page_shift)];
+                        if (id >= 0 && id < p.cache.pages)
+                            y = (int)((((int64_t)id * p.cache.hkv + w.kvh) << p.cache.page_shift) + (j & ((1 << p.cache.page_shift) - 1)));
+                        else
+                            bad = true;
+                    }
                 }
-                issued = it + 1;
+#pragma unroll
+                for (int kv = 0; kv < 2; kv++) {
+                    const int slot = issued % S::SLOTS;
+                    if (issued >= S::SLOTS && !mbar_wait(b_empty + 8 * slot, (issued / S::SLOTS - 1) & 1, plan.wait_polls))
+                        timeout = true;
+                    if (__any_sync(FULL, timeout)) {
+                        timeout = true;
+                        break;
+                    }
+                    if (lane == 0)
+                        mbar_expect_tx(b_full + 8 * slot, S::TILE);
+                    __syncwarp();
+                    if (lane < ng) {
+#pragma unroll
+                        for (int cb = 0; cb < CB; cb++)
+                            tma_load_2d(sm_ring + slot * S::TILE + cb * (KEYS * 128) + lane * g * 128, kv ? &vmap : &kmap,
+                                        cb * 64, y, b_full + 8 * slot);
+                    }
+                    issued++;
+                }
             }
         }
         // no copy is in flight when the CTA leaves, also where the work was given up
-        for (int it = issued > S::SLOTS ? issued - S::SLOTS : 0; it < issued; it++)
+        for (int it = max(issued - S::SLOTS, 0); it < issued; it++)
             mbar_wait(b_full + 8 * (it % S::SLOTS), (it / S::SLOTS) & 1);
-    } else if (lane == 0) {
-        // ------------------------------------------------------------ tensor-core issue
+    } else if (warp == 9) {
+        // ------------------------------------------------------------ tensor-core issue (the whole warp walks the items,
+        // lane 0 waits and issues)
         const uint32_t id_s = idesc_bf16(HALF, KEYS, false), id_o = idesc_bf16(HALF, DIM, true);
-        int n_p[2] = {0, 0};
+        uint32_t p_phase[2] = {0, 0}, q_phase[2] = {0, 0};
+        int ring = 0;
+        Tile w;
         auto wait = [&](uint32_t b, int parity) {
             if (!timeout && !mbar_wait(b, parity, plan.wait_polls))
                 timeout = true;
         };
-        // S of half h and tile t (relative to t0)
+        auto full = [&](int it) { wait(b_full + 8 * (it % S::SLOTS), (it / S::SLOTS) & 1); };
+        // S of half h and key tile t, whose K is there
         auto issue_s = [&](int h, int t) {
-            const int g = w.t0 + t;
-            if (timeout || g < w.lo[h] || g >= w.hi[h])
+            if (timeout || t < w.lo[h] || t >= w.hi[h])
                 return;
-            const int slot = (2 * t) % S::SLOTS;
+            if (t == w.lo[h]) {
+                wait(b_q + 8 * h, q_phase[h]);
+                q_phase[h] ^= 1;
+                if (timeout)
+                    return;
+            }
             tc_fence_after();
-            const uint32_t a = sm_q + h * S::TILE, b = sm_ring + slot * S::TILE;
+            const uint32_t a = sm_q + h * S::TILE, b = sm_ring + ((2 * (ring + t - w.t0)) % S::SLOTS) * S::TILE;
 #pragma unroll
             for (int k = 0; k < DIM / 16; k++) {
                 const uint32_t off = (k / 4) * (KEYS * 128) + (k % 4) * 32;
@@ -493,57 +543,62 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             }
             umma_commit(b_s + 8 * h);
         };
-        wait(b_q, 0);
-        for (int t = 0; t < tiles && !timeout; t++) {
-            if (t == 0) {
-                wait(b_full, 0);
-                issue_s(0, 0);
-                issue_s(1, 0);
+        for (int x = blockIdx.x; x < items && find_tile(p, plan, x, w, bad); x += gridDim.x) {
+            if (lane == 0 && !timeout && w.t1 > w.t0) {
+                full(2 * ring);
+                issue_s(0, w.t0);
+                issue_s(1, w.t0);
                 if (!timeout)
-                    umma_commit(b_empty + 8 * 0);
-            }
-            const int it = 2 * t + 1, slot = it % S::SLOTS;
-            wait(b_full + 8 * slot, (it / S::SLOTS) & 1);
-            for (int h = 0; h < 2 && !timeout; h++) {
-                const int g = w.t0 + t;
-                if (g >= w.lo[h] && g < w.hi[h]) {
-                    wait(b_p + 8 * h, n_p[h] & 1);
-                    if (timeout)
-                        break;
-                    tc_fence_after();
-                    const uint32_t b = sm_ring + slot * S::TILE;
+                    umma_commit(b_empty + 8 * ((2 * ring) % S::SLOTS));
+                for (int t = w.t0; t < w.t1 && !timeout; t++) {
+                    const int it = 2 * (ring + t - w.t0) + 1, slot = it % S::SLOTS;
+                    full(it);
+                    for (int h = 0; h < 2 && !timeout; h++) {
+                        if (t >= w.lo[h] && t < w.hi[h]) {
+                            wait(b_p + 8 * h, p_phase[h]);
+                            p_phase[h] ^= 1;
+                            if (timeout)
+                                break;
+                            tc_fence_after();
+                            const uint32_t b = sm_ring + slot * S::TILE;
 #pragma unroll
-                    for (int k = 0; k < KEYS / 16; k++)
-                        mma_f16_ts(tmem + TM_O + h * 128, tmem + TM_S + h * 128 + k * 8,
-                                   desc_sw128(b + k * 2048, KEYS * 128, 1024), id_o, n_p[h] > 0 || k > 0);
-                    n_p[h]++;
-                    if (g + 1 == w.hi[h])
-                        umma_commit(b_o + 8 * h);
-                }
-                if (t + 1 < tiles) {
-                    if (h == 0)
-                        wait(b_full + 8 * ((2 * t + 2) % S::SLOTS), ((2 * t + 2) / S::SLOTS) & 1);
-                    issue_s(h, t + 1);
+                            for (int k = 0; k < KEYS / 16; k++)
+                                mma_f16_ts(tmem + TM_O + h * 128, tmem + TM_S + h * 128 + k * 8,
+                                           desc_sw128(b + k * 2048, KEYS * 128, 1024), id_o, t > w.lo[h] || k > 0);
+                            if (t + 1 == w.hi[h])
+                                umma_commit(b_o + 8 * h);
+                        }
+                        if (t + 1 < w.t1) {
+                            if (h == 0)
+                                full(it + 1);
+                            issue_s(h, t + 1);
+                        }
+                    }
+                    if (!timeout) {
+                        umma_commit(b_empty + 8 * slot);
+                        if (t + 1 < w.t1)
+                            umma_commit(b_empty + 8 * ((it + 1) % S::SLOTS));
+                    }
                 }
             }
-            if (!timeout) {
-                umma_commit(b_empty + 8 * slot);
-                if (t + 1 < tiles)
-                    umma_commit(b_empty + 8 * ((2 * t + 2) % S::SLOTS));
-            }
+            __syncwarp();
+            if (__any_sync(FULL, timeout))
+                break;
+            ring += w.t1 - w.t0;
         }
-        // everything issued has to be through before tensor memory is freed
-        umma_commit(b_drain);
-        mbar_wait(b_drain, 0);
+        if (lane == 0) {
+            // everything issued has to be through before tensor memory is freed
+            umma_commit(b_drain);
+            mbar_wait(b_drain, 0);
+        }
+        __syncwarp();
     }
     report(p.err, bad, DEVERR_CU_SEQLENS);
     report(p.err, timeout, DEVERR_TIMEOUT);
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
-        __syncwarp();
+    if (warp == 9)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS));
-    }
 }
 
 // ---------------------------------------------------------------- host
@@ -602,7 +657,10 @@ template <int DIM> cudaError_t launch_tiles(const AttnArgs &p, const AttnPlan &p
         e = make_map(&vmap, p.cache.v, p.cache);
     if (e != cudaSuccess)
         return e;
-    const dim3 grid((unsigned)(plan.tiles * p.cache.hkv), (unsigned)plan.splits);
+    const int sms = device_sms();
+    const int grid = plan.items < sms ? plan.items : sms;
+    if (grid < 1)
+        return cudaErrorInvalidValue;
     kda_attn_tiles_kernel<DIM><<<grid, THREADS, Shape<DIM>::SMEM, st>>>(p, plan, kmap, vmap);
     return cudaGetLastError();
 }

@@ -69,7 +69,7 @@ kda_status_t check_cache_args(const void *k_cache, const void *v_cache, const in
     if (D != 64 && D != 128)
         return KDA_ERR_UNSUPPORTED;
     // cache rows and tokens are 32-bit coordinates of the bulk copies and of the launch grids
-    if (pages > INT32_MAX / page || pages * page > INT32_MAX / Hkv || (int64_t)max_pages * page > INT32_MAX)
+    if (pages > INT32_MAX / page || pages * page > INT32_MAX / Hkv || (int64_t)max_pages * page > INT32_MAX - 8192)
         return KDA_ERR_UNSUPPORTED;
     if (T > INT32_MAX || (cu_seqlens ? T : (int64_t)N * T) > INT32_MAX)
         return KDA_ERR_UNSUPPORTED;
