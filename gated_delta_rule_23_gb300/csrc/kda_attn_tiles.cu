@@ -10,7 +10,8 @@
 // shuffles;  O += P V with P (bf16) read from tensor memory where S was.  The halves take turns: while one half's
 // threads are at their exponentials, the tensor cores work for the other.  The running maximum m is moved (and O and l
 // rescaled) only when a row's maximum has grown by more than 2^8: any m gives the same quotient, and 2^8 is far from
-// overflow in the fp32 sums.
+// overflow in the fp32 sums.  So a tile's exponentials do not wait for its maximum: they are taken with the m at hand
+// while the maximum is formed, and taken again (S still stands; P is stored last) in the rare tile that moves m.
 //
 // Warps 0..3 and 4..7: the halves' softmax and epilogue; warp 8: bulk tensor copies (K and V tiles in a ring); warp 9:
 // tensor-core issue.  One CTA an SM walks the (row tile, key head, split) items: the copies run ahead into the next
@@ -148,42 +149,62 @@ __device__ __forceinline__ bool find_tile(const AttnArgs &p, const AttnPlan &pla
 }
 
 // ---------------------------------------------------------------- tensor cores and copies
-// 128-byte swizzled shared-memory matrix descriptor.  K-major: sbo between groups of 8 rows, lbo unused; MN-major: sbo
-// between groups of 8 along K, lbo between blocks of 64 along MN.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo)
-{
-    return umma_desc(saddr, lbo, sbo) | ((uint64_t)2 << 61);
-}
+// 128-byte swizzled shared-memory matrix descriptors, as their two words.  K-major: groups of 8 rows 1024 bytes apart;
+// MN-major: groups of 8 along K 1024 bytes apart, blocks of 64 along MN `lbo` apart.  The high word is the same for all;
+// in the low one a step along the operand is an addition, so that the issuing thread spends an instruction or two a
+// product (building whole descriptors there cost as much as the products themselves).
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
 // fp32 accumulator, bf16 A and B, A K-major, B K-major or (mn) MN-major
 __device__ __forceinline__ constexpr uint32_t idesc_bf16(int M, int N, bool mn)
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
            ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int acc)
+// D[tmem] (+)= A B^T, A in shared or tensor memory, B in shared memory; ACC: added to D, else as `acc` says
+template <bool ACC> __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, int acc)
 {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+    if (ACC)
+        asm volatile("{\n .reg .pred p;\n .reg .b64 x, y;\n setp.eq.u32 p, 0, 0;\n mov.b64 x, {%1, %4};\n mov.b64 y, {%2, %4};\n"
+                     " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}"
+                     ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(DESC_HI) : "memory");
+    else
+        asm volatile("{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n mov.b64 x, {%1, %4};\n mov.b64 y, {%2, %4};\n"
+                     " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}"
+                     ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(DESC_HI), "r"(acc) : "memory");
+}
+template <bool ACC> __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, int acc)
+{
+    if (ACC)
+        asm volatile("{\n .reg .pred p;\n .reg .b64 y;\n setp.eq.u32 p, 0, 0;\n mov.b64 y, {%2, %4};\n"
+                     " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}"
+                     ::"r"(d), "r"(a_tmem), "r"(b), "r"(idesc), "r"(DESC_HI) : "memory");
+    else
+        asm volatile("{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %4};\n"
+                     " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}"
+                     ::"r"(d), "r"(a_tmem), "r"(b), "r"(idesc), "r"(DESC_HI), "r"(acc) : "memory");
 }
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t mbar)
 {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
                  ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(mbar) : "memory");
 }
-#define R8(a, i) "=f"(a[i]), "=f"(a[i + 1]), "=f"(a[i + 2]), "=f"(a[i + 3]), "=f"(a[i + 4]), "=f"(a[i + 5]), "=f"(a[i + 6]), "=f"(a[i + 7])
-// 64 columns of the warp's 32 lanes, one row a thread
-__device__ __forceinline__ void tmem_ld64(uint32_t addr, float *s)
+// 32 columns of the warp's 32 lanes, one row a thread: the load, and the wait for it, which names the registers so that
+// nothing that uses them moves before it
+#define REGS8(k, a, i) k(a[i]), k(a[i + 1]), k(a[i + 2]), k(a[i + 3]), k(a[i + 4]), k(a[i + 5]), k(a[i + 6]), k(a[i + 7])
+__device__ __forceinline__ void tmem_get32(uint32_t addr, float (&s)[32])
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,"
-                 "%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
-                 "tcgen05.wait::ld.sync.aligned;"
-                 : R8(s, 0), R8(s, 8), R8(s, 16), R8(s, 24), R8(s, 32), R8(s, 40), R8(s, 48), R8(s, 56)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : REGS8("=f", s, 0), REGS8("=f", s, 8), REGS8("=f", s, 16), REGS8("=f", s, 24)
                  : "r"(addr) : "memory");
 }
-#undef R8
-
+__device__ __forceinline__ void tmem_wait32(float (&s)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : REGS8("+f", s, 0), REGS8("+f", s, 8), REGS8("+f", s, 16), REGS8("+f", s, 24)::"memory");
+}
+#undef REGS8
 // tcgen05.st of 32 columns without the wait for its completion
 __device__ __forceinline__ void tmem_put32(uint32_t addr, const uint32_t (&u)[32])
 {
@@ -320,71 +341,94 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                 }
                 s_phase ^= 1;
                 tc_fence_after();
-                float s[128];
-                tmem_ld64(tm_s, s);
-                tmem_ld64(tm_s + 64, s + 64);
                 // columns of the tile that the row sees: the window's, and the sinks'
                 const int wa = max(pos - p.window + 1, w.start) - w.start + w.sink_span - v0;
-                const int wb = pos - w.start + w.sink_span - v0;
-                if (!__all_sync(FULL, wa <= 0 && wb >= KEYS - 1)) {
-                    const int sb = min(p.sinks, pos + 1) - 1 - v0;
+                const int wb = pos - w.start + w.sink_span - v0, sb = min(p.sinks, pos + 1) - 1 - v0;
+                const bool whole = __all_sync(FULL, wa <= 0 && wb >= KEYS - 1);
+                auto hide = [&](float (&s)[32], int c) {         // 32 columns from 32 c on
+                    if (!whole) {
+                        const uint32_t mask = range_word(wa, wb, c) | range_word(-v0, sb, c);
 #pragma unroll
-                    for (int x4 = 0; x4 < 4; x4++) {
-                        const uint32_t mask = range_word(wa, wb, x4) | range_word(-v0, sb, x4);
-#pragma unroll
-                        for (int c = 0; c < 32; c++)
-                            s[32 * x4 + c] = (mask >> c) & 1 ? s[32 * x4 + c] : -INFINITY;
+                        for (int e = 0; e < 32; e++)
+                            s[e] = (mask >> e) & 1 ? s[e] : -INFINITY;
                     }
-                }
-                float mx[4] = {s[0], s[1], s[2], s[3]};
+                };
+                auto top_of = [&](const float (&s)[32], float x) {
+                    float y = s[0];
 #pragma unroll
-                for (int c = 4; c < 128; c += 8)
+                    for (int e = 1; e < 32; e += 2) {
+                        x = e + 1 < 32 ? fmaxf(x, fmaxf(s[e], s[e + 1])) : fmaxf(x, s[e]);
+                    }
+                    return fmaxf(x, y);
+                };
+                float s[2][32];
+                if (!any) {                                      // the first tile: m is its maximum
+                    float top = -INFINITY;
 #pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        mx[e] = fmaxf(mx[e], c + 4 + e < 128 ? fmaxf(s[c + e], s[c + 4 + e]) : s[c + e]);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-                // 0 x inf (scale 0) is NaN and leaves m alone
-                const bool move = top > m + RESCALE_AT;
-                if (!any) {
-                    if (top > m)
+                    for (int c = 0; c < 4; c++) {
+                        tmem_get32(tm_s + 32 * c, s[0]);
+                        tmem_wait32(s[0]);
+                        hide(s[0], c);
+                        top = top_of(s[0], top);
+                    }
+                    top *= p.scale_log2;
+                    if (top > m)                                 // not for NaN (0 x inf)
                         m = top;
-                } else if (__any_sync(FULL, move)) {
+                }
+                uint32_t pk[64];
+                f2 l0, l1;
+                for (;;) {
+                    const float mu = m == -INFINITY ? 0.0f : m;
+                    const f2 sc = f2_pack(p.scale_log2, p.scale_log2), mm = f2_pack(-mu, -mu);
+                    float top = -INFINITY;
+                    l0 = l1 = 0;
+                    tmem_get32(tm_s, s[0]);
+#pragma unroll
+                    for (int c = 0; c < 4; c++) {
+                        tmem_wait32(s[c & 1]);
+                        if (c < 3)
+                            tmem_get32(tm_s + 32 * (c + 1), s[(c + 1) & 1]);
+                        hide(s[c & 1], c);
+                        top = top_of(s[c & 1], top);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const f2 y = f2_fma(f2_pack(s[c & 1][e], s[c & 1][e + 1]), sc, mm);
+                            const float a = ex2_approx(f2_lo(y)), b = ex2_approx(f2_hi(y));
+                            if (e & 2)
+                                l1 = f2_add(l1, f2_pack(a, b));
+                            else
+                                l0 = f2_add(l0, f2_pack(a, b));
+                            const __nv_bfloat162 z = __floats2bfloat162_rn(a, b);
+                            pk[16 * c + e / 2] = *reinterpret_cast<const uint32_t *>(&z);
+                        }
+                    }
+                    top *= p.scale_log2;
+                    const bool move = top > m + RESCALE_AT;
+                    if (!__any_sync(FULL, move))
+                        break;
                     const float a = move ? ex2_approx(m - top) : 1.0f;
                     if (move)
                         m = top;
                     l *= a;
+                    if (any) {
 #pragma unroll
-                    for (int c = 0; c < DIM; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(tm_o + c, o);
+                        for (int c = 0; c < DIM; c += 32) {
+                            float o[32];
+                            tmem_get32(tm_o + c, o);
+                            tmem_wait32(o);
+                            uint32_t u[32];
 #pragma unroll
-                        for (int e = 0; e < 32; e++)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-                        tmem_put32(tm_o + c, o);
+                            for (int e = 0; e < 32; e++)
+                                u[e] = __float_as_uint(o[e] * a);
+                            tmem_put32(tm_o + c, u);
+                        }
                     }
                 }
                 any = true;
-                const float mu = m == -INFINITY ? 0.0f : m;
-                const f2 sc = f2_pack(p.scale_log2, p.scale_log2), mm = f2_pack(-mu, -mu);
-                f2 l0 = 0, l1 = 0;
-#pragma unroll
-                for (int c = 0; c < 128; c += 64) {
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int e = 0; e < 32; e++) {
-                        const f2 y = f2_fma(f2_pack(s[c + 2 * e], s[c + 2 * e + 1]), sc, mm);
-                        const float a = ex2_approx(f2_lo(y)), b = ex2_approx(f2_hi(y));
-                        if (e & 1)
-                            l1 = f2_add(l1, f2_pack(a, b));
-                        else
-                            l0 = f2_add(l0, f2_pack(a, b));
-                        const __nv_bfloat162 z = __floats2bfloat162_rn(a, b);
-                        pk[e] = *reinterpret_cast<const uint32_t *>(&z);
-                    }
-                    tmem_put32(tm_s + c / 2, pk);
-                }
                 l0 = f2_add(l0, l1);
                 l += f2_lo(l0) + f2_hi(l0);
+                tmem_put32(tm_s, *reinterpret_cast<const uint32_t (*)[32]>(pk));
+                tmem_put32(tm_s + 32, *reinterpret_cast<const uint32_t (*)[32]>(pk + 32));
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 mbar_arrive(b_p + 8 * h);
@@ -420,14 +464,16 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             const float inv = part ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
 #pragma unroll
             for (int c = 0; c < DIM; c += 32) {
-                uint32_t o[32];
-                if (stored)
-                    tmem_ld32(tm_o + c, o);
+                float o[32];
+                if (stored) {
+                    tmem_get32(tm_o + c, o);
+                    tmem_wait32(o);
+                }
 #pragma unroll
                 for (int e = 0; e < 32; e++) {
-                    const float y = stored ? __uint_as_float(o[e]) : 0.0f;
+                    const float y = stored ? o[e] : 0.0f;
                     finite &= fabsf(y) <= FLT_MAX;
-                    o[e] = __float_as_uint(part || l != 0.0f ? y * inv : 0.0f);
+                    o[e] = part || l != 0.0f ? y * inv : 0.0f;
                 }
                 if (!mine)
                     continue;
@@ -435,8 +481,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                     float4 *dst = reinterpret_cast<float4 *>(plan.part_o + (split * plan.rows + at) * DIM + c);
 #pragma unroll
                     for (int e = 0; e < 8; e++)
-                        dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                             __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+                        dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 } else {
                     uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * DIM + c);
 #pragma unroll
@@ -444,8 +489,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                         uint32_t y[4];
 #pragma unroll
                         for (int j = 0; j < 4; j++) {
-                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * j]),
-                                                                            __uint_as_float(o[8 * e + 2 * j + 1]));
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[8 * e + 2 * j], o[8 * e + 2 * j + 1]);
                             y[j] = *reinterpret_cast<const uint32_t *>(&b2);
                         }
                         dst[e] = make_uint4(y[0], y[1], y[2], y[3]);
@@ -518,7 +562,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
         const uint32_t id_s = idesc_bf16(HALF, KEYS, false), id_o = idesc_bf16(HALF, DIM, true);
         uint32_t p_phase[2] = {0, 0}, q_phase[2] = {0, 0};
         int ring = 0;
-        Tile w;
+        Tile w{};
         auto wait = [&](uint32_t b, int parity) {
             if (!timeout && !mbar_wait(b, parity, plan.wait_polls))
                 timeout = true;
@@ -535,11 +579,13 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                     return;
             }
             tc_fence_after();
-            const uint32_t a = sm_q + h * S::TILE, b = sm_ring + ((2 * (ring + t - w.t0)) % S::SLOTS) * S::TILE;
+            const uint32_t a = desc_lo(sm_q + h * S::TILE, 16), b = desc_lo(sm_ring + ((2 * (ring + t - w.t0)) % S::SLOTS) * S::TILE, 16);
+            const uint32_t d = tmem + TM_S + h * 128;
+            mma_ss<false>(d, a, b, id_s, 0);
 #pragma unroll
-            for (int k = 0; k < DIM / 16; k++) {
-                const uint32_t off = (k / 4) * (KEYS * 128) + (k % 4) * 32;
-                mma_f16_ss(tmem + TM_S + h * 128, desc_sw128(a + off, 16, 1024), desc_sw128(b + off, 16, 1024), id_s, k > 0);
+            for (int k = 1; k < DIM / 16; k++) {
+                const uint32_t off = ((k / 4) * (KEYS * 128) + (k % 4) * 32) >> 4;
+                mma_ss<true>(d, a + off, b + off, id_s, 1);
             }
             umma_commit(b_s + 8 * h);
         };
@@ -560,11 +606,12 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                             if (timeout)
                                 break;
                             tc_fence_after();
-                            const uint32_t b = sm_ring + slot * S::TILE;
+                            const uint32_t b = desc_lo(sm_ring + slot * S::TILE, KEYS * 128);
+                            const uint32_t d = tmem + TM_O + h * 128, a = tmem + TM_S + h * 128;
+                            mma_ts<false>(d, a, b, id_o, t > w.lo[h]);
 #pragma unroll
-                            for (int k = 0; k < KEYS / 16; k++)
-                                mma_f16_ts(tmem + TM_O + h * 128, tmem + TM_S + h * 128 + k * 8,
-                                           desc_sw128(b + k * 2048, KEYS * 128, 1024), id_o, t > w.lo[h] || k > 0);
+                            for (int k = 1; k < KEYS / 16; k++)
+                                mma_ts<true>(d, a + k * 8, b + k * (2048 >> 4), id_o, 1);
                             if (t + 1 == w.hi[h])
                                 umma_commit(b_o + 8 * h);
                         }
