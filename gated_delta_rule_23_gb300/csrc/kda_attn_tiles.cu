@@ -1,17 +1,20 @@
-// Windowed attention over the paged cache on the tensor cores: 256 query rows a CTA, keys in tiles of 128.
+// Windowed attention over the paged cache on the tensor cores: 256 query rows a CTA, keys in tiles of 64.
 //
 // Rows.  A CTA owns rows [256 x, 256 x + 256) of one (sequence, key head), in two halves of 128 (row = token * group
 // + head of the group, so heads that share keys share the tile).  Keys.  The tile's rows need the sinks and the
 // positions from the first row's window on: two ranges of positions, cut into granules of at most 32 positions that
-// lie in one page each, and strung together to a list of "virtual" keys; 4 to 8 granules make a key tile, so a few
+// lie in one page each, and strung together to a list of "virtual" keys; 2 to 4 granules make a key tile, so a few
 // sinks cost a granule and not a tile.  Granules past the end are loaded from outside the cache (zeros).
 //
 // Per key tile and half:  S = Q K^T (tcgen05, fp32 in tensor memory);  P = 2^(scale S - m) with one thread a row, no
-// shuffles;  O += P V with P (bf16) read from tensor memory where S was.  The halves take turns: while one half's
-// threads are at their exponentials, the tensor cores work for the other.  The running maximum m is moved (and O and l
-// rescaled) only when a row's maximum has grown by more than 2^8: any m gives the same quotient, and 2^8 is far from
-// overflow in the fp32 sums.  So a tile's exponentials do not wait for its maximum: they are taken with the m at hand
-// while the maximum is formed, and taken again (S still stands; P is stored last) in the rare tile that moves m.
+// shuffles;  O += P V with P (bf16) read from tensor memory where S was.  From the commit of S to the P that the issuing
+// thread waits for lie some 2000 cycles of latency even without any arithmetic, against 500 of tensor time in a half's S
+// and P V for 64 keys: so a half has two S in tensor memory (2 x 64 columns; O takes 128), and the S after next is formed
+// while the softmax works on this one.  (128-key tiles with one S a half: 1586 us where this takes the time in DESIGN.)
+// The running maximum m is moved (and O and l rescaled) only when a row's maximum has grown by more than 2^8: any m
+// gives the same quotient, and 2^8 is far from overflow in the fp32 sums.  So a tile's exponentials do not wait for its
+// maximum: they are taken with the m at hand while the maximum is formed, and taken again (S still stands; P is stored
+// last) in the rare tile that moves m.
 //
 // Warps 0..3 and 4..7: the halves' softmax and epilogue; warp 8: bulk tensor copies (K and V tiles in a ring); warp 9:
 // tensor-core issue.  One CTA an SM walks the (row tile, key head, split) items: the copies run ahead into the next
@@ -30,7 +33,7 @@
 namespace kda {
 namespace {
 
-constexpr int KEYS = 128;                    // keys of a tile
+constexpr int KEYS = 64;                     // keys of a tile
 constexpr int THREADS = 384;                 // three warpgroups (two warps of the last have no role)
 // Registers a thread: 168 at launch (65,536 / 384); the softmax warpgroups, which hold a row of S, take what the third gives
 // back: 2 x 128 x 208 + 128 x 88 = 384 x 168.
@@ -38,15 +41,16 @@ constexpr int REGS_SOFTMAX = 208, REGS_REST = 88;
 static_assert(2 * 128 * REGS_SOFTMAX + 128 * REGS_REST <= THREADS * 168, "register split");
 constexpr int HALF = 128;                    // rows of a half
 constexpr int TMEM_COLS = 512;
-constexpr int TM_S = 0, TM_O = 256;          // columns: S of both halves (128 each), O of both halves
+constexpr int TM_S = 0, TM_O = 256;          // columns: two S a half (64 each), O of both halves
 constexpr float RESCALE_AT = 8.0f;           // base-2 growth of the maximum that moves it
 constexpr unsigned FULL = 0xffffffffu;
 
 template <int DIM> struct Shape {
-    static constexpr int TILE = KEYS * DIM * 2;              // bytes of a K or V tile, and of a half's Q
-    static constexpr int SLOTS = DIM == 128 ? 5 : 10;        // ring: K0 V0 K1 V1 ...
-    static constexpr int BAR = 2 * TILE + SLOTS * TILE;      // mbarriers behind Q and the ring
-    static constexpr int SMEM = 1024 + BAR + 256;            // 1024: alignment of the swizzle atoms
+    static constexpr int TILE = KEYS * DIM * 2;              // bytes of a K or V tile
+    static constexpr int Q = HALF * DIM * 2;                 // of a half's Q
+    static constexpr int SLOTS = 10;                         // ring: K0 V0 K1 V1 ... (K in the even slots)
+    static constexpr int BAR = 2 * Q + SLOTS * TILE;         // mbarriers behind Q and the ring
+    static constexpr int SMEM = 1024 + BAR + 512;            // 1024: alignment of the swizzle atoms
 };
 
 struct Tile {             // one item; positions, rows and tokens fit 32 bits (checked on the host)
@@ -223,7 +227,14 @@ __device__ __forceinline__ f2 f2_add(f2 a, f2 b)
     return d;
 }
 
-// bits a..b (inclusive, any integers) of a 128-bit mask, word w; PTX shifts of 32 and more give 0
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t x;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(x));
+    return x;
+}
+
+// bits a..b (inclusive, any integers) of a mask of several words, word w; PTX shifts of 32 and more give 0
 __device__ __forceinline__ uint32_t range_word(int a, int b, int w)
 {
     uint32_t x, y;
@@ -243,7 +254,7 @@ template <int DIM> __device__ __forceinline__ void load_q(const AttnArgs &p, con
         const bool in = row < w.rows;
         const int R = w.row0 + (in ? row : 0);
         const __nv_bfloat16 *src = p.q + (int64_t)(w.bos + R / p.group) * p.q_stride + (w.kvh * p.group + R % p.group) * DIM + c * 8;
-        cp_async16(sm_q + (warp / 4) * Shape<DIM>::TILE + (c / 8) * (HALF * 128) + rh * 128 + (((c & 7) ^ (rh & 7)) << 4), src, in);
+        cp_async16(sm_q + (warp / 4) * Shape<DIM>::Q + (c / 8) * (HALF * 128) + rh * 128 + (((c & 7) ^ (rh & 7)) << 4), src, in);
     }
     cp_async_commit();
 }
@@ -258,9 +269,9 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char *const smem = smem_raw + (base - smem_u32(smem_raw));
-    const uint32_t sm_q = base, sm_ring = base + 2 * S::TILE, bar = base + S::BAR;
-    const uint32_t b_full = bar, b_empty = bar + 8 * S::SLOTS, b_q = bar + 16 * S::SLOTS, b_s = b_q + 16, b_p = b_s + 16,
-                   b_o = b_p + 16, b_drain = b_o + 16;
+    const uint32_t sm_q = base, sm_ring = base + 2 * S::Q, bar = base + S::BAR;
+    const uint32_t b_full = bar, b_empty = bar + 8 * S::SLOTS, b_q = bar + 16 * S::SLOTS, b_s = b_q + 16, b_p = b_s + 32,
+                   b_o = b_p + 32, b_drain = b_o + 32;     // S, P and P V: [half][buffer]
     __shared__ uint32_t tmem_slot;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
     const int items = plan.items, g = plan.granule;
@@ -271,9 +282,11 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
         }
         for (int h = 0; h < 2; h++) {
             mbar_init(b_q + 8 * h, 4);
-            mbar_init(b_s + 8 * h, 1);
-            mbar_init(b_p + 8 * h, HALF);
-            mbar_init(b_o + 8 * h, 1);
+            for (int i = 0; i < 2; i++) {
+                mbar_init(b_s + 16 * h + 8 * i, 1);
+                mbar_init(b_p + 16 * h + 8 * i, 4);
+                mbar_init(b_o + 16 * h + 8 * i, 1);
+            }
         }
         mbar_init(b_drain, 1);
         mbar_fence_init();
@@ -294,9 +307,11 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
         const int h = warp / 4;
         const uint32_t tm_lane = (uint32_t)(warp & 3) << 21;     // the warp's 32 lanes
-        const uint32_t tm_s = tmem + TM_S + h * 128 + tm_lane, tm_o = tmem + TM_O + h * 128 + tm_lane;
+        const uint32_t tm_s0 = tmem + TM_S + h * 128 + tm_lane, tm_o = tmem + TM_O + h * 128 + tm_lane;
         int ring = 0;                                            // key tiles of the items before
-        uint32_t s_phase = 0, o_phase = 0;
+        // Phases of the two S, and of the P V of the last P given in each.  A buffer's P V before that is through when the
+        // buffer's next S is, so at most one phase of its barrier is open when it is waited for.
+        uint32_t s_phase = 0, o_phase = 3;
         Tile w{};
         int x = blockIdx.x;
         bool have = x < items && find_tile(p, plan, x, w, bad);
@@ -330,16 +345,18 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                         break;
                     }
                     const int count = (g - (end_v & (g - 1))) * 8;       // 16-byte vectors of a column block
-                    uint4 *v = reinterpret_cast<uint4 *>(smem + 2 * S::TILE + slot * S::TILE) + end_v * 8;
+                    uint4 *v = reinterpret_cast<uint4 *>(smem + 2 * S::Q + slot * S::TILE) + end_v * 8;
                     for (int i = tid & (HALF - 1); i < count * CB; i += HALF)
                         v[(i / count) * (KEYS * 8) + i % count] = make_uint4(0, 0, 0, 0);
                     fence_async_smem();
                 }
-                if (!mbar_wait(b_s + 8 * h, s_phase, plan.wait_polls)) {
+                const int buf = (t - w.lo[h]) & 1;
+                const uint32_t tm_s = tm_s0 + 64 * buf;
+                if (!mbar_wait(b_s + 16 * h + 8 * buf, s_phase >> buf & 1, plan.wait_polls)) {
                     timeout = true;
                     break;
                 }
-                s_phase ^= 1;
+                s_phase ^= 1u << buf;
                 tc_fence_after();
                 // columns of the tile that the row sees: the window's, and the sinks'
                 const int wa = max(pos - p.window + 1, w.start) - w.start + w.sink_span - v0;
@@ -365,7 +382,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                 if (!any) {                                      // the first tile: m is its maximum
                     float top = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < 4; c++) {
+                    for (int c = 0; c < KEYS / 32; c++) {
                         tmem_get32(tm_s + 32 * c, s[0]);
                         tmem_wait32(s[0]);
                         hide(s[0], c);
@@ -375,7 +392,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                     if (top > m)                                 // not for NaN (0 x inf)
                         m = top;
                 }
-                uint32_t pk[64];
+                uint32_t pk[KEYS / 2];
                 f2 l0, l1;
                 for (;;) {
                     const float mu = m == -INFINITY ? 0.0f : m;
@@ -384,9 +401,9 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                     l0 = l1 = 0;
                     tmem_get32(tm_s, s[0]);
 #pragma unroll
-                    for (int c = 0; c < 4; c++) {
+                    for (int c = 0; c < KEYS / 32; c++) {
                         tmem_wait32(s[c & 1]);
-                        if (c < 3)
+                        if (c + 1 < KEYS / 32)
                             tmem_get32(tm_s + 32 * (c + 1), s[(c + 1) & 1]);
                         hide(s[c & 1], c);
                         top = top_of(s[c & 1], top);
@@ -411,6 +428,10 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                         m = top;
                     l *= a;
                     if (any) {
+                        // the P V before this one has to be through (the ones before it are: this S came after them)
+                        if (!mbar_wait(b_o + 16 * h + 8 * (buf ^ 1), o_phase >> (buf ^ 1) & 1, plan.wait_polls))
+                            timeout = true;
+                        tc_fence_after();
 #pragma unroll
                         for (int c = 0; c < DIM; c += 32) {
                             float o[32];
@@ -427,11 +448,13 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                 any = true;
                 l0 = f2_add(l0, l1);
                 l += f2_lo(l0) + f2_hi(l0);
-                tmem_put32(tm_s, *reinterpret_cast<const uint32_t (*)[32]>(pk));
-                tmem_put32(tm_s + 32, *reinterpret_cast<const uint32_t (*)[32]>(pk + 32));
+                tmem_put32(tm_s, pk);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
-                mbar_arrive(b_p + 8 * h);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(b_p + 16 * h + 8 * buf);
+                o_phase ^= 1u << buf;
             }
             if (__any_sync(FULL, timeout)) {
                 timeout = true;
@@ -439,6 +462,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             }
             // The next item's Q: the half's last S is formed, so its Q rows are free.
             const bool stored = any;
+            const int w_last = w.hi[h] - w.lo[h];
             ring += w.t1 - w.t0;
             x += gridDim.x;
             have = x < items && find_tile(p, plan, x, w, bad);
@@ -446,9 +470,9 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             if (more)
                 load_q<DIM>(p, w, sm_q, warp, lane);
             if (stored) {
-                if (!mbar_wait(b_o + 8 * h, o_phase, plan.wait_polls))
+                const int buf = (w_last - 1) & 1;                // the last P V: those before it are through with it
+                if (!mbar_wait(b_o + 16 * h + 8 * buf, o_phase >> buf & 1, plan.wait_polls))
                     timeout = true;
-                o_phase ^= 1;
                 tc_fence_after();
             }
             if (more)
@@ -557,83 +581,91 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
         for (int it = max(issued - S::SLOTS, 0); it < issued; it++)
             mbar_wait(b_full + 8 * (it % S::SLOTS), (it / S::SLOTS) & 1);
     } else if (warp == 9) {
-        // ------------------------------------------------------------ tensor-core issue (the whole warp walks the items,
-        // lane 0 waits and issues)
+        // ------------------------------------------------------------ tensor-core issue
+        // The whole warp walks the items and waits; one elected lane issues.  What an instruction needs (descriptors,
+        // addresses) is the same in all lanes and known to be, so that it is formed in uniform registers: issuing from
+        // one thread's own registers took longer than the products (some 80 cycles each).
         const uint32_t id_s = idesc_bf16(HALF, KEYS, false), id_o = idesc_bf16(HALF, DIM, true);
-        uint32_t p_phase[2] = {0, 0}, q_phase[2] = {0, 0};
-        int ring = 0;
+        const uint32_t tm = __shfl_sync(FULL, tmem, 0), lead = elect_one();
+        const uint32_t q_lo = desc_lo(sm_q, 16), k_lo = desc_lo(sm_ring, 16), v_lo = desc_lo(sm_ring + S::TILE, KEYS * 128);
+        uint32_t p_phase = 0, q_phase = 0;                       // bits [half][buffer], [half]
+        uint32_t ks = 0, kp = 0, vs = 0, vp = 0;                 // next K's and next V's stage, and its phase
         Tile w{};
-        auto wait = [&](uint32_t b, int parity) {
+        auto wait = [&](uint32_t b, uint32_t parity) {
             if (!timeout && !mbar_wait(b, parity, plan.wait_polls))
                 timeout = true;
+            timeout = __any_sync(FULL, timeout);
         };
-        auto full = [&](int it) { wait(b_full + 8 * (it % S::SLOTS), (it / S::SLOTS) & 1); };
-        // S of half h and key tile t, whose K is there
-        auto issue_s = [&](int h, int t) {
-            if (timeout || t < w.lo[h] || t >= w.hi[h])
-                return;
-            if (t == w.lo[h]) {
-                wait(b_q + 8 * h, q_phase[h]);
-                q_phase[h] ^= 1;
-                if (timeout)
-                    return;
-            }
-            tc_fence_after();
-            const uint32_t a = desc_lo(sm_q + h * S::TILE, 16), b = desc_lo(sm_ring + ((2 * (ring + t - w.t0)) % S::SLOTS) * S::TILE, 16);
-            const uint32_t d = tmem + TM_S + h * 128;
-            mma_ss<false>(d, a, b, id_s, 0);
+        for (int x = blockIdx.x; x < items && find_tile(p, plan, x, w, bad) && !timeout; x += gridDim.x) {
+            // uniform copies
+            const int t0 = __shfl_sync(FULL, w.t0, 0), t1 = __shfl_sync(FULL, w.t1, 0);
+            const int lo[2] = {__shfl_sync(FULL, w.lo[0], 0), __shfl_sync(FULL, w.lo[1], 0)};
+            const int hi[2] = {__shfl_sync(FULL, w.hi[0], 0), __shfl_sync(FULL, w.hi[1], 0)};
+            // S of key tile t (both halves) and the P V of tile t - 2 before it, half by half
+            for (int t = t0; t < t1 + 2 && !timeout; t++) {
+                const bool s_now = t < t1, pv_now = t >= t0 + 2;
+                if (pv_now)
+                    wait(b_full + 16 * vs + 8, vp);
+                if (s_now)
+                    wait(b_full + 16 * ks, kp);
 #pragma unroll
-            for (int k = 1; k < DIM / 16; k++) {
-                const uint32_t off = ((k / 4) * (KEYS * 128) + (k % 4) * 32) >> 4;
-                mma_ss<true>(d, a + off, b + off, id_s, 1);
-            }
-            umma_commit(b_s + 8 * h);
-        };
-        for (int x = blockIdx.x; x < items && find_tile(p, plan, x, w, bad); x += gridDim.x) {
-            if (lane == 0 && !timeout && w.t1 > w.t0) {
-                full(2 * ring);
-                issue_s(0, w.t0);
-                issue_s(1, w.t0);
-                if (!timeout)
-                    umma_commit(b_empty + 8 * ((2 * ring) % S::SLOTS));
-                for (int t = w.t0; t < w.t1 && !timeout; t++) {
-                    const int it = 2 * (ring + t - w.t0) + 1, slot = it % S::SLOTS;
-                    full(it);
-                    for (int h = 0; h < 2 && !timeout; h++) {
-                        if (t >= w.lo[h] && t < w.hi[h]) {
-                            wait(b_p + 8 * h, p_phase[h]);
-                            p_phase[h] ^= 1;
-                            if (timeout)
-                                break;
-                            tc_fence_after();
-                            const uint32_t b = desc_lo(sm_ring + slot * S::TILE, KEYS * 128);
-                            const uint32_t d = tmem + TM_O + h * 128, a = tmem + TM_S + h * 128;
-                            mma_ts<false>(d, a, b, id_o, t > w.lo[h]);
+                for (int h = 0; h < 2; h++) {
+                    const int u = t - 2;
+                    if (pv_now && u >= lo[h] && u < hi[h]) {
+                        const uint32_t buf = (u - lo[h]) & 1;
+                        wait(b_p + 16 * h + 8 * buf, p_phase >> (2 * h + buf) & 1);
+                        p_phase ^= 1u << (2 * h + buf);
+                        if (timeout)
+                            break;
+                        tc_fence_after();
+                        const uint32_t b = v_lo + vs * (2 * S::TILE >> 4), d = tm + TM_O + h * 128;
+                        const uint32_t a = tm + TM_S + h * 128 + 64 * buf;
+                        if (lead) {
+                            mma_ts<false>(d, a, b, id_o, u > lo[h]);
 #pragma unroll
                             for (int k = 1; k < KEYS / 16; k++)
                                 mma_ts<true>(d, a + k * 8, b + k * (2048 >> 4), id_o, 1);
-                            if (t + 1 == w.hi[h])
-                                umma_commit(b_o + 8 * h);
-                        }
-                        if (t + 1 < w.t1) {
-                            if (h == 0)
-                                full(it + 1);
-                            issue_s(h, t + 1);
+                            umma_commit(b_o + 16 * h + 8 * buf);
                         }
                     }
-                    if (!timeout) {
-                        umma_commit(b_empty + 8 * slot);
-                        if (t + 1 < w.t1)
-                            umma_commit(b_empty + 8 * ((it + 1) % S::SLOTS));
+                    if (s_now && t >= lo[h] && t < hi[h]) {
+                        if (t == lo[h]) {
+                            wait(b_q + 8 * h, q_phase >> h & 1);
+                            q_phase ^= 1u << h;
+                            if (timeout)
+                                break;
+                        }
+                        const uint32_t buf = (t - lo[h]) & 1;
+                        tc_fence_after();
+                        const uint32_t a = q_lo + h * (S::Q >> 4), b = k_lo + ks * (2 * S::TILE >> 4);
+                        const uint32_t d = tm + TM_S + h * 128 + 64 * buf;
+                        if (lead) {
+                            mma_ss<false>(d, a, b, id_s, 0);
+#pragma unroll
+                            for (int k = 1; k < DIM / 16; k++)
+                                mma_ss<true>(d, a + (((k / 4) * (HALF * 128) + (k % 4) * 32) >> 4),
+                                             b + (((k / 4) * (KEYS * 128) + (k % 4) * 32) >> 4), id_s, 1);
+                            umma_commit(b_s + 16 * h + 8 * buf);
+                        }
                     }
                 }
+                if (timeout)
+                    break;
+                if (pv_now) {
+                    if (lead)
+                        umma_commit(b_empty + 16 * vs + 8);
+                    if (++vs == S::SLOTS / 2)
+                        vs = 0, vp ^= 1;
+                }
+                if (s_now) {
+                    if (lead)
+                        umma_commit(b_empty + 16 * ks);
+                    if (++ks == S::SLOTS / 2)
+                        ks = 0, kp ^= 1;
+                }
             }
-            __syncwarp();
-            if (__any_sync(FULL, timeout))
-                break;
-            ring += w.t1 - w.t0;
         }
-        if (lane == 0) {
+        if (lead) {
             // everything issued has to be through before tensor memory is freed
             umma_commit(b_drain);
             mbar_wait(b_drain, 0);
