@@ -16,8 +16,9 @@
 // maximum: they are taken with the m at hand while the maximum is formed, and taken again (S still stands; P is stored
 // last) in the rare tile that moves m.
 //
-// Warps 0..3 and 4..7: the halves' softmax and epilogue; warp 8: bulk tensor copies (K and V tiles in a ring); warp 9:
-// tensor-core issue.  One CTA an SM walks the (row tile, key head, split) items: the copies run ahead into the next
+// Warps 0..3 and 4..7: the halves' softmax and epilogue; warp 8: bulk tensor copies (K and V tiles in a ring); warps 9
+// and 10: tensor-core issue for a half each (one thread for both halves spent longer issuing than the tensor cores took:
+// 1918 us at 8192 tokens, 96 heads).  One CTA an SM walks the (row tile, key head, split) items: the copies run ahead into the next
 // item, its Q is loaded and its first S formed while the last item's rows are scaled and stored.
 //
 // A key that a row does not see gets P = 0.  0 x v is NaN for an infinite or NaN v, and the matrix product has no way
@@ -34,7 +35,7 @@ namespace kda {
 namespace {
 
 constexpr int KEYS = 64;                     // keys of a tile
-constexpr int THREADS = 384;                 // three warpgroups (two warps of the last have no role)
+constexpr int THREADS = 384;                 // three warpgroups (the last warp has no role)
 // Registers a thread: 168 at launch (65,536 / 384); the softmax warpgroups, which hold a row of S, take what the third gives
 // back: 2 x 128 x 208 + 128 x 88 = 384 x 168.
 constexpr int REGS_SOFTMAX = 208, REGS_REST = 88;
@@ -48,8 +49,8 @@ constexpr unsigned FULL = 0xffffffffu;
 template <int DIM> struct Shape {
     static constexpr int TILE = KEYS * DIM * 2;              // bytes of a K or V tile
     static constexpr int Q = HALF * DIM * 2;                 // of a half's Q
-    static constexpr int SLOTS = 10;                         // ring: K0 V0 K1 V1 ... (K in the even slots)
-    static constexpr int BAR = 2 * Q + SLOTS * TILE;         // mbarriers behind Q and the ring
+    static constexpr int STAGES = 5;                         // ring of key tiles, K and V of each
+    static constexpr int BAR = 2 * Q + STAGES * 2 * TILE;         // mbarriers behind Q and the ring
     static constexpr int SMEM = 1024 + BAR + 512;            // 1024: alignment of the swizzle atoms
 };
 
@@ -270,15 +271,16 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char *const smem = smem_raw + (base - smem_u32(smem_raw));
     const uint32_t sm_q = base, sm_ring = base + 2 * S::Q, bar = base + S::BAR;
-    const uint32_t b_full = bar, b_empty = bar + 8 * S::SLOTS, b_q = bar + 16 * S::SLOTS, b_s = b_q + 16, b_p = b_s + 32,
-                   b_o = b_p + 32, b_drain = b_o + 32;     // S, P and P V: [half][buffer]
+    const uint32_t b_full = bar, b_empty = bar + 16 * S::STAGES, b_q = b_empty + 8 * S::STAGES, b_s = b_q + 16, b_p = b_s + 32,
+                   b_o = b_p + 32, b_drain = b_o + 32;     // full: [stage][K, V]; S, P, P V: [half][buffer]; drain: [half]
     __shared__ uint32_t tmem_slot;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
     const int items = plan.items, g = plan.granule;
     if (tid == 0) {
-        for (int i = 0; i < S::SLOTS; i++) {
-            mbar_init(b_full + 8 * i, 1);
-            mbar_init(b_empty + 8 * i, 1);
+        for (int i = 0; i < S::STAGES; i++) {
+            mbar_init(b_full + 16 * i, 1);
+            mbar_init(b_full + 16 * i + 8, 1);
+            mbar_init(b_empty + 8 * i, 2);
         }
         for (int h = 0; h < 2; h++) {
             mbar_init(b_q + 8 * h, 4);
@@ -287,8 +289,8 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                 mbar_init(b_p + 16 * h + 8 * i, 4);
                 mbar_init(b_o + 16 * h + 8 * i, 1);
             }
+            mbar_init(b_drain + 8 * h, 1);
         }
-        mbar_init(b_drain, 1);
         mbar_fence_init();
     }
     if (warp == 9) {
@@ -309,9 +311,9 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
         const uint32_t tm_lane = (uint32_t)(warp & 3) << 21;     // the warp's 32 lanes
         const uint32_t tm_s0 = tmem + TM_S + h * 128 + tm_lane, tm_o = tmem + TM_O + h * 128 + tm_lane;
         int ring = 0;                                            // key tiles of the items before
-        // Phases of the two S, and of the P V of the last P given in each.  A buffer's P V before that is through when the
-        // buffer's next S is, so at most one phase of its barrier is open when it is waited for.
-        uint32_t s_phase = 0, o_phase = 3;
+        // Phases of the two S, and of the P V of an item's last two key tiles, the only ones that are waited for as such: a
+        // half's S of tile t + 1 is issued right after its P V of tile t - 1.
+        uint32_t s_phase = 0, o_phase = 0;
         Tile w{};
         int x = blockIdx.x;
         bool have = x < items && find_tile(p, plan, x, w, bad);
@@ -339,13 +341,13 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                 // masked)
                 const int end_v = w.len - w.start + w.sink_span - v0;
                 if (end_v > 0 && end_v < KEYS && (end_v & (g - 1))) {
-                    const int it = 2 * (ring + t - w.t0) + 1, slot = it % S::SLOTS;
-                    if (!mbar_wait(b_full + 8 * slot, (it / S::SLOTS) & 1, plan.wait_polls)) {
+                    const int it = ring + t - w.t0, stage = it % S::STAGES;
+                    if (!mbar_wait(b_full + 16 * stage + 8, (it / S::STAGES) & 1, plan.wait_polls)) {
                         timeout = true;
                         break;
                     }
                     const int count = (g - (end_v & (g - 1))) * 8;       // 16-byte vectors of a column block
-                    uint4 *v = reinterpret_cast<uint4 *>(smem + 2 * S::Q + slot * S::TILE) + end_v * 8;
+                    uint4 *v = reinterpret_cast<uint4 *>(smem + 2 * S::Q + (2 * stage + 1) * S::TILE) + end_v * 8;
                     for (int i = tid & (HALF - 1); i < count * CB; i += HALF)
                         v[(i / count) * (KEYS * 8) + i % count] = make_uint4(0, 0, 0, 0);
                     fence_async_smem();
@@ -429,7 +431,9 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                     l *= a;
                     if (any) {
                         // the P V before this one has to be through (the ones before it are: this S came after them)
-                        if (!mbar_wait(b_o + 16 * h + 8 * (buf ^ 1), o_phase >> (buf ^ 1) & 1, plan.wait_polls))
+                        const uint32_t other = buf ^ 1;
+                        if (!mbar_wait(t + 1 < w.hi[h] ? b_s + 16 * h + 8 * other : b_o + 16 * h + 8 * other,
+                                       (t + 1 < w.hi[h] ? s_phase : o_phase) >> other & 1, plan.wait_polls))
                             timeout = true;
                         tc_fence_after();
 #pragma unroll
@@ -454,7 +458,6 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(b_p + 16 * h + 8 * buf);
-                o_phase ^= 1u << buf;
             }
             if (__any_sync(FULL, timeout)) {
                 timeout = true;
@@ -462,7 +465,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             }
             // The next item's Q: the half's last S is formed, so its Q rows are free.
             const bool stored = any;
-            const int w_last = w.hi[h] - w.lo[h];
+            const int tiles = w.hi[h] - w.lo[h];
             ring += w.t1 - w.t0;
             x += gridDim.x;
             have = x < items && find_tile(p, plan, x, w, bad);
@@ -470,9 +473,10 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             if (more)
                 load_q<DIM>(p, w, sm_q, warp, lane);
             if (stored) {
-                const int buf = (w_last - 1) & 1;                // the last P V: those before it are through with it
+                const int buf = (tiles - 1) & 1;                 // the last P V: those before it are through with it
                 if (!mbar_wait(b_o + 16 * h + 8 * buf, o_phase >> buf & 1, plan.wait_polls))
                     timeout = true;
+                o_phase ^= tiles > 1 ? 3 : 1u << buf;
                 tc_fence_after();
             }
             if (more)
@@ -555,120 +559,110 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                             bad = true;
                     }
                 }
+                const int stage = issued % S::STAGES;
+                if (issued >= S::STAGES && !mbar_wait(b_empty + 8 * stage, (issued / S::STAGES - 1) & 1, plan.wait_polls))
+                    timeout = true;
+                if (__any_sync(FULL, timeout)) {
+                    timeout = true;
+                    break;
+                }
+                if (lane == 0) {
+                    mbar_expect_tx(b_full + 16 * stage, S::TILE);
+                    mbar_expect_tx(b_full + 16 * stage + 8, S::TILE);
+                }
+                __syncwarp();
+                if (lane < ng) {
 #pragma unroll
-                for (int kv = 0; kv < 2; kv++) {
-                    const int slot = issued % S::SLOTS;
-                    if (issued >= S::SLOTS && !mbar_wait(b_empty + 8 * slot, (issued / S::SLOTS - 1) & 1, plan.wait_polls))
-                        timeout = true;
-                    if (__any_sync(FULL, timeout)) {
-                        timeout = true;
-                        break;
-                    }
-                    if (lane == 0)
-                        mbar_expect_tx(b_full + 8 * slot, S::TILE);
-                    __syncwarp();
-                    if (lane < ng) {
+                    for (int kv = 0; kv < 2; kv++)
 #pragma unroll
                         for (int cb = 0; cb < CB; cb++)
-                            tma_load_2d(sm_ring + slot * S::TILE + cb * (KEYS * 128) + lane * g * 128, kv ? &vmap : &kmap,
-                                        cb * 64, y, b_full + 8 * slot);
-                    }
-                    issued++;
+                            tma_load_2d(sm_ring + (2 * stage + kv) * S::TILE + cb * (KEYS * 128) + lane * g * 128,
+                                        kv ? &vmap : &kmap, cb * 64, y, b_full + 16 * stage + 8 * kv);
                 }
+                issued++;
             }
         }
         // no copy is in flight when the CTA leaves, also where the work was given up
-        for (int it = max(issued - S::SLOTS, 0); it < issued; it++)
-            mbar_wait(b_full + 8 * (it % S::SLOTS), (it / S::SLOTS) & 1);
-    } else if (warp == 9) {
-        // ------------------------------------------------------------ tensor-core issue
-        // The whole warp walks the items and waits; one elected lane issues.  What an instruction needs (descriptors,
-        // addresses) is the same in all lanes and known to be, so that it is formed in uniform registers: issuing from
-        // one thread's own registers took longer than the products (some 80 cycles each).
+        for (int it = max(issued - S::STAGES, 0); it < issued; it++)
+            for (int kv = 0; kv < 2; kv++)
+                mbar_wait(b_full + 16 * (it % S::STAGES) + 8 * kv, (it / S::STAGES) & 1);
+    } else if (warp == 9 || warp == 10) {
+        // ------------------------------------------------------------ tensor-core issue, warp 9 for half 0, 10 for half 1
+        // The warp walks the items; one elected lane waits and issues.  What an instruction needs (descriptors, addresses)
+        // is the same in all lanes and known to be, so that it is formed in uniform registers: issuing from one thread's
+        // own registers took some 80 cycles a product.  Once a wait has given up, nothing more is issued.
+        const int h = __shfl_sync(FULL, warp, 0) - 9;
         const uint32_t id_s = idesc_bf16(HALF, KEYS, false), id_o = idesc_bf16(HALF, DIM, true);
         const uint32_t tm = __shfl_sync(FULL, tmem, 0), lead = elect_one();
-        const uint32_t q_lo = desc_lo(sm_q, 16), k_lo = desc_lo(sm_ring, 16), v_lo = desc_lo(sm_ring + S::TILE, KEYS * 128);
-        uint32_t p_phase = 0, q_phase = 0;                       // bits [half][buffer], [half]
+        const uint32_t q_lo = desc_lo(sm_q + h * S::Q, 16), k_lo = desc_lo(sm_ring, 16), v_lo = desc_lo(sm_ring + S::TILE, KEYS * 128);
+        uint32_t p_phase = 0, q_phase = 0;
         uint32_t ks = 0, kp = 0, vs = 0, vp = 0;                 // next K's and next V's stage, and its phase
         Tile w{};
         auto wait = [&](uint32_t b, uint32_t parity) {
-            if (!timeout && !mbar_wait(b, parity, plan.wait_polls))
+            if (lead && !timeout && !mbar_wait(b, parity, plan.wait_polls))
                 timeout = true;
-            timeout = __any_sync(FULL, timeout);
         };
-        for (int x = blockIdx.x; x < items && find_tile(p, plan, x, w, bad) && !timeout; x += gridDim.x) {
+        for (int x = blockIdx.x; x < items && find_tile(p, plan, x, w, bad); x += gridDim.x) {
             // uniform copies
             const int t0 = __shfl_sync(FULL, w.t0, 0), t1 = __shfl_sync(FULL, w.t1, 0);
-            const int lo[2] = {__shfl_sync(FULL, w.lo[0], 0), __shfl_sync(FULL, w.lo[1], 0)};
-            const int hi[2] = {__shfl_sync(FULL, w.hi[0], 0), __shfl_sync(FULL, w.hi[1], 0)};
-            // S of key tile t (both halves) and the P V of tile t - 2 before it, half by half
-            for (int t = t0; t < t1 + 2 && !timeout; t++) {
-                const bool s_now = t < t1, pv_now = t >= t0 + 2;
-                if (pv_now)
+            const int lo = __shfl_sync(FULL, h ? w.lo[1] : w.lo[0], 0), hi = __shfl_sync(FULL, h ? w.hi[1] : w.hi[0], 0);
+            // P V of key tile t - 2, then S of tile t into the buffer that P came from
+            for (int t = t0; t < t1 + 2; t++) {
+                const int u = t - 2;
+                if (u >= t0) {
                     wait(b_full + 16 * vs + 8, vp);
-                if (s_now)
-                    wait(b_full + 16 * ks, kp);
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const int u = t - 2;
-                    if (pv_now && u >= lo[h] && u < hi[h]) {
-                        const uint32_t buf = (u - lo[h]) & 1;
-                        wait(b_p + 16 * h + 8 * buf, p_phase >> (2 * h + buf) & 1);
-                        p_phase ^= 1u << (2 * h + buf);
-                        if (timeout)
-                            break;
+                    if (u >= lo && u < hi) {
+                        const uint32_t buf = (u - lo) & 1;
+                        wait(b_p + 16 * h + 8 * buf, p_phase >> buf & 1);
+                        p_phase ^= 1u << buf;
                         tc_fence_after();
                         const uint32_t b = v_lo + vs * (2 * S::TILE >> 4), d = tm + TM_O + h * 128;
                         const uint32_t a = tm + TM_S + h * 128 + 64 * buf;
-                        if (lead) {
-                            mma_ts<false>(d, a, b, id_o, u > lo[h]);
+                        if (lead && !timeout) {
+                            mma_ts<false>(d, a, b, id_o, u > lo);
 #pragma unroll
                             for (int k = 1; k < KEYS / 16; k++)
                                 mma_ts<true>(d, a + k * 8, b + k * (2048 >> 4), id_o, 1);
-                            umma_commit(b_o + 16 * h + 8 * buf);
+                            if (u + 2 >= hi)
+                                umma_commit(b_o + 16 * h + 8 * buf);
                         }
                     }
-                    if (s_now && t >= lo[h] && t < hi[h]) {
-                        if (t == lo[h]) {
-                            wait(b_q + 8 * h, q_phase >> h & 1);
-                            q_phase ^= 1u << h;
-                            if (timeout)
-                                break;
+                }
+                if (t < t1) {
+                    wait(b_full + 16 * ks, kp);
+                    if (t >= lo && t < hi) {
+                        if (t == lo) {
+                            wait(b_q + 8 * h, q_phase);
+                            q_phase ^= 1;
                         }
-                        const uint32_t buf = (t - lo[h]) & 1;
+                        const uint32_t buf = (t - lo) & 1;
                         tc_fence_after();
-                        const uint32_t a = q_lo + h * (S::Q >> 4), b = k_lo + ks * (2 * S::TILE >> 4);
-                        const uint32_t d = tm + TM_S + h * 128 + 64 * buf;
-                        if (lead) {
-                            mma_ss<false>(d, a, b, id_s, 0);
+                        const uint32_t b = k_lo + ks * (2 * S::TILE >> 4), d = tm + TM_S + h * 128 + 64 * buf;
+                        if (lead && !timeout) {
+                            mma_ss<false>(d, q_lo, b, id_s, 0);
 #pragma unroll
                             for (int k = 1; k < DIM / 16; k++)
-                                mma_ss<true>(d, a + (((k / 4) * (HALF * 128) + (k % 4) * 32) >> 4),
+                                mma_ss<true>(d, q_lo + (((k / 4) * (HALF * 128) + (k % 4) * 32) >> 4),
                                              b + (((k / 4) * (KEYS * 128) + (k % 4) * 32) >> 4), id_s, 1);
                             umma_commit(b_s + 16 * h + 8 * buf);
                         }
                     }
-                }
-                if (timeout)
-                    break;
-                if (pv_now) {
-                    if (lead)
-                        umma_commit(b_empty + 16 * vs + 8);
-                    if (++vs == S::SLOTS / 2)
-                        vs = 0, vp ^= 1;
-                }
-                if (s_now) {
-                    if (lead)
-                        umma_commit(b_empty + 16 * ks);
-                    if (++ks == S::SLOTS / 2)
+                    if (++ks == S::STAGES)
                         ks = 0, kp ^= 1;
+                }
+                if (u >= t0) {
+                    // tile u's stage is free for this half (its K was used two turns ago)
+                    if (lead && !timeout)
+                        umma_commit(b_empty + 8 * vs);
+                    if (++vs == S::STAGES)
+                        vs = 0, vp ^= 1;
                 }
             }
         }
         if (lead) {
             // everything issued has to be through before tensor memory is freed
-            umma_commit(b_drain);
-            mbar_wait(b_drain, 0);
+            umma_commit(b_drain + 8 * h);
+            mbar_wait(b_drain + 8 * h, 0);
         }
         __syncwarp();
     }
