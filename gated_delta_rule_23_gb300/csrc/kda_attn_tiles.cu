@@ -402,11 +402,11 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                     float top = -INFINITY;
                     l0 = l1 = 0;
                     tmem_get32(tm_s, s[0]);
+                    tmem_get32(tm_s + 32, s[1]);
+                    tmem_wait32(s[0]);
+                    tmem_wait32(s[1]);
 #pragma unroll
                     for (int c = 0; c < KEYS / 32; c++) {
-                        tmem_wait32(s[c & 1]);
-                        if (c + 1 < KEYS / 32)
-                            tmem_get32(tm_s + 32 * (c + 1), s[(c + 1) & 1]);
                         hide(s[c & 1], c);
                         top = top_of(s[c & 1], top);
 #pragma unroll
@@ -601,6 +601,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
         auto wait = [&](uint32_t b, uint32_t parity) {
             if (lead && !timeout && !mbar_wait(b, parity, plan.wait_polls))
                 timeout = true;
+            __syncwarp();
         };
         for (int x = blockIdx.x; x < items && find_tile(p, plan, x, w, bad); x += gridDim.x) {
             // uniform copies
@@ -626,6 +627,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                             if (u + 2 >= hi)
                                 umma_commit(b_o + 16 * h + 8 * buf);
                         }
+                        __syncwarp();
                     }
                 }
                 if (t < t1) {
@@ -646,6 +648,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                                              b + (((k / 4) * (KEYS * 128) + (k % 4) * 32) >> 4), id_s, 1);
                             umma_commit(b_s + 16 * h + 8 * buf);
                         }
+                        __syncwarp();
                     }
                     if (++ks == S::STAGES)
                         ks = 0, kp ^= 1;
@@ -654,6 +657,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                     // tile u's stage is free for this half (its K was used two turns ago)
                     if (lead && !timeout)
                         umma_commit(b_empty + 8 * vs);
+                    __syncwarp();
                     if (++vs == S::STAGES)
                         vs = 0, vp ^= 1;
                 }
