@@ -110,7 +110,7 @@ int64_t most_keys(int window, int sinks, int64_t T, int page, int max_pages)
 }
 
 // The cut of a call (sizes only, so that the workspace is known beforehand).  The keys are split while that still
-// adds tiles for idle SMs, four key tiles to a split at least.
+// adds tiles for idle SMs, two key tiles to a split at least.
 AttnPlan make_plan(int window, int sinks, bool varlen, int N, int64_t T, int Hq, int Hkv, int page, int max_pages)
 {
     AttnPlan plan{};
@@ -124,9 +124,9 @@ AttnPlan make_plan(int window, int sinks, bool varlen, int N, int64_t T, int Hq,
         tiles = T * group;                // a tile holds a row at least
     const int sms = device_sms();
     const int64_t ctas = tiles * Hkv;
-    const int64_t key_tiles = (most_keys(window, sinks, T < ATTN_ROWS ? T : ATTN_ROWS, page, max_pages) + 63) / 64 + 1;
+    const int64_t key_tiles = (most_keys(window, sinks, T < ATTN_ROWS ? T : ATTN_ROWS, page, max_pages) + 127) / 128 + 1;
     int64_t s = ctas > 0 ? sms / ctas : 1;
-    s = s < key_tiles / 4 ? s : key_tiles / 4;
+    s = s < key_tiles / 2 ? s : key_tiles / 2;
     plan.splits = s < 1 ? 1 : (s > 64 ? 64 : (int)s);
     plan.items = (int)(ctas * plan.splits);
     plan.wait_polls = wait_limit();

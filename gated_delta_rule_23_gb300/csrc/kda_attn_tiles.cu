@@ -1,16 +1,17 @@
-// Windowed attention over the paged cache on the tensor cores: 256 query rows a CTA, keys in tiles of 64.
+// Windowed attention over the paged cache on the tensor cores: 256 query rows a CTA, keys in tiles of 128.
 //
 // Rows.  A CTA owns rows [256 x, 256 x + 256) of one (sequence, key head), in two halves of 128 (row = token * group
 // + head of the group, so heads that share keys share the tile).  Keys.  The tile's rows need the sinks and the
 // positions from the first row's window on: two ranges of positions, cut into granules of at most 32 positions that
-// lie in one page each, and strung together to a list of "virtual" keys; 2 to 4 granules make a key tile, so a few
+// lie in one page each, and strung together to a list of "virtual" keys; 4 to 8 granules make a key tile, so a few
 // sinks cost a granule and not a tile.  Granules past the end are loaded from outside the cache (zeros).
 //
-// Per key tile and half:  S = Q K^T (tcgen05, fp32 in tensor memory);  P = 2^(scale S - m) with one thread a row, no
-// shuffles;  O += P V with P (bf16) read from tensor memory where S was.  From the commit of S to the P that the issuing
-// thread waits for lie some 2000 cycles of latency even without any arithmetic, against 500 of tensor time in a half's S
-// and P V for 64 keys: so a half has two S in tensor memory (2 x 64 columns; O takes 128), and the S after next is formed
-// while the softmax works on this one.  (128-key tiles with one S a half: 1586 us where this takes the time in DESIGN.)
+// Per half and 64 keys (half a key tile):  S = Q K^T (tcgen05, fp32 in tensor memory);  P = 2^(scale S - m) with one
+// thread a row, no shuffles;  O += P V with P (bf16) read from tensor memory where S was.  From the commit of S to the P
+// that the issuing warp waits for lie some 2000 cycles of latency even without any arithmetic, against 500 of tensor time
+// in a half's S and P V for 64 keys: so a half has two S in tensor memory (2 x 64 columns; O takes 128), and the S after
+// next is formed while the softmax works on this one.  An issuing warp's own instructions are the next bound (1150 cycles
+// of waits and commits for 64 keys with nothing else to do), hence key tiles of twice that and a warp for each half.
 // The running maximum m is moved (and O and l rescaled) only when a row's maximum has grown by more than 2^8: any m
 // gives the same quotient, and 2^8 is far from overflow in the fp32 sums.  So a tile's exponentials do not wait for its
 // maximum: they are taken with the m at hand while the maximum is formed, and taken again (S still stands; P is stored
@@ -34,7 +35,7 @@
 namespace kda {
 namespace {
 
-constexpr int KEYS = 64;                     // keys of a tile
+constexpr int KEYS = 128, SUB = 64;          // keys of a tile, and of a step of the softmax
 constexpr int THREADS = 384;                 // three warpgroups (the last warp has no role)
 // Registers a thread: 168 at launch (65,536 / 384); the softmax warpgroups, which hold a row of S, take what the third gives
 // back: 2 x 128 x 208 + 128 x 88 = 384 x 168.
@@ -49,8 +50,8 @@ constexpr unsigned FULL = 0xffffffffu;
 template <int DIM> struct Shape {
     static constexpr int TILE = KEYS * DIM * 2;              // bytes of a K or V tile
     static constexpr int Q = HALF * DIM * 2;                 // of a half's Q
-    static constexpr int STAGES = 5;                         // ring of key tiles, K and V of each
-    static constexpr int BAR = 2 * Q + STAGES * 2 * TILE;         // mbarriers behind Q and the ring
+    static constexpr int SLOTS = DIM == 128 ? 5 : 10;        // ring: K0 V0 K1 V1 ...
+    static constexpr int BAR = 2 * Q + SLOTS * TILE;         // mbarriers behind Q and the ring
     static constexpr int SMEM = 1024 + BAR + 512;            // 1024: alignment of the swizzle atoms
 };
 
@@ -63,7 +64,7 @@ struct Tile {             // one item; positions, rows and tokens fit 32 bits (c
     int start;            // position of virtual key sink_span
     int virt;             // virtual keys in all
     int t0, t1;           // key tiles of this split
-    int lo[2], hi[2];     // of them, the ones a half needs
+    int lo[2], hi[2];     // their steps (of SUB keys) that a half needs
 };
 
 __device__ __forceinline__ int virt_pos(const Tile &w, int v) { return v < w.sink_span ? v : v - w.sink_span + w.start; }
@@ -138,17 +139,18 @@ __device__ __forceinline__ bool find_tile(const AttnArgs &p, const AttnPlan &pla
 #pragma unroll
     for (int h = 0; h < 2; h++) {
         const int first = h * HALF, last = min(w.rows, first + HALF) - 1;
-        w.lo[h] = w.hi[h] = w.t0;
+        const int s0 = 2 * w.t0, s1 = 2 * w.t1;
+        w.lo[h] = w.hi[h] = s0;
         if (first > last)
             continue;
         const int a = row_pos(p, w, w.row0 + first) - p.window + 1, b = row_pos(p, w, w.row0 + last);
         if (b < 0)
             continue;
-        // the half's window, in tiles; with sinks a half needs the tiles from the first on
-        const int lo = p.sinks > 0 || a <= w.start ? 0 : (a - w.start) / KEYS;
-        const int hi = (b - w.start + w.sink_span) / KEYS + 1;
-        w.lo[h] = min(max(lo, w.t0), w.t1);
-        w.hi[h] = max(min(max(hi, w.t0), w.t1), w.lo[h]);
+        // the half's window, in steps; with sinks a half needs the steps from the first on
+        const int lo = p.sinks > 0 || a <= w.start ? 0 : (a - w.start) / SUB;
+        const int hi = (b - w.start + w.sink_span) / SUB + 1;
+        w.lo[h] = min(max(lo, s0), s1);
+        w.hi[h] = max(min(max(hi, s0), s1), w.lo[h]);
     }
     return true;
 }
@@ -271,15 +273,14 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char *const smem = smem_raw + (base - smem_u32(smem_raw));
     const uint32_t sm_q = base, sm_ring = base + 2 * S::Q, bar = base + S::BAR;
-    const uint32_t b_full = bar, b_empty = bar + 16 * S::STAGES, b_q = b_empty + 8 * S::STAGES, b_s = b_q + 16, b_p = b_s + 32,
-                   b_o = b_p + 32, b_drain = b_o + 32;     // full: [stage][K, V]; S, P, P V: [half][buffer]; drain: [half]
+    const uint32_t b_full = bar, b_empty = bar + 8 * S::SLOTS, b_q = b_empty + 8 * S::SLOTS, b_s = b_q + 16, b_p = b_s + 32,
+                   b_o = b_p + 32, b_drain = b_o + 32;     // S, P, P V: [half][buffer]; drain: [half]
     __shared__ uint32_t tmem_slot;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
     const int items = plan.items, g = plan.granule;
     if (tid == 0) {
-        for (int i = 0; i < S::STAGES; i++) {
-            mbar_init(b_full + 16 * i, 1);
-            mbar_init(b_full + 16 * i + 8, 1);
+        for (int i = 0; i < S::SLOTS; i++) {
+            mbar_init(b_full + 8 * i, 1);
             mbar_init(b_empty + 8 * i, 2);
         }
         for (int h = 0; h < 2; h++) {
@@ -336,25 +337,27 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             float m = -INFINITY, l = 0.0f;
             bool any = false;
             for (int t = w.lo[h]; t < w.hi[h]; t++) {
-                const int v0 = t * KEYS;
-                // the sequence's end inside the tile: what lies behind it in its page is cleared from V (K's scores are
+                const int v0 = t * SUB;
+                // the sequence's end inside the step: what lies behind it in its page is cleared from V (K's scores are
                 // masked)
                 const int end_v = w.len - w.start + w.sink_span - v0;
-                if (end_v > 0 && end_v < KEYS && (end_v & (g - 1))) {
-                    const int it = ring + t - w.t0, stage = it % S::STAGES;
-                    if (!mbar_wait(b_full + 16 * stage + 8, (it / S::STAGES) & 1, plan.wait_polls)) {
+                if (end_v > 0 && end_v < SUB && (end_v & (g - 1))) {
+                    const int it = 2 * (ring + t / 2 - w.t0) + 1, slot = it % S::SLOTS;
+                    if (!mbar_wait(b_full + 8 * slot, (it / S::SLOTS) & 1, plan.wait_polls)) {
                         timeout = true;
                         break;
                     }
                     const int count = (g - (end_v & (g - 1))) * 8;       // 16-byte vectors of a column block
-                    uint4 *v = reinterpret_cast<uint4 *>(smem + 2 * S::Q + (2 * stage + 1) * S::TILE) + end_v * 8;
+                    uint4 *v = reinterpret_cast<uint4 *>(smem + 2 * S::Q + slot * S::TILE) + ((t & 1) * SUB + end_v) * 8;
                     for (int i = tid & (HALF - 1); i < count * CB; i += HALF)
                         v[(i / count) * (KEYS * 8) + i % count] = make_uint4(0, 0, 0, 0);
                     fence_async_smem();
                 }
-                const int buf = (t - w.lo[h]) & 1;
+                const int buf = t & 1;
                 const uint32_t tm_s = tm_s0 + 64 * buf;
-                if (!mbar_wait(b_s + 16 * h + 8 * buf, s_phase >> buf & 1, plan.wait_polls)) {
+                if (lane == 0 && !mbar_wait(b_s + 16 * h + 8 * buf, s_phase >> buf & 1, plan.wait_polls))
+                    timeout = true;
+                if (__any_sync(FULL, timeout)) {
                     timeout = true;
                     break;
                 }
@@ -363,7 +366,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                 // columns of the tile that the row sees: the window's, and the sinks'
                 const int wa = max(pos - p.window + 1, w.start) - w.start + w.sink_span - v0;
                 const int wb = pos - w.start + w.sink_span - v0, sb = min(p.sinks, pos + 1) - 1 - v0;
-                const bool whole = __all_sync(FULL, wa <= 0 && wb >= KEYS - 1);
+                const bool whole = __all_sync(FULL, wa <= 0 && wb >= SUB - 1);
                 auto hide = [&](float (&s)[32], int c) {         // 32 columns from 32 c on
                     if (!whole) {
                         const uint32_t mask = range_word(wa, wb, c) | range_word(-v0, sb, c);
@@ -384,7 +387,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                 if (!any) {                                      // the first tile: m is its maximum
                     float top = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < KEYS / 32; c++) {
+                    for (int c = 0; c < SUB / 32; c++) {
                         tmem_get32(tm_s + 32 * c, s[0]);
                         tmem_wait32(s[0]);
                         hide(s[0], c);
@@ -394,7 +397,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                     if (top > m)                                 // not for NaN (0 x inf)
                         m = top;
                 }
-                uint32_t pk[KEYS / 2];
+                uint32_t pk[SUB / 2];
                 f2 l0, l1;
                 for (;;) {
                     const float mu = m == -INFINITY ? 0.0f : m;
@@ -406,7 +409,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                     tmem_wait32(s[0]);
                     tmem_wait32(s[1]);
 #pragma unroll
-                    for (int c = 0; c < KEYS / 32; c++) {
+                    for (int c = 0; c < SUB / 32; c++) {
                         hide(s[c & 1], c);
                         top = top_of(s[c & 1], top);
 #pragma unroll
@@ -465,7 +468,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             }
             // The next item's Q: the half's last S is formed, so its Q rows are free.
             const bool stored = any;
-            const int tiles = w.hi[h] - w.lo[h];
+            const int steps = w.hi[h] - w.lo[h], last_buf = (w.hi[h] - 1) & 1;
             ring += w.t1 - w.t0;
             x += gridDim.x;
             have = x < items && find_tile(p, plan, x, w, bad);
@@ -473,10 +476,10 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             if (more)
                 load_q<DIM>(p, w, sm_q, warp, lane);
             if (stored) {
-                const int buf = (tiles - 1) & 1;                 // the last P V: those before it are through with it
-                if (!mbar_wait(b_o + 16 * h + 8 * buf, o_phase >> buf & 1, plan.wait_polls))
+                // the last P V: those before it are through with it
+                if (!mbar_wait(b_o + 16 * h + 8 * last_buf, o_phase >> last_buf & 1, plan.wait_polls))
                     timeout = true;
-                o_phase ^= tiles > 1 ? 3 : 1u << buf;
+                o_phase ^= steps > 1 ? 3 : 1u << last_buf;
                 tc_fence_after();
             }
             if (more)
@@ -559,44 +562,42 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                             bad = true;
                     }
                 }
-                const int stage = issued % S::STAGES;
-                if (issued >= S::STAGES && !mbar_wait(b_empty + 8 * stage, (issued / S::STAGES - 1) & 1, plan.wait_polls))
-                    timeout = true;
-                if (__any_sync(FULL, timeout)) {
-                    timeout = true;
-                    break;
-                }
-                if (lane == 0) {
-                    mbar_expect_tx(b_full + 16 * stage, S::TILE);
-                    mbar_expect_tx(b_full + 16 * stage + 8, S::TILE);
-                }
-                __syncwarp();
-                if (lane < ng) {
 #pragma unroll
-                    for (int kv = 0; kv < 2; kv++)
+                for (int kv = 0; kv < 2; kv++) {
+                    const int slot = issued % S::SLOTS;
+                    if (issued >= S::SLOTS && !mbar_wait(b_empty + 8 * slot, (issued / S::SLOTS - 1) & 1, plan.wait_polls))
+                        timeout = true;
+                    if (__any_sync(FULL, timeout)) {
+                        timeout = true;
+                        break;
+                    }
+                    if (lane == 0)
+                        mbar_expect_tx(b_full + 8 * slot, S::TILE);
+                    __syncwarp();
+                    if (lane < ng) {
 #pragma unroll
                         for (int cb = 0; cb < CB; cb++)
-                            tma_load_2d(sm_ring + (2 * stage + kv) * S::TILE + cb * (KEYS * 128) + lane * g * 128,
-                                        kv ? &vmap : &kmap, cb * 64, y, b_full + 16 * stage + 8 * kv);
+                            tma_load_2d(sm_ring + slot * S::TILE + cb * (KEYS * 128) + lane * g * 128, kv ? &vmap : &kmap,
+                                        cb * 64, y, b_full + 8 * slot);
+                    }
+                    issued++;
                 }
-                issued++;
             }
         }
         // no copy is in flight when the CTA leaves, also where the work was given up
-        for (int it = max(issued - S::STAGES, 0); it < issued; it++)
-            for (int kv = 0; kv < 2; kv++)
-                mbar_wait(b_full + 16 * (it % S::STAGES) + 8 * kv, (it / S::STAGES) & 1);
+        for (int it = max(issued - S::SLOTS, 0); it < issued; it++)
+            mbar_wait(b_full + 8 * (it % S::SLOTS), (it / S::SLOTS) & 1);
     } else if (warp == 9 || warp == 10) {
         // ------------------------------------------------------------ tensor-core issue, warp 9 for half 0, 10 for half 1
         // The warp walks the items; one elected lane waits and issues.  What an instruction needs (descriptors, addresses)
         // is the same in all lanes and known to be, so that it is formed in uniform registers: issuing from one thread's
         // own registers took some 80 cycles a product.  Once a wait has given up, nothing more is issued.
         const int h = __shfl_sync(FULL, warp, 0) - 9;
-        const uint32_t id_s = idesc_bf16(HALF, KEYS, false), id_o = idesc_bf16(HALF, DIM, true);
+        const uint32_t id_s = idesc_bf16(HALF, SUB, false), id_o = idesc_bf16(HALF, DIM, true);
         const uint32_t tm = __shfl_sync(FULL, tmem, 0), lead = elect_one();
-        const uint32_t q_lo = desc_lo(sm_q + h * S::Q, 16), k_lo = desc_lo(sm_ring, 16), v_lo = desc_lo(sm_ring + S::TILE, KEYS * 128);
+        const uint32_t q_lo = desc_lo(sm_q + h * S::Q, 16), k_lo = desc_lo(sm_ring, 16), v_lo = desc_lo(sm_ring, KEYS * 128);
         uint32_t p_phase = 0, q_phase = 0;
-        uint32_t ks = 0, kp = 0, vs = 0, vp = 0;                 // next K's and next V's stage, and its phase
+        uint32_t ks = 0, kp = 0, vs = 1, vp = 0;                 // next K's and next V's slot, and its phase
         Tile w{};
         auto wait = [&](uint32_t b, uint32_t parity) {
             if (lead && !timeout && !mbar_wait(b, parity, plan.wait_polls))
@@ -607,39 +608,39 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             // uniform copies
             const int t0 = __shfl_sync(FULL, w.t0, 0), t1 = __shfl_sync(FULL, w.t1, 0);
             const int lo = __shfl_sync(FULL, h ? w.lo[1] : w.lo[0], 0), hi = __shfl_sync(FULL, h ? w.hi[1] : w.hi[0], 0);
-            // P V of key tile t - 2, then S of tile t into the buffer that P came from
-            for (int t = t0; t < t1 + 2; t++) {
-                const int u = t - 2;
-                if (u >= t0) {
-                    wait(b_full + 16 * vs + 8, vp);
-                    if (u >= lo && u < hi) {
-                        const uint32_t buf = (u - lo) & 1;
+            // step by step P V of key tile t - 1, then S of tile t into the buffer that P came from
+            for (int t = t0; t <= t1; t++) {
+                const bool pv = t > t0, sk = t < t1;
+                if (pv)
+                    wait(b_full + 8 * vs, vp);
+#pragma unroll
+                for (int buf = 0; buf < 2; buf++) {
+                    const int now = 2 * t + buf, old = now - 2;
+                    if (pv && old >= lo && old < hi) {
                         wait(b_p + 16 * h + 8 * buf, p_phase >> buf & 1);
                         p_phase ^= 1u << buf;
                         tc_fence_after();
-                        const uint32_t b = v_lo + vs * (2 * S::TILE >> 4), d = tm + TM_O + h * 128;
+                        const uint32_t b = v_lo + vs * (S::TILE >> 4) + buf * (SUB * 128 >> 4), d = tm + TM_O + h * 128;
                         const uint32_t a = tm + TM_S + h * 128 + 64 * buf;
                         if (lead && !timeout) {
-                            mma_ts<false>(d, a, b, id_o, u > lo);
+                            mma_ts<false>(d, a, b, id_o, old > lo);
 #pragma unroll
-                            for (int k = 1; k < KEYS / 16; k++)
+                            for (int k = 1; k < SUB / 16; k++)
                                 mma_ts<true>(d, a + k * 8, b + k * (2048 >> 4), id_o, 1);
-                            if (u + 2 >= hi)
+                            if (old + 2 >= hi)
                                 umma_commit(b_o + 16 * h + 8 * buf);
                         }
                         __syncwarp();
                     }
-                }
-                if (t < t1) {
-                    wait(b_full + 16 * ks, kp);
-                    if (t >= lo && t < hi) {
-                        if (t == lo) {
+                    if (sk && buf == 0)
+                        wait(b_full + 8 * ks, kp);
+                    if (sk && now >= lo && now < hi) {
+                        if (now == lo) {
                             wait(b_q + 8 * h, q_phase);
                             q_phase ^= 1;
                         }
-                        const uint32_t buf = (t - lo) & 1;
                         tc_fence_after();
-                        const uint32_t b = k_lo + ks * (2 * S::TILE >> 4), d = tm + TM_S + h * 128 + 64 * buf;
+                        const uint32_t b = k_lo + ks * (S::TILE >> 4) + buf * (SUB * 128 >> 4), d = tm + TM_S + h * 128 + 64 * buf;
                         if (lead && !timeout) {
                             mma_ss<false>(d, q_lo, b, id_s, 0);
 #pragma unroll
@@ -650,17 +651,18 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                         }
                         __syncwarp();
                     }
-                    if (++ks == S::STAGES)
-                        ks = 0, kp ^= 1;
                 }
-                if (u >= t0) {
-                    // tile u's stage is free for this half (its K was used two turns ago)
-                    if (lead && !timeout)
+                if (lead && !timeout) {                          // this half is through with V of t - 1 and K of t
+                    if (pv)
                         umma_commit(b_empty + 8 * vs);
-                    __syncwarp();
-                    if (++vs == S::STAGES)
-                        vs = 0, vp ^= 1;
+                    if (sk)
+                        umma_commit(b_empty + 8 * ks);
                 }
+                __syncwarp();
+                if (pv && (vs += 2) >= S::SLOTS)
+                    vs -= S::SLOTS, vp ^= 1;
+                if (sk && (ks += 2) >= S::SLOTS)
+                    ks -= S::SLOTS, kp ^= 1;
             }
         }
         if (lead) {
