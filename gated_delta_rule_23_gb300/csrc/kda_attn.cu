@@ -16,6 +16,7 @@ template <int DIM> __global__ void __launch_bounds__(ROW_THREADS) kda_attn_join_
 {
     constexpr int PER = DIM / 32;
     const int64_t r = (int64_t)blockIdx.x * (ROW_THREADS / 32) + threadIdx.x / 32;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (r >= plan.rows)
         return;
     const int lane = threadIdx.x & 31;
@@ -117,19 +118,30 @@ AttnPlan make_plan(int window, int sinks, bool varlen, int N, int64_t T, int Hq,
     const int group = Hq / Hkv;
     const int64_t tokens = varlen ? T : (int64_t)N * T;
     plan.rows = tokens * Hq;
+    plan.wait_polls = wait_limit();
+    const int sms = device_sms();
+    if (!varlen && T * group <= DECODE_ROWS) {
+        // two CTAs an SM; a split has 128 keys at least (every warp two blocks)
+        plan.decode = true;
+        plan.granule = DECODE_KEYS;
+        const int64_t ctas = (int64_t)N * Hkv, most = most_keys(window, sinks, T, page, max_pages) / 128;
+        int64_t s = ctas > 0 ? 2 * sms / ctas : 1;
+        s = s < most ? s : most;
+        plan.splits = s < 1 ? 1 : (s > 64 ? 64 : (int)s);
+        plan.items = (int)(ctas * plan.splits);
+        return plan;
+    }
     plan.granule = page < 32 ? page : 32;
     int64_t tiles = varlen ? (T * group + (int64_t)(ATTN_ROWS - 1) * N) / ATTN_ROWS
                            : (int64_t)N * ((T * group + ATTN_ROWS - 1) / ATTN_ROWS);
     if (varlen && tiles > T * group)
         tiles = T * group;                // a tile holds a row at least
-    const int sms = device_sms();
     const int64_t ctas = tiles * Hkv;
     const int64_t key_tiles = (most_keys(window, sinks, T < ATTN_ROWS ? T : ATTN_ROWS, page, max_pages) + 127) / 128 + 1;
     int64_t s = ctas > 0 ? sms / ctas : 1;
     s = s < key_tiles / 2 ? s : key_tiles / 2;
     plan.splits = s < 1 ? 1 : (s > 64 ? 64 : (int)s);
     plan.items = (int)(ctas * plan.splits);
-    plan.wait_polls = wait_limit();
     return plan;
 }
 
@@ -145,11 +157,18 @@ size_t plan_bytes(const AttnPlan &plan, int dim)
 cudaError_t launch_attn_join(const AttnArgs &p, const AttnPlan &plan, cudaStream_t st)
 {
     const unsigned grid = (unsigned)((plan.rows + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32));
-    if (p.cache.dim == 128)
-        kda_attn_join_kernel<128><<<grid, ROW_THREADS, 0, st>>>(p, plan);
-    else
-        kda_attn_join_kernel<64><<<grid, ROW_THREADS, 0, st>>>(p, plan);
-    return cudaGetLastError();
+    // launched as a programmatic dependent: its CTAs wait for the results themselves
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(ROW_THREADS);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return p.cache.dim == 128 ? cudaLaunchKernelEx(&cfg, kda_attn_join_kernel<128>, p, plan)
+                              : cudaLaunchKernelEx(&cfg, kda_attn_join_kernel<64>, p, plan);
 }
 
 }  // namespace kda
@@ -190,7 +209,7 @@ extern "C" kda_status_t kda_window_attn_ws(const void *q, int64_t q_stride, cons
     plan.part_o = static_cast<float *>(workspace);
     plan.part_ml = reinterpret_cast<float2 *>(plan.part_o + (size_t)plan.splits * plan.rows * D);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_attn_tiles(p, plan, st);
+    cudaError_t e = plan.decode ? launch_attn_decode(p, plan, st) : launch_attn_tiles(p, plan, st);
     if (e == cudaSuccess && plan.splits > 1)
         e = launch_attn_join(p, plan, st);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;

@@ -1,6 +1,8 @@
 // Windowed attention over the paged cache: the problem description, and the row form of the definition.
 #pragma once
 
+#include <cuda.h>
+
 #include "kda_step.cuh"
 
 namespace kda {
@@ -22,8 +24,10 @@ struct AttnArgs {
 // r % group of the group (so that heads sharing keys share a tile); rows come in tiles, and the keys a tile needs are
 // split `splits` ways, the partial results joined by a second kernel when there is more than one.
 constexpr int ATTN_ROWS = 256;   // query rows of a tile
+constexpr int DECODE_ROWS = 16, DECODE_KEYS = 16;   // rows of the decode kernel, keys of its blocks
 
 struct AttnPlan {
+    bool decode;            // at most 16 query rows a (sequence, key head): the decode kernel, one item a CTA
     int splits;
     int items;              // (row tile, key head, split) items (ragged: an upper bound)
     int granule;            // positions of a cache page that are copied together
@@ -34,8 +38,19 @@ struct AttnPlan {
 };
 
 cudaError_t launch_attn_tiles(const AttnArgs &p, const AttnPlan &plan, cudaStream_t stream);
+cudaError_t launch_attn_decode(const AttnArgs &p, const AttnPlan &plan, cudaStream_t stream);
 cudaError_t launch_attn_join(const AttnArgs &p, const AttnPlan &plan, cudaStream_t stream);
 
+// A tensor map of the cache as rows [pages * hkv * page][dim], boxes of 64 columns by `rows` rows, 128-byte swizzle.
+cudaError_t cache_map(CUtensorMap *map, const void *ptr, const PagedCache &c, int rows);
+
+constexpr int OUTSIDE = INT32_MAX - 4096;   // a row that no cache has: a bulk copy from it gives zeros
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t mbar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(mbar) : "memory");
+}
 constexpr float LN2 = 0.6931471805599453f;
 
 // Sequence, index within it and length of token t's sequence, by a whole warp; an index outside [0, len) for a token

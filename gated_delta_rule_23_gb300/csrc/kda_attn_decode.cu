@@ -1,0 +1,326 @@
+// Windowed attention over the paged cache for few query rows: at most 16 (tokens x heads of a key head's group).
+//
+// A decode step reads every visible key and value once for a handful of rows: the floor is the cache's bytes at the
+// memory's rate, and the arithmetic (16 rows wide on mma.sync) has to stay out of the way.  One CTA takes a (sequence, key
+// head) or a split of its keys; each of its warps works by itself on blocks of 16 keys, every fourth one, that its lane 0
+// brings in with bulk tensor copies into the warp's own ring of shared memory: no barrier of the CTA in the loop, and
+// RING x 8 KB in flight a warp.  The warps' results (running maximum, sum, O in fp32) are joined once at the end, in
+// shared memory, the splits' by the join kernel.
+//
+// Keys come as in the tile kernel: the sinks' granules, then the window's, 16 positions each, which lie in one page.
+// Values that no row of the CTA sees are cleared in shared memory; where the rows differ in what they see (several
+// tokens), an output row that does not come out finite is taken again from the definition.
+#include "kda_attn.cuh"
+
+#include <atomic>
+#include <cfloat>
+
+namespace kda {
+namespace {
+
+constexpr int WARPS = 4, THREADS = 32 * WARPS;
+constexpr int KEYS = DECODE_KEYS, ROWS = DECODE_ROWS;
+constexpr float RESCALE_AT = 8.0f;           // base-2 growth of a maximum that moves it
+constexpr unsigned FULL = 0xffffffffu;
+
+template <int DIM> struct Shape {
+    static constexpr int RING = DIM == 128 ? 3 : 6;              // blocks in flight a warp
+    static constexpr int BLOCK = KEYS * DIM * 2;                 // bytes of K, and of V
+    static constexpr int WARP = RING * 2 * BLOCK;                // a warp's ring
+    static constexpr int SMEM = 1024 + WARPS * WARP;
+    static_assert(WARP >= ROWS * DIM * 4, "O of a warp goes where its ring was");
+};
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16-byte chunk c of key `key` in a block of 64-column pieces, 128-byte swizzle
+__device__ __forceinline__ uint32_t chunk_at(uint32_t block, int key, int c)
+{
+    return block + (c / 8) * (KEYS * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&x);
+}
+
+template <int DIM>
+__global__ void __launch_bounds__(THREADS, 2)
+kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap)
+{
+    using S = Shape<DIM>;
+    constexpr int CB = DIM / 64, KS = DIM / 16, NT = DIM / 8;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) uint64_t bars[WARPS * S::RING];
+    __shared__ float2 stats[WARPS][ROWS];
+    asm volatile("griddepcontrol.launch_dependents;");
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    unsigned char *const smem = smem_raw + (base - smem_u32(smem_raw));
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, g = lane / 4, t = lane % 4;
+
+    int x = blockIdx.x;
+    const int kvh = x % p.cache.hkv;
+    x /= p.cache.hkv;
+    const int n = x % p.tok.N, split = x / p.tok.N;
+    const int tokens = (int)p.tok.T, rows = tokens * p.group;
+    bool bad = false, timeout = false;
+    const int len = (int)cache_len(p.cache, n, bad);
+    const int p0 = len - tokens, p1 = len - 1;                   // positions of the first and the last token
+    // virtual keys: the sinks' granules, then the window's
+    int sink = 0, start = 0, virt = 0;
+    if (p1 >= 0) {
+        start = max(p0 - p.window + 1, 0) & -KEYS;
+        sink = (p.sinks + KEYS - 1) & -KEYS;
+        if (start <= sink)
+            sink = start = 0;
+        virt = sink + (p1 + 1 - start);
+    }
+    const int blocks = (virt + KEYS - 1) / KEYS;
+    const int b0 = (int)((int64_t)blocks * split / plan.splits), b1 = (int)((int64_t)blocks * (split + 1) / plan.splits);
+    auto position = [&](int b) { return b * KEYS < sink ? b * KEYS : b * KEYS - sink + start; };
+
+    const uint32_t ring = base + warp * S::WARP, bar = smem_u32(bars + warp * S::RING);
+    if (lane == 0) {
+        for (int i = 0; i < S::RING; i++)
+            mbar_init(bar + 8 * i, 1);
+        mbar_fence_init();
+    }
+    __syncwarp();
+    const int mine = b1 - b0 > warp ? (b1 - b0 - warp + WARPS - 1) / WARPS : 0;      // blocks b0 + warp + WARPS i
+    auto fetch = [&](int i) {                                    // by lane 0
+        const int j = position(b0 + warp + WARPS * i);
+        int y = OUTSIDE;
+        const int32_t id = p.cache.table[(int64_t)n * p.cache.max_pages + (j >> p.cache.page_shift)];
+        if (id >= 0 && id < p.cache.pages)
+            y = (int)((((int64_t)id * p.cache.hkv + kvh) << p.cache.page_shift) + (j & ((1 << p.cache.page_shift) - 1)));
+        else
+            bad = true;
+        const uint32_t at = ring + (i % S::RING) * 2 * S::BLOCK, b = bar + 8 * (i % S::RING);
+        mbar_expect_tx(b, 2 * S::BLOCK);
+#pragma unroll
+        for (int c = 0; c < CB; c++) {
+            tma_load_2d(at + c * KEYS * 128, &kmap, c * 64, y, b);
+            tma_load_2d(at + S::BLOCK + c * KEYS * 128, &vmap, c * 64, y, b);
+        }
+    };
+    if (lane == 0)
+        for (int i = 0; i < S::RING && i < mine; i++)
+            fetch(i);
+
+    // Q as the first operand: rows g and g + 8
+    uint32_t q[KS][4];
+    int pos[2];
+#pragma unroll
+    for (int r = 0; r < 2; r++) {
+        const int row = g + 8 * r;
+        const bool in = row < rows;
+        const int tok = in ? row / p.group : 0;
+        pos[r] = in ? p0 + tok : -1;
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(
+            p.q + (int64_t)(n * tokens + tok) * p.q_stride + (kvh * p.group + (in ? row % p.group : 0)) * DIM);
+#pragma unroll
+        for (int k = 0; k < KS; k++) {
+            q[k][r] = in ? __ldg(src + 8 * k + t) : 0;
+            q[k][2 + r] = in ? __ldg(src + 8 * k + 4 + t) : 0;
+        }
+    }
+    float o[NT][4];
+#pragma unroll
+    for (int c = 0; c < NT; c++)
+        o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+
+    int done = 0;
+    for (int i = 0; i < mine; i++) {
+        const int slot = i % S::RING, j0 = position(b0 + warp + WARPS * i);
+        const uint32_t kb = ring + slot * 2 * S::BLOCK, vb = kb + S::BLOCK;
+        if (!mbar_wait(bar + 8 * slot, (i / S::RING) & 1, plan.wait_polls))
+            timeout = true;
+        if (__any_sync(FULL, timeout)) {
+            timeout = true;
+            break;
+        }
+        done = i + 1;
+        // S: keys j0 .. j0 + 15 as two tiles of 8
+        float s[2][4] = {};
+#pragma unroll
+        for (int k = 0; k < KS; k++) {
+            uint32_t b[4];
+            ldsm_x4(chunk_at(kb, (lane / 16) * 8 + lane % 8, 2 * k + (lane / 8) % 2), b);
+            mma_bf16(s[0], q[k], b[0], b[1]);
+            mma_bf16(s[1], q[k], b[2], b[3]);
+        }
+        // whole: every row sees every key of the block
+        const bool whole = j0 + KEYS - 1 <= p0 && j0 > p1 - p.window;
+        if (!whole) {
+#pragma unroll
+            for (int c = 0; c < 2; c++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int j = j0 + 8 * c + 2 * t + (e & 1), at = pos[e / 2];
+                    s[c][e] = j <= at && (j > at - p.window || j < p.sinks) ? s[c][e] : -INFINITY;
+                }
+            // values that no row sees
+            for (int v = lane; v < KEYS * (DIM / 8); v += 32) {
+                const int key = v % KEYS, j = j0 + key;
+                if (j > p1 || (j <= p0 - p.window && j >= p.sinks)) {
+                    const uint32_t z = chunk_at(vb, key, v / KEYS);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(z), "r"(0) : "memory");
+                }
+            }
+            fence_async_smem();                                  // the slot's next copy comes after these
+            __syncwarp();
+        }
+        float top[2];
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+            top[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+            top[r] = fmaxf(top[r], __shfl_xor_sync(FULL, top[r], 1));
+            top[r] = fmaxf(top[r], __shfl_xor_sync(FULL, top[r], 2)) * p.scale_log2;
+        }
+        const bool move0 = top[0] > m[0] + RESCALE_AT, move1 = top[1] > m[1] + RESCALE_AT;
+        if (__any_sync(FULL, move0 || move1)) {                  // also the first block with a visible key
+            const float a0 = move0 ? ex2_approx(m[0] - top[0]) : 1.0f, a1 = move1 ? ex2_approx(m[1] - top[1]) : 1.0f;
+            m[0] = move0 ? top[0] : m[0];
+            m[1] = move1 ? top[1] : m[1];
+            l[0] *= a0;
+            l[1] *= a1;
+#pragma unroll
+            for (int c = 0; c < NT; c++) {
+                o[c][0] *= a0, o[c][1] *= a0;
+                o[c][2] *= a1, o[c][3] *= a1;
+            }
+        }
+        const float mu0 = m[0] == -INFINITY ? 0.0f : m[0], mu1 = m[1] == -INFINITY ? 0.0f : m[1];
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+            s[c][0] = ex2_approx(fmaf(s[c][0], p.scale_log2, -mu0));
+            s[c][1] = ex2_approx(fmaf(s[c][1], p.scale_log2, -mu0));
+            s[c][2] = ex2_approx(fmaf(s[c][2], p.scale_log2, -mu1));
+            s[c][3] = ex2_approx(fmaf(s[c][3], p.scale_log2, -mu1));
+            l[0] += s[c][0] + s[c][1];
+            l[1] += s[c][2] + s[c][3];
+        }
+        const uint32_t a[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
+                               pack_bf16(s[1][2], s[1][3])};
+#pragma unroll
+        for (int c = 0; c < NT; c += 2) {
+            uint32_t b[4];
+            ldsm_x4_t(chunk_at(vb, ((lane / 8) % 2) * 8 + lane % 8, c + lane / 16), b);
+            mma_bf16(o[c], a, b[0], b[1]);
+            mma_bf16(o[c + 1], a, b[2], b[3]);
+        }
+        __syncwarp();                                            // all lanes are through with the slot
+        if (lane == 0 && i + S::RING < mine)
+            fetch(i + S::RING);
+    }
+    // no copy is in flight when the work was given up
+    for (int i = done; i < mine && i < done + S::RING; i++)
+        mbar_wait(bar + 8 * (i % S::RING), (i / S::RING) & 1);
+    __syncwarp();
+
+    // the warps' results: O where the warp's ring was, row-major
+#pragma unroll
+    for (int r = 0; r < 2; r++) {
+        l[r] += __shfl_xor_sync(FULL, l[r], 1);
+        l[r] += __shfl_xor_sync(FULL, l[r], 2);
+        if (t == 0)
+            stats[warp][g + 8 * r] = make_float2(m[r], l[r]);
+    }
+    float *const part = reinterpret_cast<float *>(smem + warp * S::WARP);
+#pragma unroll
+    for (int c = 0; c < NT; c++)
+#pragma unroll
+        for (int r = 0; r < 2; r++)
+            *reinterpret_cast<float2 *>(part + (g + 8 * r) * DIM + ((8 * c + 2 * t) ^ (8 * (g & 3)))) = make_float2(o[c][2 * r], o[c][2 * r + 1]);
+    const bool failed = __syncthreads_or(timeout);
+    if (!failed) {
+        for (int row = warp; row < rows; row += WARPS) {         // a warp joins a row
+            float M = -INFINITY, L = 0.0f, w[WARPS];
+#pragma unroll
+            for (int i = 0; i < WARPS; i++)
+                M = fmaxf(M, stats[i][row].x);
+            const float mu = M == -INFINITY ? 0.0f : M;
+            bool none[WARPS];                                    // warps without a visible key
+#pragma unroll
+            for (int i = 0; i < WARPS; i++) {
+                const float2 st = stats[i][row];
+                none[i] = st.x == -INFINITY && st.y == 0.0f;
+                w[i] = ex2_approx((st.x == -INFINITY ? 0.0f : st.x) - mu);
+                if (!none[i])
+                    L += w[i] * st.y;
+            }
+            bool finite = L <= FLT_MAX;
+            const int tok = row / p.group, head = kvh * p.group + row % p.group;
+            const int64_t at = (int64_t)(n * tokens + tok) * p.hq + head;
+            const bool whole = plan.splits == 1;
+            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+            for (int e0 = 0; e0 < DIM; e0 += 64) {
+                const int e = e0 + 2 * lane;
+                float2 y = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int i = 0; i < WARPS; i++) {
+                    if (none[i])
+                        continue;
+                    const float2 z = *reinterpret_cast<const float2 *>(reinterpret_cast<const float *>(smem + i * S::WARP) +
+                                                                       row * DIM + (e ^ (8 * (row & 3))));
+                    y.x = fmaf(w[i], z.x, y.x);
+                    y.y = fmaf(w[i], z.y, y.y);
+                }
+                finite &= fabsf(y.x) <= FLT_MAX && fabsf(y.y) <= FLT_MAX;
+                if (whole)
+                    *reinterpret_cast<uint32_t *>(p.out + at * DIM + e) = L == 0.0f ? 0u : pack_bf16(y.x * inv, y.y * inv);
+                else
+                    *reinterpret_cast<float2 *>(plan.part_o + (split * plan.rows + at) * DIM + e) = y;
+            }
+            if (lane == 0) {
+                if (!whole)
+                    plan.part_ml[split * plan.rows + at] = make_float2(M, L);
+                else if (p.lse)
+                    p.lse[at] = L == 0.0f ? -INFINITY : LN2 * (M + log2f(L));
+            }
+            if (whole && __any_sync(FULL, !finite)) {
+                __syncwarp();
+                attn_row<DIM>(p, n, (int64_t)n * tokens + tok, head, p0 + tok, bad);
+            }
+        }
+    }
+    report(p.err, bad, DEVERR_CU_SEQLENS);
+    report(p.err, timeout, DEVERR_TIMEOUT);
+}
+
+template <int DIM> cudaError_t launch_decode_dim(const AttnArgs &p, const AttnPlan &plan, cudaStream_t st)
+{
+    static std::atomic<uint64_t> ready;      // devices whose kernel attribute is set
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && !(ready.load() >> dev & 1)) {
+        e = cudaFuncSetAttribute(kda_attn_decode_kernel<DIM>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<DIM>::SMEM);
+        if (e == cudaSuccess)
+            ready.fetch_or(1ull << dev);
+    }
+    CUtensorMap kmap, vmap;
+    if (e == cudaSuccess)
+        e = cache_map(&kmap, p.cache.k, p.cache, KEYS);
+    if (e == cudaSuccess)
+        e = cache_map(&vmap, p.cache.v, p.cache, KEYS);
+    if (e != cudaSuccess)
+        return e;
+    kda_attn_decode_kernel<DIM><<<(unsigned)plan.items, THREADS, Shape<DIM>::SMEM, st>>>(p, plan, kmap, vmap);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_decode(const AttnArgs &p, const AttnPlan &plan, cudaStream_t st)
+{
+    return p.cache.dim == 128 ? launch_decode_dim<128>(p, plan, st) : launch_decode_dim<64>(p, plan, st);
+}
+
+}  // namespace kda

@@ -27,8 +27,6 @@
 // finite is taken again from the definition, key by key, by attn_row.
 #include "kda_attn.cuh"
 
-#include <cuda.h>
-
 #include <atomic>
 #include <cfloat>
 
@@ -190,11 +188,6 @@ template <bool ACC> __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t 
         asm volatile("{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %4};\n"
                      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}"
                      ::"r"(d), "r"(a_tmem), "r"(b), "r"(idesc), "r"(DESC_HI), "r"(acc) : "memory");
-}
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t mbar)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-                 ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(mbar) : "memory");
 }
 // 32 columns of the warp's 32 lanes, one row a thread: the load, and the wait for it, which names the registers so that
 // nothing that uses them moves before it
@@ -551,7 +544,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
         Tile w;
         for (int x = blockIdx.x; x < items && !timeout && find_tile(p, plan, x, w, bad); x += gridDim.x) {
             for (int t = w.t0; t < w.t1 && !timeout; t++) {
-                int y = INT32_MAX - 4096;                        // outside the cache: zeros
+                int y = OUTSIDE;
                 if (lane < ng) {
                     const int v = t * KEYS + lane * g, j = virt_pos(w, v);
                     if (v < w.virt && j < w.len) {
@@ -702,23 +695,6 @@ cudaError_t encode_fn(EncodeTiled *fn)
     return cudaSuccess;
 }
 
-// The cache as a matrix of rows [pages * hkv * page][dim]; a box is 64 columns of one granule's rows.
-cudaError_t make_map(CUtensorMap *map, const void *ptr, const PagedCache &c)
-{
-    EncodeTiled fn;
-    const cudaError_t e = encode_fn(&fn);
-    if (e != cudaSuccess)
-        return e;
-    const int page = 1 << c.page_shift;
-    const cuuint64_t dims[2] = {(cuuint64_t)c.dim, (cuuint64_t)c.pages * c.hkv * page};
-    const cuuint64_t strides[1] = {(cuuint64_t)c.dim * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)(page < 32 ? page : 32)}, step[2] = {1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, step,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <int DIM> cudaError_t launch_tiles(const AttnArgs &p, const AttnPlan &plan, cudaStream_t st)
 {
     static std::atomic<uint64_t> ready;      // devices whose kernel attribute is set
@@ -731,9 +707,9 @@ template <int DIM> cudaError_t launch_tiles(const AttnArgs &p, const AttnPlan &p
     }
     CUtensorMap kmap, vmap;
     if (e == cudaSuccess)
-        e = make_map(&kmap, p.cache.k, p.cache);
+        e = cache_map(&kmap, p.cache.k, p.cache, plan.granule);
     if (e == cudaSuccess)
-        e = make_map(&vmap, p.cache.v, p.cache);
+        e = cache_map(&vmap, p.cache.v, p.cache, plan.granule);
     if (e != cudaSuccess)
         return e;
     const int sms = device_sms();
@@ -745,6 +721,23 @@ template <int DIM> cudaError_t launch_tiles(const AttnArgs &p, const AttnPlan &p
 }
 
 }  // namespace
+
+// The cache as a matrix of rows [pages * hkv * page][dim]; a box is 64 columns of `rows` rows.
+cudaError_t cache_map(CUtensorMap *map, const void *ptr, const PagedCache &c, int rows)
+{
+    EncodeTiled fn;
+    const cudaError_t e = encode_fn(&fn);
+    if (e != cudaSuccess)
+        return e;
+    const int page = 1 << c.page_shift;
+    const cuuint64_t dims[2] = {(cuuint64_t)c.dim, (cuuint64_t)c.pages * c.hkv * page};
+    const cuuint64_t strides[1] = {(cuuint64_t)c.dim * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)rows}, step[2] = {1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, step,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
 
 cudaError_t launch_attn_tiles(const AttnArgs &p, const AttnPlan &plan, cudaStream_t st)
 {
