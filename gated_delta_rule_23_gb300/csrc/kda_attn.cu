@@ -8,36 +8,77 @@ namespace {
 
 constexpr int ROW_THREADS = 256;
 
-// Joins the partial results of a split call: one warp per query row,
-//   out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s,  M = max m_s,
-// the splits always in order.  A row that does not come out finite is taken again from the definition (see
-// kda_attn_tiles.cu).
-template <int DIM> __global__ void __launch_bounds__(ROW_THREADS) kda_attn_join_kernel(const AttnArgs p, const AttnPlan plan)
+// Joins the partial results of a split call:
+//   out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s,  M = max m_s.
+// PER_ROW warps take a query row, each every PER_ROW-th split, eight splits' loads in flight; the order of the sums is
+// fixed.  The lanes read 32 splits' statistics at once.  A row that does not come out finite is taken again from the
+// definition (see kda_attn_tiles.cu).
+template <int DIM, int PER_ROW>
+__global__ void __launch_bounds__(ROW_THREADS) kda_attn_join_kernel(const AttnArgs p, const AttnPlan plan)
 {
-    constexpr int PER = DIM / 32;
-    const int64_t r = (int64_t)blockIdx.x * (ROW_THREADS / 32) + threadIdx.x / 32;
+    constexpr int PER = DIM / 32, WARPS = ROW_THREADS / 32, FLIGHT = 8;
+    __shared__ float part[WARPS][DIM];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, sub = warp % PER_ROW;
+    const int64_t r = (int64_t)blockIdx.x * (WARPS / PER_ROW) + warp / PER_ROW;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (r >= plan.rows)
-        return;
-    const int lane = threadIdx.x & 31;
+    const bool in = r < plan.rows;
     float m = -INFINITY, l = 0.0f, o[PER];
 #pragma unroll
     for (int e = 0; e < PER; e++)
         o[e] = 0.0f;
-    for (int s = 0; s < plan.splits; s++)
-        m = fmaxf(m, plan.part_ml[s * plan.rows + r].x);
-    const float mu = m == -INFINITY ? 0.0f : m;
-    for (int s = 0; s < plan.splits; s++) {
-        const float2 ml = plan.part_ml[s * plan.rows + r];
-        if (ml.x == -INFINITY && ml.y == 0.0f)
-            continue;                     // a split without a visible key
-        const float w = exp2f(ml.x - mu);
-        const float *src = plan.part_o + (s * plan.rows + r) * DIM + lane * PER;
-        l += w * ml.y;
+    if (in) {
+        for (int s = lane; s < plan.splits; s += 32)
+            m = fmaxf(m, plan.part_ml[s * plan.rows + r].x);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        const float mu = m == -INFINITY ? 0.0f : m;
+        for (int s = lane; s < plan.splits; s += 32) {
+            const float2 ml = plan.part_ml[s * plan.rows + r];
+            if (!(ml.x == -INFINITY && ml.y == 0.0f))         // a split with a visible key
+                l += exp2f(ml.x - mu) * ml.y;
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1)
+            l += __shfl_xor_sync(0xffffffffu, l, x);
+        for (int s0 = sub; s0 < plan.splits; s0 += FLIGHT * PER_ROW) {
+            float v[FLIGHT][PER], w[FLIGHT];
+#pragma unroll
+            for (int i = 0; i < FLIGHT; i++) {
+                const int s = s0 + i * PER_ROW;
+                w[i] = -1.0f;
+                if (s < plan.splits) {
+                    const float2 ml = plan.part_ml[s * plan.rows + r];
+                    if (!(ml.x == -INFINITY && ml.y == 0.0f))
+                        w[i] = exp2f(ml.x - mu);
+                    const float *src = plan.part_o + (s * plan.rows + r) * DIM + lane * PER;
+#pragma unroll
+                    for (int e = 0; e < PER; e++)
+                        v[i][e] = src[e];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < FLIGHT; i++)
+                if (!(w[i] < 0.0f))
+#pragma unroll
+                    for (int e = 0; e < PER; e++)
+                        o[e] = fmaf(w[i], v[i][e], o[e]);
+        }
+    }
+    if (PER_ROW > 1) {
 #pragma unroll
         for (int e = 0; e < PER; e++)
-            o[e] = fmaf(w, src[e], o[e]);
+            part[warp][lane * PER + e] = o[e];
+        __syncthreads();
+        if (sub == 0)
+#pragma unroll
+            for (int i = 1; i < PER_ROW; i++)
+#pragma unroll
+                for (int e = 0; e < PER; e++)
+                    o[e] += part[warp + i][lane * PER + e];
     }
+    if (!in || sub)
+        return;
     bool finite = l <= FLT_MAX;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     __nv_bfloat16 *out = p.out + r * DIM + lane * PER;
@@ -156,7 +197,10 @@ size_t plan_bytes(const AttnPlan &plan, int dim)
 
 cudaError_t launch_attn_join(const AttnArgs &p, const AttnPlan &plan, cudaStream_t st)
 {
-    const unsigned grid = (unsigned)((plan.rows + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32));
+    // few rows with many splits: all of a CTA's warps take one row
+    const bool few = plan.splits > 4 && plan.rows <= 1024;
+    const int per_cta = few ? 1 : ROW_THREADS / 32;
+    const unsigned grid = (unsigned)((plan.rows + per_cta - 1) / per_cta);
     // launched as a programmatic dependent: its CTAs wait for the results themselves
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
@@ -167,8 +211,11 @@ cudaError_t launch_attn_join(const AttnArgs &p, const AttnPlan &plan, cudaStream
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return p.cache.dim == 128 ? cudaLaunchKernelEx(&cfg, kda_attn_join_kernel<128>, p, plan)
-                              : cudaLaunchKernelEx(&cfg, kda_attn_join_kernel<64>, p, plan);
+    if (few)
+        return p.cache.dim == 128 ? cudaLaunchKernelEx(&cfg, kda_attn_join_kernel<128, 8>, p, plan)
+                                  : cudaLaunchKernelEx(&cfg, kda_attn_join_kernel<64, 8>, p, plan);
+    return p.cache.dim == 128 ? cudaLaunchKernelEx(&cfg, kda_attn_join_kernel<128, 1>, p, plan)
+                              : cudaLaunchKernelEx(&cfg, kda_attn_join_kernel<64, 1>, p, plan);
 }
 
 }  // namespace kda
