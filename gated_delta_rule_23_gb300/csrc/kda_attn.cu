@@ -110,6 +110,8 @@ kda_status_t check_attn(const void *q, int64_t q_stride, const void *k_cache, co
         return s;
     if (Hq < 1 || Hq % Hkv || window < 1 || sinks < 0)
         return KDA_ERR_INVALID_ARGUMENT;
+    if (Hq / Hkv > ATTN_ROWS)
+        return KDA_ERR_UNSUPPORTED;
     if (!(scale >= 0.0f) || scale > 3.0e38f)
         return KDA_ERR_UNSUPPORTED;
     const int64_t tokens = cu_seqlens ? T : (int64_t)N * T;
@@ -173,10 +175,11 @@ AttnPlan make_plan(int window, int sinks, bool varlen, int N, int64_t T, int Hq,
         return plan;
     }
     plan.granule = page < 32 ? page : 32;
-    int64_t tiles = varlen ? (T * group + (int64_t)(ATTN_ROWS - 1) * N) / ATTN_ROWS
-                           : (int64_t)N * ((T * group + ATTN_ROWS - 1) / ATTN_ROWS);
-    if (varlen && tiles > T * group)
-        tiles = T * group;                // a tile holds a row at least
+    plan.run = ATTN_ROWS / group;
+    plan.magic = ((1u << 20) + group - 1) / group;
+    int64_t tiles = varlen ? (T + (int64_t)(plan.run - 1) * N) / plan.run : (int64_t)N * ((T + plan.run - 1) / plan.run);
+    if (varlen && tiles > T)
+        tiles = T;                        // a tile holds a token at least
     const int64_t ctas = tiles * Hkv;
     const int64_t key_tiles = (most_keys(window, sinks, T < ATTN_ROWS ? T : ATTN_ROWS, page, max_pages) + 127) / 128 + 1;
     int64_t s = ctas > 0 ? sms / ctas : 1;
@@ -226,7 +229,8 @@ extern "C" size_t kda_window_attn_workspace_size(int window, int sinks, int varl
                                                  int D, int page, int max_pages)
 {
     if (window < 1 || sinks < 0 || N < 1 || T < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv || (D != 64 && D != 128) || page < 16 ||
-        max_pages < 1 || T > INT32_MAX || (varlen ? T : (int64_t)N * T) * Hq > INT32_MAX)
+        max_pages < 1 || T > INT32_MAX || (varlen ? T : (int64_t)N * T) > INT32_MAX / Hq ||
+        Hq / Hkv > ATTN_ROWS)
         return 0;
     return plan_bytes(make_plan(window, sinks, varlen != 0, N, T, Hq, Hkv, page, max_pages), D);
 }

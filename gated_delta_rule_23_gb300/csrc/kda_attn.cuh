@@ -21,7 +21,7 @@ struct AttnArgs {
 };
 
 // How a call is cut: every (sequence, key head) has group x Q_n query rows, row r being token r / group and head
-// r % group of the group (so that heads sharing keys share a tile); rows come in tiles, and the keys a tile needs are
+// r % group of the group (so that heads sharing keys share a tile); rows come in tiles of whole tokens, and the keys a tile needs are
 // split `splits` ways, the partial results joined by a second kernel when there is more than one.
 constexpr int ATTN_ROWS = 256;   // query rows of a tile
 constexpr int DECODE_ROWS = 16, DECODE_KEYS = 16;   // rows of the decode kernel, keys of its blocks
@@ -31,6 +31,8 @@ struct AttnPlan {
     int splits;
     int items;              // (row tile, key head, split) items (ragged: an upper bound)
     int granule;            // positions of a cache page that are copied together
+    int run;                // tokens of an item
+    uint32_t magic;         // ceil(2^20 / group)
     float *part_o;          // [splits][tokens * hq][dim] fp32, unnormalised (workspace)
     float2 *part_ml;        // [splits][tokens * hq]: running maximum (base 2) and sum
     int64_t rows;           // tokens * hq

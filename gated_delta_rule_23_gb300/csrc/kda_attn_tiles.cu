@@ -1,9 +1,9 @@
 // Windowed attention over the paged cache on the tensor cores: 256 query rows a CTA, keys in tiles of 128.
 //
-// Rows.  A CTA owns rows [256 x, 256 x + 256) of one (sequence, key head), in two halves of 128 (row = token * group
-// + head of the group, so heads that share keys share the tile).  Keys.  The tile's rows need the sinks and the
-// positions from the first row's window on: two ranges of positions, cut into granules of at most 32 positions that
-// lie in one page each, and strung together to a list of "virtual" keys; 4 to 8 granules make a key tile, so a few
+// Rows.  An item is a run of 256 / group tokens of a (sequence, key head) with all heads of the group: up to 256 rows (row
+// = token * group + head, so heads that share keys share the tile), in two halves of 128.  Keys.  The rows need the sinks
+// and the positions from the first row's window on: two ranges of positions, cut into granules of at most 32 positions
+// that lie in one page each, and strung together to a list of "virtual" keys; 4 to 8 granules make a key tile, so a few
 // sinks cost a granule and not a tile.  Granules past the end are loaded from outside the cache (zeros).
 //
 // Per half and 64 keys (half a key tile):  S = Q K^T (tcgen05, fp32 in tensor memory);  P = 2^(scale S - m) with one
@@ -17,10 +17,12 @@
 // maximum: they are taken with the m at hand while the maximum is formed, and taken again (S still stands; P is stored
 // last) in the rare tile that moves m.
 //
-// Warps 0..3 and 4..7: the halves' softmax and epilogue; warp 8: bulk tensor copies (K and V tiles in a ring); warps 9
+// Warps 0..3 and 4..7: the halves' softmax and epilogue; warp 8: bulk tensor copies of K and V tiles into a ring; warps 9
 // and 10: tensor-core issue for a half each (one thread for both halves spent longer issuing than the tensor cores took:
-// 1918 us at 8192 tokens, 96 heads).  One CTA an SM walks the (row tile, key head, split) items: the copies run ahead into the next
-// item, its Q is loaded and its first S formed while the last item's rows are scaled and stored.
+// 1918 us at 8192 tokens, 96 heads); warp 11: works out the items and brings in their Q.  One CTA an SM walks the (row
+// tile, key head, split) items: copies and first S of the next item run while the last one's rows are scaled and stored.
+// (When every warp worked out the items for itself and the softmax warps loaded Q, an item of 9 steps spent 13,000 cycles
+// between them and 16,000 in them.)
 //
 // A key that a row does not see gets P = 0.  0 x v is NaN for an infinite or NaN v, and the matrix product has no way
 // to skip it: rows past the sequence's end are cleared in shared memory, and an output row that does not come out
@@ -34,14 +36,11 @@ namespace kda {
 namespace {
 
 constexpr int KEYS = 128, SUB = 64;          // keys of a tile, and of a step of the softmax
-constexpr int THREADS = 384;                 // three warpgroups (the last warp has no role)
-// Registers a thread: 168 at launch (65,536 / 384); the softmax warpgroups, which hold a row of S, take what the third gives
-// back: 2 x 128 x 208 + 128 x 88 = 384 x 168.
-constexpr int REGS_SOFTMAX = 208, REGS_REST = 88;
-static_assert(2 * 128 * REGS_SOFTMAX + 128 * REGS_REST <= THREADS * 168, "register split");
+constexpr int THREADS = 384;                 // three warpgroups
 constexpr int HALF = 128;                    // rows of a half
 constexpr int TMEM_COLS = 512;
 constexpr int TM_S = 0, TM_O = 256;          // columns: two S a half (64 each), O of both halves
+constexpr int ITEMS = 4;                      // items worked out ahead
 constexpr float RESCALE_AT = 8.0f;           // base-2 growth of the maximum that moves it
 constexpr unsigned FULL = 0xffffffffu;
 
@@ -50,14 +49,16 @@ template <int DIM> struct Shape {
     static constexpr int Q = HALF * DIM * 2;                 // of a half's Q
     static constexpr int SLOTS = DIM == 128 ? 5 : 10;        // ring: K0 V0 K1 V1 ...
     static constexpr int BAR = 2 * Q + SLOTS * TILE;         // mbarriers behind Q and the ring
-    static constexpr int SMEM = 1024 + BAR + 512;            // 1024: alignment of the swizzle atoms
+    static constexpr int SMEM = 1024 + BAR + 768;            // 1024: alignment of the swizzle atoms
 };
 
 struct Tile {             // one item; positions, rows and tokens fit 32 bits (checked on the host)
+    int valid;            // 0: no more items
     int n, kvh, split;
-    int len_q, bos;       // tokens of the sequence, first token of it in the batch
-    int len;              // its tokens in the cache
-    int row0, rows;       // first row of the tile, rows of it (1..256)
+    int len;              // tokens of the sequence in the cache
+    int tok0;             // first token of the item in the batch
+    int pos0;             // its position
+    int rows;             // rows of the item, 1..256
     int sink_span;        // virtual keys of the sinks (a multiple of the granule)
     int start;            // position of virtual key sink_span
     int virt;             // virtual keys in all
@@ -67,29 +68,35 @@ struct Tile {             // one item; positions, rows and tokens fit 32 bits (c
 
 __device__ __forceinline__ int virt_pos(const Tile &w, int v) { return v < w.sink_span ? v : v - w.sink_span + w.start; }
 
-// Position of row r (of the sequence).
-__device__ __forceinline__ int row_pos(const AttnArgs &p, const Tile &w, int r) { return w.len - w.len_q + r / p.group; }
+// r / group for a row r < 256 of an item (plan.magic = ceil(2^20 / group), group <= 256: exact)
+__device__ __forceinline__ int token_of(const AttnPlan &plan, int r) { return (int)(((uint32_t)r * plan.magic) >> 20); }
 
-// Fills in item x; false when there is none (ragged batches have fewer tiles than the bound the grid is made for).  By a
+// Works out item x; not valid when there is none (ragged batches have fewer than the bound the grid is made for).  By a
 // whole warp.
-__device__ __forceinline__ bool find_tile(const AttnArgs &p, const AttnPlan &plan, int x, Tile &w, bool &bad)
+__device__ __forceinline__ void find_tile(const AttnArgs &p, const AttnPlan &plan, int x, Tile &w, bool &bad)
 {
     const int lane = threadIdx.x & 31;
+    w.valid = 0;
+    if (x >= plan.items)
+        return;
     // heaviest first where the work grows along a sequence: the last tiles of all key heads
     w.kvh = x % p.cache.hkv;
     x /= p.cache.hkv;
-    w.split = x % plan.splits;
-    x /= plan.splits;
-    int tile = 0;
+    w.split = 0;
+    if (plan.splits > 1) {
+        w.split = x % plan.splits;
+        x /= plan.splits;
+    }
+    const int run = plan.run;                       // tokens of an item
+    int tile = 0, len_q = 0, bos = 0;
     if (p.tok.cu) {
         int before = 0;
-        bool found = false;
-        for (int base = 0; base < p.tok.N && !found; base += 32) {
+        for (int base = 0; base < p.tok.N; base += 32) {
             const int n = base + lane;
-            int64_t bos = 0, len = 0;
+            int64_t from = 0, len = 0;
             if (n < p.tok.N)
-                bad |= seq_range(p.tok.cu, n, p.tok.N, p.tok.T, bos, len);
-            const int cnt = (int)((len * p.group + ATTN_ROWS - 1) / ATTN_ROWS);
+                bad |= seq_range(p.tok.cu, n, p.tok.N, p.tok.T, from, len);
+            const int cnt = ((int)len + run - 1) / run;
             int sum = cnt;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -101,30 +108,33 @@ __device__ __forceinline__ bool find_tile(const AttnArgs &p, const AttnPlan &pla
             if (m) {
                 const int src = __ffs(m) - 1;
                 w.n = base + src;
-                w.bos = __shfl_sync(FULL, (int)bos, src);
-                w.len_q = __shfl_sync(FULL, (int)len, src);
+                bos = __shfl_sync(FULL, (int)from, src);
+                len_q = __shfl_sync(FULL, (int)len, src);
                 tile = x - (before + __shfl_sync(FULL, sum - cnt, src));
-                found = true;
+                w.valid = 1;
+                break;
             }
             before += __shfl_sync(FULL, sum, 31);
         }
-        if (!found)
-            return false;
+        if (!w.valid)
+            return;
     } else {
-        const int per = (int)((p.tok.T * p.group + ATTN_ROWS - 1) / ATTN_ROWS);
+        len_q = (int)p.tok.T;
+        const int per = (len_q + run - 1) / run;
         w.n = x % p.tok.N;
         tile = per - 1 - x / p.tok.N;
-        w.len_q = (int)p.tok.T;
-        w.bos = (int)(w.n * p.tok.T);
+        bos = w.n * len_q;
+        w.valid = 1;
     }
-    w.row0 = tile * ATTN_ROWS;
-    w.rows = min(w.len_q * p.group - w.row0, ATTN_ROWS);
+    const int count = min(len_q - tile * run, run);  // tokens of the item
+    w.rows = count * p.group;
+    w.tok0 = bos + tile * run;
     w.len = (int)cache_len(p.cache, w.n, bad);
-    const int g = plan.granule;
-    const int p0 = row_pos(p, w, w.row0), p1 = row_pos(p, w, w.row0 + w.rows - 1);
+    w.pos0 = w.len - len_q + tile * run;
+    const int g = plan.granule, p1 = w.pos0 + count - 1;
     w.sink_span = w.start = w.virt = 0;
     if (p1 >= 0) {                                  // else all rows are before the first token
-        int lo = max(p0 - p.window + 1, 0) & -g, sink = (p.sinks + g - 1) & -g;
+        int lo = max(w.pos0 - p.window + 1, 0) & -g, sink = (p.sinks + g - 1) & -g;
         if (lo <= sink)
             sink = lo = 0;                          // one range
         w.sink_span = sink;
@@ -132,8 +142,12 @@ __device__ __forceinline__ bool find_tile(const AttnArgs &p, const AttnPlan &pla
         w.virt = sink + (p1 + 1 - lo);
     }
     const int tiles = (w.virt + KEYS - 1) / KEYS;
-    w.t0 = (int)((int64_t)tiles * w.split / plan.splits);
-    w.t1 = (int)((int64_t)tiles * (w.split + 1) / plan.splits);
+    w.t0 = 0;
+    w.t1 = tiles;
+    if (plan.splits > 1) {
+        w.t0 = (int)((int64_t)tiles * w.split / plan.splits);
+        w.t1 = (int)((int64_t)tiles * (w.split + 1) / plan.splits);
+    }
 #pragma unroll
     for (int h = 0; h < 2; h++) {
         const int first = h * HALF, last = min(w.rows, first + HALF) - 1;
@@ -141,7 +155,7 @@ __device__ __forceinline__ bool find_tile(const AttnArgs &p, const AttnPlan &pla
         w.lo[h] = w.hi[h] = s0;
         if (first > last)
             continue;
-        const int a = row_pos(p, w, w.row0 + first) - p.window + 1, b = row_pos(p, w, w.row0 + last);
+        const int a = w.pos0 + token_of(plan, first) - p.window + 1, b = w.pos0 + token_of(plan, last);
         if (b < 0)
             continue;
         // the half's window, in steps; with sinks a half needs the steps from the first on
@@ -150,7 +164,6 @@ __device__ __forceinline__ bool find_tile(const AttnArgs &p, const AttnPlan &pla
         w.lo[h] = min(max(lo, s0), s1);
         w.hi[h] = max(min(max(hi, s0), s1), w.lo[h]);
     }
-    return true;
 }
 
 // ---------------------------------------------------------------- tensor cores and copies
@@ -189,6 +202,12 @@ template <bool ACC> __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t 
                      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}"
                      ::"r"(d), "r"(a_tmem), "r"(b), "r"(idesc), "r"(DESC_HI), "r"(acc) : "memory");
 }
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t mbar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(mbar) : "memory");
+}
+
 // 32 columns of the warp's 32 lanes, one row a thread: the load, and the wait for it, which names the registers so that
 // nothing that uses them moves before it
 #define REGS8(k, a, i) k(a[i]), k(a[i + 1]), k(a[i + 2]), k(a[i + 3]), k(a[i + 4]), k(a[i + 5]), k(a[i + 6]), k(a[i + 7])
@@ -239,26 +258,10 @@ __device__ __forceinline__ uint32_t range_word(int a, int b, int w)
     return x & y;
 }
 
-// Q rows of item w's half into shared memory (not waited for): a warp loads its own 32 rows, lanes along a row; rows past
-// the end are zeros.
-template <int DIM> __device__ __forceinline__ void load_q(const AttnArgs &p, const Tile &w, uint32_t sm_q, int warp, int lane)
-{
-    constexpr int C = DIM / 8;                   // 16-byte vectors of a row
-    const int c = lane % C;
-    for (int i = lane / C; i < 32; i += 32 / C) {
-        const int row = i + 32 * warp, rh = row & (HALF - 1);
-        const bool in = row < w.rows;
-        const int R = w.row0 + (in ? row : 0);
-        const __nv_bfloat16 *src = p.q + (int64_t)(w.bos + R / p.group) * p.q_stride + (w.kvh * p.group + R % p.group) * DIM + c * 8;
-        cp_async16(sm_q + (warp / 4) * Shape<DIM>::Q + (c / 8) * (HALF * 128) + rh * 128 + (((c & 7) ^ (rh & 7)) << 4), src, in);
-    }
-    cp_async_commit();
-}
-
 template <int DIM>
 __global__ void __launch_bounds__(THREADS, 1)
 kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_constant__ CUtensorMap kmap,
-                      const __grid_constant__ CUtensorMap vmap)
+                      const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap)
 {
     using S = Shape<DIM>;
     constexpr int CB = DIM / 64;                 // 64-column blocks of a row
@@ -266,24 +269,31 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char *const smem = smem_raw + (base - smem_u32(smem_raw));
     const uint32_t sm_q = base, sm_ring = base + 2 * S::Q, bar = base + S::BAR;
-    const uint32_t b_full = bar, b_empty = bar + 8 * S::SLOTS, b_q = b_empty + 8 * S::SLOTS, b_s = b_q + 16, b_p = b_s + 32,
-                   b_o = b_p + 32, b_drain = b_o + 32;     // S, P, P V: [half][buffer]; drain: [half]
+    const uint32_t b_full = bar, b_empty = bar + 8 * S::SLOTS, b_q = b_empty + 8 * S::SLOTS, b_q_free = b_q + 8,
+                   b_s = b_q_free + 8, b_p = b_s + 32, b_o = b_p + 32, b_drain = b_o + 32,  // S, P, P V: [half][buffer]
+                   b_item = b_drain + 16, b_item_free = b_item + 8 * ITEMS;
+    __shared__ Tile item_ring[ITEMS];
     __shared__ uint32_t tmem_slot;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
-    const int items = plan.items, g = plan.granule;
+    const int g = plan.granule;
     if (tid == 0) {
         for (int i = 0; i < S::SLOTS; i++) {
             mbar_init(b_full + 8 * i, 1);
             mbar_init(b_empty + 8 * i, 2);
         }
         for (int h = 0; h < 2; h++) {
-            mbar_init(b_q + 8 * h, 4);
             for (int i = 0; i < 2; i++) {
                 mbar_init(b_s + 16 * h + 8 * i, 1);
                 mbar_init(b_p + 16 * h + 8 * i, 4);
                 mbar_init(b_o + 16 * h + 8 * i, 1);
             }
             mbar_init(b_drain + 8 * h, 1);
+        }
+        mbar_init(b_q, 1);
+        mbar_init(b_q_free, 2);
+        for (int i = 0; i < ITEMS; i++) {
+            mbar_init(b_item + 8 * i, 1);
+            mbar_init(b_item_free + 8 * i, 11);      // every warp but the one that writes
         }
         mbar_fence_init();
     }
@@ -297,10 +307,28 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     bool timeout = false, bad = false;
+    // Waits of a whole warp: every lane polls and the warp votes, so that it stays converged.  (One lane polling for the
+    // others let the compiler keep the warp split behind the wait, and everything after it ran twice: 2420 us instead of
+    // 1290 at 8192 tokens, 96 heads.)  Once a wait of the warp has given up, the later ones do at once.
+    auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+        if (__any_sync(FULL, !mbar_wait(b, parity, timeout ? 1 : plan.wait_polls)))
+            timeout = true;
+        return !timeout;
+    };
+    // The i-th item of this CTA, read by a whole warp; false when there is none or the wait gave up.
+    auto next_item = [&](int i, Tile &w) -> bool {
+        const int slot = i % ITEMS;
+        if (!wait(b_item + 8 * slot, (i / ITEMS) & 1))
+            return false;
+        w = item_ring[slot];
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(b_item_free + 8 * slot);
+        return w.valid != 0;
+    };
 
     if (warp < 8) {
-        // ------------------------------------------------------------ Q, softmax, epilogue
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
+        // ------------------------------------------------------------ softmax, epilogue
         const int h = warp / 4;
         const uint32_t tm_lane = (uint32_t)(warp & 3) << 21;     // the warp's 32 lanes
         const uint32_t tm_s0 = tmem + TM_S + h * 128 + tm_lane, tm_o = tmem + TM_O + h * 128 + tm_lane;
@@ -308,38 +336,24 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
         // Phases of the two S, and of the P V of an item's last two key tiles, the only ones that are waited for as such: a
         // half's S of tile t + 1 is issued right after its P V of tile t - 1.
         uint32_t s_phase = 0, o_phase = 0;
-        Tile w{};
-        int x = blockIdx.x;
-        bool have = x < items && find_tile(p, plan, x, w, bad);
-        auto q_ready = [&]() {                                   // the warp's Q rows are in shared memory
-            cp_async_wait_all();
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(b_q + 8 * h);
-        };
-        if (have && w.hi[h] > w.lo[h]) {
-            load_q<DIM>(p, w, sm_q, warp, lane);
-            q_ready();
-        }
-        while (have) {
+        Tile w;
+        for (int i = 0; next_item(i, w); i++) {
             const bool mine = tid < w.rows;
-            const int R = w.row0 + tid;
-            const int tok = w.bos + (mine ? R / p.group : 0), head = w.kvh * p.group + (mine ? R % p.group : 0);
-            const int pos = mine ? row_pos(p, w, R) : -1, split = w.split, n = w.n;
+            const int r_tok = mine ? token_of(plan, tid) : 0;
+            const int tok = w.tok0 + r_tok, head = w.kvh * p.group + (mine ? tid - r_tok * p.group : 0);
+            const int pos = mine ? w.pos0 + r_tok : -1;
+            const int lo = h ? w.lo[1] : w.lo[0], hi = h ? w.hi[1] : w.hi[0];
             float m = -INFINITY, l = 0.0f;
             bool any = false;
-            for (int t = w.lo[h]; t < w.hi[h]; t++) {
+            for (int t = lo; t < hi; t++) {
                 const int v0 = t * SUB;
                 // the sequence's end inside the step: what lies behind it in its page is cleared from V (K's scores are
                 // masked)
                 const int end_v = w.len - w.start + w.sink_span - v0;
                 if (end_v > 0 && end_v < SUB && (end_v & (g - 1))) {
                     const int it = 2 * (ring + t / 2 - w.t0) + 1, slot = it % S::SLOTS;
-                    if (!mbar_wait(b_full + 8 * slot, (it / S::SLOTS) & 1, plan.wait_polls)) {
-                        timeout = true;
+                    if (!wait(b_full + 8 * slot, (it / S::SLOTS) & 1))
                         break;
-                    }
                     const int count = (g - (end_v & (g - 1))) * 8;       // 16-byte vectors of a column block
                     uint4 *v = reinterpret_cast<uint4 *>(smem + 2 * S::Q + slot * S::TILE) + ((t & 1) * SUB + end_v) * 8;
                     for (int i = tid & (HALF - 1); i < count * CB; i += HALF)
@@ -348,12 +362,8 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                 }
                 const int buf = t & 1;
                 const uint32_t tm_s = tm_s0 + 64 * buf;
-                if (lane == 0 && !mbar_wait(b_s + 16 * h + 8 * buf, s_phase >> buf & 1, plan.wait_polls))
-                    timeout = true;
-                if (__any_sync(FULL, timeout)) {
-                    timeout = true;
+                if (!wait(b_s + 16 * h + 8 * buf, s_phase >> buf & 1))
                     break;
-                }
                 s_phase ^= 1u << buf;
                 tc_fence_after();
                 // columns of the tile that the row sees: the window's, and the sinks'
@@ -428,9 +438,9 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                     if (any) {
                         // the P V before this one has to be through (the ones before it are: this S came after them)
                         const uint32_t other = buf ^ 1;
-                        if (!mbar_wait(t + 1 < w.hi[h] ? b_s + 16 * h + 8 * other : b_o + 16 * h + 8 * other,
-                                       (t + 1 < w.hi[h] ? s_phase : o_phase) >> other & 1, plan.wait_polls))
-                            timeout = true;
+                        if (!wait(t + 1 < hi ? b_s + 16 * h + 8 * other : b_o + 16 * h + 8 * other,
+                                  (t + 1 < hi ? s_phase : o_phase) >> other & 1))
+                            break;
                         tc_fence_after();
 #pragma unroll
                         for (int c = 0; c < DIM; c += 32) {
@@ -455,31 +465,16 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                 if (lane == 0)
                     mbar_arrive(b_p + 16 * h + 8 * buf);
             }
-            if (__any_sync(FULL, timeout)) {
-                timeout = true;
+            if (timeout)
                 break;
-            }
-            // The next item's Q: the half's last S is formed, so its Q rows are free.
-            const bool stored = any;
-            const int steps = w.hi[h] - w.lo[h], last_buf = (w.hi[h] - 1) & 1;
             ring += w.t1 - w.t0;
-            x += gridDim.x;
-            have = x < items && find_tile(p, plan, x, w, bad);
-            const bool more = have && w.hi[h] > w.lo[h];
-            if (more)
-                load_q<DIM>(p, w, sm_q, warp, lane);
-            if (stored) {
+            if (any) {
                 // the last P V: those before it are through with it
-                if (!mbar_wait(b_o + 16 * h + 8 * last_buf, o_phase >> last_buf & 1, plan.wait_polls))
-                    timeout = true;
-                o_phase ^= steps > 1 ? 3 : 1u << last_buf;
+                const int last_buf = (hi - 1) & 1;
+                o_phase ^= hi - lo > 1 ? 3 : 1u << last_buf;
+                if (!wait(b_o + 16 * h + 8 * last_buf, (o_phase >> last_buf & 1) ^ 1))
+                    break;
                 tc_fence_after();
-            }
-            if (more)
-                q_ready();
-            if (__any_sync(FULL, timeout)) {
-                timeout = true;
-                break;
             }
             // epilogue: the row's thread scales and stores it
             bool finite = l <= FLT_MAX;
@@ -489,20 +484,20 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
 #pragma unroll
             for (int c = 0; c < DIM; c += 32) {
                 float o[32];
-                if (stored) {
+                if (any) {
                     tmem_get32(tm_o + c, o);
                     tmem_wait32(o);
                 }
 #pragma unroll
                 for (int e = 0; e < 32; e++) {
-                    const float y = stored ? o[e] : 0.0f;
+                    const float y = any ? o[e] : 0.0f;
                     finite &= fabsf(y) <= FLT_MAX;
                     o[e] = part || l != 0.0f ? y * inv : 0.0f;
                 }
                 if (!mine)
                     continue;
                 if (part) {
-                    float4 *dst = reinterpret_cast<float4 *>(plan.part_o + (split * plan.rows + at) * DIM + c);
+                    float4 *dst = reinterpret_cast<float4 *>(plan.part_o + (w.split * plan.rows + at) * DIM + c);
 #pragma unroll
                     for (int e = 0; e < 8; e++)
                         dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
@@ -522,7 +517,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             }
             tc_fence_before();                // O is read before the next item's first P lets it be overwritten
             if (mine && part)
-                plan.part_ml[split * plan.rows + at] = make_float2(m, l);
+                plan.part_ml[w.split * plan.rows + at] = make_float2(m, l);
             else if (mine && p.lse)
                 p.lse[at] = l == 0.0f ? -INFINITY : LN2 * (m + log2f(l));
             unsigned again = __ballot_sync(FULL, mine && !finite && !part);
@@ -530,19 +525,16 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                 __syncwarp();                 // the rows' first stores come before the ones below
                 for (; again; again &= again - 1) {
                     const int src = __ffs(again) - 1;
-                    attn_row<DIM>(p, n, __shfl_sync(FULL, tok, src), __shfl_sync(FULL, head, src), __shfl_sync(FULL, pos, src), bad);
+                    attn_row<DIM>(p, w.n, __shfl_sync(FULL, tok, src), __shfl_sync(FULL, head, src), __shfl_sync(FULL, pos, src), bad);
                 }
             }
         }
-    } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
-    }
-    if (warp == 8) {
+    } else if (warp == 8) {
         // ------------------------------------------------------------ copies
         const int ng = KEYS / g;
         int issued = 0;
         Tile w;
-        for (int x = blockIdx.x; x < items && !timeout && find_tile(p, plan, x, w, bad); x += gridDim.x) {
+        for (int i = 0; !timeout && next_item(i, w); i++) {
             for (int t = w.t0; t < w.t1 && !timeout; t++) {
                 int y = OUTSIDE;
                 if (lane < ng) {
@@ -558,12 +550,8 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
 #pragma unroll
                 for (int kv = 0; kv < 2; kv++) {
                     const int slot = issued % S::SLOTS;
-                    if (issued >= S::SLOTS && !mbar_wait(b_empty + 8 * slot, (issued / S::SLOTS - 1) & 1, plan.wait_polls))
-                        timeout = true;
-                    if (__any_sync(FULL, timeout)) {
-                        timeout = true;
+                    if (issued >= S::SLOTS && !wait(b_empty + 8 * slot, (issued / S::SLOTS - 1) & 1))
                         break;
-                    }
                     if (lane == 0)
                         mbar_expect_tx(b_full + 8 * slot, S::TILE);
                     __syncwarp();
@@ -582,25 +570,18 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             mbar_wait(b_full + 8 * (it % S::SLOTS), (it / S::SLOTS) & 1);
     } else if (warp == 9 || warp == 10) {
         // ------------------------------------------------------------ tensor-core issue, warp 9 for half 0, 10 for half 1
-        // The warp walks the items; one elected lane waits and issues.  What an instruction needs (descriptors, addresses)
-        // is the same in all lanes and known to be, so that it is formed in uniform registers: issuing from one thread's
-        // own registers took some 80 cycles a product.  Once a wait has given up, nothing more is issued.
+        // The warp walks the items and waits; one elected lane issues.  What an instruction needs (descriptors, addresses) is
+        // the same in all lanes and known to be, so that it is formed in uniform registers: issuing from one thread's own
+        // registers took some 80 cycles a product.  Once a wait has given up, nothing more is issued.
         const int h = __shfl_sync(FULL, warp, 0) - 9;
         const uint32_t id_s = idesc_bf16(HALF, SUB, false), id_o = idesc_bf16(HALF, DIM, true);
         const uint32_t tm = __shfl_sync(FULL, tmem, 0), lead = elect_one();
-        const uint32_t q_lo = desc_lo(sm_q + h * S::Q, 16), k_lo = desc_lo(sm_ring, 16), v_lo = desc_lo(sm_ring, KEYS * 128);
+        const uint32_t q_lo = desc_lo(sm_q + h * (HALF * 128), 16), k_lo = desc_lo(sm_ring, 16), v_lo = desc_lo(sm_ring, KEYS * 128);
         uint32_t p_phase = 0, q_phase = 0;
         uint32_t ks = 0, kp = 0, vs = 1, vp = 0;                 // next K's and next V's slot, and its phase
-        Tile w{};
-        auto wait = [&](uint32_t b, uint32_t parity) {
-            if (lead && !timeout && !mbar_wait(b, parity, plan.wait_polls))
-                timeout = true;
-            __syncwarp();
-        };
-        for (int x = blockIdx.x; x < items && find_tile(p, plan, x, w, bad); x += gridDim.x) {
-            // uniform copies
-            const int t0 = __shfl_sync(FULL, w.t0, 0), t1 = __shfl_sync(FULL, w.t1, 0);
-            const int lo = __shfl_sync(FULL, h ? w.lo[1] : w.lo[0], 0), hi = __shfl_sync(FULL, h ? w.hi[1] : w.hi[0], 0);
+        Tile w;
+        for (int i = 0; next_item(i, w); i++) {
+            const int t0 = w.t0, t1 = w.t1, lo = h ? w.lo[1] : w.lo[0], hi = h ? w.hi[1] : w.hi[0];
             // step by step P V of key tile t - 1, then S of tile t into the buffer that P came from
             for (int t = t0; t <= t1; t++) {
                 const bool pv = t > t0, sk = t < t1;
@@ -628,17 +609,15 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                     if (sk && buf == 0)
                         wait(b_full + 8 * ks, kp);
                     if (sk && now >= lo && now < hi) {
-                        if (now == lo) {
-                            wait(b_q + 8 * h, q_phase);
-                            q_phase ^= 1;
-                        }
+                        if (now == lo)
+                            wait(b_q, q_phase);
                         tc_fence_after();
                         const uint32_t b = k_lo + ks * (S::TILE >> 4) + buf * (SUB * 128 >> 4), d = tm + TM_S + h * 128 + 64 * buf;
                         if (lead && !timeout) {
                             mma_ss<false>(d, q_lo, b, id_s, 0);
 #pragma unroll
                             for (int k = 1; k < DIM / 16; k++)
-                                mma_ss<true>(d, q_lo + (((k / 4) * (HALF * 128) + (k % 4) * 32) >> 4),
+                                mma_ss<true>(d, q_lo + (((k / 4) * (2 * HALF * 128) + (k % 4) * 32) >> 4),
                                              b + (((k / 4) * (KEYS * 128) + (k % 4) * 32) >> 4), id_s, 1);
                             umma_commit(b_s + 16 * h + 8 * buf);
                         }
@@ -650,6 +629,8 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                         umma_commit(b_empty + 8 * vs);
                     if (sk)
                         umma_commit(b_empty + 8 * ks);
+                    if (t == max(t1 - 1, t0))
+                        umma_commit(b_q_free);                   // and with Q
                 }
                 __syncwarp();
                 if (pv && (vs += 2) >= S::SLOTS)
@@ -657,6 +638,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                 if (sk && (ks += 2) >= S::SLOTS)
                     ks -= S::SLOTS, kp ^= 1;
             }
+            q_phase ^= 1;
         }
         if (lead) {
             // everything issued has to be through before tensor memory is freed
@@ -664,6 +646,34 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             mbar_wait(b_drain + 8 * h, 0);
         }
         __syncwarp();
+    } else if (warp == 11) {
+        // ------------------------------------------------------------ items and their Q
+        int loaded = 0;
+        for (int i = 0;; i++) {
+            const int slot = i % ITEMS;
+            Tile w;
+            find_tile(p, plan, blockIdx.x + i * gridDim.x, w, bad);
+            if (i >= ITEMS && !wait(b_item_free + 8 * slot, (i / ITEMS - 1) & 1))
+                break;
+            if (lane == 0) {
+                item_ring[slot] = w;
+                mbar_arrive(b_item + 8 * slot);
+            }
+            if (!w.valid)
+                break;
+            // Q is free when both halves' last S of the item before is formed
+            if (i > 0 && !wait(b_q_free, (i - 1) & 1))
+                break;
+            if (lane == 0) {
+                mbar_expect_tx(b_q, (uint32_t)(CB * 128 * plan.run * p.group));
+#pragma unroll
+                for (int cb = 0; cb < CB; cb++)
+                    tma_load_3d(sm_q + cb * (2 * HALF * 128), &qmap, cb * 64, w.kvh * p.group, w.tok0, b_q);
+            }
+            loaded++;
+        }
+        if (loaded > 0)                              // no copy is in flight when the CTA leaves
+            mbar_wait(b_q, (loaded - 1) & 1);
     }
     report(p.err, bad, DEVERR_CU_SEQLENS);
     report(p.err, timeout, DEVERR_TIMEOUT);
@@ -695,6 +705,22 @@ cudaError_t encode_fn(EncodeTiled *fn)
     return cudaSuccess;
 }
 
+// Q as [tokens][hq][dim]; a box is 64 columns of an item's tokens and heads.
+cudaError_t query_map(CUtensorMap *map, const AttnArgs &p, const AttnPlan &plan)
+{
+    EncodeTiled fn;
+    const cudaError_t e = encode_fn(&fn);
+    if (e != cudaSuccess)
+        return e;
+    const cuuint64_t dims[3] = {(cuuint64_t)p.cache.dim, (cuuint64_t)p.hq, (cuuint64_t)(plan.rows / p.hq)};
+    const cuuint64_t strides[2] = {(cuuint64_t)p.cache.dim * 2, (cuuint64_t)p.q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.group, (cuuint32_t)plan.run}, step[3] = {1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16 *>(p.q), dims, strides, box, step,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <int DIM> cudaError_t launch_tiles(const AttnArgs &p, const AttnPlan &plan, cudaStream_t st)
 {
     static std::atomic<uint64_t> ready;      // devices whose kernel attribute is set
@@ -705,18 +731,20 @@ template <int DIM> cudaError_t launch_tiles(const AttnArgs &p, const AttnPlan &p
         if (e == cudaSuccess)
             ready.fetch_or(1ull << dev);
     }
-    CUtensorMap kmap, vmap;
+    CUtensorMap kmap, vmap, qmap;
     if (e == cudaSuccess)
         e = cache_map(&kmap, p.cache.k, p.cache, plan.granule);
     if (e == cudaSuccess)
         e = cache_map(&vmap, p.cache.v, p.cache, plan.granule);
+    if (e == cudaSuccess)
+        e = query_map(&qmap, p, plan);
     if (e != cudaSuccess)
         return e;
     const int sms = device_sms();
     const int grid = plan.items < sms ? plan.items : sms;
     if (grid < 1)
         return cudaErrorInvalidValue;
-    kda_attn_tiles_kernel<DIM><<<grid, THREADS, Shape<DIM>::SMEM, st>>>(p, plan, kmap, vmap);
+    kda_attn_tiles_kernel<DIM><<<grid, THREADS, Shape<DIM>::SMEM, st>>>(p, plan, kmap, vmap, qmap);
     return cudaGetLastError();
 }
 

@@ -419,8 +419,8 @@ kda_status_t kda_kv_append(const void *k, int64_t k_stride, const void *v, int64
  * a query that sees no key gets out = 0 and lse = -inf.  What lies in keys and values that a query does
  * not see (stale rows, infinities, NaN) does not reach its output.
  *
- *   q              bf16 [B, T, Hq, D], tokens q_stride elements apart; Hq a multiple of Hkv: query head h
- *                  reads key head h / (Hq / Hkv).
+ *   q              bf16 [B, T, Hq, D], tokens q_stride elements apart; Hq a multiple of Hkv, at most 256 times
+ *                  it: query head h reads key head h / (Hq / Hkv).
  *   out            bf16 [B, T, Hq, D];   lse  fp32 [B, T, Hq] or NULL.
  *   scale          finite, >= 0.
  *   window         >= 1 (INT32_MAX: every earlier key);   sinks  >= 0.

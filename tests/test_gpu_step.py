@@ -237,6 +237,30 @@ def test_attn_malformed_arrays_are_reported(kda):
             kda.device_status()
 
 
+@pytest.mark.parametrize("new", [1, 60, 400])
+def test_attn_waits_that_give_up_are_reported(kda, new):
+    """With no polls allowed every wait gives up at once: the kernels end by themselves and say so, and the next call works."""
+    from gated_delta_rule_23_gb300 import _native
+    lib = _native.load()
+    gen = _gen(9)
+    k, v, table = step_ref.make_cache([500], 2, 128, 16, gen, "cuda")
+    lens = torch.tensor([500], dtype=torch.int32, device="cuda")
+    q = torch.randn((1, new, 8, 128), generator=gen, device="cuda").to(torch.bfloat16)
+    out = torch.empty_like(q)
+    try:
+        lib.kda_set_wait_limit(0)
+        kda.kda_window_attn(q, k, v, table, lens, out, 300)
+        with pytest.raises(kda.KDAError) as e:
+            kda.device_status()
+        assert e.value.status == _native.KDA_ERR_TIMEOUT
+    finally:
+        lib.kda_set_wait_limit(_native.KDA_DEFAULT_WAIT_POLLS)
+    lse = torch.empty((1, new, 8), device="cuda")
+    kda.kda_window_attn(q, k, v, table, lens, out, 300, lse=lse)
+    kda.device_status()
+    _check_attn(out, lse, step_ref.attention([q[0]], k, v, table, [500], [new], 300, 0, 128 ** -0.5), 128)
+
+
 # ---------------------------------------------------------------------------------------------- append
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("lens, new, hq, hkv, dim, page, rotary, ragged", [
