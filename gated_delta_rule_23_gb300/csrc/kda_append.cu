@@ -11,7 +11,10 @@
 namespace kda {
 namespace {
 
-constexpr int APPEND_THREADS = 256;
+// CTAs of 128 threads, eight an SM, with the loads of two heads in flight a thread.  8192 tokens of 96 + 2 x 8 heads of 128
+// (472 MB): 76 us; four heads in flight 82, one 78; CTAs of 256 threads 79 to 96.
+constexpr int APPEND_THREADS = 128, CTAS_PER_SM = 8;
+constexpr int FLIGHT = 2;      // heads whose loads a thread has in flight
 
 struct AppendArgs {
     const __nv_bfloat16 *k, *v, *q;
@@ -67,7 +70,7 @@ template <bool INTERLEAVED> __device__ __forceinline__ Vec16 rotate(const Vec16 
 }
 
 // One CTA per token.
-template <bool INTERLEAVED> __global__ void __launch_bounds__(APPEND_THREADS) kda_append_kernel(const AppendArgs p)
+template <bool INTERLEAVED> __global__ void __launch_bounds__(APPEND_THREADS, CTAS_PER_SM) kda_append_kernel(const AppendArgs p)
 {
     const int64_t t = blockIdx.x;
     const int units = p.cache.dim / 16;
@@ -110,34 +113,38 @@ template <bool INTERLEAVED> __global__ void __launch_bounds__(APPEND_THREADS) kd
         }
     }
     const int total = p.hq + 2 * p.cache.hkv;
-    for (int h = h0; h < total; h += hstep) {
-        const __nv_bfloat16 *src;
-        __nv_bfloat16 *dst = nullptr;
-        bool turned = turn;
-        if (h < p.hq) {
-            src = p.q + t * p.q_stride + (int64_t)h * p.cache.dim;
-            dst = p.q_out + (t * p.hq + h) * p.cache.dim;
-        } else if (h < p.hq + p.cache.hkv) {
-            const int g = h - p.hq;
-            src = p.k + t * p.k_stride + (int64_t)g * p.cache.dim;
-            if (row >= 0)
-                dst = p.cache.k + row + ((int64_t)g << p.cache.page_shift) * p.cache.dim;
-        } else {
-            const int g = h - p.hq - p.cache.hkv;
-            src = p.v + t * p.v_stride + (int64_t)g * p.cache.dim;
-            if (row >= 0)
-                dst = p.cache.v + row + ((int64_t)g << p.cache.page_shift) * p.cache.dim;
-            turned = false;
+    for (int first = h0; first < total; first += FLIGHT * hstep) {
+        // all loads before the stores (q_out may be q, so the compiler would keep them in turn)
+        Vec16 x[FLIGHT];
+        __nv_bfloat16 *dst[FLIGHT];
+#pragma unroll
+        for (int i = 0; i < FLIGHT; i++) {
+            const int h = first + i * hstep;
+            const __nv_bfloat16 *src = nullptr;
+            dst[i] = nullptr;
+            if (h < p.hq) {
+                src = p.q + t * p.q_stride + (int64_t)h * p.cache.dim;
+                dst[i] = p.q_out + (t * p.hq + h) * p.cache.dim;
+            } else if (h < total && row >= 0) {
+                const bool is_k = h < p.hq + p.cache.hkv;
+                const int g = h - p.hq - (is_k ? 0 : p.cache.hkv);
+                src = (is_k ? p.k + t * p.k_stride : p.v + t * p.v_stride) + (int64_t)g * p.cache.dim;
+                dst[i] = (is_k ? p.cache.k : p.cache.v) + row + ((int64_t)g << p.cache.page_shift) * p.cache.dim;
+            }
+            if (src) {
+                x[i].a = __ldcs(reinterpret_cast<const uint4 *>(src + e0));
+                x[i].b = __ldcs(reinterpret_cast<const uint4 *>(src + e1));
+            }
         }
-        if (!dst)
-            continue;
-        Vec16 x;
-        x.a = *reinterpret_cast<const uint4 *>(src + e0);
-        x.b = *reinterpret_cast<const uint4 *>(src + e1);
-        if (turned)
-            x = rotate<INTERLEAVED>(x, c, s);
-        *reinterpret_cast<uint4 *>(dst + e0) = x.a;
-        *reinterpret_cast<uint4 *>(dst + e1) = x.b;
+#pragma unroll
+        for (int i = 0; i < FLIGHT; i++) {
+            if (!dst[i])
+                continue;
+            if (turn && first + i * hstep < p.hq + p.cache.hkv)
+                x[i] = rotate<INTERLEAVED>(x[i], c, s);
+            *reinterpret_cast<uint4 *>(dst[i] + e0) = x[i].a;
+            *reinterpret_cast<uint4 *>(dst[i] + e1) = x[i].b;
+        }
     }
     report(p.err, bad && threadIdx.x == 0, DEVERR_CU_SEQLENS);
 }

@@ -164,13 +164,18 @@ AttnPlan make_plan(int window, int sinks, bool varlen, int N, int64_t T, int Hq,
     plan.wait_polls = wait_limit();
     const int sms = device_sms();
     if (!varlen && T * group <= DECODE_ROWS) {
-        // two CTAs an SM; a split has 128 keys at least (every warp two blocks)
+        // Two CTAs an SM; a split has 128 keys at least (every warp two blocks).  A cluster of up to 8 splits saves the
+        // second launch: taken unless its CTAs are left with over 1024 keys that more splits would share.
         plan.decode = true;
         plan.granule = DECODE_KEYS;
-        const int64_t ctas = (int64_t)N * Hkv, most = most_keys(window, sinks, T, page, max_pages) / 128;
+        const int64_t ctas = (int64_t)N * Hkv, keys = most_keys(window, sinks, T, page, max_pages), most = keys / 128;
         int64_t s = ctas > 0 ? 2 * sms / ctas : 1;
         s = s < most ? s : most;
-        plan.splits = s < 1 ? 1 : (s > 64 ? 64 : (int)s);
+        s = s < 1 ? 1 : (s > 64 ? 64 : s);
+        plan.cluster = s > 1 && (s <= DECODE_CLUSTER || keys <= 1024 * DECODE_CLUSTER);
+        if (plan.cluster)
+            s = s >= 8 ? 8 : (s >= 4 ? 4 : 2);
+        plan.splits = (int)s;
         plan.items = (int)(ctas * plan.splits);
         return plan;
     }
@@ -191,7 +196,7 @@ AttnPlan make_plan(int window, int sinks, bool varlen, int N, int64_t T, int Hq,
 
 size_t plan_bytes(const AttnPlan &plan, int dim)
 {
-    if (plan.splits == 1)
+    if (plan.splits == 1 || plan.cluster)
         return 0;
     return (size_t)plan.splits * plan.rows * (dim * sizeof(float) + sizeof(float2));
 }
@@ -261,7 +266,7 @@ extern "C" kda_status_t kda_window_attn_ws(const void *q, int64_t q_stride, cons
     plan.part_ml = reinterpret_cast<float2 *>(plan.part_o + (size_t)plan.splits * plan.rows * D);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = plan.decode ? launch_attn_decode(p, plan, st) : launch_attn_tiles(p, plan, st);
-    if (e == cudaSuccess && plan.splits > 1)
+    if (e == cudaSuccess && plan.splits > 1 && !plan.cluster)
         e = launch_attn_join(p, plan, st);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

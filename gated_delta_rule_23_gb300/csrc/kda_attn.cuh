@@ -25,9 +25,11 @@ struct AttnArgs {
 // split `splits` ways, the partial results joined by a second kernel when there is more than one.
 constexpr int ATTN_ROWS = 256;   // query rows of a tile
 constexpr int DECODE_ROWS = 16, DECODE_KEYS = 16;   // rows of the decode kernel, keys of its blocks
+constexpr int DECODE_CLUSTER = 8;                   // splits that join in a cluster
 
 struct AttnPlan {
     bool decode;            // at most 16 query rows a (sequence, key head): the decode kernel, one item a CTA
+    bool cluster;           // the splits are a cluster of the decode kernel (no workspace, no join kernel)
     int splits;
     int items;              // (row tile, key head, split) items (ragged: an upper bound)
     int granule;            // positions of a cache page that are copied together

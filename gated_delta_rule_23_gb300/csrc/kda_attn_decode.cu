@@ -4,8 +4,9 @@
 // memory's rate, and the arithmetic (16 rows wide on mma.sync) has to stay out of the way.  One CTA takes a (sequence, key
 // head) or a split of its keys; each of its warps works by itself on blocks of 16 keys, every fourth one, that its lane 0
 // brings in with bulk tensor copies into the warp's own ring of shared memory: no barrier of the CTA in the loop, and
-// RING x 8 KB in flight a warp.  The warps' results (running maximum, sum, O in fp32) are joined once at the end, in
-// shared memory, the splits' by the join kernel.
+// RING x 8 KB in flight a warp.  The warps' results (running maximum, sum, O in fp32) are joined once at the end in shared
+// memory.  Up to 8 splits are a cluster, which joins its CTAs' results over distributed shared memory in the same
+// launch; more go through memory and the join kernel.
 //
 // Keys come as in the tile kernel: the sinks' granules, then the window's, 16 positions each, which lie in one page.
 // Values that no row of the CTA sees are cleared in shared memory; where the rows differ in what they see (several
@@ -19,7 +20,7 @@ namespace kda {
 namespace {
 
 constexpr int WARPS = 4, THREADS = 32 * WARPS;
-constexpr int KEYS = DECODE_KEYS, ROWS = DECODE_ROWS;
+constexpr int KEYS = DECODE_KEYS, ROWS = DECODE_ROWS, CLUSTER = DECODE_CLUSTER;
 constexpr float RESCALE_AT = 8.0f;           // base-2 growth of a maximum that moves it
 constexpr unsigned FULL = 0xffffffffu;
 
@@ -42,6 +43,42 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t block, int key, int c)
 {
     return block + (c / 8) * (KEYS * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4);
 }
+// The same shared-memory address in CTA `rank` of the cluster, and a load from there
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank)
+{
+    uint32_t x;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(x) : "r"(addr), "r"(rank));
+    return x;
+}
+__device__ __forceinline__ float2 load_cluster(uint32_t addr)
+{
+    float2 x;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(addr) : "memory");
+    return x;
+}
+// Every CTA of the cluster comes here, whatever its waits did, so that this wait always ends.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Joins N results (maximum, sum) of a row: their weights, and the row's maximum and sum.  A result without a visible key has
+// maximum -inf and sum 0; NaN scores leave a NaN sum.
+template <int N> __device__ __forceinline__ void join_stats(const float2 (&st)[N], float (&w)[N], float &M, float &L)
+{
+    M = -INFINITY;
+    L = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; i++)
+        M = fmaxf(M, st[i].x);
+    const float mu = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const bool none = st[i].x == -INFINITY && st[i].y == 0.0f;
+        w[i] = none ? -1.0f : ex2_approx((st[i].x == -INFINITY ? 0.0f : st[i].x) - mu);
+        if (!none)
+            L += w[i] * st[i].y;
+    }
+}
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
 {
     const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
@@ -57,16 +94,17 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
     constexpr int CB = DIM / 64, KS = DIM / 16, NT = DIM / 8;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t bars[WARPS * S::RING];
-    __shared__ float2 stats[WARPS][ROWS];
+    __shared__ float2 stats[WARPS][ROWS], joined[ROWS];
+    __shared__ int failed_cta;
     asm volatile("griddepcontrol.launch_dependents;");
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char *const smem = smem_raw + (base - smem_u32(smem_raw));
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, g = lane / 4, t = lane % 4;
 
     int x = blockIdx.x;
-    const int kvh = x % p.cache.hkv;
-    x /= p.cache.hkv;
-    const int n = x % p.tok.N, split = x / p.tok.N;
+    const int split = x % plan.splits;                           // the splits of an item are neighbours: a cluster
+    x /= plan.splits;
+    const int kvh = x % p.cache.hkv, n = x / p.cache.hkv;
     const int tokens = (int)p.tok.T, rows = tokens * p.group;
     bool bad = false, timeout = false;
     const int len = (int)cache_len(p.cache, n, bad);
@@ -238,58 +276,108 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
 #pragma unroll
         for (int r = 0; r < 2; r++)
             *reinterpret_cast<float2 *>(part + (g + 8 * r) * DIM + ((8 * c + 2 * t) ^ (8 * (g & 3)))) = make_float2(o[c][2 * r], o[c][2 * r + 1]);
-    const bool failed = __syncthreads_or(timeout);
+    // a row's place in the batch, and its last step: the result, or the split's part of it
+    constexpr int PIECES = DIM / 64;                             // float2's a lane has of a row
+    auto finish = [&](int row, float M, float L, const float2 (&y)[PIECES], bool whole) {
+        const int tok = row / p.group, head = kvh * p.group + row % p.group;
+        const int64_t at = (int64_t)(n * tokens + tok) * p.hq + head;
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        bool finite = L <= FLT_MAX;
+#pragma unroll
+        for (int c = 0; c < PIECES; c++) {
+            const int e = 64 * c + 2 * lane;
+            finite &= fabsf(y[c].x) <= FLT_MAX && fabsf(y[c].y) <= FLT_MAX;
+            if (whole)
+                *reinterpret_cast<uint32_t *>(p.out + at * DIM + e) = L == 0.0f ? 0u : pack_bf16(y[c].x * inv, y[c].y * inv);
+            else
+                *reinterpret_cast<float2 *>(plan.part_o + (split * plan.rows + at) * DIM + e) = y[c];
+        }
+        if (lane == 0) {
+            if (!whole)
+                plan.part_ml[split * plan.rows + at] = make_float2(M, L);
+            else if (p.lse)
+                p.lse[at] = L == 0.0f ? -INFINITY : LN2 * (M + log2f(L));
+        }
+        if (whole && __any_sync(FULL, !finite)) {
+            __syncwarp();
+            attn_row<DIM>(p, n, (int64_t)n * tokens + tok, head, p0 + tok, bad);
+        }
+    };
+    bool failed = __syncthreads_or(timeout);
+    // the CTA's part of the cluster's results: behind O in the first warp's ring
+    static_assert(S::WARP >= 2 * ROWS * DIM * 4, "room for the CTA's O");
+    float *const cta_o = reinterpret_cast<float *>(smem) + ROWS * DIM;
     if (!failed) {
         for (int row = warp; row < rows; row += WARPS) {         // a warp joins a row
-            float M = -INFINITY, L = 0.0f, w[WARPS];
+            float2 st[WARPS], y[PIECES];
+            float w[WARPS], M, L;
 #pragma unroll
             for (int i = 0; i < WARPS; i++)
-                M = fmaxf(M, stats[i][row].x);
-            const float mu = M == -INFINITY ? 0.0f : M;
-            bool none[WARPS];                                    // warps without a visible key
+                st[i] = stats[i][row];
+            join_stats(st, w, M, L);
 #pragma unroll
-            for (int i = 0; i < WARPS; i++) {
-                const float2 st = stats[i][row];
-                none[i] = st.x == -INFINITY && st.y == 0.0f;
-                w[i] = ex2_approx((st.x == -INFINITY ? 0.0f : st.x) - mu);
-                if (!none[i])
-                    L += w[i] * st.y;
-            }
-            bool finite = L <= FLT_MAX;
-            const int tok = row / p.group, head = kvh * p.group + row % p.group;
-            const int64_t at = (int64_t)(n * tokens + tok) * p.hq + head;
-            const bool whole = plan.splits == 1;
-            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-#pragma unroll
-            for (int e0 = 0; e0 < DIM; e0 += 64) {
-                const int e = e0 + 2 * lane;
-                float2 y = make_float2(0.0f, 0.0f);
+            for (int c = 0; c < PIECES; c++) {
+                y[c] = make_float2(0.0f, 0.0f);
 #pragma unroll
                 for (int i = 0; i < WARPS; i++) {
-                    if (none[i])
+                    if (w[i] < 0.0f)
                         continue;
                     const float2 z = *reinterpret_cast<const float2 *>(reinterpret_cast<const float *>(smem + i * S::WARP) +
-                                                                       row * DIM + (e ^ (8 * (row & 3))));
-                    y.x = fmaf(w[i], z.x, y.x);
-                    y.y = fmaf(w[i], z.y, y.y);
+                                                                       row * DIM + ((64 * c + 2 * lane) ^ (8 * (row & 3))));
+                    y[c].x = fmaf(w[i], z.x, y[c].x);
+                    y[c].y = fmaf(w[i], z.y, y[c].y);
                 }
-                finite &= fabsf(y.x) <= FLT_MAX && fabsf(y.y) <= FLT_MAX;
-                if (whole)
-                    *reinterpret_cast<uint32_t *>(p.out + at * DIM + e) = L == 0.0f ? 0u : pack_bf16(y.x * inv, y.y * inv);
-                else
-                    *reinterpret_cast<float2 *>(plan.part_o + (split * plan.rows + at) * DIM + e) = y;
             }
-            if (lane == 0) {
-                if (!whole)
-                    plan.part_ml[split * plan.rows + at] = make_float2(M, L);
-                else if (p.lse)
-                    p.lse[at] = L == 0.0f ? -INFINITY : LN2 * (M + log2f(L));
+            if (!plan.cluster) {
+                finish(row, M, L, y, plan.splits == 1);
+                continue;
             }
-            if (whole && __any_sync(FULL, !finite)) {
-                __syncwarp();
-                attn_row<DIM>(p, n, (int64_t)n * tokens + tok, head, p0 + tok, bad);
+#pragma unroll
+            for (int c = 0; c < PIECES; c++)
+                *reinterpret_cast<float2 *>(cta_o + row * DIM + 64 * c + 2 * lane) = y[c];
+            if (lane == 0)
+                joined[row] = make_float2(M, L);
+        }
+    }
+    if (plan.cluster) {
+        if (tid == 0)
+            failed_cta = failed;
+        __syncthreads();
+        cluster_sync();
+        for (int i = 0; i < plan.splits; i++) {
+            int x = 0;
+            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(in_cta(smem_u32(&failed_cta), i)) : "memory");
+            failed |= x != 0;
+        }
+        if (!failed) {
+            for (int row = split + plan.splits * warp; row < rows; row += plan.splits * WARPS) {
+                float2 st[CLUSTER], y[PIECES];
+                float w[CLUSTER], M, L;
+#pragma unroll
+                for (int i = 0; i < CLUSTER; i++)
+                    st[i] = i < plan.splits ? load_cluster(in_cta(smem_u32(&joined[row]), i)) : make_float2(-INFINITY, 0.0f);
+                float2 z[CLUSTER][PIECES];
+#pragma unroll
+                for (int i = 0; i < CLUSTER; i++)
+#pragma unroll
+                    for (int c = 0; c < PIECES; c++)
+                        z[i][c] = i < plan.splits ? load_cluster(in_cta(smem_u32(cta_o + row * DIM + 64 * c + 2 * lane), i))
+                                                  : make_float2(0.0f, 0.0f);
+                join_stats(st, w, M, L);
+#pragma unroll
+                for (int c = 0; c < PIECES; c++) {
+                    y[c] = make_float2(0.0f, 0.0f);
+#pragma unroll
+                    for (int i = 0; i < CLUSTER; i++)
+                        if (w[i] >= 0.0f || w[i] != w[i]) {
+                            y[c].x = fmaf(w[i], z[i][c].x, y[c].x);
+                            y[c].y = fmaf(w[i], z[i][c].y, y[c].y);
+                        }
+                }
+                finish(row, M, L, y, true);
             }
         }
+        cluster_sync();                                          // no CTA leaves while its results are read
     }
     report(p.err, bad, DEVERR_CU_SEQLENS);
     report(p.err, timeout, DEVERR_TIMEOUT);
@@ -312,8 +400,18 @@ template <int DIM> cudaError_t launch_decode_dim(const AttnArgs &p, const AttnPl
         e = cache_map(&vmap, p.cache.v, p.cache, KEYS);
     if (e != cudaSuccess)
         return e;
-    kda_attn_decode_kernel<DIM><<<(unsigned)plan.items, THREADS, Shape<DIM>::SMEM, st>>>(p, plan, kmap, vmap);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)plan.items);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = Shape<DIM>::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = plan.cluster ? (unsigned)plan.splits : 1u;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kda_attn_decode_kernel<DIM>, p, plan, kmap, vmap);
 }
 
 }  // namespace

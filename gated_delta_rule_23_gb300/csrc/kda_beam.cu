@@ -318,7 +318,7 @@ __device__ __noinline__ void list_by_keys(Pick &sh, const T *l, int t0, int t1, 
 // One CTA per (chunk, row).  The threads stream through the chunk's logits, with no barrier, and keep their maxima and
 // sums.  The maxima then give a bound that about K + 1 logits reach: only the threads (a few) whose maximum does are
 // looked at again, eight lanes reading one thread's logits out of L2.
-template <typename T> __global__ void __launch_bounds__(THREADS, 4) kda_beam_chunks_kernel(const BeamArgs p)
+template <typename T> __global__ void __launch_bounds__(THREADS, 5) kda_beam_chunks_kernel(const BeamArgs p)
 {
     constexpr int N = Vec<T>::N, STEP = THREADS * N;
     __shared__ __align__(16) Pick sh;

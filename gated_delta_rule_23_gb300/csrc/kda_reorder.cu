@@ -26,10 +26,12 @@ template <int MAXW> __global__ void __launch_bounds__(REORDER_THREADS) kda_reord
     uint4 *dst = p.dst[blockIdx.z];
     const int64_t vecs = p.vecs[blockIdx.z];
     const int64_t n0 = (int64_t)blockIdx.y * p.beams;
+    const bool in_place = src == dst;
     bool bad = false;
     for (int64_t x = (int64_t)blockIdx.x * REORDER_THREADS + threadIdx.x; x < vecs;
          x += (int64_t)gridDim.x * REORDER_THREADS) {
         uint4 r[MAXW];
+        unsigned stays = 0;               // in place, rows that are their own parents
 #pragma unroll
         for (int w = 0; w < MAXW; w++) {
             if (w < p.beams) {
@@ -38,12 +40,14 @@ template <int MAXW> __global__ void __launch_bounds__(REORDER_THREADS) kda_reord
                     bad = true;
                     from = n0 + w;
                 }
-                r[w] = src[from * vecs + x];
+                stays |= (unsigned)(in_place && from == n0 + w) << w;
+                if (!(stays >> w & 1))
+                    r[w] = src[from * vecs + x];
             }
         }
 #pragma unroll
         for (int w = 0; w < MAXW; w++)
-            if (w < p.beams)
+            if (w < p.beams && !(stays >> w & 1))
                 dst[(n0 + w) * vecs + x] = r[w];
     }
     report(p.err, bad, DEVERR_CU_SEQLENS);
