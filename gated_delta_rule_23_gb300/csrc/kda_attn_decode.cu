@@ -19,12 +19,12 @@
 namespace kda {
 namespace {
 
-constexpr int WARPS = 4, THREADS = 32 * WARPS;
 constexpr int KEYS = DECODE_KEYS, ROWS = DECODE_ROWS, CLUSTER = DECODE_CLUSTER;
 constexpr float RESCALE_AT = 8.0f;           // base-2 growth of a maximum that moves it
 constexpr unsigned FULL = 0xffffffffu;
 
-template <int DIM> struct Shape {
+// WARPS: 4, two CTAs an SM; 8, one CTA an SM, for calls of fewer CTAs than SMs.
+template <int DIM, int WARPS> struct Shape {
     static constexpr int RING = DIM == 128 ? 3 : 6;              // blocks in flight a warp
     static constexpr int BLOCK = KEYS * DIM * 2;                 // bytes of K, and of V
     static constexpr int WARP = RING * 2 * BLOCK;                // a warp's ring
@@ -85,18 +85,22 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
     return *reinterpret_cast<const uint32_t *>(&x);
 }
 
-template <int DIM>
-__global__ void __launch_bounds__(THREADS, 2)
+template <int DIM, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 8 / WARPS)
 kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap)
 {
-    using S = Shape<DIM>;
+    using S = Shape<DIM, WARPS>;
     constexpr int CB = DIM / 64, KS = DIM / 16, NT = DIM / 8;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t bars[WARPS * S::RING];
     __shared__ float2 stats[WARPS][ROWS], joined[ROWS];
     __shared__ int failed_cta;
     asm volatile("griddepcontrol.launch_dependents;");
+    if (threadIdx.x == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
+    }
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char *const smem = smem_raw + (base - smem_u32(smem_raw));
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, g = lane / 4, t = lane % 4;
@@ -107,8 +111,27 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
     const int kvh = x % p.cache.hkv, n = x / p.cache.hkv;
     const int tokens = (int)p.tok.T, rows = tokens * p.group;
     bool bad = false, timeout = false;
+    // Q as the first operand: rows g and g + 8; on its way while the lengths and the page table are read
+    uint32_t q[KS][4];
+#pragma unroll
+    for (int r = 0; r < 2; r++) {
+        const int row = g + 8 * r;
+        const bool in = row < rows;
+        const int tok = in ? row / p.group : 0;
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(
+            p.q + (int64_t)(n * tokens + tok) * p.q_stride + (kvh * p.group + (in ? row % p.group : 0)) * DIM);
+#pragma unroll
+        for (int k = 0; k < KS; k++) {
+            q[k][r] = in ? __ldg(src + 8 * k + t) : 0;
+            q[k][2 + r] = in ? __ldg(src + 8 * k + 4 + t) : 0;
+        }
+    }
     const int len = (int)cache_len(p.cache, n, bad);
     const int p0 = len - tokens, p1 = len - 1;                   // positions of the first and the last token
+    int pos[2];
+#pragma unroll
+    for (int r = 0; r < 2; r++)
+        pos[r] = g + 8 * r < rows ? p0 + (g + 8 * r) / p.group : -1;
     // virtual keys: the sinks' granules, then the window's
     int sink = 0, start = 0, virt = 0;
     if (p1 >= 0) {
@@ -150,23 +173,6 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
         for (int i = 0; i < S::RING && i < mine; i++)
             fetch(i);
 
-    // Q as the first operand: rows g and g + 8
-    uint32_t q[KS][4];
-    int pos[2];
-#pragma unroll
-    for (int r = 0; r < 2; r++) {
-        const int row = g + 8 * r;
-        const bool in = row < rows;
-        const int tok = in ? row / p.group : 0;
-        pos[r] = in ? p0 + tok : -1;
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(
-            p.q + (int64_t)(n * tokens + tok) * p.q_stride + (kvh * p.group + (in ? row % p.group : 0)) * DIM);
-#pragma unroll
-        for (int k = 0; k < KS; k++) {
-            q[k][r] = in ? __ldg(src + 8 * k + t) : 0;
-            q[k][2 + r] = in ? __ldg(src + 8 * k + 4 + t) : 0;
-        }
-    }
     float o[NT][4];
 #pragma unroll
     for (int c = 0; c < NT; c++)
@@ -383,13 +389,13 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
     report(p.err, timeout, DEVERR_TIMEOUT);
 }
 
-template <int DIM> cudaError_t launch_decode_dim(const AttnArgs &p, const AttnPlan &plan, cudaStream_t st)
+template <int DIM, int WARPS> cudaError_t launch_decode_dim(const AttnArgs &p, const AttnPlan &plan, cudaStream_t st)
 {
     static std::atomic<uint64_t> ready;      // devices whose kernel attribute is set
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && !(ready.load() >> dev & 1)) {
-        e = cudaFuncSetAttribute(kda_attn_decode_kernel<DIM>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<DIM>::SMEM);
+        e = cudaFuncSetAttribute(kda_attn_decode_kernel<DIM, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<DIM, WARPS>::SMEM);
         if (e == cudaSuccess)
             ready.fetch_or(1ull << dev);
     }
@@ -402,8 +408,8 @@ template <int DIM> cudaError_t launch_decode_dim(const AttnArgs &p, const AttnPl
         return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)plan.items);
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = Shape<DIM>::SMEM;
+    cfg.blockDim = dim3(32 * WARPS);
+    cfg.dynamicSmemBytes = Shape<DIM, WARPS>::SMEM;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -411,14 +417,16 @@ template <int DIM> cudaError_t launch_decode_dim(const AttnArgs &p, const AttnPl
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kda_attn_decode_kernel<DIM>, p, plan, kmap, vmap);
+    return cudaLaunchKernelEx(&cfg, kda_attn_decode_kernel<DIM, WARPS>, p, plan, kmap, vmap);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_decode(const AttnArgs &p, const AttnPlan &plan, cudaStream_t st)
 {
-    return p.cache.dim == 128 ? launch_decode_dim<128>(p, plan, st) : launch_decode_dim<64>(p, plan, st);
+    if (plan.items <= device_sms())
+        return p.cache.dim == 128 ? launch_decode_dim<128, 8>(p, plan, st) : launch_decode_dim<64, 8>(p, plan, st);
+    return p.cache.dim == 128 ? launch_decode_dim<128, 4>(p, plan, st) : launch_decode_dim<64, 4>(p, plan, st);
 }
 
 }  // namespace kda
