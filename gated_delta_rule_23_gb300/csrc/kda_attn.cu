@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(ROW_THREADS) kda_attn_join_kernel(const AttnAr
     }
     if (!in || sub)
         return;
-    bool finite = l <= FLT_MAX;
+    bool finite = true;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     __nv_bfloat16 *out = p.out + r * DIM + lane * PER;
 #pragma unroll
@@ -89,13 +89,13 @@ __global__ void __launch_bounds__(ROW_THREADS) kda_attn_join_kernel(const AttnAr
     }
     if (p.lse && lane == 0)
         p.lse[r] = l == 0.0f ? -INFINITY : LN2 * (m + log2f(l));
-    if (__any_sync(0xffffffffu, !finite)) {
+    if (l > 0.0f && l <= FLT_MAX && __any_sync(0xffffffffu, !finite)) {
         const int64_t t = r / p.hq;
         bool bad = false;
         int64_t i, len;
         const int n = token_place(p.tok, t, i, len, bad);
         if (i >= 0 && i < len)
-            attn_row<DIM>(p, n, t, (int)(r % p.hq), cache_len(p.cache, n, bad) - len + i, bad);
+            attn_mend_row<DIM>(p, n, t, (int)(r % p.hq), cache_len(p.cache, n, bad) - len + i, bad);
     }
 }
 
@@ -136,7 +136,8 @@ AttnArgs make_attn(const void *q, int64_t q_stride, const void *k_cache, const v
     p.q_stride = q_stride;
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.lse = lse;
-    p.scale_log2 = scale * LOG2E;
+    // never 0, which would make NaN of a masked score's -inf: scores times this are 0 all the same
+    p.scale_log2 = fmaxf(scale * LOG2E, FLT_MIN);
     // no position is beyond what the table addresses, so neither need a bound be
     const int cap = max_pages * page;
     p.window = window < cap ? window : cap, p.sinks = sinks < cap ? sinks : cap;

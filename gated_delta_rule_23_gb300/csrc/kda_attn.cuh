@@ -127,4 +127,27 @@ __device__ void attn_row(const AttnArgs &p, int n, int64_t t, int h, int64_t pos
         p.lse[t * p.hq + h] = l == 0.0f ? -INFINITY : LN2 * (m + log2f(l));
 }
 
+// A row whose softmax sum is finite and whose output is not, because a tensor-core product took in values that the row
+// does not see (0 x infinity): taken again by attn_row, by a whole warp, unless the row is right as it is -- the key at
+// its own position, which it sees, is not finite in any of the output's columns that are not.  (A sum that is not finite
+// comes from the row's own scores: its output is NaN by definition.)  The row's output has been stored.
+template <int DIM>
+__device__ void attn_mend_row(const AttnArgs &p, int n, int64_t t, int h, int64_t pos, bool &bad)
+{
+    constexpr int PER = DIM / 32;
+    const int lane = threadIdx.x & 31;
+    __syncwarp();                                    // the row's stores come before what follows
+    const int64_t row = pos >= 0 ? cache_row(p.cache, n, pos) : -1;
+    bool wrong = row < 0;
+    if (row >= 0) {
+        const __nv_bfloat16 *out = p.out + (t * p.hq + h) * DIM + lane * PER;
+        const __nv_bfloat16 *v = p.cache.v + row + ((int64_t)(h / p.group) << p.cache.page_shift) * DIM + lane * PER;
+#pragma unroll
+        for (int e = 0; e < PER; e++)
+            wrong |= !(fabsf(__bfloat162float(out[e])) <= 3.3e38f) && fabsf(__bfloat162float(v[e])) <= 3.4e38f;
+    }
+    if (__any_sync(0xffffffffu, wrong))
+        attn_row<DIM>(p, n, t, h, pos, bad);
+}
+
 }  // namespace kda

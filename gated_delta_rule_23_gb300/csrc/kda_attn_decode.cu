@@ -288,7 +288,7 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
         const int tok = row / p.group, head = kvh * p.group + row % p.group;
         const int64_t at = (int64_t)(n * tokens + tok) * p.hq + head;
         const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-        bool finite = L <= FLT_MAX;
+        bool finite = true;
 #pragma unroll
         for (int c = 0; c < PIECES; c++) {
             const int e = 64 * c + 2 * lane;
@@ -304,10 +304,8 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
             else if (p.lse)
                 p.lse[at] = L == 0.0f ? -INFINITY : LN2 * (M + log2f(L));
         }
-        if (whole && __any_sync(FULL, !finite)) {
-            __syncwarp();
-            attn_row<DIM>(p, n, (int64_t)n * tokens + tok, head, p0 + tok, bad);
-        }
+        if (whole && L > 0.0f && L <= FLT_MAX && __any_sync(FULL, !finite))
+            attn_mend_row<DIM>(p, n, (int64_t)n * tokens + tok, head, p0 + tok, bad);
     };
     bool failed = __syncthreads_or(timeout);
     // the CTA's part of the cluster's results: behind O in the first warp's ring

@@ -26,7 +26,7 @@
 //
 // A key that a row does not see gets P = 0.  0 x v is NaN for an infinite or NaN v, and the matrix product has no way
 // to skip it: rows past the sequence's end are cleared in shared memory, and an output row that does not come out
-// finite is taken again from the definition, key by key, by attn_row.
+// finite is taken again from the definition, key by key (attn_mend_row).
 #include "kda_attn.cuh"
 
 #include <atomic>
@@ -397,7 +397,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                         top = top_of(s[0], top);
                     }
                     top *= p.scale_log2;
-                    if (top > m)                                 // not for NaN (0 x inf)
+                    if (top > m)                                 // not for NaN
                         m = top;
                 }
                 uint32_t pk[SUB / 2];
@@ -477,7 +477,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                 tc_fence_after();
             }
             // epilogue: the row's thread scales and stores it
-            bool finite = l <= FLT_MAX;
+            bool finite = true;
             const int64_t at = (int64_t)tok * p.hq + head;
             const bool part = plan.splits > 1;
             const float inv = part ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
@@ -520,13 +520,10 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                 plan.part_ml[w.split * plan.rows + at] = make_float2(m, l);
             else if (mine && p.lse)
                 p.lse[at] = l == 0.0f ? -INFINITY : LN2 * (m + log2f(l));
-            unsigned again = __ballot_sync(FULL, mine && !finite && !part);
-            if (again) {
-                __syncwarp();                 // the rows' first stores come before the ones below
-                for (; again; again &= again - 1) {
-                    const int src = __ffs(again) - 1;
-                    attn_row<DIM>(p, w.n, __shfl_sync(FULL, tok, src), __shfl_sync(FULL, head, src), __shfl_sync(FULL, pos, src), bad);
-                }
+            for (unsigned again = __ballot_sync(FULL, mine && !finite && l > 0.0f && l <= FLT_MAX && !part); again; again &= again - 1) {
+                const int src = __ffs(again) - 1;
+                attn_mend_row<DIM>(p, w.n, __shfl_sync(FULL, tok, src), __shfl_sync(FULL, head, src),
+                                   __shfl_sync(FULL, pos, src), bad);
             }
         }
     } else if (warp == 8) {

@@ -152,6 +152,34 @@ def test_attn_values_out_of_sight(kda, value, new, hq):
     _check_attn([out[0][clean]], [lse[0][clean]], [tuple(x[clean] for x in ref)], 128)
 
 
+@pytest.mark.parametrize("where", ["q", "k", "v"])
+@pytest.mark.parametrize("new", [1, 3, 600])
+def test_attn_values_in_sight(kda, where, new):
+    """NaN that a row does see is in its output, in the columns it belongs to; the other rows and columns are not touched."""
+    gen = _gen(31)
+    lens, window = [900], 200
+    k, v, table = step_ref.make_cache(lens, 1, 128, 16, gen, "cuda")
+    q = torch.randn((1, new, 4, 128), generator=gen, device="cuda").to(torch.bfloat16)
+    bad = 900 - 1 - new // 2                          # a position that some rows see, from its own row on
+    page, row = int(table[0, bad // 16]), bad % 16
+    if where == "q":
+        q[0, bad - (900 - new), 2, 7] = math.nan
+    elif where == "k":
+        k[page, 0, row, 3] = math.nan
+    else:
+        v[page, 0, row, 5] = math.inf
+        v[page, 0, row, 64] = math.nan
+    out, lse = torch.empty_like(q), torch.empty((1, new, 4), device="cuda")
+    kda.kda_window_attn(q, k, v, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), out, window, lse=lse)
+    kda.device_status()
+    o, ref_lse, mag, big = step_ref.attention([q[0]], k, v, table, lens, [new], window, 0, 128 ** -0.5)[0]
+    assert torch.equal(torch.isfinite(out[0].double()), torch.isfinite(o))
+    fine = torch.isfinite(o)
+    tol = U * o.abs() + (U + 2.0 ** -13) * mag
+    assert bool(((out[0].double() - o).abs()[fine] <= tol[fine]).all())
+    assert torch.equal(torch.isnan(lse[0]), torch.isnan(ref_lse))
+
+
 def test_attn_large_scores(kda):
     """Scores in the hundreds: the running maximum moves by large steps."""
     for new, lens in ((1, [500]), (200, [500])):
