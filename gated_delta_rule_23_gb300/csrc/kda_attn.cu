@@ -27,30 +27,33 @@ __global__ void __launch_bounds__(ROW_THREADS) kda_attn_join_kernel(const AttnAr
     for (int e = 0; e < PER; e++)
         o[e] = 0.0f;
     if (in) {
-        for (int s = lane; s < plan.splits; s += 32)
-            m = fmaxf(m, plan.part_ml[s * plan.rows + r].x);
+        // the statistics, split `lane` and split 32 + lane (there are 64 at most), as weights
+        float w2[2] = {-1.0f, -1.0f};
+        float2 st[2] = {make_float2(-INFINITY, 0.0f), make_float2(-INFINITY, 0.0f)};
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            if (32 * i + lane < plan.splits)
+                st[i] = plan.part_ml[(32 * i + lane) * plan.rows + r];
+        m = fmaxf(st[0].x, st[1].x);
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1)
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
         const float mu = m == -INFINITY ? 0.0f : m;
-        for (int s = lane; s < plan.splits; s += 32) {
-            const float2 ml = plan.part_ml[s * plan.rows + r];
-            if (!(ml.x == -INFINITY && ml.y == 0.0f))         // a split with a visible key
-                l += exp2f(ml.x - mu) * ml.y;
-        }
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            if (!(st[i].x == -INFINITY && st[i].y == 0.0f)) {      // a split with a visible key
+                w2[i] = exp2f(st[i].x - mu);
+                l += w2[i] * st[i].y;
+            }
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1)
             l += __shfl_xor_sync(0xffffffffu, l, x);
         for (int s0 = sub; s0 < plan.splits; s0 += FLIGHT * PER_ROW) {
-            float v[FLIGHT][PER], w[FLIGHT];
+            float v[FLIGHT][PER];
 #pragma unroll
             for (int i = 0; i < FLIGHT; i++) {
                 const int s = s0 + i * PER_ROW;
-                w[i] = -1.0f;
                 if (s < plan.splits) {
-                    const float2 ml = plan.part_ml[s * plan.rows + r];
-                    if (!(ml.x == -INFINITY && ml.y == 0.0f))
-                        w[i] = exp2f(ml.x - mu);
                     const float *src = plan.part_o + (s * plan.rows + r) * DIM + lane * PER;
 #pragma unroll
                     for (int e = 0; e < PER; e++)
@@ -58,11 +61,14 @@ __global__ void __launch_bounds__(ROW_THREADS) kda_attn_join_kernel(const AttnAr
                 }
             }
 #pragma unroll
-            for (int i = 0; i < FLIGHT; i++)
-                if (!(w[i] < 0.0f))
+            for (int i = 0; i < FLIGHT; i++) {
+                const int s = s0 + i * PER_ROW;
+                const float w = __shfl_sync(0xffffffffu, s < 32 ? w2[0] : w2[1], s & 31);
+                if (s < plan.splits && !(w < 0.0f))
 #pragma unroll
                     for (int e = 0; e < PER; e++)
-                        o[e] = fmaf(w[i], v[i][e], o[e]);
+                        o[e] = fmaf(w, v[i][e], o[e]);
+            }
         }
     }
     if (PER_ROW > 1) {

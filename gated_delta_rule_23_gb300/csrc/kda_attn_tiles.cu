@@ -47,8 +47,10 @@ constexpr unsigned FULL = 0xffffffffu;
 template <int DIM> struct Shape {
     static constexpr int TILE = KEYS * DIM * 2;              // bytes of a K or V tile
     static constexpr int Q = HALF * DIM * 2;                 // of a half's Q
-    static constexpr int SLOTS = DIM == 128 ? 5 : 10;        // ring: K0 V0 K1 V1 ...
-    static constexpr int BAR = 2 * Q + SLOTS * TILE;         // mbarriers behind Q and the ring
+    static constexpr int SLOTS = DIM == 128 ? 4 : 8;         // ring: K0 V0 K1 V1 ...
+    static constexpr int STAGE = 32 * 128;                   // a softmax warp's rows on their way out, 128 bytes of each
+    static constexpr int OUT = 2 * Q + SLOTS * TILE;         // behind Q and the ring
+    static constexpr int BAR = OUT + 8 * STAGE;              // mbarriers last
     static constexpr int SMEM = 1024 + BAR + 768;            // 1024: alignment of the swizzle atoms
 };
 
@@ -476,11 +478,28 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                     break;
                 tc_fence_after();
             }
-            // epilogue: the row's thread scales and stores it
+            // Epilogue: the row's thread scales it; 128 bytes of each row at a time go through shared memory (16-byte
+            // chunks, swizzled) and out with eight lanes to a row.  (Stored straight by its thread, a row took a line of L1
+            // for every 16 bytes: 148 us for ragged 8192 tokens with window 512.)
             bool finite = true;
-            const int64_t at = (int64_t)tok * p.hq + head;
+            const int at = mine ? tok * p.hq + head : -1;
             const bool part = plan.splits > 1;
             const float inv = part ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+            unsigned char *const stage = smem + S::OUT + warp * S::STAGE;
+            auto put = [&](int chunk, const uint4 &x) {
+                *reinterpret_cast<uint4 *>(stage + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = x;
+            };
+            auto flush = [&](unsigned char *to, int64_t row_bytes) {
+                __syncwarp();
+#pragma unroll
+                for (int r0 = 0; r0 < 32; r0 += 4) {
+                    const int r = r0 + lane / 8, chunk = lane % 8, row = __shfl_sync(FULL, at, r);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((chunk ^ (r & 7)) << 4));
+                    if (row >= 0)
+                        *reinterpret_cast<uint4 *>(to + row * row_bytes + chunk * 16) = x;
+                }
+                __syncwarp();
+            };
 #pragma unroll
             for (int c = 0; c < DIM; c += 32) {
                 float o[32];
@@ -494,15 +513,13 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                     finite &= fabsf(y) <= FLT_MAX;
                     o[e] = part || l != 0.0f ? y * inv : 0.0f;
                 }
-                if (!mine)
-                    continue;
                 if (part) {
-                    float4 *dst = reinterpret_cast<float4 *>(plan.part_o + (w.split * plan.rows + at) * DIM + c);
 #pragma unroll
                     for (int e = 0; e < 8; e++)
-                        dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        put(e, make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
+                                          __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3])));
+                    flush(reinterpret_cast<unsigned char *>(plan.part_o + w.split * plan.rows * DIM + c), DIM * 4);
                 } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * DIM + c);
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
                         uint32_t y[4];
@@ -511,8 +528,10 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                             const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[8 * e + 2 * j], o[8 * e + 2 * j + 1]);
                             y[j] = *reinterpret_cast<const uint32_t *>(&b2);
                         }
-                        dst[e] = make_uint4(y[0], y[1], y[2], y[3]);
+                        put((c % 64) / 8 + e, make_uint4(y[0], y[1], y[2], y[3]));
                     }
+                    if (c % 64 == 32)
+                        flush(reinterpret_cast<unsigned char *>(p.out + c - 32), DIM * 2);
                 }
             }
             tc_fence_before();                // O is read before the next item's first P lets it be overwritten
