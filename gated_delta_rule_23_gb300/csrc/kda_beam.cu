@@ -23,7 +23,6 @@ constexpr int THREADS = 256;              // of the chunk kernel
 constexpr int PICK_THREADS = 512;
 constexpr int CAP = 2048;                 // keys gathered in shared memory
 constexpr int SELECTED = 1024;            // of them from the bound up: K groups of 2048 / 64 or 2048 / 128 keys at most
-constexpr int MOST_CHUNK = 32768;         // tokens of a chunk at most
 constexpr int BY_KEYS = 1 << 30;          // in a list's count: the list is the K + 1 best and ends at a logit
 constexpr unsigned FULL = 0xffffffffu;
 
@@ -107,28 +106,40 @@ struct Pick {
 __device__ __forceinline__ int groups_for(int n) { return n <= 32 ? 64 : 128; }
 
 // The n-th best of the groups' best keys; 1 (every key gets through) when fewer than n groups have one.
-template <int NT> __device__ uint64_t group_bound(Pick &sh, uint64_t best, int n)
+template <int NT, int GROUPS> __device__ __forceinline__ uint64_t group_bound_of(Pick &sh, uint64_t best, int n)
 {
-    const int groups = groups_for(n), size = NT / groups, lane = threadIdx.x % 32;
-    for (int o = 1; o < size; o <<= 1) {
+    constexpr int SIZE = NT / GROUPS;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll
+    for (int o = 1; o < SIZE; o <<= 1) {
         const uint64_t y = __shfl_xor_sync(FULL, best, o);
         best = best > y ? best : y;
     }
-    if (threadIdx.x % size == 0)
-        sh.group[threadIdx.x / size] = best;
+    if (threadIdx.x % SIZE == 0)
+        sh.group[threadIdx.x / SIZE] = best;
     if (threadIdx.x == 0)
         sh.bound = 1;
     __syncthreads();
-    for (int i = threadIdx.x / 32; i < groups; i += NT / 32) {     // a warp ranks a group
-        const uint64_t x = sh.group[i];
+    uint64_t all[GROUPS / 32];
+#pragma unroll
+    for (int j = 0; j < GROUPS / 32; j++)
+        all[j] = sh.group[32 * j + lane];
+#pragma unroll
+    for (int i = 0; i < GROUPS * 32 / NT; i++) {                   // a warp ranks a group
+        const uint64_t x = sh.group[i * (NT / 32) + warp];
         int rank = 0;
-        for (int j = 0; j < groups; j += 32)
-            rank += __popc(__ballot_sync(FULL, sh.group[j + lane] > x));
+#pragma unroll
+        for (int j = 0; j < GROUPS / 32; j++)
+            rank += __popc(__ballot_sync(FULL, all[j] > x));
         if (lane == 0 && x != 0 && rank == n - 1)
             sh.bound = x;
     }
     __syncthreads();
     return sh.bound;
+}
+template <int NT> __device__ __forceinline__ uint64_t group_bound(Pick &sh, uint64_t best, int n)
+{
+    return groups_for(n) == 64 ? group_bound_of<NT, 64>(sh, best, n) : group_bound_of<NT, 128>(sh, best, n);
 }
 
 // The same on values alone, rounded down to 24 bits: a value that the n best groups' best values reach; NaN when fewer
@@ -225,19 +236,22 @@ struct Seen {
 };
 
 // Thread i's logits of the tokens [t0, t1): N from t0 + (s THREADS + i) N on for s = 0, 1, ...  DEPTH loads of 16 bytes
-// are in flight.  DEPTH > 0: a multiple of DEPTH whole steps of a row on a 16-byte boundary; else the same logits in the
-// same order one by one, so that the result does not depend on a row's alignment.
-template <typename T, int DEPTH> __device__ __forceinline__ void stream_logits(const T *l, int t0, int t1, Seen &seen)
+// are in flight.  VECTOR: whole steps of a row on a 16-byte boundary; else the same logits in the same order one by one, so
+// that the result does not depend on a row's alignment.
+template <typename T, bool VECTOR> __device__ __forceinline__ void stream_logits(const T *l, int t0, int t1, Seen &seen)
 {
     constexpr int N = Vec<T>::N, STEP = THREADS * N;
     const int steps = (t1 - t0 + STEP - 1) / STEP;
-    if constexpr (DEPTH > 0) {
+    if constexpr (VECTOR) {
+        constexpr int DEPTH = 8;
         const uint4 *at = reinterpret_cast<const uint4 *>(l + t0) + threadIdx.x;
         uint4 raw[DEPTH];
 #pragma unroll
         for (int d = 0; d < DEPTH; d++)
-            raw[d] = __ldg(at + d * THREADS);
-        for (int s = DEPTH; s < steps; s += DEPTH) {
+            if (d < steps)
+                raw[d] = __ldg(at + d * THREADS);
+        int s = 0;
+        for (; s + 2 * DEPTH <= steps; s += DEPTH) {
             at += DEPTH * THREADS;
 #pragma unroll
             for (int d = 0; d < DEPTH; d++) {
@@ -247,12 +261,23 @@ template <typename T, int DEPTH> __device__ __forceinline__ void stream_logits(c
                 raw[d] = __ldg(at + d * THREADS);
             }
         }
+        at += DEPTH * THREADS;
 #pragma unroll
-        for (int d = 0; d < DEPTH; d++) {
-            float v[N];
-            unpack(raw[d], v, l);
-            seen.add(v);
-        }
+        for (int d = 0; d < DEPTH; d++)             // up to DEPTH more steps behind the ones in flight
+            if (s + d < steps) {
+                float v[N];
+                unpack(raw[d], v, l);
+                seen.add(v);
+                if (s + DEPTH + d < steps)
+                    raw[d] = __ldg(at + d * THREADS);
+            }
+#pragma unroll
+        for (int d = 0; d < DEPTH; d++)
+            if (s + DEPTH + d < steps) {
+                float v[N];
+                unpack(raw[d], v, l);
+                seen.add(v);
+            }
     } else {
         constexpr int FLIGHT = 16 / N;
         float raw[FLIGHT][N];
@@ -332,16 +357,10 @@ template <typename T> __global__ void __launch_bounds__(THREADS, 5) kda_beam_chu
     const T *l = static_cast<const T *>(p.logits) + row * p.row_stride;
     const int t0 = chunk * p.chunk, t1 = min(p.V, t0 + p.chunk);
     Seen seen;
-    const bool even = (reinterpret_cast<uintptr_t>(l) & 15) == 0 && (t1 - t0) % STEP == 0;
-    const int steps = (t1 - t0) / STEP;
-    if (even && steps % 8 == 0)
-        stream_logits<T, 8>(l, t0, t1, seen);
-    else if (even && steps % 2 == 0)
-        stream_logits<T, 2>(l, t0, t1, seen);
-    else if (even)
-        stream_logits<T, 1>(l, t0, t1, seen);
+    if ((reinterpret_cast<uintptr_t>(l) & 15) == 0 && (t1 - t0) % STEP == 0)
+        stream_logits<T, true>(l, t0, t1, seen);
     else
-        stream_logits<T, 0>(l, t0, t1, seen);
+        stream_logits<T, false>(l, t0, t1, seen);
     const float best = seen.best;
     float m = best;
 #pragma unroll
@@ -368,7 +387,7 @@ template <typename T> __global__ void __launch_bounds__(THREADS, 5) kda_beam_chu
     uint64_t *list = p.lists + (int64_t)blockIdx.x * p.room;
     const bool by_keys = !(fabsf(bound) <= FLT_MAX);       // too few finite values for a bound
     if (!by_keys) {
-        constexpr int TURNS = MOST_CHUNK / STEP / 8;       // of eight lanes over a thread's vectors
+        constexpr int TURNS = 16 / N;                      // of eight lanes over a thread's vectors, in flight together
         for (unsigned owners = __ballot_sync(FULL, best >= bound); owners;) {
             int of = -1;
 #pragma unroll
@@ -378,25 +397,27 @@ template <typename T> __global__ void __launch_bounds__(THREADS, 5) kda_beam_chu
                         of = tid - lane + __ffs(owners) - 1;
                     owners &= owners - 1;
                 }
-            float x[TURNS][N];
+            for (int first = t0; first < t1; first += 8 * TURNS * STEP) {
+                float x[TURNS][N];
 #pragma unroll
-            for (int j = 0; j < TURNS; j++)
+                for (int j = 0; j < TURNS; j++)
 #pragma unroll
-                for (int e = 0; e < N; e++) {
-                    const int t = t0 + ((lane % 8 + 8 * j) * THREADS + of) * N + e;
-                    x[j][e] = -INFINITY;
-                    if (of >= 0 && t < t1)
-                        x[j][e] = load_logit(l + t);
-                }
-#pragma unroll
-            for (int j = 0; j < TURNS; j++)
-#pragma unroll
-                for (int e = 0; e < N; e++)
-                    if (x[j][e] >= bound) {
-                        const int to = atomicAdd(&sh.count, 1);
-                        if (to < p.room)
-                            list[to] = key_of(x[j][e], t0 + ((lane % 8 + 8 * j) * THREADS + of) * N + e);
+                    for (int e = 0; e < N; e++) {
+                        const int t = first + ((lane % 8 + 8 * j) * THREADS + of) * N + e;
+                        x[j][e] = -INFINITY;
+                        if (of >= 0 && t < t1)
+                            x[j][e] = load_logit(l + t);
                     }
+#pragma unroll
+                for (int j = 0; j < TURNS; j++)
+#pragma unroll
+                    for (int e = 0; e < N; e++)
+                        if (x[j][e] >= bound) {
+                            const int to = atomicAdd(&sh.count, 1);
+                            if (to < p.room)
+                                list[to] = key_of(x[j][e], first + ((lane % 8 + 8 * j) * THREADS + of) * N + e);
+                        }
+            }
         }
     }
     __syncthreads();
@@ -459,6 +480,7 @@ template <typename T> __global__ void __launch_bounds__(PICK_THREADS) kda_beam_p
 {
     __shared__ __align__(16) Pick sh;
     __shared__ uint64_t sel[SELECTED];     // candidates from the bound up
+    uint64_t *const cand = sh.cand;
     __shared__ float c[32], own[32];       // the beams' offsets, and the scores of finished ones
     __shared__ int kind[32];               // 0: candidates from the lists; 1: nothing counts; 2: finished
     __shared__ int selected;
@@ -466,6 +488,24 @@ template <typename T> __global__ void __launch_bounds__(PICK_THREADS) kda_beam_p
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tid == 0)
         sh.count = selected = 0;
+    // The lists' slots, `room` a list and so warp by warp in one list each: the first HELD rounds of them are on their way
+    // while the beams' offsets are worked out.
+    constexpr int HELD = 4;
+    const float4 *stats = p.stats + (int64_t)b * p.W * p.chunks;
+    const uint64_t *lists = p.lists + (int64_t)b * p.W * p.chunks * p.room;
+    const int64_t slots = (int64_t)p.W * p.chunks * p.room;
+    uint64_t raw[HELD];
+    int list_of[HELD], have[HELD];
+    auto fetch = [&](int64_t from) {
+#pragma unroll
+        for (int i = 0; i < HELD; i++) {
+            const int64_t x = from + i * PICK_THREADS + tid;
+            list_of[i] = x < slots ? (int)((uint32_t)x / (uint32_t)p.room) : -1;    // slots < 2^31 (checked on the host)
+            raw[i] = x < slots ? lists[x] : 0;
+            have[i] = x < slots ? __float_as_int(stats[list_of[i]].w) & ~BY_KEYS : 0;
+        }
+    };
+    fetch(0);
     for (int w = warp; w < p.W; w += PICK_THREADS / 32) {
         const int64_t row = (int64_t)b * p.W + w;
         const bool done = p.finished && p.finished[row];
@@ -499,49 +539,55 @@ template <typename T> __global__ void __launch_bounds__(PICK_THREADS) kda_beam_p
         }
     }
     __syncthreads();
-    // hands every candidate to f, a warp at a list (or at a beam whose candidates are all -inf but for a finished one's
-    // eos: its first tokens, and eos); key 0: none
-    const float4 *stats = p.stats + (int64_t)b * p.W * p.chunks;
-    const uint64_t *lists = p.lists + (int64_t)b * p.W * p.chunks * p.room;
-    auto each = [&](auto f) {
-        for (int i = warp; i < p.W * p.chunks; i += PICK_THREADS / 32) {
-            const int w = i / p.chunks;
-            if (kind[w] == 0) {
-                const int have = __float_as_int(stats[i].w) & ~BY_KEYS;
-                for (int j = lane; j < (p.room + 31) / 32 * 32; j += 32) {
-                    const uint64_t k = j < p.room ? lists[(int64_t)i * p.room + j] : 0;
-                    f(j < have ? key_of(score_of(c[w], key_value(k)), (uint32_t)w * p.V + key_index(k)) : 0);
-                }
-            } else if (i % p.chunks == 0) {
-                for (int j = lane; j < (p.K + 32) / 32 * 32; j += 32) {
-                    const bool eos = kind[w] == 2 && (j < p.K ? j == p.eos : j == p.K && p.eos >= p.K);
-                    const int t = eos ? p.eos : j;
-                    f(eos || (j < p.K && j < p.V) ? key_of(eos ? own[w] : -INFINITY, (uint32_t)w * p.V + t) : 0);
-                }
-            }
-        }
+    // the candidate of slot j of a list (0: none); a beam whose candidates are all -inf but for a finished one's eos has its
+    // first tokens and eos in the slots of its first list
+    auto candidate = [&](int64_t from, int i) -> uint64_t {
+        const int list = list_of[i];
+        if (list < 0)
+            return 0;
+        const int j = (int)(from + i * PICK_THREADS + tid - (int64_t)list * p.room), w = list / p.chunks;
+        if (kind[w] == 0)
+            return j < have[i] ? key_of(score_of(c[w], key_value(raw[i])), (uint32_t)w * p.V + key_index(raw[i])) : 0;
+        if (list != w * p.chunks)
+            return 0;
+        const bool eos = kind[w] == 2 && (j < p.K ? j == p.eos : j == p.K && p.eos >= p.K);
+        return eos || (j < p.K && j < p.V) ? key_of(eos ? own[w] : -INFINITY, (uint32_t)w * p.V + (eos ? p.eos : j)) : 0;
     };
     uint64_t best = 0;
-    each([&](uint64_t k) {                 // gathered while there is room
-        best = k > best ? k : best;
-        const unsigned m = __ballot_sync(FULL, k != 0);
+    for (int64_t from = 0; from < slots; from += HELD * PICK_THREADS) {
+        if (from)
+            fetch(from);
+        uint64_t k[HELD];
+        unsigned m[HELD];
         int at = 0;
+#pragma unroll
+        for (int i = 0; i < HELD; i++) {
+            k[i] = candidate(from, i);
+            best = k[i] > best ? k[i] : best;
+            m[i] = __ballot_sync(FULL, k[i] != 0);
+            at += __popc(m[i]);
+        }
         if (lane == 0)
-            at = atomicAdd(&sh.count, __popc(m));
-        at = __shfl_sync(FULL, at, 0) + __popc(m & ((1u << lane) - 1));
-        if (k != 0 && at < CAP)
-            sh.cand[at] = k;
-    });
+            at = atomicAdd(&sh.count, at);
+        at = __shfl_sync(FULL, at, 0);
+#pragma unroll
+        for (int i = 0; i < HELD; i++) {                 // gathered while there is room
+            const int to = at + __popc(m[i] & ((1u << lane) - 1));
+            if (k[i] != 0 && to < CAP)
+                cand[to] = k[i];
+            at += __popc(m[i]);
+        }
+    }
     __syncthreads();
     const int total = sh.count;
     if (total <= CAP) {
         best = 0;
         for (int x = tid; x < total; x += PICK_THREADS)
-            best = sh.cand[x] > best ? sh.cand[x] : best;
+            best = cand[x] > best ? cand[x] : best;
     }
     const uint64_t bound = group_bound<PICK_THREADS>(sh, best, p.K);
     auto select = [&](uint64_t k) {
-        if (k >= bound) {
+        if (k != 0 && k >= bound) {
             const int to = atomicAdd(&selected, 1);
             if (to < SELECTED)
                 sel[to] = k;
@@ -549,9 +595,14 @@ template <typename T> __global__ void __launch_bounds__(PICK_THREADS) kda_beam_p
     };
     if (total <= CAP) {
         for (int x = tid; x < total; x += PICK_THREADS)
-            select(sh.cand[x]);
+            select(cand[x]);
     } else {
-        each(select);
+        for (int64_t from = 0; from < slots; from += HELD * PICK_THREADS) {
+            fetch(from);
+#pragma unroll
+            for (int i = 0; i < HELD; i++)
+                select(candidate(from, i));
+        }
     }
     __syncthreads();
     const int count = selected;
@@ -586,12 +637,17 @@ template <typename T> __global__ void __launch_bounds__(PICK_THREADS) kda_beam_p
 
 }  // namespace
 
-// Tokens of a chunk: long ones leave fewer lists to pick from, short ones put a small call's logits on more SMs.
+// Tokens of a chunk: whole steps of 2048 (what the CTA's threads take of bf16 logits at once).  Rows are cut so that the
+// chunks are one wave of five CTAs an SM, which all end together (32 x 8 rows of 131072 in 3 chunks each), but not under
+// 2048 tokens; few and long chunks also leave fewer lists to pick from.
 static int beam_chunk(int B, int W, int V)
 {
     const int64_t rows = (int64_t)B * W;
-    auto ctas = [&](int chunk) { return rows * ((V + chunk - 1) / chunk); };
-    return ctas(MOST_CHUNK) >= 304 ? MOST_CHUNK : (ctas(8192) >= 152 ? 8192 : 2048);
+    int64_t cut = 5 * 152 / rows;
+    cut = rows * cut * 10 < 5 * 152 * 9 ? cut + 1 : cut;       // a wave under nine tenths full is worse than a little over one
+    cut = cut < 1 ? 1 : cut;
+    const int64_t chunk = (V + cut - 1) / cut;
+    return (int)((chunk + 2047) / 2048 * 2048);
 }
 static int beam_chunks(int B, int W, int V)
 {
@@ -632,7 +688,7 @@ static kda_status_t check_beam(const void *logits, kda_dtype_t dtype, int64_t ro
         return KDA_ERR_INVALID_ARGUMENT;
     if (V > (1 << 24) || (int64_t)B * W > INT32_MAX || (int64_t)B * K > INT32_MAX)
         return KDA_ERR_UNSUPPORTED;
-    if ((int64_t)B * W * beam_chunks(B, W, V) > INT32_MAX)
+    if ((int64_t)B * W * beam_chunks(B, W, V) * beam_room(K) > INT32_MAX)
         return KDA_ERR_UNSUPPORTED;
     if (dtype != KDA_DTYPE_BF16 && dtype != KDA_DTYPE_FP32)
         return KDA_ERR_INVALID_ARGUMENT;
