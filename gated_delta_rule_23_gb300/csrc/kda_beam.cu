@@ -243,7 +243,7 @@ template <typename T, bool VECTOR> __device__ __forceinline__ void stream_logits
     constexpr int N = Vec<T>::N, STEP = THREADS * N;
     const int steps = (t1 - t0 + STEP - 1) / STEP;
     if constexpr (VECTOR) {
-        constexpr int DEPTH = 8;
+        constexpr int DEPTH = 32 / N;               // bf16 has twice the work a byte
         const uint4 *at = reinterpret_cast<const uint4 *>(l + t0) + threadIdx.x;
         uint4 raw[DEPTH];
 #pragma unroll
