@@ -8,6 +8,11 @@
 // memory.  Up to 8 splits are a cluster, which joins its CTAs' results over distributed shared memory in the same
 // launch; more go through memory and the join kernel.
 //
+// Measured: 256 sequences, 64 heads over 8, window 1024 and 16 sinks (1.10 GB), 164 us, 6.70 TB/s, 99% of the measured copy
+// rate (the tile kernel: 255 us).  One sequence, 32 heads over 8, window 4096: 12.3 us, a chain of latencies (lengths, page
+// table, copies, four blocks a warp, the joins); 8 splits in a cluster and 32 splits with a join kernel take the same in a
+// row of calls, the cluster 3 us less alone.
+//
 // Keys come as in the tile kernel: the sinks' granules, then the window's, 16 positions each, which lie in one page.
 // Values that no row of the CTA sees are cleared in shared memory; where the rows differ in what they see (several
 // tokens), an output row that does not come out finite is taken again from the definition.

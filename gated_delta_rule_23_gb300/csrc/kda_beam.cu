@@ -5,6 +5,10 @@
 // row, the chunk's maximum and sum and its K + 1 best logits (kda_beam_chunks_kernel), and a second kernel, one CTA a
 // batch entry, turns those few into scores and picks (kda_beam_pick_kernel).  Each logit is read once: the floor.
 //
+// Measured: 32 x 8 rows of 131072 fp32 logits (134 MB), 41 us, 3.3 TB/s, 49% of the measured copy rate: the chunks stream
+// at 60% of it and all end together, so that their tail (the bound, the few threads looked at again) and the pick's chain
+// of latencies (5.5 us) are in nobody's shadow.  One request of 4 x 32001 bf16 logits: 12.3 us, both chains.
+//
 // What the short lists may hide: logits so close that their fp32 scores are equal tie by index and not by logit.  That
 // matters only where the value a chunk's list was cut off at reaches the K-th score and a neighbouring logit value has
 // the same score too; the pick then goes over all candidates of the entry again (pick_all).
@@ -638,8 +642,9 @@ template <typename T> __global__ void __launch_bounds__(PICK_THREADS) kda_beam_p
 }  // namespace
 
 // Tokens of a chunk: whole steps of 2048 (what the CTA's threads take of bf16 logits at once).  Rows are cut so that the
-// chunks are one wave of five CTAs an SM, which all end together (32 x 8 rows of 131072 in 3 chunks each), but not under
-// 2048 tokens; few and long chunks also leave fewer lists to pick from.
+// chunks are one wave of five CTAs an SM, but not under 2048 tokens; few and long chunks also leave fewer lists to pick
+// from.  32 x 8 rows of 131072 logits, in L2: 32.8 us in 3 chunks a row, 36.8 in 4, 34.4 in 2, 40 in 8.  4 rows of 32001:
+// the same with 2048, 4096 and 8192 tokens.
 static int beam_chunk(int B, int W, int V)
 {
     const int64_t rows = (int64_t)B * W;

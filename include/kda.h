@@ -346,12 +346,12 @@ const char *kda_status_string(kda_status_t status);
  */
 kda_status_t kda_device_status(kda_stream_t stream);
 
-/* Default of kda_set_wait_limit: mbarrier polls before a wait of the chunked kernels gives up. */
+/* Default of kda_set_wait_limit: mbarrier polls before a wait of the chunked or attention kernels gives up. */
 #define KDA_DEFAULT_WAIT_POLLS 16777216u
 
 /*
- * Sets how many times a wait of the chunked kernels (kda_fwd and its variants, on the tensor cores
- * and on bulk copies) polls before it gives up, for the kernels launched after the call, process-wide
+ * Sets how many times a wait of the chunked kernels (kda_fwd and its variants) and of the attention kernels
+ * (kda_window_attn), on the tensor cores and on bulk copies, polls before it gives up, for the kernels launched after the call, process-wide
  * (default KDA_DEFAULT_WAIT_POLLS, which is far beyond any wait of a working kernel).  A wait that
  * gives up makes its CTA wait for its own work in flight (with the default limit), free its tensor
  * memory and leave; kda_device_status then reports KDA_ERR_TIMEOUT and the call's outputs are not
@@ -417,7 +417,8 @@ kda_status_t kda_kv_append(const void *k, int64_t k_stride, const void *v, int64
  * position p sees key j when j <= p and (j > p - window or j < sinks):
  *   out = sum_j softmax_j(scale q.k_j) v_j,   lse = log sum_j exp(scale q.k_j)   over the visible j;
  * a query that sees no key gets out = 0 and lse = -inf.  What lies in keys and values that a query does
- * not see (stale rows, infinities, NaN) does not reach its output.
+ * not see (stale rows, infinities, NaN) does not reach its output.  (Rows near such values are taken again key by key, which
+ * is slow; rows past a sequence's end and keys that no query of the call sees cost nothing.)
  *
  *   q              bf16 [B, T, Hq, D], tokens q_stride elements apart; Hq a multiple of Hkv, at most 256 times
  *                  it: query head h reads key head h / (Hq / Hkv).
