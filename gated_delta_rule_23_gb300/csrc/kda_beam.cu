@@ -215,17 +215,33 @@ __device__ __forceinline__ void unpack(const uint4 &x, float *v, const __nv_bflo
     for (int i = 0; i < 4; i++)
         v[2 * i] = bf16_lo(u[i]), v[2 * i + 1] = bf16_hi(u[i]);
 }
-// What a thread keeps of the logits it has seen: their maximum, and the sum of exp(v - ref) as 2^(v L - c), c = ref L
-// rounded; the factor 2^(c - ref L) is put in at the end.  ref follows the maximum only in large steps: any of the
-// logits near it serves.
+// The two largest of N values (fmaxf and fminf pass over NaN, which can only make lo larger than it is).
+template <int N> __device__ __forceinline__ void two_largest(const float *v, float &hi, float &lo)
+{
+    if constexpr (N == 2) {
+        hi = fmaxf(v[0], v[1]);
+        lo = fminf(v[0], v[1]);
+    } else {
+        float h0, l0, h1, l1;
+        two_largest<N / 2>(v, h0, l0);
+        two_largest<N / 2>(v + N / 2, h1, l1);
+        hi = fmaxf(h0, h1);
+        lo = fmaxf(fminf(h0, h1), fmaxf(l0, l1));
+    }
+}
+
+// What a thread keeps of the logits it has seen: the largest, the step it came in and the next largest, and the sum of
+// exp(v - ref) as 2^(v L - c), c = ref L rounded; the factor 2^(c - ref L) is put in at the end.  ref follows the maximum
+// only in large steps: any of the logits near it serves.
 struct Seen {
-    float best = -INFINITY, ref = -INFINITY, c = 0.0f, sum = 0.0f;
-    template <int N> __device__ __forceinline__ void add(const float (&v)[N])
+    float best = -INFINITY, next = -INFINITY, ref = -INFINITY, c = 0.0f, sum = 0.0f;
+    int at = 0;
+    template <int N> __device__ __forceinline__ void add(const float (&v)[N], int step)
     {
-        float m = v[0];                                 // fmaxf passes over NaN
-#pragma unroll
-        for (int e = 1; e < N; e++)
-            m = fmaxf(m, v[e]);
+        float m, second;
+        two_largest<N>(v, m, second);
+        next = fmaxf(next, fmaxf(second, fminf(best, m)));
+        at = m > best ? step : at;
         best = fmaxf(best, m);
         if (m > ref + 40.0f && m <= FLT_MAX) {
             const float to = m * LOG2E;
@@ -261,7 +277,7 @@ template <typename T, bool VECTOR> __device__ __forceinline__ void stream_logits
             for (int d = 0; d < DEPTH; d++) {
                 float v[N];
                 unpack(raw[d], v, l);
-                seen.add(v);
+                seen.add(v, s + d);
                 raw[d] = __ldg(at + d * THREADS);
             }
         }
@@ -271,7 +287,7 @@ template <typename T, bool VECTOR> __device__ __forceinline__ void stream_logits
             if (s + d < steps) {
                 float v[N];
                 unpack(raw[d], v, l);
-                seen.add(v);
+                seen.add(v, s + d);
                 if (s + DEPTH + d < steps)
                     raw[d] = __ldg(at + d * THREADS);
             }
@@ -280,7 +296,7 @@ template <typename T, bool VECTOR> __device__ __forceinline__ void stream_logits
             if (s + DEPTH + d < steps) {
                 float v[N];
                 unpack(raw[d], v, l);
-                seen.add(v);
+                seen.add(v, s + DEPTH + d);
             }
     } else {
         constexpr int FLIGHT = 16 / N;
@@ -297,7 +313,7 @@ template <typename T, bool VECTOR> __device__ __forceinline__ void stream_logits
                 }
 #pragma unroll
             for (int d = 0; d < FLIGHT; d++)
-                seen.add(raw[d]);
+                seen.add(raw[d], s + d);
             t += FLIGHT * STEP;
         }
     }
@@ -345,8 +361,8 @@ __device__ __noinline__ void list_by_keys(Pick &sh, const T *l, int t0, int t1, 
 }
 
 // One CTA per (chunk, row).  The threads stream through the chunk's logits, with no barrier, and keep their maxima and
-// sums.  The maxima then give a bound that about K + 1 logits reach: only the threads (a few) whose maximum does are
-// looked at again, eight lanes reading one thread's logits out of L2.
+// sums.  The maxima then give a bound that about K + 1 logits reach: a thread (of the few) whose maximum does reads that
+// one's vector again; where its next largest does too, eight lanes go over all of the thread's logits.
 template <typename T> __global__ void __launch_bounds__(THREADS, 5) kda_beam_chunks_kernel(const BeamArgs p)
 {
     constexpr int N = Vec<T>::N, STEP = THREADS * N;
@@ -392,7 +408,22 @@ template <typename T> __global__ void __launch_bounds__(THREADS, 5) kda_beam_chu
     const bool by_keys = !(fabsf(bound) <= FLT_MAX);       // too few finite values for a bound
     if (!by_keys) {
         constexpr int TURNS = 16 / N;                      // of eight lanes over a thread's vectors, in flight together
-        for (unsigned owners = __ballot_sync(FULL, best >= bound); owners;) {
+        const bool more = seen.next >= bound;
+        if (best >= bound && !more) {
+            const int t = t0 + (seen.at * THREADS + tid) * N;
+            float x[N];
+#pragma unroll
+            for (int e = 0; e < N; e++)
+                x[e] = t + e < t1 ? load_logit(l + t + e) : -INFINITY;
+#pragma unroll
+            for (int e = 0; e < N; e++)
+                if (x[e] >= bound) {
+                    const int to = atomicAdd(&sh.count, 1);
+                    if (to < p.room)
+                        list[to] = key_of(x[e], t + e);
+                }
+        }
+        for (unsigned owners = __ballot_sync(FULL, best >= bound && more); owners;) {
             int of = -1;
 #pragma unroll
             for (int k = 0; k < 4; k++)
