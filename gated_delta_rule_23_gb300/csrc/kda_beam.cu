@@ -102,7 +102,7 @@ struct Pick {
     uint64_t cand[CAP];
     uint64_t red[32];
     uint64_t bound;
-    float value;
+    uint32_t lowest;
     int count;
 };
 
@@ -146,38 +146,45 @@ template <int NT> __device__ __forceinline__ uint64_t group_bound(Pick &sh, uint
     return groups_for(n) == 64 ? group_bound_of<NT, 64>(sh, best, n) : group_bound_of<NT, 128>(sh, best, n);
 }
 
-// The same on values alone, rounded down to 24 bits: a value that the n best groups' best values reach; NaN when fewer
-// groups than n have one above -inf.  One warp finds it bit by bit.
-template <int NT> __device__ float group_bound_value(Pick &sh, float best, int n)
+// The same on values alone: the n-th best (ties counted) of the groups' best values, NaN or -inf when fewer groups than n
+// have one above -inf.
+template <int NT, int GROUPS> __device__ __forceinline__ float group_bound_value_of(Pick &sh, float best, int n)
 {
-    const int groups = groups_for(n), size = NT / groups, lane = threadIdx.x % 32;
+    constexpr int SIZE = NT / GROUPS;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     uint32_t *g = reinterpret_cast<uint32_t *>(sh.group);
-    for (int o = 1; o < size; o <<= 1)
+#pragma unroll
+    for (int o = 1; o < SIZE; o <<= 1)
         best = fmaxf(best, __shfl_xor_sync(FULL, best, o));
-    if (threadIdx.x % size == 0)
-        g[threadIdx.x / size] = (uint32_t)(key_of(best, 0) >> 32);
-    if (threadIdx.x == 0)
+    if (threadIdx.x % SIZE == 0)
+        g[threadIdx.x / SIZE] = (uint32_t)(key_of(best, 0) >> 32);
+    if (threadIdx.x == 0) {
         sh.count = 0;
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        uint32_t u[4], at = 0;
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            u[i] = i * 32 < groups ? g[i * 32 + lane] : 0;
-#pragma unroll
-        for (int bit = 31; bit >= 8; bit--) {
-            const uint32_t to = at | (1u << bit);
-            int have = __popc(__ballot_sync(FULL, u[0] >= to)) + __popc(__ballot_sync(FULL, u[1] >= to));
-            if (groups > 64)
-                have += __popc(__ballot_sync(FULL, u[2] >= to)) + __popc(__ballot_sync(FULL, u[3] >= to));
-            if (have >= n)
-                at = to;
-        }
-        if (lane == 0)
-            sh.value = key_value((uint64_t)at << 32);
+        sh.lowest = FULL;
     }
     __syncthreads();
-    return sh.value;
+    uint32_t all[GROUPS / 32], low = FULL;
+#pragma unroll
+    for (int j = 0; j < GROUPS / 32; j++)
+        all[j] = g[32 * j + lane];
+#pragma unroll
+    for (int i = 0; i < GROUPS * 32 / NT; i++) {                   // a warp ranks a group
+        const uint32_t x = g[i * (NT / 32) + warp];
+        int above = 0;
+#pragma unroll
+        for (int j = 0; j < GROUPS / 32; j++)
+            above += __popc(__ballot_sync(FULL, all[j] > x));
+        if (above < n)                                             // the smallest of the values that fewer than n are above
+            low = min(low, x);
+    }
+    if (lane == 0)
+        atomicMin(&sh.lowest, low);
+    __syncthreads();
+    return key_value((uint64_t)sh.lowest << 32);
+}
+template <int NT> __device__ __forceinline__ float group_bound_value(Pick &sh, float best, int n)
+{
+    return groups_for(n) == 64 ? group_bound_value_of<NT, 64>(sh, best, n) : group_bound_value_of<NT, 128>(sh, best, n);
 }
 
 // Ranks the gathered keys (count of them, all distinct) and hands the best n to put(rank, key), by one thread each.
@@ -690,7 +697,7 @@ static int beam_chunks(int B, int W, int V)
     const int chunk = beam_chunk(B, W, V);
     return (V + chunk - 1) / chunk;
 }
-// Keys of a list: more than K + 1 reach a bound that is rounded down and may be tied.
+// Keys of a list: some more than K + 1 reach the bound, or tie at it.
 static int beam_room(int K) { return (2 * K + 32) / 32 * 32; }
 
 namespace {
