@@ -33,7 +33,8 @@ template <int DIM, int WARPS> struct Shape {
     static constexpr int RING = DIM == 128 ? 3 : 6;              // blocks in flight a warp
     static constexpr int BLOCK = KEYS * DIM * 2;                 // bytes of K, and of V
     static constexpr int WARP = RING * 2 * BLOCK;                // a warp's ring
-    static constexpr int SMEM = 1024 + WARPS * WARP;
+    static constexpr int RECV = WARPS * WARP;                    // what a cluster's CTAs send: ROWS rows of DIM floats
+    static constexpr int SMEM = 1024 + RECV + ROWS * DIM * 4;
     static_assert(WARP >= ROWS * DIM * 4, "O of a warp goes where its ring was");
 };
 
@@ -48,18 +49,16 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t block, int key, int c)
 {
     return block + (c / 8) * (KEYS * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4);
 }
-// The same shared-memory address in CTA `rank` of the cluster, and a load from there
+// The same shared-memory address in CTA `rank` of the cluster, and a store there
 __device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank)
 {
     uint32_t x;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(x) : "r"(addr), "r"(rank));
     return x;
 }
-__device__ __forceinline__ float2 load_cluster(uint32_t addr)
+__device__ __forceinline__ void store_cluster(uint32_t addr, float2 x)
 {
-    float2 x;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(addr) : "memory");
-    return x;
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x.x), "f"(x.y) : "memory");
 }
 // Every CTA of the cluster comes here, whatever its waits did, so that this wait always ends.
 __device__ __forceinline__ void cluster_sync()
@@ -99,9 +98,10 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
     constexpr int CB = DIM / 64, KS = DIM / 16, NT = DIM / 8;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t bars[WARPS * S::RING];
-    __shared__ float2 stats[WARPS][ROWS], joined[ROWS];
-    __shared__ int failed_cta;
+    __shared__ float2 stats[WARPS][ROWS], recv_stats[ROWS], recv_failed[CLUSTER];
     asm volatile("griddepcontrol.launch_dependents;");
+    if (plan.cluster)                                            // waited for before anything is sent: every CTA has begun
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     if (threadIdx.x == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
@@ -313,9 +313,12 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
             attn_mend_row<DIM>(p, n, (int64_t)n * tokens + tok, head, p0 + tok, bad);
     };
     bool failed = __syncthreads_or(timeout);
-    // the CTA's part of the cluster's results: behind O in the first warp's ring
-    static_assert(S::WARP >= 2 * ROWS * DIM * 4, "room for the CTA's O");
-    float *const cta_o = reinterpret_cast<float *>(smem) + ROWS * DIM;
+    if (plan.cluster)
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    // Row r of a cluster's item is finished by its CTA r % splits, which the others send their parts of it: place
+    // (sender, r / splits) of its receiving area, which is nobody's ring.
+    float *const recv = reinterpret_cast<float *>(smem + S::RECV);
+    const int places = ROWS / plan.splits;
     if (!failed) {
         for (int row = warp; row < rows; row += WARPS) {         // a warp joins a row
             float2 st[WARPS], y[PIECES];
@@ -341,52 +344,44 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
                 finish(row, M, L, y, plan.splits == 1);
                 continue;
             }
+            const int to = row % plan.splits, place = split * places + row / plan.splits;
 #pragma unroll
             for (int c = 0; c < PIECES; c++)
-                *reinterpret_cast<float2 *>(cta_o + row * DIM + 64 * c + 2 * lane) = y[c];
+                store_cluster(in_cta(smem_u32(recv + place * DIM + 64 * c + 2 * lane), to), y[c]);
             if (lane == 0)
-                joined[row] = make_float2(M, L);
+                store_cluster(in_cta(smem_u32(&recv_stats[place]), to), make_float2(M, L));
         }
     }
     if (plan.cluster) {
-        if (tid == 0)
-            failed_cta = failed;
-        __syncthreads();
+        if (tid < plan.splits)
+            store_cluster(in_cta(smem_u32(&recv_failed[split]), tid), make_float2(failed ? 1.0f : 0.0f, 0.0f));
         cluster_sync();
-        for (int i = 0; i < plan.splits; i++) {
-            int x = 0;
-            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(in_cta(smem_u32(&failed_cta), i)) : "memory");
-            failed |= x != 0;
-        }
-        if (!failed) {
-            for (int row = split + plan.splits * warp; row < rows; row += plan.splits * WARPS) {
-                float2 st[CLUSTER], y[PIECES];
-                float w[CLUSTER], M, L;
+        for (int i = 0; i < plan.splits; i++)
+            failed |= recv_failed[i].x != 0.0f;
+        for (int k = warp; k < places && !failed; k += WARPS) {
+            const int row = split + plan.splits * k;
+            if (row >= rows)
+                break;
+            float2 st[CLUSTER], y[PIECES];
+            float w[CLUSTER], M, L;
 #pragma unroll
-                for (int i = 0; i < CLUSTER; i++)
-                    st[i] = i < plan.splits ? load_cluster(in_cta(smem_u32(&joined[row]), i)) : make_float2(-INFINITY, 0.0f);
-                float2 z[CLUSTER][PIECES];
+            for (int i = 0; i < CLUSTER; i++)
+                st[i] = i < plan.splits ? recv_stats[i * places + k] : make_float2(-INFINITY, 0.0f);
+            join_stats(st, w, M, L);
 #pragma unroll
-                for (int i = 0; i < CLUSTER; i++)
+            for (int c = 0; c < PIECES; c++) {
+                y[c] = make_float2(0.0f, 0.0f);
 #pragma unroll
-                    for (int c = 0; c < PIECES; c++)
-                        z[i][c] = i < plan.splits ? load_cluster(in_cta(smem_u32(cta_o + row * DIM + 64 * c + 2 * lane), i))
-                                                  : make_float2(0.0f, 0.0f);
-                join_stats(st, w, M, L);
-#pragma unroll
-                for (int c = 0; c < PIECES; c++) {
-                    y[c] = make_float2(0.0f, 0.0f);
-#pragma unroll
-                    for (int i = 0; i < CLUSTER; i++)
-                        if (w[i] >= 0.0f || w[i] != w[i]) {
-                            y[c].x = fmaf(w[i], z[i][c].x, y[c].x);
-                            y[c].y = fmaf(w[i], z[i][c].y, y[c].y);
-                        }
+                for (int i = 0; i < CLUSTER; i++) {
+                    if (i >= plan.splits || w[i] < 0.0f)
+                        continue;
+                    const float2 z = *reinterpret_cast<const float2 *>(recv + (i * places + k) * DIM + 64 * c + 2 * lane);
+                    y[c].x = fmaf(w[i], z.x, y[c].x);
+                    y[c].y = fmaf(w[i], z.y, y[c].y);
                 }
-                finish(row, M, L, y, true);
             }
+            finish(row, M, L, y, true);
         }
-        cluster_sync();                                          // no CTA leaves while its results are read
     }
     report(p.err, bad, DEVERR_CU_SEQLENS);
     report(p.err, timeout, DEVERR_TIMEOUT);
