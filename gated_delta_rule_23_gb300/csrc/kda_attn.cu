@@ -170,21 +170,35 @@ AttnPlan make_plan(int window, int sinks, bool varlen, int N, int64_t T, int Hq,
     plan.rows = tokens * Hq;
     plan.wait_polls = wait_limit();
     const int sms = device_sms();
-    if (!varlen && T * group <= DECODE_ROWS) {
-        // Two CTAs an SM; a split has 128 keys at least (every warp two blocks).  A cluster of up to 8 splits saves the
-        // second launch: taken unless its CTAs are left with over 1024 keys that more splits would share.
-        plan.decode = true;
-        plan.granule = DECODE_KEYS;
-        const int64_t ctas = (int64_t)N * Hkv, keys = most_keys(window, sinks, T, page, max_pages), most = keys / 128;
-        int64_t s = ctas > 0 ? 2 * sms / ctas : 1;
+    // The decode kernel: wherever 16 rows hold a key head's queries.  Splits of the keys are a cluster of 8, 4 or 2 CTAs of
+    // 128 keys at least (every warp two blocks); with over 8192 keys and room for more than 8 splits they go through memory.
+    // 8 splits are taken for up to sms / 16 key heads: clusters of 8 CTAs that fill an SM each leave SMs over, so 16 of them
+    // do not run at once (2048 keys: 14.4 us with 8 splits, 10.3 with 4).  4 and 2 splits while each CTA has its SM: 64 key
+    // heads gain nothing from a second CTA an SM (512 keys: 9.7 us with 4, 8.6 with 2), 128 lose by it (16.1 with 4,
+    // 10.3 with 2 or 1).
+    // With more rows, up to the tile kernel's 256, tiles of 16 take it as well while their CTAs run at once and none has
+    // over 1152 keys: they read the keys again, out of L2, but fill no 128-key tiles and wait for fewer hand-overs.
+    // Measured, 64 heads over 8, decode | tile kernel: 16 tokens of one sequence, window 512: 10.3 | 14.4 us, 2048: 14.6 |
+    // 18.4, 4096: 20.6 | 19.0; 16 tokens of four, window 512: 14.4 | 16.5, 1024: 20.5 | 18.6.
+    const int64_t row_tiles = (T * group + DECODE_ROWS - 1) / DECODE_ROWS, ctas16 = (int64_t)N * Hkv * row_tiles;
+    if (!varlen && (row_tiles == 1 || (row_tiles <= ATTN_ROWS / DECODE_ROWS && ctas16 <= sms))) {
+        const int64_t keys = most_keys(window, sinks, T, page, max_pages), most = keys / 128;
+        int64_t s = ctas16 > 0 ? 2 * sms / ctas16 : 1;
         s = s < most ? s : most;
-        s = s < 1 ? 1 : (s > 64 ? 64 : s);
-        plan.cluster = s > 1 && (s <= DECODE_CLUSTER || keys <= 1024 * DECODE_CLUSTER);
+        s = s > 64 ? 64 : s;
+        plan.cluster = s <= DECODE_CLUSTER || keys <= 1024 * DECODE_CLUSTER;
         if (plan.cluster)
-            s = s >= 8 ? 8 : (s >= 4 ? 4 : 2);
-        plan.splits = (int)s;
-        plan.items = (int)(ctas * plan.splits);
-        return plan;
+            s = s >= 8 && 16 * ctas16 <= sms ? 8 : (s >= 4 && 4 * ctas16 <= sms ? 4 : (s >= 2 && 2 * ctas16 <= sms ? 2 : 1));
+        plan.cluster = plan.cluster && s > 1;
+        if (row_tiles == 1 || (s <= DECODE_CLUSTER && keys <= 1152 * s)) {
+            plan.decode = true;
+            plan.row_tiles = (int)row_tiles;
+            plan.granule = DECODE_KEYS;
+            plan.splits = s < 1 ? 1 : (int)s;
+            plan.items = (int)(ctas16 * plan.splits);
+            return plan;
+        }
+        plan.cluster = false;
     }
     plan.granule = page < 32 ? page : 32;
     plan.run = ATTN_ROWS / group;

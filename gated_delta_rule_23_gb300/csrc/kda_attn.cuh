@@ -28,7 +28,8 @@ constexpr int DECODE_ROWS = 16, DECODE_KEYS = 16;   // rows of the decode kernel
 constexpr int DECODE_CLUSTER = 8;                   // splits that join in a cluster
 
 struct AttnPlan {
-    bool decode;            // at most 16 query rows a (sequence, key head): the decode kernel, one item a CTA
+    bool decode;            // few query rows: the decode kernel, one item a CTA
+    int row_tiles;          // of 16 rows, of a (sequence, key head) (decode kernel)
     bool cluster;           // the splits are a cluster of the decode kernel (no workspace, no join kernel)
     int splits;
     int items;              // (row tile, key head, split) items (ragged: an upper bound)

@@ -1,4 +1,4 @@
-// Windowed attention over the paged cache for few query rows: at most 16 (tokens x heads of a key head's group).
+// Windowed attention over the paged cache for few query rows: 16 (tokens x heads of a key head's group) a CTA.
 //
 // A decode step reads every visible key and value once for a handful of rows: the floor is the cache's bytes at the
 // memory's rate, and the arithmetic (16 rows wide on mma.sync) has to stay out of the way.  One CTA takes a (sequence, key
@@ -6,12 +6,13 @@
 // brings in with bulk tensor copies into the warp's own ring of shared memory: no barrier of the CTA in the loop, and
 // RING x 8 KB in flight a warp.  The warps' results (running maximum, sum, O in fp32) are joined once at the end in shared
 // memory.  Up to 8 splits are a cluster, which joins its CTAs' results over distributed shared memory in the same
-// launch; more go through memory and the join kernel.
+// launch; more go through memory and the join kernel.  Small calls with more rows are tiles of 16 rows, one a CTA.
 //
 // Measured: 256 sequences, 64 heads over 8, window 1024 and 16 sinks (1.10 GB), 164 us, 6.70 TB/s, 99% of the measured copy
-// rate (the tile kernel: 255 us).  One sequence, 32 heads over 8, window 4096: 12.3 us, a chain of latencies (lengths, page
-// table, copies, four blocks a warp, the joins); 8 splits in a cluster and 32 splits with a join kernel take the same in a
-// row of calls, the cluster 3 us less alone.
+// rate (the tile kernel: 255 us).  One sequence, 32 heads over 8, window 4096: 10.3 us, a chain of latencies (lengths, page
+// table, copies, four blocks a warp, the joins); the CTAs of a cluster send each row's parts to the CTA that finishes it,
+// which takes one barrier (10.3 us; one CTA that reads the others' parts between two barriers: 12.3 us, as do 32 splits
+// with a join kernel).
 //
 // Keys come as in the tile kernel: the sinks' granules, then the window's, 16 positions each, which lie in one page.
 // Values that no row of the CTA sees are cleared in shared memory; where the rows differ in what they see (several
@@ -113,8 +114,10 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
     int x = blockIdx.x;
     const int split = x % plan.splits;                           // the splits of an item are neighbours: a cluster
     x /= plan.splits;
+    const int row0 = x % plan.row_tiles * ROWS;                  // first of the CTA's rows among those of its key head
+    x /= plan.row_tiles;
     const int kvh = x % p.cache.hkv, n = x / p.cache.hkv;
-    const int tokens = (int)p.tok.T, rows = tokens * p.group;
+    const int tokens = (int)p.tok.T, rows = min(tokens * p.group - row0, ROWS);
     bool bad = false, timeout = false;
     // Q as the first operand: rows g and g + 8; on its way while the lengths and the page table are read
     uint32_t q[KS][4];
@@ -122,9 +125,9 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
     for (int r = 0; r < 2; r++) {
         const int row = g + 8 * r;
         const bool in = row < rows;
-        const int tok = in ? row / p.group : 0;
+        const int tok = in ? (row0 + row) / p.group : 0;
         const uint32_t *src = reinterpret_cast<const uint32_t *>(
-            p.q + (int64_t)(n * tokens + tok) * p.q_stride + (kvh * p.group + (in ? row % p.group : 0)) * DIM);
+            p.q + (int64_t)(n * tokens + tok) * p.q_stride + (kvh * p.group + (in ? (row0 + row) % p.group : 0)) * DIM);
 #pragma unroll
         for (int k = 0; k < KS; k++) {
             q[k][r] = in ? __ldg(src + 8 * k + t) : 0;
@@ -132,11 +135,12 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
         }
     }
     const int len = (int)cache_len(p.cache, n, bad);
-    const int p0 = len - tokens, p1 = len - 1;                   // positions of the first and the last token
+    // positions of the first and the last row's tokens
+    const int p0 = len - tokens + row0 / p.group, p1 = len - tokens + (row0 + rows - 1) / p.group;
     int pos[2];
 #pragma unroll
     for (int r = 0; r < 2; r++)
-        pos[r] = g + 8 * r < rows ? p0 + (g + 8 * r) / p.group : -1;
+        pos[r] = g + 8 * r < rows ? len - tokens + (row0 + g + 8 * r) / p.group : -1;
     // virtual keys: the sinks' granules, then the window's
     int sink = 0, start = 0, virt = 0;
     if (p1 >= 0) {
@@ -290,7 +294,7 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
     // a row's place in the batch, and its last step: the result, or the split's part of it
     constexpr int PIECES = DIM / 64;                             // float2's a lane has of a row
     auto finish = [&](int row, float M, float L, const float2 (&y)[PIECES], bool whole) {
-        const int tok = row / p.group, head = kvh * p.group + row % p.group;
+        const int tok = (row0 + row) / p.group, head = kvh * p.group + (row0 + row) % p.group;
         const int64_t at = (int64_t)(n * tokens + tok) * p.hq + head;
         const float inv = L == 0.0f ? 0.0f : 1.0f / L;
         bool finite = true;
@@ -310,7 +314,7 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
                 p.lse[at] = L == 0.0f ? -INFINITY : LN2 * (M + log2f(L));
         }
         if (whole && L > 0.0f && L <= FLT_MAX && __any_sync(FULL, !finite))
-            attn_mend_row<DIM>(p, n, (int64_t)n * tokens + tok, head, p0 + tok, bad);
+            attn_mend_row<DIM>(p, n, (int64_t)n * tokens + tok, head, len - tokens + tok, bad);
     };
     bool failed = __syncthreads_or(timeout);
     if (plan.cluster)

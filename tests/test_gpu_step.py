@@ -121,6 +121,22 @@ def test_attn_given_back_pages(kda, new):
           keep=lambda n, p: p < 1 or (p + 1) * page > lens[n] - new - window + 1)
 
 
+# Query rows in several tiles of 16: tokens that two tiles share, a last tile of one row, 256 rows and one more, sequences
+# shorter than their tokens, windows of one key and of fewer keys than a tile has tokens; few and many key heads.
+ROW_TILES = [
+    ([900], [6], 6, 2, 128, 16, 200, 3), ([33], [33], 5, 5, 64, 32, 9, 0), ([700, 20], [17, 17], 10, 2, 128, 16, 1, 1),
+    ([400, 0, 7], [11, 11, 11], 24, 2, 64, 128, 150, 4), ([2000], [32], 8, 1, 128, 64, 1024, 4),
+    ([2000], [257], 1, 1, 128, 16, 600, 0), ([1500], [3], 64, 1, 128, 16, 1000, 0), ([260, 255], [256, 256], 1, 1, 64, 16, 40, 2),
+    ([600] * 12, [20] * 12, 4, 2, 128, 32, 100, 2), ([3000], [9], 16, 8, 64, 16, 2500, 1), ([1200], [2], 13, 1, 128, 16, 1100, 0),
+]
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("case", ROW_TILES, ids=[str(i) for i in range(len(ROW_TILES))])
+def test_attn_row_tiles(kda, case, ragged):
+    _attn(kda, *case, ragged)
+
+
 @pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
 @pytest.mark.parametrize("new, hq", [(1, 8), (2, 4), (140, 4)])
 def test_attn_values_out_of_sight(kda, value, new, hq):
