@@ -15,7 +15,8 @@
 // The running maximum m is moved (and O and l rescaled) only when a row's maximum has grown by more than 2^8: any m
 // gives the same quotient, and 2^8 is far from overflow in the fp32 sums.  So a tile's exponentials do not wait for its
 // maximum: they are taken with the m at hand while the maximum is formed, and taken again (S still stands; P is stored
-// last) in the rare tile that moves m.
+// last) in the rare tile that moves m.  A row's first m is 0 when its first keys' maximum is within 2^8 of that either way.
+// (Reading S once for the maximum and once more for P there: 137 us for the ragged prompts below.)
 //
 // Warps 0..3 and 4..7: the halves' softmax and epilogue; warp 8: bulk tensor copies of K and V tiles into a ring; warps 9
 // and 10: tensor-core issue for a half each (one thread for both halves spent longer issuing than the tensor cores took:
@@ -25,7 +26,7 @@
 // between them and 16,000 in them.)
 //
 // Measured (bf16 rate 1875 TFLOP/s): 8192 tokens, 96 heads over 8, full window, 1.33 ms, 1243 TFLOP/s, 66%; 12 ragged
-// prompts of 8192 tokens in all, 64 heads over 8, window 512 and 4 sinks, 137 us.  What bounds it: a step of both halves takes
+// prompts of 8192 tokens in all, 64 heads over 8, window 512 and 4 sinks, 131 us.  What bounds it: a step of both halves takes
 // 1500 cycles, about what its products take with S in pieces of 64 keys, whose operands both come from shared memory (6 KB
 // for 32 cycles of tensor time, against 128 bytes a cycle); the softmax is busy for 870 of them.  Short windows pay the
 // 6000 cycles between items and the masked edges besides.
@@ -395,19 +396,6 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                     return fmaxf(x, y);
                 };
                 float s[2][32];
-                if (!any) {                                      // the first tile: m is its maximum
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < SUB / 32; c++) {
-                        tmem_get32(tm_s + 32 * c, s[0]);
-                        tmem_wait32(s[0]);
-                        hide(s[0], c);
-                        top = top_of(s[0], top);
-                    }
-                    top *= p.scale_log2;
-                    if (top > m)                                 // not for NaN
-                        m = top;
-                }
                 uint32_t pk[SUB / 2];
                 f2 l0, l1;
                 for (;;) {
@@ -436,6 +424,8 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                         }
                     }
                     top *= p.scale_log2;
+                    if (m == -INFINITY && fabsf(top) <= RESCALE_AT)
+                        m = 0.0f;                                // the row's first keys: what P was formed with will do
                     const bool move = top > m + RESCALE_AT;
                     if (!__any_sync(FULL, move))
                         break;
