@@ -477,59 +477,85 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             // Epilogue: the row's thread scales it; 128 bytes of each row at a time go through shared memory (16-byte
             // chunks, swizzled) and out with eight lanes to a row.  (Stored straight by its thread, a row took a line of L1
             // for every 16 bytes: 148 us for ragged 8192 tokens with window 512.)
-            bool finite = true;
             const int at = mine ? tok * p.hq + head : -1;
             const bool part = plan.splits > 1;
             const float inv = part ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+            const bool blank = __any_sync(FULL, l == 0.0f && !part);         // rows that see nothing: 0
+            const f2 inv2 = f2_pack(inv, inv);
+            f2 z0 = 0, z1 = 0;                                   // stay 0 while the row is finite
             unsigned char *const stage = smem + S::OUT + warp * S::STAGE;
+            int out_row[8];                                      // of the rows this lane takes out
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                out_row[k] = __shfl_sync(FULL, at, 4 * k + lane / 8);
             auto put = [&](int chunk, const uint4 &x) {
                 *reinterpret_cast<uint4 *>(stage + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = x;
             };
             auto flush = [&](unsigned char *to, int64_t row_bytes) {
                 __syncwarp();
+                uint4 x[8];
 #pragma unroll
-                for (int r0 = 0; r0 < 32; r0 += 4) {
-                    const int r = r0 + lane / 8, chunk = lane % 8, row = __shfl_sync(FULL, at, r);
-                    const uint4 x = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((chunk ^ (r & 7)) << 4));
-                    if (row >= 0)
-                        *reinterpret_cast<uint4 *>(to + row * row_bytes + chunk * 16) = x;
+                for (int k = 0; k < 8; k++) {
+                    const int r = 4 * k + lane / 8;
+                    x[k] = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((lane % 8 ^ (r & 7)) << 4));
                 }
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    if (out_row[k] >= 0)
+                        *reinterpret_cast<uint4 *>(to + out_row[k] * row_bytes + lane % 8 * 16) = x[k];
                 __syncwarp();
             };
 #pragma unroll
-            for (int c = 0; c < DIM; c += 32) {
-                float o[32];
+            for (int c = 0; c < DIM; c += 64) {
+                float o[2][32];
                 if (any) {
-                    tmem_get32(tm_o + c, o);
-                    tmem_wait32(o);
+                    tmem_get32(tm_o + c, o[0]);
+                    tmem_get32(tm_o + c + 32, o[1]);
+                    tmem_wait32(o[0]);
+                    tmem_wait32(o[1]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 64; e++)
+                        o[e / 32][e % 32] = 0.0f;
                 }
 #pragma unroll
-                for (int e = 0; e < 32; e++) {
-                    const float y = any ? o[e] : 0.0f;
-                    finite &= fabsf(y) <= FLT_MAX;
-                    o[e] = part || l != 0.0f ? y * inv : 0.0f;
+                for (int e = 0; e < 64; e += 2) {
+                    float &x = o[e / 32][e % 32], &y = o[e / 32][e % 32 + 1];
+                    const f2 xy = f2_pack(x, y), q = f2_mul(xy, inv2);
+                    if (e & 2)
+                        z1 = f2_fma(xy, 0, z1);
+                    else
+                        z0 = f2_fma(xy, 0, z0);
+                    x = f2_lo(q), y = f2_hi(q);
                 }
                 if (part) {
 #pragma unroll
-                    for (int e = 0; e < 8; e++)
-                        put(e, make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
-                                          __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3])));
-                    flush(reinterpret_cast<unsigned char *>(plan.part_o + w.split * plan.rows * DIM + c), DIM * 4);
+                    for (int i = 0; i < 2; i++) {
+#pragma unroll
+                        for (int e = 0; e < 8; e++)
+                            put(e, make_uint4(__float_as_uint(o[i][4 * e]), __float_as_uint(o[i][4 * e + 1]),
+                                              __float_as_uint(o[i][4 * e + 2]), __float_as_uint(o[i][4 * e + 3])));
+                        flush(reinterpret_cast<unsigned char *>(plan.part_o + w.split * plan.rows * DIM + c + 32 * i), DIM * 4);
+                    }
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 4; e++) {
+                    for (int e = 0; e < 8; e++) {
                         uint32_t y[4];
 #pragma unroll
                         for (int j = 0; j < 4; j++) {
-                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[8 * e + 2 * j], o[8 * e + 2 * j + 1]);
+                            const int i = 8 * e + 2 * j;
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[i / 32][i % 32], o[i / 32][i % 32 + 1]);
                             y[j] = *reinterpret_cast<const uint32_t *>(&b2);
                         }
-                        put((c % 64) / 8 + e, make_uint4(y[0], y[1], y[2], y[3]));
+                        if (blank && l == 0.0f)
+                            y[0] = y[1] = y[2] = y[3] = 0;
+                        put(e, make_uint4(y[0], y[1], y[2], y[3]));
                     }
-                    if (c % 64 == 32)
-                        flush(reinterpret_cast<unsigned char *>(p.out + c - 32), DIM * 2);
+                    flush(reinterpret_cast<unsigned char *>(p.out + c), DIM * 2);
                 }
             }
+            z0 = f2_add(z0, z1);
+            const bool finite = f2_lo(z0) + f2_hi(z0) == 0.0f;
             tc_fence_before();                // O is read before the next item's first P lets it be overwritten
             if (mine && part)
                 plan.part_ml[w.split * plan.rows + at] = make_float2(m, l);
