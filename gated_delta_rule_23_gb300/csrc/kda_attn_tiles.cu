@@ -25,11 +25,11 @@
 // (When every warp worked out the items for itself and the softmax warps loaded Q, an item of 9 steps spent 13,000 cycles
 // between them and 16,000 in them.)
 //
-// Measured (bf16 rate 1875 TFLOP/s): 8192 tokens, 96 heads over 8, full window, 1.33 ms, 1243 TFLOP/s, 66%; 12 ragged
-// prompts of 8192 tokens in all, 64 heads over 8, window 512 and 4 sinks, 131 us.  What bounds it: a step of both halves takes
+// Measured (bf16 rate 1875 TFLOP/s): 8192 tokens, 96 heads over 8, full window, 1.29 ms, 1280 TFLOP/s, 68%; 12 ragged
+// prompts of 8192 tokens in all, 64 heads over 8, window 512 and 4 sinks, 121 us.  What bounds it: a step of both halves takes
 // 1500 cycles, about what its products take with S in pieces of 64 keys, whose operands both come from shared memory (6 KB
 // for 32 cycles of tensor time, against 128 bytes a cycle); the softmax is busy for 870 of them.  Short windows pay the
-// 6000 cycles between items and the masked edges besides.
+// 5000 cycles between items and the masked edges besides.
 //
 // A key that a row does not see gets P = 0.  0 x v is NaN for an infinite or NaN v, and the matrix product has no way
 // to skip it: rows past the sequence's end are cleared in shared memory, and an output row that does not come out
@@ -345,8 +345,9 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
         // Phases of the two S, and of the P V of an item's last two key tiles, the only ones that are waited for as such: a
         // half's S of tile t + 1 is issued right after its P V of tile t - 1.
         uint32_t s_phase = 0, o_phase = 0;
-        Tile w;
-        for (int i = 0; next_item(i, w); i++) {
+        Tile w, next;
+        bool more = next_item(0, w);
+        for (int i = 1; more; i++, w = next) {
             const bool mine = tid < w.rows;
             const int r_tok = mine ? token_of(plan, tid) : 0;
             const int tok = w.tok0 + r_tok, head = w.kvh * p.group + (mine ? tid - r_tok * p.group : 0);
@@ -466,6 +467,20 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             if (timeout)
                 break;
             ring += w.t1 - w.t0;
+            // What of the epilogue needs no O, and the next item, while the last P V runs.
+            const int at = mine ? tok * p.hq + head : -1;
+            const bool part = plan.splits > 1;
+            const float inv = part ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+            const bool blank = __any_sync(FULL, l == 0.0f && !part);         // rows that see nothing: 0
+            int out_row[8];                                      // of the rows this lane takes out
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                out_row[k] = __shfl_sync(FULL, at, 4 * k + lane / 8);
+            if (mine && part)
+                plan.part_ml[w.split * plan.rows + at] = make_float2(m, l);
+            else if (mine && p.lse)
+                p.lse[at] = l == 0.0f ? -INFINITY : LN2 * (m + log2f(l));
+            more = next_item(i, next);
             if (any) {
                 // the last P V: those before it are through with it
                 const int last_buf = (hi - 1) & 1;
@@ -477,17 +492,9 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             // Epilogue: the row's thread scales it; 128 bytes of each row at a time go through shared memory (16-byte
             // chunks, swizzled) and out with eight lanes to a row.  (Stored straight by its thread, a row took a line of L1
             // for every 16 bytes: 148 us for ragged 8192 tokens with window 512.)
-            const int at = mine ? tok * p.hq + head : -1;
-            const bool part = plan.splits > 1;
-            const float inv = part ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
-            const bool blank = __any_sync(FULL, l == 0.0f && !part);         // rows that see nothing: 0
             const f2 inv2 = f2_pack(inv, inv);
             f2 z0 = 0, z1 = 0;                                   // stay 0 while the row is finite
             unsigned char *const stage = smem + S::OUT + warp * S::STAGE;
-            int out_row[8];                                      // of the rows this lane takes out
-#pragma unroll
-            for (int k = 0; k < 8; k++)
-                out_row[k] = __shfl_sync(FULL, at, 4 * k + lane / 8);
             auto put = [&](int chunk, const uint4 &x) {
                 *reinterpret_cast<uint4 *>(stage + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = x;
             };
@@ -557,10 +564,6 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             z0 = f2_add(z0, z1);
             const bool finite = f2_lo(z0) + f2_hi(z0) == 0.0f;
             tc_fence_before();                // O is read before the next item's first P lets it be overwritten
-            if (mine && part)
-                plan.part_ml[w.split * plan.rows + at] = make_float2(m, l);
-            else if (mine && p.lse)
-                p.lse[at] = l == 0.0f ? -INFINITY : LN2 * (m + log2f(l));
             for (unsigned again = __ballot_sync(FULL, mine && !finite && l > 0.0f && l <= FLT_MAX && !part); again; again &= again - 1) {
                 const int src = __ffs(again) - 1;
                 attn_mend_row<DIM>(p, w.n, __shfl_sync(FULL, tok, src), __shfl_sync(FULL, head, src),
