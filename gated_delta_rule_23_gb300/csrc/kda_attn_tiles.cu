@@ -25,8 +25,8 @@
 // (When every warp worked out the items for itself and the softmax warps loaded Q, an item of 9 steps spent 13,000 cycles
 // between them and 16,000 in them.)
 //
-// Measured (bf16 rate 1875 TFLOP/s): 8192 tokens, 96 heads over 8, full window, 1.29 ms, 1280 TFLOP/s, 68%; 12 ragged
-// prompts of 8192 tokens in all, 64 heads over 8, window 512 and 4 sinks, 121 us.  What bounds it: a step of both halves takes
+// Measured (bf16 rate 1875 TFLOP/s): 8192 tokens, 96 heads over 8, full window, 1.27 ms, 1300 TFLOP/s, 69%; 12 ragged
+// prompts of 8192 tokens in all, 64 heads over 8, window 512 and 4 sinks, 117 us.  What bounds it: a step of both halves takes
 // 1500 cycles, about what its products take with S in pieces of 64 keys, whose operands both come from shared memory (6 KB
 // for 32 cycles of tensor time, against 128 bytes a cycle); the softmax is busy for 870 of them.  Short windows pay the
 // 5000 cycles between items and the masked edges besides.
@@ -258,6 +258,23 @@ __device__ __forceinline__ uint32_t elect_one()
     return x;
 }
 
+// The next block of the grid that has not started, which then never will: asked for, its answer (16 bytes) goes to shared
+// memory and completes on the barrier.  take_answer: the block's index, -1 when there was none.
+__device__ __forceinline__ void ask_for_block(uint32_t answer, uint32_t mbar)
+{
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 ::"r"(answer), "r"(mbar) : "memory");
+}
+__device__ __forceinline__ int take_answer(uint32_t answer)
+{
+    int x;
+    asm volatile("{\n .reg .b128 a;\n .reg .pred p;\n .reg .b32 y, z, u;\n ld.shared.b128 a, [%1];\n mov.b32 %0, -1;\n"
+                 " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n"
+                 " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, u}, a;\n}"
+                 : "=r"(x) : "r"(answer) : "memory");
+    return x;
+}
+
 // bits a..b (inclusive, any integers) of a mask of several words, word w; PTX shifts of 32 and more give 0
 __device__ __forceinline__ uint32_t range_word(int a, int b, int w)
 {
@@ -280,9 +297,10 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
     const uint32_t sm_q = base, sm_ring = base + 2 * S::Q, bar = base + S::BAR;
     const uint32_t b_full = bar, b_empty = bar + 8 * S::SLOTS, b_q = b_empty + 8 * S::SLOTS, b_q_free = b_q + 8,
                    b_s = b_q_free + 8, b_p = b_s + 32, b_o = b_p + 32, b_drain = b_o + 32,  // S, P, P V: [half][buffer]
-                   b_item = b_drain + 16, b_item_free = b_item + 8 * ITEMS;
+                   b_item = b_drain + 16, b_item_free = b_item + 8 * ITEMS, b_block = b_item_free + 8 * ITEMS, b_near = b_block + 8;
     __shared__ Tile item_ring[ITEMS];
     __shared__ uint32_t tmem_slot;
+    __shared__ uint4 block_answer;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
     const int g = plan.granule;
     if (tid == 0) {
@@ -299,6 +317,8 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             mbar_init(b_drain + 8 * h, 1);
         }
         mbar_init(b_q, 1);
+        mbar_init(b_block, 1);
+        mbar_init(b_near, 1);
         mbar_init(b_q_free, 2);
         for (int i = 0; i < ITEMS; i++) {
             mbar_init(b_item + 8 * i, 1);
@@ -576,7 +596,11 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
         int issued = 0;
         Tile w;
         for (int i = 0; !timeout && next_item(i, w); i++) {
+            if (w.t0 == w.t1 && lane == 0)
+                mbar_arrive(b_near);
             for (int t = w.t0; t < w.t1 && !timeout; t++) {
+                if (t == w.t1 - 1 && lane == 0)
+                    mbar_arrive(b_near);                 // time to look for the next item
                 int y = OUTSIDE;
                 if (lane < ng) {
                     const int v = t * KEYS + lane * g, j = virt_pos(w, v);
@@ -689,11 +713,40 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
         __syncwarp();
     } else if (warp == 11) {
         // ------------------------------------------------------------ items and their Q
-        int loaded = 0;
+        // The CTA's own block first, then blocks of the grid that have not started, one when the last key tile of an item is
+        // being brought in: CTAs with less to do take more.  Blocks past a ragged batch's items are taken too, so that no CTA
+        // starts for them.  (Items dealt out beforehand, 152 apart: 1286 and 121 us for the two calls above, and as much as
+        // 133 us in another order; taken an item ahead: 1275 and 121 us.)
+        int loaded = 0, x = blockIdx.x;
+        uint32_t asked = 0, answers = 0;
+        const uint32_t answer = smem_u32(&block_answer);
+        auto next_block = [&]() -> int {
+            if (lane == 0) {
+                fence_async_smem();                      // the last answer has been read
+                mbar_expect_tx(b_block, 16);
+                ask_for_block(answer, b_block);
+            }
+            asked++;
+            __syncwarp();
+            if (!wait(b_block, answers & 1))
+                return -1;
+            answers++;
+            const int y = take_answer(answer);
+            __syncwarp();
+            return y;
+        };
         for (int i = 0;; i++) {
             const int slot = i % ITEMS;
             Tile w;
-            find_tile(p, plan, blockIdx.x + i * gridDim.x, w, bad);
+            w.valid = 0;
+            if (i > 0)
+                x = wait(b_near, (i - 1) & 1) ? next_block() : -1;
+            while (x >= 0) {
+                find_tile(p, plan, x, w, bad);
+                if (w.valid)
+                    break;
+                x = next_block();
+            }
             if (i >= ITEMS && !wait(b_item_free + 8 * slot, (i / ITEMS - 1) & 1))
                 break;
             if (lane == 0) {
@@ -715,6 +768,8 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
         }
         if (loaded > 0)                              // no copy is in flight when the CTA leaves
             mbar_wait(b_q, (loaded - 1) & 1);
+        if (asked > answers)
+            mbar_wait(b_block, answers & 1);
     }
     report(p.err, bad, DEVERR_CU_SEQLENS);
     report(p.err, timeout, DEVERR_TIMEOUT);
@@ -781,11 +836,9 @@ template <int DIM> cudaError_t launch_tiles(const AttnArgs &p, const AttnPlan &p
         e = query_map(&qmap, p, plan);
     if (e != cudaSuccess)
         return e;
-    const int sms = device_sms();
-    const int grid = plan.items < sms ? plan.items : sms;
-    if (grid < 1)
+    if (plan.items < 1)
         return cudaErrorInvalidValue;
-    kda_attn_tiles_kernel<DIM><<<grid, THREADS, Shape<DIM>::SMEM, st>>>(p, plan, kmap, vmap, qmap);
+    kda_attn_tiles_kernel<DIM><<<plan.items, THREADS, Shape<DIM>::SMEM, st>>>(p, plan, kmap, vmap, qmap);
     return cudaGetLastError();
 }
 
