@@ -186,11 +186,11 @@ AttnPlan make_plan(int window, int sinks, bool varlen, int N, int64_t T, int Hq,
         int64_t s = ctas16 > 0 ? 2 * sms / ctas16 : 1;
         s = s < most ? s : most;
         s = s > 64 ? 64 : s;
-        plan.cluster = s <= DECODE_CLUSTER || keys <= 1024 * DECODE_CLUSTER;
+        plan.cluster = s <= ATTN_CLUSTER || keys <= 1024 * ATTN_CLUSTER;
         if (plan.cluster)
             s = s >= 8 && 16 * ctas16 <= sms ? 8 : (s >= 4 && 4 * ctas16 <= sms ? 4 : (s >= 2 && 2 * ctas16 <= sms ? 2 : 1));
         plan.cluster = plan.cluster && s > 1;
-        if (row_tiles == 1 || (s <= DECODE_CLUSTER && keys <= 1152 * s)) {
+        if (row_tiles == 1 || (s <= ATTN_CLUSTER && keys <= 1152 * s)) {
             plan.decode = true;
             plan.row_tiles = (int)row_tiles;
             plan.granule = DECODE_KEYS;
@@ -210,7 +210,12 @@ AttnPlan make_plan(int window, int sinks, bool varlen, int N, int64_t T, int Hq,
     const int64_t key_tiles = (most_keys(window, sinks, T < ATTN_ROWS ? T : ATTN_ROWS, page, max_pages) + 127) / 128 + 1;
     int64_t s = ctas > 0 ? sms / ctas : 1;
     s = s < key_tiles / 2 ? s : key_tiles / 2;
-    plan.splits = s < 1 ? 1 : (s > 64 ? 64 : (int)s);
+    s = s < 1 ? 1 : (s > 64 ? 64 : s);
+    // 2, 4 or 8 splits (as above) as a cluster, which joins them in the same launch, unless more splits through memory save
+    // over four key tiles of 128, about what the join kernel takes.
+    const int64_t c = s >= 8 && 16 * ctas <= sms ? 8 : (s >= 4 ? 4 : (s >= 2 ? 2 : 1));
+    plan.cluster = c > 1 && (key_tiles + c - 1) / c <= (key_tiles + s - 1) / s + 4;
+    plan.splits = (int)(plan.cluster ? c : s);
     plan.items = (int)(ctas * plan.splits);
     return plan;
 }

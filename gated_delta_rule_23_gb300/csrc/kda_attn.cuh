@@ -22,15 +22,15 @@ struct AttnArgs {
 
 // How a call is cut: every (sequence, key head) has group x Q_n query rows, row r being token r / group and head
 // r % group of the group (so that heads sharing keys share a tile); rows come in tiles of whole tokens, and the keys a tile needs are
-// split `splits` ways, the partial results joined by a second kernel when there is more than one.
+// split `splits` ways, the partial results joined by a cluster's CTAs among themselves, or by a second kernel.
 constexpr int ATTN_ROWS = 256;   // query rows of a tile
 constexpr int DECODE_ROWS = 16, DECODE_KEYS = 16;   // rows of the decode kernel, keys of its blocks
-constexpr int DECODE_CLUSTER = 8;                   // splits that join in a cluster
+constexpr int ATTN_CLUSTER = 8;                     // splits that join in a cluster
 
 struct AttnPlan {
     bool decode;            // few query rows: the decode kernel, one item a CTA
     int row_tiles;          // of 16 rows, of a (sequence, key head) (decode kernel)
-    bool cluster;           // the splits are a cluster of the decode kernel (no workspace, no join kernel)
+    bool cluster;           // the splits are a cluster (no workspace, no join kernel)
     int splits;
     int items;              // (row tile, key head, split) items (ragged: an upper bound)
     int granule;            // positions of a cache page that are copied together
@@ -55,6 +55,27 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
 {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
                  ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(mbar) : "memory");
+}
+// The same shared-memory address in CTA `rank` of the cluster, and stores there
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank)
+{
+    uint32_t x;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(x) : "r"(addr), "r"(rank));
+    return x;
+}
+__device__ __forceinline__ void store_cluster(uint32_t addr, float2 x)
+{
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x.x), "f"(x.y) : "memory");
+}
+__device__ __forceinline__ void store_cluster(uint32_t addr, float4 x)
+{
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w) : "memory");
+}
+// Every CTA of the cluster comes here, whatever its waits did, so that this wait always ends.
+__device__ __forceinline__ void cluster_sync()
+{
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 constexpr float LN2 = 0.6931471805599453f;
 

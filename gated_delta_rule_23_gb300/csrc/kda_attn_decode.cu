@@ -25,7 +25,7 @@
 namespace kda {
 namespace {
 
-constexpr int KEYS = DECODE_KEYS, ROWS = DECODE_ROWS, CLUSTER = DECODE_CLUSTER;
+constexpr int KEYS = DECODE_KEYS, ROWS = DECODE_ROWS, CLUSTER = ATTN_CLUSTER;
 constexpr float RESCALE_AT = 8.0f;           // base-2 growth of a maximum that moves it
 constexpr unsigned FULL = 0xffffffffu;
 
@@ -49,22 +49,6 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ uint32_t chunk_at(uint32_t block, int key, int c)
 {
     return block + (c / 8) * (KEYS * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4);
-}
-// The same shared-memory address in CTA `rank` of the cluster, and a store there
-__device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank)
-{
-    uint32_t x;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(x) : "r"(addr), "r"(rank));
-    return x;
-}
-__device__ __forceinline__ void store_cluster(uint32_t addr, float2 x)
-{
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x.x), "f"(x.y) : "memory");
-}
-// Every CTA of the cluster comes here, whatever its waits did, so that this wait always ends.
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Joins N results (maximum, sum) of a row: their weights, and the row's maximum and sum.  A result without a visible key has
 // maximum -inf and sum 0; NaN scores leave a NaN sum.

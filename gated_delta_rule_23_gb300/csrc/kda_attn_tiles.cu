@@ -22,11 +22,14 @@
 // and 10: tensor-core issue for a half each (one thread for both halves spent longer issuing than the tensor cores took:
 // 1918 us at 8192 tokens, 96 heads); warp 11: works out the items and brings in their Q.  One CTA an SM walks the (row
 // tile, key head, split) items: copies and first S of the next item run while the last one's rows are scaled and stored.
+// Where there are fewer items than SMs their keys are split: 2, 4 or 8 splits are a cluster that joins them in the same
+// launch, each CTA finishing its share of the rows (two sequences of 509 tokens after 20,011, window 2049, D 64, 14 heads over 2,
+// 2 splits: 22.5 us; through memory and a second kernel: 28.7).
 // (When every warp worked out the items for itself and the softmax warps loaded Q, an item of 9 steps spent 13,000 cycles
 // between them and 16,000 in them.)
 //
-// Measured (bf16 rate 1875 TFLOP/s): 8192 tokens, 96 heads over 8, full window, 1.27 ms, 1300 TFLOP/s, 69%; 12 ragged
-// prompts of 8192 tokens in all, 64 heads over 8, window 512 and 4 sinks, 117 us.  What bounds it: a step of both halves takes
+// Measured (bf16 rate 1875 TFLOP/s): 8192 tokens, 96 heads over 8, full window, 1.26 ms, 1310 TFLOP/s, 70%; 12 ragged
+// prompts of 8192 tokens in all, 64 heads over 8, window 512 and 4 sinks, 116 us.  What bounds it: a step of both halves takes
 // 1500 cycles, about what its products take with S in pieces of 64 keys, whose operands both come from shared memory (6 KB
 // for 32 cycles of tensor time, against 128 bytes a cycle); the softmax is busy for 870 of them.  Short windows pay the
 // 5000 cycles between items and the masked edges besides.
@@ -59,6 +62,7 @@ template <int DIM> struct Shape {
     static constexpr int OUT = 2 * Q + SLOTS * TILE;         // behind Q and the ring
     static constexpr int BAR = OUT + 8 * STAGE;              // mbarriers last
     static constexpr int SMEM = 1024 + BAR + 768;            // 1024: alignment of the swizzle atoms
+    static_assert(SLOTS * TILE >= ATTN_ROWS * DIM * 4, "a cluster's parts of a CTA's rows go where the ring was");
 };
 
 struct Tile {             // one item; positions, rows and tokens fit 32 bits (checked on the host)
@@ -89,13 +93,13 @@ __device__ __forceinline__ void find_tile(const AttnArgs &p, const AttnPlan &pla
     if (x >= plan.items)
         return;
     // heaviest first where the work grows along a sequence: the last tiles of all key heads
-    w.kvh = x % p.cache.hkv;
-    x /= p.cache.hkv;
     w.split = 0;
     if (plan.splits > 1) {
-        w.split = x % plan.splits;
+        w.split = x % plan.splits;                  // the splits of an item are neighbours: a cluster
         x /= plan.splits;
     }
+    w.kvh = x % p.cache.hkv;
+    x /= p.cache.hkv;
     const int run = plan.run;                       // tokens of an item
     int tile = 0, len_q = 0, bos = 0;
     if (p.tok.cu) {
@@ -154,8 +158,8 @@ __device__ __forceinline__ void find_tile(const AttnArgs &p, const AttnPlan &pla
     w.t0 = 0;
     w.t1 = tiles;
     if (plan.splits > 1) {
-        w.t0 = (int)((int64_t)tiles * w.split / plan.splits);
-        w.t1 = (int)((int64_t)tiles * (w.split + 1) / plan.splits);
+        w.t0 = tiles * w.split / plan.splits;       // at most 2^24 tiles, 64 splits
+        w.t1 = tiles * (w.split + 1) / plan.splits;
     }
 #pragma unroll
     for (int h = 0; h < 2; h++) {
@@ -181,7 +185,8 @@ __device__ __forceinline__ void find_tile(const AttnArgs &p, const AttnPlan &pla
 // in the low one a step along the operand is an addition, so that the issuing thread spends an instruction or two a
 // product (building whole descriptors there cost as much as the products themselves).
 constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+// (In a cluster a shared-memory address has the CTA's rank above its 18 bits.)
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr & 0x3ffff) >> 4) | ((lbo >> 4) << 16); }
 // fp32 accumulator, bf16 A and B, A K-major, B K-major or (mn) MN-major
 __device__ __forceinline__ constexpr uint32_t idesc_bf16(int M, int N, bool mn)
 {
@@ -217,20 +222,25 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
                  ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(mbar) : "memory");
 }
 
-// 32 columns of the warp's 32 lanes, one row a thread: the load, and the wait for it, which names the registers so that
-// nothing that uses them moves before it
+// 32 or 64 columns of the warp's 32 lanes, one row a thread: the load and the wait for it, as one statement so that no register
+// is moved or spilled in between.
 #define REGS8(k, a, i) k(a[i]), k(a[i + 1]), k(a[i + 2]), k(a[i + 3]), k(a[i + 4]), k(a[i + 5]), k(a[i + 6]), k(a[i + 7])
-__device__ __forceinline__ void tmem_get32(uint32_t addr, float (&s)[32])
+__device__ __forceinline__ void tmem_read32(uint32_t addr, float (&s)[32])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-                 : REGS8("=f", s, 0), REGS8("=f", s, 8), REGS8("=f", s, 16), REGS8("=f", s, 24)
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n tcgen05.wait::ld.sync.aligned;"
+                 : REGS8("=&f", s, 0), REGS8("=&f", s, 8), REGS8("=&f", s, 16), REGS8("=&f", s, 24)
                  : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void tmem_wait32(float (&s)[32])
+__device__ __forceinline__ void tmem_read64(uint32_t addr, float (&s)[2][32])
 {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : REGS8("+f", s, 0), REGS8("+f", s, 8), REGS8("+f", s, 16), REGS8("+f", s, 24)::"memory");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n"
+                 " tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+                 "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n tcgen05.wait::ld.sync.aligned;"
+                 : REGS8("=&f", s[0], 0), REGS8("=&f", s[0], 8), REGS8("=&f", s[0], 16), REGS8("=&f", s[0], 24),
+                   REGS8("=&f", s[1], 0), REGS8("=&f", s[1], 8), REGS8("=&f", s[1], 16), REGS8("=&f", s[1], 24)
+                 : "r"(addr), "r"(addr + 32) : "memory");
 }
 #undef REGS8
 // tcgen05.st of 32 columns without the wait for its completion
@@ -284,7 +294,8 @@ __device__ __forceinline__ uint32_t range_word(int a, int b, int w)
     return x & y;
 }
 
-template <int DIM>
+// CLUSTERED: an item's splits are a cluster, one item a CTA.
+template <int DIM, bool CLUSTERED>
 __global__ void __launch_bounds__(THREADS, 1)
 kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap)
@@ -335,7 +346,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    bool timeout = false, bad = false;
+    bool timeout = false, bad = false, joined = false;
     // Waits of a whole warp: every lane polls and the warp votes, so that it stays converged.  (One lane polling for the
     // others let the compiler keep the warp split behind the wait, and everything after it ran twice: 2420 us instead of
     // 1290 at 8192 tokens, 96 heads.)  Once a wait of the warp has given up, the later ones do at once.
@@ -424,10 +435,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                     const f2 sc = f2_pack(p.scale_log2, p.scale_log2), mm = f2_pack(-mu, -mu);
                     float top = -INFINITY;
                     l0 = l1 = 0;
-                    tmem_get32(tm_s, s[0]);
-                    tmem_get32(tm_s + 32, s[1]);
-                    tmem_wait32(s[0]);
-                    tmem_wait32(s[1]);
+                    tmem_read64(tm_s, s);
 #pragma unroll
                     for (int c = 0; c < SUB / 32; c++) {
                         hide(s[c & 1], c);
@@ -464,8 +472,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
 #pragma unroll
                         for (int c = 0; c < DIM; c += 32) {
                             float o[32];
-                            tmem_get32(tm_o + c, o);
-                            tmem_wait32(o);
+                            tmem_read32(tm_o + c, o);
                             uint32_t u[32];
 #pragma unroll
                             for (int e = 0; e < 32; e++)
@@ -487,9 +494,60 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             if (timeout)
                 break;
             ring += w.t1 - w.t0;
+            // The last P V: those before it are through with it.
+            auto last_pv = [&]() -> bool {
+                if (any) {
+                    const int last_buf = (hi - 1) & 1;
+                    o_phase ^= hi - lo > 1 ? 3 : 1u << last_buf;
+                    if (!wait(b_o + 16 * h + 8 * last_buf, (o_phase >> last_buf & 1) ^ 1))
+                        return false;
+                    tc_fence_after();
+                }
+                return true;
+            };
+            // A cluster's CTA `split` finishes rows split * per .. of the item; the others send it their O, maximum and sum.
+            // They go where its ring and its Q were: every warp of the cluster is through with those at the first barrier.
+            const int per = CLUSTERED ? ATTN_ROWS / plan.splits : ATTN_ROWS, owner = tid / per, row = tid % per;
+            float own = 1.0f, M = 0.0f;                          // weight of this split's O (below 0: none)
+            if constexpr (CLUSTERED) {
+                if (!last_pv())
+                    break;
+                cluster_sync();
+                if (owner != w.split) {
+                    const int sender = w.split - (w.split > owner);
+                    const uint32_t to = in_cta(sm_ring + (sender * (DIM / 4) * per + row) * 16, owner);
+                    if (any)
+#pragma unroll
+                        for (int c = 0; c < DIM; c += 32) {
+                            float o[32];
+                            tmem_read32(tm_o + c, o);
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                store_cluster(to + (c + e) / 4 * per * 16, make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+                        }
+                    store_cluster(in_cta(sm_q + (sender * per + row) * 8, owner), make_float2(m, l));
+                }
+                tc_fence_before();
+                cluster_sync();
+                joined = true;
+                if (owner != w.split)
+                    break;
+                const float2 *st = reinterpret_cast<const float2 *>(smem) + row;
+                const float mine_m = m, mine_l = l;
+                for (int i = 0; i < plan.splits - 1; i++)
+                    m = fmaxf(m, st[i * per].x);
+                M = m == -INFINITY ? 0.0f : m;
+                own = mine_m == -INFINITY && mine_l == 0.0f ? -1.0f : ex2_approx(mine_m - M);
+                l = own < 0.0f ? 0.0f : own * mine_l;
+                for (int i = 0; i < plan.splits - 1; i++) {
+                    const float2 x = st[i * per];
+                    if (!(x.x == -INFINITY && x.y == 0.0f))
+                        l += ex2_approx(x.x - M) * x.y;
+                }
+            }
             // What of the epilogue needs no O, and the next item, while the last P V runs.
             const int at = mine ? tok * p.hq + head : -1;
-            const bool part = plan.splits > 1;
+            const bool part = !CLUSTERED && plan.splits > 1;
             const float inv = part ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
             const bool blank = __any_sync(FULL, l == 0.0f && !part);         // rows that see nothing: 0
             int out_row[8];                                      // of the rows this lane takes out
@@ -500,15 +558,9 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                 plan.part_ml[w.split * plan.rows + at] = make_float2(m, l);
             else if (mine && p.lse)
                 p.lse[at] = l == 0.0f ? -INFINITY : LN2 * (m + log2f(l));
-            more = next_item(i, next);
-            if (any) {
-                // the last P V: those before it are through with it
-                const int last_buf = (hi - 1) & 1;
-                o_phase ^= hi - lo > 1 ? 3 : 1u << last_buf;
-                if (!wait(b_o + 16 * h + 8 * last_buf, (o_phase >> last_buf & 1) ^ 1))
-                    break;
-                tc_fence_after();
-            }
+            more = !CLUSTERED && next_item(i, next);
+            if (!CLUSTERED && !last_pv())
+                break;
             // Epilogue: the row's thread scales it; 128 bytes of each row at a time go through shared memory (16-byte
             // chunks, swizzled) and out with eight lanes to a row.  (Stored straight by its thread, a row took a line of L1
             // for every 16 bytes: 148 us for ragged 8192 tokens with window 512.)
@@ -536,14 +588,29 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             for (int c = 0; c < DIM; c += 64) {
                 float o[2][32];
                 if (any) {
-                    tmem_get32(tm_o + c, o[0]);
-                    tmem_get32(tm_o + c + 32, o[1]);
-                    tmem_wait32(o[0]);
-                    tmem_wait32(o[1]);
+                    tmem_read64(tm_o + c, o);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 64; e++)
                         o[e / 32][e % 32] = 0.0f;
+                }
+                if constexpr (CLUSTERED) {
+#pragma unroll
+                    for (int e = 0; e < 64; e++)
+                        o[e / 32][e % 32] = own < 0.0f ? 0.0f : own * o[e / 32][e % 32];
+                    for (int i = 0; i < plan.splits - 1; i++) {
+                        const float2 x = reinterpret_cast<const float2 *>(smem)[i * per + row];
+                        if (x.x == -INFINITY && x.y == 0.0f)     // saw nothing; nor is there an O
+                            continue;
+                        const float a = ex2_approx(x.x - M);
+                        const float4 *y = reinterpret_cast<const float4 *>(smem + 2 * S::Q) + (i * (DIM / 4) + c / 4) * per + row;
+#pragma unroll
+                        for (int e = 0; e < 64; e += 4) {
+                            const float4 z = y[e / 4 * per];
+                            float *t = &o[e / 32][e % 32];
+                            t[0] = fmaf(a, z.x, t[0]), t[1] = fmaf(a, z.y, t[1]), t[2] = fmaf(a, z.z, t[2]), t[3] = fmaf(a, z.w, t[3]);
+                        }
+                    }
                 }
 #pragma unroll
                 for (int e = 0; e < 64; e += 2) {
@@ -740,12 +807,12 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             Tile w;
             w.valid = 0;
             if (i > 0)
-                x = wait(b_near, (i - 1) & 1) ? next_block() : -1;
+                x = !CLUSTERED && wait(b_near, (i - 1) & 1) ? next_block() : -1;
             while (x >= 0) {
                 find_tile(p, plan, x, w, bad);
                 if (w.valid)
                     break;
-                x = next_block();
+                x = CLUSTERED ? -1 : next_block();
             }
             if (i >= ITEMS && !wait(b_item_free + 8 * slot, (i / ITEMS - 1) & 1))
                 break;
@@ -770,6 +837,10 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             mbar_wait(b_q, (loaded - 1) & 1);
         if (asked > answers)
             mbar_wait(b_block, answers & 1);
+    }
+    if (CLUSTERED && !joined) {                      // the other warps, CTAs without an item, and those that gave up
+        cluster_sync();
+        cluster_sync();
     }
     report(p.err, bad, DEVERR_CU_SEQLENS);
     report(p.err, timeout, DEVERR_TIMEOUT);
@@ -817,13 +888,13 @@ cudaError_t query_map(CUtensorMap *map, const AttnArgs &p, const AttnPlan &plan)
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int DIM> cudaError_t launch_tiles(const AttnArgs &p, const AttnPlan &plan, cudaStream_t st)
+template <int DIM, bool CLUSTERED> cudaError_t launch_tiles(const AttnArgs &p, const AttnPlan &plan, cudaStream_t st)
 {
     static std::atomic<uint64_t> ready;      // devices whose kernel attribute is set
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && !(ready.load() >> dev & 1)) {
-        e = cudaFuncSetAttribute(kda_attn_tiles_kernel<DIM>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<DIM>::SMEM);
+        e = cudaFuncSetAttribute(kda_attn_tiles_kernel<DIM, CLUSTERED>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<DIM>::SMEM);
         if (e == cudaSuccess)
             ready.fetch_or(1ull << dev);
     }
@@ -838,8 +909,18 @@ template <int DIM> cudaError_t launch_tiles(const AttnArgs &p, const AttnPlan &p
         return e;
     if (plan.items < 1)
         return cudaErrorInvalidValue;
-    kda_attn_tiles_kernel<DIM><<<plan.items, THREADS, Shape<DIM>::SMEM, st>>>(p, plan, kmap, vmap, qmap);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)plan.items);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = Shape<DIM>::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CLUSTERED ? (unsigned)plan.splits : 1u;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CLUSTERED ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kda_attn_tiles_kernel<DIM, CLUSTERED>, p, plan, kmap, vmap, qmap);
 }
 
 }  // namespace
@@ -863,7 +944,9 @@ cudaError_t cache_map(CUtensorMap *map, const void *ptr, const PagedCache &c, in
 
 cudaError_t launch_attn_tiles(const AttnArgs &p, const AttnPlan &plan, cudaStream_t st)
 {
-    return p.cache.dim == 128 ? launch_tiles<128>(p, plan, st) : launch_tiles<64>(p, plan, st);
+    if (plan.cluster)
+        return p.cache.dim == 128 ? launch_tiles<128, true>(p, plan, st) : launch_tiles<64, true>(p, plan, st);
+    return p.cache.dim == 128 ? launch_tiles<128, false>(p, plan, st) : launch_tiles<64, false>(p, plan, st);
 }
 
 }  // namespace kda

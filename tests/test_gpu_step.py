@@ -137,6 +137,35 @@ def test_attn_row_tiles(kda, case, ragged):
     _attn(kda, *case, ragged)
 
 
+# Query tiles of 256 rows with their keys in splits: 2, 4, 8 and many of them, splits that hold no key of a half's rows, rows that
+# see nothing.
+SPLIT_TILES = [
+    ([700], [300], 2, 1, 128, 16, 500, 0), ([1500], [300], 2, 1, 64, 32, 1300, 3), ([2600], [258], 1, 1, 128, 64, 2500, 5),
+    ([9000], [40], 8, 1, 128, 16, 8800, 1), ([3000, 90, 30], [100, 90, 40], 14, 2, 64, 16, 2100, 37),
+    ([3000], [257], 1, 1, 64, 128, 30, 2500), ([2000], [600], 8, 8, 128, 32, 40, 0), ([20, 2000], [300, 300], 3, 1, 128, 16, 1000, 0),
+]
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("case", SPLIT_TILES, ids=[str(i) for i in range(len(SPLIT_TILES))])
+def test_attn_split_tiles(kda, case, ragged):
+    if len(set(case[1])) > 1 and not ragged:
+        case = (case[0], [case[1][0]] * len(case[1])) + case[2:]
+    a, b = (_attn(kda, *case, ragged) for _ in range(2))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+@pytest.mark.parametrize("lens, window", [(700, 301), (2600, 2031)])
+def test_attn_split_tiles_values_out_of_sight(kda, lens, window, value):
+    """Keys and values just before every row's window, in the tiles that the splits do bring in."""
+    def edit(k, v, table):
+        for j in range(lens - 258 - window - 15, lens - 258 - window + 1):
+            at = int(table[0, j // 16])
+            k[at, :, j % 16], v[at, :, j % 16] = value, value
+    _attn(kda, [lens], [258], 1, 1, 128, 16, window, 0, False, edit=edit)
+
+
 @pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
 @pytest.mark.parametrize("new, hq", [(1, 8), (2, 4), (140, 4)])
 def test_attn_values_out_of_sight(kda, value, new, hq):
