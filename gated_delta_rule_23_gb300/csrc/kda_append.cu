@@ -2,7 +2,7 @@
 //
 // Per pair (x, y) of a head and the position's angle a_i: (x cos a_i - y sin a_i, y cos a_i + x sin a_i), in fp32 and
 // rounded once.  Every element is read once and written once: the floor is the bytes of q, k, v and their copies.
-// Measured: 76 us for 8192 ragged tokens of 96 + 2 x 8 heads (472 MB), 6.2 TB/s, 92% of the measured copy rate; 4.1 us for
+// Measured: 74 us for 8192 ragged tokens of 96 + 2 x 8 heads (472 MB), 6.4 TB/s, 94% of the measured copy rate; 2.8 us for
 // one token, 6.1 for 256 (launch latency).
 // A thread owns one unit of 16 elements of the head (8 pairs) and walks the token's heads with the unit's 8 cosines
 // and sines in registers, so the angles are read once per token and not once per head.
@@ -80,6 +80,7 @@ template <bool INTERLEAVED> __global__ void __launch_bounds__(APPEND_THREADS, CT
     bool bad = false;
     int n;
     int64_t i, len_q;
+    stream_order();
     if (p.tok.cu) {
         int64_t bos;
         n = seq_of_token(p.tok.cu, p.tok.N, t);
@@ -198,9 +199,7 @@ extern "C" kda_status_t kda_kv_append(const void *k, int64_t k_stride, const voi
         return KDA_ERR_CUDA;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const unsigned grid = (unsigned)tokens;
-    if (interleaved)
-        kda_append_kernel<true><<<grid, APPEND_THREADS, 0, st>>>(p);
-    else
-        kda_append_kernel<false><<<grid, APPEND_THREADS, 0, st>>>(p);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    const cudaError_t e = interleaved ? launch_in_row(kda_append_kernel<true>, grid, APPEND_THREADS, 0, 1, st, p)
+                                      : launch_in_row(kda_append_kernel<false>, grid, APPEND_THREADS, 0, 1, st, p);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -20,7 +20,7 @@ __global__ void __launch_bounds__(ROW_THREADS) kda_attn_join_kernel(const AttnAr
     __shared__ float part[WARPS][DIM];
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, sub = warp % PER_ROW;
     const int64_t r = (int64_t)blockIdx.x * (WARPS / PER_ROW) + warp / PER_ROW;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    stream_order();
     const bool in = r < plan.rows;
     float m = -INFINITY, l = 0.0f, o[PER];
 #pragma unroll
@@ -235,21 +235,10 @@ cudaError_t launch_attn_join(const AttnArgs &p, const AttnPlan &plan, cudaStream
     const bool few = plan.splits > 4 && plan.rows <= 1024;
     const int per_cta = few ? 1 : ROW_THREADS / 32;
     const unsigned grid = (unsigned)((plan.rows + per_cta - 1) / per_cta);
-    // launched as a programmatic dependent: its CTAs wait for the results themselves
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(ROW_THREADS);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    const auto launch = [&](auto *kernel) { return launch_in_row(kernel, grid, ROW_THREADS, 0, 1, st, p, plan); };
     if (few)
-        return p.cache.dim == 128 ? cudaLaunchKernelEx(&cfg, kda_attn_join_kernel<128, 8>, p, plan)
-                                  : cudaLaunchKernelEx(&cfg, kda_attn_join_kernel<64, 8>, p, plan);
-    return p.cache.dim == 128 ? cudaLaunchKernelEx(&cfg, kda_attn_join_kernel<128, 1>, p, plan)
-                              : cudaLaunchKernelEx(&cfg, kda_attn_join_kernel<64, 1>, p, plan);
+        return p.cache.dim == 128 ? launch(kda_attn_join_kernel<128, 8>) : launch(kda_attn_join_kernel<64, 8>);
+    return p.cache.dim == 128 ? launch(kda_attn_join_kernel<128, 1>) : launch(kda_attn_join_kernel<64, 1>);
 }
 
 }  // namespace kda

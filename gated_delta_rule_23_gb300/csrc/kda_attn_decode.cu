@@ -9,10 +9,10 @@
 // launch; more go through memory and the join kernel.  Small calls with more rows are tiles of 16 rows, one a CTA.
 //
 // Measured: 256 sequences, 64 heads over 8, window 1024 and 16 sinks (1.10 GB), 164 us, 6.70 TB/s, 99% of the measured copy
-// rate (the tile kernel: 255 us).  One sequence, 32 heads over 8, window 4096: 10.3 us, a chain of latencies (lengths, page
+// rate (the tile kernel: 255 us).  One sequence, 32 heads over 8, window 4096: 8.9 us, a chain of latencies (lengths, page
 // table, copies, four blocks a warp, the joins); the CTAs of a cluster send each row's parts to the CTA that finishes it,
-// which takes one barrier (10.3 us; one CTA that reads the others' parts between two barriers: 12.3 us, as do 32 splits
-// with a join kernel).
+// which takes one barrier (2 us less than one CTA that reads the others' parts between two barriers, or than 32 splits with
+// a join kernel).
 //
 // Keys come as in the tile kernel: the sinks' granules, then the window's, 16 positions each, which lie in one page.
 // Values that no row of the CTA sees are cleared in shared memory; where the rows differ in what they see (several
@@ -84,7 +84,6 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t bars[WARPS * S::RING];
     __shared__ float2 stats[WARPS][ROWS], recv_stats[ROWS], recv_failed[CLUSTER];
-    asm volatile("griddepcontrol.launch_dependents;");
     if (plan.cluster)                                            // waited for before anything is sent: every CTA has begun
         asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     if (threadIdx.x == 0) {
@@ -103,6 +102,14 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
     const int kvh = x % p.cache.hkv, n = x / p.cache.hkv;
     const int tokens = (int)p.tok.T, rows = min(tokens * p.group - row0, ROWS);
     bool bad = false, timeout = false;
+    const uint32_t ring = base + warp * S::WARP, bar = smem_u32(bars + warp * S::RING);
+    if (lane == 0) {
+        for (int i = 0; i < S::RING; i++)
+            mbar_init(bar + 8 * i, 1);
+        mbar_fence_init();
+    }
+    __syncwarp();
+    stream_order();
     // Q as the first operand: rows g and g + 8; on its way while the lengths and the page table are read
     uint32_t q[KS][4];
 #pragma unroll
@@ -114,8 +121,8 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
             p.q + (int64_t)(n * tokens + tok) * p.q_stride + (kvh * p.group + (in ? (row0 + row) % p.group : 0)) * DIM);
 #pragma unroll
         for (int k = 0; k < KS; k++) {
-            q[k][r] = in ? __ldg(src + 8 * k + t) : 0;
-            q[k][2 + r] = in ? __ldg(src + 8 * k + 4 + t) : 0;
+            q[k][r] = in ? src[8 * k + t] : 0;
+            q[k][2 + r] = in ? src[8 * k + 4 + t] : 0;
         }
     }
     const int len = (int)cache_len(p.cache, n, bad);
@@ -138,13 +145,6 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
     const int b0 = (int)((int64_t)blocks * split / plan.splits), b1 = (int)((int64_t)blocks * (split + 1) / plan.splits);
     auto position = [&](int b) { return b * KEYS < sink ? b * KEYS : b * KEYS - sink + start; };
 
-    const uint32_t ring = base + warp * S::WARP, bar = smem_u32(bars + warp * S::RING);
-    if (lane == 0) {
-        for (int i = 0; i < S::RING; i++)
-            mbar_init(bar + 8 * i, 1);
-        mbar_fence_init();
-    }
-    __syncwarp();
     const int mine = b1 - b0 > warp ? (b1 - b0 - warp + WARPS - 1) / WARPS : 0;      // blocks b0 + warp + WARPS i
     auto fetch = [&](int i) {                                    // by lane 0
         const int j = position(b0 + warp + WARPS * i);
@@ -392,18 +392,8 @@ template <int DIM, int WARPS> cudaError_t launch_decode_dim(const AttnArgs &p, c
         e = cache_map(&vmap, p.cache.v, p.cache, KEYS);
     if (e != cudaSuccess)
         return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)plan.items);
-    cfg.blockDim = dim3(32 * WARPS);
-    cfg.dynamicSmemBytes = Shape<DIM, WARPS>::SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = plan.cluster ? (unsigned)plan.splits : 1u;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kda_attn_decode_kernel<DIM, WARPS>, p, plan, kmap, vmap);
+    return launch_in_row(kda_attn_decode_kernel<DIM, WARPS>, plan.items, 32 * WARPS, Shape<DIM, WARPS>::SMEM,
+                         plan.cluster ? plan.splits : 1, st, p, plan, kmap, vmap);
 }
 
 }  // namespace

@@ -24,11 +24,11 @@
 // tile, key head, split) items: copies and first S of the next item run while the last one's rows are scaled and stored.
 // Where there are fewer items than SMs their keys are split: 2, 4 or 8 splits are a cluster that joins them in the same
 // launch, each CTA finishing its share of the rows (two sequences of 509 tokens after 20,011, window 2049, D 64, 14 heads over 2,
-// 2 splits: 22.5 us; through memory and a second kernel: 28.7).
+// 2 splits: 22.5 us, through memory and a second kernel 28.7; launched as it is now 20.6).
 // (When every warp worked out the items for itself and the softmax warps loaded Q, an item of 9 steps spent 13,000 cycles
 // between them and 16,000 in them.)
 //
-// Measured (bf16 rate 1875 TFLOP/s): 8192 tokens, 96 heads over 8, full window, 1.26 ms, 1310 TFLOP/s, 70%; 12 ragged
+// Measured (bf16 rate 1875 TFLOP/s): 8192 tokens, 96 heads over 8, full window, 1.27 ms, 1300 TFLOP/s, 69%; 12 ragged
 // prompts of 8192 tokens in all, 64 heads over 8, window 512 and 4 sinks, 116 us.  What bounds it: a step of both halves takes
 // 1500 cycles, about what its products take with S in pieces of 64 keys, whose operands both come from shared memory (6 KB
 // for 32 cycles of tensor time, against 128 bytes a cycle); the softmax is busy for 870 of them.  Short windows pay the
@@ -346,6 +346,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    stream_order();
     bool timeout = false, bad = false, joined = false;
     // Waits of a whole warp: every lane polls and the warp votes, so that it stays converged.  (One lane polling for the
     // others let the compiler keep the warp split behind the wait, and everything after it ran twice: 2420 us instead of
@@ -909,18 +910,8 @@ template <int DIM, bool CLUSTERED> cudaError_t launch_tiles(const AttnArgs &p, c
         return e;
     if (plan.items < 1)
         return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)plan.items);
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = Shape<DIM>::SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CLUSTERED ? (unsigned)plan.splits : 1u;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = CLUSTERED ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kda_attn_tiles_kernel<DIM, CLUSTERED>, p, plan, kmap, vmap, qmap);
+    return launch_in_row(kda_attn_tiles_kernel<DIM, CLUSTERED>, plan.items, THREADS, Shape<DIM>::SMEM, CLUSTERED ? plan.splits : 1,
+                         st, p, plan, kmap, vmap, qmap);
 }
 
 }  // namespace

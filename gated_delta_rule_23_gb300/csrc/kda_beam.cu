@@ -5,9 +5,9 @@
 // row, the chunk's maximum and sum and its K + 1 best logits (kda_beam_chunks_kernel), and a second kernel, one CTA a
 // batch entry, turns those few into scores and picks (kda_beam_pick_kernel).  Each logit is read once: the floor.
 //
-// Measured: 32 x 8 rows of 131072 fp32 logits (134 MB), 41 us, 3.3 TB/s, 49% of the measured copy rate: the chunks stream
-// at 60% of it and all end together, so that their tail (the bound, the few threads looked at again) and the pick's chain
-// of latencies (5.5 us) are in nobody's shadow.  One request of 4 x 32001 bf16 logits: 12.3 us, both chains.
+// Measured: 32 x 8 rows of 131072 fp32 logits (134 MB), 35.5 us, 3.8 TB/s, 56% of the measured copy rate: the chunks stream
+// at 60 to 70% of it and all end together, so that their tail (the bound, the few threads looked at again) and the pick's
+// chain of latencies (5.5 us) are in nobody's shadow.  One request of 4 x 32001 bf16 logits: 9.1 us, both chains.
 //
 // What the short lists may hide: logits so close that their fp32 scores are equal tie by index and not by logit.  That
 // matters only where the value a chunk's list was cut off at reaches the K-th score and a neighbouring logit value has
@@ -276,7 +276,7 @@ template <typename T, bool VECTOR> __device__ __forceinline__ void stream_logits
 #pragma unroll
         for (int d = 0; d < DEPTH; d++)
             if (d < steps)
-                raw[d] = __ldg(at + d * THREADS);
+                raw[d] = at[d * THREADS];
         int s = 0;
         for (; s + 2 * DEPTH <= steps; s += DEPTH) {
             at += DEPTH * THREADS;
@@ -285,7 +285,7 @@ template <typename T, bool VECTOR> __device__ __forceinline__ void stream_logits
                 float v[N];
                 unpack(raw[d], v, l);
                 seen.add(v, s + d);
-                raw[d] = __ldg(at + d * THREADS);
+                raw[d] = at[d * THREADS];
             }
         }
         at += DEPTH * THREADS;
@@ -296,7 +296,7 @@ template <typename T, bool VECTOR> __device__ __forceinline__ void stream_logits
                 unpack(raw[d], v, l);
                 seen.add(v, s + d);
                 if (s + DEPTH + d < steps)
-                    raw[d] = __ldg(at + d * THREADS);
+                    raw[d] = at[d * THREADS];
             }
 #pragma unroll
         for (int d = 0; d < DEPTH; d++)
@@ -375,7 +375,7 @@ template <typename T> __global__ void __launch_bounds__(THREADS, 5) kda_beam_chu
     constexpr int N = Vec<T>::N, STEP = THREADS * N;
     __shared__ __align__(16) Pick sh;
     __shared__ float2 part[THREADS / 32];
-    asm volatile("griddepcontrol.launch_dependents;");
+    stream_order();
     const int64_t row = blockIdx.x / p.chunks;
     const int chunk = (int)(blockIdx.x % p.chunks);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, n = p.K + 1;
@@ -527,7 +527,7 @@ template <typename T> __global__ void __launch_bounds__(PICK_THREADS) kda_beam_p
     __shared__ int kind[32];               // 0: candidates from the lists; 1: nothing counts; 2: finished
     __shared__ int selected;
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    stream_order();
     if (tid == 0)
         sh.count = selected = 0;
     // The lists' slots, `room` a list and so warp by warp in one list each: the first HELD rounds of them are on their way
@@ -705,20 +705,8 @@ namespace {
 template <typename T> cudaError_t launch_beam(const BeamArgs &p, cudaStream_t st)
 {
     const unsigned grid = (unsigned)(p.chunks * p.B * p.W);
-    kda_beam_chunks_kernel<T><<<grid, THREADS, 0, st>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess)
-        return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)p.B);
-    cfg.blockDim = dim3(PICK_THREADS);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kda_beam_pick_kernel<T>, p);
+    const cudaError_t e = launch_in_row(kda_beam_chunks_kernel<T>, grid, THREADS, 0, 1, st, p);
+    return e != cudaSuccess ? e : launch_in_row(kda_beam_pick_kernel<T>, p.B, PICK_THREADS, 0, 1, st, p);
 }
 
 }  // namespace

@@ -31,6 +31,7 @@ template <int MAXW> __global__ void __launch_bounds__(REORDER_THREADS) kda_reord
     const int64_t n0 = (int64_t)blockIdx.y * p.beams;
     const bool in_place = src == dst;
     bool bad = false;
+    stream_order();
     for (int64_t x = (int64_t)blockIdx.x * REORDER_THREADS + threadIdx.x; x < vecs;
          x += (int64_t)gridDim.x * REORDER_THREADS) {
         uint4 r[MAXW];
@@ -63,12 +64,10 @@ cudaError_t launch_reorder(const ReorderArgs &p, int64_t most, int groups, int t
         gx = 4096;
     const dim3 grid((unsigned)gx, (unsigned)groups, (unsigned)tensors);
     if (p.beams <= 4)
-        kda_reorder_kernel<4><<<grid, REORDER_THREADS, 0, st>>>(p);
-    else if (p.beams <= 8)
-        kda_reorder_kernel<8><<<grid, REORDER_THREADS, 0, st>>>(p);
-    else
-        kda_reorder_kernel<32><<<grid, REORDER_THREADS, 0, st>>>(p);
-    return cudaGetLastError();
+        return launch_in_row(kda_reorder_kernel<4>, grid, REORDER_THREADS, 0, 1, st, p);
+    if (p.beams <= 8)
+        return launch_in_row(kda_reorder_kernel<8>, grid, REORDER_THREADS, 0, 1, st, p);
+    return launch_in_row(kda_reorder_kernel<32>, grid, REORDER_THREADS, 0, 1, st, p);
 }
 
 }  // namespace

@@ -34,6 +34,36 @@ inline PagedCache make_cache(const void *k, const void *v, const int32_t *table,
     return c;
 }
 
+// The decoder-step kernels are short and run in a row, so each may be set up while the one before it in its stream ends
+// (programmatic dependent launch): stream_order() stands before anything that reads or writes memory, and waits until all
+// kernels before are through and their writes to be seen; after it the next kernel may be set up.  What they read may
+// be those kernels' output: no read-only (.nc) loads, which need not stay behind the wait.  Calls in a row, launched plainly |
+// this way: append of one token 4.1 | 2.8 us, attention of one sequence's step 10.3 | 8.9, beam selection of 4 x 32001
+// 12.3 | 9.1, chunks of 509 22.5 | 20.6.
+__device__ __forceinline__ void stream_order()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+}
+template <typename... P, typename... A>
+cudaError_t launch_in_row(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st, const A &...args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 kda_status_t check_cache_args(const void *k_cache, const void *v_cache, const int32_t *block_table,
                               const int32_t *kv_lens, const int64_t *cu_seqlens, int N, int64_t T, int Hkv, int D,
                               int64_t pages, int page, int max_pages);

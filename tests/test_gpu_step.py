@@ -621,6 +621,48 @@ def test_calls_the_compiled_binding_declines(kda, monkeypatch):
 
 
 # ---------------------------------------------------------------------------------------------- graphs
+@pytest.mark.parametrize("new", [1, 70])
+def test_calls_in_a_row_read_what_the_ones_before_wrote(kda, new):
+    """Steps whose every call takes the output of the call before, with and without a wait after each call."""
+    gen = _gen(40)
+    hq, hkv, dim, page, steps, beams = 8, 2, 128, 16, 12, 4
+    full = 40 + steps * new
+    _, _, table = step_ref.make_cache([full] * beams, hkv, dim, page, gen, "cuda")
+    k_cache = torch.zeros((int(table.max()) + 1, hkv, page, dim), dtype=torch.bfloat16, device="cuda")
+    v_cache = torch.zeros_like(k_cache)
+    x = torch.randn((beams, new, hq, dim), generator=gen, device="cuda").to(torch.bfloat16)
+    angle = torch.rand((full, dim // 2), generator=gen, device="cuda") * 6.28
+    cos, sin = angle.cos(), angle.sin()
+    lens = [torch.full((beams,), 40 + (i + 1) * new, dtype=torch.int32, device="cuda") for i in range(steps)]
+
+    def run(wait):
+        k_cache.zero_(), v_cache.zero_()
+        q, q_rot, out, scores = x.clone(), torch.empty_like(x), torch.empty_like(x), torch.zeros((1, beams), device="cuda")
+        sel = (scores, torch.empty((1, beams), dtype=torch.int32, device="cuda"),
+               torch.empty((1, beams), dtype=torch.int32, device="cuda"))
+        before = torch.zeros((1, beams), device="cuda")
+        torch.cuda.synchronize()
+        for i in range(steps):
+            kda.kda_kv_append(q[:, :, :hkv], q[:, :, hkv:2 * hkv], k_cache, v_cache, table, lens[i], cos=cos, sin=sin, q=q,
+                              q_out=q_rot)
+            if wait:
+                torch.cuda.synchronize()
+            kda.kda_window_attn(q_rot, k_cache, v_cache, table, lens[i], out, 100, sinks=3)
+            if wait:
+                torch.cuda.synchronize()
+            kda.kda_beam_select(out[:, -1].reshape(1, beams, hq * dim), before, *sel)
+            if wait:
+                torch.cuda.synchronize()
+            kda.kda_state_reorder(out, sel[2].view(-1), beams, dst=q)
+            if wait:
+                torch.cuda.synchronize()
+        kda.device_status()
+        return [y.clone() for y in (q, out, *sel, k_cache, v_cache)]
+    waited = run(True)
+    for _ in range(5):
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(waited, run(False)))
+
+
 def test_step_operators_in_a_graph(kda):
     """A captured step replays with the bits of direct calls on the data then in the buffers."""
     gen = _gen(14)
