@@ -3,7 +3,7 @@
 // Per pair (x, y) of a head and the position's angle a_i: (x cos a_i - y sin a_i, y cos a_i + x sin a_i), in fp32 and
 // rounded once.  Every element is read once and written once: the floor is the bytes of q, k, v and their copies.
 // Measured: 74 us for 8192 ragged tokens of 96 + 2 x 8 heads (472 MB), 6.4 TB/s, 94% of the measured copy rate; 2.8 us for
-// one token, 6.1 for 256 (launch latency).
+// one token, 4.8 for 256 (launch latency).
 // A thread owns one unit of 16 elements of the head (8 pairs) and walks the token's heads with the unit's 8 cosines
 // and sines in registers, so the angles are read once per token and not once per head.
 #include "kda_step.cuh"
