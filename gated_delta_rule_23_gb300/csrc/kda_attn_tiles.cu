@@ -716,6 +716,10 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
         Tile w;
         for (int i = 0; next_item(i, w); i++) {
             const int t0 = w.t0, t1 = w.t1, lo = h ? w.lo[1] : w.lo[0], hi = h ? w.hi[1] : w.hi[0];
+            // Every item has a Q, also one whose rows see nothing and one without a step for this half: only when it is there
+            // do the halves hand its place back, so that neither the place nor the barrier is taken again under a copy.
+            wait(b_q, q_phase);
+            q_phase ^= 1;
             // step by step P V of key tile t - 1, then S of tile t into the buffer that P came from
             for (int t = t0; t <= t1; t++) {
                 const bool pv = t > t0, sk = t < t1;
@@ -743,8 +747,6 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                     if (sk && buf == 0)
                         wait(b_full + 8 * ks, kp);
                     if (sk && now >= lo && now < hi) {
-                        if (now == lo)
-                            wait(b_q, q_phase);
                         tc_fence_after();
                         const uint32_t b = k_lo + ks * (S::TILE >> 4) + buf * (SUB * 128 >> 4), d = tm + TM_S + h * 128 + 64 * buf;
                         if (lead && !timeout) {
@@ -772,7 +774,6 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
                 if (sk && (ks += 2) >= S::SLOTS)
                     ks -= S::SLOTS, kp ^= 1;
             }
-            q_phase ^= 1;
         }
         if (lead) {
             // everything issued has to be through before tensor memory is freed
