@@ -258,7 +258,7 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
     }
     // no copy is in flight when the work was given up
     for (int i = done; i < mine && i < done + S::RING; i++)
-        mbar_wait(bar + 8 * (i % S::RING), (i / S::RING) & 1);
+        timeout |= !mbar_wait(bar + 8 * (i % S::RING), (i / S::RING) & 1);
     __syncwarp();
 
     // the warps' results: O where the warp's ring was, row-major

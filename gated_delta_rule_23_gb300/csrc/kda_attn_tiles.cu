@@ -701,7 +701,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
         }
         // no copy is in flight when the CTA leaves, also where the work was given up
         for (int it = max(issued - S::SLOTS, 0); it < issued; it++)
-            mbar_wait(b_full + 8 * (it % S::SLOTS), (it / S::SLOTS) & 1);
+            timeout |= !mbar_wait(b_full + 8 * (it % S::SLOTS), (it / S::SLOTS) & 1);
     } else if (warp == 9 || warp == 10) {
         // ------------------------------------------------------------ tensor-core issue, warp 9 for half 0, 10 for half 1
         // The warp walks the items and waits; one elected lane issues.  What an instruction needs (descriptors, addresses) is
@@ -778,7 +778,7 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
         if (lead) {
             // everything issued has to be through before tensor memory is freed
             umma_commit(b_drain + 8 * h);
-            mbar_wait(b_drain + 8 * h, 0);
+            timeout |= !mbar_wait(b_drain + 8 * h, 0);
         }
         __syncwarp();
     } else if (warp == 11) {
@@ -837,9 +837,9 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             loaded++;
         }
         if (loaded > 0)                              // no copy is in flight when the CTA leaves
-            mbar_wait(b_q, (loaded - 1) & 1);
+            timeout |= !mbar_wait(b_q, (loaded - 1) & 1);
         if (asked > answers)
-            mbar_wait(b_block, answers & 1);
+            timeout |= !mbar_wait(b_block, answers & 1);
     }
     if (CLUSTERED && !joined) {                      // the other warps, CTAs without an item, and those that gave up
         cluster_sync();
