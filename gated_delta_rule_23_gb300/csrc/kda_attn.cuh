@@ -98,7 +98,8 @@ __device__ __forceinline__ int token_place(const Tokens &tok, int64_t t, int64_t
 
 // One query row (token t of the batch, head h) at position pos, by a whole warp, straight from the definition:
 // every visible key in order, with the running maximum m and sum l of the softmax in base 2.  Keys that the row
-// does not see are never read.
+// does not see are never read.  o is the mean of the values so far, which no finite values carry past fp32's range (their sum
+// by the weights does from about 1e38 on).
 template <int DIM>
 __device__ void attn_row(const AttnArgs &p, int n, int64_t t, int h, int64_t pos, bool &bad)
 {
@@ -134,17 +135,20 @@ __device__ void attn_row(const AttnArgs &p, int n, int64_t t, int h, int64_t pos
         const float mn = fmaxf(m, s);
         const float mu = mn == -INFINITY ? 0.0f : mn;
         const float a = exp2f(m - mu), w = exp2f(s - mu);
-        l = l * a + w;
+        const float before = l * a;
+        l = before + w;
+        if (l != 0.0f) {
+            const float keep = before / l, take = w / l;
 #pragma unroll
-        for (int e = 0; e < PER; e++)
-            o[e] = fmaf(o[e], a, w * __bfloat162float(v[e]));
+            for (int e = 0; e < PER; e++)
+                o[e] = fmaf(take, __bfloat162float(v[e]), o[e] * keep);
+        }
         m = mn;
     }
-    const float r = l == 0.0f ? 0.0f : 1.0f / l;
     __nv_bfloat16 *out = p.out + (t * p.hq + h) * DIM + lane * PER;
 #pragma unroll
     for (int e = 0; e < PER; e++)
-        out[e] = __float2bfloat16_rn(l == 0.0f ? 0.0f : o[e] * r);
+        out[e] = __float2bfloat16_rn(o[e]);
     if (p.lse && lane == 0)
         p.lse[t * p.hq + h] = l == 0.0f ? -INFINITY : LN2 * (m + log2f(l));
 }
