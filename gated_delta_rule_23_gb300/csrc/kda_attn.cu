@@ -14,7 +14,7 @@ constexpr int ROW_THREADS = 256;
 // fixed.  The lanes read 32 splits' statistics at once.  A row that does not come out finite is taken again from the
 // definition (see kda_attn_tiles.cu).
 template <int DIM, int PER_ROW>
-__global__ void __launch_bounds__(ROW_THREADS) kda_attn_join_kernel(const AttnArgs p, const AttnPlan plan)
+__global__ void __launch_bounds__(ROW_THREADS) kda_attn_join_kernel(const __grid_constant__ AttnArgs p, const AttnPlan plan)
 {
     constexpr int PER = DIM / 32, WARPS = ROW_THREADS / 32, FLIGHT = 8;
     __shared__ float part[WARPS][DIM];
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(ROW_THREADS) kda_attn_join_kernel(const AttnAr
         int64_t i, len;
         const int n = token_place(p.tok, t, i, len, bad);
         if (i >= 0 && i < len)
-            attn_mend_row<DIM>(p, n, t, (int)(r % p.hq), cache_len(p.cache, n, bad) - len + i, bad);
+            attn_mend_rows<DIM>(p, n, 1, (int)t, (int)(r % p.hq), (int)(cache_len(p.cache, n, bad) - len + i), plan.margin);
     }
 }
 
@@ -194,6 +194,7 @@ AttnPlan make_plan(int window, int sinks, bool varlen, int N, int64_t T, int Hq,
             plan.decode = true;
             plan.row_tiles = (int)row_tiles;
             plan.granule = DECODE_KEYS;
+            plan.margin = DECODE_ROWS + DECODE_KEYS;
             plan.splits = s < 1 ? 1 : (int)s;
             plan.items = (int)(ctas16 * plan.splits);
             return plan;
@@ -202,6 +203,7 @@ AttnPlan make_plan(int window, int sinks, bool varlen, int N, int64_t T, int Hq,
     }
     plan.granule = page < 32 ? page : 32;
     plan.run = ATTN_ROWS / group;
+    plan.margin = plan.run + plan.granule;
     plan.magic = ((1u << 20) + group - 1) / group;
     int64_t tiles = varlen ? (T + (int64_t)(plan.run - 1) * N) / plan.run : (int64_t)N * ((T + plan.run - 1) / plan.run);
     if (varlen && tiles > T)

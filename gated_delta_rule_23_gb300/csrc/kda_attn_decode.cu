@@ -76,7 +76,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
 
 template <int DIM, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, 8 / WARPS)
-kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_constant__ CUtensorMap kmap,
+kda_attn_decode_kernel(const __grid_constant__ AttnArgs p, const AttnPlan plan, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap)
 {
     using S = Shape<DIM, WARPS>;
@@ -298,7 +298,7 @@ kda_attn_decode_kernel(const AttnArgs p, const AttnPlan plan, const __grid_const
                 p.lse[at] = L == 0.0f ? -INFINITY : LN2 * (M + log2f(L));
         }
         if (whole && L > 0.0f && L <= FLT_MAX && __any_sync(FULL, !finite))
-            attn_mend_row<DIM>(p, n, (int64_t)n * tokens + tok, head, len - tokens + tok, bad);
+            bad |= attn_mend_rows<DIM>(p, n, 1, n * tokens + tok, head, len - tokens + tok, plan.margin);
     };
     bool failed = __syncthreads_or(timeout);
     if (plan.cluster)

@@ -37,7 +37,7 @@
 //
 // A key that a row does not see gets P = 0.  0 x v is NaN for an infinite or NaN v, and the matrix product has no way
 // to skip it: rows past the sequence's end are cleared in shared memory, and an output row that does not come out
-// finite is taken again from the definition, key by key (attn_mend_row).
+// finite is taken again from the definition, key by key, unless what it sees makes it so (attn_mend_rows).
 #include "kda_attn.cuh"
 
 #include <atomic>
@@ -298,7 +298,7 @@ __device__ __forceinline__ uint32_t range_word(int a, int b, int w)
 // CLUSTERED: an item's splits are a cluster, one item a CTA.
 template <int DIM, bool CLUSTERED>
 __global__ void __launch_bounds__(THREADS, 1)
-kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_constant__ CUtensorMap kmap,
+kda_attn_tiles_kernel(const __grid_constant__ AttnArgs p, const AttnPlan plan, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap)
 {
     using S = Shape<DIM>;
@@ -653,11 +653,9 @@ kda_attn_tiles_kernel(const AttnArgs p, const AttnPlan plan, const __grid_consta
             z0 = f2_add(z0, z1);
             const bool finite = f2_lo(z0) + f2_hi(z0) == 0.0f;
             tc_fence_before();                // O is read before the next item's first P lets it be overwritten
-            for (unsigned again = __ballot_sync(FULL, mine && !finite && l > 0.0f && l <= FLT_MAX && !part); again; again &= again - 1) {
-                const int src = __ffs(again) - 1;
-                attn_mend_row<DIM>(p, w.n, __shfl_sync(FULL, tok, src), __shfl_sync(FULL, head, src),
-                                   __shfl_sync(FULL, pos, src), bad);
-            }
+            const unsigned again = __ballot_sync(FULL, mine && !finite && l > 0.0f && l <= FLT_MAX && !part);
+            if (again)
+                bad |= attn_mend_rows<DIM>(p, w.n, again, tok, head, pos, plan.margin);
         }
     } else if (warp == 8) {
         // ------------------------------------------------------------ copies
