@@ -78,7 +78,20 @@ def _device(t: torch.Tensor, name: str) -> torch.device:
     return dev
 
 
+def _fit(fn, args) -> None:
+    """ctypes keeps the low 32 bits of an int that has more: those are refused here."""
+    for a, kind in zip(args, fn.argtypes):
+        if kind is ctypes.c_int and not -2 ** 31 <= a < 2 ** 31:
+            raise ValueError(f"{fn.__name__}: {a} does not fit the 32 bits of the argument it is for")
+
+
+def _keys(count) -> int:
+    """A window or a number of sinks: 2^31 - 1 and anything above are every key."""
+    return min(int(count), 2 ** 31 - 1)
+
+
 def _call(fn, dev: torch.device, stream: Optional[torch.cuda.Stream], *args) -> None:
+    _fit(fn, args)
     if dev.index == torch.cuda.current_device():
         rc = fn(*args, (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream)
     else:
@@ -179,9 +192,8 @@ def kda_window_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     _need(out, "out", torch.bfloat16, q.shape, dev)
     if lse is not None:
         _need(lse, "lse", torch.float32, (b, t, hq), dev)
-    window = min(int(window), 2 ** 31 - 1)
     args = (q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
-            out.data_ptr(), _ptr(lse), float(d ** -0.5 if scale is None else scale), window, int(sinks),
+            out.data_ptr(), _ptr(lse), float(d ** -0.5 if scale is None else scale), _keys(window), _keys(sinks),
             _ptr(cu_seqlens), n, t, hq, hkv, d, pages, page, block_table.shape[1])
     if workspace is None:
         _call(_native.load().kda_window_attn, dev, stream, *args)
@@ -193,9 +205,10 @@ def kda_window_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
 def window_attn_workspace_size(window: int, sinks: int, N: int, T: int, Hq: int, Hkv: int, D: int, page: int,
                                max_pages: int, varlen: bool = False) -> int:
     """Bytes of workspace a kda_window_attn call of these sizes needs on the current device."""
-    return int(_native.load().kda_window_attn_workspace_size(min(int(window), 2 ** 31 - 1), int(sinks), int(varlen),
-                                                             int(N), int(T), int(Hq), int(Hkv), int(D), int(page),
-                                                             int(max_pages)))
+    fn = _native.load().kda_window_attn_workspace_size
+    args = (_keys(window), _keys(sinks), int(varlen), int(N), int(T), int(Hq), int(Hkv), int(D), int(page), int(max_pages))
+    _fit(fn, args)
+    return int(fn(*args))
 
 
 def kda_beam_select(logits: torch.Tensor, beam_scores: torch.Tensor, scores: torch.Tensor, tokens: torch.Tensor,
@@ -242,7 +255,9 @@ def kda_beam_select(logits: torch.Tensor, beam_scores: torch.Tensor, scores: tor
 
 def beam_select_workspace_size(B: int, W: int, V: int, K: int) -> int:
     """Bytes of workspace a kda_beam_select call of these sizes needs."""
-    return int(_native.load().kda_beam_select_workspace_size(int(B), int(W), int(V), int(K)))
+    fn, args = _native.load().kda_beam_select_workspace_size, (int(B), int(W), int(V), int(K))
+    _fit(fn, args)
+    return int(fn(*args))
 
 
 def kda_state_reorder(src: Tensors, parents: torch.Tensor, beams: int, dst: Optional[Tensors] = None,
