@@ -490,8 +490,9 @@ template <typename T> __global__ void __launch_bounds__(THREADS, 5) kda_beam_chu
 // Score of a candidate whose beam has offset c (-inf: nothing of the beam counts) and logit l.
 __device__ __forceinline__ float score_of(float c, float l) { return c == -INFINITY ? c : no_nan(c + l); }
 
-// The K best of all W x V candidates, one pass for each: what the short lists are a shortcut of.
-template <typename T> __device__ __noinline__ void pick_all(const BeamArgs &p, int b, const float *c, uint64_t *red)
+// The K best of all W x V candidates, one pass for each: what the short lists are a shortcut of.  own: the beams' scores, not
+// read again from memory, where the entry's new ones may have been written over them.
+template <typename T> __device__ __noinline__ void pick_all(const BeamArgs &p, int b, const float *c, const float *own, uint64_t *red)
 {
     uint64_t last = ~0ull;
     for (int k = 0; k < p.K; k++) {
@@ -501,7 +502,7 @@ template <typename T> __device__ __noinline__ void pick_all(const BeamArgs &p, i
             const T *l = static_cast<const T *>(p.logits) + row * p.row_stride;
             const bool done = p.finished && p.finished[row];
             for (int t = threadIdx.x; t < p.V; t += PICK_THREADS) {
-                const float s = done ? (t == p.eos ? no_nan(p.beam_scores[row]) : -INFINITY)
+                const float s = done ? (t == p.eos ? own[w] : -INFINITY)
                                      : score_of(c[w], no_nan(load_logit(l + t)));
                 const uint64_t x = key_of(s, (uint32_t)w * p.V + t);
                 if (x < last && x > best)
@@ -674,7 +675,7 @@ template <typename T> __global__ void __launch_bounds__(PICK_THREADS) kda_beam_p
         }
     }
     if (__syncthreads_or(again))
-        pick_all<T>(p, b, c, sh.red);
+        pick_all<T>(p, b, c, own, sh.red);
 }
 
 }  // namespace
@@ -730,6 +731,15 @@ static kda_status_t check_beam(const void *logits, kda_dtype_t dtype, int64_t ro
     if (!is_aligned(logits, dtype == KDA_DTYPE_BF16 ? 2 : 4) || !is_aligned(beam_scores, 4) ||
         !is_aligned(scores, 4) || !is_aligned(tokens, 4) || !is_aligned(parents, 4))
         return KDA_ERR_INVALID_ARGUMENT;
+    // the outputs overlap neither each other nor an input; scores may be beam_scores where a row of both is one entry's
+    const uint64_t rows = (uint64_t)B * W, picks = (uint64_t)B * K * 4;
+    const uint64_t read = ((rows - 1) * (uint64_t)row_stride + V) * (dtype == KDA_DTYPE_BF16 ? 2 : 4);
+    if (overlap(scores, picks, tokens, picks) || overlap(scores, picks, parents, picks) || overlap(tokens, picks, parents, picks))
+        return KDA_ERR_INVALID_ARGUMENT;
+    for (const void *out : {static_cast<const void *>(scores), static_cast<const void *>(tokens), static_cast<const void *>(parents)})
+        if (overlap(out, picks, logits, read) || overlap(out, picks, finished, rows) ||
+            (overlap(out, picks, beam_scores, rows * 4) && !(out == beam_scores && out == scores && K == W)))
+            return KDA_ERR_INVALID_ARGUMENT;
     return KDA_OK;
 }
 

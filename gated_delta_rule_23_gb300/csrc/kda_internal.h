@@ -78,6 +78,12 @@ cudaError_t step_read_and_clear_error(unsigned int *flag);
 uint32_t wait_limit();
 // SM count of the current device (looked up once per device); 0 when it cannot be read.
 int device_sms();
+// Whether two buffers share a byte (NULL or empty ones do not).
+inline bool overlap(const void *a, uint64_t a_bytes, const void *b, uint64_t b_bytes)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && a_bytes && b_bytes && x < y + b_bytes && y < x + a_bytes;
+}
 inline bool is_aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace kda

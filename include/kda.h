@@ -455,7 +455,8 @@ size_t kda_window_attn_workspace_size(int window, int sinks, int varlen, int N, 
  *   logits         bf16 or fp32 [B, W, V] as dtype says, rows row_stride elements apart (>= V).
  *   beam_scores    fp32 [B, W].   finished  uint8 [B, W] or NULL.   eos  token of finished beams, in [0, V).
  *   scores         fp32 [B, K];   tokens  int32 [B, K];   parents  int32 [B, K]: b W + w, a row of the batch.
- *   W <= 32, K <= 64, K <= W V, V <= 2^24, B W < 2^31.
+ *   W <= 32, K <= 64, K <= W V, V <= 2^24, B W < 2^31.  The outputs overlap neither each other nor an input, but that
+ *   scores may be beam_scores where K = W.
  * kda_beam_select_ws takes a caller-owned workspace of kda_beam_select_workspace_size bytes, 256-byte aligned.
  */
 kda_status_t kda_beam_select(const void *logits, kda_dtype_t dtype, int64_t row_stride, const float *beam_scores,

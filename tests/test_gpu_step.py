@@ -702,3 +702,22 @@ def test_step_operators_in_a_graph(kda):
         step()
         torch.cuda.synchronize()
         assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, (out, moved, *sel, k_cache, v_cache)))
+
+
+@pytest.mark.parametrize("v", [300, 40000])
+def test_beam_scores_in_place(kda, v):
+    """scores may be beam_scores where K = W, also where the entry is picked over all candidates."""
+    x = torch.full((2, 3, v), -30.0, device="cuda")
+    at = torch.tensor([v - 1, v // 2, 250, 40, 7], device="cuda")
+    x[:, :, at] = (torch.arange(5, device="cuda") * 1e-8 + 1e-7).flip(0)     # distinct logits of one score
+    scores = torch.tensor([[-300.0, -300.0, -300.5], [-300.0, -299.0, -300.0]], device="cuda")
+    done = torch.tensor([[0, 0, 1], [0, 1, 0]], dtype=torch.uint8, device="cuda")
+    want = _select(kda, x, scores, 3, done, 9)
+    _check_select(x, scores, done, 9, want)
+    place = scores.clone()
+    tokens, parents = torch.empty_like(want[1]), torch.empty_like(want[2])
+    kda.kda_beam_select(x, place, place, tokens, parents, finished=done, eos=9)
+    kda.device_status()
+    assert torch.equal(place, want[0]) and torch.equal(tokens, want[1]) and torch.equal(parents, want[2])
+    with pytest.raises(kda.KDAError):
+        kda.kda_beam_select(x, place, place.view(-1)[:4].view(2, 2), tokens[:, :2].contiguous(), parents[:, :2].contiguous())

@@ -1,0 +1,17 @@
+"""CPU checks of buffers that a decoder-step call would read and write at once: refused before any CUDA call."""
+import pytest
+
+from gated_delta_rule_23_gb300._native import KDA_ERR_INVALID_ARGUMENT
+from tests.test_step_abi import append, attn, beam, lib, reorder  # noqa: F401
+
+M = 1 << 20
+FAR = dict(logits=M, bs=2 * M, fin=3 * M, scores=4 * M, tokens=5 * M, parents=6 * M)      # 2 x 3 beams of 100 fp32 logits, 6 kept
+
+
+@pytest.mark.parametrize("kw", [
+    dict(scores=5 * M), dict(tokens=6 * M + 44), dict(parents=4 * M - 44), dict(tokens=2 * M), dict(parents=2 * M + 20),
+    dict(scores=M + 2396), dict(tokens=M - 44), dict(parents=3 * M + 4), dict(scores=2 * M), dict(scores=2 * M, bs=2 * M + 4),
+    dict(scores=2 * M + 4, K=3), dict(tokens=2 * M, K=3), dict(scores=2 * M + 16, W=4, K=4)])
+def test_selection_refuses_shared_buffers(lib, kw):  # noqa: F811
+    """scores in the place of beam_scores is allowed where K = W alone."""
+    assert beam(lib, **dict(FAR, **kw)) == KDA_ERR_INVALID_ARGUMENT
