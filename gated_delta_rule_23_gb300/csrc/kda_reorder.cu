@@ -8,6 +8,9 @@
 // one parent hit the cache); four layers of 4 bf16 states, 16 us.
 #include "kda_step.cuh"
 
+#include <algorithm>
+#include <vector>
+
 namespace kda {
 namespace {
 
@@ -57,6 +60,24 @@ template <int MAXW> __global__ void __launch_bounds__(REORDER_THREADS) kda_reord
     report(p.err, bad, DEVERR_CU_SEQLENS);
 }
 
+// Whether a buffer that a call writes shares a byte with any other one of it.
+struct Extent {
+    uintptr_t begin, end;
+    bool written;
+};
+bool any_overlap(std::vector<Extent> &all)
+{
+    std::sort(all.begin(), all.end(), [](const Extent &a, const Extent &b) { return a.begin < b.begin; });
+    uintptr_t end = 0, written_end = 0;      // of those before
+    for (const Extent &x : all) {
+        if (x.begin < written_end || (x.written && x.begin < end))
+            return true;
+        end = std::max(end, x.end);
+        written_end = x.written ? std::max(written_end, x.end) : written_end;
+    }
+    return false;
+}
+
 cudaError_t launch_reorder(const ReorderArgs &p, int64_t most, int groups, int tensors, cudaStream_t st)
 {
     int64_t gx = (most + REORDER_THREADS - 1) / REORDER_THREADS;
@@ -85,15 +106,31 @@ extern "C" kda_status_t kda_state_reorder(const void *const *src, void *const *d
     if (N / beams > 65535)
         return KDA_ERR_UNSUPPORTED;
     for (int i = 0; i < tensors; i++) {
-        if (row_bytes[i] < 0 || row_bytes[i] % 16 || row_bytes[i] > ((int64_t)1 << 46))
+        if (row_bytes[i] < 0 || row_bytes[i] % 16 || row_bytes[i] > ((int64_t)1 << 46) / N)
             return KDA_ERR_INVALID_ARGUMENT;
         if (row_bytes[i] > 0 && (!src[i] || !dst[i] || !is_aligned(src[i], 16) || !is_aligned(dst[i], 16)))
             return KDA_ERR_INVALID_ARGUMENT;
-        // in place, or apart
-        const uintptr_t a = reinterpret_cast<uintptr_t>(src[i]), b = reinterpret_cast<uintptr_t>(dst[i]);
-        const uintptr_t bytes = (uintptr_t)row_bytes[i] * (uintptr_t)N;
-        if (a != b && a < b + bytes && b < a + bytes)
+    }
+    // The tensors of a launch move side by side: each is reordered in place or into a buffer that nothing else of the call
+    // touches (several may have one source).
+    try {
+        std::vector<Extent> all;
+        all.reserve(2 * (size_t)tensors + 1);
+        const uintptr_t at = reinterpret_cast<uintptr_t>(parents);
+        all.push_back({at, at + (uintptr_t)N * sizeof *parents, false});
+        for (int i = 0; i < tensors; i++) {
+            if (row_bytes[i] == 0)
+                continue;
+            const uintptr_t a = reinterpret_cast<uintptr_t>(src[i]), b = reinterpret_cast<uintptr_t>(dst[i]);
+            const uintptr_t bytes = (uintptr_t)row_bytes[i] * (uintptr_t)N;
+            if (a != b)
+                all.push_back({a, a + bytes, false});
+            all.push_back({b, b + bytes, true});
+        }
+        if (any_overlap(all))
             return KDA_ERR_INVALID_ARGUMENT;
+    } catch (...) {
+        return KDA_ERR_CUDA;                 // no host memory
     }
     ReorderArgs p{};
     p.parents = parents, p.beams = beams;

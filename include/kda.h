@@ -473,7 +473,8 @@ size_t kda_beam_select_workspace_size(int B, int W, int V, int K);
  * kda_state_reorder -- rows follow their beams: dst[i][n] = src[i][parents[n]] for every row n < N of every
  * tensor i < tensors (states [N, H, 128, 128], cache rows, anything of row_bytes[i] contiguous bytes a row).
  * Rows come in groups of `beams` (N a multiple of it, beams <= 32) and parents[n] lies in the group of n.
- * src[i] == dst[i] reorders in place; otherwise the two do not overlap.  src, dst and row_bytes are HOST
+ * src[i] == dst[i] reorders in place; otherwise a dst[i] overlaps no other buffer of the call (several tensors may
+ * have one source): shared ones are refused.  src, dst and row_bytes are HOST
  * arrays read before the call returns; the tensors are 16-byte aligned and row_bytes a multiple of 16.
  */
 kda_status_t kda_state_reorder(const void *const *src, void *const *dst, const int64_t *row_bytes, int tensors,

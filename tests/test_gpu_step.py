@@ -721,3 +721,20 @@ def test_beam_scores_in_place(kda, v):
     assert torch.equal(place, want[0]) and torch.equal(tokens, want[1]) and torch.equal(parents, want[2])
     with pytest.raises(kda.KDAError):
         kda.kda_beam_select(x, place, place.view(-1)[:4].view(2, 2), tokens[:, :2].contiguous(), parents[:, :2].contiguous())
+
+
+def test_reorder_buffers_of_several_tensors(kda):
+    """One source for several tensors, neighbours in one allocation, in place beside out of place; tensors swapped by one call
+    are refused."""
+    gen = _gen(15)
+    pool = torch.randn((6, 4, 64), generator=gen, device="cuda")
+    before = pool.clone()
+    parents = torch.tensor([1, 0, 3, 3], dtype=torch.int32, device="cuda")
+    p = parents.long()
+    kda.kda_state_reorder([pool[0], pool[0], pool[3], pool[5]], parents, 4, dst=[pool[1], pool[2], pool[3], pool[4]])
+    kda.device_status()
+    for i, want in ((0, before[0]), (1, before[0][p]), (2, before[0][p]), (3, before[3][p]), (4, before[5][p]), (5, before[5])):
+        assert torch.equal(pool[i], want), i
+    for src, dst in (([0, 1], [1, 0]), ([0, 1], [2, 2]), ([0, 0], [0, 0]), ([0, 1], [0, 0])):
+        with pytest.raises(kda.KDAError):
+            kda.kda_state_reorder([pool[i] for i in src], parents, 4, dst=[pool[i] for i in dst])

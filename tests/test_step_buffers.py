@@ -15,3 +15,16 @@ FAR = dict(logits=M, bs=2 * M, fin=3 * M, scores=4 * M, tokens=5 * M, parents=6 
 def test_selection_refuses_shared_buffers(lib, kw):  # noqa: F811
     """scores in the place of beam_scores is allowed where K = W alone."""
     assert beam(lib, **dict(FAR, **kw)) == KDA_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("src, dst", [
+    ((M, 2 * M), (2 * M, M)), ((M, 2 * M), (3 * M, 3 * M)), ((M, 2 * M), (3 * M, 3 * M + 1008)), ((M, M), (M, M)),
+    ((M, M + 512), (M, 3 * M)), ((M, M + 512), (M, M + 512)), ((M, 2 * M, 3 * M), (4 * M, 5 * M, 2 * M + 1008)),
+    ((M, 4 * M), (M + 1008, 4 * M)), (tuple(M * i for i in range(1, 201)), tuple(M * (201 - i) for i in range(1, 201)))])
+def test_reorder_refuses_shared_buffers(lib, src, dst):  # noqa: F811
+    """What one tensor of a call is read from or written to is nobody else's destination (4 rows of 256 bytes each)."""
+    assert reorder(lib, src=src, dst=dst, rows=(256,) * len(src), parents=M // 2) == KDA_ERR_INVALID_ARGUMENT
+
+
+def test_reorder_refuses_to_write_its_parents(lib):  # noqa: F811
+    assert reorder(lib, src=(M,), dst=(2 * M,), parents=2 * M + 1020) == KDA_ERR_INVALID_ARGUMENT
