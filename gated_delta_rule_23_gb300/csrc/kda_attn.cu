@@ -129,6 +129,10 @@ kda_status_t check_attn(const void *q, int64_t q_stride, const void *k_cache, co
         return KDA_ERR_INVALID_ARGUMENT;
     if (q_stride % 8 || q_stride < (int64_t)Hq * D)
         return KDA_ERR_INVALID_ARGUMENT;
+    // rows that are taken again read q after the first out is stored
+    const uint64_t rows = (uint64_t)tokens * Hq, read = ((uint64_t)(tokens - 1) * q_stride + (uint64_t)Hq * D) * 2;
+    if (overlap(out, rows * D * 2, q, read) || overlap(lse, rows * 4, q, read) || overlap(lse, rows * 4, out, rows * D * 2))
+        return KDA_ERR_INVALID_ARGUMENT;
     return KDA_OK;
 }
 

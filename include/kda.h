@@ -422,7 +422,7 @@ kda_status_t kda_kv_append(const void *k, int64_t k_stride, const void *v, int64
  *
  *   q              bf16 [B, T, Hq, D], tokens q_stride elements apart; Hq a multiple of Hkv, at most 256 times
  *                  it: query head h reads key head h / (Hq / Hkv).
- *   out            bf16 [B, T, Hq, D];   lse  fp32 [B, T, Hq] or NULL.
+ *   out            bf16 [B, T, Hq, D];   lse  fp32 [B, T, Hq] or NULL.  Neither overlaps q or the other.
  *   scale          finite, >= 0.
  *   window         >= 1 (INT32_MAX: every earlier key);   sinks  >= 0.
  *

@@ -28,3 +28,11 @@ def test_reorder_refuses_shared_buffers(lib, src, dst):  # noqa: F811
 
 def test_reorder_refuses_to_write_its_parents(lib):  # noqa: F811
     assert reorder(lib, src=(M,), dst=(2 * M,), parents=2 * M + 1020) == KDA_ERR_INVALID_ARGUMENT
+
+
+# q, out and lse of 2 x 3 tokens with 8 heads of 128: q and out 12288 bytes, lse 192
+@pytest.mark.parametrize("kw", [
+    dict(out=M), dict(out=M + 12272), dict(out=M - 12272), dict(qs=2048, out=M + 5 * 4096 + 2032), dict(lse=M + 12284),
+    dict(lse=M - 188), dict(lse=3 * M + 12284), dict(lse=3 * M - 188), dict(out=M, T=1)])
+def test_attention_refuses_shared_buffers(lib, kw):  # noqa: F811
+    assert attn(lib, **dict(dict(q=M, out=3 * M, lse=5 * M), **kw)) == KDA_ERR_INVALID_ARGUMENT
