@@ -184,6 +184,12 @@ extern "C" kda_status_t kda_kv_append(const void *k, int64_t k_stride, const voi
         return KDA_ERR_INVALID_ARGUMENT;
     if (q == q_out && q && q_stride != (int64_t)Hq * D)
         return KDA_ERR_INVALID_ARGUMENT;
+    // a CTA takes a token: what another token reads is not written, but for q in place
+    const uint64_t before = (uint64_t)tokens - 1, turned = (uint64_t)tokens * Hq * D * 2;
+    if ((q != q_out && overlap(q_out, turned, q, (before * q_stride + (uint64_t)Hq * D) * 2)) ||
+        overlap(q_out, turned, k, (before * k_stride + (uint64_t)Hkv * D) * 2) ||
+        overlap(q_out, turned, v, (before * v_stride + (uint64_t)Hkv * D) * 2))
+        return KDA_ERR_INVALID_ARGUMENT;
     AppendArgs p{};
     p.k = static_cast<const __nv_bfloat16 *>(k);
     p.v = static_cast<const __nv_bfloat16 *>(v);

@@ -402,7 +402,8 @@ size_t kda_fwd_smem_bytes(void);
  *   interleaved    0: element i pairs with i + rotary / 2; 1: element 2 i pairs with 2 i + 1.  Pair i is
  *                  (x, y) -> (x cos_i - y sin_i, y cos_i + x sin_i), in fp32, rounded once to bf16.
  *   q, q_out       bf16 [B, T, Hq, D] (q's tokens q_stride apart; q_out contiguous), or both NULL with
- *                  Hq = 0.  q_out may equal q where q is contiguous.  Tokens without a position are copied.
+ *                  Hq = 0.  q_out may equal q where q is contiguous; else it overlaps none of q, k and v.  Tokens
+ *                  without a position are copied.
  *
  * Positions from `positions` on have no row: reported as above.
  */

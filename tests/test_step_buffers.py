@@ -36,3 +36,11 @@ def test_reorder_refuses_to_write_its_parents(lib):  # noqa: F811
     dict(lse=M - 188), dict(lse=3 * M + 12284), dict(lse=3 * M - 188), dict(out=M, T=1)])
 def test_attention_refuses_shared_buffers(lib, kw):  # noqa: F811
     assert attn(lib, **dict(dict(q=M, out=3 * M, lse=5 * M), **kw)) == KDA_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("kw", [
+    dict(qo=M + 12272), dict(qo=M - 12272), dict(qs=2048, qo=M + 5 * 4096 + 2032), dict(qo=2 * M), dict(qo=2 * M + 3056),
+    dict(qo=3 * M - 12272), dict(q=2 * M, qo=2 * M), dict(vs=512, qo=3 * M + 5 * 1024 + 496)])
+def test_append_refuses_shared_buffers(lib, kw):  # noqa: F811
+    """q_out may be q, but no other part of it, and nothing of k or v (6 tokens of 2 heads of 128: 3072 bytes)."""
+    assert append(lib, **dict(dict(q=M, k=2 * M, v=3 * M, qo=5 * M), **kw)) == KDA_ERR_INVALID_ARGUMENT
