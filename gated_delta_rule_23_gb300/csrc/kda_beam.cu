@@ -665,9 +665,12 @@ template <typename T> __global__ void __launch_bounds__(PICK_THREADS) kda_beam_p
             const int w = x / p.chunks;
             if (kind[w] != 0)
                 continue;
-            // a list by values has every logit from l up; one by keys may have left out equals of its last, l, too
+            // a list by values has every logit from l up; one by keys may have left out equals of its last, l, too.  What was
+            // left out is a logit of type T: the neighbours are T's.  (With fp32's for bf16 logits, which often tie, as many as a
+            // quarter of the entries of rows in few chunks were picked over all candidates for a logit that bf16 does not have.)
+            constexpr bool step16 = sizeof(T) == 2;
             const float l = stats[x].z;
-            const bool by_keys = __float_as_int(stats[x].w) & BY_KEYS, step16 = by_keys && sizeof(T) == 2;
+            const bool by_keys = __float_as_int(stats[x].w) & BY_KEYS;
             if (l == l && score_of(c[w], l) == last &&
                 ((by_keys && score_of(c[w], neighbour(l, true, step16)) == last) ||
                  (l != -INFINITY && score_of(c[w], neighbour(l, false, step16)) == last)))

@@ -738,3 +738,38 @@ def test_reorder_buffers_of_several_tensors(kda):
     for src, dst in (([0, 1], [1, 0]), ([0, 1], [2, 2]), ([0, 0], [0, 0]), ([0, 1], [0, 0])):
         with pytest.raises(kda.KDAError):
             kda.kda_state_reorder([pool[i] for i in src], parents, 4, dst=[pool[i] for i in dst])
+
+
+@pytest.mark.parametrize("place", [0, 50000, 99000])
+@pytest.mark.parametrize("k", [1, 4, 8])
+def test_beam_bf16_ties_at_the_last_place(kda, k, place):
+    """bf16 logits that tie at the K-th place, in rows whose scores are so low that fp32 logits beside them would tie too:
+    picked from the short lists, not over all candidates (five times the time for K = 1, and it grows with K)."""
+    gen = _gen(k)
+    b, w, v = 64, 2, 100000
+    logits = torch.randn((b, w, v), generator=gen, device="cuda").to(torch.bfloat16)
+    scores = torch.tensor([-20.0, -60.0], device="cuda").repeat(b, 1)
+    at = place + 40 * torch.arange(k + 3, device="cuda")
+    tied = logits.clone()
+    tied[:, 0, at] = 9.0
+    distinct = logits.clone()
+    distinct[:, 0, at] = (9.0 + 0.0625 * torch.arange(k + 3, device="cuda").flip(0)).to(torch.bfloat16)
+    outs = []
+    for x in (distinct, tied):
+        out = _select(kda, x, scores, k)
+        _check_select(x, scores, None, 0, out)
+        assert out[1].tolist() == [at[:k].tolist()] * b and out[2].tolist() == [[i * w] * k for i in range(b)]
+        outs.append(out)
+    times = []
+    for x, out in zip((distinct, tied), outs):
+        best = math.inf
+        for _ in range(7):
+            a, z = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            torch.cuda.synchronize()
+            a.record()
+            kda.kda_beam_select(x, scores, *out)
+            z.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(z))
+        times.append(best)
+    assert times[1] <= 3 * times[0], times
