@@ -14,7 +14,7 @@ namespace kda {
 namespace {
 
 // CTAs of 128 threads, eight an SM, with the loads of two heads in flight a thread.  8192 tokens of 96 + 2 x 8 heads of 128
-// (472 MB): 76 us; four heads in flight 82, one 78; CTAs of 256 threads 79 to 96.
+// (472 MB), when launches did not overlap yet: 76 us (74 since); four heads in flight 82, one 78; CTAs of 256 threads 79 to 96.
 constexpr int APPEND_THREADS = 128, CTAS_PER_SM = 8;
 constexpr int FLIGHT = 2;      // heads whose loads a thread has in flight
 

@@ -2,7 +2,7 @@
 //
 // A decode step reads every visible key and value once for a handful of rows: the floor is the cache's bytes at the
 // memory's rate, and the arithmetic (16 rows wide on mma.sync) has to stay out of the way.  One CTA takes a (sequence, key
-// head) or a split of its keys; each of its warps works by itself on blocks of 16 keys, every fourth one, that its lane 0
+// head) or a split of its keys; each of its 4 or 8 warps works by itself on blocks of 16 keys, every 4th or 8th one, that its lane 0
 // brings in with bulk tensor copies into the warp's own ring of shared memory: no barrier of the CTA in the loop, and
 // RING x 8 KB in flight a warp.  The warps' results (running maximum, sum, O in fp32) are joined once at the end in shared
 // memory.  Up to 8 splits are a cluster, which joins its CTAs' results over distributed shared memory in the same
@@ -243,6 +243,8 @@ kda_attn_decode_kernel(const __grid_constant__ AttnArgs p, const AttnPlan plan, 
             l[0] += s[c][0] + s[c][1];
             l[1] += s[c][2] + s[c][3];
         }
+        // P in bf16, V's type, as the product takes it: 2^-9 of each, which leaves the output 2.3e-3 off (norm) where its own
+        // rounding alone leaves 1.65e-3; the sum l is of what P was before
         const uint32_t a[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
                                pack_bf16(s[1][2], s[1][3])};
 #pragma unroll

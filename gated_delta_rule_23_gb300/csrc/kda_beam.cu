@@ -5,9 +5,15 @@
 // row, the chunk's maximum and sum and its K + 1 best logits (kda_beam_chunks_kernel), and a second kernel, one CTA a
 // batch entry, turns those few into scores and picks (kda_beam_pick_kernel).  Each logit is read once: the floor.
 //
-// Measured: 32 x 8 rows of 131072 fp32 logits (134 MB), 35.5 us, 3.8 TB/s, 56% of the measured copy rate: the chunks stream
-// at 60 to 70% of it and all end together, so that their tail (the bound, the few threads looked at again) and the pick's
-// chain of latencies (5.5 us) are in nobody's shadow.  One request of 4 x 32001 bf16 logits: 9.1 us, both chains.
+// Measured: 32 x 8 rows of 131072 fp32 logits, a tenth of the rows finished and not read (121 MB of 134), 35.7 us, 3.4 TB/s,
+// half the measured copy rate: the chunks stream at 55 to 65% of it and all end together, so that their tail (the bound, the few
+// threads looked at again) and the pick's chain of latencies (5.5 us) are in nobody's shadow; the fp32 chunk kernel also spills (68
+// bytes at the 48 registers of five CTAs an SM).  One request of 4 x 32001 bf16 logits: 9.0 us, both chains.
+//
+// Chunks that are whole steps of rows on 16 bytes are read by vectors, others one logit at a time in the same order.  No row
+// finished, nothing left in L2, us for fp32 | bf16 logits: 131072 (all whole) 43.6 | 27.2, 128256 (the last of three chunks is not) 41.2 |
+// 32.5, 151936 45.7 | 37.0, 50304 24.1 | 20.0, 50257 (rows off 16 bytes, none is) 23.0 | 21.9: fp32 loses nothing by it, bf16 up to a
+// fifth.
 //
 // What the short lists may hide: logits so close that their fp32 scores are equal tie by index and not by logit.  That
 // matters only where the value a chunk's list was cut off at reaches the K-th score and a neighbouring logit value has
@@ -684,7 +690,7 @@ template <typename T> __global__ void __launch_bounds__(PICK_THREADS) kda_beam_p
 }  // namespace
 
 // Tokens of a chunk: whole steps of 2048 (what the CTA's threads take of bf16 logits at once).  Rows are cut so that the
-// chunks are one wave of five CTAs an SM, but not under 2048 tokens; few and long chunks also leave fewer lists to pick
+// chunks are one wave of five CTAs on each of a GB300's 152 SMs (a constant: the workspace's size follows from the sizes alone), but not under 2048 tokens; few and long chunks also leave fewer lists to pick
 // from.  32 x 8 rows of 131072 logits, in L2: 32.8 us in 3 chunks a row, 36.8 in 4, 34.4 in 2, 40 in 8.  4 rows of 32001:
 // the same with 2048, 4096 and 8192 tokens.
 static int beam_chunk(int B, int W, int V)
