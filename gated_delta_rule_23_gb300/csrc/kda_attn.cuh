@@ -138,18 +138,16 @@ __device__ void attn_row(const AttnArgs &p, int n, int64_t t, int h, int64_t pos
         const float a = exp2f(m - mu), w = exp2f(s - mu);
         const float before = l * a;
         l = before + w;
-        if (l != 0.0f) {
-            const float keep = before / l, take = w / l;
+        const float keep = l == 0.0f ? 1.0f : before / l, take = l == 0.0f ? 0.0f : w / l;
 #pragma unroll
-            for (int e = 0; e < PER; e++)
-                o[e] = fmaf(take, __bfloat162float(v[e]), o[e] * keep);
-        }
+        for (int e = 0; e < PER; e++)
+            o[e] = fmaf(take, __bfloat162float(v[e]), o[e] * keep);
         m = mn;
     }
     __nv_bfloat16 *out = p.out + (t * p.hq + h) * DIM + lane * PER;
 #pragma unroll
     for (int e = 0; e < PER; e++)
-        out[e] = __float2bfloat16_rn(o[e]);
+        out[e] = __float2bfloat16_rn(l == 0.0f ? 0.0f : o[e]);
     if (p.lse && lane == 0)
         p.lse[t * p.hq + h] = l == 0.0f ? -INFINITY : LN2 * (m + log2f(l));
 }

@@ -109,3 +109,22 @@ def test_attn_value_in_sight_holds_nobody_up(kda, batch, new, length, window, at
     clean = _best_time(call)
     v[int(table[0, at // 64]), :, at % 64, 17] = value
     assert _best_time(call) <= 10 * clean
+
+
+@pytest.mark.parametrize("new, hq", [(1, 4), (3, 4), (150, 3)])
+def test_attn_value_of_a_key_without_weight(kda, new, hq):  # noqa: F811
+    """A key whose score is -infinity has weight 0, and 0 x NaN is NaN, also in rows that are taken again (here for large values)
+    and where it is the first key that the row sees."""
+    gen = _gen(new)
+    length = 200
+    k, v, table = step_ref.make_cache([length], 1, 128, 16, gen, "cuda")
+    v.copy_(torch.where(v.isnan(), v, (3e38 - 1e37 * v.abs().clamp(max=4)).to(torch.bfloat16)))
+    page = int(table[0, 0])
+    k[page, 0, 0] = -math.inf
+    v[page, 0, 0, 9] = math.nan
+    q = torch.randn((1, new, hq, 128), generator=gen, device="cuda").abs().mul(0.3).to(torch.bfloat16)
+    out, lse = _call(kda, q, k, v, table, [length], 200)
+    for i in sorted({0, new // 2, new - 1}):
+        o, l, mag, _ = step_ref.attention([q[0, i:i + 1]], k, v, table, [length - new + i + 1], [1], 200, 0, 128 ** -0.5)[0]
+        _same_kind(out[0, i:i + 1], o, mag)
+        assert bool(torch.isnan(out[0, i, :, 9]).all()) and bool(((lse[0, i].double() - l[0]).abs() <= 1e-4 * (1 + l[0].abs())).all())
