@@ -152,8 +152,26 @@ __device__ void attn_row(const AttnArgs &p, int n, int64_t t, int h, int64_t pos
         p.lse[t * p.hq + h] = l == 0.0f ? -INFINITY : LN2 * (m + log2f(l));
 }
 
-// Columns (bit e: column e of the lane's DIM / 32) that hold a value that is not finite at one of the positions a..b of
-// sequence n, by a whole warp; it stops when all the wanted ones are found.  16 positions at a time, which lie in one page.
+// What of the lane's DIM / 32 columns is not finite: bit e for NaN in column e, bit 4 + e for +infinity, bit 8 + e for -infinity.
+template <int DIM> __device__ __forceinline__ unsigned odd_kinds(const uint32_t (&x)[DIM / 64])
+{
+    unsigned kinds = 0;
+#pragma unroll
+    for (int e = 0; e < DIM / 32; e++) {
+        const uint32_t u = e & 1 ? x[e / 2] >> 16 : x[e / 2] & 0xffffu;
+        if ((u & 0x7f80u) == 0x7f80u)
+            kinds |= 1u << (e + (u & 0x7fu ? 0 : (u & 0x8000u ? 8 : 4)));
+    }
+    return kinds;
+}
+// What of these output kinds the values found do not account for: an infinity takes one of its sign, NaN a NaN or both
+// infinities.
+__device__ __forceinline__ unsigned unexplained(unsigned kinds, unsigned found)
+{
+    return kinds & ~(found | (found >> 4 & found >> 8 & 15u));
+}
+// The kinds of values that are not finite at the positions a..b of sequence n, by a whole warp; it stops when they account for
+// all that is wanted (~0u: never).  16 positions at a time, which lie in one page.
 template <int DIM>
 __device__ unsigned odd_values(const AttnArgs &p, int n, int kvh, int a, int b, unsigned wanted)
 {
@@ -173,10 +191,8 @@ __device__ unsigned odd_values(const AttnArgs &p, int n, int kvh, int a, int b, 
                 x[i][w] = j0 + i >= a && j0 + i <= b ? v[i * (DIM / 2) + w] : 0;
 #pragma unroll
         for (int i = 0; i < 16; i++)
-#pragma unroll
-            for (int w = 0; w < WORDS; w++)
-                found |= ((x[i][w] & 0x7f80u) == 0x7f80u ? 1u : 0u) << (2 * w) | ((x[i][w] & 0x7f800000u) == 0x7f800000u ? 2u : 0u) << (2 * w);
-        if (__all_sync(0xffffffffu, (wanted & ~found) == 0))
+            found |= odd_kinds<DIM>(x[i]);
+        if (__all_sync(0xffffffffu, unexplained(wanted, found) == 0))
             break;
     }
     return found;
@@ -187,12 +203,12 @@ __device__ unsigned odd_values(const AttnArgs &p, int n, int kvh, int a, int b, 
 // definition.)  Three things do that: a value that the row sees and that is not finite, and then the output is right; one that
 // it does not see and that a tensor-core product took in (0 x infinity); and finite values whose sum passes fp32's range.  So a
 // row is left as it is when none of the positions that its products may have taken in and that it does not see holds such a value in
-// one of the output's columns that are not finite, and for each of these columns one that it sees does.  The others are taken
-// again by attn_row.  The products take in what the CTA's other rows see: up to `margin` positions before the row's window and
+// one of the output's columns that are not finite, and for each of these columns what it sees makes that infinity or that NaN.
+// The others are taken again by attn_row.  The products take in what the CTA's other rows see: up to `margin` positions before the row's window and
 // behind its own position, and the rest of the sinks' last 32.  All rows are looked at together first.
 // Measured with one NaN in a value of the call: 8192 tokens, 96 heads over 8 (1.21 ms without), the NaN in the first tokens
-// 1.43 ms, half way 39 ms, nearly all of it attn_row for the tile's rows in front of the NaN; every row by attn_row 320 ms.  A
-// decode step of 256 sequences 0.17 to 0.25 ms (0.17 without, 2.0 by attn_row).
+// 1.47 ms, half way 39 ms, nearly all of it attn_row for the tile's rows in front of the NaN; every row by attn_row 320 ms.  A
+// decode step of 256 sequences 0.17 to 0.29 ms (0.17 without, 2.0 by attn_row).
 // By a whole warp; true when an entry of the page table was out of range.
 template <int DIM>
 __device__ __noinline__ bool attn_mend_rows(const AttnArgs &p, int n, unsigned again, int t, int h, int pos, int margin)
@@ -202,43 +218,44 @@ __device__ __noinline__ bool attn_mend_rows(const AttnArgs &p, int n, unsigned a
     bool bad = false;
     __syncwarp();                                    // the rows' stores come before what follows
     const int last = (int)cache_len(p.cache, n, bad) - 1, kvh = __shfl_sync(FULL, h, __ffs(again) - 1) / p.group;
-    auto odd_columns = [&](int src) -> unsigned {    // of the row's output
+    auto kinds_of = [&](int src) -> unsigned {       // the row's output
         const int64_t at = (int64_t)__shfl_sync(FULL, t, src) * p.hq + __shfl_sync(FULL, h, src);
         const uint32_t *o = reinterpret_cast<const uint32_t *>(p.out + at * DIM) + lane * (DIM / 64);
-        unsigned x = 0;
+        uint32_t x[DIM / 64];
 #pragma unroll
         for (int w = 0; w < DIM / 64; w++)
-            x |= ((o[w] & 0x7f80u) == 0x7f80u ? 1u : 0u) << (2 * w) | ((o[w] & 0x7f800000u) == 0x7f800000u ? 2u : 0u) << (2 * w);
-        return x;
+            x[w] = o[w];
+        return odd_kinds<DIM>(x);
     };
-    // rows at positions a..b, with these columns not finite in any of them, are right as they are
-    auto right = [&](int a, int b, unsigned columns) -> bool {
+    // rows at positions a..b, whose outputs have these kinds, are right as they are
+    auto right = [&](int a, int b, unsigned kinds) -> bool {
         const int gone = b - p.window;               // the last position before b's window
         unsigned hidden = odd_values<DIM>(p, n, kvh, max(max(a - p.window + 1 - margin, p.sinks), 0), gone, ~0u);
         hidden |= odd_values<DIM>(p, n, kvh, a + 1, min(b + margin, last), ~0u);
         hidden |= odd_values<DIM>(p, n, kvh, p.sinks, min(((p.sinks + 31) & -32) - 1, gone), ~0u);
-        if (__any_sync(FULL, (hidden & columns) != 0))
+        const unsigned columns = (kinds | kinds >> 4 | kinds >> 8) & 15u;
+        if (__any_sync(FULL, ((hidden | hidden >> 4 | hidden >> 8) & columns) != 0))
             return false;
-        unsigned seen = odd_values<DIM>(p, n, kvh, 0, min(p.sinks - 1, a), columns);
-        if (__any_sync(FULL, (columns & ~seen) != 0))
-            seen |= odd_values<DIM>(p, n, kvh, max(gone + 1, p.sinks), a, columns & ~seen);
-        return __all_sync(FULL, (columns & ~seen) == 0);
+        unsigned seen = odd_values<DIM>(p, n, kvh, 0, min(p.sinks - 1, a), kinds);
+        if (__any_sync(FULL, unexplained(kinds, seen) != 0))
+            seen |= odd_values<DIM>(p, n, kvh, max(gone + 1, p.sinks), a, unexplained(kinds, seen));
+        return __all_sync(FULL, unexplained(kinds, seen) == 0);
     };
     if (again & (again - 1)) {
         int a = INT32_MAX, b = 0;
-        unsigned columns = 0;
+        unsigned kinds = 0;
         for (unsigned x = again; x; x &= x - 1) {
             const int src = __ffs(x) - 1, at = __shfl_sync(FULL, pos, src);
             a = min(a, at);
             b = max(b, at);
-            columns |= odd_columns(src);
+            kinds |= kinds_of(src);
         }
-        if (right(a, b, columns))
+        if (right(a, b, kinds))
             return bad;
     }
     for (; again; again &= again - 1) {
         const int src = __ffs(again) - 1, at = __shfl_sync(FULL, pos, src);
-        if (!right(at, at, odd_columns(src)))
+        if (!right(at, at, kinds_of(src)))
             attn_row<DIM>(p, n, __shfl_sync(FULL, t, src), __shfl_sync(FULL, h, src), at, bad);
     }
     return bad;

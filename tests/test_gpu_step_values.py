@@ -111,6 +111,23 @@ def test_attn_value_in_sight_holds_nobody_up(kda, batch, new, length, window, at
     assert _best_time(call) <= 10 * clean
 
 
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("new, hq, length, window", [(1, 4, 90, 60), (3, 4, 1300, 1200), (150, 3, 400, 90), (40, 8, 9000, 8800)])
+def test_attn_value_in_sight_among_large_ones(kda, new, hq, length, window, value):  # noqa: F811
+    """Finite values whose sums pass fp32's range beside one that is not finite: the output is of its kind."""
+    gen = _gen(new)
+    k, v, table = step_ref.make_cache([length], 1, 128, 16, gen, "cuda")
+    wide = v[..., 30:40]                              # the other columns stay finite in any form
+    wide.copy_(torch.where(wide.isnan(), wide, (3e38 - 1e37 * wide.abs().clamp(max=4)).to(torch.bfloat16)))
+    at = length - 1 - new // 2                        # rows before its position do not see it
+    v[int(table[0, at // 16]), 0, at % 16, 30:40] = value
+    q = torch.randn((1, new, hq, 128), generator=gen, device="cuda").mul(0.3).to(torch.bfloat16)
+    out, _ = _call(kda, q, k, v, table, [length], window)
+    for i in sorted({0, max(new // 2 - 1, 0), new // 2, new - 1}):
+        o, _, mag, _ = step_ref.attention([q[0, i:i + 1]], k, v, table, [length - new + i + 1], [1], window, 0, 128 ** -0.5)[0]
+        _same_kind(out[0, i:i + 1], o, mag)
+
+
 @pytest.mark.parametrize("new, hq", [(1, 4), (3, 4), (150, 3)])
 def test_attn_value_of_a_key_without_weight(kda, new, hq):  # noqa: F811
     """A key whose score is -infinity has weight 0, and 0 x NaN is NaN, also in rows that are taken again (here for large values)
