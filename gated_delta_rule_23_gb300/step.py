@@ -218,7 +218,8 @@ def kda_beam_select(logits: torch.Tensor, beam_scores: torch.Tensor, scores: tor
 
     logits: bf16 or fp32 [B, W, V] (rows evenly spaced); beam_scores: fp32 [B, W]; finished: optional uint8 or bool
     [B, W], beams whose one continuation is ``eos`` at their own score.  Writes scores fp32, tokens int32 and parents
-    int32 [B, K], best first, ties to the lower (beam, token); parents are rows b * W + w of the batch.
+    int32 [B, K], best first, ties to the lower (beam, token); parents are rows b * W + w of the batch.  ``scores`` may
+    be ``beam_scores`` where K = W; the outputs overlap nothing else.
     """
     rc = _native.binding().beam_select(logits, beam_scores, scores, tokens, parents, finished, eos,
                                        None if stream is None else stream.cuda_stream, workspace)
@@ -265,7 +266,7 @@ def kda_state_reorder(src: Tensors, parents: torch.Tensor, beams: int, dst: Opti
     """dst[i][n] = src[i][parents[n]] for every tensor of ``src`` (one tensor or a sequence of them, [N, ...]).
 
     ``parents``: int32 [N]; rows come in groups of ``beams`` and a row's parent lies in its own group (what
-    ``kda_beam_select`` writes).  ``dst`` None (or the same tensors): in place.
+    ``kda_beam_select`` writes).  ``dst`` None (or the same tensors): in place; a destination overlaps no other tensor.
     """
     src = [src] if isinstance(src, torch.Tensor) else list(src)
     dst = src if dst is None else ([dst] if isinstance(dst, torch.Tensor) else list(dst))

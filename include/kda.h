@@ -418,9 +418,10 @@ kda_status_t kda_kv_append(const void *k, int64_t k_stride, const void *v, int64
  * position p sees key j when j <= p and (j > p - window or j < sinks):
  *   out = sum_j softmax_j(scale q.k_j) v_j,   lse = log sum_j exp(scale q.k_j)   over the visible j;
  * a query that sees no key gets out = 0 and lse = -inf.  What lies in keys and values that a query does
- * not see (stale rows, infinities, NaN) does not reach its output.  (A row whose neighbours in the call see a value that is not
- * finite, or whose sinks share 32 positions with one, and that does not see it, is taken again key by key: about 0.7 us a key.  A
- * value that the row does see costs a look through the values it sees; what lies past a sequence's end costs nothing.)
+ * not see (stale rows, infinities, NaN) does not reach its output.  (A row is taken again key by key, about
+ * 0.7 us a key, when other rows of the call near it see a value that is not finite and it does not, when its sinks
+ * share 32 positions with one, and when its finite values' sum passes fp32's range.  A value that the row does
+ * see costs a look through the values it sees; what lies past a sequence's end costs nothing.)
  *
  *   q              bf16 [B, T, Hq, D], tokens q_stride elements apart; Hq a multiple of Hkv, at most 256 times
  *                  it: query head h reads key head h / (Hq / Hkv).
