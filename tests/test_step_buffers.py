@@ -44,3 +44,23 @@ def test_attention_refuses_shared_buffers(lib, kw):  # noqa: F811
 def test_append_refuses_shared_buffers(lib, kw):  # noqa: F811
     """q_out may be q, but no other part of it, and nothing of k or v (6 tokens of 2 heads of 128: 3072 bytes)."""
     assert append(lib, **dict(dict(q=M, k=2 * M, v=3 * M, qo=5 * M), **kw)) == KDA_ERR_INVALID_ARGUMENT
+
+
+# What tests/test_step_abi.py has refused with one address for every buffer, with buffers apart: each for its own reason.
+@pytest.mark.parametrize("kw", [
+    dict(kc=None), dict(table=None), dict(lens=None), dict(N=0), dict(T=-1), dict(Hkv=0), dict(pages=0), dict(max_pages=0),
+    dict(page=15), dict(page=8192), dict(kc=7 * M + 8), dict(table=9 * M + 2), dict(lens=10 * M + 1), dict(cu=11 * M + 4),
+    dict(q=None), dict(q=M + 8), dict(out=None), dict(out=3 * M + 2), dict(lse=5 * M + 2), dict(Hq=0), dict(Hq=7),
+    dict(window=0), dict(sinks=-1), dict(qs=1000), dict(qs=1028)])
+def test_attention_refuses_each_for_itself(lib, kw):  # noqa: F811
+    far = dict(q=M, out=3 * M, lse=5 * M, kc=7 * M, vc=8 * M, table=9 * M, lens=10 * M)
+    assert attn(lib, **dict(far, **kw)) == KDA_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("kw", [
+    dict(logits=None), dict(bs=None), dict(scores=None), dict(tokens=None), dict(parents=None), dict(dtype=0), dict(dtype=7),
+    dict(stride=99), dict(eos=-1), dict(eos=100), dict(B=0), dict(W=0), dict(W=33), dict(V=0), dict(K=0), dict(K=65),
+    dict(V=2, K=7, stride=2, eos=0), dict(logits=M + 2), dict(dtype=1, logits=M + 1), dict(bs=2 * M + 2), dict(scores=4 * M + 2),
+    dict(tokens=5 * M + 1), dict(parents=6 * M + 2)])
+def test_selection_refuses_each_for_itself(lib, kw):  # noqa: F811
+    assert beam(lib, **dict(FAR, **kw)) == KDA_ERR_INVALID_ARGUMENT
