@@ -18,10 +18,12 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(_PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libkda.so")
 UNITS = ["kda_api", "kda_prep", "kda_recur", "kda_recurrent", "kda_decode", "kda_host", "kda_noalloc", "kda_scan",
-         "kda_step", "kda_append", "kda_attn", "kda_attn_tiles", "kda_attn_decode", "kda_beam", "kda_reorder"]
+         "kda_step", "kda_append", "kda_attn", "kda_attn_tiles", "kda_attn_decode", "kda_beam", "kda_reorder",
+         "kda_linear", "kda_linear_tokens", "kda_verify"]
 SOURCES = [os.path.join(CSRC, u + ".cu") for u in UNITS]
 HEADERS = [os.path.join(INCLUDE, "kda.h"), os.path.join(CSRC, "kda_device.cuh"), os.path.join(CSRC, "kda_internal.h"),
-           os.path.join(CSRC, "kda_plan.h"), os.path.join(CSRC, "kda_step.cuh"), os.path.join(CSRC, "kda_attn.cuh")]
+           os.path.join(CSRC, "kda_plan.h"), os.path.join(CSRC, "kda_step.cuh"), os.path.join(CSRC, "kda_attn.cuh"),
+           os.path.join(CSRC, "kda_linear.cuh")]
 BINDING_SOURCE = os.path.join(CSRC, "kda_binding.cpp")
 BINDING_PATH = os.path.join(BUILD_DIR, "kda_binding.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -153,6 +155,20 @@ def load() -> ctypes.CDLL:
         lib.kda_beam_select_workspace_size.restype = Z
         lib.kda_state_reorder.argtypes = [P, P, P, I, P, I, I, P]
         lib.kda_state_reorder.restype = I
+        linear = [P, I64, P, I64, P, I64, P, P, F, P, P, P, I, P, P, I, I64, I, I, I]
+        lib.kda_linear_attn.argtypes = linear + [P]
+        lib.kda_linear_attn.restype = I
+        lib.kda_linear_attn_ws.argtypes = linear + [P, Z, P]
+        lib.kda_linear_attn_ws.restype = I
+        lib.kda_linear_attn_workspace_size.argtypes = [I, I, I64, I, I]
+        lib.kda_linear_attn_workspace_size.restype = Z
+        verify = [P, I, I64, P, P, P, P, P, P, P, P, I, I, I]
+        lib.kda_verify_drafts.argtypes = verify + [P]
+        lib.kda_verify_drafts.restype = I
+        lib.kda_verify_drafts_ws.argtypes = verify + [P, Z, P]
+        lib.kda_verify_drafts_ws.restype = I
+        lib.kda_verify_drafts_workspace_size.argtypes = [I, I, I, I]
+        lib.kda_verify_drafts_workspace_size.restype = Z
         _lib = lib
     return _lib
 
@@ -171,7 +187,8 @@ def binding():
         spec.loader.exec_module(mod)
         mod.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                    for f in ("kda_kv_append", "kda_window_attn", "kda_window_attn_ws", "kda_beam_select",
-                             "kda_beam_select_ws", "kda_state_reorder")))
+                             "kda_beam_select_ws", "kda_state_reorder", "kda_linear_attn", "kda_linear_attn_ws",
+                             "kda_verify_drafts", "kda_verify_drafts_ws")))
         _binding = mod
     return _binding
 

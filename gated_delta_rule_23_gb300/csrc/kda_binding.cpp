@@ -23,6 +23,10 @@ decltype(&kda_window_attn_ws) g_attn_ws;
 decltype(&kda_beam_select) g_beam;
 decltype(&kda_beam_select_ws) g_beam_ws;
 decltype(&kda_state_reorder) g_reorder;
+decltype(&kda_linear_attn) g_linear;
+decltype(&kda_linear_attn_ws) g_linear_ws;
+decltype(&kda_verify_drafts) g_verify;
+decltype(&kda_verify_drafts_ws) g_verify_ws;
 
 const at::Tensor *tensor(PyObject *o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 
@@ -287,15 +291,124 @@ PyObject *state_reorder(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
+// An optional dense tensor: its pointer, or NULL for None; false when it is something else.
+template <typename T> bool optional(PyObject *o, at::ScalarType type, at::IntArrayRef shape, int dev, const T **p)
+{
+    *p = nullptr;
+    if (o == Py_None)
+        return true;
+    const at::Tensor *t = tensor(o);
+    if (!dense(t, type, shape, dev))
+        return false;
+    *p = static_cast<const T *>(t->data_ptr());
+    return true;
+}
+
+// q, k, v, out, log_decay, gate, scale, initial_state, final_state, lens, cu_seqlens, stream, workspace
+PyObject *linear_attn(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return answer([&]() -> int {
+        if (n != 13)
+            return -1;
+        const at::Tensor *q = tensor(a[0]), *k = tensor(a[1]), *v = tensor(a[2]), *out = tensor(a[3]);
+        const int dev = device_of(q);
+        if (dev < 0 || q->dim() != 4)
+            return -1;
+        const int64_t b = q->size(0), t = q->size(1), h = q->size(2), d = q->size(3);
+        const int64_t qs = rows(q, b, t, dev), ks = rows(k, b, t, dev), vs = rows(v, b, t, dev);
+        if (qs < 0 || ks < 0 || vs < 0 || k->sizes() != v->sizes() || k->size(3) != d || h > INT32_MAX || b > INT32_MAX ||
+            d > INT32_MAX || !dense(out, at::kBFloat16, q->sizes(), dev))
+            return -1;
+        int64_t seqs = b;
+        const int64_t *cu = nullptr;
+        const int32_t *lens;
+        const float *log_decay, *gate;
+        if (a[10] != Py_None) {
+            const at::Tensor *x = tensor(a[10]);
+            if (!x || b != 1 || x->dim() != 1 || x->numel() < 2 || x->numel() > INT32_MAX || !dense(x, at::kLong, x->sizes(), dev))
+                return -1;
+            cu = static_cast<const int64_t *>(x->data_ptr());
+            seqs = x->numel() - 1;
+        }
+        if (!optional(a[9], at::kInt, {seqs}, dev, &lens) || !optional(a[4], at::kFloat, {h}, dev, &log_decay) ||
+            !optional(a[5], at::kFloat, {b, t, h}, dev, &gate))
+            return -1;
+        const at::Tensor *init = tensor(a[7]), *fin = tensor(a[8]), *any = init ? init : fin, *ws = tensor(a[12]);
+        if ((a[7] != Py_None && !init) || (a[8] != Py_None && !fin) || (a[12] != Py_None && (!ws || !dense(ws, at::kByte, ws->sizes(), dev))))
+            return -1;
+        kda_dtype_t type = KDA_DTYPE_NONE;
+        if (any) {
+            const at::ScalarType st = any->scalar_type();
+            if ((st != at::kBFloat16 && st != at::kFloat) || (init && !dense(init, st, {seqs, h, d, d}, dev)) ||
+                (fin && !dense(fin, st, {seqs, h, d, d}, dev)))
+                return -1;
+            type = st == at::kBFloat16 ? KDA_DTYPE_BF16 : KDA_DTYPE_FP32;
+        }
+        kda_stream_t s;
+        if (!stream_of(a[11], dev, &s))
+            return -1;
+        const double scale = a[6] == Py_None ? 1.0 / std::sqrt((double)d) : PyFloat_AsDouble(a[6]);
+        if (PyErr_Occurred())
+            return -1;
+        const void *ip = init ? init->data_ptr() : nullptr;
+        void *fp = fin ? fin->data_ptr() : nullptr;
+        if (ws)
+            return g_linear_ws(q->data_ptr(), qs, k->data_ptr(), ks, v->data_ptr(), vs, log_decay, gate, (float)scale,
+                               out->data_ptr(), ip, fp, type, lens, cu, (int)seqs, t, (int)h, (int)k->size(2), (int)d,
+                               ws->data_ptr(), (size_t)ws->numel(), s);
+        return g_linear(q->data_ptr(), qs, k->data_ptr(), ks, v->data_ptr(), vs, log_decay, gate, (float)scale, out->data_ptr(),
+                        ip, fp, type, lens, cu, (int)seqs, t, (int)h, (int)k->size(2), (int)d, s);
+    });
+}
+
+// logits, draft_tokens, uniform, noise, tokens, counts, draft_probs, temperature, draft_lens, stream, workspace
+PyObject *verify_drafts(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return answer([&]() -> int {
+        if (n != 11)
+            return -1;
+        const at::Tensor *l = tensor(a[0]), *drafts = tensor(a[1]), *uniform = tensor(a[2]), *noise = tensor(a[3]);
+        const at::Tensor *tokens = tensor(a[4]), *counts = tensor(a[5]), *ws = tensor(a[10]);
+        const int dev = device_of(l);
+        if (dev < 0 || l->dim() != 3 || l->numel() == 0)
+            return -1;
+        const int64_t b = l->size(0), k = l->size(1) - 1, v = l->size(2);
+        const bool half = l->scalar_type() == at::kBFloat16;
+        if ((!half && l->scalar_type() != at::kFloat) || b > INT32_MAX || k > INT32_MAX || v > INT32_MAX)
+            return -1;
+        const int64_t step = k > 0 ? l->stride(1) : (b > 1 ? l->stride(0) : v);
+        if ((v > 1 && l->stride(2) != 1) || (b > 1 && l->stride(0) != (k + 1) * step) || step < v)
+            return -1;
+        if (!dense(drafts, at::kInt, {b, k}, dev) || !dense(uniform, at::kFloat, {b, k}, dev) ||
+            !dense(noise, at::kFloat, {b, v}, dev) || !dense(tokens, at::kInt, {b, k + 1}, dev) || !dense(counts, at::kInt, {b}, dev) ||
+            (a[10] != Py_None && (!ws || !dense(ws, at::kByte, ws->sizes(), dev))))
+            return -1;
+        const float *probs, *temperature;
+        const int32_t *lens;
+        kda_stream_t s;
+        if (!optional(a[6], at::kFloat, {b, k, v}, dev, &probs) || !optional(a[7], at::kFloat, {b}, dev, &temperature) ||
+            !optional(a[8], at::kInt, {b}, dev, &lens) || !stream_of(a[9], dev, &s))
+            return -1;
+        const kda_dtype_t dtype = half ? KDA_DTYPE_BF16 : KDA_DTYPE_FP32;
+        const int32_t *dp = static_cast<const int32_t *>(drafts->data_ptr());
+        const float *up = static_cast<const float *>(uniform->data_ptr()), *np = static_cast<const float *>(noise->data_ptr());
+        int32_t *tp = static_cast<int32_t *>(tokens->data_ptr()), *cp = static_cast<int32_t *>(counts->data_ptr());
+        if (ws)
+            return g_verify_ws(l->data_ptr(), dtype, step, dp, probs, up, np, temperature, lens, tp, cp, (int)b, (int)k, (int)v,
+                               ws->data_ptr(), (size_t)ws->numel(), s);
+        return g_verify(l->data_ptr(), dtype, step, dp, probs, up, np, temperature, lens, tp, cp, (int)b, (int)k, (int)v, s);
+    });
+}
+
 // Addresses of libkda.so's entry points, in the order of the globals above.
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    void *p[6];
-    if (n != 6) {
-        PyErr_SetString(PyExc_TypeError, "bind takes 6 addresses");
+    void *p[10];
+    if (n != 10) {
+        PyErr_SetString(PyExc_TypeError, "bind takes 10 addresses");
         return nullptr;
     }
-    for (int i = 0; i < 6; i++) {
+    for (int i = 0; i < 10; i++) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (PyErr_Occurred())
             return nullptr;
@@ -306,6 +419,10 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
     g_beam = reinterpret_cast<decltype(g_beam)>(p[3]);
     g_beam_ws = reinterpret_cast<decltype(g_beam_ws)>(p[4]);
     g_reorder = reinterpret_cast<decltype(g_reorder)>(p[5]);
+    g_linear = reinterpret_cast<decltype(g_linear)>(p[6]);
+    g_linear_ws = reinterpret_cast<decltype(g_linear_ws)>(p[7]);
+    g_verify = reinterpret_cast<decltype(g_verify)>(p[8]);
+    g_verify_ws = reinterpret_cast<decltype(g_verify_ws)>(p[9]);
     Py_RETURN_NONE;
 }
 
@@ -316,6 +433,8 @@ PyMethodDef methods[] = {{"bind", as_c(bind), METH_FASTCALL, nullptr},
                          {"window_attn", as_c(window_attn), METH_FASTCALL, nullptr},
                          {"beam_select", as_c(beam_select), METH_FASTCALL, nullptr},
                          {"state_reorder", as_c(state_reorder), METH_FASTCALL, nullptr},
+                         {"linear_attn", as_c(linear_attn), METH_FASTCALL, nullptr},
+                         {"verify_drafts", as_c(verify_drafts), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "kda_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

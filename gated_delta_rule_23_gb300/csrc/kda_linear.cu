@@ -1,0 +1,120 @@
+// kda_linear_attn: checks of the arguments, and which kernel a call takes.
+#include "kda_linear.cuh"
+
+#include <cmath>
+
+namespace kda {
+
+static kda_status_t check_linear(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                 int64_t v_stride, const float *log_decay, const float *gate, float scale, const void *out,
+                                 const void *init, const void *fin, kda_dtype_t state, const int32_t *lens,
+                                 const int64_t *cu, int N, int64_t T, int H, int Hkv, int D)
+{
+    if (N < 1 || T < 0 || H < 1 || Hkv < 1 || H % Hkv)
+        return KDA_ERR_INVALID_ARGUMENT;
+    if ((init || fin) && state != KDA_DTYPE_BF16 && state != KDA_DTYPE_FP32)
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (lens && cu)
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (!is_aligned(log_decay, 4) || !is_aligned(gate, 4) || !is_aligned(init, 16) || !is_aligned(fin, 16) ||
+        !is_aligned(lens, 4) || !is_aligned(cu, 8))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (D != 64 && D != 128)
+        return KDA_ERR_UNSUPPORTED;
+    if (!std::isfinite(scale))
+        return KDA_ERR_UNSUPPORTED;
+    // tokens are 32-bit coordinates of the bulk copies; warps of the token kernel (at most 16 a pair) and its grid
+    if (T > INT32_MAX || (cu ? T : (int64_t)N * T) > INT32_MAX || (int64_t)N * H > INT32_MAX / 16)
+        return KDA_ERR_UNSUPPORTED;
+    const uint64_t states = (uint64_t)N * H * D * D * (state == KDA_DTYPE_BF16 ? 2 : 4);
+    if (init != fin && overlap(init, states, fin, states))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (overlap(fin, states, log_decay, (uint64_t)H * 4) || overlap(fin, states, lens, (uint64_t)N * 4) ||
+        overlap(fin, states, cu, (uint64_t)(N + 1) * 8))
+        return KDA_ERR_INVALID_ARGUMENT;
+    const uint64_t tokens = cu ? (uint64_t)T : (uint64_t)N * T;
+    if (tokens == 0)
+        return KDA_OK;
+    if (!q || !k || !v || !out || !is_aligned(q, 16) || !is_aligned(k, 16) || !is_aligned(v, 16) || !is_aligned(out, 16))
+        return KDA_ERR_INVALID_ARGUMENT;
+    const int64_t row = (int64_t)H * D, kv_row = (int64_t)Hkv * D;
+    if (q_stride % 8 || q_stride < row || k_stride % 8 || k_stride < kv_row || v_stride % 8 || v_stride < kv_row)
+        return KDA_ERR_INVALID_ARGUMENT;
+    // a head's CTA writes its tokens and its state while others still read theirs
+    const uint64_t written = tokens * row * 2;
+    const struct {
+        const void *p;
+        uint64_t bytes;
+    } read[] = {{q, ((tokens - 1) * q_stride + row) * 2}, {k, ((tokens - 1) * k_stride + kv_row) * 2},
+                {v, ((tokens - 1) * v_stride + kv_row) * 2}, {gate, tokens * H * 4}};
+    for (const auto &r : read)
+        if (overlap(out, written, r.p, r.bytes) || overlap(fin, states, r.p, r.bytes))
+            return KDA_ERR_INVALID_ARGUMENT;
+    if (overlap(out, written, fin, states) || overlap(out, written, init, states) || overlap(out, written, log_decay, (uint64_t)H * 4) ||
+        overlap(out, written, lens, (uint64_t)N * 4) || overlap(out, written, cu, (uint64_t)(N + 1) * 8))
+        return KDA_ERR_INVALID_ARGUMENT;
+    return KDA_OK;
+}
+
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" size_t kda_linear_attn_workspace_size(int varlen, int N, int64_t T, int H, int D)
+{
+    (void)varlen, (void)N, (void)T, (void)H, (void)D;
+    return 0;
+}
+
+extern "C" kda_status_t kda_linear_attn_ws(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                           int64_t v_stride, const float *log_decay, const float *gate, float scale, void *out,
+                                           const void *initial_state, void *final_state, kda_dtype_t state_dtype,
+                                           const int32_t *lens, const int64_t *cu_seqlens, int N, int64_t T, int H, int Hkv,
+                                           int D, void *workspace, size_t workspace_bytes, kda_stream_t stream)
+{
+    const kda_status_t s = check_linear(q, q_stride, k, k_stride, v, v_stride, log_decay, gate, scale, out, initial_state,
+                                        final_state, state_dtype, lens, cu_seqlens, N, T, H, Hkv, D);
+    if (s != KDA_OK)
+        return s;
+    const kda_dtype_t state = initial_state || final_state ? state_dtype : KDA_DTYPE_NONE;
+    const size_t need = kda_linear_attn_workspace_size(cu_seqlens != nullptr, N, T, H, D);
+    if (need > 0 && (!workspace || !is_aligned(workspace, 256) || workspace_bytes < need))
+        return KDA_ERR_INVALID_ARGUMENT;
+    LinearArgs p{};
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k = static_cast<const __nv_bfloat16 *>(k);
+    p.v = static_cast<const __nv_bfloat16 *>(v);
+    p.q_stride = q_stride, p.k_stride = k_stride, p.v_stride = v_stride;
+    p.log_decay = log_decay, p.gate = gate, p.scale = scale;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.init = initial_state, p.fin = final_state;
+    p.lens = lens;
+    p.tok = Tokens{cu_seqlens, T, N};
+    p.H = H, p.group = H / Hkv, p.dim = D;
+    if (step_error_word(&p.err) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return launch_linear_tokens(p, state, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+extern "C" kda_status_t kda_linear_attn(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                        int64_t v_stride, const float *log_decay, const float *gate, float scale, void *out,
+                                        const void *initial_state, void *final_state, kda_dtype_t state_dtype,
+                                        const int32_t *lens, const int64_t *cu_seqlens, int N, int64_t T, int H, int Hkv,
+                                        int D, kda_stream_t stream)
+{
+    const kda_status_t c = check_linear(q, q_stride, k, k_stride, v, v_stride, log_decay, gate, scale, out, initial_state,
+                                        final_state, state_dtype, lens, cu_seqlens, N, T, H, Hkv, D);
+    if (c != KDA_OK)
+        return c;
+    const size_t need = kda_linear_attn_workspace_size(cu_seqlens != nullptr, N, T, H, D);
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    void *ws = nullptr;
+    if (need > 0 && pool_alloc(&ws, need, st) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    kda_status_t s = kda_linear_attn_ws(q, q_stride, k, k_stride, v, v_stride, log_decay, gate, scale, out, initial_state,
+                                        final_state, state_dtype, lens, cu_seqlens, N, T, H, Hkv, D, ws, need, stream);
+    if (ws && cudaFreeAsync(ws, st) != cudaSuccess && s == KDA_OK)
+        s = KDA_ERR_CUDA;
+    return s;
+}

@@ -2,7 +2,9 @@
 
 A decode or prefill step of a hybrid decoder around ``kda_fwd`` / ``kda_fwd_recurrent``: ``kda_kv_append`` stores
 rotated keys and values in a paged cache, ``kda_window_attn`` attends to it through a sliding window with sinks,
-``kda_beam_select`` picks the next beams from the logits, ``kda_state_reorder`` moves the states after them.  The
+``kda_beam_select`` picks the next beams from the logits, ``kda_state_reorder`` moves the states after them.
+``kda_linear_attn`` is the recurrent layer of models without a delta rule, ``kda_verify_drafts`` decides which drafted tokens
+of a speculative run stand.  The
 caller passes CUDA tensors and pre-allocated outputs; every step of the computation runs in libkda.so.
 
 Every function first offers its arguments to the compiled binding (csrc/kda_binding.cpp), which makes the call when they
@@ -17,7 +19,7 @@ from typing import Optional, Sequence, Union
 import torch
 
 from . import _native
-from ._native import KDA_DTYPE_BF16, KDA_DTYPE_FP32, KDA_OK, KDAError
+from ._native import KDA_DTYPE_BF16, KDA_DTYPE_FP32, KDA_DTYPE_NONE, KDA_OK, KDAError
 from .api import _check, _ptr
 
 Tensors = Union[torch.Tensor, Sequence[torch.Tensor]]
@@ -289,3 +291,134 @@ def kda_state_reorder(src: Tensors, parents: torch.Tensor, beams: int, dst: Opti
             _need(b, f"dst[{i}]", a.dtype, a.shape, dev)
         ps[i], pd[i], rows[i] = a.data_ptr(), b.data_ptr(), (a.numel() // n if n else 0) * a.element_size()
     _call(_native.load().kda_state_reorder, dev, stream, ps, pd, rows, count, parents.data_ptr(), n, int(beams))
+
+
+def kda_linear_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                    log_decay: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                    scale: Optional[float] = None, initial_state: Optional[torch.Tensor] = None,
+                    final_state: Optional[torch.Tensor] = None, lens: Optional[torch.Tensor] = None,
+                    cu_seqlens: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+                    workspace: Optional[torch.Tensor] = None) -> None:
+    """Linear attention with a decay for each head: S_t = exp(a_t) S_(t-1) + k_t v_t^T, o_t = scale S_t^T q_t.
+
+    q, out: bf16 [B, T, H, D]; k, v: bf16 [B, T, Hkv, D] (tokens evenly spaced: slices of one projection's rows); the log
+    of the decay is ``log_decay`` (fp32 [H]) + ``gate`` (fp32 [B, T, H]), each optional, at most 0; ``scale`` defaults to
+    D ** -0.5.  States: bf16 or fp32 [N, H, D (v), D (k)], ``final_state`` may be ``initial_state``.  ``lens``: int32 [N],
+    the tokens of each row that count (the others' outputs stay as they were); ``cu_seqlens``: int64 [N + 1] with B = 1.
+    ``workspace``: optional uint8 tensor of ``linear_attn_workspace_size`` bytes; without it the library's pool provides one
+    where the call needs it.
+    """
+    rc = _native.binding().linear_attn(q, k, v, out, log_decay, gate, scale, initial_state, final_state, lens, cu_seqlens,
+                                       None if stream is None else stream.cuda_stream, workspace)
+    if rc is not None:
+        return _raise(rc)
+    dev = _device(q, "kda_linear_attn")
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, T, H, D] and k [B, T, Hkv, D]")
+    b, t, h, d = q.shape
+    hkv = k.shape[2]
+    lead = (b, t)
+    qs = _rows(q, "q", h, d, lead, dev)
+    ks = _rows(k, "k", hkv, d, lead, dev)
+    vs = _rows(v, "v", hkv, d, lead, dev)
+    _need(out, "out", torch.bfloat16, q.shape, dev)
+    n = b
+    if cu_seqlens is not None:
+        if b != 1:
+            raise ValueError("cu_seqlens requires B == 1")
+        if lens is not None:
+            raise ValueError("lens and cu_seqlens exclude each other")
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be int64 [N + 1]")
+        n = cu_seqlens.numel() - 1
+        _need(cu_seqlens, "cu_seqlens", torch.int64, (n + 1,), dev)
+    if lens is not None:
+        _need(lens, "lens", torch.int32, (n,), dev)
+    if log_decay is not None:
+        _need(log_decay, "log_decay", torch.float32, (h,), dev)
+    if gate is not None:
+        _need(gate, "gate", torch.float32, (b, t, h), dev)
+    dtype = KDA_DTYPE_NONE
+    for s, name in ((initial_state, "initial_state"), (final_state, "final_state")):
+        if s is None:
+            continue
+        if s.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"{name}: expected bf16 or fp32, got {s.dtype}")
+        _need(s, name, s.dtype, (n, h, d, d), dev)
+        this = KDA_DTYPE_BF16 if s.dtype is torch.bfloat16 else KDA_DTYPE_FP32
+        if dtype not in (KDA_DTYPE_NONE, this):
+            raise TypeError("initial_state and final_state must have the same dtype")
+        dtype = this
+    args = (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(log_decay), _ptr(gate),
+            float(d ** -0.5 if scale is None else scale), out.data_ptr(), _ptr(initial_state), _ptr(final_state), dtype,
+            _ptr(lens), _ptr(cu_seqlens), n, t, h, hkv, d)
+    if workspace is None:
+        _call(_native.load().kda_linear_attn, dev, stream, *args)
+    else:
+        size = _workspace(workspace, dev)
+        _call(_native.load().kda_linear_attn_ws, dev, stream, *args, workspace.data_ptr(), size)
+
+
+def linear_attn_workspace_size(N: int, T: int, H: int, D: int, varlen: bool = False) -> int:
+    """Bytes of workspace a kda_linear_attn call of these sizes needs."""
+    fn, args = _native.load().kda_linear_attn_workspace_size, (int(varlen), int(N), int(T), int(H), int(D))
+    _fit(fn, args)
+    return int(fn(*args))
+
+
+def kda_verify_drafts(logits: torch.Tensor, draft_tokens: torch.Tensor, uniform: torch.Tensor, noise: torch.Tensor,
+                      tokens: torch.Tensor, counts: torch.Tensor, draft_probs: Optional[torch.Tensor] = None,
+                      temperature: Optional[torch.Tensor] = None, draft_lens: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None, workspace: Optional[torch.Tensor] = None) -> None:
+    """Speculative decoding's verification: the drafts that the target's distribution accepts, and the token after them.
+
+    logits: bf16 or fp32 [B, K + 1, V] (rows evenly spaced), row i the target's after i drafts; draft_tokens: int32
+    [B, K]; draft_probs: fp32 [B, K, V], or None where the drafts are certain (looked up, greedy); uniform: fp32 [B, K]
+    from [0, 1); noise: fp32 [B, V] from the exponential distribution; temperature: fp32 [B], 0 for greedy (None: 1);
+    draft_lens: int32 [B], the drafts that each request has (None: K).  Writes tokens int32 [B, K + 1], the accepted
+    drafts, the token after them and then -1, and counts int32 [B], how many that is: 1 to K + 1.
+    """
+    rc = _native.binding().verify_drafts(logits, draft_tokens, uniform, noise, tokens, counts, draft_probs, temperature,
+                                         draft_lens, None if stream is None else stream.cuda_stream, workspace)
+    if rc is not None:
+        return _raise(rc)
+    dev = _device(logits, "kda_verify_drafts")
+    if logits.dim() != 3 or logits.shape[1] < 1:
+        raise ValueError("logits must be [B, K + 1, V]")
+    b, rows, v = logits.shape
+    k = rows - 1
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"logits: expected bf16 or fp32, got {logits.dtype}")
+    s = logits.stride()
+    step = s[1] if rows > 1 else (s[0] if b > 1 else v)
+    if (v > 1 and s[2] != 1) or (b > 1 and s[0] != rows * step) or step < v:
+        raise ValueError(f"logits: the rows must be contiguous and evenly spaced, got strides {s}")
+    _need(draft_tokens, "draft_tokens", torch.int32, (b, k), dev)
+    _need(uniform, "uniform", torch.float32, (b, k), dev)
+    _need(noise, "noise", torch.float32, (b, v), dev)
+    _need(tokens, "tokens", torch.int32, (b, rows), dev)
+    _need(counts, "counts", torch.int32, (b,), dev)
+    if draft_probs is not None:
+        _need(draft_probs, "draft_probs", torch.float32, (b, k, v), dev)
+    if temperature is not None:
+        _need(temperature, "temperature", torch.float32, (b,), dev)
+    if draft_lens is not None:
+        _need(draft_lens, "draft_lens", torch.int32, (b,), dev)
+    args = (logits.data_ptr(), KDA_DTYPE_BF16 if logits.dtype is torch.bfloat16 else KDA_DTYPE_FP32, step,
+            draft_tokens.data_ptr(), _ptr(draft_probs), uniform.data_ptr(), noise.data_ptr(), _ptr(temperature),
+            _ptr(draft_lens), tokens.data_ptr(), counts.data_ptr(), b, k, v)
+    if workspace is None:
+        _call(_native.load().kda_verify_drafts, dev, stream, *args)
+    else:
+        size = _workspace(workspace, dev)
+        _call(_native.load().kda_verify_drafts_ws, dev, stream, *args, workspace.data_ptr(), size)
+
+
+def verify_drafts_workspace_size(B: int, K: int, V: int, dtype: torch.dtype = torch.bfloat16) -> int:
+    """Bytes of workspace a kda_verify_drafts call of these sizes and type of logits needs."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"dtype: expected bf16 or fp32, got {dtype}")
+    fn = _native.load().kda_verify_drafts_workspace_size
+    args = (KDA_DTYPE_BF16 if dtype is torch.bfloat16 else KDA_DTYPE_FP32, int(B), int(K), int(V))
+    _fit(fn, args)
+    return int(fn(*args))

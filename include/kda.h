@@ -483,6 +483,79 @@ size_t kda_beam_select_workspace_size(int B, int W, int V, int K);
 kda_status_t kda_state_reorder(const void *const *src, void *const *dst, const int64_t *row_bytes, int tensors,
                                const int32_t *parents, int N, int beams, kda_stream_t stream);
 
+/*
+ * kda_linear_attn -- linear attention whose state decays by one factor for each head: per sequence, head h and token t
+ *   a = log_decay[h] + gate[t][h]   (one that is NULL counts 0),
+ *   S_t = exp(a) S_(t-1) + k_t v_t^T,   o_t = scale S_t^T q_t.
+ * It stands beside kda_fwd in models whose recurrent layers have no delta rule; states have kda_fwd's layout
+ * (kda_state_reorder moves them) and may be updated in place.
+ *
+ *   q              bf16 [B, T, H, D], tokens q_stride elements apart;   k, v  bf16 [B, T, Hkv, D], H a multiple of
+ *                  Hkv: head h reads key head h / (H / Hkv).  D is 64 or 128.
+ *   log_decay      fp32 [H] or NULL;   gate  fp32 [B, T, H] or NULL.  Their sum is at most 0: a positive one is taken as 0
+ *                  and reported by kda_device_status as KDA_ERR_INVALID_ARGUMENT.  -INFINITY clears the state (anything
+ *                  below -200 counts as -200, whose factor is 0 in fp32).
+ *   scale          finite.
+ *   out            bf16 [B, T, H, D].
+ *   initial_state, final_state   [N, H, D (v), D (k)] of state_dtype, or NULL (zeros; not returned).  They may be the same.
+ *   lens           int32 [N] or NULL: only the first lens[n] of a sequence's T tokens count (a batch padded on the right;
+ *                  the tokens of a speculative run that kda_verify_drafts counted); not with cu_seqlens.
+ * Rows of out behind a sequence's tokens stay as they were.  No output overlaps an input or the other output, except that
+ * final_state may be initial_state.
+ *
+ * Sequences of a few tokens are evaluated token by token in fp32, the others in chunks of 64 tokens on the tensor cores:
+ * there the scores within a chunk and the state that a chunk's queries read are rounded to bf16, as out is, while the state itself stays
+ * in fp32 from chunk to chunk; keys times their decay are two bf16 terms (2^-17) for fp32 states, one for bf16 states.  A
+ * token's infinite or NaN value reaches that token's output and later ones', and no earlier one's; a query that is not
+ * finite spoils its own output only.
+ * kda_linear_attn takes its workspace (groups' states where few heads face many tokens) from the library's pool,
+ * kda_linear_attn_ws from the caller: kda_linear_attn_workspace_size(...) bytes, 256-byte aligned (NULL when 0).
+ */
+kda_status_t kda_linear_attn(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                             int64_t v_stride, const float *log_decay, const float *gate, float scale, void *out,
+                             const void *initial_state, void *final_state, kda_dtype_t state_dtype, const int32_t *lens,
+                             const int64_t *cu_seqlens, int N, int64_t T, int H, int Hkv, int D, kda_stream_t stream);
+kda_status_t kda_linear_attn_ws(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                int64_t v_stride, const float *log_decay, const float *gate, float scale, void *out,
+                                const void *initial_state, void *final_state, kda_dtype_t state_dtype,
+                                const int32_t *lens, const int64_t *cu_seqlens, int N, int64_t T, int H, int Hkv, int D,
+                                void *workspace, size_t workspace_bytes, kda_stream_t stream);
+/* Workspace bytes of a call of these sizes (varlen: whether cu_seqlens is given); 0 for invalid sizes. */
+size_t kda_linear_attn_workspace_size(int varlen, int N, int64_t T, int H, int D);
+
+/*
+ * kda_verify_drafts -- speculative decoding's verification: which of a request's drafted tokens the target model's
+ * distribution accepts, and the token after them.  Row i of a request's logits is the target's after i drafts,
+ *   p_i = softmax(logits_i / temperature);   draft x_i is accepted while  uniform_i q_i(x_i) < p_i(x_i).
+ * At the first row r whose draft is not accepted (the row after the last draft when all are) the token is
+ *   argmax_t w_t / noise_t  over w_t > 0, ties to the lowest t;   w = max(p_r - q_r, 0) where a draft was rejected,
+ * (p_r where nothing is left of that), and w = p_r behind the last draft.  With independent uniform_i from [0, 1) and noise_t
+ * from the exponential distribution the tokens are distributed as the target's own.  Without draft_probs the drafts are certain:
+ * q_i is 1 at x_i and 0 elsewhere.  Temperature 0: a draft is accepted where its logit is the row's largest, and the token
+ * is the lowest index of the largest.
+ *
+ *   logits         bf16 or fp32 [B, K + 1, V] as dtype says, rows row_stride elements apart (>= V); NaN counts as -INFINITY.
+ *   draft_tokens   int32 [B, K];   draft_probs  fp32 [B, K, V] or NULL.
+ *   uniform        fp32 [B, K];    noise  fp32 [B, V], > 0 (a token whose noise is not is not drawn, but for 0: it is first).
+ *   temperature    fp32 [B] or NULL (1), finite and >= 0 (else reported and taken as 0).
+ *   draft_lens     int32 [B] or NULL (K): drafts of each request; the rest of its rows is not read.
+ *   tokens         int32 [B, K + 1]: the accepted drafts, the token after them, then -1.
+ *   counts         int32 [B]: tokens written, 1 to K + 1 (what a linear attention's `lens` takes to advance its states).
+ *   0 <= K <= 31, V <= 2^24.  tokens and counts overlap nothing else.
+ * A row without a finite maximum accepts nothing and gives the token -1.  A draft outside [0, V) is rejected and reported.
+ * Probabilities are fp32.  kda_verify_drafts_ws takes a caller-owned workspace, 256-byte aligned.
+ */
+kda_status_t kda_verify_drafts(const void *logits, kda_dtype_t dtype, int64_t row_stride, const int32_t *draft_tokens,
+                               const float *draft_probs, const float *uniform, const float *noise,
+                               const float *temperature, const int32_t *draft_lens, int32_t *tokens, int32_t *counts, int B,
+                               int K, int V, kda_stream_t stream);
+kda_status_t kda_verify_drafts_ws(const void *logits, kda_dtype_t dtype, int64_t row_stride, const int32_t *draft_tokens,
+                                  const float *draft_probs, const float *uniform, const float *noise,
+                                  const float *temperature, const int32_t *draft_lens, int32_t *tokens, int32_t *counts,
+                                  int B, int K, int V, void *workspace, size_t workspace_bytes, kda_stream_t stream);
+/* Workspace bytes of a verification of these sizes; 0 for invalid sizes. */
+size_t kda_verify_drafts_workspace_size(kda_dtype_t dtype, int B, int K, int V);
+
 #ifdef __cplusplus
 }
 #endif
