@@ -19,11 +19,11 @@ BUILD_DIR = os.path.join(_PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libkda.so")
 UNITS = ["kda_api", "kda_prep", "kda_recur", "kda_recurrent", "kda_decode", "kda_host", "kda_noalloc", "kda_scan",
          "kda_step", "kda_append", "kda_attn", "kda_attn_tiles", "kda_attn_decode", "kda_beam", "kda_reorder",
-         "kda_linear", "kda_linear_tokens", "kda_verify"]
+         "kda_linear", "kda_linear_tokens", "kda_linear_chunks", "kda_verify"]
 SOURCES = [os.path.join(CSRC, u + ".cu") for u in UNITS]
 HEADERS = [os.path.join(INCLUDE, "kda.h"), os.path.join(CSRC, "kda_device.cuh"), os.path.join(CSRC, "kda_internal.h"),
            os.path.join(CSRC, "kda_plan.h"), os.path.join(CSRC, "kda_step.cuh"), os.path.join(CSRC, "kda_attn.cuh"),
-           os.path.join(CSRC, "kda_linear.cuh")]
+           os.path.join(CSRC, "kda_linear.cuh"), os.path.join(CSRC, "kda_tc.cuh")]
 BINDING_SOURCE = os.path.join(CSRC, "kda_binding.cpp")
 BINDING_PATH = os.path.join(BUILD_DIR, "kda_binding.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1,9 +1,50 @@
 // kda_linear_attn: checks of the arguments, and which kernel a call takes.
 #include "kda_linear.cuh"
 
+#include <algorithm>
 #include <cmath>
 
 namespace kda {
+
+// Sequences of up to this many tokens are evaluated token by token.
+constexpr int64_t TOKENS_MOST = 16;
+static bool token_by_token(int64_t T) { return T <= TOKENS_MOST; }
+
+// The cut of a call into groups (sizes only, so that the workspace is known beforehand), for 152 SMs.
+static LinearPlan make_plan(bool varlen, int N, int64_t T, int H)
+{
+    LinearPlan plan{};
+    const int64_t chunks = (T + 63) / 64, pairs = (int64_t)N * H;
+    int64_t cut = 1;
+    if (chunks >= 32 && pairs <= 76)
+        cut = std::min<int64_t>(std::max<int64_t>(152 / (varlen ? H : pairs), 1), chunks / 8);
+    plan.group_chunks = (chunks + cut - 1) / cut;
+    plan.groups = (int)((chunks + plan.group_chunks - 1) / std::max<int64_t>(plan.group_chunks, 1));
+    if (plan.groups <= 1) {
+        plan.groups = 1;
+        plan.group_chunks = std::max<int64_t>(chunks, 1);
+    }
+    if (varlen) {
+        // every sequence has one group at least, and the cuts of all are no more than one sequence's
+        plan.items = (N + (plan.groups > 1 ? T / (64 * plan.group_chunks) : 0)) * H;
+        plan.items_before = plan.groups > 1 ? T / (64 * plan.group_chunks) * H : 0;
+    } else {
+        plan.items = pairs * plan.groups;
+        plan.items_before = pairs * (plan.groups - 1);
+    }
+    return plan;
+}
+// Slots of groups' states (slot_of is below it).
+static int64_t plan_slots(const LinearPlan &plan, bool varlen, int N, int64_t T)
+{
+    if (plan.groups <= 1)
+        return 0;
+    return varlen ? T / (64 * plan.group_chunks) + N + 1 : (int64_t)N * plan.groups;
+}
+static size_t plan_bytes(const LinearPlan &plan, bool varlen, int N, int64_t T, int H, int D)
+{
+    return (size_t)plan_slots(plan, varlen, N, T) * H * ((size_t)D * D + 2) * sizeof(float);
+}
 
 static kda_status_t check_linear(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                                  int64_t v_stride, const float *log_decay, const float *gate, float scale, const void *out,
@@ -62,8 +103,10 @@ using namespace kda;
 
 extern "C" size_t kda_linear_attn_workspace_size(int varlen, int N, int64_t T, int H, int D)
 {
-    (void)varlen, (void)N, (void)T, (void)H, (void)D;
-    return 0;
+    if (N < 1 || T < 0 || H < 1 || (D != 64 && D != 128) || T > INT32_MAX || (varlen ? T : (int64_t)N * T) > INT32_MAX ||
+        (int64_t)N * H > INT32_MAX / 16 || token_by_token(T))
+        return 0;
+    return plan_bytes(make_plan(varlen != 0, N, T, H), varlen != 0, N, T, H, D);
 }
 
 extern "C" kda_status_t kda_linear_attn_ws(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -94,7 +137,14 @@ extern "C" kda_status_t kda_linear_attn_ws(const void *q, int64_t q_stride, cons
     if (step_error_word(&p.err) != cudaSuccess)
         return KDA_ERR_CUDA;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return launch_linear_tokens(p, state, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    if (token_by_token(T))
+        return launch_linear_tokens(p, state, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    LinearPlan plan = make_plan(cu_seqlens != nullptr, N, T, H);
+    plan.states = static_cast<float *>(workspace);
+    plan.decays = reinterpret_cast<float2 *>(plan.states + plan_slots(plan, cu_seqlens != nullptr, N, T) * H * D * D);
+    plan.state_type = state;
+    plan.wait_polls = wait_limit();
+    return launch_linear_chunks(p, plan, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 extern "C" kda_status_t kda_linear_attn(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,

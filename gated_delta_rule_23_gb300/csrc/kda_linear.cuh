@@ -52,6 +52,18 @@ __device__ __forceinline__ void linear_range(const LinearArgs &p, int n, int64_t
     }
 }
 
+// How a call runs in chunks: groups of group_chunks chunks of a sequence side by side (groups = 1: none are cut).
+struct LinearPlan {
+    int64_t group_chunks;
+    int groups;               // of a sequence; of the longest there can be with cu_seqlens
+    int64_t items, items_before;   // (sequence, group, head), and those whose state a later group starts from (upper bounds)
+    float *states;            // what groups add to the state, then the next group's start: [slots][H][dim][dim]  (workspace)
+    float2 *decays;           // their decays, as factor and kind: [slots][H]  (workspace)
+    kda_dtype_t state_type;
+    uint32_t wait_polls;
+};
+
+cudaError_t launch_linear_chunks(const LinearArgs &p, const LinearPlan &plan, cudaStream_t stream);
 cudaError_t launch_linear_tokens(const LinearArgs &p, kda_dtype_t state, cudaStream_t stream);
 
 }  // namespace kda

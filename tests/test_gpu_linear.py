@@ -207,9 +207,12 @@ def test_a_value_that_is_not_finite_reaches_no_earlier_token(bad, at, d):
     a["v"][0, at, 1, 5] = bad
     out, fin = call(a)
     column = torch.zeros_like(out, dtype=torch.bool)
-    column[0, at:, 1, 5] = True
+    column[0, :, 1, 5] = True
     assert torch.equal(out[~column], clean["out"][~column])
-    assert not bool(out[column].isfinite().any())
+    assert not bool(out[0, at:, 1, 5].isfinite().any())
+    # what of the column comes before it may be summed in another order: a bf16 step
+    before, was = out[0, :at, 1, 5].double(), clean["out"][0, :at, 1, 5].double()
+    assert bool(((before - was).abs() <= 2 * BF16 * was.abs() + 2.0 ** -13).all())
     row = torch.zeros_like(fin, dtype=torch.bool)
     row[0, 1, 5] = True
     assert torch.equal(fin[~row], clean["final_state"][~row]) and not bool(fin[row].isfinite().any())
