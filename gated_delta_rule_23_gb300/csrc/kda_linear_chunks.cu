@@ -2,8 +2,8 @@
 //
 // Within a chunk, with A_i the sum of the logarithms up to token i and S the state before the chunk (rows v, columns k):
 //   P = (Q K^T) . e^(A_i - A_j)  (j <= i),   O^T = V^T P^T + e^(A_i) S Q^T,   S <- e^(A_C) S + V^T (e^(A_C - A_j) K).
-// All decays are at most 1 by construction: they are exponentials of differences that are never positive, taken from sums in 64
-// bits, so a strong decay beside a weak one costs no precision and none is divided by.
+// All decays are at most 1 by construction: they are exponentials of differences that are never positive, taken from sums of two
+// terms, so a strong decay beside a weak one costs no precision and none is divided by.
 //
 // The features lie on tensor memory's lanes: O^T and S have a row per v, so that S is the operand of its product straight from tensor
 // memory (bf16, written by the threads that hold it) and leaves shared memory's bandwidth, the first bound of such a kernel, to
@@ -17,8 +17,9 @@
 // e^(A_C) S + L, so that nothing of a state that is forgotten stays behind as rounding.
 // K~ = e^(A_C - A_j) K is not a bf16 number: TERMS bf16 terms that add up to it are multiplied with V one after another.
 //
-// Warps: 0..3 O, scaled and stored; 4..7 K~ and P; 8..15 the state; 16 copies (tensor maps, a ring of three chunks); 17 issue;
-// 18 finds the chunks, and works their decays out ahead.  Every role walks one stream of chunks, whatever sequences and heads
+// Warps: 0 copies (tensor maps, a ring of chunks); 1 and 3 issue; 2 finds the chunks, and works their decays out ahead; 4..7 P;
+// 8..11 K~; 12..19 the state; 20..23 O, scaled and stored.  (The warps that all others wait for come first: an SM's schedulers are
+// busy most of the time, and as the last ones of the block they got what the others left.)  Every role walks one stream of chunks, whatever sequences and heads
 // these belong to, so the next sequence's first chunks are under way while the last one's state is stored.
 //
 // An item is a (sequence, head), or a group of its chunks where there are too few of those for the SMs: then a first launch works
@@ -36,24 +37,44 @@
 namespace kda {
 namespace {
 
-constexpr int THREADS = 608;
+constexpr int THREADS = 768;                 // six warpgroups
 constexpr int TMEM_COLS = 512;
 constexpr int TM_S1 = 0, TM_O1 = 128, TM_O2 = 192, TM_L = 256, TM_SB = 384;
-constexpr int STAGES = 3;
-constexpr int ENTRIES = 6;
+constexpr int ENTRIES = 8;
 constexpr int TILE_CB = 64 * 128;            // bytes of 64 tokens x 64 features
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int MAX_RANKED = 128;              // sequences of a ragged batch that are taken longest first
+
+// A sum of logarithms in base 2 as two terms, good to some 2^-45 of the largest partial sum, without 64-bit arithmetic (whose unit here
+// takes longer for a chunk's sums than all else does for the chunk).
+struct Sum {
+    float hi, lo;
+};
+__device__ __forceinline__ Sum add(const Sum &a, const Sum &b)
+{
+    const float s = a.hi + b.hi, x = s - a.hi;
+    const float lo = ((a.hi - (s - x)) + (b.hi - x)) + (a.lo + b.lo), hi = s + lo;
+    return Sum{hi, lo - (hi - s)};
+}
+__device__ __forceinline__ float minus(const Sum &a, const Sum &b) { return (a.hi - b.hi) + (a.lo - b.lo); }
+constexpr float LOG2E_LO = (float)(1.4426950408889634074 - (double)LOG2E);
+__device__ __forceinline__ Sum in_base_2(float a)
+{
+    const float hi = a * LOG2E;
+    return Sum{hi, fmaf(a, LOG2E, -hi) + a * LOG2E_LO};
+}
 
 // S <- e^a S + L.  weak: factor = e^a - 1, else e^a.
 struct Decay {
     float factor;
     int weak;
 };
-__device__ __forceinline__ Decay decay_of(float a)
+__device__ __forceinline__ Decay decay_of(const Sum &a)
 {
-    const bool weak = a > -0.5f;
-    return Decay{weak ? expm1f(a) : expf(a), weak};
+    constexpr float LN2 = 0.6931471805599453f, LN2_LO = (float)(0.69314718055994530942 - (double)LN2);
+    const float x = fmaf(a.hi, LN2, fmaf(a.hi, LN2_LO, a.lo * LN2));
+    const bool weak = x > -0.5f;
+    return Decay{weak ? expm1f(x) : expf(x), weak};
 }
 __device__ __forceinline__ float decayed(const Decay &d, float s, float l)
 {
@@ -62,9 +83,10 @@ __device__ __forceinline__ float decayed(const Decay &d, float s, float l)
 }
 
 struct alignas(16) Entry {    // one chunk; the tables are read four floats at a time
-    float2 logs[64];          // A_i in base 2, as two terms
+    float hi[64], lo[64];     // A_i in base 2, as two terms
+    float up[32];             // e^(A_31 - A_j)
     float ea[64];             // scale e^(A_i)
-    float kf[64];             // e^(A_C - A_j), 0 past the end
+    uint2 kf[64];             // e^(A_C - A_j) as two bf16 terms, each twice
     int64_t at_src, at_dst;   // index of the state before and after the chunk's item
     int src, dst;             // and where that is: 0 zeros / nowhere, 1 the call's, 2 a group's
     Decay decay;              // of the whole chunk
@@ -72,18 +94,20 @@ struct alignas(16) Entry {    // one chunk; the tables are read four floats at a
     int first, last;          // of its item
     int tok0, len, h;         // first token, tokens, head
 };
-static_assert(sizeof(Entry) % 16 == 0 && offsetof(Entry, ea) % 16 == 0 && offsetof(Entry, kf) % 16 == 0, "vector reads");
+static_assert(sizeof(Entry) % 16 == 0 && offsetof(Entry, lo) % 16 == 0 && offsetof(Entry, up) % 16 == 0 && offsetof(Entry, ea) % 16 == 0, "vector reads");
 
 template <int DIM, int TERMS> struct Shape {
     static constexpr int CB = DIM / 64;
     static constexpr int TILE = CB * TILE_CB;
-    static constexpr int STAGE = 3 * TILE;                    // V, Q, K
-    static constexpr int KT = STAGES * STAGE;                 // K~: TERMS tiles
-    static constexpr int P = KT + TERMS * TILE;               // two of [64 i][64 j]
-    static constexpr int ZERO = P + 2 * TILE_CB;              // D = 64: lanes 64 to 127
+    static constexpr int STAGE = 3 * TILE;                    // V, Q, K (later K~'s first term)
+    static constexpr int STAGES = DIM == 64 ? 6 : 3;
+    static constexpr int KT = STAGES * STAGE;                 // K~'s other terms, of two chunks
+    static constexpr int P = KT + 2 * (TERMS - 1) * TILE;     // two of [64 i][64 j]
+    static constexpr int OUT = P + 2 * TILE_CB;               // O on its way out
+    static constexpr int ZERO = OUT + TILE;                   // D = 64: lanes 64 to 127
     static constexpr int ENTRY = ZERO + (DIM == 64 ? TILE_CB : 0);
     static constexpr int BAR = ENTRY + ENTRIES * (int)sizeof(Entry);
-    static constexpr int SMEM = 1024 + BAR + 320;
+    static constexpr int SMEM = 1024 + BAR + 384;
     static_assert(SMEM <= 232448, "a CTA's shared memory");
     static_assert(ENTRY % 16 == 0 && BAR % 8 == 0 && P % 1024 == 0 && KT % 1024 == 0 && ZERO % 1024 == 0, "alignment");
 };
@@ -156,7 +180,7 @@ __device__ __forceinline__ int64_t slot_of(const LinearArgs &p, const LinearPlan
 }
 
 // A row of 64-bit halves of the state in registers: COLS columns from `at` on
-template <int COLS> __device__ __forceinline__ void load_state(const void *p, kda_dtype_t type, int64_t at, float (&s)[COLS])
+template <int COLS> __device__ __forceinline__ void load_state(const void *p, kda_dtype_t type, int64_t at, f2 (&s)[COLS / 2])
 {
     if (type == KDA_DTYPE_BF16) {
         const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + at);
@@ -166,14 +190,14 @@ template <int COLS> __device__ __forceinline__ void load_state(const void *p, kd
             const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int e = 0; e < 4; e++)
-                s[8 * i + 2 * e] = bf16_lo(w[e]), s[8 * i + 2 * e + 1] = bf16_hi(w[e]);
+                s[4 * i + e] = f2_bf16x2(w[e]);
         }
     } else {
         const float4 *x = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
 #pragma unroll
         for (int i = 0; i < COLS / 4; i++) {
             const float4 y = x[i];
-            s[4 * i] = y.x, s[4 * i + 1] = y.y, s[4 * i + 2] = y.z, s[4 * i + 3] = y.w;
+            s[2 * i] = f2_pack(y.x, y.y), s[2 * i + 1] = f2_pack(y.z, y.w);
         }
     }
 }
@@ -182,19 +206,19 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&y);
 }
-template <int COLS> __device__ __forceinline__ void store_state(void *p, kda_dtype_t type, int64_t at, const float (&s)[COLS])
+template <int COLS> __device__ __forceinline__ void store_state(void *p, kda_dtype_t type, int64_t at, const f2 (&s)[COLS / 2])
 {
     if (type == KDA_DTYPE_BF16) {
         uint4 *x = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p) + at);
 #pragma unroll
         for (int i = 0; i < COLS / 8; i++)
-            x[i] = make_uint4(pack_bf16(s[8 * i], s[8 * i + 1]), pack_bf16(s[8 * i + 2], s[8 * i + 3]),
-                              pack_bf16(s[8 * i + 4], s[8 * i + 5]), pack_bf16(s[8 * i + 6], s[8 * i + 7]));
+            x[i] = make_uint4(pack_bf16(f2_lo(s[4 * i]), f2_hi(s[4 * i])), pack_bf16(f2_lo(s[4 * i + 1]), f2_hi(s[4 * i + 1])),
+                              pack_bf16(f2_lo(s[4 * i + 2]), f2_hi(s[4 * i + 2])), pack_bf16(f2_lo(s[4 * i + 3]), f2_hi(s[4 * i + 3])));
     } else {
         float4 *x = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
 #pragma unroll
         for (int i = 0; i < COLS / 4; i++)
-            x[i] = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+            x[i] = make_float4(f2_lo(s[2 * i]), f2_hi(s[2 * i]), f2_lo(s[2 * i + 1]), f2_hi(s[2 * i + 1]));
     }
 }
 __device__ __forceinline__ void tmem_put16(uint32_t addr, const uint32_t *u)
@@ -211,13 +235,85 @@ __device__ __forceinline__ float tmem_read1(uint32_t addr)
     return x;
 }
 
+__device__ __forceinline__ void tmem_read16(uint32_t addr, float (&s)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+                 " tcgen05.wait::ld.sync.aligned;"
+                 : "=&f"(s[0]), "=&f"(s[1]), "=&f"(s[2]), "=&f"(s[3]), "=&f"(s[4]), "=&f"(s[5]), "=&f"(s[6]), "=&f"(s[7]),
+                   "=&f"(s[8]), "=&f"(s[9]), "=&f"(s[10]), "=&f"(s[11]), "=&f"(s[12]), "=&f"(s[13]), "=&f"(s[14]), "=&f"(s[15])
+                 : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap *map, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z) : "memory");
+}
+// Pairs of bf16, each result rounded once
+__device__ __forceinline__ uint32_t bf16_mul(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t bf16_fma(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+// A factor as two bf16 terms, each in both halves of a word
+__device__ __forceinline__ uint2 two_terms(float f)
+{
+    const uint32_t a = pack_bf16(f, f);
+    const float rest = f - bf16_lo(a);
+    return make_uint2(a, pack_bf16(rest, rest));
+}
+// 16 lanes by 16 columns, laid out for stmatrix: thread t has columns 2 (t % 4) and the next of row t / 4, then of row t / 4 + 8,
+// then the same of the next 8 columns.  Two of them at once.
+__device__ __forceinline__ void tmem_read_pieces(uint32_t at, float (&s)[8], uint32_t bt, float (&t)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n"
+                 " tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n"
+                 " tcgen05.wait::ld.sync.aligned;"
+                 : "=&f"(s[0]), "=&f"(s[1]), "=&f"(s[2]), "=&f"(s[3]), "=&f"(s[4]), "=&f"(s[5]), "=&f"(s[6]), "=&f"(s[7]),
+                   "=&f"(t[0]), "=&f"(t[1]), "=&f"(t[2]), "=&f"(t[3]), "=&f"(t[4]), "=&f"(t[5]), "=&f"(t[6]), "=&f"(t[7])
+                 : "r"(at), "r"(bt) : "memory");
+}
+__device__ __forceinline__ void stmatrix_x4_t(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(map), "r"(src), "r"(x), "r"(y), "r"(z) : "memory");
+}
+// The warps that take O out, among themselves
+template <int N> __device__ __forceinline__ void out_sync() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }
+// Tokens 2 q and 2 q + 1 of a pair, as the halves of a word: those at or before the row's (gap = the row's token - 2 q)
+__device__ __forceinline__ uint32_t seen_pair(int gap)
+{
+    uint32_t x;
+    asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(x) : "r"(max(16 * (gap + 1), 0)));
+    return x;
+}
+// Registers of a warpgroup's threads from here on.  The kernel starts with 80 a thread, and the six shares add up to six times that.
+constexpr int REGS_O = 88, REGS_K = 64, REGS_S = 104, REGS_P = 64, REGS_X = 56;
+static_assert(REGS_O + REGS_K + 2 * REGS_S + REGS_P + REGS_X <= 6 * 80, "more than the block was launched with");
+template <int N, bool MORE> __device__ __forceinline__ void set_registers()
+{
+    if (MORE)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <int DIM, int TERMS, bool STATES_ONLY>
 __global__ void __launch_bounds__(THREADS, 1)
 kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan plan, const __grid_constant__ CUtensorMap qmap,
-                         const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
+                         const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap)
 {
     using S = Shape<DIM, TERMS>;
-    constexpr int CB = S::CB;
+    constexpr int CB = S::CB, STAGES = S::STAGES;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char *const smem = smem_raw + (base - smem_u32(smem_raw));
@@ -225,8 +321,8 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
     const uint32_t bar = base + S::BAR;
     const uint32_t b_full = bar, b_empty = b_full + 8 * STAGES, b_ent = b_empty + 8 * STAGES, b_ent_free = b_ent + 8 * ENTRIES,
                    b_s = b_ent_free + 8 * ENTRIES, b_p = b_s + 16, b_o = b_p + 16, b_sb = b_o + 16, b_pe = b_sb + 16,
-                   b_k = b_pe + 16, b_l = b_k + 8, b_l_free = b_l + 8, b_o_free = b_l_free + 8, b_block = b_o_free + 8, b_drain = b_block + 8;
-    static_assert(8 * (2 * STAGES + 2 * ENTRIES + 16) <= 320, "barriers");
+                   b_k = b_pe + 16, b_l = b_k + 16, b_l_free = b_l + 16, b_o_free = b_l_free + 8, b_block = b_o_free + 8, b_drain = b_block + 8;
+    static_assert(8 * (2 * STAGES + 2 * ENTRIES + 19) <= 384, "barriers");
     __shared__ uint32_t tmem_slot;
     __shared__ uint4 block_answer;
     __shared__ short order[MAX_RANKED];
@@ -234,28 +330,28 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
     if (tid == 0) {
         for (int i = 0; i < STAGES; i++) {
             mbar_init(b_full + 8 * i, 1);
-            mbar_init(b_empty + 8 * i, STATES_ONLY ? 1 : 5);   // products, and the epilogue's warps
+            mbar_init(b_empty + 8 * i, 1);
         }
         for (int i = 0; i < ENTRIES; i++) {
             mbar_init(b_ent + 8 * i, 1);
-            mbar_init(b_ent_free + 8 * i, 18);                 // every warp but the one that writes
+            mbar_init(b_ent_free + 8 * i, 23);                 // every warp but the one that writes
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(b_s + 8 * i, 1);
             mbar_init(b_p + 8 * i, 2);
             mbar_init(b_o + 8 * i, 1);
+            mbar_init(b_drain + 8 * i, 1);
             mbar_init(b_sb + 8 * i, 8);
             mbar_init(b_pe + 8 * i, 4);
+            mbar_init(b_k + 8 * i, 4);
+            mbar_init(b_l + 8 * i, 1);
         }
-        mbar_init(b_k, 4);
-        mbar_init(b_l, 1);
         mbar_init(b_l_free, 8);
         mbar_init(b_o_free, 4);
         mbar_init(b_block, 1);
-        mbar_init(b_drain, 1);
         mbar_fence_init();
     }
-    if (warp == 17) {
+    if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
                      "r"(TMEM_COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -288,238 +384,8 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
     };
 
     if (warp < 4) {
-        // ------------------------------------------------------------ O
-        const uint32_t quad = (uint32_t)warp << 21;
-        const int v = warp * 32 + lane;
-        for (uint32_t c = 0; next(c); c++) {
-            const Entry &e = entries[c % ENTRIES];
-            if (!STATES_ONLY) {
-                if (!wait(b_o + 8 * (c & 1), c >> 1))
-                    break;
-                tc_fence_after();
-                const int len = e.len;
-                __nv_bfloat16 *out = p.out + ((int64_t)e.tok0 * p.H + e.h) * DIM;
-                const int64_t row = (int64_t)p.H * DIM;
-                if (warp * 32 < DIM) {
-                    uint32_t w[32];                            // pairs of tokens
-                    f2 z = 0;                                  // stays 0 while the row of V^T P^T is finite
-#pragma unroll
-                    for (int half = 0; half < 2; half++) {
-                        float x[32], y[32];
-                        tmem_read32(tmem + TM_O1 + quad + 32 * half, x);
-                        tmem_read32(tmem + TM_O2 + quad + 32 * half, y);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            const float4 f = *reinterpret_cast<const float4 *>(&e.ea[32 * half + i]);
-                            z = f2_fma(f2_pack(x[i], x[i + 1]), 0, z);
-                            z = f2_fma(f2_pack(x[i + 2], x[i + 3]), 0, z);
-                            w[16 * half + i / 2] = pack_bf16(fmaf(f.x, y[i], p.scale * x[i]), fmaf(f.y, y[i + 1], p.scale * x[i + 1]));
-                            w[16 * half + i / 2 + 1] = pack_bf16(fmaf(f.z, y[i + 2], p.scale * x[i + 2]), fmaf(f.w, y[i + 3], p.scale * x[i + 3]));
-                        }
-                    }
-                    const bool odd = !(f2_lo(z) + f2_hi(z) == 0.0f);
-                    if (!__any_sync(FULL, odd)) {
-                        tc_fence_before();
-                        arrive(b_o_free);
-                        // neighbouring lanes swap halves of a pair of tokens: each stores one token's pair of features
-                        __nv_bfloat16 *to = out + (v & ~1) + (lane & 1) * row;
-                        const uint32_t pick = lane & 1 ? 0x3276 : 0x5410;
-#pragma unroll
-                        for (int i = 0; i < 32; i++) {
-                            const uint32_t y = __shfl_xor_sync(FULL, w[i], 1);
-                            if (2 * i + (lane & 1) < len)
-                                *reinterpret_cast<uint32_t *>(to + 2 * i * row) = __byte_perm(w[i], y, pick);
-                        }
-                    } else {
-                        // (both are through; waited for here so that this thread sees what they brought)
-                        if (!wait(b_full + 8 * (c % STAGES), c / STAGES) || !wait(b_p + 8 * (c & 1), c >> 1))
-                            break;
-                        const unsigned char *pt = smem + S::P + (c & 1) * TILE_CB;
-                        const unsigned char *vt = smem + (c % STAGES) * S::STAGE + (v / 64) * TILE_CB;
-                        for (int i = 0; i < len; i++) {
-                            float x = tmem_read1(tmem + TM_O1 + quad + i);
-                            const float y = tmem_read1(tmem + TM_O2 + quad + i);
-                            if (odd) {
-                                x = 0.0f;
-                                for (int j = 0; j <= i; j++) {
-                                    const __nv_bfloat16 a = *reinterpret_cast<const __nv_bfloat16 *>(
-                                        pt + i * 128 + (((j / 8) ^ (i & 7)) << 4) + (j % 8) * 2);
-                                    const __nv_bfloat16 b = *reinterpret_cast<const __nv_bfloat16 *>(
-                                        vt + j * 128 + (((v % 64 / 8) ^ (j & 7)) << 4) + (v % 8) * 2);
-                                    x = fmaf(__bfloat162float(a), __bfloat162float(b), x);
-                                }
-                            }
-                            out[i * row + v] = __float2bfloat16_rn(fmaf(e.ea[i], y, p.scale * x));
-                        }
-                        tc_fence_before();
-                        arrive(b_o_free);
-                    }
-                } else {
-                    arrive(b_o_free);
-                }
-                arrive(b_pe + 8 * (c & 1));
-                if (lane == 0)
-                    mbar_arrive(b_empty + 8 * (c % STAGES));
-            }
-            arrive(b_ent_free + 8 * (c % ENTRIES));
-        }
-    } else if (warp < 8) {
-        // ------------------------------------------------------------ K~, P
-        const int wp = warp - 4, t = tid - 128;
-        for (uint32_t c = 0; next(c); c++) {
-            const Entry &e = entries[c % ENTRIES];
-            const int st = c % STAGES, len = e.len;
-            if (!wait(b_full + 8 * st, c / STAGES) || (c > 0 && !wait(b_l, c - 1)))
-                break;
-            const unsigned char *kt = smem + st * S::STAGE + 2 * S::TILE;
-            constexpr int VECS = 64 * DIM / 8 / 128;           // 16-byte vectors of a thread
-#pragma unroll
-            for (int m = 0; m < VECS; m++) {
-                const int i = t + 128 * m, j = i / (DIM / 8), ch = i % (DIM / 8);
-                const int at = (ch / 8) * TILE_CB + j * 128 + (((ch % 8) ^ (j & 7)) << 4);
-                const uint4 x = *reinterpret_cast<const uint4 *>(kt + at);
-                const float f = e.kf[j];
-                const bool live = j < len;
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                uint32_t y[TERMS][4];
-#pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    float a = live ? bf16_lo(w[q]) * f : 0.0f, b = live ? bf16_hi(w[q]) * f : 0.0f;
-#pragma unroll
-                    for (int r = 0; r < TERMS; r++) {
-                        y[r][q] = pack_bf16(a, b);
-                        a -= bf16_lo(y[r][q]), b -= bf16_hi(y[r][q]);
-                    }
-                }
-#pragma unroll
-                for (int r = 0; r < TERMS; r++)
-                    *reinterpret_cast<uint4 *>(smem + S::KT + r * S::TILE + at) = make_uint4(y[r][0], y[r][1], y[r][2], y[r][3]);
-            }
-            if (len < 64) {                                    // what lies behind the sequence is cleared from V
-                unsigned char *vt = smem + st * S::STAGE;
-                for (int i = t; i < (64 - len) * 8 * CB; i += 128)
-                    *reinterpret_cast<uint4 *>(vt + i / ((64 - len) * 8) * TILE_CB + len * 128 + i % ((64 - len) * 8) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_async_smem();
-            arrive(b_k);
-            if (!STATES_ONLY && (wp >> 1) == (int)(c & 1)) {
-                if (!wait(b_s + 8 * (c & 1), c >> 1) || (c >= 2 && !wait(b_pe + 8 * (c & 1), (c >> 1) - 1)))
-                    break;
-                tc_fence_after();
-                const int i = (wp & 1) * 32 + lane;            // token of the row
-                unsigned char *pt = smem + S::P + (c & 1) * TILE_CB + i * 128;
-                const float2 mine = e.logs[i];
-#pragma unroll
-                for (int half = 0; half < 2; half++) {
-                    uint32_t y[16];
-                    if (half > (wp & 1)) {                     // later tokens only
-#pragma unroll
-                        for (int q = 0; q < 16; q++)
-                            y[q] = 0;
-                    } else {
-                        float s[32];
-                        tmem_read32(tmem + TM_S1 + 64 * (c & 1) + ((uint32_t)wp << 21) + 32 * half, s);
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            const float4 l = *reinterpret_cast<const float4 *>(&e.logs[32 * half + j]);
-                            const float a = s[j] * ex2_approx((mine.x - l.x) + (mine.y - l.y));
-                            const float b = s[j + 1] * ex2_approx((mine.x - l.z) + (mine.y - l.w));
-                            // bf16, V's type, as the product takes it
-                            y[j / 2] = pack_bf16(32 * half + j <= i ? a : 0.0f, 32 * half + j + 1 <= i ? b : 0.0f);
-                        }
-                    }
-#pragma unroll
-                    for (int q = 0; q < 4; q++)
-                        *reinterpret_cast<uint4 *>(pt + (((4 * half + q) ^ (i & 7)) << 4)) =
-                            make_uint4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
-                }
-                tc_fence_before();
-                fence_async_smem();
-                arrive(b_p + 8 * (c & 1));
-            }
-            arrive(b_ent_free + 8 * (c % ENTRIES));
-        }
-    } else if (warp < 16) {
-        // ------------------------------------------------------------ the state
-        constexpr int COLS = DIM / 2;
-        const int half = (warp - 8) / 4, v = (warp & 3) * 32 + lane;
-        const uint32_t quad = (uint32_t)(warp & 3) << 21;
-        const bool mine = (warp & 3) * 32 < DIM;
-        const uint32_t tm_l = tmem + TM_L + quad + half * COLS, tm_sb = tmem + TM_SB + quad + half * (COLS / 2);
-        float s[COLS];
-#pragma unroll
-        for (int i = 0; i < COLS; i++)
-            s[i] = 0.0f;
-        // S before chunk c, as the operand of its product
-        auto put = [&](uint32_t c) -> bool {
-            if (STATES_ONLY)
-                return true;
-            if (c >= 2 && !wait(b_o + 8 * (c & 1), (c >> 1) - 1))
-                return false;
-            if (mine) {
-                tc_fence_after();
-                uint32_t u[COLS / 2];
-#pragma unroll
-                for (int i = 0; i < COLS; i += 2)
-                    u[i / 2] = pack_bf16(s[i], s[i + 1]);
-                if constexpr (COLS == 64)
-                    tmem_put32(tm_sb + 64 * (c & 1), u);
-                else
-                    tmem_put16(tm_sb + 64 * (c & 1), u);
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                tc_fence_before();
-            }
-            arrive(b_sb + 8 * (c & 1));
-            return true;
-        };
-        for (uint32_t c = 0; next(c); c++) {
-            const Entry &e = entries[c % ENTRIES];
-            if (e.first) {
-                if (mine && e.src)
-                    load_state<COLS>(e.src == 1 ? p.init : plan.states, e.src == 1 ? plan.state_type : KDA_DTYPE_FP32,
-                                     (e.at_src * DIM + v) * DIM + half * COLS, s);
-                else
-#pragma unroll
-                    for (int i = 0; i < COLS; i++)
-                        s[i] = 0.0f;
-                if (!put(c))
-                    break;
-            }
-            if (!wait(b_l, c))
-                break;
-            if (mine) {
-                tc_fence_after();
-                const Decay d = e.decay;
-#pragma unroll
-                for (int i = 0; i < COLS; i += 32) {
-                    float l[32];
-                    tmem_read32(tm_l + i, l);
-#pragma unroll
-                    for (int j = 0; j < 32; j++)
-                        l[j] = fmaf(d.factor, s[i + j], l[j]);
-                    if (d.weak) {
-#pragma unroll
-                        for (int j = 0; j < 32; j++)
-                            s[i + j] += l[j];
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; j++)
-                            s[i + j] = l[j];
-                    }
-                }
-                tc_fence_before();
-            }
-            arrive(b_l_free);
-            if (!e.last) {
-                if (!put(c + 1))
-                    break;
-            } else if (mine && e.dst) {
-                store_state<COLS>(e.dst == 1 ? p.fin : plan.states, e.dst == 1 ? plan.state_type : KDA_DTYPE_FP32,
-                                  (e.at_dst * DIM + v) * DIM + half * COLS, s);
-            }
-            arrive(b_ent_free + 8 * (c % ENTRIES));
-        }
-    } else if (warp == 16) {
+      set_registers<REGS_X, false>();
+      if (warp == 0) {
         // ------------------------------------------------------------ copies
         uint32_t c = 0;
         for (; next(c); c++) {
@@ -543,107 +409,106 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
         // no copy is in flight when the CTA leaves, also where the work was given up
         for (uint32_t i = c < STAGES ? 0 : c - STAGES; i < c; i++)
             timeout |= !mbar_wait(b_full + 8 * (i % STAGES), (i / STAGES) & 1);
-    } else if (warp == 17) {
+      } else if (warp == 1 || warp == 3) {
         // ------------------------------------------------------------ tensor-core issue
-        // The whole warp waits, one elected lane issues from uniform registers.
-        const uint32_t id_s = idesc_bf16(128, 64, false), id_o1 = idesc_bf16(128, 64, false) | A_MN,
-                       id_l = idesc_bf16(128, DIM, true) | A_MN, id_o2 = idesc_bf16(128, 64, false);
+        // Warp 1 the scores, as soon as a chunk's tiles are there; warp 3 the products that wait for other warps' work.  The whole
+        // warp waits, one elected lane issues from uniform registers.
         const uint32_t tm = __shfl_sync(FULL, tmem, 0), lead = elect_one();
-        auto scores = [&](uint32_t c) {                        // Q K^T of chunk c
-            const uint32_t at = base + (c % STAGES) * S::STAGE;
-            const uint32_t a = desc_lo(at + S::TILE - (c & 1) * TILE_CB, 16), b = desc_lo(at + 2 * S::TILE, 16), d = tm + TM_S1 + 64 * (c & 1);
-            if (lead && !timeout) {
-#pragma unroll
-                for (int k = 0; k < DIM / 16; k++) {
-                    const uint32_t step = ((k / 4) * TILE_CB + (k % 4) * 32) >> 4;
-                    if (k == 0)
-                        mma_ss<false>(d, a, b, id_s, 0);
-                    else
-                        mma_ss<true>(d, a + step, b + step, id_s, 1);
-                }
-                umma_commit(b_s + 8 * (c & 1));
-            }
-            __syncwarp();
-        };
-        bool more = next(0);
-        if (more && !STATES_ONLY && wait(b_full, 0)) {
-            tc_fence_after();
-            scores(0);
-        }
-        for (uint32_t c = 0; more; c++) {
-            const int st = c % STAGES;
-            const uint32_t at = base + st * S::STAGE;
-            // V as M rows: blocks of 64 features, for D = 64 the second one zeros
-            const uint32_t v = desc_lo(at, DIM == 128 ? TILE_CB : S::ZERO - st * S::STAGE);
-            if (!wait(b_k, c) || (c > 0 && !wait(b_l_free, c - 1)))
-                break;
-            tc_fence_after();
-            if (lead && !timeout) {
-#pragma unroll
-                for (int r = TERMS - 1; r >= 0; r--) {         // small terms first
-                    const uint32_t b = desc_lo(base + S::KT + r * S::TILE, TILE_CB);
-#pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        if (r == TERMS - 1 && k == 0)
-                            mma_ss<false>(tm + TM_L, v, b, id_l, 0);
-                        else
-                            mma_ss<true>(tm + TM_L, v + k * (2048 >> 4), b + k * (2048 >> 4), id_l, 1);
-                    }
-                }
-                umma_commit(b_l);
-                if (STATES_ONLY)
-                    umma_commit(b_empty + 8 * st);
-            }
-            __syncwarp();
-            more = next(c + 1);
-            if (!STATES_ONLY) {
-                if (!wait(b_sb + 8 * (c & 1), c >> 1) || (c > 0 && !wait(b_o_free, c - 1)))
-                    break;
-                tc_fence_after();
-                const uint32_t q = desc_lo(at + S::TILE, 16), sb = tm + TM_SB + 64 * (c & 1);
-                if (lead && !timeout) {
-#pragma unroll
-                    for (int k = 0; k < DIM / 16; k++) {
-                        const uint32_t step = ((k / 4) * TILE_CB + (k % 4) * 32) >> 4;
-                        if (k == 0)
-                            mma_ts<false>(tm + TM_O2, sb, q, id_o2, 0);
-                        else
-                            mma_ts<true>(tm + TM_O2, sb + 8 * k, q + step, id_o2, 1);
-                    }
-                }
-                __syncwarp();
-                if (more) {
-                    if (!wait(b_full + 8 * ((c + 1) % STAGES), (c + 1) / STAGES))
+        if (warp == 1) {
+            const uint32_t id_s = idesc_bf16(128, 64, false);
+            for (uint32_t c = 0; next(c); c++) {
+                const uint32_t at = base + (c % STAGES) * S::STAGE;
+                if (!STATES_ONLY) {
+                    // where they go, P of the chunk before the last has been formed from
+                    if (!wait(b_full + 8 * (c % STAGES), c / STAGES) || (c >= 2 && !wait(b_p + 8 * (c & 1), (c >> 1) - 1)))
                         break;
                     tc_fence_after();
-                    scores(c + 1);
+                    const uint32_t a = desc_lo(at + S::TILE - (c & 1) * TILE_CB, 16), b = desc_lo(at + 2 * S::TILE, 16), d = tm + TM_S1 + 64 * (c & 1);
+                    if (lead && !timeout) {
+#pragma unroll
+                        for (int k = 0; k < DIM / 16; k++) {
+                            const uint32_t step = ((k / 4) * TILE_CB + (k % 4) * 32) >> 4;
+                            if (k == 0)
+                                mma_ss<false>(d, a, b, id_s, 0);
+                            else
+                                mma_ss<true>(d, a + step, b + step, id_s, 1);
+                        }
+                        umma_commit(b_s + 8 * (c & 1));
+                    }
                 }
-                if (!wait(b_p + 8 * (c & 1), c >> 1))
+                arrive(b_ent_free + 8 * (c % ENTRIES));
+            }
+        } else {
+            const uint32_t id_l = idesc_bf16(128, DIM, true) | A_MN, id_o2 = idesc_bf16(128, 64, false), id_o1 = id_o2 | A_MN;
+            for (uint32_t c = 0; next(c); c++) {
+                const int st = c % STAGES;
+                const uint32_t at = base + st * S::STAGE;
+                // V as M rows: blocks of 64 features, for D = 64 the second one zeros
+                const uint32_t v = desc_lo(at, DIM == 128 ? TILE_CB : S::ZERO - st * S::STAGE);
+                if (!wait(b_full + 8 * st, c / STAGES) || !wait(b_k + 8 * (c & 1), c >> 1) || (c > 0 && !wait(b_l_free, c - 1)))
                     break;
                 tc_fence_after();
-                const uint32_t pd = desc_lo(base + S::P + (c & 1) * TILE_CB, 16);
                 if (lead && !timeout) {
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        if (k == 0)
-                            mma_ss<false>(tm + TM_O1, v, pd, id_o1, 0);
-                        else
-                            mma_ss<true>(tm + TM_O1, v + k * (2048 >> 4), pd + k * (32 >> 4), id_o1, 1);
+                    for (int r = TERMS - 1; r >= 0; r--) {     // small terms first
+                        const uint32_t b = desc_lo(r == 0 ? at + 2 * S::TILE : base + S::KT + ((c & 1) * (TERMS - 1) + r - 1) * S::TILE, TILE_CB);
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            if (r == TERMS - 1 && k == 0)
+                                mma_ss<false>(tm + TM_L, v, b, id_l, 0);
+                            else
+                                mma_ss<true>(tm + TM_L, v + k * (2048 >> 4), b + k * (2048 >> 4), id_l, 1);
+                        }
                     }
-                    umma_commit(b_o + 8 * (c & 1));
-                    umma_commit(b_empty + 8 * st);
+                    umma_commit(b_l + 8 * (c & 1));
+                    if (STATES_ONLY)
+                        umma_commit(b_empty + 8 * st);
                 }
                 __syncwarp();
+                if (!STATES_ONLY) {
+                    if (!wait(b_sb + 8 * (c & 1), c >> 1) || (c > 0 && !wait(b_o_free, c - 1)))
+                        break;
+                    tc_fence_after();
+                    const uint32_t q = desc_lo(at + S::TILE, 16), sb = tm + TM_SB + 64 * (c & 1);
+                    if (lead && !timeout) {
+#pragma unroll
+                        for (int k = 0; k < DIM / 16; k++) {
+                            const uint32_t step = ((k / 4) * TILE_CB + (k % 4) * 32) >> 4;
+                            if (k == 0)
+                                mma_ts<false>(tm + TM_O2, sb, q, id_o2, 0);
+                            else
+                                mma_ts<true>(tm + TM_O2, sb + 8 * k, q + step, id_o2, 1);
+                        }
+                    }
+                    __syncwarp();
+                    if (!wait(b_p + 8 * (c & 1), c >> 1))
+                        break;
+                    tc_fence_after();
+                    const uint32_t pd = desc_lo(base + S::P + (c & 1) * TILE_CB, 16);
+                    if (lead && !timeout) {
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            if (k == 0)
+                                mma_ss<false>(tm + TM_O1, v, pd, id_o1, 0);
+                            else
+                                mma_ss<true>(tm + TM_O1, v + k * (2048 >> 4), pd + k * (32 >> 4), id_o1, 1);
+                        }
+                        umma_commit(b_o + 8 * (c & 1));
+                        umma_commit(b_empty + 8 * st);
+                    }
+                    __syncwarp();
+                }
+                arrive(b_ent_free + 8 * (c % ENTRIES));
             }
-            arrive(b_ent_free + 8 * (c % ENTRIES));
         }
         if (lead) {
             // everything issued has to be through before tensor memory is freed
-            umma_commit(b_drain);
-            timeout |= !mbar_wait(b_drain, 0);
+            const uint32_t b = b_drain + (warp == 3 ? 8 : 0);
+            umma_commit(b);
+            timeout |= !mbar_wait(b, 0);
         }
         __syncwarp();
-    } else {
+      } else {
         // ------------------------------------------------------------ chunks and their decays
         const short *ranked = nullptr;
         if (p.tok.cu && p.tok.N <= MAX_RANKED) {
@@ -678,74 +543,412 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
             __syncwarp();
             return y;
         };
-        auto slot_free = [&]() -> bool { return c < ENTRIES || wait(b_ent_free + 8 * (c % ENTRIES), c / ENTRIES - 1); };
+        auto slot_free = [&](uint32_t c) -> bool { return c < ENTRIES || wait(b_ent_free + 8 * (c % ENTRIES), c / ENTRIES - 1); };
         for (int x = blockIdx.x; x >= 0 && !timeout; x = next_block()) {
             Item w;
             if (!find_item<STATES_ONLY>(p, plan, ranked, x, w, bad))
                 continue;
             const int64_t chunks = (w.len + 63) / 64, c0 = (int64_t)w.g * plan.group_chunks;
             const int64_t c1 = c0 + plan.group_chunks < chunks ? c0 + plan.group_chunks : chunks;
+            const int src = w.g > 0 && !STATES_ONLY ? 2 : (!STATES_ONLY && p.init ? 1 : 0);
+            const int dst = STATES_ONLY ? 2 : (c1 == chunks && p.fin ? 1 : 0);
+            const int64_t pair = (int64_t)w.n * p.H + w.h;
+            const int64_t at_src = src == 2 ? slot_of(p, plan, w.n, w.bos, w.g - 1) * p.H + w.h : pair;
+            const int64_t at_dst = STATES_ONLY ? slot_of(p, plan, w.n, w.bos, w.g) * p.H + w.h : pair;
             const float fixed = p.log_decay ? p.log_decay[w.h] : 0.0f;
             auto gate = [&](int64_t i) -> float { return i < w.len ? log_decay_of(p, w.bos + i, w.h, fixed, bad) : 0.0f; };
-            double total = 0.0;
-            float g0 = gate(c0 * 64 + 2 * lane), g1 = gate(c0 * 64 + 2 * lane + 1);
-            for (int64_t i = c0; i < c1 || i == c0; i++) {     // (an empty sequence has one chunk of no tokens)
-                const double a0 = g0, a1 = g1;
-                if (i + 1 < c1)
-                    g0 = gate((i + 1) * 64 + 2 * lane), g1 = gate((i + 1) * 64 + 2 * lane + 1);
-                double sum = a0 + a1;
+            // Two chunks at a time, one by lanes 0..15 and one by the others, four tokens a lane.
+            const int half = lane >> 4, j = 4 * (lane & 15);
+            Sum total{0.0f, 0.0f};
+            float g[4];
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double z = __shfl_up_sync(FULL, sum, o);
-                    if (lane >= o)
-                        sum += z;
+            for (int q = 0; q < 4; q++)
+                g[q] = gate((c0 + half) * 64 + j + q);
+            for (int64_t i0 = c0; i0 < c1 || i0 == c0; i0 += 2) {   // (an empty sequence has one chunk of no tokens)
+                const int64_t i = i0 + half;
+                Sum a[4];
+                a[0] = in_base_2(g[0]);
+#pragma unroll
+                for (int q = 1; q < 4; q++)
+                    a[q] = add(a[q - 1], in_base_2(g[q]));
+                if (i0 + 2 < c1) {
+#pragma unroll
+                    for (int q = 0; q < 4; q++)
+                        g[q] = gate((i + 2) * 64 + j + q);
                 }
-                const double all = __shfl_sync(FULL, sum, 31);
-                total += all;
-                if (!slot_free())
+                Sum sum = a[3];
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) {
+                    const Sum z{__shfl_up_sync(FULL, sum.hi, o, 16), __shfl_up_sync(FULL, sum.lo, o, 16)};
+                    if ((lane & 15) >= o)
+                        sum = add(z, sum);
+                }
+                Sum before{__shfl_up_sync(FULL, sum.hi, 1, 16), __shfl_up_sync(FULL, sum.lo, 1, 16)};
+                if ((lane & 15) == 0)
+                    before = Sum{0.0f, 0.0f};
+#pragma unroll
+                for (int q = 0; q < 3; q++)
+                    a[q] = add(before, a[q]);
+                a[3] = sum;
+                const Sum all{__shfl_sync(FULL, sum.hi, 15, 16), __shfl_sync(FULL, sum.lo, 15, 16)};
+                const Sum middle{__shfl_sync(FULL, sum.hi, 7, 16), __shfl_sync(FULL, sum.lo, 7, 16)};
+                const int count = i0 + 1 < c1 ? 2 : 1;         // (the second may be the next group's first)
+                if (STATES_ONLY) {
+                    total = add(total, Sum{__shfl_sync(FULL, all.hi, 0), __shfl_sync(FULL, all.lo, 0)});
+                    if (count > 1)
+                        total = add(total, Sum{__shfl_sync(FULL, all.hi, 16), __shfl_sync(FULL, all.lo, 16)});
+                }
+                if (!slot_free(c) || (count > 1 && !slot_free(c + 1)))
                     break;
-                Entry &e = entries[c % ENTRIES];
-                const int len = (int)(w.len - i * 64 < 64 ? w.len - i * 64 : 64);
-                constexpr double L2E = 1.4426950408889634;
+                Entry &e = entries[(c + half) % ENTRIES];
+                if (half < count) {
+                    *reinterpret_cast<float4 *>(&e.hi[j]) = make_float4(a[0].hi, a[1].hi, a[2].hi, a[3].hi);
+                    *reinterpret_cast<float4 *>(&e.lo[j]) = make_float4(a[0].lo, a[1].lo, a[2].lo, a[3].lo);
+                    *reinterpret_cast<float4 *>(&e.ea[j]) = make_float4(p.scale * ex2_approx(a[0].hi), p.scale * ex2_approx(a[1].hi),
+                                                                        p.scale * ex2_approx(a[2].hi), p.scale * ex2_approx(a[3].hi));
+                    uint2 f[4];
 #pragma unroll
-                for (int q = 0; q < 2; q++) {
-                    const int j = 2 * lane + q;
-                    const double a = q ? sum : sum - a1, b = a * L2E;
-                    const float hi = (float)b;
-                    e.logs[j] = make_float2(hi, (float)(b - hi));
-                    e.ea[j] = p.scale * exp2f(hi);
-                    e.kf[j] = j < len ? expf((float)(all - a)) : 0.0f;
+                    for (int q = 0; q < 4; q++)
+                        f[q] = two_terms(ex2_approx(minus(all, a[q])));
+                    *reinterpret_cast<uint4 *>(&e.kf[j]) = make_uint4(f[0].x, f[0].y, f[1].x, f[1].y);
+                    *reinterpret_cast<uint4 *>(&e.kf[j + 2]) = make_uint4(f[2].x, f[2].y, f[3].x, f[3].y);
+                    if (j < 32)
+                        *reinterpret_cast<float4 *>(&e.up[j]) = make_float4(ex2_approx(minus(middle, a[0])), ex2_approx(minus(middle, a[1])),
+                                                                            ex2_approx(minus(middle, a[2])), ex2_approx(minus(middle, a[3])));
+                    if (j == 0) {
+                        const int left = (int)(w.len - i * 64 < 64 ? w.len - i * 64 : 64);
+                        e.valid = 1;
+                        e.first = i == c0, e.last = i + 1 >= c1;
+                        e.tok0 = (int)(w.bos + i * 64), e.len = left, e.h = w.h;
+                        e.decay = decay_of(all);
+                        e.src = src, e.at_src = at_src, e.dst = dst, e.at_dst = at_dst;
+                    }
+                    // the tiles, into L2: they are copied from there some chunks later, in a fraction of the time
+                    if ((lane & 15) < (STATES_ONLY ? 2 : 3) * CB) {
+                        const int cb = lane % CB, which = (lane & 15) / CB;
+                        prefetch_3d(which == 0 ? &kmap : (which == 1 ? &vmap : &qmap), 64 * cb, which == 2 ? w.h : w.h / p.group,
+                                    (int)(w.bos + i * 64));
+                    }
                 }
-                if (lane == 0) {
-                    e.valid = 1;
-                    e.first = i == c0, e.last = i + 1 >= c1;
-                    e.tok0 = (int)(w.bos + i * 64), e.len = len, e.h = w.h;
-                    e.decay = decay_of((float)all);
-                    e.src = w.g > 0 && !STATES_ONLY ? 2 : (!STATES_ONLY && p.init ? 1 : 0);
-                    e.at_src = e.src == 2 ? slot_of(p, plan, w.n, w.bos, w.g - 1) * p.H + w.h : (int64_t)w.n * p.H + w.h;
-                    e.dst = STATES_ONLY ? 2 : (c1 == chunks && p.fin ? 1 : 0);
-                    e.at_dst = STATES_ONLY ? slot_of(p, plan, w.n, w.bos, w.g) * p.H + w.h : (int64_t)w.n * p.H + w.h;
-                    const Decay all_of = decay_of((float)total);
-                    if (STATES_ONLY && i + 1 >= c1)
-                        plan.decays[e.at_dst] = make_float2(all_of.factor, all_of.weak ? 1.0f : 0.0f);
-                }
-                arrive(b_ent + 8 * (c % ENTRIES));
-                c++;
+                __syncwarp();
+                if (lane < count)
+                    mbar_arrive(b_ent + 8 * ((c + lane) % ENTRIES));
+                c += count;
+            }
+            if (STATES_ONLY && lane == 0) {
+                const Decay d = decay_of(total);
+                plan.decays[at_dst] = make_float2(d.factor, d.weak ? 1.0f : 0.0f);
             }
         }
-        if (slot_free()) {
+        if (slot_free(c)) {
             if (lane == 0)
                 entries[c % ENTRIES].valid = 0;
             arrive(b_ent + 8 * (c % ENTRIES));
         }
         if (asked > answers)
             timeout |= !mbar_wait(b_block, answers & 1);
+      }
+    } else if (warp < 8) {
+        // ------------------------------------------------------------ P, by two warps a chunk in turn: rows 0..31 and 32..63
+        set_registers<REGS_P, false>();
+        const int wp = warp - 4, i = (wp & 1) * 32 + lane;    // i: the thread's token
+        const f2 scale = f2_pack(p.scale, p.scale);
+        for (uint32_t c = 0; next(c); c++) {
+            const Entry &e = entries[c % ENTRIES];
+            if (!STATES_ONLY && (wp >> 1) == (int)(c & 1)) {
+                const float hi = e.hi[i], lo = e.lo[i];
+                const uint32_t tm = tmem + TM_S1 + 64 * (c & 1) + ((uint32_t)wp << 21);
+                unsigned char *pt = smem + S::P + (c & 1) * TILE_CB + i * 128;
+                auto store = [&](int chunk, const uint32_t *y) { // 8 tokens
+                    *reinterpret_cast<uint4 *>(pt + ((chunk ^ (i & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                };
+                if (!wait(b_s + 8 * (c & 1), c >> 1) || (c >= 2 && !wait(b_pe + 8 * (c & 1), (c >> 1) - 1)))
+                    break;
+                tc_fence_after();
+                // The block of 32 on the diagonal: a difference and an exponential a score.  bf16, V's type, as the product takes it.
+                const int first = (wp & 1) * 32;
+                const f2 hi2 = f2_pack(hi, hi), lo2 = f2_pack(lo, lo), minus = f2_pack(-1.0f, -1.0f);
+#pragma unroll 1
+                for (int part = 0; part < 2; part++) {
+                    float s[16];
+                    uint32_t y[8];
+                    tmem_read16(tm + first + 16 * part, s);
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 h = *reinterpret_cast<const float4 *>(&e.hi[first + 16 * part + j]);
+                        const float4 l = *reinterpret_cast<const float4 *>(&e.lo[first + 16 * part + j]);
+                        const f2 d0 = f2_add(f2_fma(f2_pack(h.x, h.y), minus, hi2), f2_fma(f2_pack(l.x, l.y), minus, lo2));
+                        const f2 d1 = f2_add(f2_fma(f2_pack(h.z, h.w), minus, hi2), f2_fma(f2_pack(l.z, l.w), minus, lo2));
+                        const f2 a = f2_mul(f2_mul(f2_pack(s[j], s[j + 1]), scale), f2_pack(ex2_approx(f2_lo(d0)), ex2_approx(f2_hi(d0))));
+                        const f2 b = f2_mul(f2_mul(f2_pack(s[j + 2], s[j + 3]), scale), f2_pack(ex2_approx(f2_lo(d1)), ex2_approx(f2_hi(d1))));
+                        y[j / 2] = pack_bf16(f2_lo(a), f2_hi(a)) & seen_pair(lane - 16 * part - j);
+                        y[j / 2 + 1] = pack_bf16(f2_lo(b), f2_hi(b)) & seen_pair(lane - 16 * part - j - 2);
+                    }
+                    store(first / 8 + 2 * part, y);
+                    store(first / 8 + 2 * part + 1, y + 4);
+                }
+                if (first == 0) {                              // tokens 32..63 are later ones
+                    const uint32_t y[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int q = 4; q < 8; q++)
+                        store(q, y);
+                } else {                                       // tokens 0..31: by way of token 31, e^(A_i - A_31) e^(A_31 - A_j)
+                    const float r = p.scale * ex2_approx((hi - e.hi[31]) + (lo - e.lo[31]));
+                    const f2 r2 = f2_pack(r, r);
+#pragma unroll 1
+                    for (int part = 0; part < 2; part++) {
+                        float s[16];
+                        uint32_t y[8];
+                        tmem_read16(tm + 16 * part, s);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 u = *reinterpret_cast<const float4 *>(&e.up[16 * part + j]);
+                            const f2 a = f2_mul(f2_pack(s[j], s[j + 1]), f2_mul(f2_pack(u.x, u.y), r2));
+                            const f2 b = f2_mul(f2_pack(s[j + 2], s[j + 3]), f2_mul(f2_pack(u.z, u.w), r2));
+                            y[j / 2] = pack_bf16(f2_lo(a), f2_hi(a));
+                            y[j / 2 + 1] = pack_bf16(f2_lo(b), f2_hi(b));
+                        }
+                        store(2 * part, y);
+                        store(2 * part + 1, y + 4);
+                    }
+                }
+                tc_fence_before();
+                fence_async_smem();
+                arrive(b_p + 8 * (c & 1));
+            }
+            arrive(b_ent_free + 8 * (c % ENTRIES));
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------------------------ K~
+        set_registers<REGS_K, false>();
+        const int t = tid - 256;
+        for (uint32_t c = 0; next(c); c++) {
+            const Entry &e = entries[c % ENTRIES];
+            const int st = c % STAGES, len = e.len;
+            // K is there and its scores are through, and so are the products with what lies in this chunk's other terms
+            if (!wait(b_full + 8 * st, c / STAGES) || (!STATES_ONLY && !wait(b_s + 8 * (c & 1), c >> 1)) ||
+                (TERMS > 1 && c >= 2 && !wait(b_l + 8 * (c & 1), (c >> 1) - 1)))
+                break;
+            constexpr int VECS = 64 * DIM / 8 / 128;           // 16-byte vectors of a thread, ROWS tokens apart
+            constexpr int ROWS = 128 / (DIM / 8);
+            const int ch = t % (DIM / 8), j0 = t / (DIM / 8);  // (ROWS is a multiple of 8: the swizzle is the same for all)
+            const int at = (ch / 8) * TILE_CB + j0 * 128 + (((ch % 8) ^ (j0 & 7)) << 4);
+            unsigned char *const kt = smem + st * S::STAGE + 2 * S::TILE + at;
+            unsigned char *const to = smem + S::KT + (c & 1) * (TERMS - 1) * S::TILE + at;
+#pragma unroll
+            for (int m = 0; m < VECS; m++) {
+                const int j = j0 + ROWS * m;
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (j < len)
+                    x = *reinterpret_cast<const uint4 *>(kt + m * (ROWS * 128));
+                const uint2 f = e.kf[j];
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                uint32_t y[TERMS][4];
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    if constexpr (TERMS == 1) {
+                        y[0][q] = bf16_fma(w[q], f.x, bf16_mul(w[q], f.y));
+                    } else {
+                        // k f1 rounded, and what that left off, which is a bf16 number, with k f2
+                        y[0][q] = bf16_mul(w[q], f.x);
+                        y[1][q] = bf16_fma(w[q], f.y, bf16_fma(w[q], f.x, y[0][q] ^ 0x80008000u));
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < TERMS; r++)
+                    *reinterpret_cast<uint4 *>((r == 0 ? kt : to + (r - 1) * S::TILE) + m * (ROWS * 128)) =
+                        make_uint4(y[r][0], y[r][1], y[r][2], y[r][3]);
+            }
+            if (len < 64) {                                    // what lies behind the sequence is cleared from V
+                unsigned char *vt = smem + st * S::STAGE;
+                for (int i = t; i < (64 - len) * 8 * CB; i += 128)
+                    *reinterpret_cast<uint4 *>(vt + i / ((64 - len) * 8) * TILE_CB + len * 128 + i % ((64 - len) * 8) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_async_smem();
+            arrive(b_k + 8 * (c & 1));
+            if (lane == 0)
+                mbar_arrive(b_ent_free + 8 * (c % ENTRIES));
+        }
+    } else if (warp < 20) {
+        // ------------------------------------------------------------ the state
+        set_registers<REGS_S, true>();
+        constexpr int COLS = DIM / 2;
+        const int half = (warp - 12) / 4, v = (warp & 3) * 32 + lane;
+        const uint32_t quad = (uint32_t)(warp & 3) << 21;
+        const bool mine = (warp & 3) * 32 < DIM;
+        const uint32_t tm_l = tmem + TM_L + quad + half * COLS, tm_sb = tmem + TM_SB + quad + half * (COLS / 2);
+        f2 s[COLS / 2];
+#pragma unroll
+        for (int i = 0; i < COLS / 2; i++)
+            s[i] = 0;
+        // S before chunk c, as the operand of its product
+        auto put = [&](uint32_t c) -> bool {
+            if (STATES_ONLY)
+                return true;
+            if (c >= 2 && !wait(b_o + 8 * (c & 1), (c >> 1) - 1))
+                return false;
+            if (mine) {
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < COLS / 32; k++) {
+                    uint32_t u[16];
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        u[i] = pack_bf16(f2_lo(s[16 * k + i]), f2_hi(s[16 * k + i]));
+                    tmem_put16(tm_sb + 64 * (c & 1) + 16 * k, u);
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+            }
+            arrive(b_sb + 8 * (c & 1));
+            return true;
+        };
+        for (uint32_t c = 0; next(c); c++) {
+            const Entry &e = entries[c % ENTRIES];
+            if (e.first) {
+                if (mine && e.src)
+                    load_state<COLS>(e.src == 1 ? p.init : plan.states, e.src == 1 ? plan.state_type : KDA_DTYPE_FP32,
+                                     (e.at_src * DIM + v) * DIM + half * COLS, s);
+                else
+#pragma unroll
+                    for (int i = 0; i < COLS / 2; i++)
+                        s[i] = 0;
+                if (!put(c))
+                    break;
+            }
+            if (!wait(b_l + 8 * (c & 1), c >> 1))
+                break;
+            if (mine) {
+                tc_fence_after();
+                const Decay d = e.decay;
+                const f2 factor = f2_pack(d.factor, d.factor);
+#pragma unroll
+                for (int i = 0; i < COLS; i += 16) {
+                    float l[16];
+                    tmem_read16(tm_l + i, l);
+                    if (d.weak) {
+#pragma unroll
+                        for (int j = 0; j < 8; j++)
+                            s[i / 2 + j] = f2_add(s[i / 2 + j], f2_fma(factor, s[i / 2 + j], f2_pack(l[2 * j], l[2 * j + 1])));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; j++)
+                            s[i / 2 + j] = f2_fma(factor, s[i / 2 + j], f2_pack(l[2 * j], l[2 * j + 1]));
+                    }
+                }
+                tc_fence_before();
+            }
+            arrive(b_l_free);
+            if (!e.last) {
+                if (!put(c + 1))
+                    break;
+            } else if (mine && e.dst) {
+                store_state<COLS>(e.dst == 1 ? p.fin : plan.states, e.dst == 1 ? plan.state_type : KDA_DTYPE_FP32,
+                                  (e.at_dst * DIM + v) * DIM + half * COLS, s);
+            }
+            arrive(b_ent_free + 8 * (c % ENTRIES));
+        }
+    } else {
+        // ------------------------------------------------------------ O
+        set_registers<REGS_O, true>();
+        const int ow = warp - 20, t = tid - 640;                // warp and thread of the four
+        const uint32_t quad = (uint32_t)ow << 21;
+        constexpr int WARPS = DIM / 32;                        // that have features
+        // where this lane's row of a piece's four 8 x 8 blocks goes: token (lane & 7) of 8, 8 features
+        const int r = lane & 7, block = lane >> 3;
+        const uint32_t to = base + S::OUT + (ow >> 1) * TILE_CB + ((block >> 1) * 8 + r) * 128;
+        const uint32_t to0 = to + ((((ow & 1) * 4 + (block & 1)) ^ r) << 4), to1 = to + ((((ow & 1) * 4 + 2 + (block & 1)) ^ r) << 4);
+        for (uint32_t c = 0; next(c); c++) {
+            const Entry &e = entries[c % ENTRIES];
+            if (!STATES_ONLY) {
+                if (!wait(b_o + 8 * (c & 1), c >> 1))
+                    break;
+                if (ow < WARPS) {
+                    tc_fence_after();
+                    const int len = e.len, tok0 = e.tok0, h = e.h;
+                    if (t == 0)
+                        bulk_wait_read_all();                  // the last chunk's O has left
+                    out_sync<32 * WARPS>();
+#pragma unroll 1
+                    for (int first = 0; first < 64; first += 16) {
+                        const float2 f0 = *reinterpret_cast<const float2 *>(&e.ea[first + 2 * (lane & 3)]);
+                        const float2 f1 = *reinterpret_cast<const float2 *>(&e.ea[first + 8 + 2 * (lane & 3)]);
+                        const f2 ea[2] = {f2_pack(f0.x, f0.y), f2_pack(f1.x, f1.y)};
+                        f2 z = 0;                              // stays 0 while V^T P^T is finite
+                        uint32_t w[2][4];
+#pragma unroll
+                        for (int up = 0; up < 2; up++) {       // lanes 0..15 and 16..31
+                            float x[8], y[8];
+                            tmem_read_pieces(tmem + TM_O1 + quad + first + (up << 20), x, tmem + TM_O2 + quad + first + (up << 20), y);
+#pragma unroll
+                            for (int i = 0; i < 4; i++) {
+                                const f2 u = f2_pack(x[2 * i], x[2 * i + 1]);
+                                z = f2_fma(u, 0, z);
+                                const f2 o = f2_fma(ea[i / 2], f2_pack(y[2 * i], y[2 * i + 1]), u);
+                                w[up][i] = pack_bf16(f2_lo(o), f2_hi(o));
+                            }
+                        }
+                        if (__any_sync(FULL, !(f2_lo(z) + f2_hi(z) == 0.0f))) {
+                            // (P is through; waited for here so that this thread sees it.  V's place may be another chunk's by now.)
+                            if (!wait(b_p + 8 * (c & 1), c >> 1))
+                                break;
+                            const int v = ow * 32 + lane;
+                            const unsigned char *pt = smem + S::P + (c & 1) * TILE_CB;
+                            const __nv_bfloat16 *vt = p.v + (int64_t)tok0 * p.v_stride + h / p.group * DIM + v;
+                            for (int i = first; i < min(first + 16, len); i++) {
+                                float u = tmem_read1(tmem + TM_O1 + quad + i);
+                                const float o = tmem_read1(tmem + TM_O2 + quad + i);
+                                if (u - u != 0.0f) {
+                                    u = 0.0f;
+                                    for (int j = 0; j <= i; j++) {
+                                        const __nv_bfloat16 a = *reinterpret_cast<const __nv_bfloat16 *>(
+                                            pt + i * 128 + (((j / 8) ^ (i & 7)) << 4) + (j % 8) * 2);
+                                        u = fmaf(__bfloat162float(a), __bfloat162float(vt[j * p.v_stride]), u);
+                                    }
+                                }
+                                *reinterpret_cast<__nv_bfloat16 *>(smem + S::OUT + (v / 64) * TILE_CB + i * 128 +
+                                                                   (((v % 64 / 8) ^ (i & 7)) << 4) + (v % 8) * 2) =
+                                    __float2bfloat16_rn(fmaf(e.ea[i], o, u));
+                            }
+                        } else {
+                            stmatrix_x4_t(to0 + first * 128, w[0][0], w[0][1], w[0][2], w[0][3]);
+                            stmatrix_x4_t(to1 + first * 128, w[1][0], w[1][1], w[1][2], w[1][3]);
+                        }
+                    }
+                    tc_fence_before();
+                    fence_async_smem();
+                    arrive(b_o_free);
+                    arrive(b_pe + 8 * (c & 1));
+                    out_sync<32 * WARPS>();
+                    if (len == 64) {
+                        if (t == 0) {
+#pragma unroll
+                            for (int cb = 0; cb < CB; cb++)
+                                tma_store_3d(&omap, base + S::OUT + cb * TILE_CB, 64 * cb, h, tok0);
+                            bulk_commit();
+                        }
+                    } else {                                   // only the sequence's tokens
+                        for (int i = t; i < len * (DIM / 8); i += 32 * WARPS) {
+                            const int tok = i / (DIM / 8), ch = i % (DIM / 8);
+                            *reinterpret_cast<uint4 *>(p.out + ((int64_t)(tok0 + tok) * p.H + h) * DIM + ch * 8) =
+                                *reinterpret_cast<const uint4 *>(smem + S::OUT + (ch / 8) * TILE_CB + tok * 128 + (((ch % 8) ^ (tok & 7)) << 4));
+                        }
+                    }
+                } else {
+                    arrive(b_o_free);
+                    arrive(b_pe + 8 * (c & 1));
+                }
+            }
+            arrive(b_ent_free + 8 * (c % ENTRIES));
+        }
+        if (t == 0)
+            bulk_wait_read_all();
     }
     report(p.err, bad, DEVERR_CU_SEQLENS);
     report(p.err, timeout, DEVERR_TIMEOUT);
     tc_fence_before();
     __syncthreads();
-    if (warp == 17)
+    if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS));
 }
 
@@ -821,18 +1024,20 @@ cudaError_t launch(const LinearArgs &p, const LinearPlan &plan, int64_t items, c
     if (e != cudaSuccess)
         return e;
     return launch_in_row(kda_linear_chunks_kernel<DIM, TERMS, STATES_ONLY>, (unsigned)items, THREADS, Shape<DIM, TERMS>::SMEM, 1, st, p,
-                         plan, maps[0], maps[1], maps[2]);
+                         plan, maps[0], maps[1], maps[2], maps[3]);
 }
 
 template <int DIM, int TERMS> cudaError_t launch_all(const LinearArgs &p, const LinearPlan &plan, cudaStream_t st)
 {
-    CUtensorMap maps[3];
+    CUtensorMap maps[4];
     const int64_t tokens = p.tok.cu ? p.tok.T : p.tok.N * p.tok.T;
     cudaError_t e = token_map(&maps[0], p.q, DIM, p.H, tokens, p.q_stride);
     if (e == cudaSuccess)
         e = token_map(&maps[1], p.k, DIM, p.H / p.group, tokens, p.k_stride);
     if (e == cudaSuccess)
         e = token_map(&maps[2], p.v, DIM, p.H / p.group, tokens, p.v_stride);
+    if (e == cudaSuccess)
+        e = token_map(&maps[3], p.out, DIM, p.H, tokens, (int64_t)p.H * DIM);
     if (e == cudaSuccess && plan.groups > 1) {
         e = launch<DIM, TERMS, true>(p, plan, plan.items_before, maps, st);
         if (e == cudaSuccess)
