@@ -8,7 +8,8 @@
 // Two kernels.  Statistics: a CTA takes a chunk of a row, holds it in registers, and writes its maximum m and
 // sum_t exp((l_t - m) / tau); every logit is read once, and that is what bounds the call.  Pick: a cluster of CTAs takes a
 // request, joins its rows' statistics (each CTA for itself: a few hundred numbers), decides r, and scans row r, the
-// draft's row r and the noise, an eighth of the vocabulary a CTA; the best eight meet in shared memory.
+// draft's row r and the noise, a share of the vocabulary a CTA; the shares' best meet in shared memory.  The race is run on
+// (e_t - q_t z) / E_t, z = sum e: no division by z.
 #include "kda_step.cuh"
 
 #include <cfloat>
@@ -17,8 +18,10 @@
 namespace kda {
 namespace {
 
-constexpr int THREADS = 256;
-constexpr int CLUSTER = 8;                  // CTAs of a request in the pick
+constexpr int THREADS = 256;                // of the statistics
+constexpr int PICK_THREADS = 512;
+constexpr int CLUSTER = 8;                  // CTAs of a request in the pick, at most
+constexpr int AHEAD = 8;                    // tokens of a thread whose loads are in flight
 constexpr int MAX_DRAFTS = 31;
 constexpr unsigned FULL = 0xffffffffu;
 
@@ -30,7 +33,8 @@ struct VerifyArgs {
     const int32_t *draft_lens;
     int32_t *tokens, *counts;
     int B, K, V;
-    int chunk, chunks;
+    int chunks, chunk_vecs;      // chunks of a row, 16-byte vectors of a chunk
+    int cluster;                 // CTAs of a request in the pick
     float2 *stats;               // [B (K + 1)][chunks]: maximum, sum of exponentials (workspace)
     unsigned int *err;
 };
@@ -73,6 +77,46 @@ template <> __device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4 &y
         x[2 * i] = bf16_lo(w[i]), x[2 * i + 1] = bf16_hi(w[i]);
 }
 
+template <typename T> __device__ __forceinline__ uint4 lowest()
+{
+    const uint32_t w = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;   // -inf
+    return make_uint4(w, w, w, w);
+}
+__device__ __forceinline__ uint32_t word_of(const uint4 &x, int i) { return i == 0 ? x.x : (i == 1 ? x.y : (i == 2 ? x.z : x.w)); }
+__device__ __forceinline__ void set_word(uint4 &x, int i, uint32_t w)
+{
+    x.x = i == 0 ? w : x.x, x.y = i == 1 ? w : x.y, x.z = i == 2 ? w : x.z, x.w = i == 3 ? w : x.w;
+}
+__device__ __forceinline__ void put(uint4 &x, int e, float v) { set_word(x, e, __float_as_uint(v)); }
+__device__ __forceinline__ void put(uint4 &x, int e, __nv_bfloat16 v)
+{
+    const uint32_t w = word_of(x, e / 2), b = __bfloat16_as_ushort(v);
+    set_word(x, e / 2, e & 1 ? (w & 0xffffu) | b << 16 : (w & 0xffff0000u) | b);
+}
+__device__ __forceinline__ uint32_t bf16_max(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// The largest of a thread's elements
+template <typename T, int N> __device__ __forceinline__ float largest(const uint4 (&x)[N])
+{
+    if constexpr (sizeof(T) == 2) {
+        uint32_t m = bf16_max(bf16_max(x[0].x, x[0].y), bf16_max(x[0].z, x[0].w));
+#pragma unroll
+        for (int i = 1; i < N; i++)
+            m = bf16_max(m, bf16_max(bf16_max(x[i].x, x[i].y), bf16_max(x[i].z, x[i].w)));
+        return fmaxf(fmaxf(bf16_lo(m), bf16_hi(m)), -INFINITY);
+    } else {
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(x[i].x), __uint_as_float(x[i].y)), fmaxf(__uint_as_float(x[i].z), __uint_as_float(x[i].w))));
+        return m;
+    }
+}
+
 __device__ __forceinline__ float block_max(float x, float *sm)
 {
 #pragma unroll
@@ -105,9 +149,9 @@ __device__ __forceinline__ float block_sum(float x, float *sm)
 // log2(e) / tau, kept finite so that a logit at the maximum still gets weight 1 for the smallest tau
 __device__ __forceinline__ float exponent_scale(float tau) { return fminf(LOG2E / tau, FLT_MAX); }
 
-// One chunk of one row a CTA: VECS 16-byte vectors a thread.  The row may start anywhere: vectors are cut at 16-byte
+// One chunk of one row a CTA: at most VECS 16-byte vectors a thread.  The row may start anywhere: vectors are cut at 16-byte
 // boundaries of memory, and one that reaches over an end of the row is read element by element.
-template <typename T, int VECS> __global__ void __launch_bounds__(THREADS) kda_verify_stats_kernel(const VerifyArgs p)
+template <typename T, int VECS> __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 4 : 3) kda_verify_stats_kernel(const VerifyArgs p)
 {
     constexpr int E = 16 / sizeof(T);
     __shared__ float sm[2][THREADS / 32];
@@ -120,48 +164,75 @@ template <typename T, int VECS> __global__ void __launch_bounds__(THREADS) kda_v
     const float tau = temperature_of(p, b, bad);
     const T *l = static_cast<const T *>(p.logits) + row * p.row_stride;
     const int off = (int)((reinterpret_cast<uintptr_t>(l) & 15) / sizeof(T));
-    float x[VECS][E];
-    float m = -INFINITY;
+    uint4 x[VECS];                                  // as they lie in memory: half the registers of floats for bf16
 #pragma unroll
     for (int i = 0; i < VECS; i++) {
-        const int at = (c * (THREADS * VECS) + i * THREADS + tid) * E - off;   // first element of the vector
-        if (at >= 0 && at + E <= p.V) {
-            unpack<T>(__ldcg(reinterpret_cast<const uint4 *>(l + at)), x[i]);
+        const int v = i * THREADS + tid, at = (c * p.chunk_vecs + v) * E - off;   // first element of the vector
+        const bool mine = v < p.chunk_vecs;
+        if (mine && at >= 0 && at + E <= p.V) {
+            x[i] = __ldcg(reinterpret_cast<const uint4 *>(l + at));
         } else {
-#pragma unroll
-            for (int e = 0; e < E; e++)
-                x[i][e] = at + e >= 0 && at + e < p.V ? as_float(l[at + e]) : -INFINITY;
+            x[i] = lowest<T>();
+            if (mine)
+                for (int e = 0; e < E; e++)
+                    if (at + e >= 0 && at + e < p.V)
+                        put(x[i], e, l[at + e]);
         }
     }
-#pragma unroll
-    for (int i = 0; i < VECS; i++)
-#pragma unroll
-        for (int e = 0; e < E; e++)
-            m = fmaxf(m, x[i][e]);                  // (fmaxf leaves NaN out)
+    float m = largest<T>(x);                        // (NaN left out)
     m = block_max(m, sm[0]);
     float s = 0.0f;
     if (tau > 0.0f && m > -INFINITY) {
         const float f = exponent_scale(tau);
+        const f2 f2f = f2_pack(f, f), minus_m = f2_pack(-m, -m), one = f2_pack(1.0f, 1.0f);
+        f2 s2 = 0;
 #pragma unroll
         for (int i = 0; i < VECS; i++)
+        {
+            float u[E];
+            unpack<T>(x[i], u);
 #pragma unroll
-            for (int e = 0; e < E; e++) {
-                const float y = ex2_approx((x[i][e] - m) * f);
-                s += y == y ? y : 0.0f;
+            for (int e = 0; e < E; e += 2) {
+                const f2 y = f2_mul(f2_fma(f2_pack(u[e], u[e + 1]), one, minus_m), f2f);
+                s2 = f2_fma(f2_pack(ex2_approx(f2_lo(y)), ex2_approx(f2_hi(y))), one, s2);
             }
+        }
+        s = f2_lo(s2) + f2_hi(s2);
+        if (s != s) {                               // a NaN among them (or an infinite maximum): those that are none
+            s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VECS; i++) {
+                float u[E];
+                unpack<T>(x[i], u);
+#pragma unroll
+                for (int e = 0; e < E; e++) {
+                    const float y = ex2_approx((u[e] - m) * f);
+                    s += y == y ? y : 0.0f;
+                }
+            }
+        }
     }
     s = block_sum(s, sm[1]);
     if (tid == 0)
         p.stats[(int64_t)row * p.chunks + c] = make_float2(m, s);
 }
 
-// exp(d / tau) for d <= 0, to about an ulp: the quotient's rounding is put back, and one too small for fp32 is 0.
-__device__ __forceinline__ float weight_of(float d, float tau, float inv)
+// exp(d / tau) for d <= 0: the exponent in base 2 as two terms, so that its rounding does not grow with it.  NaN for -inf and NaN,
+// which win no race.
+struct Exponent {
+    float hi, lo;                       // log2(e) / tau
+};
+__device__ __forceinline__ Exponent exponent_of(float tau)
 {
-    const float x = d * inv;
-    if (!(x > -104.0f))
-        return 0.0f;
-    return expf(x) * (1.0f + fmaf(-x, tau, d) * inv);
+    constexpr float LOG2E_LO = (float)(1.4426950408889634074 - (double)LOG2E);
+    const float hi = exponent_scale(tau);
+    return Exponent{hi, hi < FLT_MAX ? (fmaf(-hi, tau, LOG2E) + LOG2E_LO) / tau : 0.0f};
+}
+__device__ __forceinline__ float weight_of(float d, const Exponent &f)
+{
+    constexpr float LN2 = 0.6931471805599453f;
+    const float t = d * f.hi, r = fmaf(d, f.lo, fmaf(d, f.hi, -t)), y = ex2_approx(t);
+    return fmaf(y, r * LN2, y);
 }
 
 __device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank)
@@ -172,51 +243,65 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank)
 }
 
 // A cluster a request.
-template <typename T> __global__ void __launch_bounds__(THREADS) kda_verify_pick_kernel(const VerifyArgs p)
+template <typename T> __global__ void __launch_bounds__(PICK_THREADS, 2) kda_verify_pick_kernel(const VerifyArgs p)
 {
     __shared__ float row_max[MAX_DRAFTS + 1], row_sum[MAX_DRAFTS + 1];
     __shared__ int row_ok[MAX_DRAFTS + 1];
-    __shared__ unsigned long long best_of[THREADS / 32], best_cta[2][CLUSTER];
+    __shared__ unsigned long long best_of[PICK_THREADS / 32], best_cta[2][CLUSTER];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
-    const int b = blockIdx.x / CLUSTER, rank = blockIdx.x % CLUSTER;
+    const int b = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
+    const int share = (p.V + p.cluster - 1) / p.cluster, from = rank * share, to = min(p.V, from + share);
+    const float *noise = p.noise + (int64_t)b * p.V;
     stream_order();
+    // the first tokens' noise, which does not depend on what is decided
+    float ahead[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; i++) {
+        const int t = from + tid + i * PICK_THREADS;
+        ahead[i] = t < to ? noise[t] : -1.0f;
+    }
     bool bad = false;
     const int L = drafts_of(p, b, bad);
-    const float tau = temperature_of(p, b, bad), inv = tau > 0.0f ? fminf(1.0f / tau, FLT_MAX) : 0.0f;
+    const float tau = temperature_of(p, b, bad);
+    const bool greedy = tau == 0.0f;
+    const Exponent f = exponent_of(greedy ? 1.0f : tau);
     const T *logits = static_cast<const T *>(p.logits) + (int64_t)b * (p.K + 1) * p.row_stride;
-    for (int i = warp; i <= L; i += THREADS / 32) {
+    for (int i = warp; i <= L; i += PICK_THREADS / 32) {
         const float2 *st = p.stats + ((int64_t)b * (p.K + 1) + i) * p.chunks;
-        float m = -INFINITY, z = 0.0f;
-        for (int c = lane; c < p.chunks; c += 32)
+        const float2 none = make_float2(-INFINITY, 0.0f), first = lane < p.chunks ? __ldcg(&st[lane]) : none;
+        // the draft's logit and probability
+        float l = 0.0f, bar = 0.0f;
+        bool there = false;
+        if (i < L) {
+            const int x = p.drafts[b * p.K + i];
+            there = x >= 0 && x < p.V;
+            bad |= !there;
+            if (there) {
+                l = logit(as_float(logits[i * p.row_stride + x]));
+                bar = p.uniform[b * p.K + i] * (p.probs ? p.probs[((int64_t)b * p.K + i) * p.V + x] : 1.0f);
+            }
+        }
+        float m = first.x, z = 0.0f;
+        for (int c = lane + 32; c < p.chunks; c += 32)
             m = fmaxf(m, __ldcg(&st[c].x));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-        if (tau > 0.0f)
-            for (int c = lane; c < p.chunks; c += 32) {
+        if (!greedy) {
+            z = first.x == -INFINITY ? 0.0f : first.y * weight_of(first.x - m, f);
+            for (int c = lane + 32; c < p.chunks; c += 32) {
                 const float2 x = __ldcg(&st[c]);
-                z += x.x == -INFINITY ? 0.0f : x.y * weight_of(x.x - m, tau, inv);
+                z += x.x == -INFINITY ? 0.0f : x.y * weight_of(x.x - m, f);
             }
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             z += __shfl_xor_sync(FULL, z, o);
         if (lane == 0) {
-            bool ok = false;
-            if (i < L && fabsf(m) <= FLT_MAX) {
-                const int x = p.drafts[b * p.K + i];
-                if (x < 0 || x >= p.V) {
-                    bad = true;
-                } else {
-                    const float l = logit(as_float(logits[i * p.row_stride + x]));
-                    if (tau > 0.0f) {
-                        const float q = p.probs ? p.probs[((int64_t)b * p.K + i) * p.V + x] : 1.0f;
-                        ok = p.uniform[b * p.K + i] * q < weight_of(l - m, tau, inv) / z;
-                    } else {
-                        ok = l == m;
-                    }
-                }
-            }
-            row_max[i] = m, row_sum[i] = z, row_ok[i] = ok;
+            // a row without a finite maximum, and a draft that cannot be, accept nothing
+            const bool can = there && fabsf(m) <= FLT_MAX && l > -INFINITY;
+            row_ok[i] = can && (greedy ? l == m : bar * z < weight_of(l - m, f));
+            row_max[i] = m, row_sum[i] = z;
         }
     }
     __syncthreads();
@@ -227,32 +312,56 @@ template <typename T> __global__ void __launch_bounds__(THREADS) kda_verify_pick
     const bool alive = fabsf(m) <= FLT_MAX;
     const int x = r < L ? p.drafts[b * p.K + r] : -1;
     const T *l = logits + r * p.row_stride;
-    const float *noise = p.noise + (int64_t)b * p.V;
     const float *q = r < L && p.probs ? p.probs + ((int64_t)b * p.K + r) * p.V : nullptr;
     // the best of the race: its value's bits above the complement of its index, so that ties go to the lower one
     unsigned long long best = 0;
     for (int pass = 0; pass < 2; pass++) {
-        const int share = (p.V + CLUSTER - 1) / CLUSTER, from = rank * share, to = min(p.V, from + share);
-        best = 0;
-        if (alive) {
-#pragma unroll 4
-            for (int t = from + tid; t < to; t += THREADS) {
-                const float d = logit(as_float(l[t])) - m;
-                float v;
-                if (tau > 0.0f) {
-                    float w = weight_of(d, tau, inv) / z;
-                    if (pass == 0 && r < L)
-                        w = q ? w - q[t] : (t == x ? 0.0f : w);
-                    v = w > 0.0f ? w / noise[t] : 0.0f;
-                } else {
-                    v = d == 0.0f ? 1.0f : 0.0f;
+        float most = 0.0f;
+        int at = 0;
+        // a thread's tokens in order: the first of equal ones stays.  Only those are worked out whose p_t / E_t, in logarithms, comes
+        // near the best that the warp has seen (what is taken off p_t makes it smaller).
+        auto take = [&](float v, int t) {
+            if (v > most)
+                most = v, at = t;
+        };
+        auto scan = [&](auto score, auto value) {
+            float bound = -INFINITY;                          // what a token's score has to reach
+            for (int base = from; base < to; base += AHEAD * PICK_THREADS) {
+                const int t0 = base + tid;
+                float lt[AHEAD], e[AHEAD], qt[AHEAD];
+#pragma unroll
+                for (int i = 0; i < AHEAD; i++) {
+                    const int t = t0 + i * PICK_THREADS;
+                    const bool in = t < to;
+                    lt[i] = in ? as_float(l[t]) : -INFINITY;
+                    e[i] = pass == 0 && base == from ? ahead[i] : (in ? noise[t] : -1.0f);
+                    qt[i] = in && q && pass == 0 ? q[t] : 0.0f;
                 }
-                if (v > 0.0f) {
-                    const unsigned long long key = ((unsigned long long)__float_as_uint(v) << 32) | (uint32_t)~t;
-                    best = key > best ? key : best;
-                }
+                float high = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < AHEAD; i++)
+                    high = fmaxf(high, score(lt[i], e[i]));
+                if (!__any_sync(FULL, high >= bound))
+                    continue;
+#pragma unroll
+                for (int i = 0; i < AHEAD; i++)
+                    take(value(lt[i], e[i], qt[i], t0 + i * PICK_THREADS), t0 + i * PICK_THREADS);
+                // the warp's best so far, less more than either side's rounding
+                bound = __log2f(__uint_as_float(__reduce_max_sync(FULL, __float_as_uint(most)))) - 0.01f;
             }
+        };
+        if (!alive) {
+        } else if (greedy) {
+            scan([&](float lt, float) { return lt == m ? 0.0f : -INFINITY; }, [&](float lt, float, float, int) { return lt == m ? 1.0f : 0.0f; });
+        } else {
+            const int without = q || pass > 0 ? -1 : x;       // a certain draft that was rejected
+            scan([&](float lt, float e) { return fmaf(lt - m, f.hi, -__log2f(e)); },
+                 [&](float lt, float e, float qt, int t) {
+                const float w = fmaf(-qt, z, weight_of(lt - m, f));
+                return t != without && w > 0.0f ? w * rcp_approx(e) : 0.0f;
+            });
         }
+        best = most > 0.0f ? ((unsigned long long)__float_as_uint(most) << 32) | (uint32_t)~at : 0ull;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             const unsigned long long y = __shfl_xor_sync(FULL, best, o);
@@ -261,18 +370,17 @@ template <typename T> __global__ void __launch_bounds__(THREADS) kda_verify_pick
         if (lane == 0)
             best_of[warp] = best;
         __syncthreads();
-        if (tid < CLUSTER) {
+        if (tid < p.cluster) {
             best = best_of[0];
 #pragma unroll
-            for (int i = 1; i < THREADS / 32; i++)
+            for (int i = 1; i < PICK_THREADS / 32; i++)
                 best = best_of[i] > best ? best_of[i] : best;
             asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_cta(smem_u32(&best_cta[pass][rank]), tid)), "l"(best) : "memory");
         }
         __syncwarp();
         asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
         best = 0;
-#pragma unroll
-        for (int i = 0; i < CLUSTER; i++)
+        for (int i = 0; i < p.cluster; i++)
             best = best_cta[pass][i] > best ? best_cta[pass][i] : best;
         if (best != 0 || r == L || !alive)           // the same in every CTA of the cluster
             break;
@@ -280,7 +388,7 @@ template <typename T> __global__ void __launch_bounds__(THREADS) kda_verify_pick
     }
     if (rank == 0) {
         const int token = best ? (int)~(uint32_t)best : -1;
-        for (int i = tid; i <= p.K; i += THREADS)
+        for (int i = tid; i <= p.K; i += PICK_THREADS)
             p.tokens[b * (p.K + 1) + i] = i < r ? p.drafts[b * p.K + i] : (i == r ? token : -1);
         if (tid == 0)
             p.counts[b] = r + 1;
@@ -288,21 +396,31 @@ template <typename T> __global__ void __launch_bounds__(THREADS) kda_verify_pick
     report(p.err, bad && rank == 0, DEVERR_CU_SEQLENS);
 }
 
-constexpr int STATS_VECS = 8;       // 16-byte vectors of a thread of the statistics
+// 16-byte vectors of a thread of the statistics: 8, or 2 where that leaves most SMs without a CTA (one request of 5 x 32001 bf16
+// logits: XX against YY us).
+constexpr int VECS_MOST = 8, VECS_FEW = 2;
 
 template <typename T> cudaError_t launch_verify(const VerifyArgs &p, cudaStream_t st)
 {
-    const cudaError_t e = launch_in_row(kda_verify_stats_kernel<T, STATS_VECS>, (unsigned)(p.chunks * p.B * (p.K + 1)), THREADS, 0, 1, st, p);
-    return e != cudaSuccess ? e : launch_in_row(kda_verify_pick_kernel<T>, (unsigned)p.B * CLUSTER, THREADS, 0, CLUSTER, st, p);
+    const unsigned grid = (unsigned)(p.chunks * p.B * (p.K + 1));
+    const cudaError_t e = p.chunk_vecs > THREADS * VECS_FEW
+                              ? launch_in_row(kda_verify_stats_kernel<T, VECS_MOST>, grid, THREADS, 0, 1, st, p)
+                              : launch_in_row(kda_verify_stats_kernel<T, VECS_FEW>, grid, THREADS, 0, 1, st, p);
+    return e != cudaSuccess ? e : launch_in_row(kda_verify_pick_kernel<T>, (unsigned)(p.B * p.cluster), PICK_THREADS, 0, p.cluster, st, p);
 }
 
 }  // namespace
 
-// Logits of a chunk; a row that starts off a 16-byte boundary reaches up to 7 further into them.
-static int verify_chunk(kda_dtype_t dtype) { return THREADS * STATS_VECS * 16 / (dtype == KDA_DTYPE_BF16 ? 2 : 4); }
-static int verify_chunks(kda_dtype_t dtype, int V)
+// Vectors of a row (one that starts off a 16-byte boundary reaches into one more), its chunks, all of about the same size.
+static int verify_vecs(kda_dtype_t dtype, int V)
 {
-    return (V + (dtype == KDA_DTYPE_BF16 ? 7 : 3) + verify_chunk(dtype) - 1) / verify_chunk(dtype);
+    const int e = dtype == KDA_DTYPE_BF16 ? 8 : 4;
+    return (V + 2 * e - 2) / e;
+}
+static int verify_chunks(kda_dtype_t dtype, int B, int K, int V)
+{
+    const int vecs = verify_vecs(dtype, V), large = (vecs + THREADS * VECS_MOST - 1) / (THREADS * VECS_MOST);
+    return (int64_t)B * (K + 1) * large >= 2 * 152 ? large : (vecs + THREADS * VECS_FEW - 1) / (THREADS * VECS_FEW);
 }
 static bool verify_sizes(kda_dtype_t dtype, int B, int K, int V)
 {
@@ -310,7 +428,7 @@ static bool verify_sizes(kda_dtype_t dtype, int B, int K, int V)
 }
 static bool verify_fits(kda_dtype_t dtype, int B, int K, int V)
 {
-    return K <= MAX_DRAFTS && V <= (1 << 24) && (int64_t)B * (K + 1) * verify_chunks(dtype, V) <= INT32_MAX &&
+    return K <= MAX_DRAFTS && V <= (1 << 24) && (int64_t)B * (K + 1) * verify_chunks(dtype, B, K, V) <= INT32_MAX &&
            B <= INT32_MAX / CLUSTER;
 }
 
@@ -352,7 +470,7 @@ extern "C" size_t kda_verify_drafts_workspace_size(kda_dtype_t dtype, int B, int
 {
     if (!verify_sizes(dtype, B, K, V) || !verify_fits(dtype, B, K, V))
         return 0;
-    return (size_t)B * (K + 1) * verify_chunks(dtype, V) * sizeof(float2);
+    return (size_t)B * (K + 1) * verify_chunks(dtype, B, K, V) * sizeof(float2);
 }
 
 extern "C" kda_status_t kda_verify_drafts_ws(const void *logits, kda_dtype_t dtype, int64_t row_stride,
@@ -368,7 +486,13 @@ extern "C" kda_status_t kda_verify_drafts_ws(const void *logits, kda_dtype_t dty
     if (!workspace || !is_aligned(workspace, 256) || workspace_bytes < kda_verify_drafts_workspace_size(dtype, B, K, V))
         return KDA_ERR_INVALID_ARGUMENT;
     VerifyArgs p{logits, row_stride, draft_tokens, draft_probs, uniform, noise, temperature, draft_lens, tokens, counts, B, K, V};
-    p.chunk = verify_chunk(dtype), p.chunks = verify_chunks(dtype, V);
+    p.chunks = verify_chunks(dtype, B, K, V);
+    p.chunk_vecs = (verify_vecs(dtype, V) + p.chunks - 1) / p.chunks;
+    // as many CTAs as run at once, two an SM: more of them wait for a place and then for the same chain of loads (128 requests of 3
+    // drafts, 50257 bf16 logits, statistics included: 8 CTAs a request 38.6 us, 2 XX)
+    p.cluster = CLUSTER;
+    while (p.cluster > 1 && (int64_t)B * p.cluster > 2 * 152)
+        p.cluster /= 2;
     p.stats = static_cast<float2 *>(workspace);
     if (step_error_word(&p.err) != cudaSuccess)
         return KDA_ERR_CUDA;
