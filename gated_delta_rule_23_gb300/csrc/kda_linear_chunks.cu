@@ -7,8 +7,7 @@
 //
 // The features lie on tensor memory's lanes: O^T and S have a row per v, so that S is the operand of its product straight from tensor
 // memory (bf16, written by the threads that hold it) and leaves shared memory's bandwidth, the first bound of such a kernel, to
-// the others.  Four products a chunk: Q K^T [64 x 64] (the 64 rows of A above or below are whatever lies next to Q, and their results
-// are not read: the alternate chunks' rows come out on lanes 0..63 and 64..127, so that two pairs of warps take turns),
+// the others.  Four products a chunk: Q K^T [64 x 64] (on 16 of each warp's 32 lanes),
 // V^T K~ [D x D], S Q^T and V^T P^T [D x 64].  D = 64 fills the lanes up with a block of zeros.
 //
 // The state stays in fp32 registers (eight warps): each chunk's V^T K~ comes out of tensor memory and is added there, so the tensor cores'
@@ -39,8 +38,9 @@ namespace {
 
 constexpr int THREADS = 768;                 // six warpgroups
 constexpr int TMEM_COLS = 512;
-constexpr int TM_S1 = 0, TM_O1 = 128, TM_O2 = 192, TM_L = 256, TM_SB = 384;
+constexpr int TM_S1 = 0, TM_SB = 64, TM_O1 = 128, TM_O2 = 192, TM_L = 256;   // columns; two L
 constexpr int ENTRIES = 8;
+constexpr int EARLY = 4;                     // chunks ahead that tiles are brought into L2
 constexpr int TILE_CB = 64 * 128;            // bytes of 64 tokens x 64 features
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int MAX_RANKED = 128;              // sequences of a ragged batch that are taken longest first
@@ -84,7 +84,6 @@ __device__ __forceinline__ float decayed(const Decay &d, float s, float l)
 
 struct alignas(16) Entry {    // one chunk; the tables are read four floats at a time
     float hi[64], lo[64];     // A_i in base 2, as two terms
-    float up[32];             // e^(A_31 - A_j)
     float ea[64];             // scale e^(A_i)
     uint2 kf[64];             // e^(A_C - A_j) as two bf16 terms, each twice
     int64_t at_src, at_dst;   // index of the state before and after the chunk's item
@@ -94,7 +93,7 @@ struct alignas(16) Entry {    // one chunk; the tables are read four floats at a
     int first, last;          // of its item
     int tok0, len, h;         // first token, tokens, head
 };
-static_assert(sizeof(Entry) % 16 == 0 && offsetof(Entry, lo) % 16 == 0 && offsetof(Entry, up) % 16 == 0 && offsetof(Entry, ea) % 16 == 0, "vector reads");
+static_assert(sizeof(Entry) % 16 == 0 && offsetof(Entry, lo) % 16 == 0 && offsetof(Entry, ea) % 16 == 0, "vector reads");
 
 template <int DIM, int TERMS> struct Shape {
     static constexpr int CB = DIM / 64;
@@ -107,7 +106,7 @@ template <int DIM, int TERMS> struct Shape {
     static constexpr int ZERO = OUT + TILE;                   // D = 64: lanes 64 to 127
     static constexpr int ENTRY = ZERO + (DIM == 64 ? TILE_CB : 0);
     static constexpr int BAR = ENTRY + ENTRIES * (int)sizeof(Entry);
-    static constexpr int SMEM = 1024 + BAR + 384;
+    static constexpr int SMEM = 1024 + BAR + 512;
     static_assert(SMEM <= 232448, "a CTA's shared memory");
     static_assert(ENTRY % 16 == 0 && BAR % 8 == 0 && P % 1024 == 0 && KT % 1024 == 0 && ZERO % 1024 == 0, "alignment");
 };
@@ -179,46 +178,75 @@ __device__ __forceinline__ int64_t slot_of(const LinearArgs &p, const LinearPlan
     return p.tok.cu ? bos / (64 * (int64_t)plan.group_chunks) + n + g : (int64_t)n * plan.groups + g;
 }
 
-// A row of 64-bit halves of the state in registers: COLS columns from `at` on
-template <int COLS> __device__ __forceinline__ void load_state(const void *p, kda_dtype_t type, int64_t at, f2 (&s)[COLS / 2])
-{
-    if (type == KDA_DTYPE_BF16) {
-        const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + at);
-#pragma unroll
-        for (int i = 0; i < COLS / 8; i++) {
-            const uint4 y = x[i];
-            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                s[4 * i + e] = f2_bf16x2(w[e]);
-        }
-    } else {
-        const float4 *x = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
-#pragma unroll
-        for (int i = 0; i < COLS / 4; i++) {
-            const float4 y = x[i];
-            s[2 * i] = f2_pack(y.x, y.y), s[2 * i + 1] = f2_pack(y.z, y.w);
-        }
-    }
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
     const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&y);
 }
+// COLS columns of a row of the state, in registers as pairs.  A thread has a row of its own, so it moves 32 bytes, a whole sector, at a
+// time where the state begins on such a boundary.
+__device__ __forceinline__ void load_32(const void *p, bool whole, uint32_t (&w)[8])
+{
+    if (whole) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p) : "memory");
+    } else {
+        const uint4 x = static_cast<const uint4 *>(p)[0], y = static_cast<const uint4 *>(p)[1];
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+    }
+}
+__device__ __forceinline__ void store_32(void *p, bool whole, const uint32_t (&w)[8])
+{
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                     ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+    } else {
+        static_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+template <int COLS> __device__ __forceinline__ void load_state(const void *p, kda_dtype_t type, int64_t at, f2 (&s)[COLS / 2])
+{
+    const bool whole = (reinterpret_cast<uintptr_t>(p) & 31) == 0;
+    uint32_t w[8];
+    if (type == KDA_DTYPE_BF16) {
+#pragma unroll
+        for (int i = 0; i < COLS / 16; i++) {
+            load_32(static_cast<const __nv_bfloat16 *>(p) + at + 16 * i, whole, w);
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                s[8 * i + e] = f2_bf16x2(w[e]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < COLS / 8; i++) {
+            load_32(static_cast<const float *>(p) + at + 8 * i, whole, w);
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                s[4 * i + e] = f2_pack(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
+        }
+    }
+}
 template <int COLS> __device__ __forceinline__ void store_state(void *p, kda_dtype_t type, int64_t at, const f2 (&s)[COLS / 2])
 {
+    const bool whole = (reinterpret_cast<uintptr_t>(p) & 31) == 0;
+    uint32_t w[8];
     if (type == KDA_DTYPE_BF16) {
-        uint4 *x = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p) + at);
 #pragma unroll
-        for (int i = 0; i < COLS / 8; i++)
-            x[i] = make_uint4(pack_bf16(f2_lo(s[4 * i]), f2_hi(s[4 * i])), pack_bf16(f2_lo(s[4 * i + 1]), f2_hi(s[4 * i + 1])),
-                              pack_bf16(f2_lo(s[4 * i + 2]), f2_hi(s[4 * i + 2])), pack_bf16(f2_lo(s[4 * i + 3]), f2_hi(s[4 * i + 3])));
+        for (int i = 0; i < COLS / 16; i++) {
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                w[e] = pack_bf16(f2_lo(s[8 * i + e]), f2_hi(s[8 * i + e]));
+            store_32(static_cast<__nv_bfloat16 *>(p) + at + 16 * i, whole, w);
+        }
     } else {
-        float4 *x = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
 #pragma unroll
-        for (int i = 0; i < COLS / 4; i++)
-            x[i] = make_float4(f2_lo(s[2 * i]), f2_hi(s[2 * i]), f2_lo(s[2 * i + 1]), f2_hi(s[2 * i + 1]));
+        for (int i = 0; i < COLS / 8; i++) {
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                w[2 * e] = __float_as_uint(f2_lo(s[4 * i + e])), w[2 * e + 1] = __float_as_uint(f2_hi(s[4 * i + e]));
+            store_32(static_cast<float *>(p) + at + 8 * i, whole, w);
+        }
     }
 }
 __device__ __forceinline__ void tmem_put16(uint32_t addr, const uint32_t *u)
@@ -246,6 +274,14 @@ __device__ __forceinline__ void tmem_read16(uint32_t addr, float (&s)[16])
 __device__ __forceinline__ void prefetch_3d(const CUtensorMap *map, int x, int y, int z)
 {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z) : "memory");
+}
+// Whether a phase is through, without waiting for it (a try_wait may suspend the thread for some microseconds)
+__device__ __forceinline__ bool mbar_test(uint32_t mbar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(done) : "r"(mbar), "r"(parity) : "memory");
+    return done;
 }
 // Pairs of bf16, each result rounded once
 __device__ __forceinline__ uint32_t bf16_mul(uint32_t a, uint32_t b)
@@ -277,6 +313,10 @@ __device__ __forceinline__ void tmem_read_pieces(uint32_t at, float (&s)[8], uin
                  : "=&f"(s[0]), "=&f"(s[1]), "=&f"(s[2]), "=&f"(s[3]), "=&f"(s[4]), "=&f"(s[5]), "=&f"(s[6]), "=&f"(s[7]),
                    "=&f"(t[0]), "=&f"(t[1]), "=&f"(t[2]), "=&f"(t[3]), "=&f"(t[4]), "=&f"(t[5]), "=&f"(t[6]), "=&f"(t[7])
                  : "r"(at), "r"(bt) : "memory");
+}
+__device__ __forceinline__ void stmatrix_x4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 __device__ __forceinline__ void stmatrix_x4_t(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
@@ -321,8 +361,8 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
     const uint32_t bar = base + S::BAR;
     const uint32_t b_full = bar, b_empty = b_full + 8 * STAGES, b_ent = b_empty + 8 * STAGES, b_ent_free = b_ent + 8 * ENTRIES,
                    b_s = b_ent_free + 8 * ENTRIES, b_p = b_s + 16, b_o = b_p + 16, b_sb = b_o + 16, b_pe = b_sb + 16,
-                   b_k = b_pe + 16, b_l = b_k + 16, b_l_free = b_l + 16, b_o_free = b_l_free + 8, b_block = b_o_free + 8, b_drain = b_block + 8;
-    static_assert(8 * (2 * STAGES + 2 * ENTRIES + 19) <= 384, "barriers");
+                   b_k = b_pe + 16, b_l = b_k + 16, b_l_free = b_l + 16, b_o2 = b_l_free + 16, b_o_free = b_o2 + 8, b_block = b_o_free + 8, b_drain = b_block + 8;
+    static_assert(8 * (2 * STAGES + 2 * ENTRIES + 21) <= 512, "barriers");
     __shared__ uint32_t tmem_slot;
     __shared__ uint4 block_answer;
     __shared__ short order[MAX_RANKED];
@@ -338,15 +378,16 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(b_s + 8 * i, 1);
-            mbar_init(b_p + 8 * i, 2);
+            mbar_init(b_p + 8 * i, 4);
             mbar_init(b_o + 8 * i, 1);
             mbar_init(b_drain + 8 * i, 1);
             mbar_init(b_sb + 8 * i, 8);
             mbar_init(b_pe + 8 * i, 4);
             mbar_init(b_k + 8 * i, 4);
             mbar_init(b_l + 8 * i, 1);
+            mbar_init(b_l_free + 8 * i, 8);
         }
-        mbar_init(b_l_free, 8);
+        mbar_init(b_o2, 1);
         mbar_init(b_o_free, 4);
         mbar_init(b_block, 1);
         mbar_fence_init();
@@ -356,11 +397,12 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                      "r"(TMEM_COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    if (DIM == 64) {
+    for (int i = tid; i < 2 * TILE_CB / 16; i += THREADS)
+        reinterpret_cast<uint4 *>(smem + S::P)[i] = make_uint4(0, 0, 0, 0);
+    if (DIM == 64)
         for (int i = tid; i < TILE_CB / 16; i += THREADS)
             reinterpret_cast<uint4 *>(smem + S::ZERO)[i] = make_uint4(0, 0, 0, 0);
-        fence_async_smem();
-    }
+    fence_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -391,6 +433,14 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
         for (; next(c); c++) {
             const Entry &e = entries[c % ENTRIES];
             const int st = c % STAGES, h = e.h, tok = e.tok0;
+            // a later chunk's tiles, into L2 if it is known by now: they are copied from there in a fraction of the time
+            const uint32_t later = (c + EARLY) % ENTRIES;
+            if (__all_sync(FULL, mbar_test(b_ent + 8 * later, (c + EARLY) / ENTRIES & 1)) && entries[later].valid &&
+                lane < (STATES_ONLY ? 2 : 3) * CB) {
+                const Entry &f = entries[later];
+                const int cb = lane % CB, which = lane / CB;
+                prefetch_3d(which == 0 ? &kmap : (which == 1 ? &vmap : &qmap), 64 * cb, which == 2 ? f.h : f.h / p.group, f.tok0);
+            }
             if (c >= STAGES && !wait(b_empty + 8 * st, c / STAGES - 1))
                 break;
             if (lane == 0) {
@@ -415,15 +465,15 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
         // warp waits, one elected lane issues from uniform registers.
         const uint32_t tm = __shfl_sync(FULL, tmem, 0), lead = elect_one();
         if (warp == 1) {
-            const uint32_t id_s = idesc_bf16(128, 64, false);
+            const uint32_t id_s = idesc_bf16(64, 64, false);
             for (uint32_t c = 0; next(c); c++) {
                 const uint32_t at = base + (c % STAGES) * S::STAGE;
                 if (!STATES_ONLY) {
-                    // where they go, P of the chunk before the last has been formed from
-                    if (!wait(b_full + 8 * (c % STAGES), c / STAGES) || (c >= 2 && !wait(b_p + 8 * (c & 1), (c >> 1) - 1)))
+                    // where they go, P of the chunk before has been formed from
+                    if (!wait(b_full + 8 * (c % STAGES), c / STAGES) || (c > 0 && !wait(b_p + 8 * ((c - 1) & 1), (c - 1) >> 1)))
                         break;
                     tc_fence_after();
-                    const uint32_t a = desc_lo(at + S::TILE - (c & 1) * TILE_CB, 16), b = desc_lo(at + 2 * S::TILE, 16), d = tm + TM_S1 + 64 * (c & 1);
+                    const uint32_t a = desc_lo(at + S::TILE, 16), b = desc_lo(at + 2 * S::TILE, 16), d = tm + TM_S1;
                     if (lead && !timeout) {
 #pragma unroll
                         for (int k = 0; k < DIM / 16; k++) {
@@ -445,9 +495,11 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                 const uint32_t at = base + st * S::STAGE;
                 // V as M rows: blocks of 64 features, for D = 64 the second one zeros
                 const uint32_t v = desc_lo(at, DIM == 128 ? TILE_CB : S::ZERO - st * S::STAGE);
-                if (!wait(b_full + 8 * st, c / STAGES) || !wait(b_k + 8 * (c & 1), c >> 1) || (c > 0 && !wait(b_l_free, c - 1)))
+                if (!wait(b_full + 8 * st, c / STAGES) || !wait(b_k + 8 * (c & 1), c >> 1) ||
+                    (c >= 2 && !wait(b_l_free + 8 * (c & 1), (c >> 1) - 1)))
                     break;
                 tc_fence_after();
+                const uint32_t d = tm + TM_L + 128 * (c & 1);
                 if (lead && !timeout) {
 #pragma unroll
                     for (int r = TERMS - 1; r >= 0; r--) {     // small terms first
@@ -455,9 +507,9 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
 #pragma unroll
                         for (int k = 0; k < 4; k++) {
                             if (r == TERMS - 1 && k == 0)
-                                mma_ss<false>(tm + TM_L, v, b, id_l, 0);
+                                mma_ss<false>(d, v, b, id_l, 0);
                             else
-                                mma_ss<true>(tm + TM_L, v + k * (2048 >> 4), b + k * (2048 >> 4), id_l, 1);
+                                mma_ss<true>(d, v + k * (2048 >> 4), b + k * (2048 >> 4), id_l, 1);
                         }
                     }
                     umma_commit(b_l + 8 * (c & 1));
@@ -469,7 +521,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                     if (!wait(b_sb + 8 * (c & 1), c >> 1) || (c > 0 && !wait(b_o_free, c - 1)))
                         break;
                     tc_fence_after();
-                    const uint32_t q = desc_lo(at + S::TILE, 16), sb = tm + TM_SB + 64 * (c & 1);
+                    const uint32_t q = desc_lo(at + S::TILE, 16), sb = tm + TM_SB;
                     if (lead && !timeout) {
 #pragma unroll
                         for (int k = 0; k < DIM / 16; k++) {
@@ -479,6 +531,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                             else
                                 mma_ts<true>(tm + TM_O2, sb + 8 * k, q + step, id_o2, 1);
                         }
+                        umma_commit(b_o2);
                     }
                     __syncwarp();
                     if (!wait(b_p + 8 * (c & 1), c >> 1))
@@ -555,6 +608,12 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
             const int64_t pair = (int64_t)w.n * p.H + w.h;
             const int64_t at_src = src == 2 ? slot_of(p, plan, w.n, w.bos, w.g - 1) * p.H + w.h : pair;
             const int64_t at_dst = STATES_ONLY ? slot_of(p, plan, w.n, w.bos, w.g) * p.H + w.h : pair;
+            // the state that the item starts from, into L2
+            if (src != 0 && lane == 0) {
+                const int size = src == 1 && plan.state_type == KDA_DTYPE_BF16 ? 2 : 4;
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const char *>(src == 1 ? p.init : plan.states) +
+                             at_src * DIM * DIM * size), "r"(DIM * DIM * size) : "memory");
+            }
             const float fixed = p.log_decay ? p.log_decay[w.h] : 0.0f;
             auto gate = [&](int64_t i) -> float { return i < w.len ? log_decay_of(p, w.bos + i, w.h, fixed, bad) : 0.0f; };
             // Two chunks at a time, one by lanes 0..15 and one by the others, four tokens a lane.
@@ -591,7 +650,6 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                     a[q] = add(before, a[q]);
                 a[3] = sum;
                 const Sum all{__shfl_sync(FULL, sum.hi, 15, 16), __shfl_sync(FULL, sum.lo, 15, 16)};
-                const Sum middle{__shfl_sync(FULL, sum.hi, 7, 16), __shfl_sync(FULL, sum.lo, 7, 16)};
                 const int count = i0 + 1 < c1 ? 2 : 1;         // (the second may be the next group's first)
                 if (STATES_ONLY) {
                     total = add(total, Sum{__shfl_sync(FULL, all.hi, 0), __shfl_sync(FULL, all.lo, 0)});
@@ -612,9 +670,6 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                         f[q] = two_terms(ex2_approx(minus(all, a[q])));
                     *reinterpret_cast<uint4 *>(&e.kf[j]) = make_uint4(f[0].x, f[0].y, f[1].x, f[1].y);
                     *reinterpret_cast<uint4 *>(&e.kf[j + 2]) = make_uint4(f[2].x, f[2].y, f[3].x, f[3].y);
-                    if (j < 32)
-                        *reinterpret_cast<float4 *>(&e.up[j]) = make_float4(ex2_approx(minus(middle, a[0])), ex2_approx(minus(middle, a[1])),
-                                                                            ex2_approx(minus(middle, a[2])), ex2_approx(minus(middle, a[3])));
                     if (j == 0) {
                         const int left = (int)(w.len - i * 64 < 64 ? w.len - i * 64 : 64);
                         e.valid = 1;
@@ -622,12 +677,6 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                         e.tok0 = (int)(w.bos + i * 64), e.len = left, e.h = w.h;
                         e.decay = decay_of(all);
                         e.src = src, e.at_src = at_src, e.dst = dst, e.at_dst = at_dst;
-                    }
-                    // the tiles, into L2: they are copied from there some chunks later, in a fraction of the time
-                    if ((lane & 15) < (STATES_ONLY ? 2 : 3) * CB) {
-                        const int cb = lane % CB, which = (lane & 15) / CB;
-                        prefetch_3d(which == 0 ? &kmap : (which == 1 ? &vmap : &qmap), 64 * cb, which == 2 ? w.h : w.h / p.group,
-                                    (int)(w.bos + i * 64));
                     }
                 }
                 __syncwarp();
@@ -649,67 +698,45 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
             timeout |= !mbar_wait(b_block, answers & 1);
       }
     } else if (warp < 8) {
-        // ------------------------------------------------------------ P, by two warps a chunk in turn: rows 0..31 and 32..63
+        // ------------------------------------------------------------ P, 16 tokens a warp
+        // In blocks of 16 x 16: a thread has two neighbouring columns of rows t / 4 and t / 4 + 8, twice.  Blocks of later tokens are
+        // zeros from the start.
         set_registers<REGS_P, false>();
-        const int wp = warp - 4, i = (wp & 1) * 32 + lane;    // i: the thread's token
-        const f2 scale = f2_pack(p.scale, p.scale);
+        const int wp = warp - 4, r0 = 16 * wp + lane / 4, c0 = 2 * (lane & 3);
+        const f2 scale = f2_pack(p.scale, p.scale), minus = f2_pack(-1.0f, -1.0f);
+        // where this lane's row of a block's four 8 x 8 parts goes: rows 0..7 and 8..15 of its left columns, then of its right ones
+        const int row = 16 * wp + (lane & 7) + (lane & 8), right = lane >> 4;
+        const uint32_t to = base + S::P + row * 128;
         for (uint32_t c = 0; next(c); c++) {
             const Entry &e = entries[c % ENTRIES];
-            if (!STATES_ONLY && (wp >> 1) == (int)(c & 1)) {
-                const float hi = e.hi[i], lo = e.lo[i];
-                const uint32_t tm = tmem + TM_S1 + 64 * (c & 1) + ((uint32_t)wp << 21);
-                unsigned char *pt = smem + S::P + (c & 1) * TILE_CB + i * 128;
-                auto store = [&](int chunk, const uint32_t *y) { // 8 tokens
-                    *reinterpret_cast<uint4 *>(pt + ((chunk ^ (i & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-                };
+            if (!STATES_ONLY) {
+                const float h0 = e.hi[r0], l0 = e.lo[r0], h1 = e.hi[r0 + 8], l1 = e.lo[r0 + 8];
                 if (!wait(b_s + 8 * (c & 1), c >> 1) || (c >= 2 && !wait(b_pe + 8 * (c & 1), (c >> 1) - 1)))
                     break;
                 tc_fence_after();
-                // The block of 32 on the diagonal: a difference and an exponential a score.  bf16, V's type, as the product takes it.
-                const int first = (wp & 1) * 32;
-                const f2 hi2 = f2_pack(hi, hi), lo2 = f2_pack(lo, lo), minus = f2_pack(-1.0f, -1.0f);
+                const uint32_t tm = tmem + TM_S1 + ((uint32_t)wp << 21), pt = to + (c & 1) * TILE_CB;
 #pragma unroll 1
-                for (int part = 0; part < 2; part++) {
-                    float s[16];
-                    uint32_t y[8];
-                    tmem_read16(tm + first + 16 * part, s);
+                for (int pair = 0; 2 * pair <= wp; pair++) {   // two blocks; the second may be all of later tokens
+                    float s[2][8];
+                    tmem_read_pieces(tm + 32 * pair, s[0], tm + 32 * pair + 16, s[1]);
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        const float4 h = *reinterpret_cast<const float4 *>(&e.hi[first + 16 * part + j]);
-                        const float4 l = *reinterpret_cast<const float4 *>(&e.lo[first + 16 * part + j]);
-                        const f2 d0 = f2_add(f2_fma(f2_pack(h.x, h.y), minus, hi2), f2_fma(f2_pack(l.x, l.y), minus, lo2));
-                        const f2 d1 = f2_add(f2_fma(f2_pack(h.z, h.w), minus, hi2), f2_fma(f2_pack(l.z, l.w), minus, lo2));
-                        const f2 a = f2_mul(f2_mul(f2_pack(s[j], s[j + 1]), scale), f2_pack(ex2_approx(f2_lo(d0)), ex2_approx(f2_hi(d0))));
-                        const f2 b = f2_mul(f2_mul(f2_pack(s[j + 2], s[j + 3]), scale), f2_pack(ex2_approx(f2_lo(d1)), ex2_approx(f2_hi(d1))));
-                        y[j / 2] = pack_bf16(f2_lo(a), f2_hi(a)) & seen_pair(lane - 16 * part - j);
-                        y[j / 2 + 1] = pack_bf16(f2_lo(b), f2_hi(b)) & seen_pair(lane - 16 * part - j - 2);
-                    }
-                    store(first / 8 + 2 * part, y);
-                    store(first / 8 + 2 * part + 1, y + 4);
-                }
-                if (first == 0) {                              // tokens 32..63 are later ones
-                    const uint32_t y[4] = {0, 0, 0, 0};
+                    for (int k = 0; k < 2; k++) {
+                        uint32_t y[4];
 #pragma unroll
-                    for (int q = 4; q < 8; q++)
-                        store(q, y);
-                } else {                                       // tokens 0..31: by way of token 31, e^(A_i - A_31) e^(A_31 - A_j)
-                    const float r = p.scale * ex2_approx((hi - e.hi[31]) + (lo - e.lo[31]));
-                    const f2 r2 = f2_pack(r, r);
-#pragma unroll 1
-                    for (int part = 0; part < 2; part++) {
-                        float s[16];
-                        uint32_t y[8];
-                        tmem_read16(tm + 16 * part, s);
-#pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 u = *reinterpret_cast<const float4 *>(&e.up[16 * part + j]);
-                            const f2 a = f2_mul(f2_pack(s[j], s[j + 1]), f2_mul(f2_pack(u.x, u.y), r2));
-                            const f2 b = f2_mul(f2_pack(s[j + 2], s[j + 3]), f2_mul(f2_pack(u.z, u.w), r2));
-                            y[j / 2] = pack_bf16(f2_lo(a), f2_hi(a));
-                            y[j / 2 + 1] = pack_bf16(f2_lo(b), f2_hi(b));
+                        for (int q = 0; q < 2; q++) {          // columns 0..7 and 8..15
+                            const int j = 32 * pair + 16 * k + 8 * q + c0;
+                            const float2 h = *reinterpret_cast<const float2 *>(&e.hi[j]);
+                            const float2 l = *reinterpret_cast<const float2 *>(&e.lo[j]);
+                            const f2 hj = f2_pack(h.x, h.y), lj = f2_pack(l.x, l.y);
+                            const f2 d0 = f2_add(f2_fma(hj, minus, f2_pack(h0, h0)), f2_fma(lj, minus, f2_pack(l0, l0)));
+                            const f2 d1 = f2_add(f2_fma(hj, minus, f2_pack(h1, h1)), f2_fma(lj, minus, f2_pack(l1, l1)));
+                            const f2 a = f2_mul(f2_mul(f2_pack(s[k][4 * q], s[k][4 * q + 1]), scale), f2_pack(ex2_approx(f2_lo(d0)), ex2_approx(f2_hi(d0))));
+                            const f2 b = f2_mul(f2_mul(f2_pack(s[k][4 * q + 2], s[k][4 * q + 3]), scale), f2_pack(ex2_approx(f2_lo(d1)), ex2_approx(f2_hi(d1))));
+                            // bf16, V's type, as the product takes it; later tokens' are cleared, whatever they are
+                            y[2 * q] = pack_bf16(f2_lo(a), f2_hi(a)) & seen_pair(r0 - j);
+                            y[2 * q + 1] = pack_bf16(f2_lo(b), f2_hi(b)) & seen_pair(r0 + 8 - j);
                         }
-                        store(2 * part, y);
-                        store(2 * part + 1, y + 4);
+                        stmatrix_x4(pt + (((4 * pair + 2 * k + right) ^ (row & 7)) << 4), y[0], y[1], y[2], y[3]);
                     }
                 }
                 tc_fence_before();
@@ -785,7 +812,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
         auto put = [&](uint32_t c) -> bool {
             if (STATES_ONLY)
                 return true;
-            if (c >= 2 && !wait(b_o + 8 * (c & 1), (c >> 1) - 1))
+            if (c > 0 && !wait(b_o2, c - 1))                  // the product with the one before
                 return false;
             if (mine) {
                 tc_fence_after();
@@ -795,7 +822,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
 #pragma unroll
                     for (int i = 0; i < 16; i++)
                         u[i] = pack_bf16(f2_lo(s[16 * k + i]), f2_hi(s[16 * k + i]));
-                    tmem_put16(tm_sb + 64 * (c & 1) + 16 * k, u);
+                    tmem_put16(tm_sb + 16 * k, u);
                 }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
@@ -825,7 +852,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
 #pragma unroll
                 for (int i = 0; i < COLS; i += 16) {
                     float l[16];
-                    tmem_read16(tm_l + i, l);
+                    tmem_read16(tm_l + 128 * (c & 1) + i, l);
                     if (d.weak) {
 #pragma unroll
                         for (int j = 0; j < 8; j++)
@@ -838,7 +865,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                 }
                 tc_fence_before();
             }
-            arrive(b_l_free);
+            arrive(b_l_free + 8 * (c & 1));
             if (!e.last) {
                 if (!put(c + 1))
                     break;
