@@ -6,21 +6,29 @@
 
 namespace kda {
 
-// Sequences of up to this many tokens are evaluated token by token.
-constexpr int64_t TOKENS_MOST = 16;
-static bool token_by_token(int64_t T) { return T <= TOKENS_MOST; }
+// Short sequences are evaluated token by token.  A chunk costs the same for 1 token and for 64, about what this many take in the
+// other kernel (us, chunks | tokens): one sequence of 32 heads of 128, 16 tokens 9.8 | 7.6, 24 9.9 | 10.1; 8 x 96, 12 tokens 37 | 33, 16
+// 37 | 45; 64 x 64, 8 tokens 109 | 101, 12 110 | 144; 32 x 32 of 64, 16 tokens 26 | 16.  With cu_seqlens only the sum is known here.
+static bool token_by_token(int N, int64_t T, int H, int D) { return T <= (D == 64 ? 16 : ((int64_t)N * H <= 1024 ? 14 : 8)); }
 
-// The cut of a call into groups (sizes only, so that the workspace is known beforehand), for 152 SMs.
+// The cut of a call into groups (sizes only, so that the workspace is known beforehand), for 152 SMs.  Measured: a chunk takes 1.4 us in
+// a (sequence, head)'s chain, however few run; groups cost a pass over K and V (1.1 us a chunk) and two launches.  8192 tokens,
+// one chain | groups: 8 heads 183 | 47 us, 32 heads 185 | 101, 64 heads 186 | 177; 1024 tokens of 8 heads 29 | 27, 512 19 | 26.
 static LinearPlan make_plan(bool varlen, int N, int64_t T, int H)
 {
     LinearPlan plan{};
     const int64_t chunks = (T + 63) / 64, pairs = (int64_t)N * H;
-    int64_t cut = 1;
-    if (chunks >= 32 && pairs <= 76)
-        cut = std::min<int64_t>(std::max<int64_t>(152 / (varlen ? H : pairs), 1), chunks / 8);
-    plan.group_chunks = (chunks + cut - 1) / cut;
+    // the longest sequence; of a ragged batch only the sum is known, and twice the mean is taken for it
+    const int64_t chain = varlen && N > 1 ? std::min(chunks, 2 * ((chunks + N - 1) / N)) : chunks;
+    int64_t cut = 1, best = 143 * chain;
+    for (int64_t g = 2; g * pairs <= 152 && g <= chain; g++) {
+        const int64_t cost = (800 + 250 * ((chain + g - 1) / g) + 30 * g) * 21 / 20;
+        if (cost < best)
+            best = cost, cut = g;
+    }
+    plan.group_chunks = (chain + cut - 1) / cut;
     plan.groups = (int)((chunks + plan.group_chunks - 1) / std::max<int64_t>(plan.group_chunks, 1));
-    if (plan.groups <= 1) {
+    if (cut == 1) {
         plan.groups = 1;
         plan.group_chunks = std::max<int64_t>(chunks, 1);
     }
@@ -104,7 +112,7 @@ using namespace kda;
 extern "C" size_t kda_linear_attn_workspace_size(int varlen, int N, int64_t T, int H, int D)
 {
     if (N < 1 || T < 0 || H < 1 || (D != 64 && D != 128) || T > INT32_MAX || (varlen ? T : (int64_t)N * T) > INT32_MAX ||
-        (int64_t)N * H > INT32_MAX / 16 || token_by_token(T))
+        (int64_t)N * H > INT32_MAX / 16 || token_by_token(N, T, H, D))
         return 0;
     return plan_bytes(make_plan(varlen != 0, N, T, H), varlen != 0, N, T, H, D);
 }
@@ -137,7 +145,7 @@ extern "C" kda_status_t kda_linear_attn_ws(const void *q, int64_t q_stride, cons
     if (step_error_word(&p.err) != cudaSuccess)
         return KDA_ERR_CUDA;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (token_by_token(T))
+    if (token_by_token(N, T, H, D))
         return launch_linear_tokens(p, state, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     LinearPlan plan = make_plan(cu_seqlens != nullptr, N, T, H);
     plan.states = static_cast<float *>(workspace);

@@ -14,7 +14,9 @@
 // own accumulation spans one chunk and what a long sequence adds up is rounded to nearest.  Weak decays are taken as
 // S + (expm1(A_C) S + L): a factor next to 1 that is off by half a step in every chunk would drift by 2^-25 a chunk; strong ones as
 // e^(A_C) S + L, so that nothing of a state that is forgotten stays behind as rounding.
-// K~ = e^(A_C - A_j) K is not a bf16 number: TERMS bf16 terms that add up to it are multiplied with V one after another.
+// K~ = e^(A_C - A_j) K is not a bf16 number: two bf16 terms that add up to it (to 2^-17) are multiplied with V one after the other.  With
+// one, outputs after bf16 states were 2.6e-3 off (norm) and not 2.3e-3, 1.7e-3 of it their own rounding, and a prompt of 8192 tokens, 96
+// heads took 205 us for 211: what the tensor cores do is not what bounds a chunk.
 //
 // Warps: 0 copies (tensor maps, a ring of chunks); 1 and 3 issue; 2 finds the chunks, and works their decays out ahead; 4..7 P;
 // 8..11 K~; 12..19 the state; 20..23 O, scaled and stored.  (The warps that all others wait for come first: an SM's schedulers are
@@ -43,6 +45,7 @@ constexpr int ENTRIES = 8;
 constexpr int EARLY = 4;                     // chunks ahead that tiles are brought into L2
 constexpr int TILE_CB = 64 * 128;            // bytes of 64 tokens x 64 features
 constexpr unsigned FULL = 0xffffffffu;
+constexpr int TERMS = 2;                     // bf16 terms of K~
 constexpr int MAX_RANKED = 128;              // sequences of a ragged batch that are taken longest first
 
 // A sum of logarithms in base 2 as two terms, good to some 2^-45 of the largest partial sum, without 64-bit arithmetic (whose unit here
@@ -95,7 +98,7 @@ struct alignas(16) Entry {    // one chunk; the tables are read four floats at a
 };
 static_assert(sizeof(Entry) % 16 == 0 && offsetof(Entry, lo) % 16 == 0 && offsetof(Entry, ea) % 16 == 0, "vector reads");
 
-template <int DIM, int TERMS> struct Shape {
+template <int DIM> struct Shape {
     static constexpr int CB = DIM / 64;
     static constexpr int TILE = CB * TILE_CB;
     static constexpr int STAGE = 3 * TILE;                    // V, Q, K (later K~'s first term)
@@ -347,12 +350,12 @@ template <int N, bool MORE> __device__ __forceinline__ void set_registers()
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <int DIM, int TERMS, bool STATES_ONLY>
+template <int DIM, bool STATES_ONLY>
 __global__ void __launch_bounds__(THREADS, 1)
 kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan plan, const __grid_constant__ CUtensorMap qmap,
                          const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap)
 {
-    using S = Shape<DIM, TERMS>;
+    using S = Shape<DIM>;
     constexpr int CB = S::CB, STAGES = S::STAGES;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -366,6 +369,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
     __shared__ uint32_t tmem_slot;
     __shared__ uint4 block_answer;
     __shared__ short order[MAX_RANKED];
+    __shared__ int lengths[MAX_RANKED];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < STAGES; i++) {
@@ -566,13 +570,17 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
         const short *ranked = nullptr;
         if (p.tok.cu && p.tok.N <= MAX_RANKED) {
             for (int i = lane; i < p.tok.N; i += 32) {
-                int64_t bos, len, x, y;
+                int64_t bos, len;
                 seq_range(p.tok.cu, i, p.tok.N, p.tok.T, bos, len);
+                lengths[i] = (int)len;
+            }
+            __syncwarp();
+            for (int i = lane; i < p.tok.N; i += 32) {
+                const int len = lengths[i];
                 int rank = 0;
-                for (int j = 0; j < p.tok.N; j++) {
-                    seq_range(p.tok.cu, j, p.tok.N, p.tok.T, x, y);
-                    rank += y > len || (y == len && j < i);
-                }
+#pragma unroll 4
+                for (int j = 0; j < p.tok.N; j++)
+                    rank += lengths[j] > len || (lengths[j] == len && j < i);
                 order[rank] = (short)i;
             }
             __syncwarp();
@@ -754,7 +762,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
             const int st = c % STAGES, len = e.len;
             // K is there and its scores are through, and so are the products with what lies in this chunk's other terms
             if (!wait(b_full + 8 * st, c / STAGES) || (!STATES_ONLY && !wait(b_s + 8 * (c & 1), c >> 1)) ||
-                (TERMS > 1 && c >= 2 && !wait(b_l + 8 * (c & 1), (c >> 1) - 1)))
+                (c >= 2 && !wait(b_l + 8 * (c & 1), (c >> 1) - 1)))
                 break;
             constexpr int VECS = 64 * DIM / 8 / 128;           // 16-byte vectors of a thread, ROWS tokens apart
             constexpr int ROWS = 128 / (DIM / 8);
@@ -773,13 +781,9 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                 uint32_t y[TERMS][4];
 #pragma unroll
                 for (int q = 0; q < 4; q++) {
-                    if constexpr (TERMS == 1) {
-                        y[0][q] = bf16_fma(w[q], f.x, bf16_mul(w[q], f.y));
-                    } else {
-                        // k f1 rounded, and what that left off, which is a bf16 number, with k f2
-                        y[0][q] = bf16_mul(w[q], f.x);
-                        y[1][q] = bf16_fma(w[q], f.y, bf16_fma(w[q], f.x, y[0][q] ^ 0x80008000u));
-                    }
+                    // k f1 rounded, and what that left off, which is a bf16 number, with k f2
+                    y[0][q] = bf16_mul(w[q], f.x);
+                    y[1][q] = bf16_fma(w[q], f.y, bf16_fma(w[q], f.x, y[0][q] ^ 0x80008000u));
                 }
 #pragma unroll
                 for (int r = 0; r < TERMS; r++)
@@ -1036,25 +1040,25 @@ cudaError_t token_map(CUtensorMap *map, const __nv_bfloat16 *ptr, int dim, int h
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int DIM, int TERMS, bool STATES_ONLY>
+template <int DIM, bool STATES_ONLY>
 cudaError_t launch(const LinearArgs &p, const LinearPlan &plan, int64_t items, const CUtensorMap *maps, cudaStream_t st)
 {
     static std::atomic<uint64_t> ready;      // devices whose kernel attribute is set
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && !(ready.load() >> dev & 1)) {
-        e = cudaFuncSetAttribute(kda_linear_chunks_kernel<DIM, TERMS, STATES_ONLY>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Shape<DIM, TERMS>::SMEM);
+        e = cudaFuncSetAttribute(kda_linear_chunks_kernel<DIM, STATES_ONLY>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Shape<DIM>::SMEM);
         if (e == cudaSuccess)
             ready.fetch_or(1ull << dev);
     }
     if (e != cudaSuccess)
         return e;
-    return launch_in_row(kda_linear_chunks_kernel<DIM, TERMS, STATES_ONLY>, (unsigned)items, THREADS, Shape<DIM, TERMS>::SMEM, 1, st, p,
+    return launch_in_row(kda_linear_chunks_kernel<DIM, STATES_ONLY>, (unsigned)items, THREADS, Shape<DIM>::SMEM, 1, st, p,
                          plan, maps[0], maps[1], maps[2], maps[3]);
 }
 
-template <int DIM, int TERMS> cudaError_t launch_all(const LinearArgs &p, const LinearPlan &plan, cudaStream_t st)
+template <int DIM> cudaError_t launch_all(const LinearArgs &p, const LinearPlan &plan, cudaStream_t st)
 {
     CUtensorMap maps[4];
     const int64_t tokens = p.tok.cu ? p.tok.T : p.tok.N * p.tok.T;
@@ -1066,21 +1070,18 @@ template <int DIM, int TERMS> cudaError_t launch_all(const LinearArgs &p, const 
     if (e == cudaSuccess)
         e = token_map(&maps[3], p.out, DIM, p.H, tokens, (int64_t)p.H * DIM);
     if (e == cudaSuccess && plan.groups > 1) {
-        e = launch<DIM, TERMS, true>(p, plan, plan.items_before, maps, st);
+        e = launch<DIM, true>(p, plan, plan.items_before, maps, st);
         if (e == cudaSuccess)
             e = launch_in_row(kda_linear_join_kernel, (unsigned)((int64_t)p.tok.N * p.H * (DIM * DIM / 4 / 256)), 256, 0, 1, st, p, plan);
     }
-    return e != cudaSuccess ? e : launch<DIM, TERMS, false>(p, plan, plan.items, maps, st);
+    return e != cudaSuccess ? e : launch<DIM, false>(p, plan, plan.items, maps, st);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_chunks(const LinearArgs &p, const LinearPlan &plan, cudaStream_t st)
 {
-    const bool exact = plan.state_type == KDA_DTYPE_FP32 && p.fin;
-    if (p.dim == 128)
-        return exact ? launch_all<128, 2>(p, plan, st) : launch_all<128, 1>(p, plan, st);
-    return exact ? launch_all<64, 2>(p, plan, st) : launch_all<64, 1>(p, plan, st);
+    return p.dim == 128 ? launch_all<128>(p, plan, st) : launch_all<64>(p, plan, st);
 }
 
 }  // namespace kda

@@ -15,45 +15,42 @@ namespace {
 constexpr int THREADS = 128;
 constexpr unsigned FULL = 0xffffffffu;
 
+// A 16-byte vector of the state, as pairs for the two-wide fp32 arithmetic (which halves what several tokens a state take).
 template <typename STATE> struct Vec;
 template <> struct Vec<float> {
     static constexpr int E = 4;
-    static __device__ __forceinline__ void load(const float *p, float (&x)[4])
+    static __device__ __forceinline__ void load(const float *p, f2 (&x)[2])
     {
         const float4 y = __ldcs(reinterpret_cast<const float4 *>(p));
-        x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+        x[0] = f2_pack(y.x, y.y), x[1] = f2_pack(y.z, y.w);
     }
-    static __device__ __forceinline__ void store(float *p, const float (&x)[4])
+    static __device__ __forceinline__ void store(float *p, const f2 (&x)[2])
     {
-        __stcs(reinterpret_cast<float4 *>(p), make_float4(x[0], x[1], x[2], x[3]));
+        __stcs(reinterpret_cast<float4 *>(p), make_float4(f2_lo(x[0]), f2_hi(x[0]), f2_lo(x[1]), f2_hi(x[1])));
     }
 };
 template <> struct Vec<__nv_bfloat16> {
     static constexpr int E = 8;
-    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&x)[8])
+    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, f2 (&x)[4])
     {
         const uint4 y = __ldcs(reinterpret_cast<const uint4 *>(p));
-        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            x[2 * i] = bf16_lo(w[i]), x[2 * i + 1] = bf16_hi(w[i]);
+        x[0] = f2_bf16x2(y.x), x[1] = f2_bf16x2(y.y), x[2] = f2_bf16x2(y.z), x[3] = f2_bf16x2(y.w);
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&x)[8])
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const f2 (&x)[4])
     {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            const __nv_bfloat162 y = __floats2bfloat162_rn(f2_lo(x[i]), f2_hi(x[i]));
             w[i] = *reinterpret_cast<const uint32_t *>(&y);
         }
         __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
     }
 };
 
-// E bf16 of a token's head, as floats
-template <int E> __device__ __forceinline__ void load_bf16(const __nv_bfloat16 *p, float (&x)[E])
+// E bf16 of a token's head, as words
+template <int E> __device__ __forceinline__ void load_bf16(const __nv_bfloat16 *p, uint32_t (&w)[E / 2])
 {
-    uint32_t w[E / 2];
     if constexpr (E == 4) {
         const uint2 y = *reinterpret_cast<const uint2 *>(p);
         w[0] = y.x, w[1] = y.y;
@@ -64,9 +61,6 @@ template <int E> __device__ __forceinline__ void load_bf16(const __nv_bfloat16 *
             w[4 * i] = y.x, w[4 * i + 1] = y.y, w[4 * i + 2] = y.z, w[4 * i + 3] = y.w;
         }
     }
-#pragma unroll
-    for (int i = 0; i < E / 2; i++)
-        x[2 * i] = bf16_lo(w[i]), x[2 * i + 1] = bf16_hi(w[i]);
 }
 
 // Sums of o[0..CNT) over LANES lanes: on return o[0] is the sum of row `row` (added to), the same in `LANES` lanes at the end.
@@ -103,15 +97,15 @@ __global__ void __launch_bounds__(THREADS) kda_linear_tokens_kernel(const Linear
     const int row0 = (int)(w % PARTS) * ROWS + lane / LPR * NI;
     const int64_t at = (pair * DIM + row0) * DIM + c * E;
     stream_order();
-    float s[NI][E];
+    f2 s[NI][E / 2];
 #pragma unroll
     for (int i = 0; i < NI; i++) {
         if (p.init) {
             V::load(static_cast<const STATE *>(p.init) + at + (int64_t)i * DIM, s[i]);
         } else {
 #pragma unroll
-            for (int e = 0; e < E; e++)
-                s[i][e] = 0.0f;
+            for (int e = 0; e < E / 2; e++)
+                s[i][e] = 0;
         }
     }
     bool bad = false;
@@ -119,20 +113,40 @@ __global__ void __launch_bounds__(THREADS) kda_linear_tokens_kernel(const Linear
     linear_range(p, n, bos, len, bad);
     const float fixed = p.log_decay ? p.log_decay[h] : 0.0f;
     const int hk = h / p.group;
-    for (int64_t t = bos; t < bos + len; t++) {
-        const float decay = expf(log_decay_of(p, t, h, fixed, bad));
-        float q[E], k[E], v[NI], o[NI];
+    // a token's values are read while the one before it is worked on
+    uint32_t q[E / 2], k[E / 2], v[NI / 2];
+    float a = 0.0f;
+    auto read = [&](int64_t t) {
+        a = log_decay_of(p, t, h, fixed, bad);
         load_bf16<E>(p.q + t * p.q_stride + h * DIM + c * E, q);
         load_bf16<E>(p.k + t * p.k_stride + hk * DIM + c * E, k);
         load_bf16<NI>(p.v + t * p.v_stride + hk * DIM + row0, v);
+    };
+    if (len > 0)
+        read(bos);
+    for (int64_t t = bos; t < bos + len; t++) {
+        const float decay = expf(a);
+        const f2 decay2 = f2_pack(decay, decay);
+        f2 q2[E / 2], k2[E / 2];
+        float vf[NI], o[NI];
+#pragma unroll
+        for (int e = 0; e < E / 2; e++)
+            q2[e] = f2_bf16x2(q[e]), k2[e] = f2_bf16x2(k[e]);
+#pragma unroll
+        for (int i = 0; i < NI; i += 2)
+            vf[i] = bf16_lo(v[i / 2]), vf[i + 1] = bf16_hi(v[i / 2]);
+        if (t + 1 < bos + len)
+            read(t + 1);
 #pragma unroll
         for (int i = 0; i < NI; i++) {
-            o[i] = 0.0f;
+            const f2 v2 = f2_pack(vf[i], vf[i]);
+            f2 sum = 0;
 #pragma unroll
-            for (int e = 0; e < E; e++) {
-                s[i][e] = fmaf(decay, s[i][e], v[i] * k[e]);
-                o[i] = fmaf(s[i][e], q[e], o[i]);
+            for (int e = 0; e < E / 2; e++) {
+                s[i][e] = f2_fma(decay2, s[i][e], f2_mul(v2, k2[e]));
+                sum = f2_fma(s[i][e], q2[e], sum);
             }
+            o[i] = f2_lo(sum) + f2_hi(sum);
         }
         int row = row0;
         sum_rows<NI, LPR, NI>(o, lane, row);

@@ -242,3 +242,33 @@ def test_on_a_side_stream_and_in_a_graph():
     a["uniform"].copy_(uniform)
     graph.replay()
     assert torch.equal(a["tokens"], tokens) and torch.equal(a["counts"], counts)
+
+
+def test_what_the_binding_refuses():
+    a = make(3, 2, 50, seed=15)
+    wrong = [dict(logits=a["logits"].half()), dict(logits=a["logits"][0]), dict(draft_tokens=a["draft_tokens"].long()),
+             dict(draft_tokens=a["draft_tokens"][:, :1]), dict(uniform=a["uniform"].double()), dict(noise=a["noise"][:, :49]),
+             dict(noise=a["noise"].t().contiguous().t()), dict(tokens=a["tokens"][:, :2]), dict(counts=a["counts"].long()),
+             dict(draft_probs=a["draft_probs"].bfloat16()), dict(draft_probs=a["draft_probs"][:, :1]),
+             dict(temperature=a["temperature"].double()), dict(draft_lens=torch.zeros((2,), dtype=torch.int32, device="cuda")),
+             dict(logits=a["logits"][..., ::2]), dict(noise=a["noise"].cpu()), dict(workspace=torch.zeros((4,), device="cuda"))]
+    for kw in wrong:
+        with pytest.raises((TypeError, ValueError)):
+            kda.kda_verify_drafts(**{**a, **kw})
+
+
+def test_guards_around_the_outputs():
+    a = make(7, 3, 999, seed=16)
+    tokens, counts = torch.full((9, 4), -7, dtype=torch.int32, device="cuda"), torch.full((16,), -7, dtype=torch.int32, device="cuda")
+    a["tokens"], a["counts"] = tokens[1:8], counts[4:11]
+    call(a)
+    check(a)
+    assert bool((tokens[0] == -7).all()) and bool((tokens[8] == -7).all())
+    assert bool((counts[:4] == -7).all()) and bool((counts[11:] == -7).all())
+
+
+@pytest.mark.parametrize("b", [39, 77, 153, 400])
+def test_batches_of_every_size_of_cluster(b):
+    a = make(b, 2, 2000, torch.bfloat16, greedy=0.1, lens=True, seed=b)
+    call(a)
+    check(a)
