@@ -41,7 +41,7 @@ namespace {
 constexpr int THREADS = 768;                 // six warpgroups
 constexpr int TMEM_COLS = 512;
 constexpr int TM_S1 = 0, TM_SB = 64, TM_O1 = 128, TM_O2 = 192, TM_L = 256;   // columns; two L
-constexpr int ENTRIES = 8;
+constexpr int ENTRIES = 8;                   // chunks known ahead
 constexpr int EARLY = 4;                     // chunks ahead that tiles are brought into L2
 constexpr int TILE_CB = 64 * 128;            // bytes of 64 tokens x 64 features
 constexpr unsigned FULL = 0xffffffffu;
@@ -98,19 +98,21 @@ struct alignas(16) Entry {    // one chunk; the tables are read four floats at a
 };
 static_assert(sizeof(Entry) % 16 == 0 && offsetof(Entry, lo) % 16 == 0 && offsetof(Entry, ea) % 16 == 0, "vector reads");
 
-template <int DIM> struct Shape {
+template <int DIM, bool STATES_ONLY> struct Shape {
     static constexpr int CB = DIM / 64;
     static constexpr int TILE = CB * TILE_CB;
-    static constexpr int STAGE = 3 * TILE;                    // V, Q, K (later K~'s first term)
-    static constexpr int STAGES = DIM == 64 ? 6 : 3;
-    static constexpr int KT = STAGES * STAGE;                 // K~'s other terms, of two chunks
+    static constexpr int TILES = STATES_ONLY ? 2 : 3;         // of a chunk: V, K (later K~'s first term), Q
+    static constexpr int STAGE = TILES * TILE;
+    static constexpr int STAGES = DIM == 64 ? (STATES_ONLY ? 8 : 6) : (STATES_ONLY ? 5 : 3);
+    static constexpr int KT = STAGES * STAGE;                 // K~'s other term, of two chunks
     static constexpr int P = KT + 2 * (TERMS - 1) * TILE;     // two of [64 i][64 j]
-    static constexpr int OUT = P + 2 * TILE_CB;               // O on its way out
-    static constexpr int ZERO = OUT + TILE;                   // D = 64: lanes 64 to 127
+    static constexpr int OUT = P + (STATES_ONLY ? 0 : 2 * TILE_CB);    // O on its way out
+    static constexpr int ZERO = OUT + (STATES_ONLY ? 0 : TILE);        // D = 64: lanes 64 to 127
     static constexpr int ENTRY = ZERO + (DIM == 64 ? TILE_CB : 0);
     static constexpr int BAR = ENTRY + ENTRIES * (int)sizeof(Entry);
     static constexpr int SMEM = 1024 + BAR + 512;
     static_assert(SMEM <= 232448, "a CTA's shared memory");
+    static_assert(ENTRIES >= STAGES + 2 || STATES_ONLY, "chunks under way");
     static_assert(ENTRY % 16 == 0 && BAR % 8 == 0 && P % 1024 == 0 && KT % 1024 == 0 && ZERO % 1024 == 0, "alignment");
 };
 
@@ -340,7 +342,7 @@ __device__ __forceinline__ uint32_t seen_pair(int gap)
     return x;
 }
 // Registers of a warpgroup's threads from here on.  The kernel starts with 80 a thread, and the six shares add up to six times that.
-constexpr int REGS_O = 88, REGS_K = 64, REGS_S = 104, REGS_P = 64, REGS_X = 56;
+constexpr int REGS_O = 88, REGS_K = 64, REGS_S = 104, REGS_P = REGS_K, REGS_X = 56;
 static_assert(REGS_O + REGS_K + 2 * REGS_S + REGS_P + REGS_X <= 6 * 80, "more than the block was launched with");
 template <int N, bool MORE> __device__ __forceinline__ void set_registers()
 {
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan plan, const __grid_constant__ CUtensorMap qmap,
                          const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap)
 {
-    using S = Shape<DIM>;
+    using S = Shape<DIM, STATES_ONLY>;
     constexpr int CB = S::CB, STAGES = S::STAGES;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -387,7 +389,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
             mbar_init(b_drain + 8 * i, 1);
             mbar_init(b_sb + 8 * i, 8);
             mbar_init(b_pe + 8 * i, 4);
-            mbar_init(b_k + 8 * i, 4);
+            mbar_init(b_k + 8 * i, STATES_ONLY ? 8 : 4);
             mbar_init(b_l + 8 * i, 1);
             mbar_init(b_l_free + 8 * i, 8);
         }
@@ -401,7 +403,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                      "r"(TMEM_COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    for (int i = tid; i < 2 * TILE_CB / 16; i += THREADS)
+    for (int i = tid; i < (STATES_ONLY ? 0 : 2 * TILE_CB / 16); i += THREADS)
         reinterpret_cast<uint4 *>(smem + S::P)[i] = make_uint4(0, 0, 0, 0);
     if (DIM == 64)
         for (int i = tid; i < TILE_CB / 16; i += THREADS)
@@ -440,7 +442,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
             // a later chunk's tiles, into L2 if it is known by now: they are copied from there in a fraction of the time
             const uint32_t later = (c + EARLY) % ENTRIES;
             if (__all_sync(FULL, mbar_test(b_ent + 8 * later, (c + EARLY) / ENTRIES & 1)) && entries[later].valid &&
-                lane < (STATES_ONLY ? 2 : 3) * CB) {
+                lane < S::TILES * CB) {
                 const Entry &f = entries[later];
                 const int cb = lane % CB, which = lane / CB;
                 prefetch_3d(which == 0 ? &kmap : (which == 1 ? &vmap : &qmap), 64 * cb, which == 2 ? f.h : f.h / p.group, f.tok0);
@@ -449,13 +451,13 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                 break;
             if (lane == 0) {
                 const uint32_t to = base + st * S::STAGE, b = b_full + 8 * st;
-                mbar_expect_tx(b, (STATES_ONLY ? 2 : 3) * S::TILE);
+                mbar_expect_tx(b, S::STAGE);
 #pragma unroll
                 for (int cb = 0; cb < CB; cb++) {
-                    tma_load_3d(to + 2 * S::TILE + cb * TILE_CB, &kmap, 64 * cb, h / p.group, tok, b);
+                    tma_load_3d(to + S::TILE + cb * TILE_CB, &kmap, 64 * cb, h / p.group, tok, b);
                     tma_load_3d(to + cb * TILE_CB, &vmap, 64 * cb, h / p.group, tok, b);
                     if (!STATES_ONLY)
-                        tma_load_3d(to + S::TILE + cb * TILE_CB, &qmap, 64 * cb, h, tok, b);
+                        tma_load_3d(to + 2 * S::TILE + cb * TILE_CB, &qmap, 64 * cb, h, tok, b);
                 }
             }
             arrive(b_ent_free + 8 * (c % ENTRIES));
@@ -477,7 +479,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                     if (!wait(b_full + 8 * (c % STAGES), c / STAGES) || (c > 0 && !wait(b_p + 8 * ((c - 1) & 1), (c - 1) >> 1)))
                         break;
                     tc_fence_after();
-                    const uint32_t a = desc_lo(at + S::TILE, 16), b = desc_lo(at + 2 * S::TILE, 16), d = tm + TM_S1;
+                    const uint32_t a = desc_lo(at + 2 * S::TILE, 16), b = desc_lo(at + S::TILE, 16), d = tm + TM_S1;
                     if (lead && !timeout) {
 #pragma unroll
                         for (int k = 0; k < DIM / 16; k++) {
@@ -507,7 +509,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                 if (lead && !timeout) {
 #pragma unroll
                     for (int r = TERMS - 1; r >= 0; r--) {     // small terms first
-                        const uint32_t b = desc_lo(r == 0 ? at + 2 * S::TILE : base + S::KT + ((c & 1) * (TERMS - 1) + r - 1) * S::TILE, TILE_CB);
+                        const uint32_t b = desc_lo(r == 0 ? at + S::TILE : base + S::KT + ((c & 1) * (TERMS - 1) + r - 1) * S::TILE, TILE_CB);
 #pragma unroll
                         for (int k = 0; k < 4; k++) {
                             if (r == TERMS - 1 && k == 0)
@@ -525,7 +527,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                     if (!wait(b_sb + 8 * (c & 1), c >> 1) || (c > 0 && !wait(b_o_free, c - 1)))
                         break;
                     tc_fence_after();
-                    const uint32_t q = desc_lo(at + S::TILE, 16), sb = tm + TM_SB;
+                    const uint32_t q = desc_lo(at + 2 * S::TILE, 16), sb = tm + TM_SB;
                     if (lead && !timeout) {
 #pragma unroll
                         for (int k = 0; k < DIM / 16; k++) {
@@ -705,7 +707,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
         if (asked > answers)
             timeout |= !mbar_wait(b_block, answers & 1);
       }
-    } else if (warp < 8) {
+    } else if (!STATES_ONLY && warp < 8) {
         // ------------------------------------------------------------ P, 16 tokens a warp
         // In blocks of 16 x 16: a thread has two neighbouring columns of rows t / 4 and t / 4 + 8, twice.  Blocks of later tokens are
         // zeros from the start.
@@ -717,7 +719,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
         const uint32_t to = base + S::P + row * 128;
         for (uint32_t c = 0; next(c); c++) {
             const Entry &e = entries[c % ENTRIES];
-            if (!STATES_ONLY) {
+            {
                 const float h0 = e.hi[r0], l0 = e.lo[r0], h1 = e.hi[r0 + 8], l1 = e.lo[r0 + 8];
                 if (!wait(b_s + 8 * (c & 1), c >> 1) || (c >= 2 && !wait(b_pe + 8 * (c & 1), (c >> 1) - 1)))
                     break;
@@ -755,8 +757,10 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
         }
     } else if (warp < 12) {
         // ------------------------------------------------------------ K~
+        // (where only states are wanted the warps of P take half of it: it is what bounds a chunk there)
         set_registers<REGS_K, false>();
-        const int t = tid - 256;
+        constexpr int THREADS_K = STATES_ONLY ? 256 : 128;
+        const int t = tid - (384 - THREADS_K);
         for (uint32_t c = 0; next(c); c++) {
             const Entry &e = entries[c % ENTRIES];
             const int st = c % STAGES, len = e.len;
@@ -764,11 +768,11 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
             if (!wait(b_full + 8 * st, c / STAGES) || (!STATES_ONLY && !wait(b_s + 8 * (c & 1), c >> 1)) ||
                 (c >= 2 && !wait(b_l + 8 * (c & 1), (c >> 1) - 1)))
                 break;
-            constexpr int VECS = 64 * DIM / 8 / 128;           // 16-byte vectors of a thread, ROWS tokens apart
-            constexpr int ROWS = 128 / (DIM / 8);
+            constexpr int VECS = 64 * DIM / 8 / THREADS_K;     // 16-byte vectors of a thread, ROWS tokens apart
+            constexpr int ROWS = THREADS_K / (DIM / 8);
             const int ch = t % (DIM / 8), j0 = t / (DIM / 8);  // (ROWS is a multiple of 8: the swizzle is the same for all)
             const int at = (ch / 8) * TILE_CB + j0 * 128 + (((ch % 8) ^ (j0 & 7)) << 4);
-            unsigned char *const kt = smem + st * S::STAGE + 2 * S::TILE + at;
+            unsigned char *const kt = smem + st * S::STAGE + S::TILE + at;
             unsigned char *const to = smem + S::KT + (c & 1) * (TERMS - 1) * S::TILE + at;
 #pragma unroll
             for (int m = 0; m < VECS; m++) {
@@ -792,7 +796,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
             }
             if (len < 64) {                                    // what lies behind the sequence is cleared from V
                 unsigned char *vt = smem + st * S::STAGE;
-                for (int i = t; i < (64 - len) * 8 * CB; i += 128)
+                for (int i = t; i < (64 - len) * 8 * CB; i += THREADS_K)
                     *reinterpret_cast<uint4 *>(vt + i / ((64 - len) * 8) * TILE_CB + len * 128 + i % ((64 - len) * 8) * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_async_smem();
@@ -1011,15 +1015,26 @@ __global__ void __launch_bounds__(256) kda_linear_join_kernel(const LinearArgs p
         }
     }
     const int64_t first = slot_of(p, plan, n, bos, 0);
-#pragma unroll 4
-    for (int g = 0; g < groups; g++) {
-        const int64_t slot = (first + g) * p.H + h;
-        const float2 f = plan.decays[slot];
-        const Decay d{f.x, f.y != 0.0f};
-        float4 *y = reinterpret_cast<float4 *>(plan.states + slot * size + at);
-        const float4 l = *y;
-        s[0] = decayed(d, s[0], l.x), s[1] = decayed(d, s[1], l.y), s[2] = decayed(d, s[2], l.z), s[3] = decayed(d, s[3], l.w);
-        *y = make_float4(s[0], s[1], s[2], s[3]);
+    // (eight groups' loads before their stores, which the compiler could not tell apart: one group after the other took 13 us for 18
+    // groups of 8 heads, XX this way)
+    constexpr int AT_ONCE = 8;
+    for (int first_g = 0; first_g < groups; first_g += AT_ONCE) {
+        float4 l[AT_ONCE];
+        float2 f[AT_ONCE];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; i++)
+            if (first_g + i < groups) {
+                const int64_t slot = (first + first_g + i) * p.H + h;
+                f[i] = plan.decays[slot];
+                l[i] = *reinterpret_cast<const float4 *>(plan.states + slot * size + at);
+            }
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; i++)
+            if (first_g + i < groups) {
+                const Decay d{f[i].x, f[i].y != 0.0f};
+                s[0] = decayed(d, s[0], l[i].x), s[1] = decayed(d, s[1], l[i].y), s[2] = decayed(d, s[2], l[i].z), s[3] = decayed(d, s[3], l[i].w);
+                *reinterpret_cast<float4 *>(plan.states + ((first + first_g + i) * p.H + h) * size + at) = make_float4(s[0], s[1], s[2], s[3]);
+            }
     }
 }
 
@@ -1048,13 +1063,13 @@ cudaError_t launch(const LinearArgs &p, const LinearPlan &plan, int64_t items, c
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && !(ready.load() >> dev & 1)) {
         e = cudaFuncSetAttribute(kda_linear_chunks_kernel<DIM, STATES_ONLY>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Shape<DIM>::SMEM);
+                                 Shape<DIM, STATES_ONLY>::SMEM);
         if (e == cudaSuccess)
             ready.fetch_or(1ull << dev);
     }
     if (e != cudaSuccess)
         return e;
-    return launch_in_row(kda_linear_chunks_kernel<DIM, STATES_ONLY>, (unsigned)items, THREADS, Shape<DIM>::SMEM, 1, st, p,
+    return launch_in_row(kda_linear_chunks_kernel<DIM, STATES_ONLY>, (unsigned)items, THREADS, Shape<DIM, STATES_ONLY>::SMEM, 1, st, p,
                          plan, maps[0], maps[1], maps[2], maps[3]);
 }
 
