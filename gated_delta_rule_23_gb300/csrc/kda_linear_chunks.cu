@@ -366,7 +366,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
     const uint32_t bar = base + S::BAR;
     const uint32_t b_full = bar, b_empty = b_full + 8 * STAGES, b_ent = b_empty + 8 * STAGES, b_ent_free = b_ent + 8 * ENTRIES,
                    b_s = b_ent_free + 8 * ENTRIES, b_p = b_s + 16, b_o = b_p + 16, b_sb = b_o + 16, b_pe = b_sb + 16,
-                   b_k = b_pe + 16, b_l = b_k + 16, b_l_free = b_l + 16, b_o2 = b_l_free + 16, b_o_free = b_o2 + 8, b_block = b_o_free + 8, b_drain = b_block + 8;
+                   b_k = b_pe + 16, b_l = b_k + 16, b_o2 = b_l + 16, b_block = b_o2 + 8, b_drain = b_block + 8;
     static_assert(8 * (2 * STAGES + 2 * ENTRIES + 21) <= 512, "barriers");
     __shared__ uint32_t tmem_slot;
     __shared__ uint4 block_answer;
@@ -387,14 +387,12 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
             mbar_init(b_p + 8 * i, 4);
             mbar_init(b_o + 8 * i, 1);
             mbar_init(b_drain + 8 * i, 1);
-            mbar_init(b_sb + 8 * i, 8);
+            mbar_init(b_sb + 8 * i, 12);                       // S stored; O before it read
             mbar_init(b_pe + 8 * i, 4);
-            mbar_init(b_k + 8 * i, STATES_ONLY ? 8 : 4);
+            mbar_init(b_k + 8 * i, STATES_ONLY ? 16 : 12);     // K~ stored; L two chunks before read
             mbar_init(b_l + 8 * i, 1);
-            mbar_init(b_l_free + 8 * i, 8);
         }
         mbar_init(b_o2, 1);
-        mbar_init(b_o_free, 4);
         mbar_init(b_block, 1);
         mbar_fence_init();
     }
@@ -501,8 +499,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                 const uint32_t at = base + st * S::STAGE;
                 // V as M rows: blocks of 64 features, for D = 64 the second one zeros
                 const uint32_t v = desc_lo(at, DIM == 128 ? TILE_CB : S::ZERO - st * S::STAGE);
-                if (!wait(b_full + 8 * st, c / STAGES) || !wait(b_k + 8 * (c & 1), c >> 1) ||
-                    (c >= 2 && !wait(b_l_free + 8 * (c & 1), (c >> 1) - 1)))
+                if (!wait(b_k + 8 * (c & 1), c >> 1))          // K~ is there, and the place for the product
                     break;
                 tc_fence_after();
                 const uint32_t d = tm + TM_L + 128 * (c & 1);
@@ -524,7 +521,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                 }
                 __syncwarp();
                 if (!STATES_ONLY) {
-                    if (!wait(b_sb + 8 * (c & 1), c >> 1) || (c > 0 && !wait(b_o_free, c - 1)))
+                    if (!wait(b_sb + 8 * (c & 1), c >> 1))     // S is there, and O of the chunk before is read
                         break;
                     tc_fence_after();
                     const uint32_t q = desc_lo(at + 2 * S::TILE, 16), sb = tm + TM_SB;
@@ -764,8 +761,9 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
         for (uint32_t c = 0; next(c); c++) {
             const Entry &e = entries[c % ENTRIES];
             const int st = c % STAGES, len = e.len;
-            // K is there and its scores are through, and so are the products with what lies in this chunk's other terms
-            if (!wait(b_full + 8 * st, c / STAGES) || (!STATES_ONLY && !wait(b_s + 8 * (c & 1), c >> 1)) ||
+            // K is there and its scores are through, and so is the product of the chunk before the last: its other term lies where this
+            // one's will, and its barrier is this one's
+            if (!(STATES_ONLY ? wait(b_full + 8 * st, c / STAGES) : wait(b_s + 8 * (c & 1), c >> 1)) ||
                 (c >= 2 && !wait(b_l + 8 * (c & 1), (c >> 1) - 1)))
                 break;
             constexpr int VECS = 64 * DIM / 8 / THREADS_K;     // 16-byte vectors of a thread, ROWS tokens apart
@@ -816,6 +814,8 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
 #pragma unroll
         for (int i = 0; i < COLS / 2; i++)
             s[i] = 0;
+        if (lane == 0)
+            mbar_arrive(b_k), mbar_arrive(b_k + 8);            // both L are free
         // S before chunk c, as the operand of its product
         auto put = [&](uint32_t c) -> bool {
             if (STATES_ONLY)
@@ -873,7 +873,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                 }
                 tc_fence_before();
             }
-            arrive(b_l_free + 8 * (c & 1));
+            arrive(b_k + 8 * (c & 1));                         // for the chunk after the next
             if (!e.last) {
                 if (!put(c + 1))
                     break;
@@ -892,6 +892,8 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
         // where this lane's row of a piece's four 8 x 8 blocks goes: token (lane & 7) of 8, 8 features
         const int r = lane & 7, block = lane >> 3;
         const uint32_t to = base + S::OUT + (ow >> 1) * TILE_CB + ((block >> 1) * 8 + r) * 128;
+        if (lane == 0)
+            mbar_arrive(b_sb);                                 // O is free
         const uint32_t to0 = to + ((((ow & 1) * 4 + (block & 1)) ^ r) << 4), to1 = to + ((((ow & 1) * 4 + 2 + (block & 1)) ^ r) << 4);
         for (uint32_t c = 0; next(c); c++) {
             const Entry &e = entries[c % ENTRIES];
@@ -952,7 +954,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                     }
                     tc_fence_before();
                     fence_async_smem();
-                    arrive(b_o_free);
+                    arrive(b_sb + 8 * ((c + 1) & 1));          // for the next chunk
                     arrive(b_pe + 8 * (c & 1));
                     out_sync<32 * WARPS>();
                     if (len == 64) {
@@ -970,7 +972,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                         }
                     }
                 } else {
-                    arrive(b_o_free);
+                    arrive(b_sb + 8 * ((c + 1) & 1));          // for the next chunk
                     arrive(b_pe + 8 * (c & 1));
                 }
             }
