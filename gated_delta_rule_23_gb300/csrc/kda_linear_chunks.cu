@@ -494,7 +494,8 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
             }
         } else {
             const uint32_t id_l = idesc_bf16(128, DIM, true) | A_MN, id_o2 = idesc_bf16(128, 64, false), id_o1 = id_o2 | A_MN;
-            for (uint32_t c = 0; next(c); c++) {
+            bool more = next(0);
+            for (uint32_t c = 0; more; c++) {
                 const int st = c % STAGES;
                 const uint32_t at = base + st * S::STAGE;
                 // V as M rows: blocks of 64 features, for D = 64 the second one zeros
@@ -520,8 +521,11 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                         umma_commit(b_empty + 8 * st);
                 }
                 __syncwarp();
+                // (a wait takes some 200 cycles even where nothing is waited for: these are over while that product runs)
+                more = next(c + 1);
                 if (!STATES_ONLY) {
-                    if (!wait(b_sb + 8 * (c & 1), c >> 1))     // S is there, and O of the chunk before is read
+                    // P is there, and S, and O of the chunk before is read
+                    if (!wait(b_p + 8 * (c & 1), c >> 1) || !wait(b_sb + 8 * (c & 1), c >> 1))
                         break;
                     tc_fence_after();
                     const uint32_t q = desc_lo(at + 2 * S::TILE, 16), sb = tm + TM_SB;
@@ -535,13 +539,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                                 mma_ts<true>(tm + TM_O2, sb + 8 * k, q + step, id_o2, 1);
                         }
                         umma_commit(b_o2);
-                    }
-                    __syncwarp();
-                    if (!wait(b_p + 8 * (c & 1), c >> 1))
-                        break;
-                    tc_fence_after();
-                    const uint32_t pd = desc_lo(base + S::P + (c & 1) * TILE_CB, 16);
-                    if (lead && !timeout) {
+                        const uint32_t pd = desc_lo(base + S::P + (c & 1) * TILE_CB, 16);
 #pragma unroll
                         for (int k = 0; k < 4; k++) {
                             if (k == 0)
