@@ -41,7 +41,7 @@ namespace {
 constexpr int THREADS = 768;                 // six warpgroups
 constexpr int TMEM_COLS = 512;
 constexpr int TM_S1 = 0, TM_SB = 64, TM_O1 = 128, TM_O2 = 192, TM_L = 256;   // columns; two L
-constexpr int ENTRIES = 8;                   // chunks known ahead
+constexpr int ENTRIES = 6;                   // chunks known ahead (8: 2 us more for ragged prompts, whose last items are taken too early)
 constexpr int EARLY = 4;                     // chunks ahead that tiles are brought into L2
 constexpr int TILE_CB = 64 * 128;            // bytes of 64 tokens x 64 features
 constexpr unsigned FULL = 0xffffffffu;
@@ -112,7 +112,6 @@ template <int DIM, bool STATES_ONLY> struct Shape {
     static constexpr int BAR = ENTRY + ENTRIES * (int)sizeof(Entry);
     static constexpr int SMEM = 1024 + BAR + 512;
     static_assert(SMEM <= 232448, "a CTA's shared memory");
-    static_assert(ENTRIES >= STAGES + 2 || STATES_ONLY, "chunks under way");
     static_assert(ENTRY % 16 == 0 && BAR % 8 == 0 && P % 1024 == 0 && KT % 1024 == 0 && ZERO % 1024 == 0, "alignment");
 };
 
@@ -716,7 +715,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
             const Entry &e = entries[c % ENTRIES];
             {
                 const float h0 = e.hi[r0], l0 = e.lo[r0], h1 = e.hi[r0 + 8], l1 = e.lo[r0 + 8];
-                if (!wait(b_s + 8 * (c & 1), c >> 1) || (c >= 2 && !wait(b_pe + 8 * (c & 1), (c >> 1) - 1)))
+                if ((c >= 2 && !wait(b_pe + 8 * (c & 1), (c >> 1) - 1)) || !wait(b_s + 8 * (c & 1), c >> 1))
                     break;
                 tc_fence_after();
                 const uint32_t tm = tmem + TM_S1 + ((uint32_t)wp << 21), pt = to + (c & 1) * TILE_CB;
@@ -761,8 +760,8 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
             const int st = c % STAGES, len = e.len;
             // K is there and its scores are through, and so is the product of the chunk before the last: its other term lies where this
             // one's will, and its barrier is this one's
-            if (!(STATES_ONLY ? wait(b_full + 8 * st, c / STAGES) : wait(b_s + 8 * (c & 1), c >> 1)) ||
-                (c >= 2 && !wait(b_l + 8 * (c & 1), (c >> 1) - 1)))
+            if ((c >= 2 && !wait(b_l + 8 * (c & 1), (c >> 1) - 1)) ||
+                !(STATES_ONLY ? wait(b_full + 8 * st, c / STAGES) : wait(b_s + 8 * (c & 1), c >> 1)))
                 break;
             constexpr int VECS = 64 * DIM / 8 / THREADS_K;     // 16-byte vectors of a thread, ROWS tokens apart
             constexpr int ROWS = THREADS_K / (DIM / 8);
@@ -1016,7 +1015,7 @@ __global__ void __launch_bounds__(256) kda_linear_join_kernel(const LinearArgs p
     }
     const int64_t first = slot_of(p, plan, n, bos, 0);
     // (eight groups' loads before their stores, which the compiler could not tell apart: one group after the other took 13 us for 18
-    // groups of 8 heads, XX this way)
+    // groups of 8 heads, 8.5 this way)
     constexpr int AT_ONCE = 8;
     for (int first_g = 0; first_g < groups; first_g += AT_ONCE) {
         float4 l[AT_ONCE];
