@@ -145,6 +145,14 @@ __device__ __forceinline__ bool find_item(const LinearArgs &p, const LinearPlan 
         linear_range(p, w.n, w.bos, w.len, bad);
         return w.g < groups_of(plan, w.len, STATES_ONLY);
     }
+    if (plan.groups == 1) {                                    // every sequence is one item
+        if (y >= p.tok.N)
+            return false;
+        w.n = order ? order[y] : y;
+        w.g = 0;
+        bad |= seq_range(p.tok.cu, w.n, p.tok.N, p.tok.T, w.bos, w.len);
+        return true;
+    }
     int before = 0;
     for (int base = 0; base < p.tok.N; base += 32) {
         const int i = base + lane;
@@ -607,10 +615,14 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                 continue;
             const int64_t chunks = (w.len + 63) / 64, c0 = (int64_t)w.g * plan.group_chunks;
             const int64_t c1 = c0 + plan.group_chunks < chunks ? c0 + plan.group_chunks : chunks;
-            const int src = w.g > 0 && !STATES_ONLY ? 2 : (!STATES_ONLY && p.init ? 1 : 0);
+            // The first group's state is read from where the join has put it too: the last group, which writes the final state, perhaps
+            // in the same place, does not wait for it.
+            const int last_group = groups_of(plan, w.len, true);
+            const bool from_slot = !STATES_ONLY && (w.g > 0 || (last_group > 0 && p.init));
+            const int src = from_slot ? 2 : (!STATES_ONLY && p.init ? 1 : 0);
             const int dst = STATES_ONLY ? 2 : (c1 == chunks && p.fin ? 1 : 0);
             const int64_t pair = (int64_t)w.n * p.H + w.h;
-            const int64_t at_src = src == 2 ? slot_of(p, plan, w.n, w.bos, w.g - 1) * p.H + w.h : pair;
+            const int64_t at_src = src == 2 ? slot_of(p, plan, w.n, w.bos, w.g > 0 ? w.g - 1 : last_group) * p.H + w.h : pair;
             const int64_t at_dst = STATES_ONLY ? slot_of(p, plan, w.n, w.bos, w.g) * p.H + w.h : pair;
             // the state that the item starts from, into L2
             if (src != 0 && lane == 0) {
@@ -988,6 +1000,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
 
 // ---------------------------------------------------------------- groups' start states
 // S_0 the call's; what group g adds lies in its slot and is replaced by S_(g+1) = e^(A_g) S_g + it, the state that group g + 1 starts from.
+// The last group's slot, which no later group starts from, gets S_0.
 // Four elements a thread, the groups in turn.
 __global__ void __launch_bounds__(256) kda_linear_join_kernel(const LinearArgs p, const LinearPlan plan)
 {
@@ -1014,6 +1027,8 @@ __global__ void __launch_bounds__(256) kda_linear_join_kernel(const LinearArgs p
         }
     }
     const int64_t first = slot_of(p, plan, n, bos, 0);
+    if (p.init)                                                // the first group's own start, in the last one's slot
+        *reinterpret_cast<float4 *>(plan.states + ((first + groups) * p.H + h) * size + at) = make_float4(s[0], s[1], s[2], s[3]);
     // (eight groups' loads before their stores, which the compiler could not tell apart: one group after the other took 13 us for 18
     // groups of 8 heads, 8.5 this way)
     constexpr int AT_ONCE = 8;

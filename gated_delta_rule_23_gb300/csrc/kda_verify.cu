@@ -217,8 +217,7 @@ template <typename T, int VECS> __global__ void __launch_bounds__(THREADS, 8) kd
         p.stats[(int64_t)row * p.chunks + c] = make_float2(m, s);
 }
 
-// exp(d / tau) for d <= 0: the exponent in base 2 as two terms, so that its rounding does not grow with it.  NaN for -inf and NaN,
-// which win no race.
+// exp(d / tau) for d <= 0: the exponent in base 2 as two terms, so that its rounding does not grow with it.  0 for NaN.
 struct Exponent {
     float hi, lo;                       // log2(e) / tau
 };
@@ -232,7 +231,7 @@ __device__ __forceinline__ float weight_of(float d, const Exponent &f)
 {
     constexpr float LN2 = 0.6931471805599453f;
     const float t = d * f.hi, r = fmaf(d, f.lo, fmaf(d, f.hi, -t)), y = ex2_approx(t);
-    return fmaf(y, r * LN2, y);
+    return t > -150.0f ? fmaf(y, r * LN2, y) : 0.0f;       // (below that nothing is left, and r is none for -inf)
 }
 
 __device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank)

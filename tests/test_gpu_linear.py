@@ -442,3 +442,26 @@ def test_what_the_binding_refuses():
     with pytest.raises(KDAError):
         same = a["q"].contiguous()
         kda.kda_linear_attn(**{**a, "out": same, "q": same})
+
+
+@pytest.mark.parametrize("state", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("layout,lengths", [("batch", [2500]), ("cu", [2000, 70, 0]), ("cu", [1985]), ("lens", [2113, 1])])
+def test_state_in_place_with_groups(state, layout, lengths):
+    """Groups of a sequence run side by side; the last one may end before the first one begins."""
+    a = make(lengths, 2, 2, 128, layout, seed=30, state=state)
+    b = make(lengths, 2, 2, 128, layout, seed=30, state=state)
+    for x in (a, b):
+        x["log_decay"] *= 0.001
+        x["gate"] *= 0.002
+    start = a["initial_state"].clone()
+    a["final_state"] = a["initial_state"]
+    out, fin = call(a)
+    check(a, out, fin, start=start)
+    out2, fin2 = call(b)
+    assert torch.equal(out, out2) and torch.equal(fin, fin2)
+
+
+def test_a_thousand_sequences():
+    r = [(i * 29) % 41 for i in range(1000)]
+    a = make(r, 1, 1, 64, "cu", seed=31)
+    check(a, *call(a))

@@ -272,3 +272,19 @@ def test_batches_of_every_size_of_cluster(b):
     a = make(b, 2, 2000, torch.bfloat16, greedy=0.1, lens=True, seed=b)
     call(a)
     check(a)
+
+
+@pytest.mark.parametrize("tau", [1e-45, 1e-38, 1e-30, 1e-3, 1e30])
+def test_extreme_temperatures_over_many_chunks(tau):
+    """Exponents past fp32's range between the chunks of a row: what is far from the maximum has no weight, and no NaN comes of it."""
+    a = make(4, 2, 70001, torch.bfloat16, seed=17)
+    a["temperature"].fill_(tau)
+    a["logits"][:, :, 60000] = 40.0
+    a["draft_tokens"][:, 0] = 60000
+    tokens, counts = call(a)
+    if tau < 1.0:
+        a["draft_probs"][:] = 0.0
+        a["draft_probs"][:, :, 60000] = 1.0
+        tokens, counts = call(a)
+        assert bool((tokens[:, 0] == 60000).all())
+    assert bool((tokens.gather(1, counts.long()[:, None] - 1) >= 0).all())
