@@ -11,18 +11,19 @@ namespace kda {
 // 37 | 45; 64 x 64, 8 tokens 109 | 101, 12 110 | 144; 32 x 32 of 64, 16 tokens 26 | 16.  With cu_seqlens only the sum is known here.
 static bool token_by_token(int N, int64_t T, int H, int D) { return T <= (D == 64 ? 16 : ((int64_t)N * H <= 1024 ? 14 : 8)); }
 
-// The cut of a call into groups (sizes only, so that the workspace is known beforehand), for 152 SMs.  Measured: a chunk takes 1.4 us in
-// a (sequence, head)'s chain, however few run; groups cost a pass over K and V (1.1 us a chunk) and two launches.  8192 tokens,
-// one chain | groups: 8 heads 183 | 47 us, 32 heads 185 | 101, 64 heads 186 | 177; 1024 tokens of 8 heads 29 | 27, 512 19 | 26.
+// The cut of a call into groups (sizes only, so that the workspace is known beforehand), for 152 SMs.  Costs in 10 ns, fitted to what
+// was measured: a chunk takes 1.3 us in a (sequence, head)'s chain, however few run; with groups 2.4 us, the pass over K and V
+// included, and two launches more.  One chain | groups (us): 8192 tokens of 8 heads 175 | 44, 32 heads 176 | 96, 64 heads over 8 174 | 165
+// (a gate per token: 175 | 171), 76 heads 176 | 178; 1024 tokens of 8 heads 29 | 26, 32 heads 29 | 31, 2048 of 48 51 | 49.
 static LinearPlan make_plan(bool varlen, int N, int64_t T, int H)
 {
     LinearPlan plan{};
     const int64_t chunks = (T + 63) / 64, pairs = (int64_t)N * H;
     // the longest sequence; of a ragged batch only the sum is known, and twice the mean is taken for it
     const int64_t chain = varlen && N > 1 ? std::min(chunks, 2 * ((chunks + N - 1) / N)) : chunks;
-    int64_t cut = 1, best = 143 * chain;
+    int64_t cut = 1, best = 700 + 132 * chain;
     for (int64_t g = 2; g * pairs <= 152 && g <= chain; g++) {
-        const int64_t cost = (800 + 250 * ((chain + g - 1) / g) + 30 * g) * 21 / 20;
+        const int64_t cost = 1850 + 240 * ((chain + g - 1) / g) + 30 * g;
         if (cost < best)
             best = cost, cut = g;
     }

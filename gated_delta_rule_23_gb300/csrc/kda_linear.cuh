@@ -24,17 +24,16 @@ struct LinearArgs {
 constexpr float MIN_LOG_DECAY = -200.0f;
 
 // The logarithm of a token's decay for a head: at most 0 (a positive one is reported and taken as 0), NaN as it is.
-__device__ __forceinline__ float log_decay_of(const LinearArgs &p, int64_t token, int h, float fixed, bool &bad)
+__device__ __forceinline__ float log_decay_of(float fixed, float gate, bool &bad)
 {
-    float a = fixed;
-    if (p.gate)
-        a += p.gate[token * p.H + h];
+    float a = fixed + gate;
     if (a > 0.0f) {
         bad = true;
         a = 0.0f;
     }
     return a < MIN_LOG_DECAY ? MIN_LOG_DECAY : a;
 }
+__device__ __forceinline__ float gate_of(const LinearArgs &p, int64_t token, int h) { return p.gate ? p.gate[token * p.H + h] : 0.0f; }
 
 // First token and length of sequence n.
 __device__ __forceinline__ void linear_range(const LinearArgs &p, int n, int64_t &bos, int64_t &len, bool &bad)

@@ -631,7 +631,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                              at_src * DIM * DIM * size), "r"(DIM * DIM * size) : "memory");
             }
             const float fixed = p.log_decay ? p.log_decay[w.h] : 0.0f;
-            auto gate = [&](int64_t i) -> float { return i < w.len ? log_decay_of(p, w.bos + i, w.h, fixed, bad) : 0.0f; };
+            auto gate = [&](int64_t i) -> float { return i < w.len ? gate_of(p, w.bos + i, w.h) : 0.0f; };
             // Two chunks at a time, one by lanes 0..15 and one by the others, four tokens a lane.
             const int half = lane >> 4, j = 4 * (lane & 15);
             Sum total{0.0f, 0.0f};
@@ -642,11 +642,12 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
             for (int64_t i0 = c0; i0 < c1 || i0 == c0; i0 += 2) {   // (an empty sequence has one chunk of no tokens)
                 const int64_t i = i0 + half;
                 Sum a[4];
-                a[0] = in_base_2(g[0]);
 #pragma unroll
-                for (int q = 1; q < 4; q++)
-                    a[q] = add(a[q - 1], in_base_2(g[q]));
-                if (i0 + 2 < c1) {
+                for (int q = 0; q < 4; q++) {
+                    const Sum x = in_base_2(i * 64 + j + q < w.len ? log_decay_of(fixed, g[q], bad) : 0.0f);
+                    a[q] = q > 0 ? add(a[q > 0 ? q - 1 : 0], x) : x;
+                }
+                if (i0 + 2 < c1) {                             // loaded now and looked at in the next pass
 #pragma unroll
                     for (int q = 0; q < 4; q++)
                         g[q] = gate((i + 2) * 64 + j + q);

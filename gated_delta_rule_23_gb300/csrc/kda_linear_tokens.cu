@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(THREADS) kda_linear_tokens_kernel(const Linear
     uint32_t q[E / 2], k[E / 2], v[NI / 2];
     float a = 0.0f;
     auto read = [&](int64_t t) {
-        a = log_decay_of(p, t, h, fixed, bad);
+        a = log_decay_of(fixed, gate_of(p, t, h), bad);
         load_bf16<E>(p.q + t * p.q_stride + h * DIM + c * E, q);
         load_bf16<E>(p.k + t * p.k_stride + hk * DIM + c * E, k);
         load_bf16<NI>(p.v + t * p.v_stride + hk * DIM + row0, v);
