@@ -15,13 +15,21 @@
 // S + (expm1(A_C) S + L): a factor next to 1 that is off by half a step in every chunk would drift by 2^-25 a chunk; strong ones as
 // e^(A_C) S + L, so that nothing of a state that is forgotten stays behind as rounding.
 // K~ = e^(A_C - A_j) K is not a bf16 number: two bf16 terms that add up to it (to 2^-17) are multiplied with V one after the other.  With
-// one, outputs after bf16 states were 2.6e-3 off (norm) and not 2.3e-3, 1.7e-3 of it their own rounding, and a prompt of 8192 tokens, 96
-// heads took 205 us for 211: what the tensor cores do is not what bounds a chunk.
+// one, outputs after bf16 states were 2.6e-3 off (norm) and not 2.3e-3, 1.7e-3 of it their own rounding, and a prompt took 3% less:
+// what the tensor cores do is not what bounds a chunk.  fp32 states come out 2.7e-6 off.  The other roundings to bf16 are P's, and that of
+// the state that a chunk's queries read (outputs are bf16, rounded to 2^-9 of their own).
 //
 // Warps: 0 copies (tensor maps, a ring of chunks); 1 and 3 issue; 2 finds the chunks, and works their decays out ahead; 4..7 P;
-// 8..11 K~; 12..19 the state; 20..23 O, scaled and stored.  (The warps that all others wait for come first: an SM's schedulers are
-// busy most of the time, and as the last ones of the block they got what the others left.)  Every role walks one stream of chunks, whatever sequences and heads
+// 8..11 K~; 12..19 the state; 20..23 O, scaled and stored.  Every role walks one stream of chunks, whatever sequences and heads
 // these belong to, so the next sequence's first chunks are under way while the last one's state is stored.
+//
+// Measured (one GPU): 8192 tokens of 96 heads with fp32 states 187 to 193 us, 4.2 to 4.4 TB/s (0.62 to 0.65 of the copy rate; 152 heads,
+// a CTA on every SM, 0.88); 12 ragged prompts of as many tokens in all 171 us, 5.6 TB/s; 8192 tokens of 64 heads over 8 with gates, two
+// groups a head, 170 us; 32768 tokens of 8 heads, 19 groups, 96 us; 509 tokens of 14 heads over 2 of 64 15 us.  A chunk takes some 2,600 cycles in
+// a (sequence, head)'s chain even where nothing else runs, and that is what bounds all but the batches that fill the SMs: the issuing
+// warp's products one after the other, one O on its way out (tensor memory's columns are taken by two L) and one place for scores each
+// take about as long, so that none of them alone is what to shorten.  Slower were: V^T K~ issued by a warp of its own (224 to 245
+// us), a copying warp of its own beside it (226), scores' place given back before P is stored (190 to 197), O in two halves (206 to 210).
 //
 // An item is a (sequence, head), or a group of its chunks where there are too few of those for the SMs: then a first launch works
 // out what each group adds to the state (its products V^T K~ alone), a small kernel chains the groups' states, and the second

@@ -7,6 +7,10 @@
 // state stays in fp32 registers from the first token to the last.  The rows' sums over the lanes go through a butterfly that
 // halves the rows a lane holds as it doubles the lanes that a sum covers, NI - 1 shuffles and not NI log2(LPR).
 // The state is read once and written once, which is the floor of a single token.
+//
+// Measured (one GPU): 256 sequences of one token, 96 heads of 128, fp32 states (3.25 GB) 458 us, 7.1 TB/s, the memory's rate; one sequence
+// of 32 heads 2.8 us, a launch; 64 sequences of 5 tokens, 64 heads over 8, bf16 states 60.8 us, 4.5 TB/s: there the tokens' arithmetic on the
+// state (two fmas an element and token, 80 us before they went in pairs) takes longer than reading and writing it does (40.8 us).
 #include "kda_linear.cuh"
 
 namespace kda {
