@@ -24,12 +24,16 @@
 // these belong to, so the next sequence's first chunks are under way while the last one's state is stored.
 //
 // Measured (one GPU): 8192 tokens of 96 heads with fp32 states 187 to 193 us, 4.2 to 4.4 TB/s (0.62 to 0.65 of the copy rate; 152 heads,
-// a CTA on every SM, 0.88); 12 ragged prompts of as many tokens in all 171 us, 5.6 TB/s; 8192 tokens of 64 heads over 8 with gates, two
-// groups a head, 170 us; 32768 tokens of 8 heads, 19 groups, 96 us; 509 tokens of 14 heads over 2 of 64 15 us.  A chunk takes some 2,600 cycles in
-// a (sequence, head)'s chain even where nothing else runs, and that is what bounds all but the batches that fill the SMs: the issuing
-// warp's products one after the other, one O on its way out (tensor memory's columns are taken by two L) and one place for scores each
-// take about as long, so that none of them alone is what to shorten.  Slower were: V^T K~ issued by a warp of its own (224 to 245
-// us), a copying warp of its own beside it (226), scores' place given back before P is stored (190 to 197), O in two halves (206 to 210).
+// a CTA on every SM, 0.88); 12 ragged prompts of as many tokens in all 170 us, 5.6 TB/s; 8192 tokens of 64 heads over 8 with gates, two
+// groups a head, 164 us; 32768 tokens of 8 heads, 19 groups, 94 us; 509 tokens of 14 heads over 2 of 64 15 us.  A chunk takes some 2,600 cycles in
+// a (sequence, head)'s chain even where nothing else runs, and that is what bounds all but the batches that fill the SMs.  At 128 bytes a
+// cycle shared memory alone is busy for 2,100 of them: 48 KB come in, 48 KB are read and written for K~, 8 KB written for P, the products
+// read 32 + 64 + 16 + 24 KB, O goes out through 32 KB.  The issuing warp's products one after the other, one O on its way out (tensor memory's
+// columns are taken by two L) and one place for scores each take nearly as long.  Where only states are wanted a chunk moves 144 KB and
+// takes 1,600 cycles; four L on their way there, and chunks dealt out to the two halves of K~'s warps, changed nothing.  Slower were:
+// V^T K~ issued by a warp of its own (224 to 245 us), a copying warp of its own beside it (226), scores' place given back before P is
+// stored (190 to 197), O in two halves (206 to 210), barriers tested two at a time (4096 tokens of 152 heads 118 for 112: code of many
+// roles is dear in instruction caches), a longer ring of chunks known ahead.
 //
 // An item is a (sequence, head), or a group of its chunks where there are too few of those for the SMs: then a first launch works
 // out what each group adds to the state (its products V^T K~ alone), a small kernel chains the groups' states, and the second
@@ -676,19 +680,18 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                 a[3] = sum;
                 const Sum all{__shfl_sync(FULL, sum.hi, 15, 16), __shfl_sync(FULL, sum.lo, 15, 16)};
                 const int count = i0 + 1 < c1 ? 2 : 1;         // (the second may be the next group's first)
-                if (STATES_ONLY) {
-                    total = add(total, Sum{__shfl_sync(FULL, all.hi, 0), __shfl_sync(FULL, all.lo, 0)});
-                    if (count > 1)
-                        total = add(total, Sum{__shfl_sync(FULL, all.hi, 16), __shfl_sync(FULL, all.lo, 16)});
-                }
-                if (!slot_free(c) || (count > 1 && !slot_free(c + 1)))
+                if (STATES_ONLY && half < count)
+                    total = add(total, all);                   // every other chunk's
+                if (!slot_free(c + count - 1))                 // and the one before, which every warp is through with earlier
                     break;
                 Entry &e = entries[(c + half) % ENTRIES];
                 if (half < count) {
-                    *reinterpret_cast<float4 *>(&e.hi[j]) = make_float4(a[0].hi, a[1].hi, a[2].hi, a[3].hi);
-                    *reinterpret_cast<float4 *>(&e.lo[j]) = make_float4(a[0].lo, a[1].lo, a[2].lo, a[3].lo);
-                    *reinterpret_cast<float4 *>(&e.ea[j]) = make_float4(p.scale * ex2_approx(a[0].hi), p.scale * ex2_approx(a[1].hi),
-                                                                        p.scale * ex2_approx(a[2].hi), p.scale * ex2_approx(a[3].hi));
+                    if (!STATES_ONLY) {                        // what P and O want
+                        *reinterpret_cast<float4 *>(&e.hi[j]) = make_float4(a[0].hi, a[1].hi, a[2].hi, a[3].hi);
+                        *reinterpret_cast<float4 *>(&e.lo[j]) = make_float4(a[0].lo, a[1].lo, a[2].lo, a[3].lo);
+                        *reinterpret_cast<float4 *>(&e.ea[j]) = make_float4(p.scale * ex2_approx(a[0].hi), p.scale * ex2_approx(a[1].hi),
+                                                                            p.scale * ex2_approx(a[2].hi), p.scale * ex2_approx(a[3].hi));
+                    }
                     uint2 f[4];
 #pragma unroll
                     for (int q = 0; q < 4; q++)
@@ -709,9 +712,10 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                     mbar_arrive(b_ent + 8 * ((c + lane) % ENTRIES));
                 c += count;
             }
-            if (STATES_ONLY && lane == 0) {
-                const Decay d = decay_of(total);
-                plan.decays[at_dst] = make_float2(d.factor, d.weak ? 1.0f : 0.0f);
+            if (STATES_ONLY) {
+                const Decay d = decay_of(add(total, Sum{__shfl_xor_sync(FULL, total.hi, 16), __shfl_xor_sync(FULL, total.lo, 16)}));
+                if (lane == 0)
+                    plan.decays[at_dst] = make_float2(d.factor, d.weak ? 1.0f : 0.0f);
             }
         }
         if (slot_free(c)) {
