@@ -112,24 +112,27 @@ __global__ void __launch_bounds__(THREADS) kda_linear_tokens_kernel(const Linear
                 s[i][e] = 0;
         }
     }
-    bool bad = false;
-    int64_t bos, len;
-    linear_range(p, n, bos, len, bad);
     const float fixed = p.log_decay ? p.log_decay[h] : 0.0f;
     const int hk = h / p.group;
-    // a token's values are read while the one before it is worked on
+    // a token's values are read while the one before it is worked on, and not looked at before their turn
     uint32_t q[E / 2], k[E / 2], v[NI / 2];
-    float a = 0.0f;
+    float gate = 0.0f;
     auto read = [&](int64_t t) {
-        a = log_decay_of(fixed, gate_of(p, t, h), bad);
+        gate = gate_of(p, t, h);
         load_bf16<E>(p.q + t * p.q_stride + h * DIM + c * E, q);
         load_bf16<E>(p.k + t * p.k_stride + hk * DIM + c * E, k);
         load_bf16<NI>(p.v + t * p.v_stride + hk * DIM + row0, v);
     };
-    if (len > 0)
+    // the first ones, where it is known which, before the sequence's length is (it may be 0: they are not used then)
+    if (!p.tok.cu && p.tok.T > 0)
+        read(n * p.tok.T);
+    bool bad = false;
+    int64_t bos, len;
+    linear_range(p, n, bos, len, bad);
+    if (p.tok.cu && len > 0)
         read(bos);
     for (int64_t t = bos; t < bos + len; t++) {
-        const float decay = expf(a);
+        const float decay = expf(log_decay_of(fixed, gate, bad));
         const f2 decay2 = f2_pack(decay, decay);
         f2 q2[E / 2], k2[E / 2];
         float vf[NI], o[NI];
