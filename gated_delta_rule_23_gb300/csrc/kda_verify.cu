@@ -52,11 +52,9 @@ __device__ __forceinline__ int drafts_of(const VerifyArgs &p, int b, bool &bad)
     bad |= n < 0 || n > p.K;
     return min(max(n, 0), p.K);
 }
-__device__ __forceinline__ float temperature_of(const VerifyArgs &p, int b, bool &bad)
+__device__ __forceinline__ float given_temperature(const VerifyArgs &p, int b) { return p.temperature ? p.temperature[b] : 1.0f; }
+__device__ __forceinline__ float checked_temperature(float t, bool &bad)
 {
-    if (!p.temperature)
-        return 1.0f;
-    const float t = p.temperature[b];
     if (t >= 0.0f && t <= FLT_MAX)
         return t;
     bad = true;
@@ -163,7 +161,7 @@ template <typename T, int VECS> __global__ void __launch_bounds__(THREADS, 8) kd
     const int tid = threadIdx.x;
     stream_order();
     bool bad = false;
-    const float tau = temperature_of(p, b, bad);
+    const float given = given_temperature(p, b);
     if (row - b * (p.K + 1) > drafts_of(p, b, bad))
         return;                                     // behind the request's last draft
     const T *l = static_cast<const T *>(p.logits) + row * p.row_stride;
@@ -183,6 +181,7 @@ template <typename T, int VECS> __global__ void __launch_bounds__(THREADS, 8) kd
                         put(x[i], e, l[at + e]);
         }
     }
+    const float tau = checked_temperature(given, bad);    // (looked at here: the logits' loads do not wait for it)
     float m = largest<T>(x);                        // (NaN left out)
     m = block_max(m, sm[0]);
     float s = 0.0f;
@@ -281,35 +280,50 @@ template <typename T, int W> __global__ void __launch_bounds__(PICK_THREADS, 2) 
         else if (t < to)
             read_four(noise + t, &ahead[i]);
     }
+    // What the rows' tests need, of every row a warp may have: loads that wait for no length and no temperature.
+    const T *logits = static_cast<const T *>(p.logits) + (int64_t)b * (p.K + 1) * p.row_stride;
+    const float2 *stats = p.stats + (int64_t)b * (p.K + 1) * p.chunks;
+    constexpr int WARPS = PICK_THREADS / 32, ROWS = (MAX_DRAFTS + WARPS) / WARPS;
+    const float2 none = make_float2(-INFINITY, 0.0f);
+    float2 first[ROWS];
+    int draft[ROWS];
+    float drafted[ROWS], bar[ROWS];                 // the draft's logit, and u q of it
+    bool there[ROWS];
+#pragma unroll
+    for (int k = 0; k < ROWS; k++) {
+        const int i = warp + k * WARPS;
+        draft[k] = i < p.K ? p.drafts[b * p.K + i] : -1;
+        bar[k] = i < p.K ? p.uniform[b * p.K + i] : 0.0f;
+        first[k] = i <= p.K && lane < p.chunks ? __ldcg(&stats[i * p.chunks + lane]) : none;
+    }
+#pragma unroll
+    for (int k = 0; k < ROWS; k++) {
+        const int i = warp + k * WARPS;
+        there[k] = draft[k] >= 0 && draft[k] < p.V;
+        drafted[k] = there[k] ? logit(as_float(logits[i * p.row_stride + draft[k]])) : -INFINITY;
+        if (there[k] && p.probs)
+            bar[k] *= p.probs[((int64_t)b * p.K + i) * p.V + draft[k]];
+    }
     bool bad = false;
     const int L = drafts_of(p, b, bad);
-    const float tau = temperature_of(p, b, bad);
+    const float tau = checked_temperature(given_temperature(p, b), bad);
     const bool greedy = tau == 0.0f;
     const Exponent f = exponent_of(greedy ? 1.0f : tau);
-    const T *logits = static_cast<const T *>(p.logits) + (int64_t)b * (p.K + 1) * p.row_stride;
-    for (int i = warp; i <= L; i += PICK_THREADS / 32) {
-        const float2 *st = p.stats + ((int64_t)b * (p.K + 1) + i) * p.chunks;
-        const float2 none = make_float2(-INFINITY, 0.0f), first = lane < p.chunks ? __ldcg(&st[lane]) : none;
-        // the draft's logit and probability
-        float l = 0.0f, bar = 0.0f;
-        bool there = false;
-        if (i < L) {
-            const int x = p.drafts[b * p.K + i];
-            there = x >= 0 && x < p.V;
-            bad |= !there;
-            if (there) {
-                l = logit(as_float(logits[i * p.row_stride + x]));
-                bar = p.uniform[b * p.K + i] * (p.probs ? p.probs[((int64_t)b * p.K + i) * p.V + x] : 1.0f);
-            }
-        }
-        float m = first.x, z = 0.0f;
+#pragma unroll
+    for (int k = 0; k < ROWS; k++) {
+        const int i = warp + k * WARPS;
+        if (i > L)
+            break;                                  // (no statistics behind the last draft's)
+        const float2 *st = stats + i * p.chunks;
+        bad |= i < L && !there[k];
+        float m = first[k].x, z = 0.0f;
         for (int c = lane + 32; c < p.chunks; c += 32)
             m = fmaxf(m, __ldcg(&st[c].x));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
         if (!greedy) {
-            z = first.x == -INFINITY ? 0.0f : first.y * weight_of(first.x - m, f);
+            z = first[k].x == -INFINITY ? 0.0f : first[k].y * weight_of(first[k].x - m, f);
             for (int c = lane + 32; c < p.chunks; c += 32) {
                 const float2 x = __ldcg(&st[c]);
                 z += x.x == -INFINITY ? 0.0f : x.y * weight_of(x.x - m, f);
@@ -320,8 +334,8 @@ template <typename T, int W> __global__ void __launch_bounds__(PICK_THREADS, 2) 
             z += __shfl_xor_sync(FULL, z, o);
         if (lane == 0) {
             // a row without a finite maximum, and a draft that cannot be, accept nothing
-            const bool can = there && fabsf(m) <= FLT_MAX && l > -INFINITY;
-            row_ok[i] = can && (greedy ? l == m : bar * z < weight_of(l - m, f));
+            const bool can = i < L && there[k] && fabsf(m) <= FLT_MAX && drafted[k] > -INFINITY;
+            row_ok[i] = can && (greedy ? drafted[k] == m : bar[k] * z < weight_of(drafted[k] - m, f));
             row_max[i] = m, row_sum[i] = z;
         }
     }
