@@ -11,9 +11,9 @@
 // draft's row r and the noise, a share of the vocabulary a CTA; the shares' best meet in shared memory.  The race is run on
 // (e_t - q_t z) / E_t, z = sum e: no division by z.
 //
-// Measured (one GPU): 64 requests of 4 drafts, 131072 fp32 logits and the drafts' distributions (235 MB) 44.4 us, 5.3 TB/s, of which the
-// statistics take 30 (5.6 TB/s) and the pick 15: a cluster waits for its rows' statistics, reads one row, and waits for the shares.
-// 128 requests of 3 looked-up drafts, 50257 bf16 logits, 24.3 us; one of 4 drafts, 32001 bf16 logits, 6.4 us: two launches.
+// Measured (one GPU): 64 requests of 4 drafts, 131072 fp32 logits and the drafts' distributions (235 MB) 43 us, 5.5 TB/s, of which the
+// statistics take 30 (5.6 TB/s) and the pick the rest: a cluster waits for its rows' statistics, reads one row, and waits for the shares.
+// 128 requests of 3 looked-up drafts, 50257 bf16 logits, 23.3 us; one of 4 drafts, 32001 bf16 logits, 6.2 us: two launches.
 #include "kda_step.cuh"
 
 #include <cfloat>
@@ -257,8 +257,9 @@ __device__ __forceinline__ void read_four(const __nv_bfloat16 *p, float *x)
 }
 
 // A cluster a request.  W neighbouring tokens a thread: 4 where all rows begin on 16 bytes (8 of bf16) and no row ends within four, else 1
-// (64 requests of 4 drafts, fp32, statistics included: 44.4 us with 4, 46.8 with 1).
-template <typename T, int W> __global__ void __launch_bounds__(PICK_THREADS, 2) kda_verify_pick_kernel(const VerifyArgs p)
+// (64 requests of 4 drafts, fp32, statistics included: 44.4 us with 4, 46.8 with 1).  PROBS: the drafts were drawn, not looked up (without
+// a kernel of their own these take 24.2 us for 23.3).
+template <typename T, int W, bool PROBS> __global__ void __launch_bounds__(PICK_THREADS, 2) kda_verify_pick_kernel(const VerifyArgs p)
 {
     __shared__ float row_max[MAX_DRAFTS + 1], row_sum[MAX_DRAFTS + 1];
     __shared__ int row_ok[MAX_DRAFTS + 1];
@@ -301,7 +302,7 @@ template <typename T, int W> __global__ void __launch_bounds__(PICK_THREADS, 2) 
         const int i = warp + k * WARPS;
         there[k] = draft[k] >= 0 && draft[k] < p.V;
         drafted[k] = there[k] ? logit(as_float(logits[i * p.row_stride + draft[k]])) : -INFINITY;
-        if (there[k] && p.probs)
+        if (PROBS && there[k])
             bar[k] *= p.probs[((int64_t)b * p.K + i) * p.V + draft[k]];
     }
     bool bad = false;
@@ -347,7 +348,7 @@ template <typename T, int W> __global__ void __launch_bounds__(PICK_THREADS, 2) 
     const bool alive = fabsf(m) <= FLT_MAX;
     const int x = r < L ? p.drafts[b * p.K + r] : -1;
     const T *l = logits + r * p.row_stride;
-    const float *q = r < L && p.probs ? p.probs + ((int64_t)b * p.K + r) * p.V : nullptr;
+    const float *q = PROBS && r < L ? p.probs + ((int64_t)b * p.K + r) * p.V : nullptr;
     // the best of the race: its value's bits above the complement of its index, so that ties go to the lower one
     unsigned long long best = 0;
     for (int pass = 0; pass < 2; pass++) {
@@ -446,8 +447,9 @@ template <typename T> cudaError_t launch_verify(const VerifyArgs &p, cudaStream_
         return e;
     const bool fours = p.V % 4 == 0 && p.row_stride % 4 == 0 && is_aligned(p.logits, 4 * sizeof(T)) && is_aligned(p.probs, 16) &&
                        is_aligned(p.noise, 16);
-    return fours ? launch_in_row(kda_verify_pick_kernel<T, 4>, (unsigned)(p.B * p.cluster), PICK_THREADS, 0, p.cluster, st, p)
-                 : launch_in_row(kda_verify_pick_kernel<T, 1>, (unsigned)(p.B * p.cluster), PICK_THREADS, 0, p.cluster, st, p);
+    const auto kernel = p.probs ? (fours ? kda_verify_pick_kernel<T, 4, true> : kda_verify_pick_kernel<T, 1, true>)
+                                : (fours ? kda_verify_pick_kernel<T, 4, false> : kda_verify_pick_kernel<T, 1, false>);
+    return launch_in_row(kernel, (unsigned)(p.B * p.cluster), PICK_THREADS, 0, p.cluster, st, p);
 }
 
 }  // namespace
