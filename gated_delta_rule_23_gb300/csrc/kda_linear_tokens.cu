@@ -8,9 +8,10 @@
 // halves the rows a lane holds as it doubles the lanes that a sum covers, NI - 1 shuffles and not NI log2(LPR).
 // The state is read once and written once, which is the floor of a single token.
 //
-// Measured (one GPU): 256 sequences of one token, 96 heads of 128, fp32 states (3.25 GB) 458 us, 7.1 TB/s, the memory's rate; one sequence
-// of 32 heads 2.8 us, a launch; 64 sequences of 5 tokens, 64 heads over 8, bf16 states 60.8 us, 4.5 TB/s: there the tokens' arithmetic on the
-// state (two fmas an element and token, 80 us before they went in pairs) takes longer than reading and writing it does (40.8 us).
+// Measured (one GPU): 256 sequences of one token, 96 heads of 128, fp32 states (3.25 GB) 457 us, 7.1 TB/s, the memory's rate; one sequence
+// of 32 heads 2.7 us, a launch; 64 sequences of up to 5 tokens, 64 heads over 8, bf16 states 56.4 us, 4.9 TB/s (40.8 at the memory's rate):
+// there the tokens' arithmetic on the state takes 33 us of issue slots (two-wide; 80 us in all without).  Rows a warp, bf16: 8 of each lane group
+// 56 us, 4 64 (fp32: 16 and 8 take the same).  A gate is only looked at in its turn: at once, its load held up the warp (60.8 us).
 #include "kda_linear.cuh"
 
 namespace kda {

@@ -538,7 +538,7 @@ size_t kda_linear_attn_workspace_size(int varlen, int N, int64_t T, int H, int D
  *   draft_tokens   int32 [B, K];   draft_probs  fp32 [B, K, V] or NULL.
  *   uniform        fp32 [B, K];    noise  fp32 [B, V], > 0 (a token whose noise is not is not drawn, but for 0: it is first).
  *   temperature    fp32 [B] or NULL (1), finite and >= 0 (else reported and taken as 0).
- *   draft_lens     int32 [B] or NULL (K): drafts of each request; the rest of its rows is not read.
+ *   draft_lens     int32 [B] or NULL (K): drafts of each request; what the rest of its rows holds does not matter.
  *   tokens         int32 [B, K + 1]: the accepted drafts, the token after them, then -1.
  *   counts         int32 [B]: tokens written, 1 to K + 1 (what a linear attention's `lens` takes to advance its states).
  *   0 <= K <= 31, V <= 2^24.  tokens and counts overlap nothing else.
