@@ -351,8 +351,16 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t sr
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
                  ::"l"(map), "r"(src), "r"(x), "r"(y), "r"(z) : "memory");
 }
-// The warps that take O out, among themselves
+// The warps that take O out, among themselves.  Whether they go on they decide together: a wait may give up in one of them alone, and a
+// barrier that it does not come to would hold the others for ever.
 template <int N> __device__ __forceinline__ void out_sync() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }
+template <int N> __device__ __forceinline__ bool out_agree(bool go)
+{
+    uint32_t all;
+    asm volatile("{ .reg .pred p, q; setp.ne.u32 p, %1, 0; bar.red.and.pred q, 1, %2, p; selp.u32 %0, 1, 0, q; }"
+                 : "=r"(all) : "r"((uint32_t)go), "n"(N) : "memory");
+    return all;
+}
 // Tokens 2 q and 2 q + 1 of a pair, as the halves of a word: those at or before the row's (gap = the row's token - 2 q)
 __device__ __forceinline__ uint32_t seen_pair(int gap)
 {
@@ -917,17 +925,20 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
         if (lane == 0)
             mbar_arrive(b_sb);                                 // O is free
         const uint32_t to0 = to + ((((ow & 1) * 4 + (block & 1)) ^ r) << 4), to1 = to + ((((ow & 1) * 4 + 2 + (block & 1)) ^ r) << 4);
-        for (uint32_t c = 0; next(c); c++) {
+        for (uint32_t c = 0;; c++) {
+            bool go = next(c) && (STATES_ONLY || wait(b_o + 8 * (c & 1), c >> 1));
+            if (!STATES_ONLY && ow < WARPS) {
+                if (t == 0)
+                    bulk_wait_read_all();                      // the last chunk's O has left
+                go = out_agree<32 * WARPS>(go);
+            }
+            if (!go)
+                break;
             const Entry &e = entries[c % ENTRIES];
             if (!STATES_ONLY) {
-                if (!wait(b_o + 8 * (c & 1), c >> 1))
-                    break;
                 if (ow < WARPS) {
                     tc_fence_after();
                     const int len = e.len, tok0 = e.tok0, h = e.h;
-                    if (t == 0)
-                        bulk_wait_read_all();                  // the last chunk's O has left
-                    out_sync<32 * WARPS>();
 #pragma unroll 1
                     for (int first = 0; first < 64; first += 16) {
                         const float2 f0 = *reinterpret_cast<const float2 *>(&e.ea[first + 2 * (lane & 3)]);
@@ -949,8 +960,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                         }
                         if (__any_sync(FULL, !(f2_lo(z) + f2_hi(z) == 0.0f))) {
                             // (P is through; waited for here so that this thread sees it.  V's place may be another chunk's by now.)
-                            if (!wait(b_p + 8 * (c & 1), c >> 1))
-                                break;
+                            wait(b_p + 8 * (c & 1), c >> 1);
                             const int v = ow * 32 + lane;
                             const unsigned char *pt = smem + S::P + (c & 1) * TILE_CB;
                             const __nv_bfloat16 *vt = p.v + (int64_t)tok0 * p.v_stride + h / p.group * DIM + v;

@@ -402,6 +402,24 @@ def test_a_wait_that_gives_up_is_reported(t):
     check(a, *call(a))
 
 
+@pytest.mark.parametrize("t", [70, 3000])
+def test_waits_that_give_up_in_some_warps_alone(t):
+    """Whatever comes of such a call, it ends, and the next one is right."""
+    a = make([t, t], 3, 3, 128, "batch", seed=27)
+    lib = kda.load()
+    try:
+        for polls in (1, 2, 5):
+            lib.kda_set_wait_limit(polls)
+            try:
+                call(a)
+            except KDAError as e:
+                assert e.status == KDA_ERR_TIMEOUT
+    finally:
+        lib.kda_set_wait_limit(KDA_DEFAULT_WAIT_POLLS)
+    a["out"].fill_(5.0)
+    check(a, *call(a))
+
+
 def test_two_graphs_with_workspaces_of_their_own():
     """Captured calls in groups, replayed on two streams at once."""
     calls, graphs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
