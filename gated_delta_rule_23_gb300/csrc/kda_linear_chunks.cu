@@ -1,42 +1,41 @@
 // Linear attention in chunks of 64 tokens on the tensor cores.
 //
 // Within a chunk, with A_i the sum of the logarithms up to token i and S the state before the chunk (rows v, columns k):
-//   P = (Q K^T) . e^(A_i - A_j)  (j <= i),   O^T = V^T P^T + e^(A_i) S Q^T,   S <- e^(A_C) S + V^T (e^(A_C - A_j) K).
+//   P = (Q K^T) . e^(A_i - A_j)  (j <= i),   O^T = V^T P^T + e^(A_i) S Q^T,   S <- e^(A_C) S + (e^(A_C - A_j) V)^T K.
 // All decays are at most 1 by construction: they are exponentials of differences that are never positive, taken from sums of two
 // terms, so a strong decay beside a weak one costs no precision and none is divided by.
 //
-// The features lie on tensor memory's lanes: O^T and S have a row per v, so that S is the operand of its product straight from tensor
-// memory (bf16, written by the threads that hold it) and leaves shared memory's bandwidth, the first bound of such a kernel, to
-// the others.  Four products a chunk: Q K^T [64 x 64] (on 16 of each warp's 32 lanes),
-// V^T K~ [D x D], S Q^T and V^T P^T [D x 64].  D = 64 fills the lanes up with a block of zeros.
+// The features lie on tensor memory's lanes: O^T and S have a row per v, so that S and V~ = e^(A_C - A_j) V are operands straight from tensor
+// memory (bf16, written by the threads that hold S, and by those that turn V) and leave shared memory's bandwidth, the first bound of
+// such a kernel, to the others.  Four products a chunk: Q K^T [64 x 64] (on 16 of each warp's 32 lanes),
+// V~^T K [D x D], S Q^T and V^T P^T [D x 64].  D = 64 fills the lanes up with a block of zeros.
 //
-// The state stays in fp32 registers (eight warps): each chunk's V^T K~ comes out of tensor memory and is added there, so the tensor cores'
+// The state stays in fp32 registers (eight warps): each chunk's V~^T K comes out of tensor memory and is added there, so the tensor cores'
 // own accumulation spans one chunk and what a long sequence adds up is rounded to nearest.  Weak decays are taken as
 // S + (expm1(A_C) S + L): a factor next to 1 that is off by half a step in every chunk would drift by 2^-25 a chunk; strong ones as
 // e^(A_C) S + L, so that nothing of a state that is forgotten stays behind as rounding.
-// K~ = e^(A_C - A_j) K is not a bf16 number: two bf16 terms that add up to it (to 2^-17) are multiplied with V one after the other.  With
+// V~ is not a bf16 number: two bf16 terms that add up to it (to 2^-17) are multiplied with K one after the other.  With
 // one, outputs after bf16 states were 2.6e-3 off (norm) and not 2.3e-3, 1.7e-3 of it their own rounding, and a prompt took 3% less:
 // what the tensor cores do is not what bounds a chunk.  fp32 states come out 2.7e-6 off.  The other roundings to bf16 are P's, and that of
 // the state that a chunk's queries read (outputs are bf16, rounded to 2^-9 of their own).
 //
 // Warps: 0 copies (tensor maps, a ring of chunks); 1 and 3 issue; 2 finds the chunks, and works their decays out ahead; 4..7 P;
-// 8..11 K~; 12..19 the state; 20..23 O, scaled and stored.  Every role walks one stream of chunks, whatever sequences and heads
+// 8..11 V~; 12..19 the state; 20..23 O, scaled and stored.  Every role walks one stream of chunks, whatever sequences and heads
 // these belong to, so the next sequence's first chunks are under way while the last one's state is stored.
 //
-// Measured (one GPU): 8192 tokens of 96 heads with fp32 states 187 to 193 us, 4.2 to 4.4 TB/s (0.62 to 0.65 of the copy rate; 152 heads,
-// a CTA on every SM, 0.88); 12 ragged prompts of as many tokens in all 170 us, 5.6 TB/s; 8192 tokens of 64 heads over 8 with gates, two
-// groups a head, 164 us; 32768 tokens of 8 heads, 19 groups, 94 us; 509 tokens of 14 heads over 2 of 64 15 us.  A chunk takes some 2,600 cycles in
-// a (sequence, head)'s chain even where nothing else runs, and that is what bounds all but the batches that fill the SMs.  At 128 bytes a
-// cycle shared memory alone is busy for 2,100 of them: 48 KB come in, 48 KB are read and written for K~, 8 KB written for P, the products
-// read 32 + 64 + 16 + 24 KB, O goes out through 32 KB.  The issuing warp's products one after the other, one O on its way out (tensor memory's
-// columns are taken by two L) and one place for scores each take nearly as long.  Where only states are wanted a chunk moves 144 KB and
-// takes 1,600 cycles; four L on their way there, and chunks dealt out to the two halves of K~'s warps, changed nothing.  Slower were:
-// V^T K~ issued by a warp of its own (224 to 245 us), a copying warp of its own beside it (226), scores' place given back before P is
-// stored (190 to 197), O in two halves (206 to 210), barriers tested two at a time (4096 tokens of 152 heads 118 for 112: code of many
-// roles is dear in instruction caches), a longer ring of chunks known ahead.
+// Measured (one GPU): 8192 tokens of 96 heads with fp32 states 177 us, 4.6 TB/s (0.68 of the copy rate); 12 ragged prompts of as many
+// tokens in all 162 us, 5.9 TB/s; 8192 tokens of 64 heads over 8 with gates, two groups a head, 156 us; 32768 tokens of 8 heads, 19
+// groups, 91 us; 509 tokens of 14 heads over 2 of 64 15 us.  A chunk takes some 2,400 cycles in a (sequence, head)'s chain even where
+// nothing else runs, and that is what bounds all but the batches that fill the SMs.  At 128 bytes a cycle shared memory alone is busy for 1,600 of
+// them: 48 KB come in, 16 KB are read to be turned, 8 KB written for P, the products read 32 + 32 + 16 + 24 KB, O goes out through 32 KB.
+// (With K~ = e^(A_C - A_j) K, formed in shared memory and read from there as V is, it was 272 KB, and the five took 193, 171, 164, 94 and 15 us.)  The
+// issuing warp's products one after the other, one L, one O on its way out and one place for scores each take nearly as long.  Before
+// that change were slower: the state's product issued by a warp of its own (224 to 245 us), a copying warp of its own beside it (226), scores'
+// place given back before P is stored (190 to 197), O in two halves (206 to 210), barriers tested two at a time (4096 tokens of 152
+// heads 118 for 112: code of many roles is dear in instruction caches), a longer ring of chunks known ahead.
 //
 // An item is a (sequence, head), or a group of its chunks where there are too few of those for the SMs: then a first launch works
-// out what each group adds to the state (its products V^T K~ alone), a small kernel chains the groups' states, and the second
+// out what each group adds to the state (its products V~^T K alone), a small kernel chains the groups' states, and the second
 // launch runs all groups side by side.
 //
 // A token's infinite or NaN v gets P = 0 in the columns of earlier tokens, and 0 x v is NaN in the matrix product: a row of V^T P^T
@@ -52,12 +51,12 @@ namespace {
 
 constexpr int THREADS = 768;                 // six warpgroups
 constexpr int TMEM_COLS = 512;
-constexpr int TM_S1 = 0, TM_SB = 64, TM_O1 = 128, TM_O2 = 192, TM_L = 256;   // columns; two L
+constexpr int TM_S1 = 0, TM_SB = 64, TM_O1 = 128, TM_O2 = 192, TM_L = 256, TM_V = 384;   // columns; two V~, a term 32 each
 constexpr int ENTRIES = 6;                   // chunks known ahead (8: 2 us more for ragged prompts, whose last items are taken too early)
 constexpr int EARLY = 4;                     // chunks ahead that tiles are brought into L2
 constexpr int TILE_CB = 64 * 128;            // bytes of 64 tokens x 64 features
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int TERMS = 2;                     // bf16 terms of K~
+constexpr int TERMS = 2;                     // bf16 terms of V~
 constexpr int MAX_RANKED = 128;              // sequences of a ragged batch that are taken longest first
 
 // A sum of logarithms in base 2 as two terms, good to some 2^-45 of the largest partial sum, without 64-bit arithmetic (whose unit here
@@ -100,7 +99,7 @@ __device__ __forceinline__ float decayed(const Decay &d, float s, float l)
 struct alignas(16) Entry {    // one chunk; the tables are read four floats at a time
     float hi[64], lo[64];     // A_i in base 2, as two terms
     float ea[64];             // scale e^(A_i)
-    uint2 kf[64];             // e^(A_C - A_j) as two bf16 terms, each twice
+    uint32_t f[TERMS][32];    // e^(A_C - A_j) as two bf16 terms, tokens in pairs
     int64_t at_src, at_dst;   // index of the state before and after the chunk's item
     int src, dst;             // and where that is: 0 zeros / nowhere, 1 the call's, 2 a group's
     Decay decay;              // of the whole chunk
@@ -115,16 +114,15 @@ template <int DIM, bool STATES_ONLY> struct Shape {
     static constexpr int TILE = CB * TILE_CB;
     static constexpr int TILES = STATES_ONLY ? 2 : 3;         // of a chunk: V, K (later K~'s first term), Q
     static constexpr int STAGE = TILES * TILE;
-    static constexpr int STAGES = DIM == 64 ? (STATES_ONLY ? 8 : 6) : (STATES_ONLY ? 5 : 3);
-    static constexpr int KT = STAGES * STAGE;                 // K~'s other term, of two chunks
-    static constexpr int P = KT + 2 * (TERMS - 1) * TILE;     // two of [64 i][64 j]
+    static constexpr int STAGES = DIM == 64 ? (STATES_ONLY ? 8 : 6) : (STATES_ONLY ? 6 : 3);
+    static constexpr int P = STAGES * STAGE;                  // two of [64 i][64 j]
     static constexpr int OUT = P + (STATES_ONLY ? 0 : 2 * TILE_CB);    // O on its way out
     static constexpr int ZERO = OUT + (STATES_ONLY ? 0 : TILE);        // D = 64: lanes 64 to 127
     static constexpr int ENTRY = ZERO + (DIM == 64 ? TILE_CB : 0);
     static constexpr int BAR = ENTRY + ENTRIES * (int)sizeof(Entry);
     static constexpr int SMEM = 1024 + BAR + 512;
     static_assert(SMEM <= 232448, "a CTA's shared memory");
-    static_assert(ENTRY % 16 == 0 && BAR % 8 == 0 && P % 1024 == 0 && KT % 1024 == 0 && ZERO % 1024 == 0, "alignment");
+    static_assert(ENTRY % 16 == 0 && BAR % 8 == 0 && P % 1024 == 0 && ZERO % 1024 == 0, "alignment");
 };
 
 // ---------------------------------------------------------------- items
@@ -320,12 +318,17 @@ __device__ __forceinline__ uint32_t bf16_fma(uint32_t a, uint32_t b, uint32_t c)
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
-// A factor as two bf16 terms, each in both halves of a word
-__device__ __forceinline__ uint2 two_terms(float f)
+// Two factors as two bf16 terms each
+__device__ __forceinline__ uint2 two_terms(float f, float g)
 {
-    const uint32_t a = pack_bf16(f, f);
-    const float rest = f - bf16_lo(a);
-    return make_uint2(a, pack_bf16(rest, rest));
+    const uint32_t a = pack_bf16(f, g);
+    return make_uint2(a, pack_bf16(f - bf16_lo(a), g - bf16_hi(a)));
+}
+// 16 lanes by 16 columns (32 bf16): thread t has columns t % 4, t % 4 + 4, .. of row t / 4 and, in between, of row t / 4 + 8
+__device__ __forceinline__ void tmem_put_pairs(uint32_t addr, const uint32_t (&u)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(u[0]), "r"(u[1]),
+                 "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]) : "memory");
 }
 // 16 lanes by 16 columns, laid out for stmatrix: thread t has columns 2 (t % 4) and the next of row t / 4, then of row t / 4 + 8,
 // then the same of the next 8 columns.  Two of them at once.
@@ -416,7 +419,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
             mbar_init(b_drain + 8 * i, 1);
             mbar_init(b_sb + 8 * i, 12);                       // S stored; O before it read
             mbar_init(b_pe + 8 * i, 4);
-            mbar_init(b_k + 8 * i, STATES_ONLY ? 16 : 12);     // K~ stored; L two chunks before read
+            mbar_init(b_k + 8 * i, STATES_ONLY ? 16 : 12);     // V~ stored; the last L read
             mbar_init(b_l + 8 * i, 1);
         }
         mbar_init(b_o2, 1);
@@ -520,27 +523,27 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                 arrive(b_ent_free + 8 * (c % ENTRIES));
             }
         } else {
-            const uint32_t id_l = idesc_bf16(128, DIM, true) | A_MN, id_o2 = idesc_bf16(128, 64, false), id_o1 = id_o2 | A_MN;
+            const uint32_t id_l = idesc_bf16(128, DIM, true), id_o2 = idesc_bf16(128, 64, false), id_o1 = id_o2 | A_MN;
             bool more = next(0);
             for (uint32_t c = 0; more; c++) {
                 const int st = c % STAGES;
                 const uint32_t at = base + st * S::STAGE;
                 // V as M rows: blocks of 64 features, for D = 64 the second one zeros
                 const uint32_t v = desc_lo(at, DIM == 128 ? TILE_CB : S::ZERO - st * S::STAGE);
-                if (!wait(b_k + 8 * (c & 1), c >> 1))          // K~ is there, and the place for the product
+                if (!wait(b_k + 8 * (c & 1), c >> 1))          // V~ is there, and the place for the product
                     break;
                 tc_fence_after();
-                const uint32_t d = tm + TM_L + 128 * (c & 1);
+                const uint32_t d = tm + TM_L, b = desc_lo(at + S::TILE, TILE_CB);
                 if (lead && !timeout) {
 #pragma unroll
                     for (int r = TERMS - 1; r >= 0; r--) {     // small terms first
-                        const uint32_t b = desc_lo(r == 0 ? at + S::TILE : base + S::KT + ((c & 1) * (TERMS - 1) + r - 1) * S::TILE, TILE_CB);
+                        const uint32_t a = tm + TM_V + 64 * (c & 1) + 32 * r;
 #pragma unroll
                         for (int k = 0; k < 4; k++) {
                             if (r == TERMS - 1 && k == 0)
-                                mma_ss<false>(d, v, b, id_l, 0);
+                                mma_ts<false>(d, a, b, id_l, 0);
                             else
-                                mma_ss<true>(d, v + k * (2048 >> 4), b + k * (2048 >> 4), id_l, 1);
+                                mma_ts<true>(d, a + 8 * k, b + k * (2048 >> 4), id_l, 1);
                         }
                     }
                     umma_commit(b_l + 8 * (c & 1));
@@ -700,12 +703,10 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                         *reinterpret_cast<float4 *>(&e.ea[j]) = make_float4(p.scale * ex2_approx(a[0].hi), p.scale * ex2_approx(a[1].hi),
                                                                             p.scale * ex2_approx(a[2].hi), p.scale * ex2_approx(a[3].hi));
                     }
-                    uint2 f[4];
-#pragma unroll
-                    for (int q = 0; q < 4; q++)
-                        f[q] = two_terms(ex2_approx(minus(all, a[q])));
-                    *reinterpret_cast<uint4 *>(&e.kf[j]) = make_uint4(f[0].x, f[0].y, f[1].x, f[1].y);
-                    *reinterpret_cast<uint4 *>(&e.kf[j + 2]) = make_uint4(f[2].x, f[2].y, f[3].x, f[3].y);
+                    const uint2 f = two_terms(ex2_approx(minus(all, a[0])), ex2_approx(minus(all, a[1])));
+                    const uint2 g = two_terms(ex2_approx(minus(all, a[2])), ex2_approx(minus(all, a[3])));
+                    *reinterpret_cast<uint2 *>(&e.f[0][j / 2]) = make_uint2(f.x, g.x);
+                    *reinterpret_cast<uint2 *>(&e.f[1][j / 2]) = make_uint2(f.y, g.y);
                     if (j == 0) {
                         const int left = (int)(w.len - i * 64 < 64 ? w.len - i * 64 : 64);
                         e.valid = 1;
@@ -783,51 +784,65 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
             arrive(b_ent_free + 8 * (c % ENTRIES));
         }
     } else if (warp < 12) {
-        // ------------------------------------------------------------ K~
-        // (where only states are wanted the warps of P take half of it: it is what bounds a chunk there)
+        // ------------------------------------------------------------ V~
+        // From shared memory, turned, into tensor memory: 16 features by 32 tokens at a time.  (Where only states are wanted the warps
+        // of P take half of the tokens.)
         set_registers<REGS_K, false>();
         constexpr int THREADS_K = STATES_ONLY ? 256 : 128;
-        const int t = tid - (384 - THREADS_K);
+        const int t = tid - (384 - THREADS_K), quad = warp & 3, r = lane & 7;
+        const int tok0 = STATES_ONLY && warp < 8 ? 32 : 0, tok1 = STATES_ONLY && warp >= 8 ? 32 : 64;
         for (uint32_t c = 0; next(c); c++) {
             const Entry &e = entries[c % ENTRIES];
             const int st = c % STAGES, len = e.len;
-            // K is there and its scores are through, and so is the product of the chunk before the last: its other term lies where this
-            // one's will, and its barrier is this one's
-            if ((c >= 2 && !wait(b_l + 8 * (c & 1), (c >> 1) - 1)) ||
-                !(STATES_ONLY ? wait(b_full + 8 * st, c / STAGES) : wait(b_s + 8 * (c & 1), c >> 1)))
+            // V is there, and the product of the chunk before the last is through, whose V~ lies where this one's will
+            if ((c >= 2 && !wait(b_l + 8 * (c & 1), (c >> 1) - 1)) || !wait(b_full + 8 * st, c / STAGES))
                 break;
-            constexpr int VECS = 64 * DIM / 8 / THREADS_K;     // 16-byte vectors of a thread, ROWS tokens apart
-            constexpr int ROWS = THREADS_K / (DIM / 8);
-            const int ch = t % (DIM / 8), j0 = t / (DIM / 8);  // (ROWS is a multiple of 8: the swizzle is the same for all)
-            const int at = (ch / 8) * TILE_CB + j0 * 128 + (((ch % 8) ^ (j0 & 7)) << 4);
-            unsigned char *const kt = smem + st * S::STAGE + S::TILE + at;
-            unsigned char *const to = smem + S::KT + (c & 1) * (TERMS - 1) * S::TILE + at;
-#pragma unroll
-            for (int m = 0; m < VECS; m++) {
-                const int j = j0 + ROWS * m;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (j < len)
-                    x = *reinterpret_cast<const uint4 *>(kt + m * (ROWS * 128));
-                const uint2 f = e.kf[j];
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                uint32_t y[TERMS][4];
-#pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    // k f1 rounded, and what that left off, which is a bf16 number, with k f2
-                    y[0][q] = bf16_mul(w[q], f.x);
-                    y[1][q] = bf16_fma(w[q], f.y, bf16_fma(w[q], f.x, y[0][q] ^ 0x80008000u));
-                }
-#pragma unroll
-                for (int r = 0; r < TERMS; r++)
-                    *reinterpret_cast<uint4 *>((r == 0 ? kt : to + (r - 1) * S::TILE) + m * (ROWS * 128)) =
-                        make_uint4(y[r][0], y[r][1], y[r][2], y[r][3]);
-            }
-            if (len < 64) {                                    // what lies behind the sequence is cleared from V
-                unsigned char *vt = smem + st * S::STAGE;
+            unsigned char *const stage = smem + st * S::STAGE;
+            if (len < 64) {
+                // What lies behind the sequence is cleared from K, by all, and from V, by the warps that turn it.  (The scores' product may
+                // read K meanwhile: what it makes of these rows is masked, whatever it is.)
                 for (int i = t; i < (64 - len) * 8 * CB; i += THREADS_K)
-                    *reinterpret_cast<uint4 *>(vt + i / ((64 - len) * 8) * TILE_CB + len * 128 + i % ((64 - len) * 8) * 16) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(stage + S::TILE + i / ((64 - len) * 8) * TILE_CB + len * 128 + i % ((64 - len) * 8) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                if (32 * quad < DIM)
+                    for (int i = lane; i < 64 * 4; i += 32) {
+                        const int tok = i / 4;
+                        if (tok >= len && tok >= tok0 && tok < tok1)
+                            *reinterpret_cast<uint4 *>(stage + quad / 2 * TILE_CB + tok * 128 + (((quad % 2 * 4 + i % 4) ^ (tok & 7)) << 4)) =
+                                make_uint4(0, 0, 0, 0);
+                    }
+                fence_async_smem();
+                __syncwarp();
             }
-            fence_async_smem();
+            if (32 * quad < DIM) {
+                tc_fence_after();
+                const uint32_t vt = base + st * S::STAGE + quad / 2 * TILE_CB;
+#pragma unroll 1
+                for (int i = tok0 / 16; i < tok1 / 16; i++) {
+                    const int half = i & 1, tok = 32 * (i >> 1);
+                    // four blocks of 8 x 8 a load: two of neighbouring features, of 8 tokens and of the next 8
+                    const uint32_t from = vt + (tok + (lane >> 4) * 8 + r) * 128 + (((quad % 2 * 4 + 2 * half + (lane >> 3 & 1)) ^ r) << 4);
+                    uint32_t w[2][4], y[TERMS][8];
+                    ldsm_x4_t(from, w[0]);
+                    ldsm_x4_t(from + 16 * 128, w[1]);
+#pragma unroll
+                    for (int q = 0; q < 4; q++) {
+                        const uint32_t f = e.f[0][tok / 2 + 4 * q + (lane & 3)], g = e.f[1][tok / 2 + 4 * q + (lane & 3)];
+#pragma unroll
+                        for (int x = 2 * q; x < 2 * q + 2; x++) {
+                            // v f1 rounded, and what that left off, which is a bf16 number, with v f2
+                            const uint32_t v = w[x / 4][x % 4];
+                            y[0][x] = bf16_mul(v, f);
+                            y[1][x] = bf16_fma(v, g, bf16_fma(v, f, y[0][x] ^ 0x80008000u));
+                        }
+                    }
+                    const uint32_t to = tmem + TM_V + 64 * (c & 1) + tok / 2 + ((uint32_t)(32 * quad + 16 * half) << 16);
+                    tmem_put_pairs(to, y[0]);
+                    tmem_put_pairs(to + 32, y[1]);
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+            }
             arrive(b_k + 8 * (c & 1));
             if (lane == 0)
                 mbar_arrive(b_ent_free + 8 * (c % ENTRIES));
@@ -845,7 +860,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
         for (int i = 0; i < COLS / 2; i++)
             s[i] = 0;
         if (lane == 0)
-            mbar_arrive(b_k), mbar_arrive(b_k + 8);            // both L are free
+            mbar_arrive(b_k);                                  // L is free
         // S before chunk c, as the operand of its product
         auto put = [&](uint32_t c) -> bool {
             if (STATES_ONLY)
@@ -890,7 +905,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
 #pragma unroll
                 for (int i = 0; i < COLS; i += 16) {
                     float l[16];
-                    tmem_read16(tm_l + 128 * (c & 1) + i, l);
+                    tmem_read16(tm_l + i, l);
                     if (d.weak) {
 #pragma unroll
                         for (int j = 0; j < 8; j++)
@@ -903,7 +918,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                 }
                 tc_fence_before();
             }
-            arrive(b_k + 8 * (c & 1));                         // for the chunk after the next
+            arrive(b_k + 8 * ((c + 1) & 1));                   // for the next chunk
             if (!e.last) {
                 if (!put(c + 1))
                     break;
