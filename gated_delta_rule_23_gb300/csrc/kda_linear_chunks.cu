@@ -341,6 +341,20 @@ __device__ __forceinline__ void tmem_read_pieces(uint32_t at, float (&s)[8], uin
                    "=&f"(t[0]), "=&f"(t[1]), "=&f"(t[2]), "=&f"(t[3]), "=&f"(t[4]), "=&f"(t[5]), "=&f"(t[6]), "=&f"(t[7])
                  : "r"(at), "r"(bt) : "memory");
 }
+// The same of lanes 0..15 and 16..31, of all four at once: one wait
+__device__ __forceinline__ void tmem_read_pieces(uint32_t at, float (&s)[2][8], uint32_t bt, float (&t)[2][8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%32];\n"
+                 " tcgen05.ld.sync.aligned.16x256b.x2.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%33];\n"
+                 " tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%34];\n"
+                 " tcgen05.ld.sync.aligned.16x256b.x2.b32 {%24,%25,%26,%27,%28,%29,%30,%31}, [%35];\n"
+                 " tcgen05.wait::ld.sync.aligned;"
+                 : "=&f"(s[0][0]), "=&f"(s[0][1]), "=&f"(s[0][2]), "=&f"(s[0][3]), "=&f"(s[0][4]), "=&f"(s[0][5]), "=&f"(s[0][6]), "=&f"(s[0][7]),
+                   "=&f"(s[1][0]), "=&f"(s[1][1]), "=&f"(s[1][2]), "=&f"(s[1][3]), "=&f"(s[1][4]), "=&f"(s[1][5]), "=&f"(s[1][6]), "=&f"(s[1][7]),
+                   "=&f"(t[0][0]), "=&f"(t[0][1]), "=&f"(t[0][2]), "=&f"(t[0][3]), "=&f"(t[0][4]), "=&f"(t[0][5]), "=&f"(t[0][6]), "=&f"(t[0][7]),
+                   "=&f"(t[1][0]), "=&f"(t[1][1]), "=&f"(t[1][2]), "=&f"(t[1][3]), "=&f"(t[1][4]), "=&f"(t[1][5]), "=&f"(t[1][6]), "=&f"(t[1][7])
+                 : "r"(at), "r"(bt), "r"(at + (1u << 20)), "r"(bt + (1u << 20)) : "memory");
+}
 __device__ __forceinline__ void stmatrix_x4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -961,15 +975,15 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                         const f2 ea[2] = {f2_pack(f0.x, f0.y), f2_pack(f1.x, f1.y)};
                         f2 z = 0;                              // stays 0 while V^T P^T is finite
                         uint32_t w[2][4];
+                        float x[2][8], y[2][8];
+                        tmem_read_pieces(tmem + TM_O1 + quad + first, x, tmem + TM_O2 + quad + first, y);
 #pragma unroll
                         for (int up = 0; up < 2; up++) {       // lanes 0..15 and 16..31
-                            float x[8], y[8];
-                            tmem_read_pieces(tmem + TM_O1 + quad + first + (up << 20), x, tmem + TM_O2 + quad + first + (up << 20), y);
 #pragma unroll
                             for (int i = 0; i < 4; i++) {
-                                const f2 u = f2_pack(x[2 * i], x[2 * i + 1]);
+                                const f2 u = f2_pack(x[up][2 * i], x[up][2 * i + 1]);
                                 z = f2_fma(u, 0, z);
-                                const f2 o = f2_fma(ea[i / 2], f2_pack(y[2 * i], y[2 * i + 1]), u);
+                                const f2 o = f2_fma(ea[i / 2], f2_pack(y[up][2 * i], y[up][2 * i + 1]), u);
                                 w[up][i] = pack_bf16(f2_lo(o), f2_hi(o));
                             }
                         }
