@@ -12,18 +12,18 @@ namespace kda {
 static bool token_by_token(int N, int64_t T, int H, int D) { return T <= (D == 64 ? 16 : ((int64_t)N * H <= 1024 ? 14 : 8)); }
 
 // The cut of a call into groups (sizes only, so that the workspace is known beforehand), for 152 SMs.  Costs in 10 ns, fitted to what
-// was measured: a chunk takes 1.3 us in a (sequence, head)'s chain, however few run; with groups 2.4 us, the pass over K and V
-// included, and two launches more.  One chain | groups (us): 8192 tokens of 8 heads 175 | 44, 32 heads 176 | 96, 64 heads over 8 174 | 165
-// (a gate per token: 175 | 171), 76 heads 176 | 178; 1024 tokens of 8 heads 29 | 26, 32 heads 29 | 31, 2048 of 48 51 | 49.
+// was measured: a chunk takes 1.15 us in a (sequence, head)'s chain, however few run; with groups 2.1 us, the pass over K and V
+// included, and two launches and the groups' states more.  One chain | groups (us): 8192 tokens of 8 heads 153 | 43, 32 heads over 8 154 | 87,
+// 64 over 8 156 | 150, 76 157 | 163; 2048 of 48 45 | 45; 1024 of 8 heads 24.6 | 22.5.
 static LinearPlan make_plan(bool varlen, int N, int64_t T, int H)
 {
     LinearPlan plan{};
     const int64_t chunks = (T + 63) / 64, pairs = (int64_t)N * H;
     // the longest sequence; of a ragged batch only the sum is known, and twice the mean is taken for it
     const int64_t chain = varlen && N > 1 ? std::min(chunks, 2 * ((chunks + N - 1) / N)) : chunks;
-    int64_t cut = 1, best = 700 + 132 * chain;
+    int64_t cut = 1, best = 650 + 115 * chain;
     for (int64_t g = 2; g * pairs <= 152 && g <= chain; g++) {
-        const int64_t cost = 1850 + 240 * ((chain + g - 1) / g) + 30 * g;
+        const int64_t cost = 1150 + 210 * ((chain + g - 1) / g) + 30 * g + 5 * g * pairs;
         if (cost < best)
             best = cost, cut = g;
     }

@@ -23,16 +23,18 @@
 // 8..11 V~; 12..19 the state; 20..23 O, scaled and stored.  Every role walks one stream of chunks, whatever sequences and heads
 // these belong to, so the next sequence's first chunks are under way while the last one's state is stored.
 //
-// Measured (one GPU): 8192 tokens of 96 heads with fp32 states 177 us, 4.6 TB/s (0.68 of the copy rate); 12 ragged prompts of as many
-// tokens in all 162 us, 5.9 TB/s; 8192 tokens of 64 heads over 8 with gates, two groups a head, 156 us; 32768 tokens of 8 heads, 19
-// groups, 91 us; 509 tokens of 14 heads over 2 of 64 15 us.  A chunk takes some 2,400 cycles in a (sequence, head)'s chain even where
+// Measured (one GPU): 8192 tokens of 96 heads with fp32 states 162 to 164 us, 5.0 TB/s (0.74 of the copy rate); 12 ragged prompts of as many
+// tokens in all 158 to 162 us; 8192 tokens of 64 heads over 8 with gates, two groups a head, 149 us; 32768 tokens of 8 heads, 19
+// groups, 91 us; 509 tokens of 14 heads over 2 of 64 14.3 us.  A chunk takes some 2,200 cycles in a (sequence, head)'s chain even where
 // nothing else runs, and that is what bounds all but the batches that fill the SMs.  At 128 bytes a cycle shared memory alone is busy for 1,600 of
 // them: 48 KB come in, 16 KB are read to be turned, 8 KB written for P, the products read 32 + 32 + 16 + 24 KB, O goes out through 32 KB.
-// (With K~ = e^(A_C - A_j) K, formed in shared memory and read from there as V is, it was 272 KB, and the five took 193, 171, 164, 94 and 15 us.)  The
-// issuing warp's products one after the other, one L, one O on its way out and one place for scores each take nearly as long.  Before
-// that change were slower: the state's product issued by a warp of its own (224 to 245 us), a copying warp of its own beside it (226), scores'
-// place given back before P is stored (190 to 197), O in two halves (206 to 210), barriers tested two at a time (4096 tokens of 152
-// heads 118 for 112: code of many roles is dear in instruction caches), a longer ring of chunks known ahead.
+// (With K~ = e^(A_C - A_j) K, formed in shared memory and read from there as V is, it was 272 KB, and the five took 193, 171, 164, 94 and 15 us.)
+// The chain is O's: products into its one place, 500 cycles, their issue and the barriers, 700, and O on its way out, which took 1,600
+// while its pieces were waited for two at a time and looked at for NaN in every round (177 us; four at a time 170; looked at once at the
+// end 162).  One L and one place for scores take nearly as long.  Before V~ were slower: the state's product issued by a warp of its own (224 to
+// 245 us), a copying warp of its own beside it (226), scores' place given back before P is stored (190 to 197), O in two halves (206 to
+// 210), barriers tested two at a time (4096 tokens of 152 heads 118 for 112: code of many roles is dear in instruction caches), a longer ring of
+// chunks known ahead; with it, O's rounds unrolled by two (179 for 170).
 //
 // An item is a (sequence, head), or a group of its chunks where there are too few of those for the SMs: then a first launch works
 // out what each group adds to the state (its products V~^T K alone), a small kernel chains the groups' states, and the second
@@ -968,12 +970,12 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                 if (ow < WARPS) {
                     tc_fence_after();
                     const int len = e.len, tok0 = e.tok0, h = e.h;
+                    f2 z = 0;                                  // stays 0 while V^T P^T is finite
 #pragma unroll 1
                     for (int first = 0; first < 64; first += 16) {
                         const float2 f0 = *reinterpret_cast<const float2 *>(&e.ea[first + 2 * (lane & 3)]);
                         const float2 f1 = *reinterpret_cast<const float2 *>(&e.ea[first + 8 + 2 * (lane & 3)]);
                         const f2 ea[2] = {f2_pack(f0.x, f0.y), f2_pack(f1.x, f1.y)};
-                        f2 z = 0;                              // stays 0 while V^T P^T is finite
                         uint32_t w[2][4];
                         float x[2][8], y[2][8];
                         tmem_read_pieces(tmem + TM_O1 + quad + first, x, tmem + TM_O2 + quad + first, y);
@@ -987,31 +989,31 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                                 w[up][i] = pack_bf16(f2_lo(o), f2_hi(o));
                             }
                         }
-                        if (__any_sync(FULL, !(f2_lo(z) + f2_hi(z) == 0.0f))) {
-                            // (P is through; waited for here so that this thread sees it.  V's place may be another chunk's by now.)
-                            wait(b_p + 8 * (c & 1), c >> 1);
-                            const int v = ow * 32 + lane;
-                            const unsigned char *pt = smem + S::P + (c & 1) * TILE_CB;
-                            const __nv_bfloat16 *vt = p.v + (int64_t)tok0 * p.v_stride + h / p.group * DIM + v;
-                            for (int i = first; i < min(first + 16, len); i++) {
-                                float u = tmem_read1(tmem + TM_O1 + quad + i);
-                                const float o = tmem_read1(tmem + TM_O2 + quad + i);
-                                if (u - u != 0.0f) {
-                                    u = 0.0f;
-                                    for (int j = 0; j <= i; j++) {
-                                        const __nv_bfloat16 a = *reinterpret_cast<const __nv_bfloat16 *>(
-                                            pt + i * 128 + (((j / 8) ^ (i & 7)) << 4) + (j % 8) * 2);
-                                        u = fmaf(__bfloat162float(a), __bfloat162float(vt[j * p.v_stride]), u);
-                                    }
+                        stmatrix_x4_t(to0 + first * 128, w[0][0], w[0][1], w[0][2], w[0][3]);
+                        stmatrix_x4_t(to1 + first * 128, w[1][0], w[1][1], w[1][2], w[1][3]);
+                    }
+                    if (__any_sync(FULL, !(f2_lo(z) + f2_hi(z) == 0.0f))) {
+                        // (P is through; waited for here so that this thread sees it.  V's place may be another chunk's by now.)
+                        wait(b_p + 8 * (c & 1), c >> 1);
+                        const int v = ow * 32 + lane;
+                        const unsigned char *pt = smem + S::P + (c & 1) * TILE_CB;
+                        const __nv_bfloat16 *vt = p.v + (int64_t)tok0 * p.v_stride + h / p.group * DIM + v;
+                        for (int i = 0; i < len; i++) {
+                            float u = tmem_read1(tmem + TM_O1 + quad + i);
+                            const float o = tmem_read1(tmem + TM_O2 + quad + i);
+                            if (u - u != 0.0f) {
+                                u = 0.0f;
+                                for (int j = 0; j <= i; j++) {
+                                    const __nv_bfloat16 a = *reinterpret_cast<const __nv_bfloat16 *>(
+                                        pt + i * 128 + (((j / 8) ^ (i & 7)) << 4) + (j % 8) * 2);
+                                    u = fmaf(__bfloat162float(a), __bfloat162float(vt[j * p.v_stride]), u);
                                 }
-                                *reinterpret_cast<__nv_bfloat16 *>(smem + S::OUT + (v / 64) * TILE_CB + i * 128 +
-                                                                   (((v % 64 / 8) ^ (i & 7)) << 4) + (v % 8) * 2) =
-                                    __float2bfloat16_rn(fmaf(e.ea[i], o, u));
                             }
-                        } else {
-                            stmatrix_x4_t(to0 + first * 128, w[0][0], w[0][1], w[0][2], w[0][3]);
-                            stmatrix_x4_t(to1 + first * 128, w[1][0], w[1][1], w[1][2], w[1][3]);
+                            *reinterpret_cast<__nv_bfloat16 *>(smem + S::OUT + (v / 64) * TILE_CB + i * 128 +
+                                                               (((v % 64 / 8) ^ (i & 7)) << 4) + (v % 8) * 2) =
+                                __float2bfloat16_rn(fmaf(e.ea[i], o, u));
                         }
+                        __syncwarp();
                     }
                     tc_fence_before();
                     fence_async_smem();
