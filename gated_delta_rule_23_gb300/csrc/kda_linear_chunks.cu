@@ -34,7 +34,7 @@
 // end 162).  One L and one place for scores take nearly as long.  Before V~ were slower: the state's product issued by a warp of its own (224 to
 // 245 us), a copying warp of its own beside it (226), scores' place given back before P is stored (190 to 197), O in two halves (206 to
 // 210), barriers tested two at a time (4096 tokens of 152 heads 118 for 112: code of many roles is dear in instruction caches), a longer ring of
-// chunks known ahead; with it, O's rounds unrolled by two (179 for 170).
+// chunks known ahead; with it, O's rounds unrolled by two (179 for 170), and two places for S Q^T with one for V~ (174 for 162).
 //
 // An item is a (sequence, head), or a group of its chunks where there are too few of those for the SMs: then a first launch works
 // out what each group adds to the state (its products V~^T K alone), a small kernel chains the groups' states, and the second
@@ -114,7 +114,7 @@ static_assert(sizeof(Entry) % 16 == 0 && offsetof(Entry, lo) % 16 == 0 && offset
 template <int DIM, bool STATES_ONLY> struct Shape {
     static constexpr int CB = DIM / 64;
     static constexpr int TILE = CB * TILE_CB;
-    static constexpr int TILES = STATES_ONLY ? 2 : 3;         // of a chunk: V, K (later K~'s first term), Q
+    static constexpr int TILES = STATES_ONLY ? 2 : 3;         // of a chunk: V, K, Q
     static constexpr int STAGE = TILES * TILE;
     static constexpr int STAGES = DIM == 64 ? (STATES_ONLY ? 8 : 6) : (STATES_ONLY ? 6 : 3);
     static constexpr int P = STAGES * STAGE;                  // two of [64 i][64 j]
