@@ -505,7 +505,7 @@ kda_status_t kda_state_reorder(const void *const *src, void *const *dst, const i
  *
  * Sequences of a few tokens are evaluated token by token in fp32, the others in chunks of 64 tokens on the tensor cores:
  * there the scores within a chunk and the state that a chunk's queries read are rounded to bf16, as out is, while the state itself stays
- * in fp32 from chunk to chunk, fed with keys times their decay as two bf16 terms (2^-17).  A
+ * in fp32 from chunk to chunk, fed with values times their decay as two bf16 terms (2^-17).  A
  * token's infinite or NaN value reaches that token's output and later ones', and no earlier one's; a query that is not
  * finite spoils its own output only.
  * kda_linear_attn takes its workspace (groups' states where few heads face many tokens) from the library's pool,
