@@ -264,6 +264,7 @@ template <typename T, int W, bool PROBS> __global__ void __launch_bounds__(PICK_
     __shared__ float row_max[MAX_DRAFTS + 1], row_sum[MAX_DRAFTS + 1];
     __shared__ int row_ok[MAX_DRAFTS + 1];
     __shared__ unsigned long long best_of[PICK_THREADS / 32], best_cta[2][CLUSTER];
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // waited for before anything is sent: every CTA has begun
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
     const int b = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
     const int share = (p.V + p.cluster * W - 1) / (p.cluster * W) * W, from = rank * share, to = min(p.V, from + share);
@@ -407,6 +408,8 @@ template <typename T, int W, bool PROBS> __global__ void __launch_bounds__(PICK_
         if (lane == 0)
             best_of[warp] = best;
         __syncthreads();
+        if (pass == 0)
+            asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
         if (tid < p.cluster) {
             best = best_of[0];
 #pragma unroll
