@@ -11,9 +11,9 @@
 // V~^T K [D x D], S Q^T and V^T P^T [D x 64].  D = 64 fills the lanes up with a block of zeros.
 //
 // The state stays in fp32 registers (eight warps): each chunk's V~^T K comes out of tensor memory and is added there, so the tensor cores'
-// own accumulation spans one chunk and what a long sequence adds up is rounded to nearest.  Weak decays are taken as
-// S + (expm1(A_C) S + L): a factor next to 1 that is off by half a step in every chunk would drift by 2^-25 a chunk; strong ones as
-// e^(A_C) S + L, so that nothing of a state that is forgotten stays behind as rounding.
+// own accumulation spans one chunk and what a long sequence adds up is rounded to nearest.  A decay is two numbers, hi S + (lo S + L): a factor
+// next to 1 that is off by half a step in every chunk would drift by 2^-25 a chunk.  A state that is forgotten (both 0) leaves nothing behind as
+// rounding, and an infinite one stays infinite.
 // V~ is not a bf16 number: two bf16 terms that add up to it (to 2^-17) are multiplied with K one after the other.  With
 // one, outputs after bf16 states were 2.6e-3 off (norm) and not 2.3e-3, 1.7e-3 of it their own rounding, and a prompt took 3% less:
 // what the tensor cores do is not what bounds a chunk.  fp32 states come out 2.7e-6 off.  The other roundings to bf16 are P's, and that of
@@ -80,22 +80,28 @@ __device__ __forceinline__ Sum in_base_2(float a)
     return Sum{hi, fmaf(a, LOG2E, -hi) + a * LOG2E_LO};
 }
 
-// S <- e^a S + L.  weak: factor = e^a - 1, else e^a.
+// S <- e^a S + L as hi S + (lo S + L): hi lies just below e^a, and lo is what it leaves off (of a weak decay out of expm1, good to 2^-47).  Both
+// products have S's sign, so that an infinite S stays what it is unless e^a is 0.  ZEROS: the state began with zeros, and a strong decay
+// is one product (lo = 0): 32768 tokens of 8 heads 91.3 us, without it 92.7; where states are read, a branch between the two forms takes
+// longer than the second product (8192 tokens of 96 heads 163.1 us, with it 166.3).
 struct Decay {
-    float factor;
-    int weak;
+    float hi, lo;
 };
-__device__ __forceinline__ Decay decay_of(const Sum &a)
+template <bool ZEROS> __device__ __forceinline__ Decay decay_of(const Sum &a)
 {
     constexpr float LN2 = 0.6931471805599453f, LN2_LO = (float)(0.69314718055994530942 - (double)LN2);
     const float x = fmaf(a.hi, LN2, fmaf(a.hi, LN2_LO, a.lo * LN2));
-    const bool weak = x > -0.5f;
-    return Decay{weak ? expm1f(x) : expf(x), weak};
+    auto below = [](float y) { return __uint_as_float(__float_as_uint(y) - (y > 0.0f)); };
+    if (!(x > -0.5f)) {
+        const float e = expf(x), hi = ZEROS ? e : below(e);
+        return Decay{hi, ZEROS ? 0.0f : e - hi};
+    }
+    const float less = expm1f(x), hi = below(1.0f + less);
+    return Decay{hi, (1.0f - hi) + less};
 }
 __device__ __forceinline__ float decayed(const Decay &d, float s, float l)
 {
-    const float x = fmaf(d.factor, s, l);
-    return d.weak ? s + x : x;
+    return fmaf(d.hi, s, fmaf(d.lo, s, l));
 }
 
 struct alignas(16) Entry {    // one chunk; the tables are read four floats at a time
@@ -728,7 +734,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                         e.valid = 1;
                         e.first = i == c0, e.last = i + 1 >= c1;
                         e.tok0 = (int)(w.bos + i * 64), e.len = left, e.h = w.h;
-                        e.decay = decay_of(all);
+                        e.decay = decay_of<STATES_ONLY>(all);
                         e.src = src, e.at_src = at_src, e.dst = dst, e.at_dst = at_dst;
                     }
                 }
@@ -738,9 +744,9 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                 c += count;
             }
             if (STATES_ONLY) {
-                const Decay d = decay_of(add(total, Sum{__shfl_xor_sync(FULL, total.hi, 16), __shfl_xor_sync(FULL, total.lo, 16)}));
+                const Decay d = decay_of<false>(add(total, Sum{__shfl_xor_sync(FULL, total.hi, 16), __shfl_xor_sync(FULL, total.lo, 16)}));
                 if (lane == 0)
-                    plan.decays[at_dst] = make_float2(d.factor, d.weak ? 1.0f : 0.0f);
+                    plan.decays[at_dst] = make_float2(d.hi, d.lo);
             }
         }
         if (slot_free(c)) {
@@ -917,19 +923,19 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
             if (mine) {
                 tc_fence_after();
                 const Decay d = e.decay;
-                const f2 factor = f2_pack(d.factor, d.factor);
+                const f2 hi = f2_pack(d.hi, d.hi), lo = f2_pack(d.lo, d.lo);
 #pragma unroll
                 for (int i = 0; i < COLS; i += 16) {
                     float l[16];
                     tmem_read16(tm_l + i, l);
-                    if (d.weak) {
+                    if (STATES_ONLY && d.lo == 0.0f) {
 #pragma unroll
                         for (int j = 0; j < 8; j++)
-                            s[i / 2 + j] = f2_add(s[i / 2 + j], f2_fma(factor, s[i / 2 + j], f2_pack(l[2 * j], l[2 * j + 1])));
+                            s[i / 2 + j] = f2_fma(hi, s[i / 2 + j], f2_pack(l[2 * j], l[2 * j + 1]));
                     } else {
 #pragma unroll
                         for (int j = 0; j < 8; j++)
-                            s[i / 2 + j] = f2_fma(factor, s[i / 2 + j], f2_pack(l[2 * j], l[2 * j + 1]));
+                            s[i / 2 + j] = f2_fma(hi, s[i / 2 + j], f2_fma(lo, s[i / 2 + j], f2_pack(l[2 * j], l[2 * j + 1])));
                     }
                 }
                 tc_fence_before();
@@ -1099,7 +1105,7 @@ __global__ void __launch_bounds__(256) kda_linear_join_kernel(const LinearArgs p
 #pragma unroll
         for (int i = 0; i < AT_ONCE; i++)
             if (first_g + i < groups) {
-                const Decay d{f[i].x, f[i].y != 0.0f};
+                const Decay d{f[i].x, f[i].y};
                 s[0] = decayed(d, s[0], l[i].x), s[1] = decayed(d, s[1], l[i].y), s[2] = decayed(d, s[2], l[i].z), s[3] = decayed(d, s[3], l[i].w);
                 *reinterpret_cast<float4 *>(plan.states + ((first + first_g + i) * p.H + h) * size + at) = make_float4(s[0], s[1], s[2], s[3]);
             }

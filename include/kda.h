@@ -506,8 +506,9 @@ kda_status_t kda_state_reorder(const void *const *src, void *const *dst, const i
  * Sequences of a few tokens are evaluated token by token in fp32, the others in chunks of 64 tokens on the tensor cores:
  * there the scores within a chunk and the state that a chunk's queries read are rounded to bf16, as out is, while the state itself stays
  * in fp32 from chunk to chunk, fed with values times their decay as two bf16 terms (2^-17).  A
- * token's infinite or NaN value reaches that token's output and later ones', and no earlier one's; a query that is not
- * finite spoils its own output only.
+ * token's infinite or NaN value reaches that token's output and later ones', and no earlier one's (in chunks its row of the state is
+ * then NaN); a query that is not finite spoils its own output only.  An infinite element of initial_state stays infinite while
+ * decays are above 0.
  * kda_linear_attn takes its workspace (groups' states where few heads face many tokens) from the library's pool,
  * kda_linear_attn_ws from the caller: kda_linear_attn_workspace_size(...) bytes, 256-byte aligned (NULL when 0).
  */
