@@ -1005,6 +1005,7 @@ kda_linear_chunks_kernel(const __grid_constant__ LinearArgs p, const LinearPlan 
                         const unsigned char *pt = smem + S::P + (c & 1) * TILE_CB;
                         const __nv_bfloat16 *vt = p.v + (int64_t)tok0 * p.v_stride + h / p.group * DIM + v;
                         for (int i = 0; i < len; i++) {
+                            __syncwarp();                      // the reads are the whole warp's
                             float u = tmem_read1(tmem + TM_O1 + quad + i);
                             const float o = tmem_read1(tmem + TM_O2 + quad + i);
                             if (u - u != 0.0f) {

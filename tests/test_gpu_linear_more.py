@@ -47,3 +47,36 @@ def test_an_infinite_state_stays_infinite(layout, lengths, d, state, decay):
     fine = live & o.isfinite()
     assert bool(((got - o).abs() <= BF16 * o.abs() + (BF16 + 2.0 ** -13) * mag)[fine].all())
     assert bool((got[~live] == 5.0).all())
+
+
+# -------------------------------------------------------------------------------------------- values that are not finite
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("seed", range(4))
+def test_many_values_that_are_not_finite(d, seed):
+    """Columns of one warp that take their outputs again from different tokens on, or not at all: each token's outputs before its column's
+    first bad value are what the finite values make of them, and those of other columns do not change by a bit."""
+    a = make([150, 90], 2, 1, d, "lens", seed=60 + seed, total=160)
+    clean = {x: (y.clone() if isinstance(y, torch.Tensor) else y) for x, y in a.items()}
+    call(clean)
+    g = torch.Generator().manual_seed(seed)
+    first = torch.full((2, d), 1 << 20)                           # first bad token of a sequence's column
+    for n, count in ((0, 150), (1, 90)):
+        for _ in range(d // 3):
+            t, c = int(torch.randint(count, (1,), generator=g)), int(torch.randint(d, (1,), generator=g))
+            a["v"][n, t, 0, c] = (math.nan, math.inf, -math.inf)[t % 3]
+            first[n, c] = min(int(first[n, c]), t)
+    out, fin = call(a)
+    o, s, mag, size = linear_ref.linear(a["q"].flatten(0, 1), a["k"].flatten(0, 1), a["v"].flatten(0, 1), logs(a), d ** -0.5,
+                                        a["initial_state"], ranges_of(a))
+    o, mag = o.view(out.shape), mag.view(out.shape)
+    t = torch.arange(160)[None, :, None]
+    live = (t < torch.tensor([150, 90])[:, None, None]).expand(2, 160, d)
+    before = (live & (t < first[:, None])).cuda()[:, :, None].expand(out.shape)
+    behind = (live & (t >= first[:, None])).cuda()[:, :, None].expand(out.shape)
+    assert bool(((out.double() - o).abs() <= BF16 * o.abs() + (BF16 + 2.0 ** -13) * mag)[before].all())
+    assert not bool(out[behind].isfinite().any())
+    untouched = (first == 1 << 20).cuda()
+    for n in range(2):
+        assert torch.equal(out[n][..., untouched[n]], clean["out"][n][..., untouched[n]])
+        assert torch.equal(fin[n][:, untouched[n]], clean["final_state"][n][:, untouched[n]])
+        assert not bool(fin[n][:, ~untouched[n]].isfinite().any())
