@@ -148,7 +148,10 @@ __device__ __forceinline__ float block_sum(float x, float *sm)
     return x;
 }
 
-// log2(e) / tau, kept finite so that a logit at the maximum still gets weight 1 for the smallest tau
+// log2(e) / tau, kept finite so that a logit at the maximum still gets weight 1 for the smallest tau.  One number is enough for the statistics:
+// its rounding (2^-23.7 at most, the constant's included) counts times the exponent, which is taken from the chunk's own maximum.  The weights of 4096 or 8192
+// tokens matter up to some 8 below it, so a sum is off by 2^-21 at the worst (each chunk a token beside a body 7 below it), by 2^-24
+// where one chunk alone has the row's peak.  A second term here: 64 requests of 4 drafts 44.3 us for 43.5.
 __device__ __forceinline__ float exponent_scale(float tau) { return fminf(LOG2E / tau, FLT_MAX); }
 
 // One chunk of one row a CTA: at most VECS 16-byte vectors a thread.  The row may start anywhere: vectors are cut at 16-byte
