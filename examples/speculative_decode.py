@@ -82,7 +82,7 @@ def pick(logits, drafts, probs, temperature, gen):
     counts = torch.empty((b,), dtype=torch.int32, device="cuda")
     noise = torch.empty((b, vocab), device="cuda").exponential_(generator=gen).clamp_(min=1e-20)
     kda.kda_verify_drafts(logits, drafts, torch.rand((b, rows - 1), generator=gen, device="cuda"), noise, tokens, counts,
-                          draft_probs=probs, temperature=torch.full((b,), temperature, device="cuda"))
+                          draft_probs=probs, temperature=torch.full((b,), temperature, device="cuda"), first_largest=True)
     return tokens, counts
 
 

@@ -167,6 +167,8 @@ def load() -> ctypes.CDLL:
         lib.kda_verify_drafts.restype = I
         lib.kda_verify_drafts_ws.argtypes = verify + [P, Z, P]
         lib.kda_verify_drafts_ws.restype = I
+        lib.kda_verify_drafts_opt.argtypes = verify + [ctypes.c_uint32, P, Z, P]
+        lib.kda_verify_drafts_opt.restype = I
         lib.kda_verify_drafts_workspace_size.argtypes = [I, I, I, I]
         lib.kda_verify_drafts_workspace_size.restype = Z
         _lib = lib
@@ -188,7 +190,7 @@ def binding():
         mod.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                    for f in ("kda_kv_append", "kda_window_attn", "kda_window_attn_ws", "kda_beam_select",
                              "kda_beam_select_ws", "kda_state_reorder", "kda_linear_attn", "kda_linear_attn_ws",
-                             "kda_verify_drafts", "kda_verify_drafts_ws")))
+                             "kda_verify_drafts_opt")))
         _binding = mod
     return _binding
 
@@ -205,6 +207,7 @@ KDA_VARIANT_BF16_STATE, KDA_VARIANT_NEUMANN_INVERSE = 1, 2
 # status codes, as in include/kda.h
 KDA_OK, KDA_ERR_INVALID_ARGUMENT, KDA_ERR_UNSUPPORTED, KDA_ERR_CUDA, KDA_ERR_TIMEOUT, KDA_ERR_NONFINITE = range(6)
 KDA_DTYPE_NONE, KDA_DTYPE_BF16, KDA_DTYPE_FP32 = range(3)
+KDA_VERIFY_FIRST_LARGEST = 1
 
 
 class KDAError(RuntimeError):

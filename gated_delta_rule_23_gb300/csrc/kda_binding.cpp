@@ -25,8 +25,7 @@ decltype(&kda_beam_select_ws) g_beam_ws;
 decltype(&kda_state_reorder) g_reorder;
 decltype(&kda_linear_attn) g_linear;
 decltype(&kda_linear_attn_ws) g_linear_ws;
-decltype(&kda_verify_drafts) g_verify;
-decltype(&kda_verify_drafts_ws) g_verify_ws;
+decltype(&kda_verify_drafts_opt) g_verify;
 
 const at::Tensor *tensor(PyObject *o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 
@@ -361,11 +360,11 @@ PyObject *linear_attn(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
-// logits, draft_tokens, uniform, noise, tokens, counts, draft_probs, temperature, draft_lens, stream, workspace
+// logits, draft_tokens, uniform, noise, tokens, counts, draft_probs, temperature, draft_lens, stream, workspace, first_largest
 PyObject *verify_drafts(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     return answer([&]() -> int {
-        if (n != 11)
+        if (n != 12)
             return -1;
         const at::Tensor *l = tensor(a[0]), *drafts = tensor(a[1]), *uniform = tensor(a[2]), *noise = tensor(a[3]);
         const at::Tensor *tokens = tensor(a[4]), *counts = tensor(a[5]), *ws = tensor(a[10]);
@@ -393,22 +392,23 @@ PyObject *verify_drafts(PyObject *, PyObject *const *a, Py_ssize_t n)
         const int32_t *dp = static_cast<const int32_t *>(drafts->data_ptr());
         const float *up = static_cast<const float *>(uniform->data_ptr()), *np = static_cast<const float *>(noise->data_ptr());
         int32_t *tp = static_cast<int32_t *>(tokens->data_ptr()), *cp = static_cast<int32_t *>(counts->data_ptr());
-        if (ws)
-            return g_verify_ws(l->data_ptr(), dtype, step, dp, probs, up, np, temperature, lens, tp, cp, (int)b, (int)k, (int)v,
-                               ws->data_ptr(), (size_t)ws->numel(), s);
-        return g_verify(l->data_ptr(), dtype, step, dp, probs, up, np, temperature, lens, tp, cp, (int)b, (int)k, (int)v, s);
+        const int first = PyObject_IsTrue(a[11]);
+        if (first < 0 || (ws && ws->numel() == 0))
+            return -1;
+        return g_verify(l->data_ptr(), dtype, step, dp, probs, up, np, temperature, lens, tp, cp, (int)b, (int)k, (int)v,
+                        first ? KDA_VERIFY_FIRST_LARGEST : 0, ws ? ws->data_ptr() : nullptr, ws ? (size_t)ws->numel() : 0, s);
     });
 }
 
 // Addresses of libkda.so's entry points, in the order of the globals above.
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    void *p[10];
-    if (n != 10) {
-        PyErr_SetString(PyExc_TypeError, "bind takes 10 addresses");
+    void *p[9];
+    if (n != 9) {
+        PyErr_SetString(PyExc_TypeError, "bind takes 9 addresses");
         return nullptr;
     }
-    for (int i = 0; i < 10; i++) {
+    for (int i = 0; i < 9; i++) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (PyErr_Occurred())
             return nullptr;
@@ -422,7 +422,6 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
     g_linear = reinterpret_cast<decltype(g_linear)>(p[6]);
     g_linear_ws = reinterpret_cast<decltype(g_linear_ws)>(p[7]);
     g_verify = reinterpret_cast<decltype(g_verify)>(p[8]);
-    g_verify_ws = reinterpret_cast<decltype(g_verify_ws)>(p[9]);
     Py_RETURN_NONE;
 }
 

@@ -39,7 +39,8 @@ struct VerifyArgs {
     int B, K, V;
     int chunks, chunk_vecs;      // chunks of a row, 16-byte vectors of a chunk
     int cluster;                 // CTAs of a request in the pick
-    float2 *stats;               // [B (K + 1)][chunks]: maximum, sum of exponentials (workspace)
+    bool first;                  // greedy: a draft that ties for the largest stands only where it is the first of them
+    float2 *stats;               // [B (K + 1)][chunks]: maximum, sum of exponentials or (greedy, first) its lowest index  (workspace)
     unsigned int *err;
 };
 
@@ -148,6 +149,19 @@ __device__ __forceinline__ float block_sum(float x, float *sm)
     return x;
 }
 
+__device__ __forceinline__ int block_min(int x, float *sm)
+{
+    x = __reduce_min_sync(FULL, x);
+    if ((threadIdx.x & 31) == 0)
+        sm[threadIdx.x / 32] = __int_as_float(x);
+    __syncthreads();
+    x = __float_as_int(sm[0]);
+#pragma unroll
+    for (int i = 1; i < THREADS / 32; i++)
+        x = min(x, __float_as_int(sm[i]));
+    return x;
+}
+
 // log2(e) / tau, kept finite so that a logit at the maximum still gets weight 1 for the smallest tau.  One number is enough for the statistics:
 // its rounding (2^-23.7 at most, the constant's included) counts times the exponent, which is taken from the chunk's own maximum.  The weights of 4096 or 8192
 // tokens matter up to some 8 below it, so a sum is off by 2^-21 at the worst (each chunk a token beside a body 7 below it), by 2^-24
@@ -218,7 +232,20 @@ template <typename T, int VECS> __global__ void __launch_bounds__(THREADS, 8) kd
             }
         }
     }
-    s = block_sum(s, sm[1]);
+    if (p.first && tau == 0.0f) {
+        int at = INT32_MAX;                         // the lowest index of the maximum
+#pragma unroll
+        for (int i = VECS - 1; i >= 0; i--) {
+            float u[E];
+            unpack<T>(x[i], u);
+#pragma unroll
+            for (int e = E - 1; e >= 0; e--)
+                at = u[e] == m ? (c * p.chunk_vecs + i * THREADS + tid) * E - off + e : at;
+        }
+        s = __int_as_float(block_min(at, sm[1]));
+    } else {
+        s = block_sum(s, sm[1]);
+    }
     if (tid == 0)
         p.stats[(int64_t)row * p.chunks + c] = make_float2(m, s);
 }
@@ -342,6 +369,24 @@ template <typename T, int W, bool PROBS> __global__ void __launch_bounds__(PICK_
             const bool can = i < L && there[k] && fabsf(m) <= FLT_MAX && drafted[k] > -INFINITY;
             row_ok[i] = can && (greedy ? drafted[k] == m : bar[k] * z < weight_of(drafted[k] - m, f));
             row_max[i] = m, row_sum[i] = z;
+        }
+    }
+    if (greedy && p.first) {                        // of the largest only the first
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < ROWS; k++) {
+            const int i = warp + k * WARPS;
+            if (i >= L)
+                break;
+            const float m = row_max[i];
+            int lowest = first[k].x == m ? __float_as_int(first[k].y) : INT32_MAX;
+            for (int c = lane + 32; c < p.chunks; c += 32) {
+                const float2 x = __ldcg(&stats[i * p.chunks + c]);
+                lowest = x.x == m ? min(lowest, __float_as_int(x.y)) : lowest;
+            }
+            lowest = __reduce_min_sync(FULL, lowest);
+            if (lane == 0 && draft[k] != lowest)
+                row_ok[i] = 0;
         }
     }
     __syncthreads();
@@ -522,17 +567,21 @@ extern "C" size_t kda_verify_drafts_workspace_size(kda_dtype_t dtype, int B, int
     return (size_t)B * (K + 1) * verify_chunks(dtype, B, K, V) * sizeof(float2);
 }
 
-extern "C" kda_status_t kda_verify_drafts_ws(const void *logits, kda_dtype_t dtype, int64_t row_stride,
-                                             const int32_t *draft_tokens, const float *draft_probs, const float *uniform,
-                                             const float *noise, const float *temperature, const int32_t *draft_lens,
-                                             int32_t *tokens, int32_t *counts, int B, int K, int V, void *workspace,
-                                             size_t workspace_bytes, kda_stream_t stream)
+extern "C" kda_status_t kda_verify_drafts_opt(const void *logits, kda_dtype_t dtype, int64_t row_stride,
+                                              const int32_t *draft_tokens, const float *draft_probs, const float *uniform,
+                                              const float *noise, const float *temperature, const int32_t *draft_lens,
+                                              int32_t *tokens, int32_t *counts, int B, int K, int V, uint32_t options,
+                                              void *workspace, size_t workspace_bytes, kda_stream_t stream)
 {
     const kda_status_t s = check_verify(logits, dtype, row_stride, draft_tokens, draft_probs, uniform, noise, temperature,
                                         draft_lens, tokens, counts, B, K, V);
     if (s != KDA_OK)
         return s;
-    if (!workspace || !is_aligned(workspace, 256) || workspace_bytes < kda_verify_drafts_workspace_size(dtype, B, K, V))
+    if (options & ~KDA_VERIFY_FIRST_LARGEST)
+        return KDA_ERR_INVALID_ARGUMENT;
+    const size_t need = kda_verify_drafts_workspace_size(dtype, B, K, V);
+    const bool pool = !workspace && workspace_bytes == 0;
+    if (!pool && (!workspace || !is_aligned(workspace, 256) || workspace_bytes < need))
         return KDA_ERR_INVALID_ARGUMENT;
     VerifyArgs p{logits, row_stride, draft_tokens, draft_probs, uniform, noise, temperature, draft_lens, tokens, counts, B, K, V};
     p.chunks = verify_chunks(dtype, B, K, V);
@@ -542,12 +591,27 @@ extern "C" kda_status_t kda_verify_drafts_ws(const void *logits, kda_dtype_t dty
     p.cluster = CLUSTER;
     while (p.cluster > 1 && (int64_t)B * p.cluster > 2 * 152)
         p.cluster /= 2;
-    p.stats = static_cast<float2 *>(workspace);
+    p.first = options & KDA_VERIFY_FIRST_LARGEST;
     if (step_error_word(&p.err) != cudaSuccess)
         return KDA_ERR_CUDA;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == KDA_DTYPE_BF16 ? launch_verify<__nv_bfloat16>(p, st) : launch_verify<float>(p, st);
-    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    if (pool && pool_alloc(&workspace, need, st) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    p.stats = static_cast<float2 *>(workspace);
+    cudaError_t e = dtype == KDA_DTYPE_BF16 ? launch_verify<__nv_bfloat16>(p, st) : launch_verify<float>(p, st);
+    const cudaError_t freed = pool ? cudaFreeAsync(workspace, st) : cudaSuccess;
+    return e == cudaSuccess && freed == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+extern "C" kda_status_t kda_verify_drafts_ws(const void *logits, kda_dtype_t dtype, int64_t row_stride,
+                                             const int32_t *draft_tokens, const float *draft_probs, const float *uniform,
+                                             const float *noise, const float *temperature, const int32_t *draft_lens,
+                                             int32_t *tokens, int32_t *counts, int B, int K, int V, void *workspace,
+                                             size_t workspace_bytes, kda_stream_t stream)
+{
+    // (none at all would be the pool's)
+    return kda_verify_drafts_opt(logits, dtype, row_stride, draft_tokens, draft_probs, uniform, noise, temperature, draft_lens,
+                                 tokens, counts, B, K, V, 0, workspace, workspace ? workspace_bytes : 1, stream);
 }
 
 extern "C" kda_status_t kda_verify_drafts(const void *logits, kda_dtype_t dtype, int64_t row_stride,
@@ -555,18 +619,6 @@ extern "C" kda_status_t kda_verify_drafts(const void *logits, kda_dtype_t dtype,
                                           const float *noise, const float *temperature, const int32_t *draft_lens,
                                           int32_t *tokens, int32_t *counts, int B, int K, int V, kda_stream_t stream)
 {
-    const kda_status_t c = check_verify(logits, dtype, row_stride, draft_tokens, draft_probs, uniform, noise, temperature,
-                                        draft_lens, tokens, counts, B, K, V);
-    if (c != KDA_OK)
-        return c;
-    const size_t need = kda_verify_drafts_workspace_size(dtype, B, K, V);
-    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    void *ws = nullptr;
-    if (pool_alloc(&ws, need, st) != cudaSuccess)
-        return KDA_ERR_CUDA;
-    kda_status_t s = kda_verify_drafts_ws(logits, dtype, row_stride, draft_tokens, draft_probs, uniform, noise, temperature,
-                                          draft_lens, tokens, counts, B, K, V, ws, need, stream);
-    if (cudaFreeAsync(ws, st) != cudaSuccess && s == KDA_OK)
-        s = KDA_ERR_CUDA;
-    return s;
+    return kda_verify_drafts_opt(logits, dtype, row_stride, draft_tokens, draft_probs, uniform, noise, temperature, draft_lens,
+                                 tokens, counts, B, K, V, 0, nullptr, 0, stream);
 }

@@ -19,7 +19,7 @@ from typing import Optional, Sequence, Union
 import torch
 
 from . import _native
-from ._native import KDA_DTYPE_BF16, KDA_DTYPE_FP32, KDA_DTYPE_NONE, KDA_OK, KDAError
+from ._native import KDA_DTYPE_BF16, KDA_DTYPE_FP32, KDA_DTYPE_NONE, KDA_OK, KDA_VERIFY_FIRST_LARGEST, KDAError
 from .api import _check, _ptr
 
 Tensors = Union[torch.Tensor, Sequence[torch.Tensor]]
@@ -369,17 +369,20 @@ def linear_attn_workspace_size(N: int, T: int, H: int, D: int, varlen: bool = Fa
 def kda_verify_drafts(logits: torch.Tensor, draft_tokens: torch.Tensor, uniform: torch.Tensor, noise: torch.Tensor,
                       tokens: torch.Tensor, counts: torch.Tensor, draft_probs: Optional[torch.Tensor] = None,
                       temperature: Optional[torch.Tensor] = None, draft_lens: Optional[torch.Tensor] = None,
-                      stream: Optional[torch.cuda.Stream] = None, workspace: Optional[torch.Tensor] = None) -> None:
+                      stream: Optional[torch.cuda.Stream] = None, workspace: Optional[torch.Tensor] = None,
+                      first_largest: bool = False) -> None:
     """Speculative decoding's verification: the drafts that the target's distribution accepts, and the token after them.
 
     logits: bf16 or fp32 [B, K + 1, V] (rows evenly spaced), row i the target's after i drafts; draft_tokens: int32
     [B, K]; draft_probs: fp32 [B, K, V], or None where the drafts are certain (looked up, greedy); uniform: fp32 [B, K]
     from [0, 1); noise: fp32 [B, V] from the exponential distribution; temperature: fp32 [B], 0 for greedy (None: 1);
     draft_lens: int32 [B], the drafts that each request has (None: K).  Writes tokens int32 [B, K + 1], the accepted
-    drafts, the token after them and then -1, and counts int32 [B], how many that is: 1 to K + 1.
+    drafts, the token after them and then -1, and counts int32 [B], how many that is: 1 to K + 1.  Greedy requests take a draft
+    whose logit is the row's largest; with ``first_largest``, of several that tie, only the lowest index, which is what decoding one
+    token at a time gives.
     """
     rc = _native.binding().verify_drafts(logits, draft_tokens, uniform, noise, tokens, counts, draft_probs, temperature,
-                                         draft_lens, None if stream is None else stream.cuda_stream, workspace)
+                                         draft_lens, None if stream is None else stream.cuda_stream, workspace, first_largest)
     if rc is not None:
         return _raise(rc)
     dev = _device(logits, "kda_verify_drafts")
@@ -406,12 +409,12 @@ def kda_verify_drafts(logits: torch.Tensor, draft_tokens: torch.Tensor, uniform:
         _need(draft_lens, "draft_lens", torch.int32, (b,), dev)
     args = (logits.data_ptr(), KDA_DTYPE_BF16 if logits.dtype is torch.bfloat16 else KDA_DTYPE_FP32, step,
             draft_tokens.data_ptr(), _ptr(draft_probs), uniform.data_ptr(), noise.data_ptr(), _ptr(temperature),
-            _ptr(draft_lens), tokens.data_ptr(), counts.data_ptr(), b, k, v)
+            _ptr(draft_lens), tokens.data_ptr(), counts.data_ptr(), b, k, v, KDA_VERIFY_FIRST_LARGEST if first_largest else 0)
     if workspace is None:
-        _call(_native.load().kda_verify_drafts, dev, stream, *args)
+        _call(_native.load().kda_verify_drafts_opt, dev, stream, *args, None, 0)
     else:
         size = _workspace(workspace, dev)
-        _call(_native.load().kda_verify_drafts_ws, dev, stream, *args, workspace.data_ptr(), size)
+        _call(_native.load().kda_verify_drafts_opt, dev, stream, *args, workspace.data_ptr(), max(size, 1))   # (an empty one is too small)
 
 
 def verify_drafts_workspace_size(B: int, K: int, V: int, dtype: torch.dtype = torch.bfloat16) -> int:

@@ -533,7 +533,8 @@ size_t kda_linear_attn_workspace_size(int varlen, int N, int64_t T, int H, int D
  * (p_r where nothing is left of that), and w = p_r behind the last draft.  With independent uniform_i from [0, 1) and noise_t
  * from the exponential distribution the tokens are distributed as the target's own.  Without draft_probs the drafts are certain:
  * q_i is 1 at x_i and 0 elsewhere.  Temperature 0: a draft is accepted where its logit is the row's largest, and the token
- * is the lowest index of the largest.
+ * is the lowest index of the largest.  Where several logits tie for it (bf16 ones often do) any of them stands as a draft, so
+ * the tokens may depend on the drafts; with KDA_VERIFY_FIRST_LARGEST only the lowest index does, and they are those of decoding one at a time.
  *
  *   logits         bf16 or fp32 [B, K + 1, V] as dtype says, rows row_stride elements apart (>= V); NaN counts as -INFINITY.
  *   draft_tokens   int32 [B, K];   draft_probs  fp32 [B, K, V] or NULL.
@@ -554,6 +555,13 @@ kda_status_t kda_verify_drafts_ws(const void *logits, kda_dtype_t dtype, int64_t
                                   const float *draft_probs, const float *uniform, const float *noise,
                                   const float *temperature, const int32_t *draft_lens, int32_t *tokens, int32_t *counts,
                                   int B, int K, int V, void *workspace, size_t workspace_bytes, kda_stream_t stream);
+/* With options, KDA_VERIFY_* or'ed together (any other bit is KDA_ERR_INVALID_ARGUMENT); workspace NULL and 0 bytes: from the library's pool. */
+#define KDA_VERIFY_FIRST_LARGEST 1u
+kda_status_t kda_verify_drafts_opt(const void *logits, kda_dtype_t dtype, int64_t row_stride, const int32_t *draft_tokens,
+                                   const float *draft_probs, const float *uniform, const float *noise,
+                                   const float *temperature, const int32_t *draft_lens, int32_t *tokens, int32_t *counts,
+                                   int B, int K, int V, uint32_t options, void *workspace, size_t workspace_bytes,
+                                   kda_stream_t stream);
 /* Workspace bytes of a verification of these sizes; 0 for invalid sizes. */
 size_t kda_verify_drafts_workspace_size(kda_dtype_t dtype, int B, int K, int V);
 

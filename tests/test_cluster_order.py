@@ -27,7 +27,7 @@ def test_there_are_such_kernels():
     assert len(list(kernels())) >= 3
 
 
-@pytest.mark.parametrize("body", kernels())
+@pytest.mark.parametrize("body", list(kernels()))
 def test_a_cluster_has_begun_before_its_ctas_write_to_each_other(body):
     wait = WAITS.search(body)
     assert wait and wait.start() < SENDS.search(body).start()

@@ -1,7 +1,11 @@
 """Draft verification where a request is short of work or a decision hangs on little: against the same 64-bit restatement."""
+import math
+
 import pytest
 import torch
 
+import gated_delta_rule_23_gb300 as kda
+from gated_delta_rule_23_gb300._native import KDA_ERR_INVALID_ARGUMENT, KDAError
 from tests.test_gpu_verify import call, check, make
 
 pytestmark = pytest.mark.gpu
@@ -48,3 +52,68 @@ def test_a_rows_sum_is_right_to_a_step_in_a_million(dtype, body, tau):
     sure = off.abs() > 7.5e-7
     assert bool(sure[0]) and bool(sure[-1])
     assert torch.equal((counts.cpu() == 2)[sure], (off < 0)[sure])
+
+
+# -------------------------------------------------------------------------------------------- greedy requests whose logits tie
+def tied(b, k, v, dtype, seed):
+    """Rows with several largest logits, some of them in other chunks and some NaN before them; drafts that are the first, a later one, or none."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    a = make(b, k, v, dtype, probs=False, seed=seed)
+    a["temperature"] = torch.zeros((b,), device="cuda")
+    first = torch.randint(0, v, (b, k + 1), generator=g, device="cuda")
+    for _ in range(3):
+        at = torch.randint(0, v, (b, k + 1), generator=g, device="cuda")
+        a["logits"].scatter_(2, at[..., None], 40.0)
+        first = torch.minimum(first, at)
+    a["logits"].scatter_(2, first[..., None], 40.0)
+    a["logits"][:, :, 0][first > 0] = math.nan
+    which = torch.rand((b, k), generator=g, device="cuda")
+    a["draft_tokens"].copy_(torch.where(which < 0.75, first[:, :k], torch.where(which < 0.9, at[:, :k], a["draft_tokens"].long())))
+    return a, first
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("b,k,v", [(1, 4, 1), (7, 4, 3), (40, 3, 1000), (9, 5, 8191), (200, 3, 5001), (3, 31, 40003), (2, 4, 1 << 20)])
+def test_greedy_tokens_are_those_of_single_steps(dtype, b, k, v):
+    """With first_largest every token is the row's first largest, whatever the drafts; also beside requests that sample."""
+    a, first = tied(b, k, v, dtype, seed=b + v)
+    tokens, counts = call(a, first_largest=True)
+    taken = (a["draft_tokens"] == first[:, :k]).long().cumprod(1).sum(1)
+    assert torch.equal(counts.long(), taken + 1)
+    at = torch.arange(k + 1, device="cuda")
+    assert torch.equal(tokens.long(), torch.where(at <= taken[:, None], first, -1))
+    # one token at a time: the same call with no drafts, on the rows in turn
+    alone = torch.empty((b, 1), dtype=torch.int32, device="cuda")
+    one = torch.empty((b,), dtype=torch.int32, device="cuda")
+    kda.kda_verify_drafts(a["logits"][:, 0].contiguous()[:, None], torch.empty((b, 0), dtype=torch.int32, device="cuda"),
+                          torch.empty((b, 0), device="cuda"), a["noise"], alone, one, temperature=a["temperature"], first_largest=True)
+    assert torch.equal(alone[:, 0], tokens[:, 0])
+    # requests that sample do not change by it
+    a["temperature"][::2] = 0.8
+    tokens, counts = (x.clone() for x in call(a, first_largest=True))
+    call(a)
+    assert torch.equal(tokens[::2], a["tokens"][::2]) and torch.equal(counts[::2], a["counts"][::2])
+    check(a)                                                          # any of the largest stands where that is not asked for
+
+
+def test_a_row_without_a_maximum_under_the_first_of_the_largest():
+    a, _ = tied(4, 2, 300, torch.float32, seed=3)
+    a["logits"][0] = -math.inf
+    a["logits"][1] = math.nan
+    a["logits"][2, 0, 7] = math.inf
+    a["draft_tokens"][2, 0] = 7
+    tokens, counts = call(a, first_largest=True)
+    assert counts[:3].tolist() == [1, 1, 1] and tokens[:3].tolist() == [[-1, -1, -1]] * 3
+
+
+def test_the_first_of_the_largest_with_a_workspace():
+    a, first = tied(6, 4, 20000, torch.bfloat16, seed=4)
+    ws = torch.empty((kda.verify_drafts_workspace_size(6, 4, 20000),), dtype=torch.uint8, device="cuda")
+    tokens, counts = (x.clone() for x in call(a, first_largest=True))
+    a["tokens"].fill_(-9)
+    call(a, first_largest=True, workspace=ws)
+    assert torch.equal(a["tokens"], tokens) and torch.equal(a["counts"], counts)
+    for small in (ws[:-8], ws[:0]):
+        with pytest.raises(KDAError) as e:
+            call(a, workspace=small)
+        assert e.value.status == KDA_ERR_INVALID_ARGUMENT
