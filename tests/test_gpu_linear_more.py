@@ -80,3 +80,58 @@ def test_many_values_that_are_not_finite(d, seed):
         assert torch.equal(out[n][..., untouched[n]], clean["out"][n][..., untouched[n]])
         assert torch.equal(fin[n][:, untouched[n]], clean["final_state"][n][:, untouched[n]])
         assert not bool(fin[n][:, ~untouched[n]].isfinite().any())
+
+
+# -------------------------------------------------------------------------------------------- bars of each kernel's own
+def restated(a):
+    o, s, mag, size = linear_ref.linear(a["q"].flatten(0, 1), a["k"].flatten(0, 1), a["v"].flatten(0, 1), logs(a),
+                                        a["q"].shape[-1] ** -0.5, a["initial_state"], ranges_of(a))
+    return o, s, mag, size, ~o.isnan().all(-1).all(-1)
+
+
+def takes_tokens(a):
+    """Whether a call goes token by token (sizes alone say so)."""
+    t, h, d = a["q"].shape[1:]
+    return t <= (16 if d == 64 else 14 if len(ranges_of(a)) * h <= 1024 else 8)
+
+
+@pytest.mark.parametrize("layout,lengths", [("batch", [1] * 5), ("batch", [2, 2]), ("batch", [8] * 200), ("batch", [14] * 3), ("lens", [0, 13, 1, 7]),
+                                            ("lens", [0, 5, 3, 8] * 80), ("cu", [1, 0, 9, 4]), ("cu", [1] * 14)])
+@pytest.mark.parametrize("h,hkv,d,state", [(6, 2, 128, torch.float32), (6, 2, 128, torch.bfloat16), (8, 8, 64, torch.float32),
+                                           (8, 1, 64, torch.bfloat16)])
+def test_token_by_token_is_fp32(layout, lengths, h, hkv, d, state):
+    """Token by token all but the outputs' (and a bf16 state's) own rounding is fp32's.
+
+    Per token a state takes expf's two units, 2^-22, the rounding of its argument, |a| e^a 2^-24 under 2^-25, and one fma, 2^-24 (products of
+    bf16 numbers are exact): under 1.4 x 2^-22 of the magnitudes.  An output's sum adds at most 13 roundings of 2^-24 and its scale's, 4 x 2^-22.
+    A bf16 rounding is off by 2^-8 of the value at most, and by 2^-8 / sqrt(3) in the norm; fp32's, independent but for a head's common
+    decay, by 2^-23 a token, as the root of the number of tokens.
+    """
+    a = make(lengths, h, hkv, d, layout, seed=70, state=state)
+    assert takes_tokens(a)
+    out, fin = call(a)
+    o, s, mag, size, live = restated(a)
+    tokens = max(lengths)
+    got = out.flatten(0, 1).double()
+    assert bool(((got - o).abs() <= BF16 * o.abs() + (1.4 * tokens + 4) * 2.0 ** -22 * mag)[live].all())
+    assert float((got - o)[live].norm() / o[live].norm()) <= BF16 / 3 ** 0.5
+    half = BF16 if state == torch.bfloat16 else 0.0
+    assert bool(((fin.double() - s).abs() <= half * s.abs() + 1.4 * tokens * 2.0 ** -22 * size).all())
+    if state == torch.float32:
+        assert float((fin.double() - s).norm() / s.norm()) <= (2 + tokens ** 0.5) * 2.0 ** -23
+
+
+@pytest.mark.parametrize("layout,lengths", [("batch", [64]), ("batch", [100, 100]), ("batch", [1000, 1000]), ("lens", [15, 300, 64, 0]), ("cu", [700, 2, 65, 900]),
+                                            ("batch", [2500])])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("slow", [1.0, 0.01])
+def test_fp32_states_of_chunks_in_the_norm(layout, lengths, d, slow):
+    """A decayed value is two bf16 terms of a factor that is two terms itself: each pair leaves off 2^-17 of it at most, independently from token to
+    token, so the norm is off by sqrt(2) 2^-17 / sqrt(3), and fp32's sums add far less: under 2^-17."""
+    a = make(lengths, 4, 2, d, layout, seed=71, state=torch.float32)
+    a["log_decay"] *= slow
+    a["gate"] *= slow
+    assert not takes_tokens(a)
+    _, fin = call(a)
+    _, s, _, _, _ = restated(a)
+    assert float((fin.double() - s).norm() / s.norm()) <= 2.0 ** -17
