@@ -4,6 +4,8 @@ import math
 import pytest
 import torch
 
+import gated_delta_rule_23_gb300 as kda
+from gated_delta_rule_23_gb300._native import KDA_ERR_INVALID_ARGUMENT, KDAError
 from tests import linear_ref
 from tests.test_gpu_linear import BF16, call, logs, make, ranges_of
 
@@ -135,3 +137,53 @@ def test_fp32_states_of_chunks_in_the_norm(layout, lengths, d, slow):
     _, fin = call(a)
     _, s, _, _, _ = restated(a)
     assert float((fin.double() - s).norm() / s.norm()) <= 2.0 ** -17
+
+
+# -------------------------------------------------------------------------------------------- malformed arrays, every kernel
+def guarded(shape, dtype, value):
+    """A tensor between two stretches that nothing may touch, and these."""
+    size = math.prod(shape)
+    store = torch.full((size + 2048,), value, dtype=dtype, device="cuda")
+    return store[1024:1024 + size].view(shape), (store[:1024], store[1024 + size:])
+
+
+def run_guarded(a, total):
+    n, h, d = len(ranges_of(a)), a["q"].shape[2], a["q"].shape[3]
+    varlen = a["cu_seqlens"] is not None
+    need = kda.linear_attn_workspace_size(n, total, h, d, varlen=varlen)
+    ws, edges = guarded((need,), torch.uint8, 7)
+    a["out"], out_edges = guarded(a["out"].shape, torch.bfloat16, 5.0)
+    a["final_state"], fin_edges = guarded(a["final_state"].shape, a["final_state"].dtype, 9.0)
+    with pytest.raises(KDAError) as e:
+        call(a, workspace=ws if need else None)
+    assert e.value.status == KDA_ERR_INVALID_ARGUMENT
+    kda.device_status()
+    for e, value in ((edges, 7), (out_edges, 5.0), (fin_edges, 9.0)):
+        assert all(bool((x == value).all()) for x in e)
+    return need
+
+
+@pytest.mark.parametrize("total,lengths", [(10, [5, 5]), (300, [150, 150]), (3000, [1500, 1500])])
+@pytest.mark.parametrize("cu", [[0, 4 / 3, 1], [0, -0.1, 1], [0.1, 0.15, 1], [0, 1 / 3, 1e9], [1, 2 / 3, 1 / 3], [-1e9, 1e9, -1e9], [0, 1, 1 / 2]])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_malformed_cu_seqlens_in_every_kernel(total, lengths, cu, d):
+    """Token by token, in chunks, and in groups: reported, and nothing outside the outputs and the workspace is written."""
+    a = make(lengths, 2, 2, d, "cu", seed=80)
+    a["cu_seqlens"].copy_(torch.tensor([int(x * total) for x in cu]))
+    need = run_guarded(a, total)
+    assert (need > 0) == (total == 3000)
+
+
+@pytest.mark.parametrize("t", [4, 150, 2500])
+@pytest.mark.parametrize("d", [64, 128])
+def test_lens_out_of_range_in_every_kernel(t, d):
+    a = make([t, t, t], 2, 1, d, "lens", seed=81)
+    a["lens"].copy_(torch.tensor([-3, t + 9, t // 2], dtype=torch.int32))
+    need = run_guarded(a, t)
+    assert (need > 0) == (t == 2500)
+    # clamped: what the call makes of them in range
+    a["lens"].copy_(torch.tensor([0, t, t // 2], dtype=torch.int32))
+    o, s, mag, size, live = restated(a)
+    got = a["out"].flatten(0, 1).double()
+    assert bool(((got - o).abs() <= BF16 * o.abs() + (BF16 + 2.0 ** -13) * mag)[live].all()) and bool((got[~live] == 5.0).all())
+    assert bool(((a["final_state"].double() - s).abs() <= (2.0 ** -17 + 2.0 ** -16) * size).all())

@@ -6,7 +6,7 @@ import torch
 
 import gated_delta_rule_23_gb300 as kda
 from gated_delta_rule_23_gb300._native import KDA_ERR_INVALID_ARGUMENT, KDAError
-from tests.test_gpu_verify import call, check, make
+from tests.test_gpu_verify import call, check, expected, make
 
 pytestmark = pytest.mark.gpu
 
@@ -117,3 +117,30 @@ def test_the_first_of_the_largest_with_a_workspace():
         with pytest.raises(KDAError) as e:
             call(a, workspace=small)
         assert e.value.status == KDA_ERR_INVALID_ARGUMENT
+
+
+# -------------------------------------------------------------------------------------------- temperatures and rows without a maximum
+@pytest.mark.parametrize("tau", [1.0, 30.0, 1e4, 1e30, 3e38])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_high_temperatures_over_many_chunks(tau, dtype):
+    """Against the restatement: weights of all tokens come near 1, and each counts."""
+    a = make(4, 2, 70001, dtype, seed=21)
+    a["temperature"].fill_(tau)
+    a["logits"][:, :, 60000] = 40.0
+    a["draft_tokens"][:2, 0] = 60000
+    call(a)
+    check(a)
+
+
+def test_a_row_of_nan_after_an_accepted_draft():
+    """The first draft stands (its test is 0 < p), the row behind it has no maximum: one token, and then none."""
+    a = make(3, 2, 700, seed=22)
+    a["uniform"].zero_()
+    a["logits"][1, 1:] = math.nan
+    a["logits"][2, 1:] = -math.inf
+    tokens, counts = call(a)
+    # (0 < 0 at a row without a maximum is no matter of rounding, so the restatement's tokens count as they are)
+    want, many, _ = expected(a)
+    assert counts.tolist() == many.tolist() == [3, 2, 2] and tokens.tolist() == want.tolist()
+    for b in (1, 2):
+        assert tokens[b].tolist() == [int(a["draft_tokens"][b, 0]), -1, -1]
