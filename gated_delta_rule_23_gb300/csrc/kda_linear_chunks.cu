@@ -16,25 +16,20 @@
 // rounding, and an infinite one stays infinite.
 // V~ is not a bf16 number: two bf16 terms that add up to it (to 2^-17) are multiplied with K one after the other.  With
 // one, outputs after bf16 states were 2.6e-3 off (norm) and not 2.3e-3, 1.7e-3 of it their own rounding, and a prompt took 3% less:
-// what the tensor cores do is not what bounds a chunk.  fp32 states come out 2.7e-6 off.  The other roundings to bf16 are P's, and that of
+// what the tensor cores do is not what bounds a chunk.  fp32 states come out 4.1e-6 off (3.1e-6 after a first chunk of 16 tokens; token by token 1e-7).  The other roundings to bf16 are P's, and that of
 // the state that a chunk's queries read (outputs are bf16, rounded to 2^-9 of their own).
 //
 // Warps: 0 copies (tensor maps, a ring of chunks); 1 and 3 issue; 2 finds the chunks, and works their decays out ahead; 4..7 P;
 // 8..11 V~; 12..19 the state; 20..23 O, scaled and stored.  Every role walks one stream of chunks, whatever sequences and heads
 // these belong to, so the next sequence's first chunks are under way while the last one's state is stored.
 //
-// Measured (one GPU): 8192 tokens of 96 heads with fp32 states 162 to 164 us, 5.0 TB/s (0.74 of the copy rate); 12 ragged prompts of as many
-// tokens in all 158 to 162 us; 8192 tokens of 64 heads over 8 with gates, two groups a head, 149 us; 32768 tokens of 8 heads, 19
-// groups, 91 us; 509 tokens of 14 heads over 2 of 64 14.3 us.  A chunk takes some 2,200 cycles in a (sequence, head)'s chain even where
-// nothing else runs, and that is what bounds all but the batches that fill the SMs.  At 128 bytes a cycle shared memory alone is busy for 1,600 of
-// them: 48 KB come in, 16 KB are read to be turned, 8 KB written for P, the products read 32 + 32 + 16 + 24 KB, O goes out through 32 KB.
-// (With K~ = e^(A_C - A_j) K, formed in shared memory and read from there as V is, it was 272 KB, and the five took 193, 171, 164, 94 and 15 us.)
-// The chain is O's: products into its one place, 500 cycles, their issue and the barriers, 700, and O on its way out, which took 1,600
-// while its pieces were waited for two at a time and looked at for NaN in every round (177 us; four at a time 170; looked at once at the
-// end 162).  One L and one place for scores take nearly as long.  Before V~ were slower: the state's product issued by a warp of its own (224 to
-// 245 us), a copying warp of its own beside it (226), scores' place given back before P is stored (190 to 197), O in two halves (206 to
-// 210), barriers tested two at a time (4096 tokens of 152 heads 118 for 112: code of many roles is dear in instruction caches), a longer ring of
-// chunks known ahead; with it, O's rounds unrolled by two (179 for 170), and two places for S Q^T with one for V~ (174 for 162).
+// Measured (one GPU): 8192 tokens of 96 heads with fp32 states 163 us, 5.0 TB/s (0.74 of the copy rate), of 96 heads of 64 147 us; 12 ragged
+// prompts of as many tokens in all 159 us; 8192 tokens of 64 heads over 8 with gates, two groups a head, 150 us; 32768 tokens of 8 heads, 19
+// groups, 91 us; 509 tokens of 14 heads over 2 of 64 14.4 us.  A chunk takes some 2,200 cycles in a (sequence, head)'s chain even where
+// nothing else runs, and that is what bounds all but the batches that fill the SMs: O's products into its one place, their issue and the
+// barriers, and O on its way out.  Beside it shared memory alone is busy for 1,600 (at 128 bytes a cycle: 48 KB come in, 16 KB are read to be
+// turned, 8 KB written for P, the products read 32 + 32 + 16 + 24 KB, O goes out through 32 KB), and the tensor pipe for 70% of
+// the time on SMs that have work.
 //
 // An item is a (sequence, head), or a group of its chunks where there are too few of those for the SMs: then a first launch works
 // out what each group adds to the state (its products V~^T K alone), a small kernel chains the groups' states, and the second

@@ -331,13 +331,16 @@ const char *kda_status_string(kda_status_t status);
 
 /*
  * Waits for `stream`, then reports what the kernels of this library on this device (kda_fwd and
- * its variants, kda_fwd_recurrent) recorded since the last call, and clears it:
+ * its variants, kda_fwd_recurrent, the decoder-step operators below) recorded since the last call, and clears it:
  *   KDA_ERR_TIMEOUT           a kernel gave up a bounded wait on the tensor cores or a bulk copy;
  *                             the outputs of that call are not valid;
  *   KDA_ERR_INVALID_ARGUMENT  a device-resident cu_seqlens broke its contract (cu[0] != 0,
  *                             cu[N] != T or a decreasing entry); the kernels clamped every
  *                             sequence into [0, T] and the chunk table into the workspace, so no
- *                             access left the buffers, but the outputs are not valid;
+ *                             access left the buffers, but the outputs are not valid; or another
+ *                             device-resident argument did, and was clamped or left out as its
+ *                             operator says: a length or a page out of range, a positive decay, a
+ *                             draft outside the vocabulary, a negative or infinite temperature;
  *   KDA_ERR_NONFINITE         the chunked path ended a (sequence, head) with a non-finite state:
  *                             an inf / NaN input, or a value beyond the fp16 range of its
  *                             tensor-core operands (see Numerics above);
@@ -351,7 +354,7 @@ kda_status_t kda_device_status(kda_stream_t stream);
 
 /*
  * Sets how many times a wait of the chunked kernels (kda_fwd and its variants) and of the attention kernels
- * (kda_window_attn), on the tensor cores and on bulk copies, polls before it gives up, for the kernels launched after the call, process-wide
+ * (kda_window_attn) and of linear attention in chunks (kda_linear_attn), on the tensor cores and on bulk copies, polls before it gives up, for the kernels launched after the call, process-wide
  * (default KDA_DEFAULT_WAIT_POLLS, which is far beyond any wait of a working kernel).  A wait that
  * gives up makes its CTA wait for its own work in flight (with the default limit), free its tensor
  * memory and leave; kda_device_status then reports KDA_ERR_TIMEOUT and the call's outputs are not
@@ -503,9 +506,10 @@ kda_status_t kda_state_reorder(const void *const *src, void *const *dst, const i
  * Rows of out behind a sequence's tokens stay as they were.  No output overlaps an input or the other output, except that
  * final_state may be initial_state.
  *
- * Sequences of a few tokens are evaluated token by token in fp32, the others in chunks of 64 tokens on the tensor cores:
+ * Calls of a few tokens (T up to 8, 14 or 16, by sizes) are evaluated token by token in fp32, the others in chunks of 64 tokens on the tensor cores:
  * there the scores within a chunk and the state that a chunk's queries read are rounded to bf16, as out is, while the state itself stays
- * in fp32 from chunk to chunk, fed with values times their decay as two bf16 terms (2^-17).  A
+ * in fp32 from chunk to chunk, fed with values times their decay as two bf16 terms (2^-17: 4e-6 of a state's norm, token by token
+ * 1e-7).  With cu_seqlens T is the sum, so a batch of single tokens is better given as [N, 1, ...].  A
  * token's infinite or NaN value reaches that token's output and later ones', and no earlier one's (in chunks its row of the state is
  * then NaN); a query that is not finite spoils its own output only.  An infinite element of initial_state stays infinite while
  * decays are above 0.
