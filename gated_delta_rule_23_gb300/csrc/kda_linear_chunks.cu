@@ -24,7 +24,7 @@
 // these belong to, so the next sequence's first chunks are under way while the last one's state is stored.
 //
 // Measured (one GPU): 8192 tokens of 96 heads with fp32 states 163 us, 5.0 TB/s (0.74 of the copy rate), of 96 heads of 64 147 us; 12 ragged
-// prompts of as many tokens in all 159 us; 8192 tokens of 64 heads over 8 with gates, two groups a head, 150 us; 32768 tokens of 8 heads, 19
+// prompts of as many tokens in all 159 to 163 us; 8192 tokens of 64 heads over 8 with gates, two groups a head, 150 us; 32768 tokens of 8 heads, 19
 // groups, 91 us; 509 tokens of 14 heads over 2 of 64 14.4 us.  A chunk takes some 2,200 cycles in a (sequence, head)'s chain even where
 // nothing else runs, and that is what bounds all but the batches that fill the SMs: O's products into its one place, their issue and the
 // barriers, and O on its way out.  Beside it shared memory alone is busy for 1,600 (at 128 bytes a cycle: 48 KB come in, 16 KB are read to be
